@@ -203,6 +203,83 @@ qmm_status gemm(Fmt fmt, const void *w, const uint16_t *x_bf16, float *y, int64_
                                       : launch_gemm_q8_0(wb, x_bf16, y, m, n, k, st, ctx, part, budget));
 }
 
+// ---- serving operators ----------------------------------------------------------
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens of one call
+constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
+
+// log2 of a page size the cache takes (a power of two, 16..1024), else -1.
+int page_shift_of(int page_size) {
+    for (int s = 4; s <= 10; ++s)
+        if (page_size == 1 << s) return s;
+    return -1;
+}
+
+size_t codes_bytes(const KvCache &c) {
+    return (static_cast<size_t>(c.num_pages) * c.kv_heads << c.page_shift) * (c.head_dim / 2);
+}
+size_t scales_bytes(const KvCache &c) {
+    return (static_cast<size_t>(c.num_pages) * c.kv_heads << c.page_shift) * (c.head_dim / kQK) * 2;
+}
+
+// Sizes that define a cache; pointers are check_cache's part.
+qmm_status check_cache_sizes(const qmm_kv_q4_0 *cache, KvCache *c) {
+    if (!cache) return QMM_ERR_NULL;
+    if (cache->num_pages < 1 || cache->kv_heads < 1 || cache->head_dim < 1 || cache->page_size < 1)
+        return QMM_ERR_SHAPE;
+    const int shift = page_shift_of(cache->page_size);
+    if (shift < 0 || (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256))
+        return QMM_ERR_UNSUPPORTED;
+    if (cache->num_pages > kMaxIndex || cache->kv_heads > 1024 ||
+        (cache->num_pages * cache->kv_heads) << shift > kMaxIndex)
+        return QMM_ERR_UNSUPPORTED;
+    *c = KvCache{cache->k_codes, cache->k_scales, cache->v_codes, cache->v_scales,
+                 cache->num_pages, shift, cache->kv_heads, cache->head_dim};
+    return QMM_OK;
+}
+
+qmm_status check_cache(const qmm_kv_q4_0 *cache, KvCache *c) {
+    const qmm_status s = check_cache_sizes(cache, c);
+    if (s != QMM_OK) return s;
+    if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return QMM_ERR_NULL;
+    if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) ||
+        !aligned(c->v_scales, 16))
+        return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
+bool overlaps_cache(const KvCache &c, const void *p, size_t bytes) {
+    return overlaps(p, bytes, c.k_codes, codes_bytes(c)) || overlaps(p, bytes, c.v_codes, codes_bytes(c)) ||
+           overlaps(p, bytes, c.k_scales, scales_bytes(c)) || overlaps(p, bytes, c.v_scales, scales_bytes(c));
+}
+
+bool valid_dtype(qmm_dtype t) { return t == QMM_F32 || t == QMM_BF16; }
+size_t dtype_bytes(qmm_dtype t) { return t == QMM_F32 ? 4 : 2; }
+
+// Bytes from the first to the last element of `rows` rows `stride` elements apart.
+size_t rows_bytes(int64_t rows, int64_t stride, int64_t width, size_t size) {
+    return rows < 1 ? 0 : (static_cast<size_t>(rows - 1) * stride + width) * size;
+}
+
+struct Range {
+    const void *p;
+    size_t bytes;
+};
+
+// No output range may overlap an input or another output (null ranges are absent).
+bool outputs_clear(const Range *outs, int no, const Range *ins, int ni) {
+    for (int i = 0; i < no; ++i) {
+        if (!outs[i].p || !outs[i].bytes) continue;
+        for (int j = 0; j < ni; ++j)
+            if (ins[j].p && ins[j].bytes && overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
+                return false;
+        for (int j = 0; j < i; ++j)
+            if (outs[j].p && outs[j].bytes && overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+                return false;
+    }
+    return true;
+}
+
 }  // namespace
 
 bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,
@@ -426,6 +503,168 @@ qmm_status qmm_gemm_q4_0_geglu_ws(const void *wg, const void *wu, const uint16_t
                                             k, st, ctx));
 }
 
+qmm_status qmm_kv_plan(const int32_t *cached, const int32_t *added, int batch,
+                       const int32_t *free_pages, int64_t num_free, int32_t *table,
+                       int64_t table_width, int page_size, int32_t *q_start, int32_t *kv_len,
+                       int64_t *slots, int32_t *positions, int64_t capacity, int32_t *taken,
+                       qmm_stream_t stream) {
+    if (!cached || !added || !table || !q_start || !kv_len || !taken) return QMM_ERR_NULL;
+    if (batch < 1 || num_free < 0 || table_width < 1 || capacity < 0 || page_size < 1) return QMM_ERR_SHAPE;
+    if ((num_free > 0 && !free_pages) || (capacity > 0 && (!slots || !positions))) return QMM_ERR_NULL;
+    const int shift = page_shift_of(page_size);
+    if (shift < 0 || batch > kMaxBatch || num_free > kMaxIndex || table_width > kMaxIndex ||
+        capacity > kMaxIndex)
+        return QMM_ERR_UNSUPPORTED;
+    if (!aligned(cached, 4) || !aligned(added, 4) || !aligned(free_pages, 4) || !aligned(table, 4) ||
+        !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(slots, 8) || !aligned(positions, 4) ||
+        !aligned(taken, 4))
+        return QMM_ERR_ALIGN;
+    const size_t b = static_cast<size_t>(batch), n = static_cast<size_t>(capacity);
+    const Range ins[] = {{cached, 4 * b}, {added, 4 * b}, {free_pages, 4 * static_cast<size_t>(num_free)}};
+    const Range outs[] = {{table, 4 * b * static_cast<size_t>(table_width)}, {q_start, 4 * (b + 1)},
+                          {kv_len, 4 * b}, {slots, 8 * n}, {positions, 4 * n}, {taken, 4}};
+    if (!outputs_clear(outs, 6, ins, 3)) return QMM_ERR_UNSUPPORTED;
+    LaunchCtx ctx;
+    if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
+    const KvPlan plan = {cached, added, free_pages, table, q_start, kv_len, positions, taken, slots,
+                         num_free, table_width, capacity, batch, shift};
+    return from_cuda(launch_kv_plan(plan, reinterpret_cast<cudaStream_t>(stream), ctx));
+}
+
+qmm_status qmm_kv_append_q4_0(const qmm_kv_q4_0 *cache, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, qmm_dtype type, const int64_t *slots, int64_t n,
+                              qmm_stream_t stream) {
+    KvCache c;
+    const qmm_status s = check_cache(cache, &c);
+    if (s != QMM_OK) return s;
+    if (n < 0 || !valid_dtype(type)) return QMM_ERR_SHAPE;
+    if (n == 0) return QMM_OK;
+    if (!k || !v || !slots) return QMM_ERR_NULL;
+    const int64_t width = static_cast<int64_t>(c.kv_heads) * c.head_dim;
+    if (k_stride < width || v_stride < width) return QMM_ERR_SHAPE;
+    if (n > kMaxRows || k_stride > kMaxIndex || v_stride > kMaxIndex) return QMM_ERR_UNSUPPORTED;
+    const size_t size = dtype_bytes(type);
+    if (!aligned(k, size) || !aligned(v, size) || !aligned(slots, 8)) return QMM_ERR_ALIGN;
+    if (overlaps_cache(c, k, rows_bytes(n, k_stride, width, size)) ||
+        overlaps_cache(c, v, rows_bytes(n, v_stride, width, size)) ||
+        overlaps_cache(c, slots, 8 * static_cast<size_t>(n)))
+        return QMM_ERR_UNSUPPORTED;
+    LaunchCtx ctx;
+    if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
+    return from_cuda(launch_kv_append(c, k, k_stride, v, v_stride, type == QMM_BF16, slots, n,
+                                      reinterpret_cast<cudaStream_t>(stream), ctx));
+}
+
+qmm_status qmm_kv_read_q4_0(const qmm_kv_q4_0 *cache, const int64_t *slots, int64_t n, float *k_out,
+                            float *v_out, qmm_stream_t stream) {
+    KvCache c;
+    const qmm_status s = check_cache(cache, &c);
+    if (s != QMM_OK) return s;
+    if (n < 0) return QMM_ERR_SHAPE;
+    if (n == 0) return QMM_OK;
+    if (!slots || (!k_out && !v_out)) return QMM_ERR_NULL;
+    if (n > kMaxRows) return QMM_ERR_UNSUPPORTED;
+    if (!aligned(slots, 8) || !aligned(k_out, 4) || !aligned(v_out, 4)) return QMM_ERR_ALIGN;
+    const size_t bytes = 4 * static_cast<size_t>(n) * c.kv_heads * c.head_dim;
+    const Range ins[] = {{slots, 8 * static_cast<size_t>(n)}};
+    const Range outs[] = {{k_out, bytes}, {v_out, bytes}};
+    if (!outputs_clear(outs, 2, ins, 1) || (k_out && overlaps_cache(c, k_out, bytes)) ||
+        (v_out && overlaps_cache(c, v_out, bytes)))
+        return QMM_ERR_UNSUPPORTED;
+    LaunchCtx ctx;
+    if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
+    return from_cuda(launch_kv_read(c, slots, n, k_out, v_out, reinterpret_cast<cudaStream_t>(stream), ctx));
+}
+
+size_t qmm_attn_q4_0_workspace_bytes(const qmm_kv_q4_0 *cache, int heads) {
+    KvCache c;
+    if (check_cache_sizes(cache, &c) != QMM_OK || heads < 1 || heads % c.kv_heads != 0) return 0;
+    return attn_workspace_bytes(c, heads);
+}
+
+qmm_status qmm_attn_q4_0(const qmm_kv_q4_0 *cache, const qmm_attn_args *args, qmm_stream_t stream) {
+    KvCache c;
+    qmm_status s = check_cache(cache, &c);
+    if (s != QMM_OK) return s;
+    if (!args) return QMM_ERR_NULL;
+    const qmm_attn_args &a = *args;
+    if (a.batch < 1 || a.total_q < 0 || a.max_q < 1 || a.heads < 1 || a.heads % c.kv_heads != 0 ||
+        a.table_width < 1 || a.window < 0 || (a.window > 0 && !a.causal) || !(a.scale - a.scale == 0.0f) ||
+        !valid_dtype(a.q_type) || !valid_dtype(a.out_type))
+        return QMM_ERR_SHAPE;
+    if (a.total_q == 0) return QMM_OK;
+    if (!a.q || !a.out || !a.table || !a.q_start || !a.kv_len) return QMM_ERR_NULL;
+    const int64_t width = static_cast<int64_t>(a.heads) * c.head_dim;
+    if (a.q_stride < width || a.out_stride < width) return QMM_ERR_SHAPE;
+    if (a.batch > kMaxBatch || a.total_q > kMaxRows || a.heads > 1024 || a.table_width > kMaxIndex ||
+        a.q_stride > kMaxIndex || a.out_stride > kMaxIndex)
+        return QMM_ERR_UNSUPPORTED;
+    if (!aligned(a.q, dtype_bytes(a.q_type)) || !aligned(a.out, dtype_bytes(a.out_type)) ||
+        !aligned(a.lse, 4) || !aligned(a.table, 4) || !aligned(a.q_start, 4) || !aligned(a.kv_len, 4))
+        return QMM_ERR_ALIGN;
+    const size_t need = attn_workspace_bytes(c, a.heads);
+    if (need) {
+        if (!a.workspace) return QMM_ERR_NULL;
+        s = check_workspace(a.workspace, a.workspace_bytes, need);
+        if (s != QMM_OK) return s;
+    }
+    const size_t out_bytes = rows_bytes(a.total_q, a.out_stride, width, dtype_bytes(a.out_type));
+    const size_t lse_bytes = 4 * static_cast<size_t>(a.total_q) * a.heads, b = static_cast<size_t>(a.batch);
+    const Range ins[] = {{a.q, rows_bytes(a.total_q, a.q_stride, width, dtype_bytes(a.q_type))},
+                         {a.table, 4 * b * static_cast<size_t>(a.table_width)},
+                         {a.q_start, 4 * (b + 1)}, {a.kv_len, 4 * b}};
+    const Range outs[] = {{a.out, out_bytes}, {a.lse, lse_bytes}, {a.workspace, need}};
+    if (!outputs_clear(outs, 3, ins, 4)) return QMM_ERR_UNSUPPORTED;
+    for (const Range &o : outs)
+        if (o.p && o.bytes && overlaps_cache(c, o.p, o.bytes)) return QMM_ERR_UNSUPPORTED;
+    LaunchCtx ctx;
+    if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
+    const AttnArgs k = {a.q, a.out, a.lse, a.table, a.q_start, a.kv_len, a.q_stride, a.out_stride,
+                        a.table_width, a.total_q, a.batch, a.max_q, a.heads, a.causal != 0, a.window,
+                        a.scale, a.q_type == QMM_BF16, a.out_type == QMM_BF16, a.workspace};
+    return from_cuda(launch_attn(c, k, reinterpret_cast<cudaStream_t>(stream), ctx));
+}
+
+qmm_status qmm_logits_adjust(const qmm_logits_args *args, qmm_stream_t stream) {
+    if (!args) return QMM_ERR_NULL;
+    const qmm_logits_args &a = *args;
+    if (!a.logits || !a.out) return QMM_ERR_NULL;
+    if (a.rows < 1 || a.vocab < 1 || a.logits_stride < a.vocab || a.out_stride < a.vocab ||
+        a.history_len < 0 || a.bias_len < 0)
+        return QMM_ERR_SHAPE;
+    // lists come whole or not at all; an empty list may have no storage
+    if ((a.history && !a.hist_start) || (a.hist_start && !a.history && a.history_len > 0) ||
+        (a.bias_ids && (!a.bias_values || !a.bias_start)) ||
+        (!a.bias_ids && (a.bias_values || (a.bias_start && a.bias_len > 0))))
+        return QMM_ERR_NULL;
+    if (a.rows > 65535 || a.vocab > kMaxIndex - 65536 || a.history_len > kMaxIndex ||
+        a.bias_len > kMaxIndex || a.logits_stride > (int64_t(1) << 40) || a.out_stride > (int64_t(1) << 40))
+        return QMM_ERR_UNSUPPORTED;
+    for (const void *p : {static_cast<const void *>(a.logits), static_cast<const void *>(a.out),
+                          static_cast<const void *>(a.history), static_cast<const void *>(a.hist_start),
+                          static_cast<const void *>(a.prompt_len), static_cast<const void *>(a.repetition),
+                          static_cast<const void *>(a.frequency), static_cast<const void *>(a.presence),
+                          static_cast<const void *>(a.bias_ids), static_cast<const void *>(a.bias_values),
+                          static_cast<const void *>(a.bias_start), static_cast<const void *>(a.allowed)})
+        if (!aligned(p, 4)) return QMM_ERR_ALIGN;
+    const size_t m = static_cast<size_t>(a.rows);
+    const bool in_place = a.logits == a.out && a.logits_stride == a.out_stride;
+    const Range ins[] = {{in_place ? nullptr : a.logits, rows_bytes(a.rows, a.logits_stride, a.vocab, 4)},
+                         {a.history, 4 * static_cast<size_t>(a.history_len)}, {a.hist_start, 4 * (m + 1)},
+                         {a.prompt_len, 4 * m}, {a.repetition, 4 * m}, {a.frequency, 4 * m},
+                         {a.presence, 4 * m}, {a.bias_ids, 4 * static_cast<size_t>(a.bias_len)},
+                         {a.bias_values, 4 * static_cast<size_t>(a.bias_len)}, {a.bias_start, 4 * (m + 1)},
+                         {a.allowed, 4 * m * static_cast<size_t>((a.vocab + 31) / 32)}};
+    const Range outs[] = {{a.out, rows_bytes(a.rows, a.out_stride, a.vocab, 4)}};
+    if (!outputs_clear(outs, 1, ins, 11)) return QMM_ERR_UNSUPPORTED;
+    LaunchCtx ctx;
+    if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
+    const LogitsArgs k = {a.logits, a.out, a.history, a.hist_start, a.prompt_len, a.repetition,
+                          a.frequency, a.presence, a.bias_ids, a.bias_values, a.bias_start, a.allowed,
+                          a.logits_stride, a.out_stride, a.rows, a.vocab, a.history_len, a.bias_len};
+    return from_cuda(launch_logits_adjust(k, reinterpret_cast<cudaStream_t>(stream), ctx));
+}
+
 const char *qmm_status_string(qmm_status status) {
     switch (status) {
         case QMM_OK: return "ok";
@@ -437,11 +676,12 @@ const char *qmm_status_string(qmm_status status) {
         case QMM_ERR_TIMEOUT: return "a device-side wait timed out";
         case QMM_ERR_SCRATCH:
             return "problem larger than the entry point's fixed scratch (qmm_gemm_q4_0_prefill: k > 131072)";
+        case QMM_ERR_INDEX: return "a page, slot or length on the device lies outside its array";
     }
     return "unknown status";
 }
 
-int qmm_version(void) { return 400; }  // 0.4.0: qmm_copy added
+int qmm_version(void) { return 500; }  // 0.5.0: Q4_0 cache, attention and logits added
 
 qmm_status qmm_get_device_error(qmm_stream_t stream) {
     cudaError_t e;

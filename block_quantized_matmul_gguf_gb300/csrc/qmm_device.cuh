@@ -11,7 +11,7 @@
 namespace qmm {
 
 // Error codes written to the device error word (match qmm_status values).
-enum : uint32_t { kDevErrTimeout = 6 };
+enum : uint32_t { kDevErrTimeout = 6, kDevErrIndex = 8 };
 
 // Per-launch context every kernel receives.
 struct LaunchCtx {

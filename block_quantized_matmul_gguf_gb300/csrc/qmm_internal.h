@@ -228,6 +228,61 @@ bool gemv_tc_shape_ok(int m, int64_t n, int64_t k);
 cudaError_t launch_gemv_tc_q4_0(const uint8_t *w, const float *x, float *y, int m, int64_t n,
                                 int64_t k, cudaStream_t stream, const LaunchCtx &ctx);
 
+// ---- serving operators (include/qmm.h has the formulas) -----------------------
+
+// The paged Q4_0 cache, checked: head_dim 64, 128 or 256.
+struct KvCache {
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t num_pages;
+    int page_shift, kv_heads, head_dim;  // 1 << page_shift slots in a page
+};
+
+struct KvPlan {
+    const int32_t *cached, *added, *free_pages;
+    int32_t *table, *q_start, *kv_len, *positions, *taken;
+    int64_t *slots;
+    int64_t num_free, table_width, capacity;
+    int batch, page_shift;
+};
+constexpr int kMaxBatch = 16384;
+
+cudaError_t launch_kv_plan(const KvPlan &plan, cudaStream_t stream, const LaunchCtx &ctx);
+cudaError_t launch_kv_append(const KvCache &cache, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, bool bf16, const int64_t *slots, int64_t n,
+                             cudaStream_t stream, const LaunchCtx &ctx);
+cudaError_t launch_kv_read(const KvCache &cache, const int64_t *slots, int64_t n, float *k_out,
+                           float *v_out, cudaStream_t stream, const LaunchCtx &ctx);
+
+struct AttnArgs {
+    const void *q;
+    void *out;
+    float *lse;
+    const int32_t *table, *q_start, *kv_len;
+    int64_t q_stride, out_stride, table_width, total_q;
+    int batch, max_q, heads, causal, window;
+    float scale;
+    bool q_bf16, out_bf16;
+    void *workspace;
+};
+
+size_t attn_workspace_bytes(const KvCache &cache, int heads);
+cudaError_t launch_attn(const KvCache &cache, const AttnArgs &args, cudaStream_t stream,
+                        const LaunchCtx &ctx);
+
+struct LogitsArgs {
+    const float *logits;
+    float *out;
+    const int32_t *history, *hist_start, *prompt_len;
+    const float *repetition, *frequency, *presence;
+    const int32_t *bias_ids;
+    const float *bias_values;
+    const int32_t *bias_start;
+    const uint32_t *allowed;
+    int64_t logits_stride, out_stride, rows, vocab, history_len, bias_len;
+};
+
+cudaError_t launch_logits_adjust(const LogitsArgs &args, cudaStream_t stream, const LaunchCtx &ctx);
+
 cudaError_t launch_selftest_wait(cudaStream_t stream, const LaunchCtx &ctx);
 
 }  // namespace qmm

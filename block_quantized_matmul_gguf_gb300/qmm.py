@@ -23,6 +23,9 @@ QMM_ERR_UNSUPPORTED = 4
 QMM_ERR_CUDA = 5
 QMM_ERR_TIMEOUT = 6
 QMM_ERR_SCRATCH = 7
+QMM_ERR_INDEX = 8
+QMM_F32 = 0
+QMM_BF16 = 1
 QMM_GEMV_MAX_M = 16
 
 QMM_GEMV_MAX_OUTPUTS = 4
@@ -34,12 +37,46 @@ EXPORTED = (
     "qmm_gemm_q4_0_ws", "qmm_gemm_q8_0_ws", "qmm_gemm_q4_0_geglu_ws", "qmm_gemm_q4_0_prefill",
     "qmm_gemm_workspace_bytes", "qmm_gemm_geglu_workspace_bytes", "qmm_status_string", "qmm_version", "qmm_get_device_error",
     "qmm_set_wait_timeout_ns", "qmm_selftest_wait_timeout", "qmm_copy",
+    "qmm_kv_plan", "qmm_kv_append_q4_0", "qmm_kv_read_q4_0",
+    "qmm_attn_q4_0_workspace_bytes", "qmm_attn_q4_0", "qmm_logits_adjust",
 )
 
 
 class GemvOut(ctypes.Structure):
     """struct qmm_gemv_out: one weight matrix and its output."""
     _fields_ = [("w", ctypes.c_void_p), ("y", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class KvQ4_0(ctypes.Structure):
+    """struct qmm_kv_q4_0: the arrays and sizes of a paged Q4_0 cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class AttnArgs(ctypes.Structure):
+    """struct qmm_attn_args."""
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("q_type", ctypes.c_int),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64), ("out_type", ctypes.c_int),
+                ("lse", ctypes.c_void_p), ("table", ctypes.c_void_p), ("table_width", ctypes.c_int64),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("batch", ctypes.c_int),
+                ("total_q", ctypes.c_int64), ("max_q", ctypes.c_int), ("heads", ctypes.c_int),
+                ("scale", ctypes.c_float), ("causal", ctypes.c_int), ("window", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class LogitsArgs(ctypes.Structure):
+    """struct qmm_logits_args."""
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("history", ctypes.c_void_p), ("hist_start", ctypes.c_void_p),
+                ("history_len", ctypes.c_int64), ("prompt_len", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p),
+                ("bias_values", ctypes.c_void_p), ("bias_start", ctypes.c_void_p),
+                ("bias_len", ctypes.c_int64), ("allowed", ctypes.c_void_p)]
 
 
 class QmmError(RuntimeError):
@@ -87,6 +124,11 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "qmm_get_device_error": [P],
         "qmm_selftest_wait_timeout": [U64, P],
         "qmm_copy": [P, P, SZ, P],
+        "qmm_kv_plan": [P, P, I32, P, I64, P, I64, I32, P, P, P, P, I64, P, P],
+        "qmm_kv_append_q4_0": [P, P, I64, P, I64, I32, P, I64, P],
+        "qmm_kv_read_q4_0": [P, P, I64, P, P, P],
+        "qmm_attn_q4_0": [P, P, P],
+        "qmm_logits_adjust": [P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -99,6 +141,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     for name in ("qmm_gemm_workspace_bytes", "qmm_gemm_geglu_workspace_bytes"):
         getattr(lib, name).argtypes = [I64, I64]
         getattr(lib, name).restype = SZ
+    lib.qmm_attn_q4_0_workspace_bytes.argtypes = [P, I32]
+    lib.qmm_attn_q4_0_workspace_bytes.restype = SZ
     lib.qmm_set_wait_timeout_ns.argtypes = [U64]
     lib.qmm_set_wait_timeout_ns.restype = None
     _lib = lib
@@ -267,6 +311,166 @@ def qmm_set_wait_timeout_ns(ns: int) -> None:
 def qmm_selftest_wait_timeout(timeout_ns: int, stream=None) -> None:
     _check(load().qmm_selftest_wait_timeout(int(timeout_ns), _stream(stream)),
            "qmm_selftest_wait_timeout")
+
+
+# ---- serving operators: paged Q4_0 cache, attention, logits -------------------
+
+class KvCacheQ4_0:
+    """A paged Q4_0 cache of keys and values over the caller's four tensors:
+    codes uint8 [pages][kv_heads][page_size][head_dim/2], scales float16
+    [pages][kv_heads][page_size][head_dim/32].  Keeps them alive and holds
+    the struct that the calls read."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        import torch
+        pages, heads, page_size, half = k_codes.shape
+        for codes, scales in ((k_codes, k_scales), (v_codes, v_scales)):
+            if codes.dtype != torch.uint8 or scales.dtype != torch.float16:
+                raise ValueError("codes must be uint8 and scales float16")
+            if tuple(codes.shape) != (pages, heads, page_size, half) or \
+                    tuple(scales.shape) != (pages, heads, page_size, half // 16):
+                raise ValueError("codes [pages][kv_heads][page_size][head_dim/2] and scales "
+                                 "[pages][kv_heads][page_size][head_dim/32] expected")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page_size, 2 * half
+        self.struct = KvQ4_0(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
+                             pages, page_size, heads, 2 * half)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def kv_cache_q4_0(num_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> KvCacheQ4_0:
+    """A new cache of zeros."""
+    import torch
+    shape = (num_pages, kv_heads, page_size)
+    codes = [torch.zeros((*shape, head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.zeros((*shape, head_dim // 32), dtype=torch.float16, device=device) for _ in range(2)]
+    return KvCacheQ4_0(codes[0], scales[0], codes[1], scales[1])
+
+
+def _typed(t, dtype, what: str) -> int:
+    """The pointer of a contiguous tensor of this dtype (None: NULL)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    return _ptr(t)
+
+
+def _rows(t, heads: int, dim: int, what: str):
+    """(pointer, row stride, qmm_dtype) of [n][heads][dim] whose rows may lie apart."""
+    import torch
+    if t.dtype == torch.float32:
+        kind = QMM_F32
+    elif t.dtype == torch.bfloat16:
+        kind = QMM_BF16
+    else:
+        raise ValueError(f"{what} must be float32 or bfloat16")
+    n, h, d = t.shape
+    stride = t.stride()
+    if h != heads or d != dim or (stride[2] != 1 and dim > 1) or (stride[1] != dim and heads > 1):
+        raise ValueError(f"{what} must be [rows][{heads}][{dim}] with dense rows")
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    return t.data_ptr(), (stride[0] if n > 1 else heads * dim), kind
+
+
+def qmm_kv_plan(cached, added, free_pages, table, page_size: int, q_start, kv_len, slots, positions, taken,
+                stream=None) -> None:
+    """Page tables and slot maps of the next step from the requests' lengths."""
+    import torch
+    i32, batch = torch.int32, cached.numel()
+    if added.numel() != batch or table.shape[0] != batch or q_start.numel() != batch + 1 or \
+            kv_len.numel() != batch or positions.numel() != slots.numel():
+        raise ValueError("added, table, q_start, kv_len and positions must match cached and slots in size")
+    _check(load().qmm_kv_plan(
+        _typed(cached, i32, "cached"), _typed(added, i32, "added"), batch,
+        _typed(free_pages, i32, "free_pages"), free_pages.numel(), _typed(table, i32, "table"),
+        table.shape[1], page_size, _typed(q_start, i32, "q_start"), _typed(kv_len, i32, "kv_len"),
+        _typed(slots, torch.int64, "slots"), _typed(positions, i32, "positions"), slots.numel(),
+        _typed(taken, i32, "taken"), _stream(stream)), "qmm_kv_plan")
+
+
+def qmm_kv_append_q4_0(cache: KvCacheQ4_0, k, v, slots, stream=None) -> None:
+    """Quantize k and v [n][kv_heads][head_dim] (fp32 or bf16) into the slots of the cache."""
+    import torch
+    kp, ks, kind = _rows(k, cache.kv_heads, cache.head_dim, "k")
+    vp, vs, other = _rows(v, cache.kv_heads, cache.head_dim, "v")
+    n = slots.numel()
+    if kind != other or k.shape[0] != n or v.shape[0] != n:
+        raise ValueError("k and v must have one dtype and a row for each slot")
+    _check(load().qmm_kv_append_q4_0(cache.ref, kp, ks, vp, vs, kind, _typed(slots, torch.int64, "slots"),
+                                     n, _stream(stream)), "qmm_kv_append_q4_0")
+
+
+def qmm_kv_read_q4_0(cache: KvCacheQ4_0, slots, k_out, v_out, stream=None) -> None:
+    """The fp32 values of cache slots, k_out and v_out [n][kv_heads][head_dim] (either may be None)."""
+    import torch
+    n = slots.numel()
+    for t in (k_out, v_out):
+        if t is not None and t.numel() != n * cache.kv_heads * cache.head_dim:
+            raise ValueError("outputs must be [slots][kv_heads][head_dim]")
+    _check(load().qmm_kv_read_q4_0(cache.ref, _typed(slots, torch.int64, "slots"), n,
+                                   _typed(k_out, torch.float32, "k_out"),
+                                   _typed(v_out, torch.float32, "v_out"), _stream(stream)),
+           "qmm_kv_read_q4_0")
+
+
+def attn_workspace(cache: KvCacheQ4_0, heads: int):
+    """A workspace for attention calls on this cache (calls that overlap on the GPU need their own)."""
+    import torch
+    n = int(load().qmm_attn_q4_0_workspace_bytes(cache.ref, heads))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k_codes.device)
+
+
+def qmm_attn_q4_0(cache: KvCacheQ4_0, q, out, table, q_start, kv_len, max_q: int, scale: float,
+                  causal: bool = True, window: int = 0, lse=None, workspace=None, stream=None) -> None:
+    """Attention of q [rows][heads][head_dim] (fp32 or bf16) over the cache into out (fp32 or bf16)."""
+    import torch
+    i32, heads = torch.int32, q.shape[1]
+    qp, q_stride, q_type = _rows(q, heads, cache.head_dim, "q")
+    op, out_stride, out_type = _rows(out, heads, cache.head_dim, "out")
+    batch, rows = kv_len.numel(), q.shape[0]
+    if out.shape[0] != rows or table.shape[0] != batch or q_start.numel() != batch + 1 or \
+            (lse is not None and lse.numel() != rows * heads):
+        raise ValueError("out, lse, table and q_start must match q and kv_len in size")
+    if workspace is None:
+        workspace = attn_workspace(cache, heads)
+    args = AttnArgs(qp, q_stride, q_type, op, out_stride, out_type,
+                    _typed(lse, torch.float32, "lse"), _typed(table, i32, "table"), table.shape[1],
+                    _typed(q_start, i32, "q_start"), _typed(kv_len, i32, "kv_len"), batch, rows, max_q,
+                    heads, scale, int(causal), window, _ptr(workspace),
+                    workspace.numel() * workspace.element_size())
+    _check(load().qmm_attn_q4_0(cache.ref, ctypes.addressof(args), _stream(stream)), "qmm_attn_q4_0")
+
+
+def qmm_logits_adjust(logits, out, history=None, hist_start=None, prompt_len=None, repetition=None,
+                      frequency=None, presence=None, bias_ids=None, bias_values=None, bias_start=None,
+                      allowed=None, stream=None) -> None:
+    """Penalties, biases and grammar masks on logits [rows][vocab] (fp32); out may be logits."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    rows, vocab = logits.shape
+    for t, what in ((logits, "logits"), (out, "out")):
+        if t.dtype != f32 or tuple(t.shape) != (rows, vocab) or (t.stride(1) != 1 and vocab > 1) or not t.is_cuda:
+            raise ValueError(f"{what} must be float32 [rows][vocab] on a CUDA device with dense rows")
+    for t, n, what in ((hist_start, rows + 1, "hist_start"), (bias_start, rows + 1, "bias_start"),
+                       (prompt_len, rows, "prompt_len"), (repetition, rows, "repetition"),
+                       (frequency, rows, "frequency"), (presence, rows, "presence"),
+                       (allowed, rows * ((vocab + 31) // 32), "allowed")):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{what} must have {n} entries")
+    if (bias_ids is None) != (bias_values is None) or \
+            (bias_ids is not None and bias_ids.numel() != bias_values.numel()):
+        raise ValueError("bias_ids and bias_values go together")
+    args = LogitsArgs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab,
+                      out.data_ptr(), out.stride(0) if rows > 1 else vocab, rows, vocab,
+                      _typed(history, i32, "history"), _typed(hist_start, i32, "hist_start"),
+                      0 if history is None else history.numel(), _typed(prompt_len, i32, "prompt_len"),
+                      _typed(repetition, f32, "repetition"), _typed(frequency, f32, "frequency"),
+                      _typed(presence, f32, "presence"), _typed(bias_ids, i32, "bias_ids"),
+                      _typed(bias_values, f32, "bias_values"), _typed(bias_start, i32, "bias_start"),
+                      0 if bias_ids is None else bias_ids.numel(), _typed(allowed, i32, "allowed"))
+    _check(load().qmm_logits_adjust(ctypes.addressof(args), _stream(stream)), "qmm_logits_adjust")
 
 
 # ---- tensor-level conveniences (allocate the output, then call the ABI) ----

@@ -17,6 +17,13 @@
  *   geglu   : h = gelu(x.Wg^T) * (x.Wu^T), the feed-forward input, for
  *             decode (gemv) and prefill (gemm)
  *
+ * and, around those products, what a serving step does between them:
+ *
+ *   kv      : a paged cache of keys and values held in Q4_0: page tables and
+ *             slot maps from request lengths, append (quantize), read back
+ *   attn    : attention over that cache, single tokens and prompts
+ *   logits  : penalties, biases and grammar masks on the LM head's output
+ *
  * Block formats (GGUF; 32 weights per block, K a multiple of 32):
  *   Q4_0, 18 bytes: binary16 scale d (little endian) then qs[16]; qs[j] holds
  *         weight j in its low nibble and weight j+16 in its high nibble;
@@ -49,7 +56,10 @@
  * of them by then, so after QMM_ERR_CUDA the contents of its outputs (and of
  * any workspace) are undefined.  Device-side waits are bounded: a kernel that gives up
  * records QMM_ERR_TIMEOUT in the device error word, which
- * qmm_get_device_error() reports.  No entry point aborts the process.
+ * qmm_get_device_error() reports.  Page indices, slots and lengths that live
+ * in device memory are checked by the kernels: one that lies outside its
+ * array is not followed, and QMM_ERR_INDEX goes to the same word.  No entry
+ * point aborts the process.
  */
 #ifndef QMM_H
 #define QMM_H
@@ -69,8 +79,10 @@ typedef enum qmm_status {
     QMM_ERR_UNSUPPORTED = 4, /* valid arguments this build does not handle     */
     QMM_ERR_CUDA = 5,        /* a CUDA runtime call or launch failed           */
     QMM_ERR_TIMEOUT = 6,     /* a device-side wait hit its limit               */
-    QMM_ERR_SCRATCH = 7      /* the problem exceeds an entry point's fixed
+    QMM_ERR_SCRATCH = 7,     /* the problem exceeds an entry point's fixed
                                 scratch (qmm_gemm_q4_0_prefill only)          */
+    QMM_ERR_INDEX = 8        /* a page, slot or length read on the device lies
+                                outside its array (device error word only)    */
 } qmm_status;
 
 /* Same type as cudaStream_t; NULL is the legacy default stream. */
@@ -277,6 +289,186 @@ qmm_status qmm_gemm_q4_0_geglu_ws(const void *wg, const void *wu, const uint16_t
                                   uint16_t *h_bf16, int64_t m, int64_t n, int64_t k,
                                   void *workspace, size_t workspace_bytes, qmm_stream_t stream);
 
+/* ---- Paged Q4_0 cache of keys and values -------------------------------
+ * The cache holds num_pages pages of page_size token slots; slot s is place
+ * s % page_size of page s / page_size.  Keys and values are Q4_0 blocks of 32
+ * consecutive values of a head, with the codes and the scales of a block in
+ * two arrays so that both keep 16-byte alignment:
+ *   codes  : uint8  [num_pages][kv_heads][page_size][head_dim / 2]; the 16
+ *            bytes of a block are those of the GGUF block (byte j: value j
+ *            in its low, value j+16 in its high four bits)
+ *   scales : binary16 [num_pages][kv_heads][page_size][head_dim / 32]
+ *   value  = (nibble - 8) * scale
+ * head_dim is 64, 128 or 256; page_size a power of two from 16 to 1024; all
+ * four pointers 16-byte aligned; num_pages * kv_heads * page_size < 2^31
+ * (else QMM_ERR_UNSUPPORTED).  The struct lives in host memory and is read
+ * during the call. */
+typedef struct qmm_kv_q4_0 {
+    void *k_codes;
+    void *k_scales;
+    void *v_codes;
+    void *v_scales;
+    int64_t num_pages;
+    int page_size;
+    int kv_heads;
+    int head_dim;
+} qmm_kv_q4_0;
+
+/* Element types of activations where a call takes more than one. */
+typedef enum qmm_dtype { QMM_F32 = 0, QMM_BF16 = 1 } qmm_dtype;
+
+/* Page tables and slot maps of the next step, from the requests' lengths.
+ * Request b holds cached[b] tokens, in ceil(cached[b] / page_size) pages
+ * that table[b] already names, and gets added[b] more.  The call takes the
+ * pages that are then missing from the front of free_pages, request after
+ * request, and writes (all int32 unless said)
+ *   table[b][i]    the new pages only (a program that keeps one table per
+ *                  request hands it in again every step)
+ *   q_start[b]     first row of request b among the step's new tokens;
+ *                  q_start[batch] is their number
+ *   kv_len[b]      cached[b] + added[b]
+ *   slots[t]       int64, cache slot of new token t
+ *   positions[t]   its position in its request
+ *   taken[0]       pages needed from free_pages
+ * Entries t from q_start[batch] up to capacity are -1 in slots and
+ * positions, so that a captured graph may run with one capacity for every
+ * step.  Where free_pages or a row of the table is too short, the pages and
+ * slots concerned are -1; where the tokens exceed capacity, q_start stops at
+ * capacity; each of these, and a negative length (taken as 0), records
+ * QMM_ERR_INDEX.  The same call again gives the same result.
+ * Requires batch >= 1 (at most 16384, else QMM_ERR_UNSUPPORTED), page_size
+ * as above, table_width >= 1, num_free >= 0, capacity >= 0, both below 2^31;
+ * free_pages may be NULL when num_free is 0, slots and positions when
+ * capacity is 0.  No output may overlap an input or another output. */
+qmm_status qmm_kv_plan(const int32_t *cached, const int32_t *added, int batch,
+                       const int32_t *free_pages, int64_t num_free, int32_t *table,
+                       int64_t table_width, int page_size, int32_t *q_start, int32_t *kv_len,
+                       int64_t *slots, int32_t *positions, int64_t capacity, int32_t *taken,
+                       qmm_stream_t stream);
+
+/* Quantizes n tokens' keys and values into the cache.  k and v are [n] rows
+ * of kv_heads * head_dim values of type `type`, rows k_stride and v_stride
+ * elements apart (so that they may be columns of one projection's output);
+ * slots[n] names their cache slots: -1 skips the token, any other slot
+ * outside the cache is skipped and records QMM_ERR_INDEX.  Two tokens with
+ * one slot leave either's block there.
+ * Per 32 values x: with e = max x if max x >= -min x, else min x, the scale
+ * is d = binary16(e / -8), kept within +-65504, and the code of x is
+ * round(x / d) (to nearest even) + 8, within 0..15, or 8 where d is 0.  A
+ * block that holds a NaN or an infinity reads back as NaN.
+ * Requires n >= 0 (0 launches nothing), n <= 2^30, strides at least
+ * kv_heads * head_dim, k and v aligned to their type, slots to 8 bytes. */
+qmm_status qmm_kv_append_q4_0(const qmm_kv_q4_0 *cache, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, qmm_dtype type,
+                              const int64_t *slots, int64_t n, qmm_stream_t stream);
+
+/* The fp32 values of n cache slots: k_out and v_out [n][kv_heads][head_dim]
+ * (either may be NULL), each (float)(nibble - 8) * scale, exact.  Rows of
+ * slots outside the cache are 0 (-1 silently, others record QMM_ERR_INDEX).
+ * Requires n >= 0, n <= 2^30, outputs 4-byte aligned, slots 8-byte. */
+qmm_status qmm_kv_read_q4_0(const qmm_kv_q4_0 *cache, const int64_t *slots, int64_t n,
+                            float *k_out, float *v_out, qmm_stream_t stream);
+
+/* ---- Attention over the Q4_0 cache --------------------------------------
+ * Rows q_start[b] .. q_start[b+1]-1 of q are request b's new tokens, already
+ * appended: the i-th stands at position p = kv_len[b] - (q_start[b+1] -
+ * q_start[b]) + i.  Query head h reads key head h / (heads / kv_heads):
+ *   s_j    = scale * sum_d q[d] * k_j[d],  j < kv_len[b]; with causal j <= p,
+ *            with window > 0 also j > p - window
+ *   out    = sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j)
+ * A row that sees no key is 0 with lse -inf.  Keys that a row does not see
+ * do not enter it, whatever their slots hold.
+ *   q, out     [total_q] rows of heads * head_dim, q_stride and out_stride
+ *              elements apart; q_type and out_type may differ
+ *   lse        fp32 [total_q][heads], or NULL
+ *   table      int32 [batch][table_width] page indices
+ *   max_q      host-side bound of a request's new tokens
+ *   workspace  16-byte aligned device memory of at least
+ *              qmm_attn_q4_0_workspace_bytes() bytes, scratch of the call
+ * The sizes of the launch depend on the host-side arguments alone, so the
+ * call may be captured in a graph and replayed for other lengths.  Rows from
+ * q_start[batch] to total_q are not written.  A page index outside the
+ * cache, a kv_len beyond the table, more than max_q tokens or a row beyond
+ * total_q record QMM_ERR_INDEX; the keys or rows concerned are left out.
+ * Arithmetic: scores, softmax statistics and sums in fp32 and the cached
+ * values exact.  With out_type QMM_F32, q and the softmax weights enter the
+ * products in two binary16 parts (22 bits); with QMM_BF16, in one (11 bits),
+ * below the rounding of the output.
+ * Requires heads a multiple of kv_heads, heads <= 1024, batch and max_q >= 1,
+ * total_q >= 0 (0 launches nothing), window >= 0 and 0 unless causal, scale
+ * finite, strides at least heads * head_dim, pointers aligned to their type;
+ * at most 2^30 rows and batch <= 16384 (else QMM_ERR_UNSUPPORTED).  out and
+ * lse must overlap no input. */
+typedef struct qmm_attn_args {
+    const void *q;
+    int64_t q_stride;
+    qmm_dtype q_type;
+    void *out;
+    int64_t out_stride;
+    qmm_dtype out_type;
+    float *lse;
+    const int32_t *table;
+    int64_t table_width;
+    const int32_t *q_start;
+    const int32_t *kv_len;
+    int batch;
+    int64_t total_q;
+    int max_q;
+    int heads;
+    float scale;
+    int causal;
+    int window;
+    void *workspace;
+    size_t workspace_bytes;
+} qmm_attn_args;
+
+size_t qmm_attn_q4_0_workspace_bytes(const qmm_kv_q4_0 *cache, int heads);
+qmm_status qmm_attn_q4_0(const qmm_kv_q4_0 *cache, const qmm_attn_args *args,
+                         qmm_stream_t stream);
+
+/* ---- Penalties, biases and grammar masks on logits ----------------------
+ * out[i][t] for i < rows, t < vocab, from x = logits[i][t]:
+ *   1. repetition: where t occurs in row i's history, x > 0 ? x / r : x * r
+ *   2. x -= c * frequency + (c > 0 ? presence : 0), c the number of times t
+ *      occurs in the history from entry prompt_len on
+ *   3. x += the values of row i's bias entries for t, in their order
+ *   4. -inf where bit t % 32 of allowed[i][t / 32] is 0
+ *   logits, out  fp32, rows logits_stride and out_stride elements apart; out
+ *                may be logits itself (same stride), else must not overlap
+ *   history      int32; row i has entries hist_start[i] .. hist_start[i+1]-1;
+ *                ids outside the vocabulary are passed over
+ *   prompt_len   int32 [rows]; NULL: no prompt
+ *   repetition, frequency, presence   fp32 [rows]; NULL leaves the step out
+ *   bias_ids, bias_values, bias_start   entries of row i as for history
+ *   allowed      uint32 [rows][ceil(vocab / 32)]
+ * history and hist_start are NULL or given together, likewise the three of
+ * the bias; allowed may be NULL.  A start outside 0..history_len (bias_len)
+ * is moved to the nearer end and records QMM_ERR_INDEX.
+ * Requires rows >= 1 (at most 65535), vocab >= 1, both products below 2^31
+ * per row, strides at least vocab, 4-byte alignment. */
+typedef struct qmm_logits_args {
+    const float *logits;
+    int64_t logits_stride;
+    float *out;
+    int64_t out_stride;
+    int64_t rows;
+    int64_t vocab;
+    const int32_t *history;
+    const int32_t *hist_start;
+    int64_t history_len;
+    const int32_t *prompt_len;
+    const float *repetition;
+    const float *frequency;
+    const float *presence;
+    const int32_t *bias_ids;
+    const float *bias_values;
+    const int32_t *bias_start;
+    int64_t bias_len;
+    const uint32_t *allowed;
+} qmm_logits_args;
+
+qmm_status qmm_logits_adjust(const qmm_logits_args *args, qmm_stream_t stream);
+
 /* ---- Stream-ordered copies by the SMs ----------------------------------
  * Copies `bytes` bytes from src to dst in stream order, as one kernel launch
  * that loads and stores through the device's address space.  The pages have
@@ -310,7 +502,9 @@ int qmm_version(void);
 
 /* Synchronises `stream`, then returns and clears the current device's error
  * word: QMM_OK, QMM_ERR_TIMEOUT if a kernel gave up a bounded wait since the
- * last call, or QMM_ERR_CUDA if the synchronisation itself failed. */
+ * last call, QMM_ERR_INDEX if one met an index outside its array (the later
+ * of the two where both happened), or QMM_ERR_CUDA if the synchronisation
+ * itself failed. */
 qmm_status qmm_get_device_error(qmm_stream_t stream);
 
 /* Time limit, in nanoseconds of the GPU global timer, of every device-side
