@@ -1,143 +1,1079 @@
 // qmm_attn.cu -- attention over the paged Q4_0 cache (include/qmm.h,
-// qmm_attn_q4_0).
+// qmm_attn_q4_0): the streaming form, for single tokens and small groups of
+// query rows.
 //
-// One CTA per query row and head: each of its four warps takes every fourth
-// key, keeps the running maximum and sum of the softmax and its share of the
-// output, and the warps' shares are joined at the end.  A lane holds the
-// values of head_dim / 64 code bytes of a key, the same bytes for every key.
+// Mathematics.  With codes n (0..15) and scales d of 32-value blocks b,
+//   s_j = scale * sum_b d_jb * sum_i (n_jbi - 8) q_bi
+//   o_i = sum_j (p_j d_jb) (n_jbi - 8),  p_j = 2^(s_j log2(e) - M)
+// so both products have small integers on the cache's side and the scales
+// leave them: K's multiply fp32 block sums, V's join the softmax weights.
+// The integers are exact in binary16, therefore the products run on
+// mma.sync m16n8k16 with the cache as the 16-row operand, taken from the
+// 4-bit codes in registers: a code masked in place is a subnormal binary16
+// number (n * 2^-24, or 16 n * 2^-24 for the upper of two), the powers of
+// two are folded into q or undone at the end.  tcgen05 would need those
+// operands written out to shared or tensor memory first, 3.6 times the bytes
+// of the codes, for 8 columns that it cannot fill.
+//
+// Precision.  fp32 output: q and p*d enter as two binary16 parts each (22
+// bits) in neighbouring columns, four query rows to 8 columns.  bf16
+// output: one part (11 bits), eight rows.  Both are scaled by powers of two
+// so that the largest lies below 2^15 (q per row, p*d per tile).  Weights
+// below 2^-24 of a tile's largest, which binary16 would lose, take a second
+// pass over the tile's values.  V's sums run over 64 keys in the tensor
+// core, then join the fp32 running output.
+//
+// Work.  The keys of all (request, key head, row group) items, in tiles of
+// 64 keys, form one line that is cut into equal parts for all warps of a
+// grid that fills the GPU, whatever the lengths are.  Each warp streams its
+// tiles through its own shared-memory buffers (TMA boxes of code rows,
+// swizzled so that ldmatrix reads them without conflicts, and bulk copies of
+// the scales): while it works on a tile's values the next tile's keys
+// arrive, and the other way round.  An item that several warps share leaves
+// a maximum, a sum and an unnormalised output per warp; a CTA joins what its
+// warps hold, and a second kernel joins what several CTAs hold.
 #include "qmm_internal.h"
+#include "qmm_tc.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 namespace qmm {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;  // of a CTA, at most
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 64;  // keys
+constexpr float kFaint = 1.0f / 16777216.0f;  // 2^-24
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float load_one(const void *p, int64_t i, bool bf16) {
+// One head dimension's shared memory, per warp.
+template <int D, int NT, bool EXACT>
+struct Layout {
+    static constexpr int NB = D / 32;
+    static constexpr int rows = EXACT ? 4 * NT : 8 * NT;  // query rows of an item
+    static constexpr int codes = kTile * D / 2, scales = kTile * NB * 2;
+    static constexpr int p_stride = EXACT ? 72 : 68;  // floats: banks of the P stores do not collide
+    // codes first: 1024-byte aligned, and together the room of a partial
+    // record of 8 rows
+    static constexpr int v_codes = codes, k_scales = 2 * codes, v_scales = k_scales + scales;
+    static constexpr int q = v_scales + scales;              // B fragments [NT][NB][32 lanes] x 16 bytes
+    static constexpr int bias = q + NT * NB * 512;           // -8 sum q [NT][NB][8 columns]
+    static constexpr int p = bias + NT * NB * 32;            // [rows][p_stride]
+    static constexpr int raw = p + rows * p_stride * 4;
+    static constexpr int bytes = (raw + 1023) / 1024 * 1024;
+    static constexpr int warps = D == 256 && NT == 2 ? 7 : kWarps;  // as many as fit shared memory
+    static constexpr int threads = warps * 32;
+    static_assert(rows * D * 4 <= 2 * codes, "a partial record fits the code buffers");
+};
+
+// Where an item's rows go.
+struct Target {
+    int row0, rows, kv_head, group;
+};
+
+// A warp holds at most two parts of items that it shares with others: one
+// that an earlier warp began (head), and one that a later warp goes on with
+// (tail; always its last).
+enum : int {
+    kHead = 1,        // there is a head part
+    kHeadOpen = 2,    // ... which a later warp goes on with
+    kHeadLast = 4,    // ... and which is the warp's last part
+    kTail = 8,        // there is a tail part
+    kEmpty = 16       // no tiles at all
+};
+
+// What the CTA's threads share, after the warps' buffers.
+struct Shared {
+    int64_t prefix[kThreads];  // tiles before each thread's requests
+    int64_t scratch[kWarps];
+    uint64_t bars[kWarps][2];  // K tile, V tile
+    int flags[kWarps];
+    Target target[kWarps][2];     // of head and tail
+    float stat[kWarps][2][8][2];  // maximum and sum of each row
+};
+
+// A CTA's parts in global memory, the same way: flags and the tail's target.
+struct CtaParts {
+    int flags;
+    Target target;
+};
+
+struct StreamParams {
+    AttnArgs a;
+    const __half *k_scales, *v_scales;
+    int64_t num_pages;
+    int page_shift, kv_heads;
+    float *warp_records;  // [CTAs * kWarps]: head parts that are not the last
+    float *cta_records;   // [CTAs][2]: head and tail part
+    CtaParts *parts;      // [CTAs]
+    LaunchCtx ctx;
+};
+
+// Floats of one record in global memory: outputs [rows][D] and then maximum
+// and sum [rows][2], at most 8 rows of 256.
+constexpr int kRecord = 8 * 256 + 16;
+constexpr int kRecordStat = 8 * 256;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// binary16 pair, lo in the low half: toward zero, or to nearest
+__device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float half_lo(uint32_t v) { return half_bits_to_float(v & 0xFFFFu); }
+__device__ __forceinline__ float half_hi(uint32_t v) { return half_bits_to_float(v >> 16); }
+
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// floor(log2 x) of a positive normal x (-127 for zero and subnormals)
+__device__ __forceinline__ int exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
+
+__device__ __forceinline__ float load_value(const void *p, int64_t i, bool bf16) {
     if (bf16)
         return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
     return static_cast<const float *>(p)[i];
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_row_kernel(AttnArgs a, KvCache c, LaunchCtx ctx) {
-    constexpr int B = D / 64;  // code bytes per lane
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t row = blockIdx.x;
-    const int head = blockIdx.y;
-    if (row == 0 && head == 0 && threadIdx.x == 0 && a.q_start[a.batch] > a.total_q)
-        record_error(ctx, kDevErrIndex);
-    if (row >= a.q_start[a.batch] || row < a.q_start[0]) return;
-    int lo = 0, hi = a.batch;
+__device__ __forceinline__ void store_value(void *p, int64_t i, bool bf16, float v) {
+    if (bf16)
+        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<float *>(p)[i] = v;
+}
+
+// ---- the line of tiles -----------------------------------------------------------
+
+// One request as the line sees it.
+struct Request {
+    int row0, rows;      // first row of q, and rows that are there
+    int len;             // keys, within the table
+    int first;           // position of row 0 (may be negative)
+    int tile0, tiles;    // of every item of the request
+    int groups;          // row groups
+    bool bad;
+};
+
+template <int ROWS>
+__device__ __forceinline__ Request request(const StreamParams &p, int b) {
+    const AttnArgs &a = p.a;
+    Request r;
+    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], total = static_cast<int>(a.total_q);
+    const int n = max(s1 - s0, 0), len = a.kv_len[b];
+    r.row0 = min(max(s0, 0), total);
+    r.rows = min(max(min(s1, total) - r.row0, 0), n);
+    const int64_t room = a.table_width << p.page_shift;
+    r.len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), room));
+    r.first = max(len, 0) - n;
+    r.bad = s0 < 0 || s1 > total || s1 < s0 || n > a.max_q || len < 0 || len > room;
+    const int lo = a.window ? max(0, r.first - a.window + 1) : 0;
+    r.tile0 = lo / kTile;
+    r.tiles = max(1, (r.len + kTile - 1) / kTile - r.tile0);
+    r.groups = (r.rows * (a.heads / p.kv_heads) + ROWS - 1) / ROWS;
+    return r;
+}
+
+template <int ROWS>
+__device__ __forceinline__ int64_t request_tiles(const StreamParams &p, const Request &r) {
+    return static_cast<int64_t>(r.tiles) * r.groups * p.kv_heads;
+}
+
+// Fills sh.prefix; returns the number of tiles.
+template <int ROWS, int THREADS>
+__device__ __forceinline__ int64_t build_line(const StreamParams &p, Shared &sh) {
+    const int per = (p.a.batch + THREADS - 1) / THREADS;
+    const int b0 = min(p.a.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.a.batch, b0 + per);
+    int64_t mine = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = request<ROWS>(p, b);
+        mine += request_tiles<ROWS>(p, r);
+        bad |= r.bad;
+    }
+    if (bad && blockIdx.x == 0) record_error(p.ctx, kDevErrIndex);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += up;
+    }
+    if (lane == 31) sh.scratch[warp] = sum;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += sh.scratch[w];
+        total += sh.scratch[w];
+    }
+    sh.prefix[threadIdx.x] = before + sum - mine;
+    __syncthreads();
+    return total;
+}
+
+// The request that holds tile x of the line, and the tiles before it.
+template <int ROWS, int THREADS>
+__device__ __forceinline__ int find_request(const StreamParams &p, const Shared &sh, int64_t x, int64_t &before,
+                                            Request &r) {
+    int lo = 0, hi = THREADS;  // prefix[lo] <= x < prefix[hi]; equal entries: the last one holds requests
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.q_start[mid] <= row)
+        if (sh.prefix[mid] <= x)
             lo = mid;
         else
             hi = mid;
     }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    bool bad = false;
-    int64_t len = max(a.kv_len[lo], 0);
-    const int64_t pos = len - (a.q_start[lo + 1] - row);
-    bad |= a.q_start[lo + 1] - a.q_start[lo] > a.max_q;
-    if (len > (a.table_width << c.page_shift)) {
-        len = a.table_width << c.page_shift;
-        bad = true;
+    const int per = (p.a.batch + THREADS - 1) / THREADS;
+    int b = lo * per;
+    before = sh.prefix[lo];
+    for (;; ++b) {
+        r = request<ROWS>(p, b);
+        const int64_t n = request_tiles<ROWS>(p, r);
+        if (x < before + n || b + 1 >= p.a.batch) return b;
+        before += n;
     }
-    const int64_t end = a.causal ? min(len, pos + 1) : len;
-    const int64_t begin = a.window ? max(int64_t(0), pos - a.window + 1) : 0;
-    float q[2 * B], o[2 * B];
+}
+
+// An item: a key head and a group of rows of one request.
+struct Item {
+    int b, kv_head, group;
+};
+
+// ---- one warp's tiles -------------------------------------------------------------
+
+template <int D, int NT, bool EXACT>
+struct WarpState {
+    using L = Layout<D, NT, EXACT>;
+    static constexpr int NB = L::NB;
+    static constexpr int R = EXACT ? 1 : 2;  // query rows per lane and column tile
+
+    uint8_t *buf;
+    uint64_t *bars;
+    uint32_t phase[2];
+    int lane, g, t;
+    bool dead;
+    // running statistics of this lane's rows: maximum and sum of the weights
+    // 2^(s - top)
+    float top[NT][R], sum[NT][R];
+    float out[NT][NB][2][4];          // [block][even, odd value]: two columns of value i, two of 16 + i (x 16)
+    float scale_a, scale_b[NT][R];    // score = (sum * scale_a) * scale_b
+    int lo[NT][R], hi[NT][R];         // keys that the lane's rows see
+};
+
+template <int D, int NT, bool EXACT>
+__device__ __forceinline__ void issue(const StreamParams &p, const CUtensorMap *map, const __half *scales,
+                                      uint8_t *buf, int codes_at, int scales_at, uint64_t *bar, int kv_head,
+                                      int key0, int lo, int hi, int32_t pages, int page0) {
+    // Lane 0 asks for the pages of tile [key0, key0 + 64) that hold keys of
+    // [lo, hi); lane i holds the index of page page0 + i.
+    constexpr int NB = D / 32;
+    const int step = min(1 << p.page_shift, kTile);  // keys of one page in the tile
+    uint32_t bytes = 0;
+    for (int k = 0; k < kTile; k += step) {
+        const int32_t page = __shfl_sync(0xFFFFFFFFu, pages, ((key0 + k) >> p.page_shift) - page0);
+        if (key0 + k < hi && key0 + k + step > lo && page >= 0 && page < p.num_pages) bytes += step * (D / 2 + NB * 2);
+    }
+    if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(bar, bytes);
+    __syncwarp();
+    for (int k = 0; k < kTile; k += step) {
+        const int32_t page = __shfl_sync(0xFFFFFFFFu, pages, ((key0 + k) >> p.page_shift) - page0);
+        if (key0 + k < hi && key0 + k + step > lo && page >= 0 && page < p.num_pages &&
+            (threadIdx.x & 31) == 0) {
+            const int64_t row = ((static_cast<int64_t>(page) * p.kv_heads + kv_head) << p.page_shift) +
+                                ((key0 + k) & ((1 << p.page_shift) - 1));
+            tma_load_2d(smem_addr(buf + codes_at + k * (D / 2)), map, 0, static_cast<int>(row), smem_addr(bar));
+            bulk_g2s(buf + scales_at + k * NB * 2, scales + row * NB, step * NB * 2, bar);
+        }
+    }
+}
+
+// q of the item's rows as B fragments, scaled to below 2^15, with -8 times
+// the block sums (the codes are used as 0..15).
+template <int D, int NT, bool EXACT>
+__device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, EXACT> &w, const Request &r,
+                                        const Item &it) {
+    using L = Layout<D, NT, EXACT>;
+    constexpr int NB = L::NB, E = D / 32;  // values per lane: a lane's lie in one block
+    const AttnArgs &a = p.a;
+    const int heads = a.heads / p.kv_heads, all = r.rows * heads;
+    __half *frag = reinterpret_cast<__half *>(w.buf + L::q);
+    float *bias = reinterpret_cast<float *>(w.buf + L::bias);
+    const int d0 = w.lane * E, block = d0 / 32;
+    w.scale_a = a.scale * kLog2e * 16777216.0f;
+    for (int row = 0; row < L::rows; ++row) {
+        const int flat = min(it.group * L::rows + row, all - 1);  // rows past the end repeat the last
+        const int token = flat / heads, head = it.kv_head * heads + flat - token * heads;
+        const int64_t at = (static_cast<int64_t>(r.row0) + token) * a.q_stride + static_cast<int64_t>(head) * D + d0;
+        float v[E], big = 0.0f;
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-        const int byte = lane + 32 * i;
-        const int64_t at = row * a.q_stride + head * D + (byte >> 4) * 32 + (byte & 15);
-        q[2 * i] = load_one(a.q, at, a.q_bf16);
-        q[2 * i + 1] = load_one(a.q, at + 16, a.q_bf16);
-        o[2 * i] = o[2 * i + 1] = 0.0f;
+        for (int i = 0; i < E; ++i) {
+            v[i] = load_value(a.q, at + i, a.q_bf16);
+            big = fmaxf(big, fabsf(v[i]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+        const int up = min(max(14 - exponent(big), -113), 100);
+        const float f = pow2i(up);
+        const int nt = row / (L::rows / NT), in = row % (L::rows / NT);
+        float s_hi = 0.0f, s_lo = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int d5 = (d0 + i) & 31, high = d5 >> 4, quad = (d5 & 15) >> 2, e = d5 & 3;
+            const float x = v[i] * f * (high ? 0.0625f : 1.0f);
+            const int reg = (e & 1) * 2 + high;
+            const __half h = EXACT ? __float2half_rz(x) : __float2half_rn(x);
+            const float hf = __half2float(h);
+            const int col = EXACT ? in * 2 : in;
+            const int at16 = ((((nt * NB + block) * 32 + col * 4 + quad) * 4) + reg) * 2 + (e >> 1);
+            frag[at16] = h;
+            s_hi += hf * (high ? 16.0f : 1.0f);
+            if constexpr (EXACT) {
+                const __half l = __float2half_rn(x - hf);
+                frag[at16 + 32] = l;  // the next column: four lanes of four registers further
+                s_lo += __half2float(l) * (high ? 16.0f : 1.0f);
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 32 / E; o <<= 1) {
+            s_hi += __shfl_xor_sync(0xFFFFFFFFu, s_hi, o);
+            if constexpr (EXACT) s_lo += __shfl_xor_sync(0xFFFFFFFFu, s_lo, o);
+        }
+        if (w.lane % (32 / E) == 0) {
+            const float m8 = -8.0f / 16777216.0f;
+            if constexpr (EXACT) {
+                bias[(nt * NB + block) * 8 + in * 2] = s_hi * m8;
+                bias[(nt * NB + block) * 8 + in * 2 + 1] = s_lo * m8;
+            } else {
+                bias[(nt * NB + block) * 8 + in] = s_hi * m8;
+            }
+        }
+        // the lane that holds this row's scores keeps its factor and range
+        const int pos = r.first + token;
+        const int hi = a.causal ? min(r.len, pos + 1) : r.len;
+        const int lo = a.window ? max(0, pos - a.window + 1) : 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < w.R; ++k)
+                if (n == nt && (EXACT ? w.t : w.t * 2 + k) == in) {
+                    w.scale_b[n][k] = pow2i(-up);
+                    w.lo[n][k] = lo;
+                    w.hi[n][k] = hi;
+                }
     }
-    const int kv_head = head / (a.heads / c.kv_heads);
-    const uint8_t *kc = static_cast<const uint8_t *>(c.k_codes), *vc = static_cast<const uint8_t *>(c.v_codes);
-    const __half *ks = static_cast<const __half *>(c.k_scales), *vs = static_cast<const __half *>(c.v_scales);
+    __syncwarp();
+}
+
+// Scores of the tile in base-2 units: s[nt][mt][row of pair][key g, g + 8].
+template <int D, int NT, bool EXACT>
+__device__ __forceinline__ void tile_scores(WarpState<D, NT, EXACT> &w, float (&s)[NT][4][WarpState<D, NT, EXACT>::R][2]) {
+    using L = Layout<D, NT, EXACT>;
+    constexpr int NB = L::NB;
+    const uint4 *frag = reinterpret_cast<const uint4 *>(w.buf + L::q);
+    const float2 *bias = reinterpret_cast<const float2 *>(w.buf + L::bias);
+    const uint16_t *ks = reinterpret_cast<const uint16_t *>(w.buf + L::k_scales);
+    const int sw = D == 256 ? (w.lane & 7) : D == 128 ? ((w.lane >> 1) & 3) : ((w.lane >> 2) & 1);
+    const uint32_t base = smem_addr(w.buf) + w.lane * (D / 2);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        // scales of keys 32 half + {0, 8, 16, 24} + g
+        uint32_t d[4][NB / 2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint16_t *row = ks + (half * 32 + k * 8 + w.g) * NB;
+            if constexpr (NB == 8) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(row);
+                d[k][0] = v.x; d[k][1] = v.y; d[k][2] = v.z; d[k][3] = v.w;
+            } else if constexpr (NB == 4) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(row);
+                d[k][0] = v.x; d[k][1] = v.y;
+            } else {
+                d[k][0] = *reinterpret_cast<const uint32_t *>(row);
+            }
+        }
+        float acc[NT][2][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][m][i] = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            uint32_t c[4];
+            ldsm4(c, base + half * 32 * (D / 2) + ((b ^ sw) << 4));
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t x = c[2 * m], y = c[2 * m + 1], x8 = x >> 8, y8 = y >> 8;
+                const uint32_t dx = d[2 * m][b / 2], dy = d[2 * m + 1][b / 2];
+                const float df = b & 1 ? half_hi(dx) : half_lo(dx), dg = b & 1 ? half_hi(dy) : half_lo(dy);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint4 q = frag[(n * NB + b) * 32 + w.lane];
+                    const float2 c8 = bias[(n * NB + b) * 4 + w.t];
+                    float z[4] = {c8.x, c8.y, c8.x, c8.y};
+                    mma16816(z, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u, q.x, q.y);
+                    mma16816(z, x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x00F000F0u, q.z, q.w);
+                    acc[n][m][0] = fmaf(df, z[0], acc[n][m][0]);
+                    acc[n][m][1] = fmaf(df, z[1], acc[n][m][1]);
+                    acc[n][m][2] = fmaf(dg, z[2], acc[n][m][2]);
+                    acc[n][m][3] = fmaf(dg, z[3], acc[n][m][3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (EXACT) {
+                        s[n][half * 2 + m][0][h] =
+                            (acc[n][m][2 * h] + acc[n][m][2 * h + 1]) * w.scale_a * w.scale_b[n][0];
+                    } else {
+                        s[n][half * 2 + m][0][h] = acc[n][m][2 * h] * w.scale_a * w.scale_b[n][0];
+                        s[n][half * 2 + m][1][h] = acc[n][m][2 * h + 1] * w.scale_a * w.scale_b[n][1];
+                    }
+                }
+    }
+}
+
+// out = out * f + g * sum over the tile's keys of (p d) (n - 8).  EDGE: some
+// row does not see some key of the tile; such a key's scale may be anything.
+template <int D, int NT, bool EXACT, bool EDGE>
+__device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const float (&f)[NT][WarpState<D, NT, EXACT>::R],
+                                            const float (&g)[NT][WarpState<D, NT, EXACT>::R]) {
+    using L = Layout<D, NT, EXACT>;
+    constexpr int NB = L::NB;
+    const uint32_t *vs = reinterpret_cast<const uint32_t *>(w.buf + L::v_scales);
+    const float *p = reinterpret_cast<const float *>(w.buf + L::p);
+    const int token = w.lane & 15, upper = w.lane >> 4;
+    const int sw = D == 256 ? (token & 7) : D == 128 ? ((token >> 1) & 3) : ((token >> 2) & 1);
+    const uint32_t base = smem_addr(w.buf) + L::v_codes + token * (D / 2);
+    const uint32_t keep = EXACT && (w.g & 1) ? 0xFFFFE000u : 0u;  // odd columns hold the second part
+#pragma unroll
+    for (int bp = 0; bp < NB / 2; ++bp) {
+        float acc[NT][2][2][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[n][i >> 3][(i >> 2) & 1][i & 3] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t c[4];
+            ldsm4_t(c, base + ks * 16 * (D / 2) + (((2 * bp + upper) ^ sw) << 4));
+            uint32_t d[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                d[k] = vs[((ks * 16 + 2 * w.t + (k & 1) + (k >> 1) * 8) * NB) / 2 + bp];
+            float2 pw[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float *row = p + (EXACT ? n * 4 + (w.g >> 1) : n * 8 + w.g) * L::p_stride + ks * 16 + 2 * w.t;
+                pw[n][0] = *reinterpret_cast<const float2 *>(row);
+                pw[n][1] = *reinterpret_cast<const float2 *>(row + 8);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float df[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) df[k] = h ? half_hi(d[k]) : half_lo(d[k]);
+                const uint32_t x = c[2 * h], y = c[2 * h + 1], x8 = x >> 8, y8 = y >> 8;
+                // n - 8 (lower codes) and 16 (n - 8) (upper codes), times 2^-24
+                const uint32_t xa = hadd2(x & 0x000F000Fu, 0x80088008u), ya = hadd2(y & 0x000F000Fu, 0x80088008u);
+                const uint32_t xb = hadd2(x & 0x00F000F0u, 0x80808080u), yb = hadd2(y & 0x00F000F0u, 0x80808080u);
+                const uint32_t xc = hadd2(x8 & 0x000F000Fu, 0x80088008u), yc = hadd2(y8 & 0x000F000Fu, 0x80088008u);
+                const uint32_t xd = hadd2(x8 & 0x00F000F0u, 0x80808080u), yd = hadd2(y8 & 0x00F000F0u, 0x80808080u);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float v[4] = {pw[n][0].x * df[0], pw[n][0].y * df[1], pw[n][1].x * df[2], pw[n][1].y * df[3]};
+                    if constexpr (EDGE) {
+                        v[0] = pw[n][0].x == 0.0f ? 0.0f : v[0];
+                        v[1] = pw[n][0].y == 0.0f ? 0.0f : v[1];
+                        v[2] = pw[n][1].x == 0.0f ? 0.0f : v[2];
+                        v[3] = pw[n][1].y == 0.0f ? 0.0f : v[3];
+                    }
+                    uint32_t b0, b1;
+                    if constexpr (EXACT) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] -= __uint_as_float(__float_as_uint(v[k]) & keep);
+                        b0 = pack_rz(v[0], v[1]);
+                        b1 = pack_rz(v[2], v[3]);
+                    } else {
+                        b0 = pack_rn(v[0], v[1]);
+                        b1 = pack_rn(v[2], v[3]);
+                    }
+                    mma16816(acc[n][h][0], xa, xb, ya, yb, b0, b1);
+                    mma16816(acc[n][h][1], xc, xd, yc, yd, b0, b1);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w.out[n][2 * bp + h][m][i] = fmaf(w.out[n][2 * bp + h][m][i], f[n][EXACT ? 0 : i & 1],
+                                                          acc[n][h][m][i] * g[n][EXACT ? 0 : i & 1]);
+    }
+}
+
+// Tiles [t0, t1) of an item.
+template <int D, int NT, bool EXACT>
+__device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMap *kmap, const CUtensorMap *vmap,
+                                         WarpState<D, NT, EXACT> &w, const Request &r, const Item &it, int t0,
+                                         int t1) {
+    using L = Layout<D, NT, EXACT>;
+    constexpr int NB = L::NB, R = WarpState<D, NT, EXACT>::R;
+    const AttnArgs &a = p.a;
     const float ninf = __uint_as_float(0xFF800000u);
-    float m = ninf, l = 0.0f;
-    for (int64_t j = begin + warp; j < end; j += kWarps) {
-        const int32_t page = a.table[lo * a.table_width + (j >> c.page_shift)];
-        if (page < 0 || page >= c.num_pages) {
-            bad = true;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            w.top[n][k] = ninf;
+            w.sum[n][k] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < NB * 8; ++i) w.out[n][i >> 3][(i >> 2) & 1][i & 3] = 0.0f;
+    }
+    // the keys that any, and that every, row of the group sees
+    const int heads = a.heads / p.kv_heads, all = r.rows * heads;
+    const int pos0 = r.first + it.group * L::rows / heads;
+    const int pos1 = r.first + (min((it.group + 1) * L::rows, all) - 1) / heads;
+    const int lo = a.window ? max(0, pos0 - a.window + 1) : 0, hi = a.causal ? min(r.len, pos1 + 1) : r.len;
+    const int lo_all = a.window ? max(0, pos1 - a.window + 1) : 0, hi_all = a.causal ? min(r.len, pos0 + 1) : r.len;
+    t0 = max(t0, lo / kTile - r.tile0);
+    t1 = min(t1, (hi + kTile - 1) / kTile - r.tile0);
+    if (w.dead) return;
+
+    // page indices of the tiles ahead: lane i holds page page0 + i
+    const int32_t *table = a.table + it.b * a.table_width;
+    int page0 = 0;
+    int32_t pages = -1;
+    auto fetch = [&](int tile) {  // pages of `tile` and after
+        page0 = ((r.tile0 + tile) * kTile) >> p.page_shift;
+        const int i = page0 + w.lane;
+        pages = i < a.table_width ? table[i] : -1;
+    };
+    const int tile_pages = max(1, kTile >> p.page_shift);
+    auto ahead = [&](int tile) {  // makes `tile`'s pages known
+        if ((((r.tile0 + tile) * kTile) >> p.page_shift) + tile_pages > page0 + 32) fetch(tile);
+    };
+    auto issue_k = [&](int tile) {
+        issue<D, NT, EXACT>(p, kmap, p.k_scales, w.buf, 0, L::k_scales, w.bars, it.kv_head, (r.tile0 + tile) * kTile,
+                            lo, hi, pages, page0);
+    };
+    auto issue_v = [&](int tile) {
+        issue<D, NT, EXACT>(p, vmap, p.v_scales, w.buf, L::v_codes, L::v_scales, w.bars + 1, it.kv_head,
+                            (r.tile0 + tile) * kTile, lo, hi, pages, page0);
+    };
+    if (t0 < t1) {
+        fetch(t0);
+        issue_k(t0);
+        issue_v(t0);
+    }
+    stage_q<D, NT, EXACT>(p, w, r, it);
+    for (int tile = t0; tile < t1; ++tile) {
+        const int key0 = (r.tile0 + tile) * kTile;
+        // 16-key groups whose page can be read
+        int live = 15;
+        for (int k = 0; k < 4; ++k) {
+            const int32_t page = __shfl_sync(0xFFFFFFFFu, pages, ((key0 + 16 * k) >> p.page_shift) - page0);
+            if ((page < 0 || page >= p.num_pages) && key0 + 16 * k < hi && key0 + 16 * k + 16 > lo) live &= ~(1 << k);
+        }
+        if (live != 15 && w.lane == 0) record_error(p.ctx, kDevErrIndex);
+        const bool edge = live != 15 || key0 < lo_all || key0 + kTile > hi_all;
+
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(w.bars, w.phase[0], p.ctx))) w.dead = true;
+        w.phase[0] ^= 1;
+        float s[NT][4][R][2];
+        tile_scores<D, NT, EXACT>(w, s);
+        __syncwarp();
+        const bool asked = tile + 1 < t1 && !w.dead;
+        if (asked) {
+            ahead(tile + 1);
+            issue_k(tile + 1);
+        }
+        if (edge) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int k = 0; k < R; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int key = key0 + 16 * m + 8 * h + w.g;
+                            if (key < w.lo[n][k] || key >= w.hi[n][k] || !((live >> m) & 1)) s[n][m][k][h] = ninf;
+                        }
+        }
+        // maxima of the tile's scores, and the weights relative to them
+        float top[NT][R];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                float v = ninf;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) v = fmaxf(v, fmaxf(s[n][m][k][0], s[n][m][k][1]));
+                v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+                top[n][k] = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+            }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(w.bars + 1, w.phase[1], p.ctx))) w.dead = true;
+        w.phase[1] ^= 1;
+        uint32_t *vs = reinterpret_cast<uint32_t *>(w.buf + L::v_scales);
+        if (edge) {  // scales of keys that no row sees may hold anything
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int i = w.lane + 32 * k;
+                if (key0 + i < lo || key0 + i >= hi || !((live >> (i >> 4)) & 1))
+#pragma unroll
+                    for (int j = 0; j < NB / 2; ++j) vs[i * (NB / 2) + j] = 0u;
+            }
+            fence_proxy_async_smem();  // before a later copy into the same place
+            __syncwarp();
+        }
+        // the largest |d| of the tile: NaN is passed over, infinity counts as 65504
+        uint32_t big = 0u;
+#pragma unroll
+        for (int i = 0; i < kTile * NB / 64; ++i) {
+            const uint32_t v = vs[i * 32 + w.lane] & 0x7FFF7FFFu;
+            asm("max.f16x2 %0, %1, %2;" : "=r"(big) : "r"(big), "r"(v));
+        }
+        float dmax = fminf(fmaxf(half_lo(big), half_hi(big)), 65504.0f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dmax = fmaxf(dmax, __shfl_xor_sync(0xFFFFFFFFu, dmax, o));
+        const int room = dmax > 0.0f ? 14 - exponent(dmax) : 0;
+        const float up = pow2i(room);
+        // f: factor of what is there already; g: of this tile's products
+        float f[NT][R], g[NT][R];
+        float *pp = reinterpret_cast<float *>(w.buf + L::p);
+        bool faint = false;  // some weight lies below 2^-24
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const float here = top[n][k] == ninf ? 0.0f : top[n][k], now = fmaxf(w.top[n][k], top[n][k]);
+                f[n][k] = w.top[n][k] == ninf ? 0.0f : exp2_fast(w.top[n][k] - now);
+                const float fresh = top[n][k] == ninf ? 0.0f : exp2_fast(top[n][k] - now);
+                g[n][k] = fresh * pow2i(24 - room);
+                w.top[n][k] = now;
+                float sum = 0.0f;
+                float *row = pp + (EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k) * L::p_stride + w.g;
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float e = exp2_fast(s[n][m][k][h] - here);
+                        s[n][m][k][h] = e;
+                        sum += e;
+                        const bool low = e < kFaint;
+                        faint |= low && e > 0.0f;
+                        row[16 * m + 8 * h] = low ? 0.0f : e * up;
+                    }
+                w.sum[n][k] = fmaf(w.sum[n][k], f[n][k], sum * fresh);
+            }
+        __syncwarp();
+        if (edge)
+            tile_values<D, NT, EXACT, true>(w, f, g);
+        else
+            tile_values<D, NT, EXACT, false>(w, f, g);
+        __syncwarp();
+        // Weights far below the tile's largest would fall out of binary16's
+        // range, which shows where the large ones meet zeros: they go in
+        // passes of their own, raised by 2^24 each time.
+        for (float raise = 1.0f / kFaint; __any_sync(0xFFFFFFFFu, faint); raise *= 1.0f / kFaint) {
+            faint = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    f[n][k] = 1.0f;
+                    g[n][k] *= kFaint;
+                    float *row = pp + (EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k) * L::p_stride + w.g;
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float e = s[n][m][k][h] * raise;
+                            const bool low = e < kFaint;
+                            faint |= low && e > 0.0f;
+                            row[16 * m + 8 * h] = low || !(e < 1.0f) ? 0.0f : e * up;
+                        }
+                }
+            __syncwarp();
+            tile_values<D, NT, EXACT, true>(w, f, g);
+            __syncwarp();
+        }
+        if (w.dead) {  // a wait gave up: take no more tiles, let the copy that is under way end
+            if (asked) mbar_wait(w.bars, w.phase[0], p.ctx);
+            break;
+        }
+        if (tile + 1 < t1) issue_v(tile + 1);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            w.sum[n][k] += __shfl_xor_sync(0xFFFFFFFFu, w.sum[n][k], 4);
+            w.sum[n][k] += __shfl_xor_sync(0xFFFFFFFFu, w.sum[n][k], 8);
+            w.sum[n][k] += __shfl_xor_sync(0xFFFFFFFFu, w.sum[n][k], 16);
+        }
+}
+
+// The lane's accumulators as outputs: fn(row, column, value), unnormalised.
+template <int D, int NT, bool EXACT, typename Fn>
+__device__ __forceinline__ void each_output(const WarpState<D, NT, EXACT> &w, Fn fn) {
+    constexpr int NB = D / 32;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int d = 32 * b + 16 * h + 2 * w.g + m;
+                    const float down = h ? 0.0625f : 1.0f;
+                    const float x = w.out[n][b][m][2 * h] * down, y = w.out[n][b][m][2 * h + 1] * down;
+                    if constexpr (EXACT) {
+                        fn(n, 0, n * 4 + w.t, d, x + y);
+                    } else {
+                        fn(n, 0, n * 8 + 2 * w.t, d, x);
+                        fn(n, 1, n * 8 + 2 * w.t + 1, d, y);
+                    }
+                }
+}
+
+__device__ __forceinline__ Target target_of(const Request &r, const Item &it) {
+    return Target{r.row0, r.rows, it.kv_head, it.group};
+}
+
+// The row of q, and the head, that row `row` of an item stands for; false for
+// rows past the request's last.
+template <int ROWS>
+__device__ __forceinline__ bool locate(const StreamParams &p, const Target &to, int row, int64_t &at, int &head) {
+    const int heads = p.a.heads / p.kv_heads, flat = to.group * ROWS + row;
+    if (flat >= to.rows * heads) return false;
+    const int token = flat / heads;
+    head = to.kv_head * heads + flat - token * heads;
+    at = static_cast<int64_t>(to.row0) + token;
+    return true;
+}
+
+template <int D, int ROWS>
+__device__ __forceinline__ void write_out(const StreamParams &p, const Target &to, int row, int d, float v, float sum) {
+    int64_t at;
+    int head;
+    if (locate<ROWS>(p, to, row, at, head))
+        store_value(p.a.out, at * p.a.out_stride + static_cast<int64_t>(head) * D + d, p.a.out_bf16,
+                    sum == 0.0f ? 0.0f : v / sum);
+}
+
+template <int ROWS>
+__device__ __forceinline__ void write_lse(const StreamParams &p, const Target &to, int row, float top, float sum) {
+    int64_t at;
+    int head;
+    if (p.a.lse && locate<ROWS>(p, to, row, at, head))
+        p.a.lse[at * p.a.heads + head] = sum == 0.0f ? __uint_as_float(0xFF800000u) : (top + log2f(sum)) * kLn2;
+}
+
+template <int D, int NT, bool EXACT>
+__global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), D == 256 ? 1 : D == 128 ? 2 : 3)
+    attn_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const StreamParams p) {
+    using L = Layout<D, NT, EXACT>;
+    constexpr int R = WarpState<D, NT, EXACT>::R, ROWS = L::rows, W = L::warps;
+    extern __shared__ uint8_t attn_smem[];
+    uint8_t *base = attn_smem + ((1024u - (smem_addr(attn_smem) & 1023u)) & 1023u);
+    Shared &sh = *reinterpret_cast<Shared *>(base + W * L::bytes);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < W * 2; ++i) mbar_init(&sh.bars[0][0] + i, 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    asm volatile("fence.proxy.async.global;" ::: "memory");  // the cache's last writer used plain stores
+    const int64_t total = build_line<ROWS, L::threads>(p, sh);
+
+    WarpState<D, NT, EXACT> w;
+    w.buf = base + warp * L::bytes;
+    w.bars = sh.bars[warp];
+    w.phase[0] = w.phase[1] = 0;
+    w.lane = threadIdx.x & 31;
+    w.g = w.lane >> 2;
+    w.t = w.lane & 3;
+    w.dead = false;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * W;
+    const int64_t me = static_cast<int64_t>(blockIdx.x) * W + warp;
+    const int64_t x0 = total * me / warps, x1 = total * (me + 1) / warps;
+    int flags = x0 < x1 ? 0 : kEmpty;
+    for (int64_t x = x0; x < x1;) {
+        int64_t before;
+        Request r;
+        Item it;
+        it.b = find_request<ROWS, L::threads>(p, sh, x, before, r);
+        const int item = static_cast<int>((x - before) / r.tiles);
+        it.kv_head = item / r.groups;
+        it.group = item - it.kv_head * r.groups;
+        const int t0 = static_cast<int>(x - before - static_cast<int64_t>(item) * r.tiles);
+        const int t1 = static_cast<int>(min(static_cast<int64_t>(r.tiles), t0 + (x1 - x)));
+        run_part<D, NT, EXACT>(p, &kmap, &vmap, w, r, it, t0, t1);
+        x += t1 - t0;
+        const Target to = target_of(r, it);
+        if (t0 == 0 && t1 == r.tiles) {
+            each_output<D, NT, EXACT>(w, [&](int n, int k, int row, int d, float v) {
+                write_out<D, ROWS>(p, to, row, d, v, w.sum[n][k]);
+            });
+            if (w.g == 0)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < R; ++k)
+                        write_lse<ROWS>(p, to, EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k, w.top[n][k], w.sum[n][k]);
             continue;
         }
-        const int64_t r = ((static_cast<int64_t>(page) * c.kv_heads + kv_head) << c.page_shift) +
-                          (j & ((int64_t(1) << c.page_shift) - 1));
-        float s = 0.0f;
+        // the warp's last part stays in its code buffers, which no later tile
+        // needs; an earlier one goes to global memory
+        const bool head = t0 > 0;
+        float *rec = x >= x1 ? reinterpret_cast<float *>(w.buf) : p.warp_records + me * kRecord;
+        each_output<D, NT, EXACT>(w, [&](int, int, int row, int d, float v) { rec[row * D + d] = v; });
+        if (w.g == 0)
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int byte = lane + 32 * i;
-            const uint32_t w = kc[r * (D / 2) + byte];
-            const float d = __half2float(ks[r * (D / 32) + (byte >> 4)]);
-            s = fmaf(q[2 * i], (static_cast<float>(w & 15u) - 8.0f) * d, s);
-            s = fmaf(q[2 * i + 1], (static_cast<float>(w >> 4) - 8.0f) * d, s);
-        }
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-        s *= a.scale;
-        const float mn = fmaxf(m, s);
-        const float ref = mn == ninf ? 0.0f : mn;
-        const float f = expf(m - ref), w = expf(s - ref);
-        m = mn;
-        l = fmaf(l, f, w);
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int byte = lane + 32 * i;
-            const uint32_t b = vc[r * (D / 2) + byte];
-            const float d = __half2float(vs[r * (D / 32) + (byte >> 4)]);
-            o[2 * i] = fmaf(o[2 * i], f, w * ((static_cast<float>(b & 15u) - 8.0f) * d));
-            o[2 * i + 1] = fmaf(o[2 * i + 1], f, w * ((static_cast<float>(b >> 4) - 8.0f) * d));
-        }
-    }
-    __shared__ float share[kWarps][D];
-    __shared__ float stat[kWarps][2];
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-        const int byte = lane + 32 * i;
-        share[warp][(byte >> 4) * 32 + (byte & 15)] = o[2 * i];
-        share[warp][(byte >> 4) * 32 + (byte & 15) + 16] = o[2 * i + 1];
-    }
-    if (lane == 0) {
-        stat[warp][0] = m;
-        stat[warp][1] = l;
-        if (bad) record_error(ctx, kDevErrIndex);
-    }
-    __syncthreads();
-    float top = ninf, sum = 0.0f, f[kWarps];
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][0]);
-    for (int w = 0; w < kWarps; ++w) {
-        f[w] = top == ninf ? 0.0f : expf(stat[w][0] - top);
-        sum = fmaf(f[w], stat[w][1], sum);
-    }
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-        float y = 0.0f;
-        for (int w = 0; w < kWarps; ++w) y = fmaf(f[w], share[w][d], y);
-        if (top != ninf) y /= sum;
-        const int64_t at = row * a.out_stride + head * D + d;
-        if (a.out_bf16)
-            static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(y);
+                for (int k = 0; k < R; ++k) {
+                    float *s = sh.stat[warp][head ? 0 : 1][EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k];
+                    s[0] = w.top[n][k];
+                    s[1] = w.sum[n][k];
+                }
+        if (w.lane == 0) sh.target[warp][head ? 0 : 1] = to;
+        if (head)
+            flags |= kHead | (t1 < r.tiles ? kHeadOpen : 0) | (x >= x1 ? kHeadLast : 0);
         else
-            static_cast<float *>(a.out)[at] = y;
+            flags |= kTail;
     }
-    if (a.lse && threadIdx.x == 0) a.lse[row * a.heads + head] = top == ninf ? ninf : top + logf(sum);
+    if (w.lane == 0) sh.flags[warp] = flags;
+    __syncthreads();
+
+    // Join the warps' parts.  A chain begins with a tail, or with the head of
+    // the first warp that has tiles, and goes on over heads while they are
+    // open; empty warps may lie between.
+    CtaParts mine = {kEmpty, {}};
+    for (int c = 0; c < W; ++c) {
+        const int fc = sh.flags[c];
+        if (fc & kEmpty) continue;
+        const bool first = mine.flags == kEmpty;
+        if (first) mine.flags = 0;
+        for (int kind = first && (fc & kHead) ? 0 : 1; kind < 2; ++kind) {
+            if (kind == 1 && !(fc & kTail)) continue;
+            bool open = kind == 1 || (fc & kHeadOpen);
+            unsigned members = 0;
+            for (int j = c + 1; j < W && open; ++j) {
+                if (sh.flags[j] & kEmpty) continue;
+                members |= 1u << j;
+                open = sh.flags[j] & kHeadOpen;
+            }
+            const Target to = sh.target[c][kind];
+            const bool whole = kind == 1 && !open;
+            float *dst = p.cta_records + (static_cast<int64_t>(blockIdx.x) * 2 + kind) * kRecord;
+            for (int i = threadIdx.x; i < ROWS * D; i += L::threads) {
+                const int row = i / D, d = i - row * D;
+                const float *sc = sh.stat[c][kind][row];
+                float top = sc[0];
+                for (int j = c + 1; j < W; ++j)
+                    if ((members >> j) & 1u) top = fmaxf(top, sh.stat[j][0][row][0]);
+                const float ref = top == __uint_as_float(0xFF800000u) ? 0.0f : top;
+                float v = 0.0f, sum = 0.0f;
+                for (int j = c; j < W; ++j) {
+                    if (j > c && !((members >> j) & 1u)) continue;
+                    const int kj = j == c ? kind : 0;
+                    const float *rec = kj == 1 || (sh.flags[j] & kHeadLast)
+                                           ? reinterpret_cast<const float *>(base + j * L::bytes)
+                                           : p.warp_records + (static_cast<int64_t>(blockIdx.x) * W + j) * kRecord;
+                    const float f = exp2_fast(sh.stat[j][kj][row][0] - ref);
+                    v = fmaf(f, rec[i], v);
+                    sum = fmaf(f, sh.stat[j][kj][row][1], sum);
+                }
+                if (whole) {
+                    write_out<D, ROWS>(p, to, row, d, v, sum);
+                    if (d == 0) write_lse<ROWS>(p, to, row, top, sum);
+                } else {
+                    dst[i] = v;
+                    if (d == 0) {
+                        dst[kRecordStat + 2 * row] = top;
+                        dst[kRecordStat + 2 * row + 1] = sum;
+                    }
+                }
+            }
+            if (!whole) {
+                if (kind == 0) {
+                    mine.flags |= kHead | (open ? kHeadOpen : 0);
+                } else {
+                    mine.flags |= kTail;
+                    mine.target = to;
+                }
+            }
+        }
+    }
+    if (threadIdx.x == 0) p.parts[blockIdx.x] = mine;
+}
+
+// Joins the items that several CTAs hold: CTA x of this grid the one that CTA
+// x's tail begins, 256 outputs of it per y.
+constexpr int kMaxCtas = 1024;
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(const StreamParams p) {
+    constexpr int RB = kThreads / D;  // rows of a CTA
+    __shared__ int flags[kMaxCtas];
+    __shared__ int last;
+    __shared__ float tops[RB];
+    __shared__ float weight[RB][kMaxCtas];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int n = gridDim.x, c = blockIdx.x;
+    if (!(p.parts[c].flags & kTail)) return;
+    for (int i = threadIdx.x; i < n; i += kThreads) flags[i] = p.parts[i].flags;
+    if (threadIdx.x == 0) last = n - 1;
+    __syncthreads();
+    // the chain ends at the first head after c that is not open
+    for (int i = c + 1 + threadIdx.x; i < n; i += kThreads)
+        if (!(flags[i] & kEmpty) && !(flags[i] & kHeadOpen)) atomicMin(&last, i);
+    __syncthreads();
+    const int end = last;
+    const int sub = threadIdx.x / D, d = threadIdx.x - sub * D, row = blockIdx.y * RB + sub;
+    auto record = [&](int j) { return p.cta_records + (static_cast<int64_t>(j) * 2 + (j == c ? 1 : 0)) * kRecord; };
+    // each row's maximum and weights, by the row's threads (whole warps)
+    const float ninf = __uint_as_float(0xFF800000u);
+    float top = ninf;
+    for (int j = c + (d & 31); j <= end; j += 32)
+        if (j == c || (flags[j] & kHead)) top = fmaxf(top, record(j)[kRecordStat + 2 * row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float ref = top == ninf ? 0.0f : top;
+    float sum = 0.0f;
+    for (int j = c + (d & 31); j <= end; j += 32) {
+        float f = 0.0f;
+        if (j == c || (flags[j] & kHead)) {
+            f = exp2_fast(record(j)[kRecordStat + 2 * row] - ref);
+            sum = fmaf(f, record(j)[kRecordStat + 2 * row + 1], sum);
+        }
+        if (d < 32) weight[sub][j - c] = f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (d == 0) tops[sub] = sum;
+    __syncthreads();
+    sum = tops[sub];
+    float v = 0.0f;
+#pragma unroll 8
+    for (int j = c; j <= end; ++j)
+        if (j == c || (flags[j] & kHead)) v = fmaf(weight[sub][j - c], record(j)[row * D + d], v);
+    const Target to = p.parts[c].target;
+    write_out<D, ROWS>(p, to, row, d, v, sum);
+    if (d == 0) write_lse<ROWS>(p, to, row, top, sum);
+}
+
+int ctas_per_sm(int dim) { return dim == 256 ? 1 : dim == 128 ? 2 : 3; }
+
+template <int D, int NT, bool EXACT>
+cudaError_t launch_stream(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    using L = Layout<D, NT, EXACT>;
+    static int limits[kMaxDevices];
+    constexpr size_t smem = static_cast<size_t>(L::warps) * L::bytes + sizeof(Shared) + 1024;
+    static_assert(smem <= 232448, "shared memory per CTA");
+    auto *kernel = attn_stream_kernel<D, NT, EXACT>;
+    cudaError_t e = ensure_smem(kernel, smem, false, limits);
+    if (e != cudaSuccess) return e;
+    const uint64_t rows = static_cast<uint64_t>(c.num_pages) * c.kv_heads << c.page_shift;
+    const uint32_t box = static_cast<uint32_t>(std::min(1 << c.page_shift, kTile));
+    const CUtensorMapSwizzle sw = D == 256   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                             : CU_TENSOR_MAP_SWIZZLE_32B;
+    CUtensorMap maps[2];
+    const void *codes[2] = {c.k_codes, c.v_codes};
+    for (int i = 0; i < 2; ++i)
+        if (!encode_tmap_2d(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, codes[i], D / 2, rows, D / 2, D / 2, box, sw))
+            return cudaErrorInvalidValue;
+    const int ctas = std::min(device_sm_count() * ctas_per_sm(D), kMaxCtas);
+    StreamParams p = {};
+    p.a = a;
+    p.k_scales = static_cast<const __half *>(c.k_scales);
+    p.v_scales = static_cast<const __half *>(c.v_scales);
+    p.num_pages = c.num_pages;
+    p.page_shift = c.page_shift;
+    p.kv_heads = c.kv_heads;
+    p.warp_records = static_cast<float *>(a.workspace);
+    p.cta_records = p.warp_records + static_cast<size_t>(ctas) * kWarps * kRecord;
+    p.parts = reinterpret_cast<CtaParts *>(p.cta_records + static_cast<size_t>(ctas) * 2 * kRecord);
+    p.ctx = ctx;
+    e = launch_kernel(kernel, dim3(ctas), dim3(L::threads), smem, stream, 1, maps[0], maps[1], p);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(attn_join_kernel<D, L::rows>, dim3(ctas, L::rows * D / kThreads), dim3(kThreads), 0, stream,
+                         1, p);
+}
+
+template <int D>
+cudaError_t launch_dim(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    if (a.out_bf16) return launch_stream<D, 1, false>(c, a, stream, ctx);
+    // four rows fill a column tile; with more, two tiles share the codes' work
+    if (static_cast<int64_t>(a.max_q) * (a.heads / c.kv_heads) <= 4) return launch_stream<D, 1, true>(c, a, stream, ctx);
+    return launch_stream<D, 2, true>(c, a, stream, ctx);
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(const KvCache &, int) { return 0; }
+size_t attn_workspace_bytes(const KvCache &c, int) {
+    const size_t ctas = std::min(device_sm_count() * ctas_per_sm(c.head_dim), kMaxCtas);
+    return ctas * ((kWarps + 2) * kRecord * sizeof(float) + sizeof(CtaParts));
+}
 
 cudaError_t launch_attn(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
-    auto *kernel = c.head_dim == 64 ? attn_row_kernel<64> : c.head_dim == 128 ? attn_row_kernel<128> : attn_row_kernel<256>;
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(a.total_q), a.heads), dim3(kWarps * 32), 0, stream, 1, a, c, ctx);
+    if (c.head_dim == 64) return launch_dim<64>(c, a, stream, ctx);
+    if (c.head_dim == 128) return launch_dim<128>(c, a, stream, ctx);
+    return launch_dim<256>(c, a, stream, ctx);
 }
 
 }  // namespace qmm
