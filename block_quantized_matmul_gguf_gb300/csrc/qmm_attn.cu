@@ -55,18 +55,24 @@ struct Layout {
     static constexpr int NB = D / 32;
     static constexpr int rows = EXACT ? 4 * NT : 8 * NT;  // query rows of an item
     static constexpr int codes = kTile * D / 2, scales = kTile * NB * 2;
-    static constexpr int p_stride = EXACT ? 72 : 68;  // floats: banks of the P stores do not collide
-    // codes first: 1024-byte aligned, and together the room of a partial
-    // record of 8 rows
-    static constexpr int v_codes = codes, k_scales = 2 * codes, v_scales = k_scales + scales;
-    static constexpr int q = v_scales + scales;              // B fragments [NT][NB][32 lanes] x 16 bytes
-    static constexpr int bias = q + NT * NB * 512;           // -8 sum q [NT][NB][8 columns]
-    static constexpr int p = bias + NT * NB * 32;            // [rows][p_stride]
-    static constexpr int raw = p + rows * p_stride * 4;
-    static constexpr int bytes = (raw + 1023) / 1024 * 1024;
-    static constexpr int warps = D == 256 && NT == 2 ? 7 : kWarps;  // as many as fit shared memory
+    static constexpr int p_stride = kTile + 8;  // floats
+    // the code buffers lie in front of everything, 1024-byte aligned; together
+    // they have room for a partial record
+    static constexpr int code_bytes = 2 * codes;
+    // the rest, from its own start
+    static constexpr int v_scales = scales;
+    static constexpr int q = v_scales + scales;          // B fragments [NT][NB][32 lanes] x 16 bytes
+    static constexpr int bias = q + NT * NB * 512;       // -8 sum q [NT][NB][4 lanes] x {c0, c1, c0, c1}
+    static constexpr int d = bias + NT * NB * 64;        // V's scales by block: pairs of keys, binary16 or fp32
+    static constexpr int p = d + NB * kTile * (EXACT ? 4 : 2);  // weights [rows][p_stride], EXACT only
+    static constexpr int rest_bytes = p + (EXACT ? rows * p_stride * 4 : 0);
+    // CTAs on an SM: as the registers of the accumulators allow
+    static constexpr int ctas = D == 256 ? 1 : D == 128 && NT == 2 ? 1 : 2;
+    static constexpr int fit = (232448 / ctas - 1024 - 4096) / (code_bytes + rest_bytes);
+    static constexpr int warps = fit < kWarps ? fit : kWarps;  // as many as fit shared memory
     static constexpr int threads = warps * 32;
-    static_assert(rows * D * 4 <= 2 * codes, "a partial record fits the code buffers");
+    static_assert(rows * D * 4 <= code_bytes, "a partial record fits the code buffers");
+    static_assert(rest_bytes % 16 == 0, "alignment of the next warp's part");
 };
 
 // Where an item's rows go.
@@ -133,12 +139,19 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+// d = a b + c: 16 x 16 by 16 x 8, binary16 with fp32 sums
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+// the transpose of an 8 x 8 matrix of binary16, a row's pair per lane
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 // binary16 pair, lo in the low half: toward zero, or to nearest
 __device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
@@ -156,8 +169,15 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float half_lo(uint32_t v) { return half_bits_to_float(v & 0xFFFFu); }
-__device__ __forceinline__ float half_hi(uint32_t v) { return half_bits_to_float(v >> 16); }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// 0xFFFF in each half that is not zero (NaN is not)
+__device__ __forceinline__ uint32_t not_zero2(uint32_t v) {
+    return __hneu2_mask(*reinterpret_cast<const __half2 *>(&v), __half2half2(__ushort_as_half(0)));
+}
 
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
@@ -282,7 +302,7 @@ struct WarpState {
     static constexpr int NB = L::NB;
     static constexpr int R = EXACT ? 1 : 2;  // query rows per lane and column tile
 
-    uint8_t *buf;
+    uint8_t *codes, *rest;
     uint64_t *bars;
     uint32_t phase[2];
     int lane, g, t;
@@ -290,36 +310,48 @@ struct WarpState {
     // running statistics of this lane's rows: maximum and sum of the weights
     // 2^(s - top)
     float top[NT][R], sum[NT][R];
-    float out[NT][NB][2][4];          // [block][even, odd value]: two columns of value i, two of 16 + i (x 16)
-    float scale_a, scale_b[NT][R];    // score = (sum * scale_a) * scale_b
+    float2 out[NT][NB][2][2];         // [block][even, odd value][value i, 16 + i (x 16)]: two columns
+    float unit[NT][R];                // score = sum * unit > 0
     int lo[NT][R], hi[NT][R];         // keys that the lane's rows see
 };
 
-template <int D, int NT, bool EXACT>
+// The pages of one tile that hold keys [lo, hi): a 4-bit set of its 16-key
+// groups that can be read, and each page's index by shuffle.
+struct Pages {
+    int32_t lane_page;  // lane i: page first + i of the request
+    int first;
+};
+
+// Asks for the codes and scales of tile [key0, key0 + 64).
+template <int D>
 __device__ __forceinline__ void issue(const StreamParams &p, const CUtensorMap *map, const __half *scales,
-                                      uint8_t *buf, int codes_at, int scales_at, uint64_t *bar, int kv_head,
-                                      int key0, int lo, int hi, int32_t pages, int page0) {
-    // Lane 0 asks for the pages of tile [key0, key0 + 64) that hold keys of
-    // [lo, hi); lane i holds the index of page page0 + i.
+                                      uint8_t *codes_to, uint8_t *scales_to, uint64_t *bar, int kv_head, int key0,
+                                      int lo, int hi, const Pages &pages) {
     constexpr int NB = D / 32;
-    const int step = min(1 << p.page_shift, kTile);  // keys of one page in the tile
-    uint32_t bytes = 0;
-    for (int k = 0; k < kTile; k += step) {
-        const int32_t page = __shfl_sync(0xFFFFFFFFu, pages, ((key0 + k) >> p.page_shift) - page0);
-        if (key0 + k < hi && key0 + k + step > lo && page >= 0 && page < p.num_pages) bytes += step * (D / 2 + NB * 2);
-    }
-    if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(bar, bytes);
-    __syncwarp();
-    for (int k = 0; k < kTile; k += step) {
-        const int32_t page = __shfl_sync(0xFFFFFFFFu, pages, ((key0 + k) >> p.page_shift) - page0);
-        if (key0 + k < hi && key0 + k + step > lo && page >= 0 && page < p.num_pages &&
-            (threadIdx.x & 31) == 0) {
-            const int64_t row = ((static_cast<int64_t>(page) * p.kv_heads + kv_head) << p.page_shift) +
-                                ((key0 + k) & ((1 << p.page_shift) - 1));
-            tma_load_2d(smem_addr(buf + codes_at + k * (D / 2)), map, 0, static_cast<int>(row), smem_addr(bar));
-            bulk_g2s(buf + scales_at + k * NB * 2, scales + row * NB, step * NB * 2, bar);
+    const int lane = threadIdx.x & 31, shift = p.page_shift;
+    auto copy = [&](int32_t page, int k, int n) {
+        const int64_t row = ((static_cast<int64_t>(page) * p.kv_heads + kv_head) << shift) +
+                            ((key0 + k) & ((1 << shift) - 1));
+        tma_load_2d(smem_addr(codes_to + k * (D / 2)), map, 0, static_cast<int>(row), smem_addr(bar));
+        bulk_g2s(scales_to + k * NB * 2, scales + row * NB, n * NB * 2, bar);
+    };
+    if (shift >= 6) {
+        const int32_t page = __shfl_sync(0xFFFFFFFFu, pages.lane_page, (key0 >> shift) - pages.first);
+        if (lane == 0) {
+            const bool there = page >= 0 && page < p.num_pages;
+            mbar_arrive_expect_tx(bar, there ? kTile * (D / 2 + NB * 2) : 0);
+            if (there) copy(page, 0, kTile);
         }
+        return;
     }
+    // lane i takes the tile's i-th page
+    const int step = 1 << shift, k = lane << shift;
+    const int32_t page = __shfl_sync(0xFFFFFFFFu, pages.lane_page, ((key0 >> shift) - pages.first + lane) & 31);
+    const bool there = k < kTile && key0 + k < hi && key0 + k + step > lo && page >= 0 && page < p.num_pages;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, there));
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * step * (D / 2 + NB * 2));
+    __syncwarp();
+    if (there) copy(page, k, step);
 }
 
 // q of the item's rows as B fragments, scaled to below 2^15, with -8 times
@@ -331,10 +363,12 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
     constexpr int NB = L::NB, E = D / 32;  // values per lane: a lane's lie in one block
     const AttnArgs &a = p.a;
     const int heads = a.heads / p.kv_heads, all = r.rows * heads;
-    __half *frag = reinterpret_cast<__half *>(w.buf + L::q);
-    float *bias = reinterpret_cast<float *>(w.buf + L::bias);
+    __half *frag = reinterpret_cast<__half *>(w.rest + L::q);
+    float *bias = reinterpret_cast<float *>(w.rest + L::bias);
     const int d0 = w.lane * E, block = d0 / 32;
-    w.scale_a = a.scale * kLog2e * 16777216.0f;
+    // the sign of the scale goes to q; a scale of 0 takes q with it
+    const float size = fabsf(a.scale) * kLog2e, sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
+    const int size_up = exponent(size);
     for (int row = 0; row < L::rows; ++row) {
         const int flat = min(it.group * L::rows + row, all - 1);  // rows past the end repeat the last
         const int token = flat / heads, head = it.kv_head * heads + flat - token * heads;
@@ -342,13 +376,15 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
         float v[E], big = 0.0f;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            v[i] = load_value(a.q, at + i, a.q_bf16);
+            v[i] = load_value(a.q, at + i, a.q_bf16) * sign;
             big = fmaxf(big, fabsf(v[i]));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-        const int up = min(max(14 - exponent(big), -113), 100);
+        // 2^up brings q below 2^15; the score's unit, size * 2^(24 - up), stays a normal number
+        const int up = min(max(14 - exponent(big), max(-113, size_up - 96)), 100);
         const float f = pow2i(up);
+        const float unit = sign == 0.0f ? 1.0f : fmaxf(ldexpf(size, 24 - up), 1.17549435e-38f);
         const int nt = row / (L::rows / NT), in = row % (L::rows / NT);
         float s_hi = 0.0f, s_lo = 0.0f;
 #pragma unroll
@@ -375,14 +411,15 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
         }
         if (w.lane % (32 / E) == 0) {
             const float m8 = -8.0f / 16777216.0f;
+            float *to = bias + (nt * NB + block) * 16;
             if constexpr (EXACT) {
-                bias[(nt * NB + block) * 8 + in * 2] = s_hi * m8;
-                bias[(nt * NB + block) * 8 + in * 2 + 1] = s_lo * m8;
+                to[in * 4] = to[in * 4 + 2] = s_hi * m8;
+                to[in * 4 + 1] = to[in * 4 + 3] = s_lo * m8;
             } else {
-                bias[(nt * NB + block) * 8 + in] = s_hi * m8;
+                to[(in >> 1) * 4 + (in & 1)] = to[(in >> 1) * 4 + 2 + (in & 1)] = s_hi * m8;
             }
         }
-        // the lane that holds this row's scores keeps its factor and range
+        // the lane that holds this row's scores keeps their unit and range
         const int pos = r.first + token;
         const int hi = a.causal ? min(r.len, pos + 1) : r.len;
         const int lo = a.window ? max(0, pos - a.window + 1) : 0;
@@ -391,7 +428,7 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
 #pragma unroll
             for (int k = 0; k < w.R; ++k)
                 if (n == nt && (EXACT ? w.t : w.t * 2 + k) == in) {
-                    w.scale_b[n][k] = pow2i(-up);
+                    w.unit[n][k] = unit;
                     w.lo[n][k] = lo;
                     w.hi[n][k] = hi;
                 }
@@ -399,60 +436,70 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
     __syncwarp();
 }
 
-// Scores of the tile in base-2 units: s[nt][mt][row of pair][key g, g + 8].
+__device__ __forceinline__ float low_float(uint32_t v) {
+    return __low2float(*reinterpret_cast<const __half2 *>(&v));
+}
+__device__ __forceinline__ float high_float(uint32_t v) {
+    return __high2float(*reinterpret_cast<const __half2 *>(&v));
+}
+
+// NB binary16 scales of one key.
+template <int NB>
+__device__ __forceinline__ void load_scales(const uint16_t *row, uint32_t (&d)[NB / 2]) {
+    if constexpr (NB == 8) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(row);
+        d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+    } else if constexpr (NB == 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(row);
+        d[0] = v.x; d[1] = v.y;
+    } else {
+        d[0] = *reinterpret_cast<const uint32_t *>(row);
+    }
+}
+
+// Sums of the tile before their unit: s[nt][mt][row of pair][key g, g + 8].
 template <int D, int NT, bool EXACT>
 __device__ __forceinline__ void tile_scores(WarpState<D, NT, EXACT> &w, float (&s)[NT][4][WarpState<D, NT, EXACT>::R][2]) {
     using L = Layout<D, NT, EXACT>;
     constexpr int NB = L::NB;
-    const uint4 *frag = reinterpret_cast<const uint4 *>(w.buf + L::q);
-    const float2 *bias = reinterpret_cast<const float2 *>(w.buf + L::bias);
-    const uint16_t *ks = reinterpret_cast<const uint16_t *>(w.buf + L::k_scales);
+    const uint4 *frag = reinterpret_cast<const uint4 *>(w.rest + L::q) + w.lane;
+    const float4 *bias = reinterpret_cast<const float4 *>(w.rest + L::bias) + w.t;
+    const uint16_t *ks = reinterpret_cast<const uint16_t *>(w.rest);
     const int sw = D == 256 ? (w.lane & 7) : D == 128 ? ((w.lane >> 1) & 3) : ((w.lane >> 2) & 1);
-    const uint32_t base = smem_addr(w.buf) + w.lane * (D / 2);
+    const uint32_t base = smem_addr(w.codes) + w.lane * (D / 2);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         // scales of keys 32 half + {0, 8, 16, 24} + g
         uint32_t d[4][NB / 2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint16_t *row = ks + (half * 32 + k * 8 + w.g) * NB;
-            if constexpr (NB == 8) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(row);
-                d[k][0] = v.x; d[k][1] = v.y; d[k][2] = v.z; d[k][3] = v.w;
-            } else if constexpr (NB == 4) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(row);
-                d[k][0] = v.x; d[k][1] = v.y;
-            } else {
-                d[k][0] = *reinterpret_cast<const uint32_t *>(row);
-            }
-        }
+        for (int k = 0; k < 4; ++k) load_scales<NB>(ks + (half * 32 + k * 8 + w.g) * NB, d[k]);
         float acc[NT][2][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][m][i] = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             uint32_t c[4];
             ldsm4(c, base + half * 32 * (D / 2) + ((b ^ sw) << 4));
+            uint4 q[NT];
+            float4 c8[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                q[n] = frag[(n * NB + b) * 32];
+                c8[n] = bias[(n * NB + b) * 4];
+            }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const uint32_t x = c[2 * m], y = c[2 * m + 1], x8 = x >> 8, y8 = y >> 8;
                 const uint32_t dx = d[2 * m][b / 2], dy = d[2 * m + 1][b / 2];
-                const float df = b & 1 ? half_hi(dx) : half_lo(dx), dg = b & 1 ? half_hi(dy) : half_lo(dy);
+                const float df = b & 1 ? high_float(dx) : low_float(dx), dg = b & 1 ? high_float(dy) : low_float(dy);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const uint4 q = frag[(n * NB + b) * 32 + w.lane];
-                    const float2 c8 = bias[(n * NB + b) * 4 + w.t];
-                    float z[4] = {c8.x, c8.y, c8.x, c8.y};
-                    mma16816(z, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u, q.x, q.y);
-                    mma16816(z, x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x00F000F0u, q.z, q.w);
-                    acc[n][m][0] = fmaf(df, z[0], acc[n][m][0]);
-                    acc[n][m][1] = fmaf(df, z[1], acc[n][m][1]);
-                    acc[n][m][2] = fmaf(dg, z[2], acc[n][m][2]);
-                    acc[n][m][3] = fmaf(dg, z[3], acc[n][m][3]);
+                    float z[4];
+                    mma16816(z, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u, q[n].x, q[n].y,
+                             c8[n].x, c8[n].y, c8[n].z, c8[n].w);
+                    mma16816(z, x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x00F000F0u, q[n].z,
+                             q[n].w, z[0], z[1], z[2], z[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[n][m][i] = b ? fmaf(i < 2 ? df : dg, z[i], acc[n][m][i]) : (i < 2 ? df : dg) * z[i];
                 }
             }
         }
@@ -463,96 +510,155 @@ __device__ __forceinline__ void tile_scores(WarpState<D, NT, EXACT> &w, float (&
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if constexpr (EXACT) {
-                        s[n][half * 2 + m][0][h] =
-                            (acc[n][m][2 * h] + acc[n][m][2 * h + 1]) * w.scale_a * w.scale_b[n][0];
+                        s[n][half * 2 + m][0][h] = acc[n][m][2 * h] + acc[n][m][2 * h + 1];
                     } else {
-                        s[n][half * 2 + m][0][h] = acc[n][m][2 * h] * w.scale_a * w.scale_b[n][0];
-                        s[n][half * 2 + m][1][h] = acc[n][m][2 * h + 1] * w.scale_a * w.scale_b[n][1];
+                        s[n][half * 2 + m][0][h] = acc[n][m][2 * h];
+                        s[n][half * 2 + m][1][h] = acc[n][m][2 * h + 1];
                     }
                 }
     }
 }
 
-// out = out * f + g * sum over the tile's keys of (p d) (n - 8).  EDGE: some
-// row does not see some key of the tile; such a key's scale may be anything.
+// V's scales, by block and in the order the B operand takes keys: 0 1 8 9
+// 2 3 10 11 ... of each 16.  They are scaled so that the largest lies in
+// [1, 2) (binary16) or [2^14, 2^15) (fp32), and 0 where `seen` has no bit for
+// the key (bit i: key 2 lane + i).  Returns the exponent of the largest.
+template <int D, int NT, bool EXACT>
+__device__ __forceinline__ int tile_scales(WarpState<D, NT, EXACT> &w, unsigned seen) {
+    using L = Layout<D, NT, EXACT>;
+    constexpr int NB = L::NB;
+    const uint16_t *vs = reinterpret_cast<const uint16_t *>(w.rest + L::v_scales) + w.lane * 2 * NB;
+    uint32_t d[2][NB / 2];
+    load_scales<NB>(vs, d[0]);
+    load_scales<NB>(vs + NB, d[1]);
+    uint32_t big = 0u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+            if (!((seen >> k) & 1u)) d[k][i] = 0u;
+            // NaN is passed over
+            asm("max.f16x2 %0, %1, %2;" : "=r"(big) : "r"(big), "r"(d[k][i] & 0x7FFF7FFFu));
+        }
+    // infinity counts as 65504; the order of positive numbers is that of their bits
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(fmaxf(low_float(big), high_float(big)), 65504.0f)));
+    const int e = top ? exponent(__uint_as_float(top)) : 0;
+    const int i8 = w.lane >> 3, i4 = (w.lane >> 2) & 1, i2 = w.lane & 3;
+    if constexpr (EXACT) {
+        float2 *to = reinterpret_cast<float2 *>(w.rest + L::d) + i8 * 8 + i2 * 2 + i4;
+        const float up = pow2i(14 - e);
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+            to[(2 * i) * (kTile / 2)] = make_float2(low_float(d[0][i]) * up, low_float(d[1][i]) * up);
+            to[(2 * i + 1) * (kTile / 2)] = make_float2(high_float(d[0][i]) * up, high_float(d[1][i]) * up);
+        }
+    } else {
+        uint32_t *to = reinterpret_cast<uint32_t *>(w.rest + L::d) + i8 * 8 + i2 * 2 + i4;
+        // 2^-e in two factors that binary16 has
+        const float f1 = pow2i(min(-e, 15)), f2 = pow2i(-e - min(-e, 15));
+        const uint32_t h1 = pack_rn(f1, f1), h2 = pack_rn(f2, f2);
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+            to[(2 * i) * (kTile / 2)] = hmul2(hmul2(__byte_perm(d[0][i], d[1][i], 0x5410), h1), h2);
+            to[(2 * i + 1) * (kTile / 2)] = hmul2(hmul2(__byte_perm(d[0][i], d[1][i], 0x7632), h1), h2);
+        }
+    }
+    return e;
+}
+
+// out = out * f + g * sum over the tile's keys of (p d) (n - 8), with the
+// weights in shared memory (EXACT) or in pw, as binary16 B operands.
+// EDGE: some row does not see some key of the tile, whose scale may then be
+// anything.
 template <int D, int NT, bool EXACT, bool EDGE>
-__device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const float (&f)[NT][WarpState<D, NT, EXACT>::R],
+__device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const uint32_t (&pw)[NT][4][2],
+                                            const float (&f)[NT][WarpState<D, NT, EXACT>::R],
                                             const float (&g)[NT][WarpState<D, NT, EXACT>::R]) {
     using L = Layout<D, NT, EXACT>;
     constexpr int NB = L::NB;
-    const uint32_t *vs = reinterpret_cast<const uint32_t *>(w.buf + L::v_scales);
-    const float *p = reinterpret_cast<const float *>(w.buf + L::p);
+    const float *p = reinterpret_cast<const float *>(w.rest + L::p);
     const int token = w.lane & 15, upper = w.lane >> 4;
     const int sw = D == 256 ? (token & 7) : D == 128 ? ((token >> 1) & 3) : ((token >> 2) & 1);
-    const uint32_t base = smem_addr(w.buf) + L::v_codes + token * (D / 2);
+    const uint32_t base = smem_addr(w.codes) + L::codes + token * (D / 2);
     const uint32_t keep = EXACT && (w.g & 1) ? 0xFFFFE000u : 0u;  // odd columns hold the second part
 #pragma unroll
     for (int bp = 0; bp < NB / 2; ++bp) {
         float acc[NT][2][2][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[n][i >> 3][(i >> 2) & 1][i & 3] = 0.0f;
-#pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             uint32_t c[4];
             ldsm4_t(c, base + ks * 16 * (D / 2) + (((2 * bp + upper) ^ sw) << 4));
-            uint32_t d[4];
+            float4 pe[NT];
+            if constexpr (EXACT) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                d[k] = vs[((ks * 16 + 2 * w.t + (k & 1) + (k >> 1) * 8) * NB) / 2 + bp];
-            float2 pw[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float *row = p + (EXACT ? n * 4 + (w.g >> 1) : n * 8 + w.g) * L::p_stride + ks * 16 + 2 * w.t;
-                pw[n][0] = *reinterpret_cast<const float2 *>(row);
-                pw[n][1] = *reinterpret_cast<const float2 *>(row + 8);
+                for (int n = 0; n < NT; ++n)
+                    pe[n] = *reinterpret_cast<const float4 *>(p + (n * 4 + (w.g >> 1)) * L::p_stride + ks * 16 + 4 * w.t);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float df[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) df[k] = h ? half_hi(d[k]) : half_lo(d[k]);
                 const uint32_t x = c[2 * h], y = c[2 * h + 1], x8 = x >> 8, y8 = y >> 8;
                 // n - 8 (lower codes) and 16 (n - 8) (upper codes), times 2^-24
                 const uint32_t xa = hadd2(x & 0x000F000Fu, 0x80088008u), ya = hadd2(y & 0x000F000Fu, 0x80088008u);
                 const uint32_t xb = hadd2(x & 0x00F000F0u, 0x80808080u), yb = hadd2(y & 0x00F000F0u, 0x80808080u);
                 const uint32_t xc = hadd2(x8 & 0x000F000Fu, 0x80088008u), yc = hadd2(y8 & 0x000F000Fu, 0x80088008u);
                 const uint32_t xd = hadd2(x8 & 0x00F000F0u, 0x80808080u), yd = hadd2(y8 & 0x00F000F0u, 0x80808080u);
+                uint32_t b0[NT], b1[NT];
+                if constexpr (EXACT) {
+                    const float4 d = *reinterpret_cast<const float4 *>(
+                        reinterpret_cast<const float *>(w.rest + L::d) + (2 * bp + h) * kTile + ks * 16 + 4 * w.t);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float v[4] = {pw[n][0].x * df[0], pw[n][0].y * df[1], pw[n][1].x * df[2], pw[n][1].y * df[3]};
-                    if constexpr (EDGE) {
-                        v[0] = pw[n][0].x == 0.0f ? 0.0f : v[0];
-                        v[1] = pw[n][0].y == 0.0f ? 0.0f : v[1];
-                        v[2] = pw[n][1].x == 0.0f ? 0.0f : v[2];
-                        v[3] = pw[n][1].y == 0.0f ? 0.0f : v[3];
-                    }
-                    uint32_t b0, b1;
-                    if constexpr (EXACT) {
+                    for (int n = 0; n < NT; ++n) {
+                        float v[4] = {pe[n].x * d.x, pe[n].y * d.y, pe[n].z * d.z, pe[n].w * d.w};
+                        if constexpr (EDGE) {
+                            v[0] = pe[n].x == 0.0f ? 0.0f : v[0];
+                            v[1] = pe[n].y == 0.0f ? 0.0f : v[1];
+                            v[2] = pe[n].z == 0.0f ? 0.0f : v[2];
+                            v[3] = pe[n].w == 0.0f ? 0.0f : v[3];
+                        }
 #pragma unroll
                         for (int k = 0; k < 4; ++k) v[k] -= __uint_as_float(__float_as_uint(v[k]) & keep);
-                        b0 = pack_rz(v[0], v[1]);
-                        b1 = pack_rz(v[2], v[3]);
-                    } else {
-                        b0 = pack_rn(v[0], v[1]);
-                        b1 = pack_rn(v[2], v[3]);
+                        b0[n] = pack_rz(v[0], v[1]);
+                        b1[n] = pack_rz(v[2], v[3]);
                     }
-                    mma16816(acc[n][h][0], xa, xb, ya, yb, b0, b1);
-                    mma16816(acc[n][h][1], xc, xd, yc, yd, b0, b1);
+                } else {
+                    const uint2 d = *reinterpret_cast<const uint2 *>(
+                        reinterpret_cast<const uint32_t *>(w.rest + L::d) + (2 * bp + h) * (kTile / 2) + ks * 8 + 2 * w.t);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        b0[n] = hmul2(pw[n][ks][0], d.x);
+                        b1[n] = hmul2(pw[n][ks][1], d.y);
+                        if constexpr (EDGE) {
+                            b0[n] &= not_zero2(pw[n][ks][0]);
+                            b1[n] &= not_zero2(pw[n][ks][1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float (&a0)[4] = acc[n][h][0], (&a1)[4] = acc[n][h][1];
+                    if (ks == 0) {
+                        mma16816(a0, xa, xb, ya, yb, b0[n], b1[n], 0.0f, 0.0f, 0.0f, 0.0f);
+                        mma16816(a1, xc, xd, yc, yd, b0[n], b1[n], 0.0f, 0.0f, 0.0f, 0.0f);
+                    } else {
+                        mma16816(a0, xa, xb, ya, yb, b0[n], b1[n], a0[0], a0[1], a0[2], a0[3]);
+                        mma16816(a1, xc, xd, yc, yd, b0[n], b1[n], a1[0], a1[1], a1[2], a1[3]);
+                    }
                 }
             }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            const float2 f2 = make_float2(f[n][0], f[n][EXACT ? 0 : 1]), g2 = make_float2(g[n][0], g[n][EXACT ? 0 : 1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w.out[n][2 * bp + h][m][i] = fmaf(w.out[n][2 * bp + h][m][i], f[n][EXACT ? 0 : i & 1],
-                                                          acc[n][h][m][i] * g[n][EXACT ? 0 : i & 1]);
+                    for (int i = 0; i < 2; ++i)
+                        w.out[n][2 * bp + h][m][i] =
+                            __ffma2_rn(w.out[n][2 * bp + h][m][i], f2,
+                                       __fmul2_rn(make_float2(acc[n][h][m][2 * i], acc[n][h][m][2 * i + 1]), g2));
+        }
     }
 }
 
@@ -573,7 +679,7 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
             w.sum[n][k] = 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < NB * 8; ++i) w.out[n][i >> 3][(i >> 2) & 1][i & 3] = 0.0f;
+        for (int i = 0; i < NB * 4; ++i) w.out[n][i >> 2][(i >> 1) & 1][i & 1] = make_float2(0.0f, 0.0f);
     }
     // the keys that any, and that every, row of the group sees
     const int heads = a.heads / p.kv_heads, all = r.rows * heads;
@@ -585,43 +691,35 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
     t1 = min(t1, (hi + kTile - 1) / kTile - r.tile0);
     if (w.dead) return;
 
-    // page indices of the tiles ahead: lane i holds page page0 + i
+    // page indices of the tiles ahead
     const int32_t *table = a.table + it.b * a.table_width;
-    int page0 = 0;
-    int32_t pages = -1;
-    auto fetch = [&](int tile) {  // pages of `tile` and after
-        page0 = ((r.tile0 + tile) * kTile) >> p.page_shift;
-        const int i = page0 + w.lane;
-        pages = i < a.table_width ? table[i] : -1;
-    };
     const int tile_pages = max(1, kTile >> p.page_shift);
-    auto ahead = [&](int tile) {  // makes `tile`'s pages known
-        if ((((r.tile0 + tile) * kTile) >> p.page_shift) + tile_pages > page0 + 32) fetch(tile);
+    Pages pages = {-1, -64};
+    auto ahead = [&](int key0) {  // makes the pages of the tile at key0 known
+        const int first = key0 >> p.page_shift;
+        if (first + tile_pages > pages.first + 32) {
+            pages.first = first;
+            pages.lane_page = first + w.lane < a.table_width ? table[first + w.lane] : -1;
+        }
     };
-    auto issue_k = [&](int tile) {
-        issue<D, NT, EXACT>(p, kmap, p.k_scales, w.buf, 0, L::k_scales, w.bars, it.kv_head, (r.tile0 + tile) * kTile,
-                            lo, hi, pages, page0);
-    };
-    auto issue_v = [&](int tile) {
-        issue<D, NT, EXACT>(p, vmap, p.v_scales, w.buf, L::v_codes, L::v_scales, w.bars + 1, it.kv_head,
-                            (r.tile0 + tile) * kTile, lo, hi, pages, page0);
-    };
+    uint8_t *const vcodes = w.codes + L::codes, *const vscales = w.rest + L::v_scales;
     if (t0 < t1) {
-        fetch(t0);
-        issue_k(t0);
-        issue_v(t0);
+        const int key0 = (r.tile0 + t0) * kTile;
+        ahead(key0);
+        issue<D>(p, kmap, p.k_scales, w.codes, w.rest, w.bars, it.kv_head, key0, lo, hi, pages);
+        issue<D>(p, vmap, p.v_scales, vcodes, vscales, w.bars + 1, it.kv_head, key0, lo, hi, pages);
     }
     stage_q<D, NT, EXACT>(p, w, r, it);
     for (int tile = t0; tile < t1; ++tile) {
         const int key0 = (r.tile0 + tile) * kTile;
-        // 16-key groups whose page can be read
-        int live = 15;
-        for (int k = 0; k < 4; ++k) {
-            const int32_t page = __shfl_sync(0xFFFFFFFFu, pages, ((key0 + 16 * k) >> p.page_shift) - page0);
-            if ((page < 0 || page >= p.num_pages) && key0 + 16 * k < hi && key0 + 16 * k + 16 > lo) live &= ~(1 << k);
-        }
-        if (live != 15 && w.lane == 0) record_error(p.ctx, kDevErrIndex);
-        const bool edge = live != 15 || key0 < lo_all || key0 + kTile > hi_all;
+        // 16-key groups whose page can be read: lane i looks at group i
+        const int32_t page = __shfl_sync(0xFFFFFFFFu, pages.lane_page,
+                                         (((key0 + 16 * w.lane) >> p.page_shift) - pages.first) & 31);
+        const int key = key0 + 16 * w.lane;
+        const unsigned lost = __ballot_sync(0xFFFFFFFFu, w.lane < 4 && key < hi && key + 16 > lo &&
+                                                             (page < 0 || page >= p.num_pages));
+        if (lost && w.lane == 0) record_error(p.ctx, kDevErrIndex);
+        const bool edge = lost || key0 < lo_all || key0 + kTile > hi_all;
 
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(w.bars, w.phase[0], p.ctx))) w.dead = true;
         w.phase[0] ^= 1;
@@ -630,9 +728,10 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
         __syncwarp();
         const bool asked = tile + 1 < t1 && !w.dead;
         if (asked) {
-            ahead(tile + 1);
-            issue_k(tile + 1);
+            ahead(key0 + kTile);
+            issue<D>(p, kmap, p.k_scales, w.codes, w.rest, w.bars, it.kv_head, key0 + kTile, lo, hi, pages);
         }
+        unsigned seen = 3u;  // keys 2 lane and 2 lane + 1, by any row
         if (edge) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -642,114 +741,126 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
                     for (int k = 0; k < R; ++k)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const int key = key0 + 16 * m + 8 * h + w.g;
-                            if (key < w.lo[n][k] || key >= w.hi[n][k] || !((live >> m) & 1)) s[n][m][k][h] = ninf;
+                            const int j = key0 + 16 * m + 8 * h + w.g;
+                            if (j < w.lo[n][k] || j >= w.hi[n][k] || ((lost >> m) & 1u)) s[n][m][k][h] = ninf;
                         }
+            const int j = key0 + 2 * w.lane;
+            seen = (lost >> (w.lane >> 3)) & 1u ? 0u : (j >= lo && j < hi ? 1u : 0u) | (j + 1 >= lo && j + 1 < hi ? 2u : 0u);
         }
-        // maxima of the tile's scores, and the weights relative to them
+        // the rows' largest and smallest scores of the tile
         float top[NT][R];
+        bool faint = false;  // some weight lies below 2^-24 of the tile's largest
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                float v = ninf;
+                float v = s[n][0][k][0], u = v;
 #pragma unroll
-                for (int m = 0; m < 4; ++m) v = fmaxf(v, fmaxf(s[n][m][k][0], s[n][m][k][1]));
+                for (int i = 1; i < 8; ++i) {
+                    v = fmaxf(v, s[n][i >> 1][k][i & 1]);
+                    u = fminf(u, s[n][i >> 1][k][i & 1]);
+                }
                 v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
                 v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-                top[n][k] = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+                v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+                top[n][k] = v * w.unit[n][k];
+                faint |= u * w.unit[n][k] < top[n][k] - 23.5f;
             }
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(w.bars + 1, w.phase[1], p.ctx))) w.dead = true;
         w.phase[1] ^= 1;
-        uint32_t *vs = reinterpret_cast<uint32_t *>(w.buf + L::v_scales);
-        if (edge) {  // scales of keys that no row sees may hold anything
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int i = w.lane + 32 * k;
-                if (key0 + i < lo || key0 + i >= hi || !((live >> (i >> 4)) & 1))
-#pragma unroll
-                    for (int j = 0; j < NB / 2; ++j) vs[i * (NB / 2) + j] = 0u;
-            }
-            fence_proxy_async_smem();  // before a later copy into the same place
-            __syncwarp();
-        }
-        // the largest |d| of the tile: NaN is passed over, infinity counts as 65504
-        uint32_t big = 0u;
-#pragma unroll
-        for (int i = 0; i < kTile * NB / 64; ++i) {
-            const uint32_t v = vs[i * 32 + w.lane] & 0x7FFF7FFFu;
-            asm("max.f16x2 %0, %1, %2;" : "=r"(big) : "r"(big), "r"(v));
-        }
-        float dmax = fminf(fmaxf(half_lo(big), half_hi(big)), 65504.0f);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dmax = fmaxf(dmax, __shfl_xor_sync(0xFFFFFFFFu, dmax, o));
-        const int room = dmax > 0.0f ? 14 - exponent(dmax) : 0;
-        const float up = pow2i(room);
-        // f: factor of what is there already; g: of this tile's products
+        const int e_max = tile_scales<D, NT, EXACT>(w, seen);
+        // f: factor of what is there already; g: of this tile's products.  The
+        // products carry 2^-24 of the codes and the scales' factor (fp32:
+        // 2^(14 - e_max); binary16: 2^-e_max and 2^14 of the weights).
         float f[NT][R], g[NT][R];
-        float *pp = reinterpret_cast<float *>(w.buf + L::p);
-        bool faint = false;  // some weight lies below 2^-24
+        float *pp = reinterpret_cast<float *>(w.rest + L::p) + (w.g >> 1) * 4 + (w.g & 1);
+        uint32_t pw[NT][4][2];
+        const float unit_out = pow2i(10 + e_max);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int k = 0; k < R; ++k) {
                 const float here = top[n][k] == ninf ? 0.0f : top[n][k], now = fmaxf(w.top[n][k], top[n][k]);
                 f[n][k] = w.top[n][k] == ninf ? 0.0f : exp2_fast(w.top[n][k] - now);
                 const float fresh = top[n][k] == ninf ? 0.0f : exp2_fast(top[n][k] - now);
-                g[n][k] = fresh * pow2i(24 - room);
+                g[n][k] = fresh * unit_out;
                 w.top[n][k] = now;
                 float sum = 0.0f;
-                float *row = pp + (EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k) * L::p_stride + w.g;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float e = exp2_fast(fmaf(s[n][i >> 1][k][i & 1], w.unit[n][k], -here));
+                    s[n][i >> 1][k][i & 1] = e;
+                    sum += e;
+                }
+                w.sum[n][k] = fmaf(w.sum[n][k], f[n][k], sum * fresh);
+            }
+        }
+        if (__any_sync(0xFFFFFFFFu, faint)) {  // hidden keys, whose weight is 0, do not count
+            faint = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < R; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) faint |= s[n][i >> 1][k][i & 1] < kFaint && s[n][i >> 1][k][i & 1] > 0.0f;
+            faint = __any_sync(0xFFFFFFFFu, faint);
+        }
+        // the weights as the B operand's keys and columns
+        auto hand_over = [&](auto pick) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float e = exp2_fast(s[n][m][k][h] - here);
-                        s[n][m][k][h] = e;
-                        sum += e;
-                        const bool low = e < kFaint;
-                        faint |= low && e > 0.0f;
-                        row[16 * m + 8 * h] = low ? 0.0f : e * up;
+                        if constexpr (EXACT) {
+                            pp[(n * 4 + w.t) * L::p_stride + 16 * m + 2 * h] = pick(s[n][m][0][h]);
+                        } else {
+                            pw[n][m][h] = transpose8(pack_rn(pick(s[n][m][0][h]) * 16384.0f, pick(s[n][m][R - 1][h]) * 16384.0f));
+                        }
                     }
-                w.sum[n][k] = fmaf(w.sum[n][k], f[n][k], sum * fresh);
-            }
-        __syncwarp();
-        if (edge)
-            tile_values<D, NT, EXACT, true>(w, f, g);
+            __syncwarp();
+        };
+        if (faint)
+            hand_over([](float e) { return e < kFaint ? 0.0f : e; });
         else
-            tile_values<D, NT, EXACT, false>(w, f, g);
+            hand_over([](float e) { return e; });
+        if (edge)
+            tile_values<D, NT, EXACT, true>(w, pw, f, g);
+        else
+            tile_values<D, NT, EXACT, false>(w, pw, f, g);
         __syncwarp();
         // Weights far below the tile's largest would fall out of binary16's
         // range, which shows where the large ones meet zeros: they go in
         // passes of their own, raised by 2^24 each time.
-        for (float raise = 1.0f / kFaint; __any_sync(0xFFFFFFFFu, faint); raise *= 1.0f / kFaint) {
-            faint = false;
+        for (float raise = 1.0f / kFaint; faint; raise *= 1.0f / kFaint) {
+            bool more = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
                     f[n][k] = 1.0f;
                     g[n][k] *= kFaint;
-                    float *row = pp + (EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k) * L::p_stride + w.g;
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float e = s[n][m][k][h] * raise;
-                            const bool low = e < kFaint;
-                            faint |= low && e > 0.0f;
-                            row[16 * m + 8 * h] = low || !(e < 1.0f) ? 0.0f : e * up;
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        const float e = s[n][i >> 1][k][i & 1] * raise;
+                        more |= e < kFaint && e > 0.0f;
+                    }
                 }
+            hand_over([raise](float v) {
+                const float e = v * raise;
+                return e >= kFaint && e < 1.0f ? e : 0.0f;
+            });
+            tile_values<D, NT, EXACT, true>(w, pw, f, g);
             __syncwarp();
-            tile_values<D, NT, EXACT, true>(w, f, g);
-            __syncwarp();
+            faint = __any_sync(0xFFFFFFFFu, more);
         }
         if (w.dead) {  // a wait gave up: take no more tiles, let the copy that is under way end
             if (asked) mbar_wait(w.bars, w.phase[0], p.ctx);
             break;
         }
-        if (tile + 1 < t1) issue_v(tile + 1);
+        if (tile + 1 < t1)
+            issue<D>(p, vmap, p.v_scales, vcodes, vscales, w.bars + 1, it.kv_head, key0 + kTile, lo, hi, pages);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -775,7 +886,7 @@ __device__ __forceinline__ void each_output(const WarpState<D, NT, EXACT> &w, Fn
                 for (int h = 0; h < 2; ++h) {
                     const int d = 32 * b + 16 * h + 2 * w.g + m;
                     const float down = h ? 0.0625f : 1.0f;
-                    const float x = w.out[n][b][m][2 * h] * down, y = w.out[n][b][m][2 * h + 1] * down;
+                    const float x = w.out[n][b][m][h].x * down, y = w.out[n][b][m][h].y * down;
                     if constexpr (EXACT) {
                         fn(n, 0, n * 4 + w.t, d, x + y);
                     } else {
@@ -819,14 +930,14 @@ __device__ __forceinline__ void write_lse(const StreamParams &p, const Target &t
 }
 
 template <int D, int NT, bool EXACT>
-__global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), D == 256 ? 1 : D == 128 ? 2 : 3)
+__global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT, EXACT>::ctas))
     attn_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const StreamParams p) {
     using L = Layout<D, NT, EXACT>;
     constexpr int R = WarpState<D, NT, EXACT>::R, ROWS = L::rows, W = L::warps;
     extern __shared__ uint8_t attn_smem[];
     uint8_t *base = attn_smem + ((1024u - (smem_addr(attn_smem) & 1023u)) & 1023u);
-    Shared &sh = *reinterpret_cast<Shared *>(base + W * L::bytes);
+    Shared &sh = *reinterpret_cast<Shared *>(base + W * (L::code_bytes + L::rest_bytes));
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < W * 2; ++i) mbar_init(&sh.bars[0][0] + i, 1);
@@ -838,7 +949,8 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), D == 256 ? 1 
     const int64_t total = build_line<ROWS, L::threads>(p, sh);
 
     WarpState<D, NT, EXACT> w;
-    w.buf = base + warp * L::bytes;
+    w.codes = base + warp * L::code_bytes;
+    w.rest = base + W * L::code_bytes + warp * L::rest_bytes;
     w.bars = sh.bars[warp];
     w.phase[0] = w.phase[1] = 0;
     w.lane = threadIdx.x & 31;
@@ -877,7 +989,7 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), D == 256 ? 1 
         // the warp's last part stays in its code buffers, which no later tile
         // needs; an earlier one goes to global memory
         const bool head = t0 > 0;
-        float *rec = x >= x1 ? reinterpret_cast<float *>(w.buf) : p.warp_records + me * kRecord;
+        float *rec = x >= x1 ? reinterpret_cast<float *>(w.codes) : p.warp_records + me * kRecord;
         each_output<D, NT, EXACT>(w, [&](int, int, int row, int d, float v) { rec[row * D + d] = v; });
         if (w.g == 0)
 #pragma unroll
@@ -930,7 +1042,7 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), D == 256 ? 1 
                     if (j > c && !((members >> j) & 1u)) continue;
                     const int kj = j == c ? kind : 0;
                     const float *rec = kj == 1 || (sh.flags[j] & kHeadLast)
-                                           ? reinterpret_cast<const float *>(base + j * L::bytes)
+                                           ? reinterpret_cast<const float *>(base + j * L::code_bytes)
                                            : p.warp_records + (static_cast<int64_t>(blockIdx.x) * W + j) * kRecord;
                     const float f = exp2_fast(sh.stat[j][kj][row][0] - ref);
                     v = fmaf(f, rec[i], v);
@@ -1016,13 +1128,11 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const StreamParams 
     if (d == 0) write_lse<ROWS>(p, to, row, top, sum);
 }
 
-int ctas_per_sm(int dim) { return dim == 256 ? 1 : dim == 128 ? 2 : 3; }
-
 template <int D, int NT, bool EXACT>
 cudaError_t launch_stream(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
     using L = Layout<D, NT, EXACT>;
     static int limits[kMaxDevices];
-    constexpr size_t smem = static_cast<size_t>(L::warps) * L::bytes + sizeof(Shared) + 1024;
+    constexpr size_t smem = static_cast<size_t>(L::warps) * (L::code_bytes + L::rest_bytes) + sizeof(Shared) + 1024;
     static_assert(smem <= 232448, "shared memory per CTA");
     auto *kernel = attn_stream_kernel<D, NT, EXACT>;
     cudaError_t e = ensure_smem(kernel, smem, false, limits);
@@ -1037,7 +1147,7 @@ cudaError_t launch_stream(const KvCache &c, const AttnArgs &a, cudaStream_t stre
     for (int i = 0; i < 2; ++i)
         if (!encode_tmap_2d(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, codes[i], D / 2, rows, D / 2, D / 2, box, sw))
             return cudaErrorInvalidValue;
-    const int ctas = std::min(device_sm_count() * ctas_per_sm(D), kMaxCtas);
+    const int ctas = std::min(device_sm_count() * L::ctas, kMaxCtas);
     StreamParams p = {};
     p.a = a;
     p.k_scales = static_cast<const __half *>(c.k_scales);
@@ -1065,8 +1175,8 @@ cudaError_t launch_dim(const KvCache &c, const AttnArgs &a, cudaStream_t stream,
 
 }  // namespace
 
-size_t attn_workspace_bytes(const KvCache &c, int) {
-    const size_t ctas = std::min(device_sm_count() * ctas_per_sm(c.head_dim), kMaxCtas);
+size_t attn_workspace_bytes(const KvCache &, int) {
+    const size_t ctas = std::min(device_sm_count() * 2, kMaxCtas);  // as the smaller head dimensions take
     return ctas * ((kWarps + 2) * kRecord * sizeof(float) + sizeof(CtaParts));
 }
 
