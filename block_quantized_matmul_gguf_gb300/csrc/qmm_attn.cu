@@ -369,18 +369,32 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
     // the sign of the scale goes to q; a scale of 0 takes q with it
     const float size = fabsf(a.scale) * kLog2e, sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
     const int size_up = exponent(size);
+    // all rows' loads first
+    float v[L::rows][E];
+    int pos[L::rows];
+#pragma unroll
     for (int row = 0; row < L::rows; ++row) {
         const int flat = min(it.group * L::rows + row, all - 1);  // rows past the end repeat the last
         const int token = flat / heads, head = it.kv_head * heads + flat - token * heads;
         const int64_t at = (static_cast<int64_t>(r.row0) + token) * a.q_stride + static_cast<int64_t>(head) * D + d0;
-        float v[E], big = 0.0f;
+        pos[row] = r.first + token;
+        if (a.q_bf16) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[row][i] = load_value(a.q, at + i, true);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[row][i] = load_value(a.q, at + i, false);
+        }
+    }
+#pragma unroll
+    for (int row = 0; row < L::rows; ++row) {
+        uint32_t bits = 0;  // of the largest value: positive numbers order as their bits do
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            v[i] = load_value(a.q, at + i, a.q_bf16) * sign;
-            big = fmaxf(big, fabsf(v[i]));
+            v[row][i] *= sign;
+            bits = max(bits, __float_as_uint(v[row][i]) & 0x7FFFFFFFu);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+        const float big = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, bits));
         // 2^up brings q below 2^15; the score's unit, size * 2^(24 - up), stays a normal number
         const int up = min(max(14 - exponent(big), max(-113, size_up - 96)), 100);
         const float f = pow2i(up);
@@ -390,7 +404,7 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const int d5 = (d0 + i) & 31, high = d5 >> 4, quad = (d5 & 15) >> 2, e = d5 & 3;
-            const float x = v[i] * f * (high ? 0.0625f : 1.0f);
+            const float x = v[row][i] * f * (high ? 0.0625f : 1.0f);
             const int reg = (e & 1) * 2 + high;
             const __half h = EXACT ? __float2half_rz(x) : __float2half_rn(x);
             const float hf = __half2float(h);
@@ -420,9 +434,8 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
             }
         }
         // the lane that holds this row's scores keeps their unit and range
-        const int pos = r.first + token;
-        const int hi = a.causal ? min(r.len, pos + 1) : r.len;
-        const int lo = a.window ? max(0, pos - a.window + 1) : 0;
+        const int hi = a.causal ? min(r.len, pos[row] + 1) : r.len;
+        const int lo = a.window ? max(0, pos[row] - a.window + 1) : 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -872,28 +885,27 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
         }
 }
 
-// The lane's accumulators as outputs: fn(row, column, value), unnormalised.
-template <int D, int NT, bool EXACT, typename Fn>
-__device__ __forceinline__ void each_output(const WarpState<D, NT, EXACT> &w, Fn fn) {
-    constexpr int NB = D / 32;
+// The lane's accumulators as outputs, unnormalised, row by row: begin(n, k,
+// row) returns a function of (dimension, value).
+template <int D, int NT, bool EXACT, typename Begin>
+__device__ __forceinline__ void each_output(const WarpState<D, NT, EXACT> &w, Begin begin) {
+    constexpr int NB = D / 32, R = WarpState<D, NT, EXACT>::R;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int k = 0; k < R; ++k) {
+            auto put = begin(n, k, EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k);
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int d = 32 * b + 16 * h + 2 * w.g + m;
-                    const float down = h ? 0.0625f : 1.0f;
-                    const float x = w.out[n][b][m][h].x * down, y = w.out[n][b][m][h].y * down;
-                    if constexpr (EXACT) {
-                        fn(n, 0, n * 4 + w.t, d, x + y);
-                    } else {
-                        fn(n, 0, n * 8 + 2 * w.t, d, x);
-                        fn(n, 1, n * 8 + 2 * w.t + 1, d, y);
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 o = w.out[n][b][m][h];
+                        const float v = EXACT ? o.x + o.y : k ? o.y : o.x;
+                        put(32 * b + 16 * h + 2 * w.g + m, v * (h ? 0.0625f : 1.0f));
                     }
-                }
+        }
 }
 
 __device__ __forceinline__ Target target_of(const Request &r, const Item &it) {
@@ -975,8 +987,15 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
         x += t1 - t0;
         const Target to = target_of(r, it);
         if (t0 == 0 && t1 == r.tiles) {
-            each_output<D, NT, EXACT>(w, [&](int n, int k, int row, int d, float v) {
-                write_out<D, ROWS>(p, to, row, d, v, w.sum[n][k]);
+            each_output<D, NT, EXACT>(w, [&](int n, int k, int row) {
+                int64_t at = 0;
+                int head = 0;
+                const bool there = locate<ROWS>(p, to, row, at, head);
+                at = at * p.a.out_stride + static_cast<int64_t>(head) * D;
+                const float down = w.sum[n][k] == 0.0f ? 0.0f : 1.0f / w.sum[n][k];
+                return [&p, there, at, down](int d, float v) {
+                    if (there) store_value(p.a.out, at + d, p.a.out_bf16, v * down);
+                };
             });
             if (w.g == 0)
 #pragma unroll
@@ -990,7 +1009,7 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
         // needs; an earlier one goes to global memory
         const bool head = t0 > 0;
         float *rec = x >= x1 ? reinterpret_cast<float *>(w.codes) : p.warp_records + me * kRecord;
-        each_output<D, NT, EXACT>(w, [&](int, int, int row, int d, float v) { rec[row * D + d] = v; });
+        each_output<D, NT, EXACT>(w, [rec](int, int, int row) { return [=](int d, float v) { rec[row * D + d] = v; }; });
         if (w.g == 0)
 #pragma unroll
             for (int n = 0; n < NT; ++n)

@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
 // the inputs; a decode step's few blocks are bound by latency.
 
 struct KvView {
-    uint8_t *codes[2];
-    __half *scales[2];
+    uint8_t *k_codes, *v_codes;
+    __half *k_scales, *v_scales;
     int64_t slots;  // of the whole cache
     int page_shift, kv_heads;
 };
@@ -172,14 +172,31 @@ __device__ __forceinline__ int64_t cache_row(const KvView &c, int64_t slot, int 
     return ((((slot >> c.page_shift) * c.kv_heads) + head) << c.page_shift) + place;
 }
 
-__device__ __forceinline__ float4 load_quad(const float *p, bool wide) {
-    if (wide) return *reinterpret_cast<const float4 *>(p);
+// How a CTA's threads share tokens: `per` quads a token (a multiple of 32, so
+// that a warp holds one token's), several tokens at a time where they fit.
+// kAhead tokens per thread are loaded before the first is worked on.
+constexpr int kAhead = 4;
+
+struct Spread {
+    int per, par, sub, at;
+    __device__ explicit Spread(int quads) : per(quads) {
+        par = max(1, kThreads / per);
+        sub = threadIdx.x / per;
+        at = threadIdx.x - sub * per;
+        if (sub >= par) sub = -1;  // threads that are left over
+    }
+};
+
+template <bool kWide>
+__device__ __forceinline__ float4 load_quad(const float *p) {
+    if constexpr (kWide) return __ldcs(reinterpret_cast<const float4 *>(p));
     return make_float4(p[0], p[1], p[2], p[3]);
 }
-__device__ __forceinline__ float4 load_quad(const uint16_t *p, bool wide) {
+template <bool kWide>
+__device__ __forceinline__ float4 load_quad(const uint16_t *p) {
     uint32_t lo, hi;
-    if (wide) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    if constexpr (kWide) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
         lo = v.x;
         hi = v.y;
     } else {
@@ -196,66 +213,78 @@ __device__ __forceinline__ uint32_t code_of(float x, float d) {
     return static_cast<uint32_t>(fminf(fmaxf(r, 0.0f), 15.0f));
 }
 
-template <typename T>
+// kWide: rows of quads are aligned to their size.
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads) append_kernel(KvView c, const T *__restrict__ k,
                                                           int64_t k_stride,
                                                           const T *__restrict__ v,
                                                           int64_t v_stride,
                                                           const int64_t *__restrict__ slots,
-                                                          int64_t n, int dim, int wide,
-                                                          LaunchCtx ctx) {
+                                                          int64_t n, int dim, LaunchCtx ctx) {
     pdl_wait();
     pdl_launch_dependents();
-    const int quads = c.kv_heads * dim / 4;  // of a token's keys (or values): a multiple of 16
-    const int64_t total = n * 2 * quads;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-    // eight consecutive threads hold one block and leave the loop together
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += step) {
-        const int64_t token = i / (2 * quads);
-        int at = static_cast<int>(i - token * (2 * quads));
-        const int half = at >= quads;
-        at -= half * quads;
-        const int64_t slot = slots[token];
-        const bool live = slot >= 0 && slot < c.slots;
-        if (!live && slot != -1) record_error(ctx, kDevErrIndex);
-        const unsigned group = 0xFFu << (threadIdx.x & 24);
-        if (!live) continue;  // the whole block together
-        const T *src = half ? v + token * v_stride : k + token * k_stride;
-        const float4 x = load_quad(src + at * 4, wide);
-        float top = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
-        float low = fminf(fminf(x.x, x.y), fminf(x.z, x.w));
-        // 0 * x is NaN for the values that a block cannot hold
-        float odd = 0.0f * x.x + 0.0f * x.y + (0.0f * x.z + 0.0f * x.w);
+    const int quads = c.kv_heads * dim / 4;  // of a token's keys, and of its values
+    const Spread sp(2 * quads);
+    if (sp.sub < 0) return;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * sp.par * kAhead + sp.sub; base < n;
+         base += static_cast<int64_t>(gridDim.x) * sp.par * kAhead) {
+        int64_t slot[kAhead];
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(group, top, o));
-            low = fminf(low, __shfl_xor_sync(group, low, o));
-            odd += __shfl_xor_sync(group, odd, o);
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t token = base + u * sp.par;
+            slot[u] = token < n ? slots[token] : -1;
+            if (slot[u] < -1 || slot[u] >= c.slots) {
+                record_error(ctx, kDevErrIndex);
+                slot[u] = -1;
+            }
         }
-        const float e = top >= -low ? top : low;
-        const __half dh = __float2half_rn(fminf(fmaxf(e * -0.125f, -65504.0f), 65504.0f));
-        const float d = __half2float(dh);
-        uint32_t q = 0x08080808u;
-        const bool finite = odd == 0.0f;
-        if (finite && d != 0.0f)
-            q = code_of(x.x, d) | (code_of(x.y, d) << 8) | (code_of(x.z, d) << 16) |
-                (code_of(x.w, d) << 24);
-        const uint32_t high = __shfl_down_sync(group, q, 4, 8);
-        const int lane8 = threadIdx.x & 7;
-        const int head = at * 4 / dim, block = (at * 4 - head * dim) / kQK;
-        const int64_t row = cache_row(c, slot, head);
-        if (lane8 < 4)
-            *reinterpret_cast<uint32_t *>(c.codes[half] + row * (dim / 2) + block * 16 + lane8 * 4) =
-                q | (high << 4);
-        if (lane8 == 0)
-            c.scales[half][row * (dim / kQK) + block] =
-                finite ? dh : __ushort_as_half(static_cast<unsigned short>(0x7FFF));
+        for (int i = sp.at; i < sp.per; i += kThreads) {
+            const int half = i >= quads, at = i - half * quads;
+            const T *src = (half ? v : k) + at * 4;
+            const int64_t stride = half ? v_stride : k_stride;
+            float4 x[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                x[u] = slot[u] >= 0 ? load_quad<kWide>(src + (base + u * sp.par) * stride)
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int head = at * 4 / dim, block = (at * 4 - head * dim) / kQK, lane8 = threadIdx.x & 7;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (slot[u] < 0) continue;  // the whole warp: one token
+                float top = fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w));
+                float low = fminf(fminf(x[u].x, x[u].y), fminf(x[u].z, x[u].w));
+                // 0 * x is NaN for the values that a block cannot hold
+                float odd = 0.0f * x[u].x + 0.0f * x[u].y + (0.0f * x[u].z + 0.0f * x[u].w);
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) {
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
+                    odd += __shfl_xor_sync(0xFFFFFFFFu, odd, o);
+                }
+                const float e = top >= -low ? top : low;
+                const __half dh = __float2half_rn(fminf(fmaxf(e * -0.125f, -65504.0f), 65504.0f));
+                const float d = __half2float(dh);
+                uint32_t q = 0x08080808u;
+                const bool finite = odd == 0.0f;
+                if (finite && d != 0.0f)
+                    q = code_of(x[u].x, d) | (code_of(x[u].y, d) << 8) | (code_of(x[u].z, d) << 16) |
+                        (code_of(x[u].w, d) << 24);
+                const uint32_t high = __shfl_down_sync(0xFFFFFFFFu, q, 4, 8);
+                const int64_t row = cache_row(c, slot[u], head);
+                if (lane8 < 4)
+                    *reinterpret_cast<uint32_t *>((half ? c.v_codes : c.k_codes) + row * (dim / 2) + block * 16 + lane8 * 4) =
+                        q | (high << 4);
+                if (lane8 == 0)
+                    (half ? c.v_scales : c.k_scales)[row * (dim / kQK) + block] =
+                        finite ? dh : __ushort_as_half(static_cast<unsigned short>(0x7FFF));
+            }
+        }
     }
 }
 
 // ---- read ----------------------------------------------------------------------
-// Eight lanes share a block, four consecutive values each (as dequant).
-// kWide: both outputs are 16-byte aligned.
+// Eight lanes share a block, four consecutive values each (as dequant); keys
+// and values as two halves of a token where both are wanted.
 template <bool kWide>
 __global__ void __launch_bounds__(kThreads) read_kernel(KvView c, const int64_t *__restrict__ slots,
                                                         int64_t n, int dim, float *__restrict__ k_out,
@@ -263,58 +292,90 @@ __global__ void __launch_bounds__(kThreads) read_kernel(KvView c, const int64_t 
     pdl_wait();
     pdl_launch_dependents();
     const int quads = c.kv_heads * dim / 4;
-    const int64_t total = n * quads;
-    const int half = blockIdx.y;
-    float *out = half ? v_out : k_out;
-    if (!out) return;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += step) {
-        const int64_t token = i / quads;
-        const int at = static_cast<int>(i - token * quads) * 4;
-        const int64_t slot = slots[token];
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (slot >= 0 && slot < c.slots) {
-            const int head = at / dim, in = at - head * dim;
-            const int64_t row = cache_row(c, slot, head);
-            const int j = in & 15;
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(c.codes[half] + row * (dim / 2) +
-                                                                   (in / kQK) * 16 + j) >>
-                               ((in & 16) ? 4 : 0);
-            const float d = __half2float(c.scales[half][row * (dim / kQK) + in / kQK]);
-            y.x = (static_cast<float>(w & 15u) - 8.0f) * d;
-            y.y = (static_cast<float>((w >> 8) & 15u) - 8.0f) * d;
-            y.z = (static_cast<float>((w >> 16) & 15u) - 8.0f) * d;
-            y.w = (static_cast<float>((w >> 24) & 15u) - 8.0f) * d;
-        } else if (slot != -1) {
-            record_error(ctx, kDevErrIndex);
+    const int only = k_out ? (v_out ? -1 : 0) : 1;  // the half that is wanted, or both
+    const Spread sp(only < 0 ? 2 * quads : quads);
+    if (sp.sub < 0) return;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * sp.par * kAhead + sp.sub; base < n;
+         base += static_cast<int64_t>(gridDim.x) * sp.par * kAhead) {
+        int64_t slot[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t token = base + u * sp.par;
+            slot[u] = token < n ? slots[token] : -1;
+            if (slot[u] < -1 || slot[u] >= c.slots) {
+                record_error(ctx, kDevErrIndex);
+                slot[u] = -1;
+            }
         }
-        float *dst = out + i * 4;
-        if constexpr (kWide) {
-            *reinterpret_cast<float4 *>(dst) = y;
-        } else {
-            dst[0] = y.x;
-            dst[1] = y.y;
-            dst[2] = y.z;
-            dst[3] = y.w;
+        for (int i = sp.at; i < sp.per; i += kThreads) {
+            const int half = only < 0 ? i >= quads : only, at = (only < 0 && half ? i - quads : i) * 4;
+            const int head = at / dim, in = at - head * dim;
+            uint32_t w[kAhead];
+            __half d[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                w[u] = 0x88888888u;  // zeros for slots that are not there
+                d[u] = __ushort_as_half(0);
+                if (slot[u] >= 0) {
+                    const int64_t row = cache_row(c, slot[u], head);
+                    w[u] = *reinterpret_cast<const uint32_t *>((half ? c.v_codes : c.k_codes) + row * (dim / 2) + (in / kQK) * 16 + (in & 15));
+                    d[u] = (half ? c.v_scales : c.k_scales)[row * (dim / kQK) + in / kQK];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int64_t token = base + u * sp.par;
+                if (token >= n) break;
+                const uint32_t q = w[u] >> ((in & 16) ? 4 : 0);
+                const float f = __half2float(d[u]);
+                float4 y;
+                y.x = (static_cast<float>(q & 15u) - 8.0f) * f;
+                y.y = (static_cast<float>((q >> 8) & 15u) - 8.0f) * f;
+                y.z = (static_cast<float>((q >> 16) & 15u) - 8.0f) * f;
+                y.w = (static_cast<float>((q >> 24) & 15u) - 8.0f) * f;
+                float *dst = (half ? v_out : k_out) + token * quads * 4 + at;
+                if constexpr (kWide) {
+                    *reinterpret_cast<float4 *>(dst) = y;
+                } else {
+                    dst[0] = y.x;
+                    dst[1] = y.y;
+                    dst[2] = y.z;
+                    dst[3] = y.w;
+                }
+            }
         }
     }
 }
 
 KvView view(const KvCache &c) {
     KvView v;
-    v.codes[0] = static_cast<uint8_t *>(c.k_codes);
-    v.codes[1] = static_cast<uint8_t *>(c.v_codes);
-    v.scales[0] = static_cast<__half *>(c.k_scales);
-    v.scales[1] = static_cast<__half *>(c.v_scales);
+    v.k_codes = static_cast<uint8_t *>(c.k_codes);
+    v.v_codes = static_cast<uint8_t *>(c.v_codes);
+    v.k_scales = static_cast<__half *>(c.k_scales);
+    v.v_scales = static_cast<__half *>(c.v_scales);
     v.slots = c.num_pages << c.page_shift;
     v.page_shift = c.page_shift;
     v.kv_heads = c.kv_heads;
     return v;
 }
 
-unsigned grid_for(int64_t threads, int per_sm) {
-    const int64_t cap = static_cast<int64_t>(device_sm_count()) * per_sm;
-    return static_cast<unsigned>(std::min((threads + kThreads - 1) / kThreads, cap));
+// CTAs for n tokens of `quads` quads each, at most 32 per SM.
+unsigned grid_for(int64_t n, int quads) {
+    const int64_t per_cta = static_cast<int64_t>(std::max(1, kThreads / quads)) * kAhead;
+    const int64_t cap = static_cast<int64_t>(device_sm_count()) * 32;
+    return static_cast<unsigned>(std::min((n + per_cta - 1) / per_cta, cap));
+}
+
+template <typename T>
+cudaError_t launch_append(const KvCache &c, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                          const int64_t *slots, int64_t n, cudaStream_t stream, const LaunchCtx &ctx) {
+    constexpr uintptr_t quad = 4 * sizeof(T);
+    const bool wide = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % quad == 0 &&
+                      k_stride % 4 == 0 && v_stride % 4 == 0;
+    const dim3 grid(grid_for(n, c.kv_heads * c.head_dim / 2));
+    return launch_kernel(wide ? append_kernel<T, true> : append_kernel<T, false>, grid, dim3(kThreads), 0, stream, 1,
+                         view(c), static_cast<const T *>(k), k_stride, static_cast<const T *>(v), v_stride, slots, n,
+                         c.head_dim, ctx);
 }
 
 }  // namespace
@@ -339,27 +400,16 @@ cudaError_t launch_kv_plan(const KvPlan &a, cudaStream_t stream, const LaunchCtx
 cudaError_t launch_kv_append(const KvCache &c, const void *k, int64_t k_stride, const void *v,
                              int64_t v_stride, bool bf16, const int64_t *slots, int64_t n,
                              cudaStream_t stream, const LaunchCtx &ctx) {
-    const int64_t threads = n * 2 * (static_cast<int64_t>(c.kv_heads) * c.head_dim / 4);
-    const uintptr_t wide_bytes = bf16 ? 8 : 16;
-    const bool wide = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % wide_bytes == 0 &&
-                      k_stride % 4 == 0 && v_stride % 4 == 0;
-    const dim3 grid(grid_for(threads, 8));
-    if (bf16)
-        return launch_kernel(append_kernel<uint16_t>, grid, dim3(kThreads), 0, stream, 1, view(c),
-                             static_cast<const uint16_t *>(k), k_stride,
-                             static_cast<const uint16_t *>(v), v_stride, slots, n, c.head_dim,
-                             static_cast<int>(wide), ctx);
-    return launch_kernel(append_kernel<float>, grid, dim3(kThreads), 0, stream, 1, view(c),
-                         static_cast<const float *>(k), k_stride, static_cast<const float *>(v),
-                         v_stride, slots, n, c.head_dim, static_cast<int>(wide), ctx);
+    return bf16 ? launch_append<uint16_t>(c, k, k_stride, v, v_stride, slots, n, stream, ctx)
+                : launch_append<float>(c, k, k_stride, v, v_stride, slots, n, stream, ctx);
 }
 
 cudaError_t launch_kv_read(const KvCache &c, const int64_t *slots, int64_t n, float *k_out,
                            float *v_out, cudaStream_t stream, const LaunchCtx &ctx) {
-    const int64_t threads = n * (static_cast<int64_t>(c.kv_heads) * c.head_dim / 4);
     const bool wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 15) == 0;
-    return launch_kernel(wide ? read_kernel<true> : read_kernel<false>, dim3(grid_for(threads, 8), 2), dim3(kThreads), 0, stream, 1,
-                         view(c), slots, n, c.head_dim, k_out, v_out, ctx);
+    const int quads = c.kv_heads * c.head_dim / 4 * (k_out && v_out ? 2 : 1);
+    return launch_kernel(wide ? read_kernel<true> : read_kernel<false>, dim3(grid_for(n, quads)), dim3(kThreads), 0,
+                         stream, 1, view(c), slots, n, c.head_dim, k_out, v_out, ctx);
 }
 
 }  // namespace qmm

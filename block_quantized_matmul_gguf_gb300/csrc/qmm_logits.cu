@@ -16,6 +16,7 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 8;  // history entries a thread has under way
 constexpr uint32_t kInPrompt = 0x80000000u;  // the other bits count what was generated
 
 __device__ __forceinline__ int32_t bounded(int32_t v, int64_t len, bool &bad) {
@@ -64,14 +65,24 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitsArgs a, LaunchCt
         const int32_t h0 = bounded(a.hist_start[row], a.history_len, bad);
         const int32_t h1 = bounded(a.hist_start[row + 1], a.history_len, bad);
         const int64_t made = h0 + static_cast<int64_t>(a.prompt_len ? max(a.prompt_len[row], 0) : 0);
-        for (int64_t h = h0 + static_cast<int64_t>(threadIdx.x); h < h1; h += kThreads) {
-            const int64_t id = a.history[h];
-            const int64_t e = id - base;
-            if (e >= 0 && e < S && id >= 0 && id < a.vocab) {
-                if (h < made)
-                    atomicOr(seen + e, kInPrompt);
-                else
-                    atomicAdd(seen + e, 1u);
+        const int first = static_cast<int>(max(base, int64_t(0))), count = static_cast<int>(min(base + S, a.vocab)) - first;
+        const int shift = static_cast<int>(first - base);
+        for (int64_t h = h0; h < h1; h += kThreads * kAhead) {
+            int32_t id[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int64_t i = h + u * kThreads + threadIdx.x;
+                id[u] = i < h1 ? a.history[i] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const uint32_t e = static_cast<uint32_t>(id[u]) - static_cast<uint32_t>(first);
+                if (e < static_cast<uint32_t>(count)) {  // also false for ids below 0
+                    if (h + u * kThreads + threadIdx.x < made)
+                        atomicOr(seen + shift + e, kInPrompt);
+                    else
+                        atomicAdd(seen + shift + e, 1u);
+                }
             }
         }
     }
@@ -162,6 +173,10 @@ cudaError_t launch_slices(const LogitsArgs &a, cudaStream_t stream, const Launch
 }  // namespace
 
 cudaError_t launch_logits_adjust(const LogitsArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    // Long slices read each history fewer times; short ones spread a few
+    // rows over the whole GPU.
+    const int64_t wide = a.rows * ((a.vocab + 8191) / 8192);
+    if (wide >= 2 * device_sm_count()) return launch_slices<8>(a, stream, ctx);
     return launch_slices<2>(a, stream, ctx);
 }
 

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import build as _build
 
@@ -161,10 +162,29 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
+_torch = None
+_raw_stream = None  # torch's own look-up of the current stream, without a Stream object
+
+
+def _torch_module():
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _torch = torch
+        current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if current is None or device is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            _raw_stream = lambda: current(device())  # noqa: E731
+    return _torch
+
+
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _torch_module().cuda.init()
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -351,68 +371,71 @@ def _typed(t, dtype, what: str) -> int:
     """The pointer of a contiguous tensor of this dtype (None: NULL)."""
     if t is None:
         return 0
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{what} must be {dtype}")
-    return _ptr(t)
+    if not t.is_cuda or not t.is_contiguous():
+        return _ptr(t)  # its errors
+    return t.data_ptr()
 
 
 def _rows(t, heads: int, dim: int, what: str):
     """(pointer, row stride, qmm_dtype) of [n][heads][dim] whose rows may lie apart."""
-    import torch
-    if t.dtype == torch.float32:
+    dtype = t.dtype
+    if dtype is _torch.float32:
         kind = QMM_F32
-    elif t.dtype == torch.bfloat16:
+    elif dtype is _torch.bfloat16:
         kind = QMM_BF16
     else:
         raise ValueError(f"{what} must be float32 or bfloat16")
     n, h, d = t.shape
-    stride = t.stride()
-    if h != heads or d != dim or (stride[2] != 1 and dim > 1) or (stride[1] != dim and heads > 1):
+    row, head, one = t.stride()
+    if h != heads or d != dim or (one != 1 and dim > 1) or (head != dim and heads > 1):
         raise ValueError(f"{what} must be [rows][{heads}][{dim}] with dense rows")
     if not t.is_cuda:
         raise ValueError("tensor must live on a CUDA device")
-    return t.data_ptr(), (stride[0] if n > 1 else heads * dim), kind
+    return t.data_ptr(), (row if n > 1 else heads * dim), kind
 
 
 def qmm_kv_plan(cached, added, free_pages, table, page_size: int, q_start, kv_len, slots, positions, taken,
                 stream=None) -> None:
     """Page tables and slot maps of the next step from the requests' lengths."""
-    import torch
-    i32, batch = torch.int32, cached.numel()
-    if added.numel() != batch or table.shape[0] != batch or q_start.numel() != batch + 1 or \
-            kv_len.numel() != batch or positions.numel() != slots.numel():
+    i32, batch, n = _torch_module().int32, cached.numel(), slots.numel()
+    rows, width = table.shape
+    if added.numel() != batch or rows != batch or q_start.numel() != batch + 1 or \
+            kv_len.numel() != batch or positions.numel() != n:
         raise ValueError("added, table, q_start, kv_len and positions must match cached and slots in size")
-    _check(load().qmm_kv_plan(
+    status = (_lib or load()).qmm_kv_plan(
         _typed(cached, i32, "cached"), _typed(added, i32, "added"), batch,
         _typed(free_pages, i32, "free_pages"), free_pages.numel(), _typed(table, i32, "table"),
-        table.shape[1], page_size, _typed(q_start, i32, "q_start"), _typed(kv_len, i32, "kv_len"),
-        _typed(slots, torch.int64, "slots"), _typed(positions, i32, "positions"), slots.numel(),
-        _typed(taken, i32, "taken"), _stream(stream)), "qmm_kv_plan")
+        width, page_size, _typed(q_start, i32, "q_start"), _typed(kv_len, i32, "kv_len"),
+        _typed(slots, _torch.int64, "slots"), _typed(positions, i32, "positions"), n,
+        _typed(taken, i32, "taken"), _stream(stream))
+    _check(status, "qmm_kv_plan")
 
 
 def qmm_kv_append_q4_0(cache: KvCacheQ4_0, k, v, slots, stream=None) -> None:
     """Quantize k and v [n][kv_heads][head_dim] (fp32 or bf16) into the slots of the cache."""
-    import torch
+    i64 = _torch_module().int64
     kp, ks, kind = _rows(k, cache.kv_heads, cache.head_dim, "k")
     vp, vs, other = _rows(v, cache.kv_heads, cache.head_dim, "v")
     n = slots.numel()
     if kind != other or k.shape[0] != n or v.shape[0] != n:
         raise ValueError("k and v must have one dtype and a row for each slot")
-    _check(load().qmm_kv_append_q4_0(cache.ref, kp, ks, vp, vs, kind, _typed(slots, torch.int64, "slots"),
-                                     n, _stream(stream)), "qmm_kv_append_q4_0")
+    status = (_lib or load()).qmm_kv_append_q4_0(cache.ref, kp, ks, vp, vs, kind, _typed(slots, i64, "slots"), n,
+                                                 _stream(stream))
+    _check(status, "qmm_kv_append_q4_0")
 
 
 def qmm_kv_read_q4_0(cache: KvCacheQ4_0, slots, k_out, v_out, stream=None) -> None:
     """The fp32 values of cache slots, k_out and v_out [n][kv_heads][head_dim] (either may be None)."""
-    import torch
-    n = slots.numel()
-    for t in (k_out, v_out):
-        if t is not None and t.numel() != n * cache.kv_heads * cache.head_dim:
-            raise ValueError("outputs must be [slots][kv_heads][head_dim]")
-    _check(load().qmm_kv_read_q4_0(cache.ref, _typed(slots, torch.int64, "slots"), n,
-                                   _typed(k_out, torch.float32, "k_out"),
-                                   _typed(v_out, torch.float32, "v_out"), _stream(stream)),
-           "qmm_kv_read_q4_0")
+    f32, n = _torch_module().float32, slots.numel()
+    size = n * cache.kv_heads * cache.head_dim
+    if (k_out is not None and k_out.numel() != size) or (v_out is not None and v_out.numel() != size):
+        raise ValueError("outputs must be [slots][kv_heads][head_dim]")
+    status = (_lib or load()).qmm_kv_read_q4_0(cache.ref, _typed(slots, _torch.int64, "slots"), n,
+                                               _typed(k_out, f32, "k_out"), _typed(v_out, f32, "v_out"),
+                                               _stream(stream))
+    _check(status, "qmm_kv_read_q4_0")
 
 
 def attn_workspace(cache: KvCacheQ4_0, heads: int):
@@ -422,37 +445,43 @@ def attn_workspace(cache: KvCacheQ4_0, heads: int):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k_codes.device)
 
 
+# struct qmm_attn_args and qmm_logits_args with the compiler's own padding
+# (AttnArgs and LogitsArgs name the fields)
+_ATTN_ARGS = struct.Struct("@PqiPqiPPqPPiqiifiiPN")
+_LOGITS_ARGS = struct.Struct("@PqPqqqPPqPPPPPPPqP")
+
+
 def qmm_attn_q4_0(cache: KvCacheQ4_0, q, out, table, q_start, kv_len, max_q: int, scale: float,
                   causal: bool = True, window: int = 0, lse=None, workspace=None, stream=None) -> None:
     """Attention of q [rows][heads][head_dim] (fp32 or bf16) over the cache into out (fp32 or bf16)."""
-    import torch
-    i32, heads = torch.int32, q.shape[1]
+    i32 = _torch_module().int32
+    rows, heads, _ = q.shape
     qp, q_stride, q_type = _rows(q, heads, cache.head_dim, "q")
     op, out_stride, out_type = _rows(out, heads, cache.head_dim, "out")
-    batch, rows = kv_len.numel(), q.shape[0]
-    if out.shape[0] != rows or table.shape[0] != batch or q_start.numel() != batch + 1 or \
+    batch = kv_len.numel()
+    tables, width = table.shape
+    if out.shape[0] != rows or tables != batch or q_start.numel() != batch + 1 or \
             (lse is not None and lse.numel() != rows * heads):
         raise ValueError("out, lse, table and q_start must match q and kv_len in size")
     if workspace is None:
         workspace = attn_workspace(cache, heads)
-    args = AttnArgs(qp, q_stride, q_type, op, out_stride, out_type,
-                    _typed(lse, torch.float32, "lse"), _typed(table, i32, "table"), table.shape[1],
-                    _typed(q_start, i32, "q_start"), _typed(kv_len, i32, "kv_len"), batch, rows, max_q,
-                    heads, scale, int(causal), window, _ptr(workspace),
-                    workspace.numel() * workspace.element_size())
-    _check(load().qmm_attn_q4_0(cache.ref, ctypes.addressof(args), _stream(stream)), "qmm_attn_q4_0")
+    args = _ATTN_ARGS.pack(qp, q_stride, q_type, op, out_stride, out_type, _typed(lse, _torch.float32, "lse"),
+                           _typed(table, i32, "table"), width, _typed(q_start, i32, "q_start"),
+                           _typed(kv_len, i32, "kv_len"), batch, rows, max_q, heads, scale, bool(causal), window,
+                           _ptr(workspace), workspace.numel() * workspace.element_size())
+    _check((_lib or load()).qmm_attn_q4_0(cache.ref, args, _stream(stream)), "qmm_attn_q4_0")
 
 
 def qmm_logits_adjust(logits, out, history=None, hist_start=None, prompt_len=None, repetition=None,
                       frequency=None, presence=None, bias_ids=None, bias_values=None, bias_start=None,
                       allowed=None, stream=None) -> None:
     """Penalties, biases and grammar masks on logits [rows][vocab] (fp32); out may be logits."""
-    import torch
+    torch = _torch_module()
     i32, f32 = torch.int32, torch.float32
     rows, vocab = logits.shape
-    for t, what in ((logits, "logits"), (out, "out")):
-        if t.dtype != f32 or tuple(t.shape) != (rows, vocab) or (t.stride(1) != 1 and vocab > 1) or not t.is_cuda:
-            raise ValueError(f"{what} must be float32 [rows][vocab] on a CUDA device with dense rows")
+    for t in (logits, out):
+        if t.dtype is not f32 or t.shape != logits.shape or (t.stride(1) != 1 and vocab > 1) or not t.is_cuda:
+            raise ValueError("logits and out must be float32 [rows][vocab] on a CUDA device with dense rows")
     for t, n, what in ((hist_start, rows + 1, "hist_start"), (bias_start, rows + 1, "bias_start"),
                        (prompt_len, rows, "prompt_len"), (repetition, rows, "repetition"),
                        (frequency, rows, "frequency"), (presence, rows, "presence"),
@@ -462,15 +491,15 @@ def qmm_logits_adjust(logits, out, history=None, hist_start=None, prompt_len=Non
     if (bias_ids is None) != (bias_values is None) or \
             (bias_ids is not None and bias_ids.numel() != bias_values.numel()):
         raise ValueError("bias_ids and bias_values go together")
-    args = LogitsArgs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab,
-                      out.data_ptr(), out.stride(0) if rows > 1 else vocab, rows, vocab,
-                      _typed(history, i32, "history"), _typed(hist_start, i32, "hist_start"),
-                      0 if history is None else history.numel(), _typed(prompt_len, i32, "prompt_len"),
-                      _typed(repetition, f32, "repetition"), _typed(frequency, f32, "frequency"),
-                      _typed(presence, f32, "presence"), _typed(bias_ids, i32, "bias_ids"),
-                      _typed(bias_values, f32, "bias_values"), _typed(bias_start, i32, "bias_start"),
-                      0 if bias_ids is None else bias_ids.numel(), _typed(allowed, i32, "allowed"))
-    _check(load().qmm_logits_adjust(ctypes.addressof(args), _stream(stream)), "qmm_logits_adjust")
+    args = _LOGITS_ARGS.pack(
+        logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, out.data_ptr(),
+        out.stride(0) if rows > 1 else vocab, rows, vocab, _typed(history, i32, "history"),
+        _typed(hist_start, i32, "hist_start"), 0 if history is None else history.numel(),
+        _typed(prompt_len, i32, "prompt_len"), _typed(repetition, f32, "repetition"),
+        _typed(frequency, f32, "frequency"), _typed(presence, f32, "presence"), _typed(bias_ids, i32, "bias_ids"),
+        _typed(bias_values, f32, "bias_values"), _typed(bias_start, i32, "bias_start"),
+        0 if bias_ids is None else bias_ids.numel(), _typed(allowed, i32, "allowed"))
+    _check((_lib or load()).qmm_logits_adjust(args, _stream(stream)), "qmm_logits_adjust")
 
 
 # ---- tensor-level conveniences (allocate the output, then call the ABI) ----

@@ -148,3 +148,14 @@ def test_logits_checks(lib, kw, status):
 
 def test_index_status_has_its_text(lib):
     assert "outside" in qmm.status_string(qmm.QMM_ERR_INDEX)
+
+
+def test_packed_arguments_have_the_structs_layout():
+    """The binding packs the argument structs; each field must land where the
+    declared struct has it."""
+    for packer, cls in ((qmm._ATTN_ARGS, qmm.AttnArgs), (qmm._LOGITS_ARGS, qmm.LogitsArgs)):
+        values = list(range(1, len(cls._fields_) + 1))
+        raw = packer.pack(*values)
+        assert ctypes.sizeof(cls) - 8 < len(raw) <= ctypes.sizeof(cls)
+        s = cls.from_buffer_copy(raw.ljust(ctypes.sizeof(cls), b"\0"))
+        assert [getattr(s, name) for name, _ in cls._fields_] == values
