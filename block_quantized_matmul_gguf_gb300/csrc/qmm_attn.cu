@@ -68,7 +68,7 @@ struct Layout {
     static constexpr int rest_bytes = p + (EXACT ? rows * p_stride * 4 : 0);
     // CTAs on an SM: as the registers of the accumulators allow
     static constexpr int ctas = D == 256 ? 1 : D == 128 && NT == 2 ? 1 : 2;
-    static constexpr int fit = (232448 / ctas - 1024 - 4096) / (code_bytes + rest_bytes);
+    static constexpr int fit = (232448 / ctas - 1024 - 14336) / (code_bytes + rest_bytes);
     static constexpr int warps = fit < kWarps ? fit : kWarps;  // as many as fit shared memory
     static constexpr int threads = warps * 32;
     static_assert(rows * D * 4 <= code_bytes, "a partial record fits the code buffers");
@@ -91,14 +91,27 @@ enum : int {
     kEmpty = 16       // no tiles at all
 };
 
+// One request as the line sees it.
+struct Request {
+    int row0, rows;      // first row of q, and rows that are there
+    int len;             // keys, within the table
+    int first;           // position of row 0 (may be negative)
+    int tile0, tiles;    // of every item of the request
+    int groups;          // row groups
+    int bad;
+};
+
 // What the CTA's threads share, after the warps' buffers.
 struct Shared {
-    int64_t prefix[kThreads];  // tiles before each thread's requests
-    int64_t scratch[kWarps];
-    uint64_t bars[kWarps][2];  // K tile, V tile
+    int64_t prefix[kThreads];   // line places before each thread's requests
+    Request request[kThreads];  // the requests, where every thread has at most one
+    int64_t scratch[kWarps][2];
+    uint64_t bars[kWarps][2];   // K tile, V tile
     int flags[kWarps];
-    Target target[kWarps][2];     // of head and tail
-    float stat[kWarps][2][8][2];  // maximum and sum of each row
+    Target target[kWarps][2];      // of head and tail
+    float stat[kWarps][2][8][2];   // maximum and sum of each row
+    float weight[8][kWarps];       // of a chain's parts, by row
+    float total[8][2];             // its maximum and sum
 };
 
 // A CTA's parts in global memory, the same way: flags and the tail's target.
@@ -112,6 +125,7 @@ struct StreamParams {
     const __half *k_scales, *v_scales;
     int64_t num_pages;
     int page_shift, kv_heads;
+    bool q_pairs;         // rows of q are aligned to two values
     float *warp_records;  // [CTAs * kWarps]: head parts that are not the last
     float *cta_records;   // [CTAs][2]: head and tail part
     CtaParts *parts;      // [CTAs]
@@ -199,15 +213,11 @@ __device__ __forceinline__ void store_value(void *p, int64_t i, bool bf16, float
 
 // ---- the line of tiles -----------------------------------------------------------
 
-// One request as the line sees it.
-struct Request {
-    int row0, rows;      // first row of q, and rows that are there
-    int len;             // keys, within the table
-    int first;           // position of row 0 (may be negative)
-    int tile0, tiles;    // of every item of the request
-    int groups;          // row groups
-    bool bad;
-};
+// The first key that position pos sees, and the number of tiles up to key n.
+__device__ __forceinline__ int first_key(const AttnArgs &a, int pos) {
+    return a.window && pos >= a.window ? pos - a.window + 1 : 0;
+}
+__device__ __forceinline__ int tiles_to(int n) { return (n + kTile - 1) / kTile; }
 
 template <int ROWS>
 __device__ __forceinline__ Request request(const StreamParams &p, int b) {
@@ -217,73 +227,95 @@ __device__ __forceinline__ Request request(const StreamParams &p, int b) {
     const int n = max(s1 - s0, 0), len = a.kv_len[b];
     r.row0 = min(max(s0, 0), total);
     r.rows = min(max(min(s1, total) - r.row0, 0), n);
-    const int64_t room = a.table_width << p.page_shift;
+    const int64_t room = min(a.table_width << p.page_shift, static_cast<int64_t>(INT32_MAX - 2 * kTile));
     r.len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), room));
     r.first = max(len, 0) - n;
     r.bad = s0 < 0 || s1 > total || s1 < s0 || n > a.max_q || len < 0 || len > room;
-    const int lo = a.window ? max(0, r.first - a.window + 1) : 0;
-    r.tile0 = lo / kTile;
-    r.tiles = max(1, (r.len + kTile - 1) / kTile - r.tile0);
+    r.tile0 = first_key(a, r.first) / kTile;
+    r.tiles = max(1, tiles_to(r.len) - r.tile0);
     r.groups = (r.rows * (a.heads / p.kv_heads) + ROWS - 1) / ROWS;
     return r;
 }
 
-template <int ROWS>
-__device__ __forceinline__ int64_t request_tiles(const StreamParams &p, const Request &r) {
-    return static_cast<int64_t>(r.tiles) * r.groups * p.kv_heads;
+// The line: where each warp's tiles lie.  Places are tiles; in the spread
+// form an item takes a whole number of CTAs' warps, one tile each.
+struct Line {
+    int64_t total;
+    bool spread;
+};
+
+// Places of one item.
+template <int W>
+__device__ __forceinline__ int item_places(const Request &r, bool spread) {
+    return spread ? (r.tiles + W - 1) / W * W : r.tiles;
 }
 
-// Fills sh.prefix; returns the number of tiles.
-template <int ROWS, int THREADS>
-__device__ __forceinline__ int64_t build_line(const StreamParams &p, Shared &sh) {
-    const int per = (p.a.batch + THREADS - 1) / THREADS;
+// Fills sh.prefix (and sh.request).  Spread is taken when no warp then gets
+// more than one tile: an item of few tiles is then joined within its CTA.
+template <int ROWS, int W>
+__device__ __forceinline__ Line build_line(const StreamParams &p, Shared &sh) {
+    constexpr int threads = W * 32;
+    const int per = (p.a.batch + threads - 1) / threads;
     const int b0 = min(p.a.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.a.batch, b0 + per);
-    int64_t mine = 0;
-    bool bad = false;
+    int64_t tiles = 0, places = 0;
+    int bad = 0;
     for (int b = b0; b < b1; ++b) {
         const Request r = request<ROWS>(p, b);
-        mine += request_tiles<ROWS>(p, r);
+        const int64_t items = static_cast<int64_t>(r.groups) * p.kv_heads;
+        tiles += items * r.tiles;
+        places += items * item_places<W>(r, true);
         bad |= r.bad;
+        if (per == 1) sh.request[threadIdx.x] = r;
     }
     if (bad && blockIdx.x == 0) record_error(p.ctx, kDevErrIndex);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t sum = mine;
+    int64_t sum[2] = {tiles, places};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += up;
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum[0], o), y = __shfl_up_sync(0xFFFFFFFFu, sum[1], o);
+        if (lane >= o) {
+            sum[0] += x;
+            sum[1] += y;
+        }
     }
-    if (lane == 31) sh.scratch[warp] = sum;
+    if (lane == 31) {
+        sh.scratch[warp][0] = sum[0];
+        sh.scratch[warp][1] = sum[1];
+    }
     __syncthreads();
-    int64_t before = 0, total = 0;
+    int64_t before[2] = {0, 0}, total[2] = {0, 0};
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += sh.scratch[w];
-        total += sh.scratch[w];
-    }
-    sh.prefix[threadIdx.x] = before + sum - mine;
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (w < warp) before[i] += sh.scratch[w][i];
+            total[i] += sh.scratch[w][i];
+        }
+    const bool spread = total[1] <= static_cast<int64_t>(gridDim.x) * W;
+    sh.prefix[threadIdx.x] = spread ? before[1] + sum[1] - places : before[0] + sum[0] - tiles;
     __syncthreads();
-    return total;
+    return Line{spread ? total[1] : total[0], spread};
 }
 
-// The request that holds tile x of the line, and the tiles before it.
-template <int ROWS, int THREADS>
-__device__ __forceinline__ int find_request(const StreamParams &p, const Shared &sh, int64_t x, int64_t &before,
-                                            Request &r) {
-    int lo = 0, hi = THREADS;  // prefix[lo] <= x < prefix[hi]; equal entries: the last one holds requests
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sh.prefix[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
+// The request that holds place x of the line, and the places before it.
+template <int ROWS, int W>
+__device__ __forceinline__ int find_request(const StreamParams &p, const Shared &sh, const Line &line, int64_t x,
+                                            int64_t &before, Request &r) {
+    constexpr int threads = W * 32;
+    // the last thread whose prefix is at most x holds it: 8 ranges a lane
+    const int lane = threadIdx.x & 31;
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) count += __popc(__ballot_sync(0xFFFFFFFFu, sh.prefix[i * 32 + lane] <= x));
+    const int at = count - 1, per = (p.a.batch + threads - 1) / threads;
+    before = sh.prefix[at];
+    if (per == 1) {
+        r = sh.request[at];
+        return at;
     }
-    const int per = (p.a.batch + THREADS - 1) / THREADS;
-    int b = lo * per;
-    before = sh.prefix[lo];
-    for (;; ++b) {
+    for (int b = at * per;; ++b) {
         r = request<ROWS>(p, b);
-        const int64_t n = request_tiles<ROWS>(p, r);
+        const int64_t n = static_cast<int64_t>(item_places<W>(r, line.spread)) * r.groups * p.kv_heads;
         if (x < before + n || b + 1 >= p.a.batch) return b;
         before += n;
     }
@@ -354,38 +386,62 @@ __device__ __forceinline__ void issue(const StreamParams &p, const CUtensorMap *
     if (there) copy(page, k, step);
 }
 
-// q of the item's rows as B fragments, scaled to below 2^15, with -8 times
-// the block sums (the codes are used as 0..15).
+// The lane's D / 32 consecutive values of each of the item's rows of q: they
+// lie in one block.  Rows past the end repeat the last.
 template <int D, int NT, bool EXACT>
-__device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, EXACT> &w, const Request &r,
-                                        const Item &it) {
-    using L = Layout<D, NT, EXACT>;
-    constexpr int NB = L::NB, E = D / 32;  // values per lane: a lane's lie in one block
+struct QueryRows {
+    float v[Layout<D, NT, EXACT>::rows][D / 32];
+    int pos[Layout<D, NT, EXACT>::rows];
+};
+
+template <int D, int NT, bool EXACT>
+__device__ __forceinline__ void load_q(const StreamParams &p, QueryRows<D, NT, EXACT> &q, const Request &r,
+                                       const Item &it, int lane) {
+    constexpr int ROWS = Layout<D, NT, EXACT>::rows, E = D / 32;
     const AttnArgs &a = p.a;
     const int heads = a.heads / p.kv_heads, all = r.rows * heads;
+#pragma unroll
+    for (int row = 0; row < ROWS; ++row) {
+        const int flat = min(it.group * ROWS + row, all - 1), token = flat / heads;
+        const int64_t at = (static_cast<int64_t>(r.row0) + token) * a.q_stride +
+                           static_cast<int64_t>(it.kv_head * heads + flat - token * heads) * D + lane * E;
+        q.pos[row] = r.first + token;
+        if (p.q_pairs) {  // rows are aligned to pairs of values
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                if (a.q_bf16) {
+                    const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.q) + at + i);
+                    q.v[row][i] = __uint_as_float(u << 16);
+                    q.v[row][i + 1] = __uint_as_float(u & 0xFFFF0000u);
+                } else {
+                    const float2 u = *reinterpret_cast<const float2 *>(static_cast<const float *>(a.q) + at + i);
+                    q.v[row][i] = u.x;
+                    q.v[row][i + 1] = u.y;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) q.v[row][i] = load_value(a.q, at + i, a.q_bf16);
+        }
+    }
+}
+
+// Those rows as B fragments, scaled to below 2^15, with -8 times the block
+// sums (the codes are used as 0..15).
+template <int D, int NT, bool EXACT>
+__device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, EXACT> &w,
+                                        QueryRows<D, NT, EXACT> &rows, const Request &r) {
+    using L = Layout<D, NT, EXACT>;
+    constexpr int NB = L::NB, E = D / 32;
+    const AttnArgs &a = p.a;
+    float (&v)[L::rows][E] = rows.v;
+    const int (&pos)[L::rows] = rows.pos;
     __half *frag = reinterpret_cast<__half *>(w.rest + L::q);
     float *bias = reinterpret_cast<float *>(w.rest + L::bias);
     const int d0 = w.lane * E, block = d0 / 32;
     // the sign of the scale goes to q; a scale of 0 takes q with it
     const float size = fabsf(a.scale) * kLog2e, sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
     const int size_up = exponent(size);
-    // all rows' loads first
-    float v[L::rows][E];
-    int pos[L::rows];
-#pragma unroll
-    for (int row = 0; row < L::rows; ++row) {
-        const int flat = min(it.group * L::rows + row, all - 1);  // rows past the end repeat the last
-        const int token = flat / heads, head = it.kv_head * heads + flat - token * heads;
-        const int64_t at = (static_cast<int64_t>(r.row0) + token) * a.q_stride + static_cast<int64_t>(head) * D + d0;
-        pos[row] = r.first + token;
-        if (a.q_bf16) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[row][i] = load_value(a.q, at + i, true);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[row][i] = load_value(a.q, at + i, false);
-        }
-    }
 #pragma unroll
     for (int row = 0; row < L::rows; ++row) {
         uint32_t bits = 0;  // of the largest value: positive numbers order as their bits do
@@ -435,7 +491,7 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
         }
         // the lane that holds this row's scores keeps their unit and range
         const int hi = a.causal ? min(r.len, pos[row] + 1) : r.len;
-        const int lo = a.window ? max(0, pos[row] - a.window + 1) : 0;
+        const int lo = first_key(a, pos[row]);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -698,10 +754,10 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
     const int heads = a.heads / p.kv_heads, all = r.rows * heads;
     const int pos0 = r.first + it.group * L::rows / heads;
     const int pos1 = r.first + (min((it.group + 1) * L::rows, all) - 1) / heads;
-    const int lo = a.window ? max(0, pos0 - a.window + 1) : 0, hi = a.causal ? min(r.len, pos1 + 1) : r.len;
-    const int lo_all = a.window ? max(0, pos1 - a.window + 1) : 0, hi_all = a.causal ? min(r.len, pos0 + 1) : r.len;
+    const int lo = first_key(a, pos0), hi = a.causal ? min(r.len, pos1 + 1) : r.len;
+    const int lo_all = first_key(a, pos1), hi_all = a.causal ? min(r.len, pos0 + 1) : r.len;
     t0 = max(t0, lo / kTile - r.tile0);
-    t1 = min(t1, (hi + kTile - 1) / kTile - r.tile0);
+    t1 = min(t1, tiles_to(hi) - r.tile0);
     if (w.dead) return;
 
     // page indices of the tiles ahead
@@ -716,13 +772,15 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
         }
     };
     uint8_t *const vcodes = w.codes + L::codes, *const vscales = w.rest + L::v_scales;
+    QueryRows<D, NT, EXACT> rows;
     if (t0 < t1) {
         const int key0 = (r.tile0 + t0) * kTile;
         ahead(key0);
+        load_q(p, rows, r, it, w.lane);  // under way while the pages are looked up
         issue<D>(p, kmap, p.k_scales, w.codes, w.rest, w.bars, it.kv_head, key0, lo, hi, pages);
         issue<D>(p, vmap, p.v_scales, vcodes, vscales, w.bars + 1, it.kv_head, key0, lo, hi, pages);
+        stage_q(p, w, rows, r);
     }
-    stage_q<D, NT, EXACT>(p, w, r, it);
     for (int tile = t0; tile < t1; ++tile) {
         const int key0 = (r.tile0 + tile) * kTile;
         // 16-key groups whose page can be read: lane i looks at group i
@@ -924,13 +982,19 @@ __device__ __forceinline__ bool locate(const StreamParams &p, const Target &to, 
     return true;
 }
 
+// Four consecutive outputs of an item's row, from their weighted sums.
 template <int D, int ROWS>
-__device__ __forceinline__ void write_out(const StreamParams &p, const Target &to, int row, int d, float v, float sum) {
+__device__ __forceinline__ void write_out(const StreamParams &p, const Target &to, int row, int d, const float4 &v,
+                                          float sum) {
     int64_t at;
     int head;
-    if (locate<ROWS>(p, to, row, at, head))
-        store_value(p.a.out, at * p.a.out_stride + static_cast<int64_t>(head) * D + d, p.a.out_bf16,
-                    sum == 0.0f ? 0.0f : v / sum);
+    if (!locate<ROWS>(p, to, row, at, head)) return;
+    at = at * p.a.out_stride + static_cast<int64_t>(head) * D + d;
+    const float down = sum == 0.0f ? 0.0f : 1.0f / sum;
+    store_value(p.a.out, at, p.a.out_bf16, v.x * down);
+    store_value(p.a.out, at + 1, p.a.out_bf16, v.y * down);
+    store_value(p.a.out, at + 2, p.a.out_bf16, v.z * down);
+    store_value(p.a.out, at + 3, p.a.out_bf16, v.w * down);
 }
 
 template <int ROWS>
@@ -958,7 +1022,7 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
     pdl_wait();
     pdl_launch_dependents();
     asm volatile("fence.proxy.async.global;" ::: "memory");  // the cache's last writer used plain stores
-    const int64_t total = build_line<ROWS, L::threads>(p, sh);
+    const Line line = build_line<ROWS, W>(p, sh);
 
     WarpState<D, NT, EXACT> w;
     w.codes = base + warp * L::code_bytes;
@@ -971,18 +1035,26 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
     w.dead = false;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * W;
     const int64_t me = static_cast<int64_t>(blockIdx.x) * W + warp;
-    const int64_t x0 = total * me / warps, x1 = total * (me + 1) / warps;
-    int flags = x0 < x1 ? 0 : kEmpty;
+    // equal shares of the line, or one place each
+    const int64_t share = line.total / warps, left = line.total - share * warps;
+    const int64_t x0 = line.spread ? min(me, line.total) : share * me + min(me, left);
+    const int64_t x1 = line.spread ? min(me + 1, line.total) : x0 + share + (me < left ? 1 : 0);
+    int flags = kEmpty;
     for (int64_t x = x0; x < x1;) {
         int64_t before;
         Request r;
         Item it;
-        it.b = find_request<ROWS, L::threads>(p, sh, x, before, r);
-        const int item = static_cast<int>((x - before) / r.tiles);
+        it.b = find_request<ROWS, W>(p, sh, line, x, before, r);
+        const int places = item_places<W>(r, line.spread);
+        // most offsets fit 32 bits, whose division is far cheaper
+        const int64_t off = x - before;
+        const int item = off <= INT32_MAX ? static_cast<int>(off) / places : static_cast<int>(off / places);
         it.kv_head = item / r.groups;
         it.group = item - it.kv_head * r.groups;
-        const int t0 = static_cast<int>(x - before - static_cast<int64_t>(item) * r.tiles);
+        const int t0 = static_cast<int>(off - static_cast<int64_t>(item) * places);
+        if (t0 >= r.tiles) break;  // a place without a tile (spread: the warp's only one)
         const int t1 = static_cast<int>(min(static_cast<int64_t>(r.tiles), t0 + (x1 - x)));
+        flags &= ~kEmpty;
         run_part<D, NT, EXACT>(p, &kmap, &vmap, w, r, it, t0, t1);
         x += t1 - t0;
         const Target to = target_of(r, it);
@@ -1049,35 +1121,51 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
             const Target to = sh.target[c][kind];
             const bool whole = kind == 1 && !open;
             float *dst = p.cta_records + (static_cast<int64_t>(blockIdx.x) * 2 + kind) * kRecord;
-            for (int i = threadIdx.x; i < ROWS * D; i += L::threads) {
-                const int row = i / D, d = i - row * D;
-                const float *sc = sh.stat[c][kind][row];
-                float top = sc[0];
-                for (int j = c + 1; j < W; ++j)
-                    if ((members >> j) & 1u) top = fmaxf(top, sh.stat[j][0][row][0]);
+            if (threadIdx.x < ROWS * kWarps) {  // weights of the parts, eight lanes a row
+                const int row = threadIdx.x / kWarps, j = threadIdx.x % kWarps;
+                const bool member = j < W && (j == c || (j > c && ((members >> j) & 1u)));
+                const float *st = sh.stat[member ? j : c][member && j > c ? 0 : kind][row];
+                float top = st[0];
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
                 const float ref = top == __uint_as_float(0xFF800000u) ? 0.0f : top;
-                float v = 0.0f, sum = 0.0f;
-                for (int j = c; j < W; ++j) {
-                    if (j > c && !((members >> j) & 1u)) continue;
-                    const int kj = j == c ? kind : 0;
-                    const float *rec = kj == 1 || (sh.flags[j] & kHeadLast)
-                                           ? reinterpret_cast<const float *>(base + j * L::code_bytes)
-                                           : p.warp_records + (static_cast<int64_t>(blockIdx.x) * W + j) * kRecord;
-                    const float f = exp2_fast(sh.stat[j][kj][row][0] - ref);
-                    v = fmaf(f, rec[i], v);
-                    sum = fmaf(f, sh.stat[j][kj][row][1], sum);
-                }
-                if (whole) {
-                    write_out<D, ROWS>(p, to, row, d, v, sum);
-                    if (d == 0) write_lse<ROWS>(p, to, row, top, sum);
-                } else {
-                    dst[i] = v;
-                    if (d == 0) {
-                        dst[kRecordStat + 2 * row] = top;
-                        dst[kRecordStat + 2 * row + 1] = sum;
-                    }
+                const float f = member ? exp2_fast(st[0] - ref) : 0.0f;
+                float sum = member ? f * st[1] : 0.0f;
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                sh.weight[row][j] = f;
+                if (j == 0) {
+                    sh.total[row][0] = top;
+                    sh.total[row][1] = sum;
+                    if (whole)
+                        write_lse<ROWS>(p, to, row, top, sum);
+                    else
+                        *reinterpret_cast<float2 *>(dst + kRecordStat + 2 * row) = make_float2(top, sum);
                 }
             }
+            __syncthreads();
+            for (int i = threadIdx.x; i < ROWS * D / 4; i += L::threads) {
+                const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    if (j != c && !((members >> j) & 1u)) continue;
+                    const bool inside = (j == c && kind == 1) || (sh.flags[j] & kHeadLast);
+                    const float *rec = inside ? reinterpret_cast<const float *>(base + j * L::code_bytes)
+                                              : p.warp_records + (static_cast<int64_t>(blockIdx.x) * W + j) * kRecord;
+                    const float4 x = *reinterpret_cast<const float4 *>(rec + i * 4);
+                    const float f = sh.weight[row][j];
+                    v.x = fmaf(f, x.x, v.x);
+                    v.y = fmaf(f, x.y, v.y);
+                    v.z = fmaf(f, x.z, v.z);
+                    v.w = fmaf(f, x.w, v.w);
+                }
+                if (whole)
+                    write_out<D, ROWS>(p, to, row, d, v, sh.total[row][1]);
+                else
+                    *reinterpret_cast<float4 *>(dst + i * 4) = v;
+            }
+            __syncthreads();
             if (!whole) {
                 if (kind == 0) {
                     mine.flags |= kHead | (open ? kHeadOpen : 0);
@@ -1092,59 +1180,96 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
 }
 
 // Joins the items that several CTAs hold: CTA x of this grid the one that CTA
-// x's tail begins, 256 outputs of it per y.
-constexpr int kMaxCtas = 1024;
+// x's tail begins, 128 outputs of it per y.  The eight warps take every eighth
+// part each, a lane four outputs of it.
+constexpr int kMaxCtas = 512;
+constexpr int kJoinOutputs = 128;
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const StreamParams p) {
-    constexpr int RB = kThreads / D;  // rows of a CTA
+    constexpr int RB = D < kJoinOutputs ? kJoinOutputs / D : 1;  // rows of a CTA
     __shared__ int flags[kMaxCtas];
-    __shared__ int last;
-    __shared__ float tops[RB];
+    __shared__ int list[kMaxCtas];
+    __shared__ int count;
     __shared__ float weight[RB][kMaxCtas];
+    __shared__ float total[RB][2];
+    __shared__ float4 share[kWarps][32];
     pdl_wait();
     pdl_launch_dependents();
-    const int n = gridDim.x, c = blockIdx.x;
-    if (!(p.parts[c].flags & kTail)) return;
+    const int n = gridDim.x, c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const CtaParts mine = p.parts[c];
+    if (!(mine.flags & kTail)) return;
     for (int i = threadIdx.x; i < n; i += kThreads) flags[i] = p.parts[i].flags;
-    if (threadIdx.x == 0) last = n - 1;
     __syncthreads();
-    // the chain ends at the first head after c that is not open
-    for (int i = c + 1 + threadIdx.x; i < n; i += kThreads)
-        if (!(flags[i] & kEmpty) && !(flags[i] & kHeadOpen)) atomicMin(&last, i);
-    __syncthreads();
-    const int end = last;
-    const int sub = threadIdx.x / D, d = threadIdx.x - sub * D, row = blockIdx.y * RB + sub;
-    auto record = [&](int j) { return p.cta_records + (static_cast<int64_t>(j) * 2 + (j == c ? 1 : 0)) * kRecord; };
-    // each row's maximum and weights, by the row's threads (whole warps)
-    const float ninf = __uint_as_float(0xFF800000u);
-    float top = ninf;
-    for (int j = c + (d & 31); j <= end; j += 32)
-        if (j == c || (flags[j] & kHead)) top = fmaxf(top, record(j)[kRecordStat + 2 * row]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float ref = top == ninf ? 0.0f : top;
-    float sum = 0.0f;
-    for (int j = c + (d & 31); j <= end; j += 32) {
-        float f = 0.0f;
-        if (j == c || (flags[j] & kHead)) {
-            f = exp2_fast(record(j)[kRecordStat + 2 * row] - ref);
-            sum = fmaf(f, record(j)[kRecordStat + 2 * row + 1], sum);
+    if (warp == 0) {  // the parts: c's tail, then heads up to the first that is not open
+        int k = 1;
+        if (lane == 0) list[0] = c;
+        for (int i = c + 1; i < n; i += 32) {
+            const int f = i + lane < n ? flags[i + lane] : kEmpty;
+            const bool there = !(f & kEmpty), ends = there && !(f & kHeadOpen);
+            const unsigned stop = __ballot_sync(0xFFFFFFFFu, ends);
+            const unsigned upto = stop ? (stop & -stop) * 2u - 1u : 0xFFFFFFFFu;  // lanes up to the first that ends
+            const unsigned take = __ballot_sync(0xFFFFFFFFu, there) & upto;
+            if ((take >> lane) & 1u) list[k + __popc(take & ((1u << lane) - 1u))] = i + lane;
+            k += __popc(take);
+            if (stop) break;
         }
-        if (d < 32) weight[sub][j - c] = f;
+        if (lane == 0) count = k;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (d == 0) tops[sub] = sum;
     __syncthreads();
-    sum = tops[sub];
-    float v = 0.0f;
-#pragma unroll 8
-    for (int j = c; j <= end; ++j)
-        if (j == c || (flags[j] & kHead)) v = fmaf(weight[sub][j - c], record(j)[row * D + d], v);
-    const Target to = p.parts[c].target;
-    write_out<D, ROWS>(p, to, row, d, v, sum);
-    if (d == 0) write_lse<ROWS>(p, to, row, top, sum);
+    const int k = count, first = blockIdx.y * kJoinOutputs;
+    auto record = [&](int i) { return p.cta_records + (static_cast<int64_t>(list[i]) * 2 + (i == 0 ? 1 : 0)) * kRecord; };
+    if (warp < RB) {  // the weights of one row
+        const int row = first / D + warp;
+        const float ninf = __uint_as_float(0xFF800000u);
+        float top = ninf;
+        for (int i = lane; i < k; i += 32) {
+            const float t = record(i)[kRecordStat + 2 * row];
+            weight[warp][i] = t;
+            top = fmaxf(top, t);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const float ref = top == ninf ? 0.0f : top;
+        float sum = 0.0f;
+        for (int i = lane; i < k; i += 32) {
+            const float f = exp2_fast(weight[warp][i] - ref);
+            weight[warp][i] = f;
+            sum = fmaf(f, record(i)[kRecordStat + 2 * row + 1], sum);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == 0) {
+            total[warp][0] = top;
+            total[warp][1] = sum;
+        }
+    }
+    __syncthreads();
+    const int at = first + lane * 4, sub = at / D - first / D;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = warp; i < k; i += kWarps) {
+        const float4 x = *reinterpret_cast<const float4 *>(record(i) + at);
+        const float f = weight[sub][i];
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+        v.z = fmaf(f, x.z, v.z);
+        v.w = fmaf(f, x.w, v.w);
+    }
+    share[warp][lane] = v;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int j = 1; j < kWarps; ++j) {
+        const float4 x = share[j][lane];
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+    }
+    const int row = at / D, d = at - row * D;
+    write_out<D, ROWS>(p, mine.target, row, d, v, total[sub][1]);
+    if (d == 0) write_lse<ROWS>(p, mine.target, row, total[sub][0], total[sub][1]);
 }
 
 template <int D, int NT, bool EXACT>
@@ -1152,7 +1277,7 @@ cudaError_t launch_stream(const KvCache &c, const AttnArgs &a, cudaStream_t stre
     using L = Layout<D, NT, EXACT>;
     static int limits[kMaxDevices];
     constexpr size_t smem = static_cast<size_t>(L::warps) * (L::code_bytes + L::rest_bytes) + sizeof(Shared) + 1024;
-    static_assert(smem <= 232448, "shared memory per CTA");
+    static_assert(sizeof(Shared) <= 14336 && smem <= 232448, "shared memory per CTA");
     auto *kernel = attn_stream_kernel<D, NT, EXACT>;
     cudaError_t e = ensure_smem(kernel, smem, false, limits);
     if (e != cudaSuccess) return e;
@@ -1174,13 +1299,14 @@ cudaError_t launch_stream(const KvCache &c, const AttnArgs &a, cudaStream_t stre
     p.num_pages = c.num_pages;
     p.page_shift = c.page_shift;
     p.kv_heads = c.kv_heads;
+    p.q_pairs = a.q_stride % 2 == 0 && reinterpret_cast<uintptr_t>(a.q) % (a.q_bf16 ? 4 : 8) == 0;
     p.warp_records = static_cast<float *>(a.workspace);
     p.cta_records = p.warp_records + static_cast<size_t>(ctas) * kWarps * kRecord;
     p.parts = reinterpret_cast<CtaParts *>(p.cta_records + static_cast<size_t>(ctas) * 2 * kRecord);
     p.ctx = ctx;
     e = launch_kernel(kernel, dim3(ctas), dim3(L::threads), smem, stream, 1, maps[0], maps[1], p);
     if (e != cudaSuccess) return e;
-    return launch_kernel(attn_join_kernel<D, L::rows>, dim3(ctas, L::rows * D / kThreads), dim3(kThreads), 0, stream,
+    return launch_kernel(attn_join_kernel<D, L::rows>, dim3(ctas, L::rows * D / kJoinOutputs), dim3(kThreads), 0, stream,
                          1, p);
 }
 
