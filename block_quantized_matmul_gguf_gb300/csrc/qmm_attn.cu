@@ -26,14 +26,14 @@
 // Work.  The keys of all (request, key head, row group) items, in tiles of
 // 64 keys, form one line that is cut into equal parts for all warps of a
 // grid that fills the GPU, whatever the lengths are.  Each warp streams its
-// tiles through its own shared-memory buffers (TMA boxes of code rows,
-// swizzled so that ldmatrix reads them without conflicts, and bulk copies of
-// the scales): while it works on a tile's values the next tile's keys
-// arrive, and the other way round.  An item that several warps share leaves
+// tiles through its own shared-memory buffers (16-byte asynchronous copies,
+// placed so that ldmatrix reads them without conflicts): while it works on a
+// tile's values the next tile's keys arrive, and the other way round.  TMA
+// boxes of the 32 to 128 byte rows kept the warps waiting to issue them, 4700
+// of 13000 cycles a tile.  An item that several warps share leaves
 // a maximum, a sum and an unnormalised output per warp; a CTA joins what its
 // warps hold, and a second kernel joins what several CTAs hold.
 #include "qmm_internal.h"
-#include "qmm_tc.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -106,7 +106,6 @@ struct Shared {
     int64_t prefix[kThreads];   // line places before each thread's requests
     Request request[kThreads];  // the requests, where every thread has at most one
     int64_t scratch[kWarps][2];
-    uint64_t bars[kWarps][2];   // K tile, V tile
     int flags[kWarps];
     Target target[kWarps][2];      // of head and tail
     float stat[kWarps][2][8][2];   // maximum and sum of each row
@@ -122,9 +121,8 @@ struct CtaParts {
 
 struct StreamParams {
     AttnArgs a;
-    const __half *k_scales, *v_scales;
-    int64_t num_pages;
-    int page_shift, kv_heads;
+    const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int num_pages, page_shift, kv_heads;
     bool q_pairs;         // rows of q are aligned to two values
     float *warp_records;  // [CTAs * kWarps]: head parts that are not the last
     float *cta_records;   // [CTAs][2]: head and tail part
@@ -335,10 +333,7 @@ struct WarpState {
     static constexpr int R = EXACT ? 1 : 2;  // query rows per lane and column tile
 
     uint8_t *codes, *rest;
-    uint64_t *bars;
-    uint32_t phase[2];
     int lane, g, t;
-    bool dead;
     // running statistics of this lane's rows: maximum and sum of the weights
     // 2^(s - top)
     float top[NT][R], sum[NT][R];
@@ -347,43 +342,63 @@ struct WarpState {
     int lo[NT][R], hi[NT][R];         // keys that the lane's rows see
 };
 
-// The pages of one tile that hold keys [lo, hi): a 4-bit set of its 16-key
-// groups that can be read, and each page's index by shuffle.
+// Page indices of the keys ahead: lane i holds page first + i of the request.
 struct Pages {
-    int32_t lane_page;  // lane i: page first + i of the request
+    int32_t lane_page;
     int first;
 };
 
-// Asks for the codes and scales of tile [key0, key0 + 64).
-template <int D>
-__device__ __forceinline__ void issue(const StreamParams &p, const CUtensorMap *map, const __half *scales,
-                                      uint8_t *codes_to, uint8_t *scales_to, uint64_t *bar, int kv_head, int key0,
-                                      int lo, int hi, const Pages &pages) {
-    constexpr int NB = D / 32;
-    const int lane = threadIdx.x & 31, shift = p.page_shift;
-    auto copy = [&](int32_t page, int k, int n) {
-        const int64_t row = ((static_cast<int64_t>(page) * p.kv_heads + kv_head) << shift) +
-                            ((key0 + k) & ((1 << shift) - 1));
-        tma_load_2d(smem_addr(codes_to + k * (D / 2)), map, 0, static_cast<int>(row), smem_addr(bar));
-        bulk_g2s(scales_to + k * NB * 2, scales + row * NB, n * NB * 2, bar);
-    };
-    if (shift >= 6) {
-        const int32_t page = __shfl_sync(0xFFFFFFFFu, pages.lane_page, (key0 >> shift) - pages.first);
-        if (lane == 0) {
-            const bool there = page >= 0 && page < p.num_pages;
-            mbar_arrive_expect_tx(bar, there ? kTile * (D / 2 + NB * 2) : 0);
-            if (there) copy(page, 0, kTile);
-        }
-        return;
-    }
-    // lane i takes the tile's i-th page
-    const int step = 1 << shift, k = lane << shift;
-    const int32_t page = __shfl_sync(0xFFFFFFFFu, pages.lane_page, ((key0 >> shift) - pages.first + lane) & 31);
-    const bool there = k < kTile && key0 + k < hi && key0 + k + step > lo && page >= 0 && page < p.num_pages;
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, there));
-    if (lane == 0) mbar_arrive_expect_tx(bar, n * step * (D / 2 + NB * 2));
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the latest group of this thread's copies are there, for the warp.
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncwarp();
-    if (there) copy(page, k, step);
+}
+
+// By how much the 16-byte chunks of a row of codes are rotated (exclusive or),
+// so that eight rows' chunks of one block lie in different banks.
+template <int D>
+__device__ __forceinline__ int chunk_swizzle(int row) {
+    return D == 256 ? (row & 7) : D == 128 ? ((row >> 1) & 3) : ((row >> 2) & 1);
+}
+
+// Starts the copies of the codes and scales of tile [key0, key0 + 64), those
+// of 16-key groups that hold keys of [lo, hi) and have a page, as one group.
+template <int D>
+__device__ __forceinline__ void fetch_tile(const StreamParams &p, const uint8_t *codes, const uint8_t *scales,
+                                           uint32_t codes_to, uint32_t scales_to, int kv_head, int key0, int lo, int hi,
+                                           const Pages &pages, int lane) {
+    constexpr int row_bytes = D / 2, group_bytes = 16 * row_bytes, scale_bytes = D / 16;  // of a row, 16 rows, a row
+    const int shift = p.page_shift, mask = (1 << shift) - 1;
+    // lane i < 4: the row of the cache where group i begins, or -1
+    const int key = key0 + 16 * (lane & 3);
+    const int32_t page = __shfl_sync(0xFFFFFFFFu, pages.lane_page, ((key >> shift) - pages.first) & 31);
+    int row = -1;
+    if (key < hi && key + 16 > lo && page >= 0 && page < p.num_pages)
+        row = (((page * p.kv_heads) + kv_head) << shift) + (key & mask);  // below 2^31
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int at = __shfl_sync(0xFFFFFFFFu, row, g);
+        if (at < 0) continue;
+        const uint8_t *src = codes + static_cast<int64_t>(at) * row_bytes + lane * 16;
+#pragma unroll
+        for (int j = 0; j < group_bytes / 512; ++j) {
+            const int r = (lane + 32 * j) / (row_bytes / 16), c = (lane + 32 * j) % (row_bytes / 16);
+            copy16(codes_to + (16 * g + r) * row_bytes + ((c ^ chunk_swizzle<D>(r)) << 4), src + j * 512);
+        }
+    }
+    // the scales: chunk i of the tile's 4 D bytes, in group i / (D / 16)
+#pragma unroll
+    for (int j = 0; j < (D + 127) / 128; ++j) {
+        const int i = lane + 32 * j, g = i / (D / 16);
+        const int at = __shfl_sync(0xFFFFFFFFu, row, g & 3);
+        if (at >= 0 && i < D / 4)
+            copy16(scales_to + i * 16, scales + static_cast<int64_t>(at) * scale_bytes + (i % (D / 16)) * 16);
+    }
+    copies_commit();
 }
 
 // The lane's D / 32 consecutive values of each of the item's rows of q: they
@@ -436,7 +451,7 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
     const AttnArgs &a = p.a;
     float (&v)[L::rows][E] = rows.v;
     const int (&pos)[L::rows] = rows.pos;
-    __half *frag = reinterpret_cast<__half *>(w.rest + L::q);
+    uint32_t *frag = reinterpret_cast<uint32_t *>(w.rest + L::q);
     float *bias = reinterpret_cast<float *>(w.rest + L::bias);
     const int d0 = w.lane * E, block = d0 / 32;
     // the sign of the scale goes to q; a scale of 0 takes q with it
@@ -454,24 +469,41 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
         // 2^up brings q below 2^15; the score's unit, size * 2^(24 - up), stays a normal number
         const int up = min(max(14 - exponent(big), max(-113, size_up - 96)), 100);
         const float f = pow2i(up);
-        const float unit = sign == 0.0f ? 1.0f : fmaxf(ldexpf(size, 24 - up), 1.17549435e-38f);
+        const float unit = sign == 0.0f ? 1.0f : fmaxf(size * pow2i((24 - up) / 2) * pow2i(24 - up - (24 - up) / 2), 1.17549435e-38f);
         const int nt = row / (L::rows / NT), in = row % (L::rows / NT);
         float s_hi = 0.0f, s_lo = 0.0f;
+        // value d of a block: lane (d & 15) / 4 of the column, register
+        // (d & 1) * 2 + d / 16, half (d / 2) & 1; a lane's values share d / 16
+        const int high = (d0 >> 4) & 1;
+        const float f16 = f * (high ? 0.0625f : 1.0f), back = high ? 16.0f : 1.0f;
+        float one[E], two[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const int d5 = (d0 + i) & 31, high = d5 >> 4, quad = (d5 & 15) >> 2, e = d5 & 3;
-            const float x = v[row][i] * f * (high ? 0.0625f : 1.0f);
-            const int reg = (e & 1) * 2 + high;
-            const __half h = EXACT ? __float2half_rz(x) : __float2half_rn(x);
-            const float hf = __half2float(h);
-            const int col = EXACT ? in * 2 : in;
-            const int at16 = ((((nt * NB + block) * 32 + col * 4 + quad) * 4) + reg) * 2 + (e >> 1);
-            frag[at16] = h;
-            s_hi += hf * (high ? 16.0f : 1.0f);
+            const float x = v[row][i] * f16;
+            one[i] = __half2float(EXACT ? __float2half_rz(x) : __float2half_rn(x));
+            two[i] = EXACT ? __half2float(__float2half_rn(x - one[i])) : 0.0f;
+            s_hi += one[i] * back;
+            s_lo += two[i] * back;
+        }
+        uint32_t *to = frag + ((nt * NB + block) * 32 + (EXACT ? in * 2 : in) * 4) * 4;
+        if constexpr (E >= 4) {
+#pragma unroll
+            for (int i = 0; i < E; i += 4) {
+                uint32_t *at = to + (((d0 + i) & 15) >> 2) * 4 + high;
+                at[0] = pack_rn(one[i], one[i + 2]);
+                at[2] = pack_rn(one[i + 1], one[i + 3]);
+                if constexpr (EXACT) {  // the next column: four lanes of four registers further
+                    at[16] = pack_rn(two[i], two[i + 2]);
+                    at[18] = pack_rn(two[i + 1], two[i + 3]);
+                }
+            }
+        } else {  // two values: 0 1 or 2 3 of a quad
+            __half *at = reinterpret_cast<__half *>(to + ((d0 & 15) >> 2) * 4 + high) + ((d0 >> 1) & 1);
+            at[0] = __float2half_rn(one[0]);
+            at[4] = __float2half_rn(one[1]);
             if constexpr (EXACT) {
-                const __half l = __float2half_rn(x - hf);
-                frag[at16 + 32] = l;  // the next column: four lanes of four registers further
-                s_lo += __half2float(l) * (high ? 16.0f : 1.0f);
+                at[32] = __float2half_rn(two[0]);
+                at[36] = __float2half_rn(two[1]);
             }
         }
 #pragma unroll
@@ -481,12 +513,12 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
         }
         if (w.lane % (32 / E) == 0) {
             const float m8 = -8.0f / 16777216.0f;
-            float *to = bias + (nt * NB + block) * 16;
+            float *b8 = bias + (nt * NB + block) * 16;
             if constexpr (EXACT) {
-                to[in * 4] = to[in * 4 + 2] = s_hi * m8;
-                to[in * 4 + 1] = to[in * 4 + 3] = s_lo * m8;
+                b8[in * 4] = b8[in * 4 + 2] = s_hi * m8;
+                b8[in * 4 + 1] = b8[in * 4 + 3] = s_lo * m8;
             } else {
-                to[(in >> 1) * 4 + (in & 1)] = to[(in >> 1) * 4 + 2 + (in & 1)] = s_hi * m8;
+                b8[(in >> 1) * 4 + (in & 1)] = b8[(in >> 1) * 4 + 2 + (in & 1)] = s_hi * m8;
             }
         }
         // the lane that holds this row's scores keeps their unit and range
@@ -534,7 +566,7 @@ __device__ __forceinline__ void tile_scores(WarpState<D, NT, EXACT> &w, float (&
     const uint4 *frag = reinterpret_cast<const uint4 *>(w.rest + L::q) + w.lane;
     const float4 *bias = reinterpret_cast<const float4 *>(w.rest + L::bias) + w.t;
     const uint16_t *ks = reinterpret_cast<const uint16_t *>(w.rest);
-    const int sw = D == 256 ? (w.lane & 7) : D == 128 ? ((w.lane >> 1) & 3) : ((w.lane >> 2) & 1);
+    const int sw = chunk_swizzle<D>(w.lane);
     const uint32_t base = smem_addr(w.codes) + w.lane * (D / 2);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -647,7 +679,7 @@ __device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const ui
     constexpr int NB = L::NB;
     const float *p = reinterpret_cast<const float *>(w.rest + L::p);
     const int token = w.lane & 15, upper = w.lane >> 4;
-    const int sw = D == 256 ? (token & 7) : D == 128 ? ((token >> 1) & 3) : ((token >> 2) & 1);
+    const int sw = chunk_swizzle<D>(token);
     const uint32_t base = smem_addr(w.codes) + L::codes + token * (D / 2);
     const uint32_t keep = EXACT && (w.g & 1) ? 0xFFFFE000u : 0u;  // odd columns hold the second part
 #pragma unroll
@@ -733,9 +765,8 @@ __device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const ui
 
 // Tiles [t0, t1) of an item.
 template <int D, int NT, bool EXACT>
-__device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMap *kmap, const CUtensorMap *vmap,
-                                         WarpState<D, NT, EXACT> &w, const Request &r, const Item &it, int t0,
-                                         int t1) {
+__device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT, EXACT> &w, const Request &r,
+                                         const Item &it, int t0, int t1) {
     using L = Layout<D, NT, EXACT>;
     constexpr int NB = L::NB, R = WarpState<D, NT, EXACT>::R;
     const AttnArgs &a = p.a;
@@ -758,8 +789,6 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
     const int lo_all = first_key(a, pos1), hi_all = a.causal ? min(r.len, pos0 + 1) : r.len;
     t0 = max(t0, lo / kTile - r.tile0);
     t1 = min(t1, tiles_to(hi) - r.tile0);
-    if (w.dead) return;
-
     // page indices of the tiles ahead
     const int32_t *table = a.table + it.b * a.table_width;
     const int tile_pages = max(1, kTile >> p.page_shift);
@@ -771,14 +800,21 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
             pages.lane_page = first + w.lane < a.table_width ? table[first + w.lane] : -1;
         }
     };
-    uint8_t *const vcodes = w.codes + L::codes, *const vscales = w.rest + L::v_scales;
+    const uint32_t codes_at = smem_addr(w.codes), scales_at = smem_addr(w.rest);
+    auto fetch_k = [&](int key0) {
+        fetch_tile<D>(p, p.k_codes, p.k_scales, codes_at, scales_at, it.kv_head, key0, lo, hi, pages, w.lane);
+    };
+    auto fetch_v = [&](int key0) {
+        fetch_tile<D>(p, p.v_codes, p.v_scales, codes_at + L::codes, scales_at + L::v_scales, it.kv_head, key0, lo, hi,
+                      pages, w.lane);
+    };
     QueryRows<D, NT, EXACT> rows;
     if (t0 < t1) {
         const int key0 = (r.tile0 + t0) * kTile;
         ahead(key0);
         load_q(p, rows, r, it, w.lane);  // under way while the pages are looked up
-        issue<D>(p, kmap, p.k_scales, w.codes, w.rest, w.bars, it.kv_head, key0, lo, hi, pages);
-        issue<D>(p, vmap, p.v_scales, vcodes, vscales, w.bars + 1, it.kv_head, key0, lo, hi, pages);
+        fetch_k(key0);
+        fetch_v(key0);
         stage_q(p, w, rows, r);
     }
     for (int tile = t0; tile < t1; ++tile) {
@@ -792,15 +828,15 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
         if (lost && w.lane == 0) record_error(p.ctx, kDevErrIndex);
         const bool edge = lost || key0 < lo_all || key0 + kTile > hi_all;
 
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(w.bars, w.phase[0], p.ctx))) w.dead = true;
-        w.phase[0] ^= 1;
+        copies_wait();  // K is there; V may be under way
         float s[NT][4][R][2];
         tile_scores<D, NT, EXACT>(w, s);
         __syncwarp();
-        const bool asked = tile + 1 < t1 && !w.dead;
-        if (asked) {
+        if (tile + 1 < t1) {
             ahead(key0 + kTile);
-            issue<D>(p, kmap, p.k_scales, w.codes, w.rest, w.bars, it.kv_head, key0 + kTile, lo, hi, pages);
+            fetch_k(key0 + kTile);
+        } else {
+            copies_commit();
         }
         unsigned seen = 3u;  // keys 2 lane and 2 lane + 1, by any row
         if (edge) {
@@ -837,8 +873,7 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
                 top[n][k] = v * w.unit[n][k];
                 faint |= u * w.unit[n][k] < top[n][k] - 23.5f;
             }
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(w.bars + 1, w.phase[1], p.ctx))) w.dead = true;
-        w.phase[1] ^= 1;
+        copies_wait();  // V is there; the next K may be under way
         const int e_max = tile_scales<D, NT, EXACT>(w, seen);
         // f: factor of what is there already; g: of this tile's products.  The
         // products carry 2^-24 of the codes and the scales' factor (fp32:
@@ -926,12 +961,7 @@ __device__ __forceinline__ void run_part(const StreamParams &p, const CUtensorMa
             __syncwarp();
             faint = __any_sync(0xFFFFFFFFu, more);
         }
-        if (w.dead) {  // a wait gave up: take no more tiles, let the copy that is under way end
-            if (asked) mbar_wait(w.bars, w.phase[0], p.ctx);
-            break;
-        }
-        if (tile + 1 < t1)
-            issue<D>(p, vmap, p.v_scales, vcodes, vscales, w.bars + 1, it.kv_head, key0 + kTile, lo, hi, pages);
+        if (tile + 1 < t1) fetch_v(key0 + kTile);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -1007,32 +1037,23 @@ __device__ __forceinline__ void write_lse(const StreamParams &p, const Target &t
 
 template <int D, int NT, bool EXACT>
 __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT, EXACT>::ctas))
-    attn_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const StreamParams p) {
+    attn_stream_kernel(const __grid_constant__ StreamParams p) {
     using L = Layout<D, NT, EXACT>;
     constexpr int R = WarpState<D, NT, EXACT>::R, ROWS = L::rows, W = L::warps;
     extern __shared__ uint8_t attn_smem[];
     uint8_t *base = attn_smem + ((1024u - (smem_addr(attn_smem) & 1023u)) & 1023u);
     Shared &sh = *reinterpret_cast<Shared *>(base + W * (L::code_bytes + L::rest_bytes));
     const int warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < W * 2; ++i) mbar_init(&sh.bars[0][0] + i, 1);
-        fence_mbar_init();
-    }
     pdl_wait();
     pdl_launch_dependents();
-    asm volatile("fence.proxy.async.global;" ::: "memory");  // the cache's last writer used plain stores
     const Line line = build_line<ROWS, W>(p, sh);
 
     WarpState<D, NT, EXACT> w;
     w.codes = base + warp * L::code_bytes;
     w.rest = base + W * L::code_bytes + warp * L::rest_bytes;
-    w.bars = sh.bars[warp];
-    w.phase[0] = w.phase[1] = 0;
     w.lane = threadIdx.x & 31;
     w.g = w.lane >> 2;
     w.t = w.lane & 3;
-    w.dead = false;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * W;
     const int64_t me = static_cast<int64_t>(blockIdx.x) * W + warp;
     // equal shares of the line, or one place each
@@ -1055,7 +1076,7 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
         if (t0 >= r.tiles) break;  // a place without a tile (spread: the warp's only one)
         const int t1 = static_cast<int>(min(static_cast<int64_t>(r.tiles), t0 + (x1 - x)));
         flags &= ~kEmpty;
-        run_part<D, NT, EXACT>(p, &kmap, &vmap, w, r, it, t0, t1);
+        run_part<D, NT, EXACT>(p, w, r, it, t0, t1);
         x += t1 - t0;
         const Target to = target_of(r, it);
         if (t0 == 0 && t1 == r.tiles) {
@@ -1281,22 +1302,14 @@ cudaError_t launch_stream(const KvCache &c, const AttnArgs &a, cudaStream_t stre
     auto *kernel = attn_stream_kernel<D, NT, EXACT>;
     cudaError_t e = ensure_smem(kernel, smem, false, limits);
     if (e != cudaSuccess) return e;
-    const uint64_t rows = static_cast<uint64_t>(c.num_pages) * c.kv_heads << c.page_shift;
-    const uint32_t box = static_cast<uint32_t>(std::min(1 << c.page_shift, kTile));
-    const CUtensorMapSwizzle sw = D == 256   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                  : D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                             : CU_TENSOR_MAP_SWIZZLE_32B;
-    CUtensorMap maps[2];
-    const void *codes[2] = {c.k_codes, c.v_codes};
-    for (int i = 0; i < 2; ++i)
-        if (!encode_tmap_2d(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, codes[i], D / 2, rows, D / 2, D / 2, box, sw))
-            return cudaErrorInvalidValue;
     const int ctas = std::min(device_sm_count() * L::ctas, kMaxCtas);
     StreamParams p = {};
     p.a = a;
-    p.k_scales = static_cast<const __half *>(c.k_scales);
-    p.v_scales = static_cast<const __half *>(c.v_scales);
-    p.num_pages = c.num_pages;
+    p.k_codes = static_cast<const uint8_t *>(c.k_codes);
+    p.k_scales = static_cast<const uint8_t *>(c.k_scales);
+    p.v_codes = static_cast<const uint8_t *>(c.v_codes);
+    p.v_scales = static_cast<const uint8_t *>(c.v_scales);
+    p.num_pages = static_cast<int>(c.num_pages);
     p.page_shift = c.page_shift;
     p.kv_heads = c.kv_heads;
     p.q_pairs = a.q_stride % 2 == 0 && reinterpret_cast<uintptr_t>(a.q) % (a.q_bf16 ? 4 : 8) == 0;
@@ -1304,7 +1317,7 @@ cudaError_t launch_stream(const KvCache &c, const AttnArgs &a, cudaStream_t stre
     p.cta_records = p.warp_records + static_cast<size_t>(ctas) * kWarps * kRecord;
     p.parts = reinterpret_cast<CtaParts *>(p.cta_records + static_cast<size_t>(ctas) * 2 * kRecord);
     p.ctx = ctx;
-    e = launch_kernel(kernel, dim3(ctas), dim3(L::threads), smem, stream, 1, maps[0], maps[1], p);
+    e = launch_kernel(kernel, dim3(ctas), dim3(L::threads), smem, stream, 1, p);
     if (e != cudaSuccess) return e;
     return launch_kernel(attn_join_kernel<D, L::rows>, dim3(ctas, L::rows * D / kJoinOutputs), dim3(kThreads), 0, stream,
                          1, p);
