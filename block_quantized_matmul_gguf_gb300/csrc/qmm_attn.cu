@@ -101,12 +101,23 @@ struct Request {
     int bad;
 };
 
+// A warp's place in the line and the part that it works on.
+struct Part {
+    int64_t x, end;
+    int t0, t1, tiles;  // tiles of the item
+    Target to;
+    int b;                       // request
+    int lo, hi, lo_all, hi_all;  // keys that any, and that every, row sees
+    int row_lo[8], row_hi[8];    // keys that each row sees
+};
+
 // What the CTA's threads share, after the warps' buffers.
 struct Shared {
     int64_t prefix[kThreads];   // line places before each thread's requests
     Request request[kThreads];  // the requests, where every thread has at most one
     int64_t scratch[kWarps][2];
     int flags[kWarps];
+    Part part[kWarps];             // what a warp is at, kept out of its registers
     Target target[kWarps][2];      // of head and tail
     float stat[kWarps][2][8][2];   // maximum and sum of each row
     float weight[8][kWarps];       // of a chain's parts, by row
@@ -339,7 +350,6 @@ struct WarpState {
     float top[NT][R], sum[NT][R];
     float2 out[NT][NB][2][2];         // [block][even, odd value][value i, 16 + i (x 16)]: two columns
     float unit[NT][R];                // score = sum * unit > 0
-    int lo[NT][R], hi[NT][R];         // keys that the lane's rows see
 };
 
 // Page indices of the keys ahead: lane i holds page first + i of the request.
@@ -445,7 +455,7 @@ __device__ __forceinline__ void load_q(const StreamParams &p, QueryRows<D, NT, E
 // sums (the codes are used as 0..15).
 template <int D, int NT, bool EXACT>
 __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, EXACT> &w,
-                                        QueryRows<D, NT, EXACT> &rows, const Request &r) {
+                                        QueryRows<D, NT, EXACT> &rows, Part &part, const Request &r) {
     using L = Layout<D, NT, EXACT>;
     constexpr int NB = L::NB, E = D / 32;
     const AttnArgs &a = p.a;
@@ -521,18 +531,16 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
                 b8[(in >> 1) * 4 + (in & 1)] = b8[(in >> 1) * 4 + 2 + (in & 1)] = s_hi * m8;
             }
         }
-        // the lane that holds this row's scores keeps their unit and range
-        const int hi = a.causal ? min(r.len, pos[row] + 1) : r.len;
-        const int lo = first_key(a, pos[row]);
+        if (w.lane == 0) {
+            part.row_lo[row] = first_key(a, pos[row]);
+            part.row_hi[row] = a.causal ? min(r.len, pos[row] + 1) : r.len;
+        }
+        // the lanes that hold this row's scores keep their unit
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < w.R; ++k)
-                if (n == nt && (EXACT ? w.t : w.t * 2 + k) == in) {
-                    w.unit[n][k] = unit;
-                    w.lo[n][k] = lo;
-                    w.hi[n][k] = hi;
-                }
+                if (n == nt && (EXACT ? w.t : w.t * 2 + k) == in) w.unit[n][k] = unit;
     }
     __syncwarp();
 }
@@ -765,8 +773,8 @@ __device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const ui
 
 // Tiles [t0, t1) of an item.
 template <int D, int NT, bool EXACT>
-__device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT, EXACT> &w, const Request &r,
-                                         const Item &it, int t0, int t1) {
+__device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT, EXACT> &w, Part &part,
+                                         const Request &r, const Item &it, int t0, int t1) {
     using L = Layout<D, NT, EXACT>;
     constexpr int NB = L::NB, R = WarpState<D, NT, EXACT>::R;
     const AttnArgs &a = p.a;
@@ -781,58 +789,66 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
 #pragma unroll
         for (int i = 0; i < NB * 4; ++i) w.out[n][i >> 2][(i >> 1) & 1][i & 1] = make_float2(0.0f, 0.0f);
     }
-    // the keys that any, and that every, row of the group sees
-    const int heads = a.heads / p.kv_heads, all = r.rows * heads;
-    const int pos0 = r.first + it.group * L::rows / heads;
-    const int pos1 = r.first + (min((it.group + 1) * L::rows, all) - 1) / heads;
-    const int lo = first_key(a, pos0), hi = a.causal ? min(r.len, pos1 + 1) : r.len;
-    const int lo_all = first_key(a, pos1), hi_all = a.causal ? min(r.len, pos0 + 1) : r.len;
-    t0 = max(t0, lo / kTile - r.tile0);
-    t1 = min(t1, tiles_to(hi) - r.tile0);
-    // page indices of the tiles ahead
-    const int32_t *table = a.table + it.b * a.table_width;
-    const int tile_pages = max(1, kTile >> p.page_shift);
+    // page indices of the keys ahead
     Pages pages = {-1, -64};
     auto ahead = [&](int key0) {  // makes the pages of the tile at key0 known
         const int first = key0 >> p.page_shift;
-        if (first + tile_pages > pages.first + 32) {
+        if (first + max(1, kTile >> p.page_shift) > pages.first + 32) {
             pages.first = first;
-            pages.lane_page = first + w.lane < a.table_width ? table[first + w.lane] : -1;
+            pages.lane_page =
+                first + w.lane < a.table_width ? a.table[part.b * a.table_width + first + w.lane] : -1;
         }
     };
     const uint32_t codes_at = smem_addr(w.codes), scales_at = smem_addr(w.rest);
     auto fetch_k = [&](int key0) {
-        fetch_tile<D>(p, p.k_codes, p.k_scales, codes_at, scales_at, it.kv_head, key0, lo, hi, pages, w.lane);
+        fetch_tile<D>(p, p.k_codes, p.k_scales, codes_at, scales_at, part.to.kv_head, key0, part.lo, part.hi, pages,
+                      w.lane);
     };
     auto fetch_v = [&](int key0) {
-        fetch_tile<D>(p, p.v_codes, p.v_scales, codes_at + L::codes, scales_at + L::v_scales, it.kv_head, key0, lo, hi,
-                      pages, w.lane);
+        fetch_tile<D>(p, p.v_codes, p.v_scales, codes_at + L::codes, scales_at + L::v_scales, part.to.kv_head, key0,
+                      part.lo, part.hi, pages, w.lane);
     };
-    QueryRows<D, NT, EXACT> rows;
-    if (t0 < t1) {
-        const int key0 = (r.tile0 + t0) * kTile;
-        ahead(key0);
-        load_q(p, rows, r, it, w.lane);  // under way while the pages are looked up
-        fetch_k(key0);
-        fetch_v(key0);
-        stage_q(p, w, rows, r);
+    int key0, end;
+    {
+        // the keys that any, and that every, row of the group sees
+        const int heads = a.heads / p.kv_heads, all = r.rows * heads;
+        const int pos0 = r.first + it.group * L::rows / heads;
+        const int pos1 = r.first + (min((it.group + 1) * L::rows, all) - 1) / heads;
+        const int lo = first_key(a, pos0), hi = a.causal ? min(r.len, pos1 + 1) : r.len;
+        key0 = max((r.tile0 + t0) * kTile, lo / kTile * kTile);
+        end = min((r.tile0 + t1) * kTile, hi);
+        if (w.lane == 0) {
+            part.b = it.b;
+            part.lo = lo;
+            part.hi = hi;
+            part.lo_all = first_key(a, pos1);
+            part.hi_all = a.causal ? min(r.len, pos0 + 1) : r.len;
+        }
+        __syncwarp();
+        if (key0 < end) {
+            QueryRows<D, NT, EXACT> rows;
+            ahead(key0);
+            load_q(p, rows, r, it, w.lane);  // under way while the pages are looked up
+            fetch_k(key0);
+            fetch_v(key0);
+            stage_q(p, w, rows, part, r);
+        }
     }
-    for (int tile = t0; tile < t1; ++tile) {
-        const int key0 = (r.tile0 + tile) * kTile;
+    for (; key0 < end; key0 += kTile) {
         // 16-key groups whose page can be read: lane i looks at group i
         const int32_t page = __shfl_sync(0xFFFFFFFFu, pages.lane_page,
                                          (((key0 + 16 * w.lane) >> p.page_shift) - pages.first) & 31);
         const int key = key0 + 16 * w.lane;
-        const unsigned lost = __ballot_sync(0xFFFFFFFFu, w.lane < 4 && key < hi && key + 16 > lo &&
+        const unsigned lost = __ballot_sync(0xFFFFFFFFu, w.lane < 4 && key < part.hi && key + 16 > part.lo &&
                                                              (page < 0 || page >= p.num_pages));
         if (lost && w.lane == 0) record_error(p.ctx, kDevErrIndex);
-        const bool edge = lost || key0 < lo_all || key0 + kTile > hi_all;
+        const bool edge = lost || key0 < part.lo_all || key0 + kTile > part.hi_all;
 
         copies_wait();  // K is there; V may be under way
         float s[NT][4][R][2];
         tile_scores<D, NT, EXACT>(w, s);
         __syncwarp();
-        if (tile + 1 < t1) {
+        if (key0 + kTile < end) {
             ahead(key0 + kTile);
             fetch_k(key0 + kTile);
         } else {
@@ -845,13 +861,16 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
 #pragma unroll
-                    for (int k = 0; k < R; ++k)
+                    for (int k = 0; k < R; ++k) {
+                        const int row = EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k;
+                        const int row_lo = part.row_lo[row], row_hi = part.row_hi[row];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int j = key0 + 16 * m + 8 * h + w.g;
-                            if (j < w.lo[n][k] || j >= w.hi[n][k] || ((lost >> m) & 1u)) s[n][m][k][h] = ninf;
+                            if (j < row_lo || j >= row_hi || ((lost >> m) & 1u)) s[n][m][k][h] = ninf;
                         }
-            const int j = key0 + 2 * w.lane;
+                    }
+            const int j = key0 + 2 * w.lane, lo = part.lo, hi = part.hi;
             seen = (lost >> (w.lane >> 3)) & 1u ? 0u : (j >= lo && j < hi ? 1u : 0u) | (j + 1 >= lo && j + 1 < hi ? 2u : 0u);
         }
         // the rows' largest and smallest scores of the tile
@@ -927,41 +946,46 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
                     }
             __syncwarp();
         };
-        if (faint)
+        // Weights far below the tile's largest would fall out of binary16's
+        // range, which shows where the large ones meet zeros: they go in
+        // passes of their own, raised by 2^24 each time.
+        if (faint) {
+            for (float raise = 1.0f / kFaint; faint; raise *= 1.0f / kFaint) {
+                bool more = false;
+                float low[NT][R];  // factor of the pass's products
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < R; ++k) {
+                        low[n][k] = g[n][k] / raise;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float e = s[n][i >> 1][k][i & 1] * raise;
+                            more |= e < kFaint && e > 0.0f;
+                        }
+                    }
+                hand_over([raise](float v) {
+                    const float e = v * raise;
+                    return e >= kFaint && e < 1.0f ? e : 0.0f;
+                });
+                tile_values<D, NT, EXACT, true>(w, pw, f, low);
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < R; ++k) f[n][k] = 1.0f;
+                faint = __any_sync(0xFFFFFFFFu, more);
+            }
             hand_over([](float e) { return e < kFaint ? 0.0f : e; });
-        else
+        } else {
             hand_over([](float e) { return e; });
+        }
         if (edge)
             tile_values<D, NT, EXACT, true>(w, pw, f, g);
         else
             tile_values<D, NT, EXACT, false>(w, pw, f, g);
         __syncwarp();
-        // Weights far below the tile's largest would fall out of binary16's
-        // range, which shows where the large ones meet zeros: they go in
-        // passes of their own, raised by 2^24 each time.
-        for (float raise = 1.0f / kFaint; faint; raise *= 1.0f / kFaint) {
-            bool more = false;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int k = 0; k < R; ++k) {
-                    f[n][k] = 1.0f;
-                    g[n][k] *= kFaint;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float e = s[n][i >> 1][k][i & 1] * raise;
-                        more |= e < kFaint && e > 0.0f;
-                    }
-                }
-            hand_over([raise](float v) {
-                const float e = v * raise;
-                return e >= kFaint && e < 1.0f ? e : 0.0f;
-            });
-            tile_values<D, NT, EXACT, true>(w, pw, f, g);
-            __syncwarp();
-            faint = __any_sync(0xFFFFFFFFu, more);
-        }
-        if (tile + 1 < t1) fetch_v(key0 + kTile);
+        if (key0 + kTile < end) fetch_v(key0 + kTile);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -994,10 +1018,6 @@ __device__ __forceinline__ void each_output(const WarpState<D, NT, EXACT> &w, Be
                         put(32 * b + 16 * h + 2 * w.g + m, v * (h ? 0.0625f : 1.0f));
                     }
         }
-}
-
-__device__ __forceinline__ Target target_of(const Request &r, const Item &it) {
-    return Target{r.row0, r.rows, it.kv_head, it.group};
 }
 
 // The row of q, and the head, that row `row` of an item stands for; false for
@@ -1060,26 +1080,42 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
     const int64_t share = line.total / warps, left = line.total - share * warps;
     const int64_t x0 = line.spread ? min(me, line.total) : share * me + min(me, left);
     const int64_t x1 = line.spread ? min(me + 1, line.total) : x0 + share + (me < left ? 1 : 0);
-    int flags = kEmpty;
-    for (int64_t x = x0; x < x1;) {
-        int64_t before;
-        Request r;
-        Item it;
-        it.b = find_request<ROWS, W>(p, sh, line, x, before, r);
-        const int places = item_places<W>(r, line.spread);
-        // most offsets fit 32 bits, whose division is far cheaper
-        const int64_t off = x - before;
-        const int item = off <= INT32_MAX ? static_cast<int>(off) / places : static_cast<int>(off / places);
-        it.kv_head = item / r.groups;
-        it.group = item - it.kv_head * r.groups;
-        const int t0 = static_cast<int>(off - static_cast<int64_t>(item) * places);
-        if (t0 >= r.tiles) break;  // a place without a tile (spread: the warp's only one)
-        const int t1 = static_cast<int>(min(static_cast<int64_t>(r.tiles), t0 + (x1 - x)));
-        flags &= ~kEmpty;
-        run_part<D, NT, EXACT>(p, w, r, it, t0, t1);
-        x += t1 - t0;
-        const Target to = target_of(r, it);
-        if (t0 == 0 && t1 == r.tiles) {
+    Part &part = sh.part[warp];
+    if (w.lane == 0) {
+        sh.flags[warp] = kEmpty;
+        part.x = x0;
+        part.end = x1;
+    }
+    __syncwarp();
+    while (part.x < part.end) {
+        {
+            const int64_t x = part.x;
+            int64_t before;
+            Request r;
+            Item it;
+            it.b = find_request<ROWS, W>(p, sh, line, x, before, r);
+            const int places = item_places<W>(r, line.spread);
+            // most offsets fit 32 bits, whose division is far cheaper
+            const int64_t off = x - before;
+            const int item = off <= INT32_MAX ? static_cast<int>(off) / places : static_cast<int>(off / places);
+            it.kv_head = item / r.groups;
+            it.group = item - it.kv_head * r.groups;
+            const int t0 = static_cast<int>(off - static_cast<int64_t>(item) * places);
+            if (t0 >= r.tiles) break;  // a place without a tile (spread: the warp's only one)
+            const int t1 = static_cast<int>(min(static_cast<int64_t>(r.tiles), t0 + (part.end - x)));
+            __syncwarp();
+            if (w.lane == 0) {
+                part.x = x + t1 - t0;
+                part.t0 = t0;
+                part.t1 = t1;
+                part.tiles = r.tiles;
+                part.to = Target{r.row0, r.rows, it.kv_head, it.group};
+            }
+            run_part<D, NT, EXACT>(p, w, part, r, it, t0, t1);
+            __syncwarp();
+        }
+        const Target to = part.to;
+        if (part.t0 == 0 && part.t1 == part.tiles) {
             each_output<D, NT, EXACT>(w, [&](int n, int k, int row) {
                 int64_t at = 0;
                 int head = 0;
@@ -1096,12 +1132,15 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
 #pragma unroll
                     for (int k = 0; k < R; ++k)
                         write_lse<ROWS>(p, to, EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k, w.top[n][k], w.sum[n][k]);
+            if (w.lane == 0) sh.flags[warp] &= ~kEmpty;
+            __syncwarp();
             continue;
         }
         // the warp's last part stays in its code buffers, which no later tile
         // needs; an earlier one goes to global memory
-        const bool head = t0 > 0;
-        float *rec = x >= x1 ? reinterpret_cast<float *>(w.codes) : p.warp_records + me * kRecord;
+        const bool head = part.t0 > 0, last = part.x >= part.end;
+        float *rec = last ? reinterpret_cast<float *>(w.codes)
+                          : p.warp_records + (static_cast<int64_t>(blockIdx.x) * W + warp) * kRecord;
         each_output<D, NT, EXACT>(w, [rec](int, int, int row) { return [=](int d, float v) { rec[row * D + d] = v; }; });
         if (w.g == 0)
 #pragma unroll
@@ -1112,13 +1151,13 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
                     s[0] = w.top[n][k];
                     s[1] = w.sum[n][k];
                 }
-        if (w.lane == 0) sh.target[warp][head ? 0 : 1] = to;
-        if (head)
-            flags |= kHead | (t1 < r.tiles ? kHeadOpen : 0) | (x >= x1 ? kHeadLast : 0);
-        else
-            flags |= kTail;
+        if (w.lane == 0) {
+            sh.target[warp][head ? 0 : 1] = to;
+            sh.flags[warp] = (sh.flags[warp] & ~kEmpty) |
+                             (head ? kHead | (part.t1 < part.tiles ? kHeadOpen : 0) | (last ? kHeadLast : 0) : kTail);
+        }
+        __syncwarp();
     }
-    if (w.lane == 0) sh.flags[warp] = flags;
     __syncthreads();
 
     // Join the warps' parts.  A chain begins with a tail, or with the head of
