@@ -47,6 +47,7 @@ constexpr int kWarps = 8;  // of a CTA, at most
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;  // keys
 constexpr float kFaint = 1.0f / 16777216.0f;  // 2^-24
+constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // binary16 pairs, times 2^-24
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // One head dimension's shared memory, per warp.
@@ -383,6 +384,25 @@ __device__ __forceinline__ void fetch_tile(const StreamParams &p, const uint8_t 
                                            const Pages &pages, int lane) {
     constexpr int row_bytes = D / 2, group_bytes = 16 * row_bytes, scale_bytes = D / 16;  // of a row, 16 rows, a row
     const int shift = p.page_shift, mask = (1 << shift) - 1;
+    if (shift >= 6) {  // the tile lies in one page
+        const int32_t page = __shfl_sync(0xFFFFFFFFu, pages.lane_page, (key0 >> shift) - pages.first);
+        if (page >= 0 && page < p.num_pages) {
+            const int64_t row = ((page * p.kv_heads + kv_head) << shift) + (key0 & mask);
+            const uint8_t *src = codes + row * row_bytes + lane * 16;
+            const int r0 = lane / (row_bytes / 16), c = lane % (row_bytes / 16);
+#pragma unroll
+            for (int j = 0; j < 4 * group_bytes / 512; ++j) {
+                const int r = r0 + j * (512 / row_bytes);
+                copy16(codes_to + r * row_bytes + ((c ^ chunk_swizzle<D>(r)) << 4), src + j * 512);
+            }
+            const uint8_t *from = scales + row * scale_bytes + lane * 16;
+#pragma unroll
+            for (int j = 0; j < (D + 127) / 128; ++j)
+                if (D >= 128 || lane < D / 4) copy16(scales_to + (lane + 32 * j) * 16, from + j * 512);
+        }
+        copies_commit();
+        return;
+    }
     // lane i < 4: the row of the cache where group i begins, or -1
     const int key = key0 + 16 * (lane & 3);
     const int32_t page = __shfl_sync(0xFFFFFFFFu, pages.lane_page, ((key >> shift) - pages.first) & 31);
@@ -412,7 +432,7 @@ __device__ __forceinline__ void fetch_tile(const StreamParams &p, const uint8_t 
 }
 
 // The lane's D / 32 consecutive values of each of the item's rows of q: they
-// lie in one block.  Rows past the end repeat the last.
+// lie in one block.
 template <int D, int NT, bool EXACT>
 struct QueryRows {
     float v[Layout<D, NT, EXACT>::rows][D / 32];
@@ -427,7 +447,7 @@ __device__ __forceinline__ void load_q(const StreamParams &p, QueryRows<D, NT, E
     const int heads = a.heads / p.kv_heads, all = r.rows * heads;
 #pragma unroll
     for (int row = 0; row < ROWS; ++row) {
-        const int flat = min(it.group * ROWS + row, all - 1), token = flat / heads;
+        const int flat = min(it.group * ROWS + row, all - 1), token = flat / heads;  // past the end: the last again
         const int64_t at = (static_cast<int64_t>(r.row0) + token) * a.q_stride +
                            static_cast<int64_t>(it.kv_head * heads + flat - token * heads) * D + lane * E;
         q.pos[row] = r.first + token;
@@ -451,11 +471,31 @@ __device__ __forceinline__ void load_q(const StreamParams &p, QueryRows<D, NT, E
     }
 }
 
+template <int D, int NT, bool EXACT>
+__device__ __forceinline__ void stage_zero(WarpState<D, NT, EXACT> &w, Part &part, int row) {
+    using L = Layout<D, NT, EXACT>;
+    constexpr int NB = L::NB;
+    const int nt = row / (L::rows / NT), in = row % (L::rows / NT), cols = EXACT ? 2 : 1;
+    uint4 *frag = reinterpret_cast<uint4 *>(w.rest + L::q) + nt * NB * 32 + in * cols * 4;
+    float *bias = reinterpret_cast<float *>(w.rest + L::bias) + nt * NB * 16;
+    for (int i = w.lane; i < NB * cols * 4; i += 32)
+        frag[i / (cols * 4) * 32 + i % (cols * 4)] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = w.lane; i < NB * cols; i += 32) {
+        const int col = in * cols + i % cols;
+        float *b8 = bias + i / cols * 16 + (col >> 1) * 4 + (col & 1);
+        b8[0] = b8[2] = 0.0f;
+    }
+    if (w.lane == 0) {
+        part.row_lo[row] = part.row_lo[0];
+        part.row_hi[row] = part.row_hi[0];
+    }
+}
+
 // Those rows as B fragments, scaled to below 2^15, with -8 times the block
 // sums (the codes are used as 0..15).
 template <int D, int NT, bool EXACT>
 __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, EXACT> &w,
-                                        QueryRows<D, NT, EXACT> &rows, Part &part, const Request &r) {
+                                        QueryRows<D, NT, EXACT> &rows, Part &part, const Request &r, int rows_here) {
     using L = Layout<D, NT, EXACT>;
     constexpr int NB = L::NB, E = D / 32;
     const AttnArgs &a = p.a;
@@ -469,6 +509,10 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
     const int size_up = exponent(size);
 #pragma unroll
     for (int row = 0; row < L::rows; ++row) {
+        if (row >= rows_here) {  // columns without a row: zeros, which see what row 0 sees
+            stage_zero<D, NT, EXACT>(w, part, row);
+            continue;
+        }
         uint32_t bits = 0;  // of the largest value: positive numbers order as their bits do
 #pragma unroll
         for (int i = 0; i < E; ++i) {
@@ -675,6 +719,11 @@ __device__ __forceinline__ int tile_scales(WarpState<D, NT, EXACT> &w, unsigned 
     return e;
 }
 
+// -(x & keep)
+__device__ __forceinline__ float minus_part(float x, uint32_t keep) {
+    return __uint_as_float((__float_as_uint(x) & keep) ^ 0x80000000u);
+}
+
 // out = out * f + g * sum over the tile's keys of (p d) (n - 8), with the
 // weights in shared memory (EXACT) or in pw, as binary16 B operands.
 // EDGE: some row does not see some key of the tile, whose scale may then be
@@ -706,28 +755,33 @@ __device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const ui
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t x = c[2 * h], y = c[2 * h + 1], x8 = x >> 8, y8 = y >> 8;
-                // n - 8 (lower codes) and 16 (n - 8) (upper codes), times 2^-24
-                const uint32_t xa = hadd2(x & 0x000F000Fu, 0x80088008u), ya = hadd2(y & 0x000F000Fu, 0x80088008u);
-                const uint32_t xb = hadd2(x & 0x00F000F0u, 0x80808080u), yb = hadd2(y & 0x00F000F0u, 0x80808080u);
-                const uint32_t xc = hadd2(x8 & 0x000F000Fu, 0x80088008u), yc = hadd2(y8 & 0x000F000Fu, 0x80088008u);
-                const uint32_t xd = hadd2(x8 & 0x00F000F0u, 0x80808080u), yd = hadd2(y8 & 0x00F000F0u, 0x80808080u);
+                // n - 8 (lower codes) and 16 (n - 8) (upper codes), times 2^-24;
+                // -8 times the sum of the weights as a product of its own would
+                // take fewer instructions, but a heavy key's code 8 must leave
+                // exactly nothing
+                const uint32_t xa = hadd2(x & 0x000F000Fu, kMinus8), ya = hadd2(y & 0x000F000Fu, kMinus8);
+                const uint32_t xb = hadd2(x & 0x00F000F0u, kMinus128), yb = hadd2(y & 0x00F000F0u, kMinus128);
+                const uint32_t xc = hadd2(x8 & 0x000F000Fu, kMinus8), yc = hadd2(y8 & 0x000F000Fu, kMinus8);
+                const uint32_t xd = hadd2(x8 & 0x00F000F0u, kMinus128), yd = hadd2(y8 & 0x00F000F0u, kMinus128);
                 uint32_t b0[NT], b1[NT];
                 if constexpr (EXACT) {
                     const float4 d = *reinterpret_cast<const float4 *>(
                         reinterpret_cast<const float *>(w.rest + L::d) + (2 * bp + h) * kTile + ks * 16 + 4 * w.t);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float v[4] = {pe[n].x * d.x, pe[n].y * d.y, pe[n].z * d.z, pe[n].w * d.w};
+                        float2 u = __fmul2_rn(make_float2(pe[n].x, pe[n].y), make_float2(d.x, d.y));
+                        float2 v = __fmul2_rn(make_float2(pe[n].z, pe[n].w), make_float2(d.z, d.w));
                         if constexpr (EDGE) {
-                            v[0] = pe[n].x == 0.0f ? 0.0f : v[0];
-                            v[1] = pe[n].y == 0.0f ? 0.0f : v[1];
-                            v[2] = pe[n].z == 0.0f ? 0.0f : v[2];
-                            v[3] = pe[n].w == 0.0f ? 0.0f : v[3];
+                            u.x = pe[n].x == 0.0f ? 0.0f : u.x;
+                            u.y = pe[n].y == 0.0f ? 0.0f : u.y;
+                            v.x = pe[n].z == 0.0f ? 0.0f : v.x;
+                            v.y = pe[n].w == 0.0f ? 0.0f : v.y;
                         }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] -= __uint_as_float(__float_as_uint(v[k]) & keep);
-                        b0[n] = pack_rz(v[0], v[1]);
-                        b1[n] = pack_rz(v[2], v[3]);
+                        // odd columns: minus the first part
+                        u = __fadd2_rn(u, make_float2(minus_part(u.x, keep), minus_part(u.y, keep)));
+                        v = __fadd2_rn(v, make_float2(minus_part(v.x, keep), minus_part(v.y, keep)));
+                        b0[n] = pack_rz(u.x, u.y);
+                        b1[n] = pack_rz(v.x, v.y);
                     }
                 } else {
                     const uint2 d = *reinterpret_cast<const uint2 *>(
@@ -763,10 +817,10 @@ __device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const ui
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        w.out[n][2 * bp + h][m][i] =
-                            __ffma2_rn(w.out[n][2 * bp + h][m][i], f2,
-                                       __fmul2_rn(make_float2(acc[n][h][m][2 * i], acc[n][h][m][2 * i + 1]), g2));
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 v = make_float2(acc[n][h][m][2 * i], acc[n][h][m][2 * i + 1]);
+                        w.out[n][2 * bp + h][m][i] = __ffma2_rn(w.out[n][2 * bp + h][m][i], f2, __fmul2_rn(v, g2));
+                    }
         }
     }
 }
@@ -779,6 +833,8 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
     constexpr int NB = L::NB, R = WarpState<D, NT, EXACT>::R;
     const AttnArgs &a = p.a;
     const float ninf = __uint_as_float(0xFF800000u);
+    // the weights' largest value, and the least that goes with it in one pass
+    constexpr float kFull = EXACT ? 1.0f : 16384.0f, kLow = kFull * kFaint, kRaise = 14.0f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -817,6 +873,10 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
         const int lo = first_key(a, pos0), hi = a.causal ? min(r.len, pos1 + 1) : r.len;
         key0 = max((r.tile0 + t0) * kTile, lo / kTile * kTile);
         end = min((r.tile0 + t1) * kTile, hi);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < R; ++k) w.unit[n][k] = 1.0f;
         if (w.lane == 0) {
             part.b = it.b;
             part.lo = lo;
@@ -831,7 +891,7 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
             load_q(p, rows, r, it, w.lane);  // under way while the pages are looked up
             fetch_k(key0);
             fetch_v(key0);
-            stage_q(p, w, rows, part, r);
+            stage_q(p, w, rows, part, r, all - it.group * L::rows);
         }
     }
     for (; key0 < end; key0 += kTile) {
@@ -910,14 +970,16 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
                 const float fresh = top[n][k] == ninf ? 0.0f : exp2_fast(top[n][k] - now);
                 g[n][k] = fresh * unit_out;
                 w.top[n][k] = now;
+                // bf16 output: raised by 2^14 as the B operand takes them
+                const float base = EXACT ? -here : kRaise - here;
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float e = exp2_fast(fmaf(s[n][i >> 1][k][i & 1], w.unit[n][k], -here));
+                    const float e = exp2_fast(fmaf(s[n][i >> 1][k][i & 1], w.unit[n][k], base));
                     s[n][i >> 1][k][i & 1] = e;
                     sum += e;
                 }
-                w.sum[n][k] = fmaf(w.sum[n][k], f[n][k], sum * fresh);
+                w.sum[n][k] = fmaf(w.sum[n][k], f[n][k], sum * (EXACT ? fresh : fresh * (1.0f / 16384.0f)));
             }
         }
         if (__any_sync(0xFFFFFFFFu, faint)) {  // hidden keys, whose weight is 0, do not count
@@ -927,7 +989,7 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
 #pragma unroll
                 for (int k = 0; k < R; ++k)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) faint |= s[n][i >> 1][k][i & 1] < kFaint && s[n][i >> 1][k][i & 1] > 0.0f;
+                    for (int i = 0; i < 8; ++i) faint |= s[n][i >> 1][k][i & 1] < kLow && s[n][i >> 1][k][i & 1] > 0.0f;
             faint = __any_sync(0xFFFFFFFFu, faint);
         }
         // the weights as the B operand's keys and columns
@@ -941,7 +1003,7 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
                         if constexpr (EXACT) {
                             pp[(n * 4 + w.t) * L::p_stride + 16 * m + 2 * h] = pick(s[n][m][0][h]);
                         } else {
-                            pw[n][m][h] = transpose8(pack_rn(pick(s[n][m][0][h]) * 16384.0f, pick(s[n][m][R - 1][h]) * 16384.0f));
+                            pw[n][m][h] = transpose8(pack_rn(pick(s[n][m][0][h]), pick(s[n][m][R - 1][h])));
                         }
                     }
             __syncwarp();
@@ -961,12 +1023,12 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float e = s[n][i >> 1][k][i & 1] * raise;
-                            more |= e < kFaint && e > 0.0f;
+                            more |= e < kLow && e > 0.0f;
                         }
                     }
                 hand_over([raise](float v) {
                     const float e = v * raise;
-                    return e >= kFaint && e < 1.0f ? e : 0.0f;
+                    return e >= kLow && e < kFull ? e : 0.0f;
                 });
                 tile_values<D, NT, EXACT, true>(w, pw, f, low);
                 __syncwarp();
@@ -976,7 +1038,7 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
                     for (int k = 0; k < R; ++k) f[n][k] = 1.0f;
                 faint = __any_sync(0xFFFFFFFFu, more);
             }
-            hand_over([](float e) { return e < kFaint ? 0.0f : e; });
+            hand_over([](float e) { return e < kLow ? 0.0f : e; });
         } else {
             hand_over([](float e) { return e; });
         }
@@ -1000,13 +1062,15 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
 // The lane's accumulators as outputs, unnormalised, row by row: begin(n, k,
 // row) returns a function of (dimension, value).
 template <int D, int NT, bool EXACT, typename Begin>
-__device__ __forceinline__ void each_output(const WarpState<D, NT, EXACT> &w, Begin begin) {
+__device__ __forceinline__ void each_output(const WarpState<D, NT, EXACT> &w, int rows, Begin begin) {
     constexpr int NB = D / 32, R = WarpState<D, NT, EXACT>::R;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            auto put = begin(n, k, EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k);
+            const int row = EXACT ? n * 4 + w.t : n * 8 + 2 * w.t + k;
+            if (row >= rows) continue;
+            auto put = begin(n, k, row);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -1018,6 +1082,12 @@ __device__ __forceinline__ void each_output(const WarpState<D, NT, EXACT> &w, Be
                         put(32 * b + 16 * h + 2 * w.g + m, v * (h ? 0.0625f : 1.0f));
                     }
         }
+}
+
+// How many rows an item has.
+template <int ROWS>
+__device__ __forceinline__ int rows_of(const StreamParams &p, const Target &to) {
+    return min(ROWS, to.rows * (p.a.heads / p.kv_heads) - to.group * ROWS);
 }
 
 // The row of q, and the head, that row `row` of an item stands for; false for
@@ -1115,16 +1185,15 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
             __syncwarp();
         }
         const Target to = part.to;
+        const int rows = rows_of<ROWS>(p, to);
         if (part.t0 == 0 && part.t1 == part.tiles) {
-            each_output<D, NT, EXACT>(w, [&](int n, int k, int row) {
+            each_output<D, NT, EXACT>(w, rows, [&](int n, int k, int row) {
                 int64_t at = 0;
                 int head = 0;
-                const bool there = locate<ROWS>(p, to, row, at, head);
+                locate<ROWS>(p, to, row, at, head);
                 at = at * p.a.out_stride + static_cast<int64_t>(head) * D;
                 const float down = w.sum[n][k] == 0.0f ? 0.0f : 1.0f / w.sum[n][k];
-                return [&p, there, at, down](int d, float v) {
-                    if (there) store_value(p.a.out, at + d, p.a.out_bf16, v * down);
-                };
+                return [&p, at, down](int d, float v) { store_value(p.a.out, at + d, p.a.out_bf16, v * down); };
             });
             if (w.g == 0)
 #pragma unroll
@@ -1141,7 +1210,7 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
         const bool head = part.t0 > 0, last = part.x >= part.end;
         float *rec = last ? reinterpret_cast<float *>(w.codes)
                           : p.warp_records + (static_cast<int64_t>(blockIdx.x) * W + warp) * kRecord;
-        each_output<D, NT, EXACT>(w, [rec](int, int, int row) { return [=](int d, float v) { rec[row * D + d] = v; }; });
+        each_output<D, NT, EXACT>(w, rows, [rec](int, int, int row) { return [=](int d, float v) { rec[row * D + d] = v; }; });
         if (w.g == 0)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -1204,7 +1273,7 @@ __global__ void __launch_bounds__((Layout<D, NT, EXACT>::threads), (Layout<D, NT
                 }
             }
             __syncthreads();
-            for (int i = threadIdx.x; i < ROWS * D / 4; i += L::threads) {
+            for (int i = threadIdx.x; i < rows_of<ROWS>(p, to) * (D / 4); i += L::threads) {
                 const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -1258,7 +1327,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const StreamParams 
     pdl_launch_dependents();
     const int n = gridDim.x, c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const CtaParts mine = p.parts[c];
-    if (!(mine.flags & kTail)) return;
+    if (!(mine.flags & kTail) || static_cast<int>(blockIdx.y) * kJoinOutputs >= rows_of<ROWS>(p, mine.target) * D) return;
     for (int i = threadIdx.x; i < n; i += kThreads) flags[i] = p.parts[i].flags;
     __syncthreads();
     if (warp == 0) {  // the parts: c's tail, then heads up to the first that is not open
