@@ -33,10 +33,7 @@
 // of 13000 cycles a tile.  An item that several warps share leaves
 // a maximum, a sum and an unnormalised output per warp; a CTA joins what its
 // warps hold, and a second kernel joins what several CTAs hold.
-#include "qmm_internal.h"
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include "qmm_attn.cuh"
 
 #include <algorithm>
 
@@ -48,7 +45,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;  // keys
 constexpr float kFaint = 1.0f / 16777216.0f;  // 2^-24
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // binary16 pairs, times 2^-24
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // One head dimension's shared memory, per warp.
 template <int D, int NT, bool EXACT>
@@ -93,13 +89,9 @@ enum : int {
 };
 
 // One request as the line sees it.
-struct Request {
-    int row0, rows;      // first row of q, and rows that are there
-    int len;             // keys, within the table
-    int first;           // position of row 0 (may be negative)
+struct Request : RequestRows {
     int tile0, tiles;    // of every item of the request
     int groups;          // row groups
-    int bad;
 };
 
 // A warp's place in the line and the part that it works on.
@@ -147,12 +139,6 @@ struct StreamParams {
 constexpr int kRecord = 8 * 256 + 16;
 constexpr int kRecordStat = 8 * 256;
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -177,70 +163,21 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// binary16 pair, lo in the low half: toward zero, or to nearest
-__device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 // 0xFFFF in each half that is not zero (NaN is not)
 __device__ __forceinline__ uint32_t not_zero2(uint32_t v) {
     return __hneu2_mask(*reinterpret_cast<const __half2 *>(&v), __half2half2(__ushort_as_half(0)));
 }
 
-// 2^e for -126 <= e <= 127
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
-// floor(log2 x) of a positive normal x (-127 for zero and subnormals)
-__device__ __forceinline__ int exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
-
-__device__ __forceinline__ float load_value(const void *p, int64_t i, bool bf16) {
-    if (bf16)
-        return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
-    return static_cast<const float *>(p)[i];
-}
-
-__device__ __forceinline__ void store_value(void *p, int64_t i, bool bf16, float v) {
-    if (bf16)
-        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<float *>(p)[i] = v;
-}
-
 // ---- the line of tiles -----------------------------------------------------------
 
-// The first key that position pos sees, and the number of tiles up to key n.
-__device__ __forceinline__ int first_key(const AttnArgs &a, int pos) {
-    return a.window && pos >= a.window ? pos - a.window + 1 : 0;
-}
+// The number of tiles up to key n.
 __device__ __forceinline__ int tiles_to(int n) { return (n + kTile - 1) / kTile; }
 
 template <int ROWS>
 __device__ __forceinline__ Request request(const StreamParams &p, int b) {
     const AttnArgs &a = p.a;
     Request r;
-    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], total = static_cast<int>(a.total_q);
-    const int n = max(s1 - s0, 0), len = a.kv_len[b];
-    r.row0 = min(max(s0, 0), total);
-    r.rows = min(max(min(s1, total) - r.row0, 0), n);
-    const int64_t room = min(a.table_width << p.page_shift, static_cast<int64_t>(INT32_MAX - 2 * kTile));
-    r.len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), room));
-    r.first = max(len, 0) - n;
-    r.bad = s0 < 0 || s1 > total || s1 < s0 || n > a.max_q || len < 0 || len > room;
+    static_cast<RequestRows &>(r) = request_rows(a, p.page_shift, b);
     r.tile0 = first_key(a, r.first) / kTile;
     r.tiles = max(1, tiles_to(r.len) - r.tile0);
     r.groups = (r.rows * (a.heads / p.kv_heads) + ROWS - 1) / ROWS;
@@ -506,7 +443,6 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
     const int d0 = w.lane * E, block = d0 / 32;
     // the sign of the scale goes to q; a scale of 0 takes q with it
     const float size = fabsf(a.scale) * kLog2e, sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
-    const int size_up = exponent(size);
 #pragma unroll
     for (int row = 0; row < L::rows; ++row) {
         if (row >= rows_here) {  // columns without a row: zeros, which see what row 0 sees
@@ -520,10 +456,8 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
             bits = max(bits, __float_as_uint(v[row][i]) & 0x7FFFFFFFu);
         }
         const float big = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, bits));
-        // 2^up brings q below 2^15; the score's unit, size * 2^(24 - up), stays a normal number
-        const int up = min(max(14 - exponent(big), max(-113, size_up - 96)), 100);
-        const float f = pow2i(up);
-        const float unit = sign == 0.0f ? 1.0f : fmaxf(size * pow2i((24 - up) / 2) * pow2i(24 - up - (24 - up) / 2), 1.17549435e-38f);
+        const int up = query_raise(big, size);
+        const float f = pow2i(up), unit = score_unit(size, 24 - up);
         const int nt = row / (L::rows / NT), in = row % (L::rows / NT);
         float s_hi = 0.0f, s_lo = 0.0f;
         // value d of a block: lane (d & 15) / 4 of the column, register
@@ -587,13 +521,6 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
                 if (n == nt && (EXACT ? w.t : w.t * 2 + k) == in) w.unit[n][k] = unit;
     }
     __syncwarp();
-}
-
-__device__ __forceinline__ float low_float(uint32_t v) {
-    return __low2float(*reinterpret_cast<const __half2 *>(&v));
-}
-__device__ __forceinline__ float high_float(uint32_t v) {
-    return __high2float(*reinterpret_cast<const __half2 *>(&v));
 }
 
 // NB binary16 scales of one key.
@@ -691,7 +618,7 @@ __device__ __forceinline__ int tile_scales(WarpState<D, NT, EXACT> &w, unsigned 
         for (int i = 0; i < NB / 2; ++i) {
             if (!((seen >> k) & 1u)) d[k][i] = 0u;
             // NaN is passed over
-            asm("max.f16x2 %0, %1, %2;" : "=r"(big) : "r"(big), "r"(d[k][i] & 0x7FFF7FFFu));
+            big = hmax2(big, d[k][i] & 0x7FFF7FFFu);
         }
     // infinity counts as 65504; the order of positive numbers is that of their bits
     const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(fmaxf(low_float(big), high_float(big)), 65504.0f)));
@@ -1447,6 +1374,7 @@ size_t attn_workspace_bytes(const KvCache &, int) {
 }
 
 cudaError_t launch_attn(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    if (attn_tiles_pay(c, a)) return launch_attn_tiles(c, a, stream, ctx);
     if (c.head_dim == 64) return launch_dim<64>(c, a, stream, ctx);
     if (c.head_dim == 128) return launch_dim<128>(c, a, stream, ctx);
     return launch_dim<256>(c, a, stream, ctx);

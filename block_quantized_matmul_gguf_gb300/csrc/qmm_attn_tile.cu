@@ -1,0 +1,774 @@
+// qmm_attn_tile.cu -- attention over the paged Q4_0 cache on the tcgen05
+// tensor cores, for the prompts' many query rows (bf16 output).
+//
+// One CTA takes 128 query rows (head_dim 256) or 256 (64, 128) of one request
+// and key head -- the query heads of a group side by side -- over all their
+// keys, in tiles of 64:
+//   S = Q K^T    M = 128 rows, N = 64 keys, K = head_dim; Q in tensor memory
+//   P = 2^(S - m) in binary16, written over S
+//   O += P V     M = 128 rows, N = head_dim, K = 64 keys; O in tensor memory
+// Warps by role:
+//   softmax   4 per 128 rows, a thread per row: stages Q, turns S into P,
+//             keeps maximum and sum, scales O when the maximum has grown by
+//             more than 2 (powers of two), writes the output
+//   dequant   8: codes and scales from global memory, a tile ahead in
+//             registers, to binary16 rows of 64 values with the 128-byte
+//             swizzle; K is then a K-major operand and V, its rows being keys
+//             too, an MN-major one of the same layout
+//   MMA       one thread; the products of tile t + 1 run while tile t is in
+//             the softmax
+// Values keep the order in which a word of codes gives them (0 2 16 18 1 3 17
+// 19 and so on); Q is staged in that order and the outputs are put back.
+//
+// Precision: q, (n - 8) d and the weights are rounded once to binary16 each.
+// A tile's K and V are scaled by powers of two to below 16, q per row to
+// below 2^15 and the weights to at most 2^15, so that nothing overflows; weights
+// below 2^-38 of a row's largest fall out of binary16's range, which shows
+// only where the heavy keys' codes leave (nearly) nothing: such rows are done
+// again by all warps in fp32.
+//
+// Bound by the issue slots of the dequantisation and the softmax beside the
+// products (about 0.9 slots a cycle at head_dim 256 if the products never
+// waited).
+#include "qmm_attn.cuh"
+#include "qmm_tc.cuh"
+
+#include <algorithm>
+
+namespace qmm {
+namespace {
+
+constexpr int kKeys = 64;                  // of a tile
+constexpr int kDequantWarps = 8;
+constexpr int kRing = 16;                  // tiles whose exponents are kept
+constexpr int kPanel = kKeys * 128;        // bytes of 64 values of a tile's keys
+constexpr float kRaise = 13.0f;            // the reference weight is 2^13
+constexpr float kSlack = 2.0f;             // ... and the largest at most 2^15
+
+template <int D>
+struct Tile {
+    static constexpr int QT = D == 256 ? 1 : 2;  // 128-row tiles; O of both fits tensor memory
+    static constexpr int rows = 128 * QT;
+    static constexpr int stages = D == 256 ? 3 : 4;
+    static constexpr int bytes = kKeys * D * 2;
+    static constexpr int softmax_warps = 4 * QT;
+    static constexpr int mma_warp = softmax_warps + kDequantWarps;
+    static constexpr int threads = (mma_warp + 1) * 32;
+    static constexpr int units = D == 256 ? 2 : 1;  // blocks of 32 values per dequant thread
+    // tensor memory columns
+    static constexpr int o_col = 0, q_col = QT * D, s_col = q_col + QT * D / 2;
+    static constexpr uint32_t tmem_cols = 512;
+    static_assert(s_col + 2 * kKeys <= 512, "tensor memory");
+};
+
+struct TileInfo {
+    int k_exp, v_exp;      // K and V of the tile are scaled by 2^-exp
+    uint32_t lost;         // 16-key groups without a page
+    uint32_t odd[2];       // keys whose V holds a NaN or an infinity
+};
+
+struct Block {
+    int b, kv_head;
+    int q_row0, flat0, rows, all;  // first row of q of the request; first flat row, rows of the block, of the request
+    int first, len;
+    int lo, hi, lo_all, hi_all;    // keys that any, and that every, row sees
+    int key0, tiles;
+};
+
+struct TileShared {
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full[2], p_full[2], pv_done[2], q_ready, final;
+    TileInfo info[kRing];
+    int exps[2][2][kDequantWarps];  // [tile parity][K, V][warp]
+    int64_t scratch[32];
+    Block block;
+    uint32_t tmem;
+    int abort;
+    uint32_t again[8];              // rows to do again, a bit each
+    float part[32][2];              // of those: the warps' maxima and sums
+};
+
+struct TileParams {
+    AttnArgs a;
+    const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int num_pages, page_shift, kv_heads;
+    bool q_wide, out_wide;  // rows are 16-byte aligned
+    LaunchCtx ctx;
+};
+
+// kind::f16 with binary16 operands and fp32 sums, M = 128; b_rows: B's rows
+// are along K (MN-major).
+constexpr uint32_t tile_idesc(int n, bool b_rows) {
+    return (1u << 4) | (b_rows ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// B operand with rows along K: 8-row groups 1024 bytes apart, 64-value panels
+// kPanel bytes apart.
+__device__ __forceinline__ uint64_t rows_desc(uint32_t saddr) {
+    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(kPanel >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// ---- which block of rows this CTA takes ------------------------------------------
+
+template <int D>
+__device__ __forceinline__ int request_blocks(const TileParams &p, const RequestRows &r) {
+    return (r.rows * (p.a.heads / p.kv_heads) + Tile<D>::rows - 1) / Tile<D>::rows;
+}
+
+// Fills sh.block; block.b is -1 for CTAs past the last block.
+template <int D>
+__device__ __forceinline__ void find_block(const TileParams &p, TileShared &sh) {
+    using T = Tile<D>;
+    const AttnArgs &a = p.a;
+    const int blk = blockIdx.x / p.kv_heads, kv_head = blockIdx.x - blk * p.kv_heads;
+    const int per = (a.batch + T::threads - 1) / T::threads;
+    const int b0 = min(a.batch, static_cast<int>(threadIdx.x) * per), b1 = min(a.batch, b0 + per);
+    int64_t mine = 0;
+    int bad = 0;
+    for (int b = b0; b < b1; ++b) {
+        const RequestRows r = request_rows(a, p.page_shift, b);
+        mine += request_blocks<D>(p, r);
+        bad |= r.bad;
+    }
+    if (bad && blockIdx.x == 0) record_error(p.ctx, kDevErrIndex);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += up;
+    }
+    if (lane == 31) sh.scratch[warp] = sum;
+    if (threadIdx.x == 0) sh.block.b = -1;
+    __syncthreads();
+    int64_t before = sum - mine;
+    for (int w = 0; w < warp; ++w) before += sh.scratch[w];
+    if (blk >= before && blk < before + mine) {
+        for (int b = b0; b < b1; ++b) {
+            const RequestRows r = request_rows(a, p.page_shift, b);
+            const int n = request_blocks<D>(p, r);
+            if (blk >= before + n) {
+                before += n;
+                continue;
+            }
+            // the last rows see the most keys: they go first
+            const int at = n - 1 - static_cast<int>(blk - before), heads = a.heads / p.kv_heads;
+            Block k;
+            k.b = b;
+            k.kv_head = kv_head;
+            k.q_row0 = r.row0;
+            k.all = r.rows * heads;
+            k.flat0 = at * T::rows;
+            k.rows = min(T::rows, k.all - k.flat0);
+            k.first = r.first;
+            k.len = r.len;
+            const int pos0 = r.first + k.flat0 / heads, pos1 = r.first + (k.flat0 + k.rows - 1) / heads;
+            k.lo = first_key(a, pos0);
+            k.hi = a.causal ? min(r.len, pos1 + 1) : r.len;
+            k.lo_all = first_key(a, pos1);
+            k.hi_all = a.causal ? min(r.len, pos0 + 1) : r.len;
+            k.key0 = k.lo / kKeys * kKeys;
+            k.tiles = k.hi > k.lo ? (k.hi - k.key0 + kKeys - 1) / kKeys : 0;
+            sh.block = k;
+            break;
+        }
+    }
+    __syncthreads();
+}
+
+// ---- dequantisation ----------------------------------------------------------------
+
+// The 16 bytes of one block to 32 binary16 values times the pair d2, in the
+// words' own order, as four 16-byte chunks.
+__device__ __forceinline__ void dequant_block(const uint4 &codes, uint32_t d2, uint4 (&out)[4]) {
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    const uint32_t magic = 0x64006400u;                      // 1024, 1024
+    const uint32_t minus = 0xE408E408u;                      // -1032
+    const uint32_t sixteenth = 0x2C002C00u, minus72 = 0xD480D480u;  // 1/16, -72
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = w[i], x8 = x >> 8;
+        out[i].x = hmul2(hadd2((x & 0x000F000Fu) | magic, minus), d2);
+        out[i].y = hmul2(hfma2((x & 0x00F000F0u) | magic, sixteenth, minus72), d2);
+        out[i].z = hmul2(hadd2((x8 & 0x000F000Fu) | magic, minus), d2);
+        out[i].w = hmul2(hfma2((x8 & 0x00F000F0u) | magic, sixteenth, minus72), d2);
+    }
+}
+
+// What a dequant thread holds of one tile: its key's blocks.
+template <int D>
+struct Held {
+    uint4 codes[2][Tile<D>::units];
+    uint16_t scale[2][Tile<D>::units];
+    bool there;
+};
+
+template <int D>
+__device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh, uint8_t *smem, int w8, int lane) {
+    using T = Tile<D>;
+    constexpr int NB = D / 32, U = T::units;
+    const Block bk = sh.block;
+    // the thread's key in each tile, and its first block; head_dim 64: four
+    // warps for K and four for V
+    const int key = D == 64 ? (w8 & 3) * 16 + (lane & 15) : w8 * 8 + (lane & 7);
+    const int block = D == 64 ? lane >> 4 : lane >> 3;
+    const int half0 = D == 64 ? w8 >> 2 : 0, half1 = D == 64 ? half0 + 1 : 2;
+    const int32_t *table = p.a.table + bk.b * p.a.table_width;
+    auto page_of = [&](int t) -> int32_t {
+        const int k = bk.key0 + t * kKeys + key;
+        if (t >= bk.tiles || k < bk.lo || k >= bk.hi) return -2;  // no key
+        return table[k >> p.page_shift];
+    };
+    auto load = [&](int t, int32_t page, Held<D> &h) {
+        const int k = bk.key0 + t * kKeys + key;
+        h.there = page >= 0 && page < p.num_pages;
+        const int64_t row = h.there ? (((page * p.kv_heads) + bk.kv_head) << p.page_shift) + (k & ((1 << p.page_shift) - 1)) : 0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                h.codes[half][u] = make_uint4(0u, 0u, 0u, 0u);
+                h.scale[half][u] = 0;
+                if (h.there && half >= half0 && half < half1) {
+                    const int b = block + 4 * u;
+                    h.codes[half][u] = __ldg(reinterpret_cast<const uint4 *>((half ? p.v_codes : p.k_codes) + row * (D / 2)) + b);
+                    h.scale[half][u] = __ldg(reinterpret_cast<const uint16_t *>(half ? p.v_scales : p.k_scales) + row * NB + b);
+                }
+            }
+        }
+    };
+    int32_t page = page_of(0), page_next = page_of(1);
+    Held<D> next;
+    load(0, page, next);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool live = true;
+    for (int t = 0; t < bk.tiles; ++t) {
+        Held<D> cur = next;
+        const int32_t page_here = page;
+        page = page_next;
+        page_next = page_of(t + 2);
+        load(t + 1, page, next);
+        // the tile's largest scales
+        TileInfo &info = sh.info[t % kRing];
+        int e[2] = {0, 0};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                uint32_t bits = cur.scale[half][u] & 0x7FFFu;
+                if (bits >= 0x7C00u) {
+                    if (half && cur.there) atomicOr(&info.odd[key >> 5], 1u << (key & 31));
+                    bits = 0;  // NaN and infinity do not set the scale
+                }
+                top = max(top, bits);
+            }
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            e[half] = top ? exponent(__half2float(__ushort_as_half(static_cast<unsigned short>(top)))) : -24;
+            if (lane == 0) sh.exps[t & 1][half][w8] = e[half];
+        }
+        const unsigned gone = __ballot_sync(0xFFFFFFFFu, !cur.there && page_here != -2);
+        if (gone && lane == 0) {
+            record_error(p.ctx, kDevErrIndex);
+            atomicOr(&info.lost, 1u << (key >> 4));  // lane 0's key: the warp's keys lie in one group
+        }
+        asm volatile("bar.sync 1, %0;" ::"r"(kDequantWarps * 32) : "memory");
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            int top = -24;
+#pragma unroll
+            for (int w = 0; w < kDequantWarps; ++w)
+                if (D != 64 || (w >> 2) == half) top = max(top, sh.exps[t & 1][half][w]);
+            e[half] = top;
+        }
+        if (w8 == 0 && lane == 0) {
+            info.k_exp = e[0];
+            info.v_exp = e[1];
+            TileInfo &later = sh.info[(t + kRing / 2) % kRing];  // not in use: readers lag by less
+            later.lost = later.odd[0] = later.odd[1] = 0;
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t empty = smem_addr(half ? sh.v_empty + stage : sh.k_empty + stage);
+            const uint32_t full = smem_addr(half ? sh.v_full + stage : sh.k_full + stage);
+            // after a wait that gave up, the warp goes on without waiting: the
+            // others expect it at the barrier above
+            if (live) live = warp_wait_or_abort(empty, phase ^ 1u, &sh.abort, p.ctx);
+            if (half >= half0 && half < half1) {
+                uint8_t *rows = smem + (half * T::stages + stage) * T::bytes + key * 128;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int b = block + 4 * u;
+                    float d = __half2float(__ushort_as_half(cur.scale[half][u]));
+                    if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd
+                    d *= pow2i(-e[half]);
+                    uint4 out[4];
+                    dequant_block(cur.codes[half][u], pack_rn(d, d), out);
+                    uint8_t *panel = rows + (b >> 1) * kPanel;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(panel + ((((b & 1) * 4 + i) ^ (key & 7)) << 4)) = out[i];
+                }
+                fence_proxy_async_smem();  // generic writes -> tensor-core reads
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_addr(full);
+        }
+        if (++stage == T::stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+}
+
+// ---- the products --------------------------------------------------------------------
+
+template <int D>
+__device__ __forceinline__ void mma_role(const TileParams &p, TileShared &sh, uint32_t smem, uint32_t tmem) {
+    using T = Tile<D>;
+    const int jobs = sh.block.tiles * T::QT;
+    constexpr uint32_t qk_desc = tile_idesc(kKeys, false), pv_desc = tile_idesc(D, true);
+    int *abort = &sh.abort;
+    bool issued = false;
+    // job j: rows tile j % QT with key tile j / QT, S buffer j % 2
+    auto qk = [&](int j) -> bool {
+        const int t = j / T::QT, qt = j % T::QT, stage = t % T::stages;
+        if (qt == 0 && !wait_or_abort(smem_addr(sh.k_full + stage), (t / T::stages) & 1u, abort, p.ctx)) return false;
+        tc_fence_after();
+        const uint64_t b0 = sw128_desc(smem + stage * T::bytes);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+            umma_bf16_cta_ta(tmem + T::s_col + (j & 1) * kKeys, tmem + T::q_col + qt * (D / 2) + s * 8,
+                             b0 + (((s >> 2) * kPanel + (s & 3) * 32) >> 4), qk_desc, s > 0);
+        issued = true;
+        umma_commit_cta(smem_addr(sh.s_full + (j & 1)));
+        if (qt == T::QT - 1) umma_commit_cta(smem_addr(sh.k_empty + stage));
+        return true;
+    };
+    bool ok = jobs == 0 || wait_or_abort(smem_addr(&sh.q_ready), 0, abort, p.ctx);
+    if (ok && jobs > 0) ok = qk(0);
+    if (ok && jobs > 1) ok = qk(1);
+    for (int j = 0; ok && j < jobs; ++j) {
+        const int t = j / T::QT, qt = j % T::QT, stage = t % T::stages;
+        if (!wait_or_abort(smem_addr(sh.p_full + (j & 1)), (j >> 1) & 1u, abort, p.ctx)) break;
+        if (qt == 0 && !wait_or_abort(smem_addr(sh.v_full + stage), (t / T::stages) & 1u, abort, p.ctx)) break;
+        tc_fence_after();
+        const uint64_t b0 = rows_desc(smem + (T::stages + stage) * T::bytes);
+#pragma unroll
+        for (int s = 0; s < kKeys / 16; ++s)
+            umma_bf16_cta_ta(tmem + T::o_col + qt * D, tmem + T::s_col + (j & 1) * kKeys + s * 8, b0 + ((s * 2048) >> 4),
+                             pv_desc, t > 0 || s > 0);
+        umma_commit_cta(smem_addr(sh.pv_done + qt));
+        if (qt == T::QT - 1) umma_commit_cta(smem_addr(sh.v_empty + stage));
+        // the next S goes where P lies, once its product has read it (products
+        // with different accumulators are not ordered among themselves)
+        if (j + 2 < jobs) ok = wait_or_abort(smem_addr(sh.pv_done + qt), t & 1u, abort, p.ctx) && qk(j + 2);
+    }
+    if (issued) {  // all products end before tensor memory is freed
+        umma_commit_cta(smem_addr(&sh.final));
+        wait_drain(smem_addr(&sh.final), 0, p.ctx);
+    }
+}
+
+// ---- softmax ----------------------------------------------------------------------------
+
+// Eight consecutive values of a row of q.
+__device__ __forceinline__ void load8(const AttnArgs &a, int64_t at, bool wide, float (&v)[8]) {
+    if (wide && a.q_bf16) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else if (wide) {
+        const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at);
+        const float4 y = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at + 4);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = load_value(a.q, at + i, a.q_bf16);
+    }
+}
+
+// Value d of a block is at this place of the order in which words give them.
+__host__ __device__ constexpr int place_of(int d) {
+    return ((d & 15) >> 2) * 8 + ((d & 1) << 2) + ((d >> 4) << 1) + ((d >> 1) & 1);
+}
+
+template <int D>
+__device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh, uint32_t tmem, int warp, int lane) {
+    using T = Tile<D>;
+    constexpr int NB = D / 32;
+    const AttnArgs &a = p.a;
+    const Block bk = sh.block;
+    const int qt = warp >> 2, row = warp * 32 + lane, heads = a.heads / p.kv_heads;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float ninf = __uint_as_float(0xFF800000u);
+    const bool mine = row < bk.rows;
+    const int flat = bk.flat0 + (mine ? row : 0), token = flat / heads, head = bk.kv_head * heads + flat - token * heads;
+    const int64_t q_at = (static_cast<int64_t>(bk.q_row0) + token) * a.q_stride + static_cast<int64_t>(head) * D;
+
+    // the row of q, scaled to below 2^15, into tensor memory
+    const float size = fabsf(a.scale) * kLog2e, sign = !mine || a.scale == 0.0f ? 0.0f : a.scale < 0.0f ? -1.0f : 1.0f;
+    float unit;
+    if (bk.tiles > 0) {
+        uint32_t bits = 0;
+#pragma unroll 4
+        for (int i = 0; i < D; i += 8) {
+            float v[8];
+            load8(a, q_at + i, p.q_wide, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) bits = max(bits, __float_as_uint(v[k] * sign) & 0x7FFFFFFFu);
+        }
+        const int up = query_raise(__uint_as_float(bits), size);
+        const float f = pow2i(up) * sign;
+        unit = score_unit(size, -up);
+#pragma unroll 1
+        for (int b = 0; b < NB; ++b) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                float u[8];
+                load8(a, q_at + b * 32 + i, p.q_wide, u);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[i + k] = u[k] * f;
+            }
+            uint32_t cols[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {  // values d and d + 2 stand side by side
+                const int d = ((i >> 2) << 2) + ((i >> 1) & 1) + ((i & 1) << 4);
+                cols[i] = pack_rn(v[d], v[d + 2]);
+            }
+            tmem_st_16cols(tmem + lanes + T::q_col + qt * (D / 2) + b * 16, cols);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_addr(smem_addr(&sh.q_ready));
+    }
+
+    const int pos = bk.first + token;
+    const int lo = mine ? first_key(a, pos) : 0, hi = mine ? (a.causal ? min(bk.len, pos + 1) : bk.len) : 0;
+    float top = ninf, sum = 0.0f;  // the weights' reference (of 2^kRaise), and their sum
+    int e_ref = -24;               // exponent of V's unit in O
+    bool faint = false;            // a weight fell below binary16's normal numbers
+    bool ok = true;
+    for (int t = 0; t < bk.tiles; ++t) {
+        const int j = t * T::QT + qt;
+        if (!warp_wait_or_abort(smem_addr(sh.s_full + (j & 1)), (j >> 1) & 1u, &sh.abort, p.ctx) ||
+            !warp_wait_or_abort(smem_addr(sh.v_full + t % T::stages), (t / T::stages) & 1u, &sh.abort, p.ctx)) {
+            ok = false;
+            break;
+        }
+        tc_fence_after();
+        const uint32_t s_at = tmem + lanes + T::s_col + (j & 1) * kKeys;
+        uint32_t s[64];
+        tmem_ld_64cols(s_at, s);
+        const TileInfo &info = sh.info[t % kRing];
+        const float u = unit * pow2i(info.k_exp);
+        const int key0 = bk.key0 + t * kKeys;
+        const bool edge = info.lost || info.odd[0] || info.odd[1] || key0 < bk.lo_all || key0 + kKeys > bk.hi_all;
+        if (edge) {
+            const uint32_t odd[2] = {info.odd[0], info.odd[1]}, lost = info.lost;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+                if ((odd[i >> 5] >> (i & 31)) & 1u) s[i] = 0x7FFFFFFFu;  // its value is no number
+                if (key0 + i < lo || key0 + i >= hi || ((lost >> (i >> 4)) & 1u)) s[i] = 0xFF800000u;
+            }
+        }
+        float big = __uint_as_float(s[0]), small = big;
+#pragma unroll
+        for (int i = 1; i < 64; ++i) {
+            big = fmaxf(big, __uint_as_float(s[i]));
+            small = fminf(small, __uint_as_float(s[i]));
+        }
+        if (edge) {  // of the keys that the row sees
+            small = __uint_as_float(0x7F800000u);
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (s[i] != 0xFF800000u) small = fminf(small, __uint_as_float(s[i]));
+        }
+        const float here = big * u;
+        // a new reference where the largest weight would pass 2^15, and where
+        // V's unit grows
+        const bool grow = here > top + kSlack;
+        const int e_now = max(e_ref, info.v_exp);
+        const float now = grow || top == ninf ? fmaxf(top, here) : top;
+        if (__any_sync(0xFFFFFFFFu, now != top || e_now != e_ref)) {
+            const float f = top == ninf ? 0.0f : exp2_fast(top - now);
+            sum *= f;
+            if (t > 0) {
+                const float scale = f * pow2i(e_ref - e_now);
+                if (!warp_wait_or_abort(smem_addr(sh.pv_done + qt), (t - 1) & 1u, &sh.abort, p.ctx)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32], v[16];
+                    const uint32_t at = tmem + lanes + T::o_col + qt * D + c;
+                    tmem_ld_32cols(at, o);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(o[16 * h + i]) * scale);
+                        tmem_st_16cols(at + 16 * h, v);
+                    }
+                }
+            }
+            top = now;
+            e_ref = e_now;
+        }
+        const int shift = info.v_exp - e_ref;
+        const float base = kRaise + static_cast<float>(shift) - (top == ninf ? 0.0f : top);
+        faint |= fmaf(small, u, base) < -14.0f;
+        float add = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = exp2_fast(fmaf(__uint_as_float(s[32 * h + 2 * i]), u, base));
+                const float y = exp2_fast(fmaf(__uint_as_float(s[32 * h + 2 * i + 1]), u, base));
+                add += x + y;
+                w[i] = pack_rn(x, y);
+            }
+            tmem_st_16cols(s_at + 16 * h, w);
+        }
+        sum = fmaf(add, pow2i(-13 - shift), sum);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_addr(smem_addr(sh.p_full + (j & 1)));
+    }
+
+    // outputs
+    if (ok && bk.tiles > 0) ok = warp_wait_or_abort(smem_addr(sh.pv_done + qt), (bk.tiles - 1) & 1u, &sh.abort, p.ctx);
+    tc_fence_after();
+    const int64_t out_row = static_cast<int64_t>(bk.q_row0) + token;
+    const int64_t out_at = out_row * a.out_stride + static_cast<int64_t>(head) * D;
+    const float down = sum == 0.0f ? 0.0f : pow2i(e_ref - 13) / sum;
+    float least = __uint_as_float(0x7F800000u);
+    if (ok) {
+#pragma unroll 1
+        for (int b = 0; b < NB; ++b) {
+            uint32_t o[32];
+            if (bk.tiles > 0) {
+                tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) least = fminf(least, fabsf(__uint_as_float(o[i])));
+            if (!mine) continue;
+            if (p.out_wide) {
+                uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_at + b * 32);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int d = c * 8 + i * 2;
+                        w[i] = pack_bf16x2(__uint_as_float(o[place_of(d)]) * down, __uint_as_float(o[place_of(d + 1)]) * down);
+                    }
+                    to[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else {
+#pragma unroll
+                for (int d = 0; d < 32; ++d)
+                    store_value(a.out, out_at + b * 32 + d, true, __uint_as_float(o[place_of(d)]) * down);
+            }
+        }
+        if (mine && a.lse) a.lse[out_row * a.heads + head] = sum == 0.0f ? ninf : (top + log2f(sum)) * kLn2;
+    }
+    // A faint weight is off by at most 2^-25, times values below 16, a key:
+    // where an output is smaller than 2^11 times that, the row is done again.
+    const float keys = static_cast<float>(bk.tiles * kKeys);
+    const unsigned again = __ballot_sync(0xFFFFFFFFu, ok && mine && faint && least < keys * (1.0f / 1024.0f));
+    if (lane == 0) sh.again[warp] = again;
+}
+
+// One row in fp32 by all warps: warp w takes every W-th key, a lane the same
+// code bytes of each.
+template <int D>
+__device__ __noinline__ void row_again(const TileParams &p, TileShared &sh, float *share, int row) {
+    constexpr int B = D / 64, W = Tile<D>::threads / 32;  // code bytes per lane
+    const AttnArgs &a = p.a;
+    const Block &bk = sh.block;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = a.heads / p.kv_heads;
+    const int flat = bk.flat0 + row, token = flat / heads, head = bk.kv_head * heads + flat - token * heads;
+    const int64_t at = (static_cast<int64_t>(bk.q_row0) + token) * a.q_stride + static_cast<int64_t>(head) * D;
+    const int pos = bk.first + token;
+    const int lo = first_key(a, pos), hi = a.causal ? min(bk.len, pos + 1) : bk.len;
+    const float ninf = __uint_as_float(0xFF800000u);
+    float q[2 * B], o[2 * B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+        const int byte = lane + 32 * i, d = (byte >> 4) * 32 + (byte & 15);
+        q[2 * i] = load_value(a.q, at + d, a.q_bf16);
+        q[2 * i + 1] = load_value(a.q, at + d + 16, a.q_bf16);
+        o[2 * i] = o[2 * i + 1] = 0.0f;
+    }
+    float m = ninf, l = 0.0f;
+    for (int j = lo + warp; j < hi; j += W) {
+        const int32_t page = a.table[bk.b * a.table_width + (j >> p.page_shift)];
+        if (page < 0 || page >= p.num_pages) continue;
+        const int64_t r = (((page * p.kv_heads) + bk.kv_head) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int byte = lane + 32 * i;
+            const uint32_t w = p.k_codes[r * (D / 2) + byte];
+            const float d = __half2float(reinterpret_cast<const __half *>(p.k_scales)[r * (D / 32) + (byte >> 4)]);
+            s = fmaf(q[2 * i], (static_cast<float>(w & 15u) - 8.0f) * d, s);
+            s = fmaf(q[2 * i + 1], (static_cast<float>(w >> 4) - 8.0f) * d, s);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+        s *= a.scale * kLog2e;
+        const float now = fmaxf(m, s), ref = now == ninf ? 0.0f : now;
+        const float f = exp2_fast(m - ref), w = exp2_fast(s - ref);
+        m = now;
+        l = fmaf(l, f, w);
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int byte = lane + 32 * i;
+            const uint32_t c = p.v_codes[r * (D / 2) + byte];
+            const float d = __half2float(reinterpret_cast<const __half *>(p.v_scales)[r * (D / 32) + (byte >> 4)]);
+            o[2 * i] = fmaf(o[2 * i], f, w * ((static_cast<float>(c & 15u) - 8.0f) * d));
+            o[2 * i + 1] = fmaf(o[2 * i + 1], f, w * ((static_cast<float>(c >> 4) - 8.0f) * d));
+        }
+    }
+    __syncthreads();  // the last row's shares have been read
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+        const int byte = lane + 32 * i, d = (byte >> 4) * 32 + (byte & 15);
+        share[warp * D + d] = o[2 * i];
+        share[warp * D + d + 16] = o[2 * i + 1];
+    }
+    if (lane == 0) {
+        sh.part[warp][0] = m;
+        sh.part[warp][1] = l;
+    }
+    __syncthreads();
+    float top = ninf, sum = 0.0f;
+    for (int w = 0; w < W; ++w) top = fmaxf(top, sh.part[w][0]);
+    const float ref = top == ninf ? 0.0f : top;
+    for (int w = 0; w < W; ++w) sum = fmaf(exp2_fast(sh.part[w][0] - ref), sh.part[w][1], sum);
+    for (int d = threadIdx.x; d < D; d += Tile<D>::threads) {
+        float y = 0.0f;
+        for (int w = 0; w < W; ++w) y = fmaf(exp2_fast(sh.part[w][0] - ref), share[w * D + d], y);
+        store_value(a.out, (static_cast<int64_t>(bk.q_row0) + token) * a.out_stride + static_cast<int64_t>(head) * D + d,
+                    true, sum == 0.0f ? 0.0f : y / sum);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __grid_constant__ TileParams p) {
+    using T = Tile<D>;
+    extern __shared__ uint8_t tile_smem[];
+    uint8_t *smem = tile_smem + ((1024u - (smem_addr(tile_smem) & 1023u)) & 1023u);
+    TileShared &sh = *reinterpret_cast<TileShared *>(smem + 2 * T::stages * T::bytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    find_block<D>(p, sh);
+    if (sh.block.b < 0) return;  // the whole CTA
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < T::stages; ++i) {
+            mbar_init(sh.k_full + i, kDequantWarps);
+            mbar_init(sh.k_empty + i, 1);
+            mbar_init(sh.v_full + i, kDequantWarps);
+            mbar_init(sh.v_empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sh.s_full + i, 1);
+            mbar_init(sh.p_full + i, 4);
+            mbar_init(sh.pv_done + i, 1);
+        }
+        mbar_init(&sh.q_ready, T::softmax_warps);
+        mbar_init(&sh.final, 1);
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < kRing; i += T::threads) sh.info[i] = TileInfo{0, 0, 0u, {0u, 0u}};
+    if (threadIdx.x < 8) sh.again[threadIdx.x] = 0;
+    if (warp == T::mma_warp) tmem_alloc_cta(smem_addr(&sh.tmem), T::tmem_cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sh.tmem);
+
+    if (warp < T::softmax_warps) {
+        softmax_role<D>(p, sh, tmem, warp, lane);
+    } else if (warp < T::mma_warp) {
+        dequant_role<D>(p, sh, smem, warp - T::softmax_warps, lane);
+    } else {
+        if (lane == 0) mma_role<D>(p, sh, smem_addr(smem), tmem);
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == T::mma_warp) tmem_dealloc_cta(tmem, T::tmem_cols);
+#pragma unroll 1
+    for (int w = 0; w < T::softmax_warps; ++w)
+        for (uint32_t again = sh.again[w]; again; again &= again - 1)
+            row_again<D>(p, sh, reinterpret_cast<float *>(smem), w * 32 + __ffs(again) - 1);
+}
+
+template <int D>
+int64_t tile_blocks(const KvCache &c, const AttnArgs &a) {
+    const int64_t heads = a.heads / c.kv_heads;
+    return ((a.total_q * heads + Tile<D>::rows - 1) / Tile<D>::rows + a.batch) * c.kv_heads;
+}
+
+template <int D>
+cudaError_t launch_tiles(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    using T = Tile<D>;
+    static int limits[kMaxDevices];
+    constexpr size_t smem = 2 * T::stages * T::bytes + sizeof(TileShared) + 1024;
+    static_assert(smem <= 232448 && T::threads / 32 * D * 4 <= 2 * T::stages * T::bytes, "shared memory per CTA");
+    const cudaError_t e = ensure_smem(attn_tile_kernel<D>, smem, false, limits);
+    if (e != cudaSuccess) return e;
+    TileParams p = {};
+    p.a = a;
+    p.k_codes = static_cast<const uint8_t *>(c.k_codes);
+    p.k_scales = static_cast<const uint8_t *>(c.k_scales);
+    p.v_codes = static_cast<const uint8_t *>(c.v_codes);
+    p.v_scales = static_cast<const uint8_t *>(c.v_scales);
+    p.num_pages = static_cast<int>(c.num_pages);
+    p.page_shift = c.page_shift;
+    p.kv_heads = c.kv_heads;
+    const int q_size = a.q_bf16 ? 2 : 4;
+    p.q_wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_stride * q_size % 16 == 0;
+    p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride * 2 % 16 == 0;
+    p.ctx = ctx;
+    return launch_kernel(attn_tile_kernel<D>, dim3(static_cast<unsigned>(tile_blocks<D>(c, a))), dim3(T::threads), smem,
+                         stream, 1, p);
+}
+
+}  // namespace
+
+bool attn_tiles_pay(const KvCache &c, const AttnArgs &a) {
+    const int64_t rows = static_cast<int64_t>(a.max_q) * (a.heads / c.kv_heads);
+    return a.out_bf16 && rows >= 64 && tile_blocks<256>(c, a) <= INT32_MAX;
+}
+
+cudaError_t launch_attn_tiles(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    if (c.head_dim == 64) return launch_tiles<64>(c, a, stream, ctx);
+    if (c.head_dim == 128) return launch_tiles<128>(c, a, stream, ctx);
+    return launch_tiles<256>(c, a, stream, ctx);
+}
+
+}  // namespace qmm

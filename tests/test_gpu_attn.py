@@ -128,6 +128,16 @@ def test_long_prompts(qmm, heads, kv_heads, dim, new, lens, out_type, window):
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
 
 
+@pytest.mark.parametrize("dim,heads,kv_heads", [(256, 8, 2), (128, 16, 4), (64, 8, 1)])
+def test_prompts_give_the_same_bits_every_time(qmm, dim, heads, kv_heads):
+    c = Case(qmm, [1500, 700, 333], [900, 700, 64], heads, kv_heads, dim, 32, seed=dim, q_type=BF16)
+    first = c.call(qmm, BF16)
+    for _ in range(30):
+        again = c.call(qmm, BF16)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
 @pytest.mark.parametrize("dim,page,n,out_type", [(256, 16, 20011, F32), (128, 64, 50000, BF16), (64, 128, 30001, F32)])
 def test_long_contexts(qmm, dim, page, n, out_type):
     """One request over the whole GPU, beside short ones."""
