@@ -42,8 +42,8 @@ constexpr int kKeys = 64;                  // of a tile
 constexpr int kDequantWarps = 8;
 constexpr int kRing = 16;                  // tiles whose exponents are kept
 constexpr int kPanel = kKeys * 128;        // bytes of 64 values of a tile's keys
-constexpr float kRaise = 13.0f;            // the reference weight is 2^13
-constexpr float kSlack = 2.0f;             // ... and the largest at most 2^15
+constexpr int kRaise = 10;                 // the reference weight is 2^10
+constexpr float kSlack = 5.0f;             // ... and the largest at most 2^15
 
 template <int D>
 struct Tile {
@@ -293,32 +293,34 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
             TileInfo &later = sh.info[(t + kRing / 2) % kRing];  // not in use: readers lag by less
             later.lost = later.odd[0] = later.odd[1] = 0;
         }
+        // after a wait that gave up, the warp goes on without waiting: the
+        // others expect it at the barrier above
+        if (live)
+            live = warp_wait_or_abort(smem_addr(sh.k_empty + stage), phase ^ 1u, &sh.abort, p.ctx) &&
+                   warp_wait_or_abort(smem_addr(sh.v_empty + stage), phase ^ 1u, &sh.abort, p.ctx);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const uint32_t empty = smem_addr(half ? sh.v_empty + stage : sh.k_empty + stage);
-            const uint32_t full = smem_addr(half ? sh.v_full + stage : sh.k_full + stage);
-            // after a wait that gave up, the warp goes on without waiting: the
-            // others expect it at the barrier above
-            if (live) live = warp_wait_or_abort(empty, phase ^ 1u, &sh.abort, p.ctx);
-            if (half >= half0 && half < half1) {
-                uint8_t *rows = smem + (half * T::stages + stage) * T::bytes + key * 128;
+            if (half < half0 || half >= half1) continue;
+            uint8_t *rows = smem + (half * T::stages + stage) * T::bytes + key * 128;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int b = block + 4 * u;
-                    float d = __half2float(__ushort_as_half(cur.scale[half][u]));
-                    if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd
-                    d *= pow2i(-e[half]);
-                    uint4 out[4];
-                    dequant_block(cur.codes[half][u], pack_rn(d, d), out);
-                    uint8_t *panel = rows + (b >> 1) * kPanel;
+            for (int u = 0; u < U; ++u) {
+                const int b = block + 4 * u;
+                float d = __half2float(__ushort_as_half(cur.scale[half][u]));
+                if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd
+                d *= pow2i(-e[half]);
+                uint4 out[4];
+                dequant_block(cur.codes[half][u], pack_rn(d, d), out);
+                uint8_t *panel = rows + (b >> 1) * kPanel;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4 *>(panel + ((((b & 1) * 4 + i) ^ (key & 7)) << 4)) = out[i];
-                }
-                fence_proxy_async_smem();  // generic writes -> tensor-core reads
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(panel + ((((b & 1) * 4 + i) ^ (key & 7)) << 4)) = out[i];
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive_addr(full);
+        }
+        fence_proxy_async_smem();  // generic writes -> tensor-core reads
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive_addr(smem_addr(sh.k_full + stage));
+            mbar_arrive_addr(smem_addr(sh.v_full + stage));
         }
         if (++stage == T::stages) {
             stage = 0;
@@ -457,7 +459,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
 
     const int pos = bk.first + token;
     const int lo = mine ? first_key(a, pos) : 0, hi = mine ? (a.causal ? min(bk.len, pos + 1) : bk.len) : 0;
-    float top = ninf, sum = 0.0f;  // the weights' reference (of 2^kRaise), and their sum
+    float top = ninf, sum = 0.0f;  // the weights' reference (2^kRaise there), and their sum
     int e_ref = -24;               // exponent of V's unit in O
     bool faint = false;            // a weight fell below binary16's normal numbers
     bool ok = true;
@@ -484,18 +486,12 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                 if (key0 + i < lo || key0 + i >= hi || ((lost >> (i >> 4)) & 1u)) s[i] = 0xFF800000u;
             }
         }
-        float big = __uint_as_float(s[0]), small = big;
+        float most[4];
 #pragma unroll
-        for (int i = 1; i < 64; ++i) {
-            big = fmaxf(big, __uint_as_float(s[i]));
-            small = fminf(small, __uint_as_float(s[i]));
-        }
-        if (edge) {  // of the keys that the row sees
-            small = __uint_as_float(0x7F800000u);
+        for (int i = 0; i < 4; ++i) most[i] = __uint_as_float(s[i]);
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (s[i] != 0xFF800000u) small = fminf(small, __uint_as_float(s[i]));
-        }
+        for (int i = 4; i < 64; ++i) most[i & 3] = fmaxf(most[i & 3], __uint_as_float(s[i]));
+        const float big = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
         const float here = big * u;
         // a new reference where the largest weight would pass 2^15, and where
         // V's unit grows
@@ -529,9 +525,14 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             e_ref = e_now;
         }
         const int shift = info.v_exp - e_ref;
-        const float base = kRaise + static_cast<float>(shift) - (top == ninf ? 0.0f : top);
-        faint |= fmaf(small, u, base) < -14.0f;
-        float add = 0.0f;
+        const float base = static_cast<float>(kRaise + shift) - (top == ninf ? 0.0f : top);
+        if (edge) {  // hidden keys' weights are 0 and do not count
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                faint |= s[i] != 0xFF800000u && fmaf(__uint_as_float(s[i]), u, base) < -14.0f;
+        }
+        float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        uint32_t least[2] = {0x7C007C00u, 0x7C007C00u};  // smallest weights
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t w[16];
@@ -539,12 +540,21 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             for (int i = 0; i < 16; ++i) {
                 const float x = exp2_fast(fmaf(__uint_as_float(s[32 * h + 2 * i]), u, base));
                 const float y = exp2_fast(fmaf(__uint_as_float(s[32 * h + 2 * i + 1]), u, base));
-                add += x + y;
+                add[i & 1] = __fadd2_rn(add[i & 1], make_float2(x, y));
                 w[i] = pack_rn(x, y);
+                least[i & 1] = hmin2(least[i & 1], w[i]);
             }
             tmem_st_16cols(s_at + 16 * h, w);
         }
-        sum = fmaf(add, pow2i(-13 - shift), sum);
+        least[0] = hmin2(least[0], least[1]);
+        if (!edge) faint |= (least[0] & 0x7C00u) == 0 || (least[0] & 0x7C000000u) == 0;  // below the normal numbers
+        // Every phase of pv_done is waited for in turn, before the next product
+        // can start: a barrier's parity tells neighbouring phases apart only.
+        if (t > 0 && !warp_wait_or_abort(smem_addr(sh.pv_done + qt), (t - 1) & 1u, &sh.abort, p.ctx)) {
+            ok = false;
+            break;
+        }
+        sum = fmaf((add[0].x + add[0].y) + (add[1].x + add[1].y), pow2i(-kRaise - shift), sum);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -556,7 +566,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
     tc_fence_after();
     const int64_t out_row = static_cast<int64_t>(bk.q_row0) + token;
     const int64_t out_at = out_row * a.out_stride + static_cast<int64_t>(head) * D;
-    const float down = sum == 0.0f ? 0.0f : pow2i(e_ref - 13) / sum;
+    const float down = sum == 0.0f ? 0.0f : pow2i(e_ref - kRaise) / sum;
     float least = __uint_as_float(0x7F800000u);
     if (ok) {
 #pragma unroll 1
@@ -591,10 +601,12 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
         }
         if (mine && a.lse) a.lse[out_row * a.heads + head] = sum == 0.0f ? ninf : (top + log2f(sum)) * kLn2;
     }
-    // A faint weight is off by at most 2^-25, times values below 16, a key:
-    // where an output is smaller than 2^11 times that, the row is done again.
+    // A faint weight is off by at most 2^-25, times values below 16, a key.
+    // Scores that lie 24 powers of two apart are themselves uncertain by more
+    // than 2^-6 of a weight (binary16 q and K, A >= 8), so an output has to be
+    // 2^6 times that sum at least; else the row is done again.
     const float keys = static_cast<float>(bk.tiles * kKeys);
-    const unsigned again = __ballot_sync(0xFFFFFFFFu, ok && mine && faint && least < keys * (1.0f / 1024.0f));
+    const unsigned again = __ballot_sync(0xFFFFFFFFu, ok && mine && faint && least < keys * (1.0f / 32768.0f));
     if (lane == 0) sh.again[warp] = again;
 }
 
