@@ -53,7 +53,15 @@ struct Tile {
     static constexpr int bytes = kKeys * D * 2;
     static constexpr int softmax_warps = 4 * QT;
     static constexpr int mma_warp = softmax_warps + kDequantWarps;
-    static constexpr int threads = (mma_warp + 1) * 32;
+    static constexpr int threads = (mma_warp + 4) * 32;  // whole warpgroups: three warps only hold registers
+    // registers of a thread: at launch, and by role (at most as many in all:
+    // 512 x 128 >= 128 x (208 + 2 x 104 + 56), 640 x 96 >= 128 x (2 x 144 + 2 x 72 + 40))
+    static constexpr int launch_regs = D == 256 ? 128 : 96;
+    static constexpr int softmax_regs = D == 256 ? 208 : 144;
+    static constexpr int dequant_regs = D == 256 ? 104 : 72;
+    static constexpr int mma_regs = D == 256 ? 56 : 40;
+    static_assert(softmax_warps * softmax_regs + kDequantWarps * dequant_regs + 4 * mma_regs <= threads / 32 * launch_regs,
+                  "more registers than the block was launched with would be waited for in vain");
     static constexpr int units = D == 256 ? 2 : 1;  // blocks of 32 values per dequant thread
     // tensor memory columns
     static constexpr int o_col = 0, q_col = QT * D, s_col = q_col + QT * D / 2;
@@ -111,6 +119,16 @@ __device__ __forceinline__ uint64_t rows_desc(uint32_t saddr) {
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
     return d;
+}
+
+// A warpgroup's registers per thread, from its launch's pool.
+template <int N>
+__device__ __forceinline__ void registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---- which block of rows this CTA takes ------------------------------------------
@@ -423,33 +441,39 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
     float unit;
     if (bk.tiles > 0) {
         uint32_t bits = 0;
-#pragma unroll 4
-        for (int i = 0; i < D; i += 8) {
-            float v[8];
-            load8(a, q_at + i, p.q_wide, v);
+#pragma unroll 1
+        for (int i = 0; i < D; i += 64) {  // many loads under way at a time
+            float v[8][8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) bits = max(bits, __float_as_uint(v[k] * sign) & 0x7FFFFFFFu);
+            for (int c = 0; c < 8; ++c) load8(a, q_at + i + c * 8, p.q_wide, v[c]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) bits = max(bits, __float_as_uint(v[c][k] * sign) & 0x7FFFFFFFu);
         }
         const int up = query_raise(__uint_as_float(bits), size);
         const float f = pow2i(up) * sign;
         unit = score_unit(size, -up);
 #pragma unroll 1
-        for (int b = 0; b < NB; ++b) {
-            float v[32];
+        for (int b = 0; b < NB; b += 2) {
+            float v[2][32];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+            for (int i = 0; i < 64; i += 8) {
                 float u[8];
                 load8(a, q_at + b * 32 + i, p.q_wide, u);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[i + k] = u[k] * f;
+                for (int k = 0; k < 8; ++k) v[i >> 5][(i & 31) + k] = u[k];
             }
-            uint32_t cols[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {  // values d and d + 2 stand side by side
-                const int d = ((i >> 2) << 2) + ((i >> 1) & 1) + ((i & 1) << 4);
-                cols[i] = pack_rn(v[d], v[d + 2]);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t cols[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {  // values d and d + 2 stand side by side
+                    const int d = ((i >> 2) << 2) + ((i >> 1) & 1) + ((i & 1) << 4);
+                    cols[i] = pack_rn(v[h][d] * f, v[h][d + 2] * f);
+                }
+                tmem_st_16cols(tmem + lanes + T::q_col + qt * (D / 2) + (b + h) * 16, cols);
             }
-            tmem_st_16cols(tmem + lanes + T::q_col + qt * (D / 2) + b * 16, cols);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -722,16 +746,25 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sh.tmem);
 
     if (warp < T::softmax_warps) {
+        registers_up<T::softmax_regs>();
         softmax_role<D>(p, sh, tmem, warp, lane);
     } else if (warp < T::mma_warp) {
+        registers_down<T::dequant_regs>();
         dequant_role<D>(p, sh, smem, warp - T::softmax_warps, lane);
     } else {
-        if (lane == 0) mma_role<D>(p, sh, smem_addr(smem), tmem);
+        registers_down<T::mma_regs>();
+        if (warp == T::mma_warp && lane == 0) mma_role<D>(p, sh, smem_addr(smem), tmem);
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // back to equal shares, after the barrier only: a role that ended early
+    // would take the registers that the softmax still waits for
+    if (warp < T::softmax_warps)
+        registers_down<T::launch_regs>();
+    else
+        registers_up<T::launch_regs>();
     if (warp == T::mma_warp) tmem_dealloc_cta(tmem, T::tmem_cols);
 #pragma unroll 1
     for (int w = 0; w < T::softmax_warps; ++w)
