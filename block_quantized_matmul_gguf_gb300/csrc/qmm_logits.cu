@@ -2,12 +2,13 @@
 // the logits of a batch (include/qmm.h, qmm_logits_adjust).
 //
 // One launch, no workspace: a CTA owns a slice of one row's vocabulary, keeps
-// that slice's token counts (and bias sums) in shared memory, reads the row's
-// whole history and counts the ids that fall into its slice, then passes its
-// logits through once.  The counts are integers, so the order of the shared
-// atomics does not matter; bias entries are added by one warp in list order.
-// Bound by HBM (8 bytes a logit); the histories are read once per slice, from
-// L2, so rows with long histories get larger slices.
+// a word per logit of it in shared memory (times generated, and whether the
+// prompt or the bias list names it), reads the row's whole history and counts
+// the ids that fall into its slice, then passes its logits through once, of
+// which only the marked ones take more than a mask.  The counts are integers,
+// so the order of the shared atomics does not matter; bias entries are added
+// in list order.  Bound by HBM (8 bytes a logit); the histories
+// are read once per slice, from L2.
 #include "qmm_internal.h"
 
 #include <algorithm>
@@ -16,8 +17,8 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 8;  // history entries a thread has under way
-constexpr uint32_t kInPrompt = 0x80000000u;  // the other bits count what was generated
+constexpr int kAhead = 8;  // list entries a thread has under way
+constexpr uint32_t kInPrompt = 0x80000000u, kBiased = 0x40000000u;  // the other bits count what was generated
 
 __device__ __forceinline__ int32_t bounded(int32_t v, int64_t len, bool &bad) {
     const int64_t w = min(max(static_cast<int64_t>(v), int64_t(0)), len);
@@ -25,149 +26,195 @@ __device__ __forceinline__ int32_t bounded(int32_t v, int64_t len, bool &bad) {
     return static_cast<int32_t>(w);
 }
 
-// Q float4 per thread: the slice is Q * 1024 logits.
+// What a CTA keeps of the bias list: the entries of its slice, in list order.
+// Beyond kBiasKept of them the marked logits read the list itself.
+struct BiasEntry {
+    int32_t id;
+    float value;
+};
+constexpr int kBiasKept = 512;
+
+// Sum of the entries for id, in their order.
+__device__ __forceinline__ float bias_of(const LogitsArgs &a, const BiasEntry *kept, int n, int32_t b0, int32_t b1,
+                                         int32_t id) {
+    float v = 0.0f;
+    if (n <= kBiasKept) {
+        for (int i = 0; i < n; ++i)
+            if (kept[i].id == id) v += kept[i].value;
+    } else {
+        for (int32_t i = b0; i < b1; ++i)
+            if (a.bias_ids[i] == id) v += a.bias_values[i];
+    }
+    return v;
+}
+
+// Q float4 per thread: the slice is Q * 1024 logits.  All of them pass through
+// at once, with the mask alone; the marked ones are written again when the
+// lists have been read, which nothing of the stream then waits for.
 template <int Q>
-__global__ void __launch_bounds__(kThreads) logits_kernel(LogitsArgs a, LaunchCtx ctx) {
+__global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant__ LogitsArgs a, LaunchCtx ctx) {
     constexpr int S = Q * 4 * kThreads;
-    extern __shared__ uint32_t seen[];                       // [S] if there is a history
-    float *bias = reinterpret_cast<float *>(seen + (a.history ? S : 0));  // [S] if there is a bias
-    const int64_t row = blockIdx.y;
+    __shared__ __align__(16) uint32_t seen[S];
+    __shared__ uint16_t marked[S];  // places of the marked logits, in any order
+    __shared__ BiasEntry kept[kBiasKept];
+    __shared__ int kept_n, marked_n;
+    // all rows' first slices first: low ids are common, and the slices that
+    // hold many of a history's take longest
+    const int slice = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.rows));
+    const int64_t row = blockIdx.x - static_cast<unsigned>(slice) * static_cast<unsigned>(a.rows);
     const float *in = a.logits + row * a.logits_stride;
     float *out = a.out + row * a.out_stride;
     // The slices are cut at 16-byte boundaries of the input: place e of the
     // row is index e + pad.
-    const int pad = static_cast<int>((reinterpret_cast<uintptr_t>(in) >> 2) & 3);
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * S - pad;  // the slice's first place
-    if (base >= a.vocab) return;
-    const bool wide_out = ((reinterpret_cast<uintptr_t>(out) >> 2) & 3) == pad;
+    const int pad = static_cast<int>((reinterpret_cast<uintptr_t>(in) >> 2) & 3), vocab = static_cast<int>(a.vocab);
+    const int base = slice * S - pad;  // the slice's first place
+    if (base >= vocab) return;
+    const bool wide_out = static_cast<int>((reinterpret_cast<uintptr_t>(out) >> 2) & 3) == pad;
+    const bool whole = base >= 0 && base + S <= vocab;
+    const int e0 = base + static_cast<int>(threadIdx.x) * 4;  // the thread's first place; then every 4 kThreads
+    const float ninf = __uint_as_float(0xFF800000u);
 
     pdl_wait();
     pdl_launch_dependents();
-    float4 x[Q];
+    // the lists' ends, under way before the stream's loads
+    bool bad = false;
+    int32_t h0 = 0, h1 = 0, b0 = 0, b1 = 0;
+    int64_t made = 0;
+    if (a.history) {
+        h0 = bounded(a.hist_start[row], a.history_len, bad);
+        h1 = bounded(a.hist_start[row + 1], a.history_len, bad);
+        made = h0 + static_cast<int64_t>(a.prompt_len ? max(a.prompt_len[row], 0) : 0);
+    }
+    if (a.bias_ids) {
+        b0 = bounded(a.bias_start[row], a.bias_len, bad);
+        b1 = bounded(a.bias_start[row + 1], a.bias_len, bad);
+    }
+    const uint32_t *allowed = a.allowed ? a.allowed + row * ((a.vocab + 31) / 32) : nullptr;
+    if (whole) {
+        float4 x[Q];
+        uint32_t bits[Q];  // of four logits each
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-        const int64_t e = base + (i * kThreads + threadIdx.x) * 4;
-        if (e >= 0 && e + 4 <= a.vocab) {
-            x[i] = *reinterpret_cast<const float4 *>(in + e);
-        } else {
-            x[i].x = e >= 0 && e < a.vocab ? in[e] : 0.0f;
-            x[i].y = e + 1 >= 0 && e + 1 < a.vocab ? in[e + 1] : 0.0f;
-            x[i].z = e + 2 >= 0 && e + 2 < a.vocab ? in[e + 2] : 0.0f;
-            x[i].w = e + 3 >= 0 && e + 3 < a.vocab ? in[e + 3] : 0.0f;
+        for (int i = 0; i < Q; ++i) x[i] = reinterpret_cast<const float4 *>(in + e0)[i * kThreads];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            bits[i] = 15u;
+            if (allowed) {
+                const int e = e0 + i * 4 * kThreads;
+                const uint32_t w = allowed[e >> 5];
+                bits[i] = __funnelshift_r(w, pad ? allowed[(e + 3) >> 5] : w, e & 31);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            float4 y = x[i];
+            if (!(bits[i] & 1u)) y.x = ninf;
+            if (!(bits[i] & 2u)) y.y = ninf;
+            if (!(bits[i] & 4u)) y.z = ninf;
+            if (!(bits[i] & 8u)) y.w = ninf;
+            if (wide_out) {
+                __stcs(reinterpret_cast<float4 *>(out + e0) + i * kThreads, y);
+            } else {
+                float *to = out + e0 + i * 4 * kThreads;
+                to[0] = y.x, to[1] = y.y, to[2] = y.z, to[3] = y.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int e = e0 + i * 4 * kThreads + t;
+                if (e >= 0 && e < vocab)
+                    out[e] = !allowed || ((allowed[e >> 5] >> (e & 31)) & 1u) ? in[e] : ninf;
+            }
         }
     }
-    const int used = (a.history ? S : 0) + (a.bias_ids ? S : 0);
-    for (int i = threadIdx.x * 4; i < used; i += kThreads * 4)
-        *reinterpret_cast<uint4 *>(seen + i) = make_uint4(0u, 0u, 0u, 0u);
+    if (!a.history && !a.bias_ids) return;
+
+    // ids of the slice: first .. first + count - 1, the first at place `shift`
+    const int first = max(base, 0), shift = first - base;
+    const uint32_t count = static_cast<uint32_t>(min(base + S, vocab) - first);
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+        *reinterpret_cast<uint4 *>(seen + (i * kThreads + threadIdx.x) * 4) = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x == 0) {
+        marked_n = 0;
+        if (bad) record_error(ctx, kDevErrIndex);
+    }
+    int32_t id[kAhead];
+    auto load_ids = [&](const int32_t *list, int64_t from, int32_t end, int step, int lane) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t i = from + u * step + lane;
+            id[u] = i < end ? list[i] : -1;
+        }
+    };
+    // the last warp reads the bias list, the others the history
+    const int readers = a.bias_ids ? kThreads - 32 : kThreads, lane = threadIdx.x & 31;
+    const bool bias_warp = static_cast<int>(threadIdx.x) >= readers;
+    if (bias_warp)
+        load_ids(a.bias_ids, b0, b1, 32, lane);
+    else
+        load_ids(a.history, h0, h1, readers, threadIdx.x);
+    auto mark = [&](uint32_t e, uint32_t old) {  // the first mark of a logit lists it
+        if (!old) marked[atomicAdd(&marked_n, 1)] = static_cast<uint16_t>(e);
+    };
     __syncthreads();
-    bool bad = false;
-    if (a.history) {
-        const int32_t h0 = bounded(a.hist_start[row], a.history_len, bad);
-        const int32_t h1 = bounded(a.hist_start[row + 1], a.history_len, bad);
-        const int64_t made = h0 + static_cast<int64_t>(a.prompt_len ? max(a.prompt_len[row], 0) : 0);
-        const int first = static_cast<int>(max(base, int64_t(0))), count = static_cast<int>(min(base + S, a.vocab)) - first;
-        const int shift = static_cast<int>(first - base);
-        for (int64_t h = h0; h < h1; h += kThreads * kAhead) {
-            int32_t id[kAhead];
+    if (bias_warp) {
+        int n = 0;
+        for (int64_t b = b0; b < b1; b += 32 * kAhead) {
+            if (b > b0) load_ids(a.bias_ids, b, b1, 32, lane);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const int64_t i = h + u * kThreads + threadIdx.x;
-                id[u] = i < h1 ? a.history[i] : -1;
+                const uint32_t e = static_cast<uint32_t>(id[u] - first);
+                const bool here = id[u] >= 0 && e < count;
+                const unsigned all = __ballot_sync(0xFFFFFFFFu, here);
+                const int at = n + __popc(all & ((1u << lane) - 1u));
+                if (here) {
+                    mark(shift + e, atomicOr(seen + shift + e, kBiased));
+                    if (at < kBiasKept) kept[at] = BiasEntry{id[u], a.bias_values[b + u * 32 + lane]};
+                }
+                n += __popc(all);
             }
+        }
+        if (lane == 0) kept_n = n;
+    } else {
+        for (int64_t h = h0; h < h1; h += static_cast<int64_t>(readers) * kAhead) {
+            if (h > h0) load_ids(a.history, h, h1, readers, threadIdx.x);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const uint32_t e = static_cast<uint32_t>(id[u]) - static_cast<uint32_t>(first);
-                if (e < static_cast<uint32_t>(count)) {  // also false for ids below 0
-                    if (h + u * kThreads + threadIdx.x < made)
-                        atomicOr(seen + shift + e, kInPrompt);
-                    else
-                        atomicAdd(seen + shift + e, 1u);
+                const uint32_t e = static_cast<uint32_t>(id[u] - first);  // ids below 0 lie far off
+                if (id[u] >= 0 && e < count) {
+                    const bool late = h + u * readers + threadIdx.x >= made;
+                    mark(shift + e, late ? atomicAdd(seen + shift + e, 1u) : atomicOr(seen + shift + e, kInPrompt));
                 }
             }
         }
     }
-    if (a.bias_ids && threadIdx.x < 32) {
-        const int32_t b0 = bounded(a.bias_start[row], a.bias_len, bad);
-        const int32_t b1 = bounded(a.bias_start[row + 1], a.bias_len, bad);
-        for (int64_t b = b0; b < b1; b += 32) {
-            const int64_t i = b + threadIdx.x;
-            int64_t e = -1;
-            float v = 0.0f;
-            if (i < b1) {
-                const int64_t id = a.bias_ids[i];
-                if (id >= 0 && id < a.vocab && id >= base && id < base + S) e = id - base;
-                v = a.bias_values[i];
-            }
-            // in list order: the entries of one id one after another
-            unsigned todo = __ballot_sync(0xFFFFFFFFu, e >= 0);
-            while (todo) {
-                const int from = __ffs(todo) - 1;
-                if (static_cast<int>(threadIdx.x) == from) bias[e] += v;
-                __syncwarp();
-                todo &= todo - 1;
-            }
-        }
-    }
-    if (bad && threadIdx.x == 0) record_error(ctx, kDevErrIndex);
-    __syncthreads();
     const float rep = a.repetition ? a.repetition[row] : 1.0f;
     const float freq = a.frequency ? a.frequency[row] : 0.0f;
     const float pres = a.presence ? a.presence[row] : 0.0f;
-    const uint32_t *allowed = a.allowed ? a.allowed + row * ((a.vocab + 31) / 32) : nullptr;
-#pragma unroll
-    for (int i = 0; i < Q; ++i) {
-        const int at = (i * kThreads + threadIdx.x) * 4;
-        const int64_t e = base + at;
-        float y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        if (a.history) {
-            const uint4 s4 = *reinterpret_cast<const uint4 *>(seen + at);
-            const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (s[t]) {  // few logits were seen
-                    if (a.repetition) y[t] = y[t] > 0.0f ? __fdiv_rn(y[t], rep) : y[t] * rep;
-                    const uint32_t c = s[t] & ~kInPrompt;
-                    y[t] -= __fmul_rn(static_cast<float>(c), freq) + (c ? pres : 0.0f);
-                }
-            }
+    __syncthreads();
+    for (int i = threadIdx.x; i < marked_n; i += kThreads) {
+        const int at = marked[i], e = base + at;
+        if (allowed && !((allowed[e >> 5] >> (e & 31)) & 1u)) continue;  // masked for good
+        const uint32_t mark = seen[at], n = mark & ~(kInPrompt | kBiased);
+        float y = in[e];  // in place: its own value still, as the mask left it alone
+        if (n || (mark & kInPrompt)) {
+            if (a.repetition) y = y > 0.0f ? __fdiv_rn(y, rep) : y * rep;
+            y -= __fmul_rn(static_cast<float>(n), freq) + (n ? pres : 0.0f);
         }
-        if (a.bias_ids) {
-            const float4 b = *reinterpret_cast<const float4 *>(bias + at);
-            y[0] += b.x;
-            y[1] += b.y;
-            y[2] += b.z;
-            y[3] += b.w;
-        }
-        if (allowed) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int64_t f = e + t;
-                if (f >= 0 && f < a.vocab && !((allowed[f >> 5] >> (f & 31)) & 1u))
-                    y[t] = __uint_as_float(0xFF800000u);
-            }
-        }
-        if (wide_out && e >= 0 && e + 4 <= a.vocab) {
-            *reinterpret_cast<float4 *>(out + e) = make_float4(y[0], y[1], y[2], y[3]);
-        } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                if (e + t >= 0 && e + t < a.vocab) out[e + t] = y[t];
-        }
+        if (mark & kBiased) y += bias_of(a, kept, kept_n, b0, b1, e);
+        out[e] = y;
     }
 }
 
 template <int Q>
 cudaError_t launch_slices(const LogitsArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
     constexpr int S = Q * 4 * kThreads;
-    static int limits[kMaxDevices];
-    const size_t smem = sizeof(uint32_t) * S * ((a.history ? 1 : 0) + (a.bias_ids ? 1 : 0));
-    if (smem > 48 * 1024) {
-        const cudaError_t e = ensure_smem(logits_kernel<Q>, smem, false, limits);
-        if (e != cudaSuccess) return e;
-    }
     const unsigned slices = static_cast<unsigned>((a.vocab + 3 + S - 1) / S);  // + 3: the padding
-    return launch_kernel(logits_kernel<Q>, dim3(slices, static_cast<unsigned>(a.rows)), dim3(kThreads),
-                         smem, stream, 1, a, ctx);
+    return launch_kernel(logits_kernel<Q>, dim3(slices * static_cast<unsigned>(a.rows)), dim3(kThreads), 0, stream, 1, a,
+                         ctx);
 }
 
 }  // namespace
@@ -176,7 +223,7 @@ cudaError_t launch_logits_adjust(const LogitsArgs &a, cudaStream_t stream, const
     // Long slices read each history fewer times; short ones spread a few
     // rows over the whole GPU.
     const int64_t wide = a.rows * ((a.vocab + 8191) / 8192);
-    if (wide >= 2 * device_sm_count()) return launch_slices<8>(a, stream, ctx);
+    if (wide >= 2 * device_sm_count()) return launch_slices<4>(a, stream, ctx);
     return launch_slices<2>(a, stream, ctx);
 }
 
