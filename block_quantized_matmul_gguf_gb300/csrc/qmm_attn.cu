@@ -9,9 +9,11 @@
 // leave them: K's multiply fp32 block sums, V's join the softmax weights.
 // The integers are exact in binary16, therefore the products run on
 // mma.sync m16n8k16 with the cache as the 16-row operand, taken from the
-// 4-bit codes in registers: a code masked in place is a subnormal binary16
-// number (n * 2^-24, or 16 n * 2^-24 for the upper of two), the powers of
-// two are folded into q or undone at the end.  tcgen05 would need those
+// 4-bit codes in registers.  For bf16 outputs a code masked in place is a
+// subnormal binary16 number (n * 2^-24, or 16 n * 2^-24 for the upper of two),
+// the powers of two being folded into q or undone at the end; fp32 outputs
+// take two more instructions for normal numbers, because the tensor cores'
+// sums of subnormal operands keep some 18 bits (6e-6 of the output, measured).  tcgen05 would need those
 // operands written out to shared or tensor memory first, 3.6 times the bytes
 // of the codes, for 8 columns that it cannot fill.
 //
@@ -59,8 +61,8 @@ struct Layout {
     // the rest, from its own start
     static constexpr int v_scales = scales;
     static constexpr int q = v_scales + scales;          // B fragments [NT][NB][32 lanes] x 16 bytes
-    static constexpr int bias = q + NT * NB * 512;       // -8 sum q [NT][NB][4 lanes] x {c0, c1, c0, c1}
-    static constexpr int d = bias + NT * NB * 64;        // V's scales by block: pairs of keys, binary16 or fp32
+    static constexpr int bias = q + NT * NB * 512;       // -8 sum q [NT][NB][4 lanes] x {c0, c1, c0, c1}, bf16 only
+    static constexpr int d = bias + (EXACT ? 0 : NT * NB * 64);        // V's scales by block: pairs of keys, binary16 or fp32
     static constexpr int p = d + NB * kTile * (EXACT ? 4 : 2);  // weights [rows][p_stride], EXACT only
     static constexpr int rest_bytes = p + (EXACT ? rows * p_stride * 4 : 0);
     // CTAs on an SM: as the registers of the accumulators allow
@@ -128,6 +130,7 @@ struct StreamParams {
     const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
     int num_pages, page_shift, kv_heads;
     bool q_pairs;         // rows of q are aligned to two values
+    uint32_t magic;       // 1024, 1024 in binary16: a register where a constant would cost an instruction
     float *warp_records;  // [CTAs * kWarps]: head parts that are not the last
     float *cta_records;   // [CTAs][2]: head and tail part
     CtaParts *parts;      // [CTAs]
@@ -414,13 +417,11 @@ __device__ __forceinline__ void stage_zero(WarpState<D, NT, EXACT> &w, Part &par
     constexpr int NB = L::NB;
     const int nt = row / (L::rows / NT), in = row % (L::rows / NT), cols = EXACT ? 2 : 1;
     uint4 *frag = reinterpret_cast<uint4 *>(w.rest + L::q) + nt * NB * 32 + in * cols * 4;
-    float *bias = reinterpret_cast<float *>(w.rest + L::bias) + nt * NB * 16;
     for (int i = w.lane; i < NB * cols * 4; i += 32)
         frag[i / (cols * 4) * 32 + i % (cols * 4)] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = w.lane; i < NB * cols; i += 32) {
-        const int col = in * cols + i % cols;
-        float *b8 = bias + i / cols * 16 + (col >> 1) * 4 + (col & 1);
-        b8[0] = b8[2] = 0.0f;
+    if constexpr (!EXACT) {
+        float *bias = reinterpret_cast<float *>(w.rest + L::bias) + nt * NB * 16 + (in >> 1) * 4 + (in & 1);
+        for (int i = w.lane; i < NB; i += 32) bias[i * 16] = bias[i * 16 + 2] = 0.0f;
     }
     if (w.lane == 0) {
         part.row_lo[row] = part.row_lo[0];
@@ -457,13 +458,13 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
         }
         const float big = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, bits));
         const int up = query_raise(big, size);
-        const float f = pow2i(up), unit = score_unit(size, 24 - up);
+        const float f = pow2i(up), unit = score_unit(size, (EXACT ? 0 : 24) - up);
         const int nt = row / (L::rows / NT), in = row % (L::rows / NT);
-        float s_hi = 0.0f, s_lo = 0.0f;
+        float s_hi = 0.0f;
         // value d of a block: lane (d & 15) / 4 of the column, register
         // (d & 1) * 2 + d / 16, half (d / 2) & 1; a lane's values share d / 16
         const int high = (d0 >> 4) & 1;
-        const float f16 = f * (high ? 0.0625f : 1.0f), back = high ? 16.0f : 1.0f;
+        const float f16 = f * (!EXACT && high ? 0.0625f : 1.0f), back = high ? 16.0f : 1.0f;
         float one[E], two[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) {
@@ -471,7 +472,6 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
             one[i] = __half2float(EXACT ? __float2half_rz(x) : __float2half_rn(x));
             two[i] = EXACT ? __half2float(__float2half_rn(x - one[i])) : 0.0f;
             s_hi += one[i] * back;
-            s_lo += two[i] * back;
         }
         uint32_t *to = frag + ((nt * NB + block) * 32 + (EXACT ? in * 2 : in) * 4) * 4;
         if constexpr (E >= 4) {
@@ -494,20 +494,14 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
                 at[36] = __float2half_rn(two[1]);
             }
         }
+        if constexpr (!EXACT) {
 #pragma unroll
-        for (int o = 1; o < 32 / E; o <<= 1) {
-            s_hi += __shfl_xor_sync(0xFFFFFFFFu, s_hi, o);
-            if constexpr (EXACT) s_lo += __shfl_xor_sync(0xFFFFFFFFu, s_lo, o);
+            for (int o = 1; o < 32 / E; o <<= 1) s_hi += __shfl_xor_sync(0xFFFFFFFFu, s_hi, o);
         }
-        if (w.lane % (32 / E) == 0) {
+        if (!EXACT && w.lane % (32 / E) == 0) {
             const float m8 = -8.0f / 16777216.0f;
-            float *b8 = bias + (nt * NB + block) * 16;
-            if constexpr (EXACT) {
-                b8[in * 4] = b8[in * 4 + 2] = s_hi * m8;
-                b8[in * 4 + 1] = b8[in * 4 + 3] = s_lo * m8;
-            } else {
-                b8[(in >> 1) * 4 + (in & 1)] = b8[(in >> 1) * 4 + 2 + (in & 1)] = s_hi * m8;
-            }
+            float *b8 = bias + (nt * NB + block) * 16 + (in >> 1) * 4 + (in & 1);
+            b8[0] = b8[2] = s_hi * m8;
         }
         if (w.lane == 0) {
             part.row_lo[row] = first_key(a, pos[row]);
@@ -521,6 +515,17 @@ __device__ __forceinline__ void stage_q(const StreamParams &p, WarpState<D, NT, 
                 if (n == nt && (EXACT ? w.t : w.t * 2 + k) == in) w.unit[n][k] = unit;
     }
     __syncwarp();
+}
+
+// n - 8 of the lower and of the upper codes of a word as binary16 pairs.
+// fp32 output: normal numbers, by way of 1024 + n.  A subnormal operand is
+// summed with the exponent of the smallest normal number, and loses the ten
+// bits between from the fp32 sums' low end.
+__device__ __forceinline__ uint32_t lower8(uint32_t x, uint32_t magic) {
+    return hadd2((x & 0x000F000Fu) | magic, 0xE408E408u);  // - 1032
+}
+__device__ __forceinline__ uint32_t upper8(uint32_t x, uint32_t magic) {
+    return hfma2((x & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
 }
 
 // NB binary16 scales of one key.
@@ -539,7 +544,8 @@ __device__ __forceinline__ void load_scales(const uint16_t *row, uint32_t (&d)[N
 
 // Sums of the tile before their unit: s[nt][mt][row of pair][key g, g + 8].
 template <int D, int NT, bool EXACT>
-__device__ __forceinline__ void tile_scores(WarpState<D, NT, EXACT> &w, float (&s)[NT][4][WarpState<D, NT, EXACT>::R][2]) {
+__device__ __forceinline__ void tile_scores(WarpState<D, NT, EXACT> &w, uint32_t magic,
+                                            float (&s)[NT][4][WarpState<D, NT, EXACT>::R][2]) {
     using L = Layout<D, NT, EXACT>;
     constexpr int NB = L::NB;
     const uint4 *frag = reinterpret_cast<const uint4 *>(w.rest + L::q) + w.lane;
@@ -563,20 +569,29 @@ __device__ __forceinline__ void tile_scores(WarpState<D, NT, EXACT> &w, float (&
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 q[n] = frag[(n * NB + b) * 32];
-                c8[n] = bias[(n * NB + b) * 4];
+                if constexpr (!EXACT) c8[n] = bias[(n * NB + b) * 4];
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const uint32_t x = c[2 * m], y = c[2 * m + 1], x8 = x >> 8, y8 = y >> 8;
+                uint32_t k1[4], k2[4];  // A operands: the values of the first and of the second product
+                if constexpr (EXACT) {
+                    k1[0] = lower8(x, magic), k1[1] = lower8(y, magic), k1[2] = upper8(x, magic), k1[3] = upper8(y, magic);
+                    k2[0] = lower8(x8, magic), k2[1] = lower8(y8, magic), k2[2] = upper8(x8, magic), k2[3] = upper8(y8, magic);
+                } else {
+                    k1[0] = x & 0x000F000Fu, k1[1] = y & 0x000F000Fu, k1[2] = x & 0x00F000F0u, k1[3] = y & 0x00F000F0u;
+                    k2[0] = x8 & 0x000F000Fu, k2[1] = y8 & 0x000F000Fu, k2[2] = x8 & 0x00F000F0u, k2[3] = y8 & 0x00F000F0u;
+                }
                 const uint32_t dx = d[2 * m][b / 2], dy = d[2 * m + 1][b / 2];
                 const float df = b & 1 ? high_float(dx) : low_float(dx), dg = b & 1 ? high_float(dy) : low_float(dy);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float z[4];
-                    mma16816(z, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u, q[n].x, q[n].y,
-                             c8[n].x, c8[n].y, c8[n].z, c8[n].w);
-                    mma16816(z, x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u, y8 & 0x00F000F0u, q[n].z,
-                             q[n].w, z[0], z[1], z[2], z[3]);
+                    if constexpr (EXACT)
+                        mma16816(z, k1[0], k1[1], k1[2], k1[3], q[n].x, q[n].y, 0.0f, 0.0f, 0.0f, 0.0f);
+                    else
+                        mma16816(z, k1[0], k1[1], k1[2], k1[3], q[n].x, q[n].y, c8[n].x, c8[n].y, c8[n].z, c8[n].w);
+                    mma16816(z, k2[0], k2[1], k2[2], k2[3], q[n].z, q[n].w, z[0], z[1], z[2], z[3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         acc[n][m][i] = b ? fmaf(i < 2 ? df : dg, z[i], acc[n][m][i]) : (i < 2 ? df : dg) * z[i];
@@ -656,7 +671,7 @@ __device__ __forceinline__ float minus_part(float x, uint32_t keep) {
 // EDGE: some row does not see some key of the tile, whose scale may then be
 // anything.
 template <int D, int NT, bool EXACT, bool EDGE>
-__device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const uint32_t (&pw)[NT][4][2],
+__device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, uint32_t magic, const uint32_t (&pw)[NT][4][2],
                                             const float (&f)[NT][WarpState<D, NT, EXACT>::R],
                                             const float (&g)[NT][WarpState<D, NT, EXACT>::R]) {
     using L = Layout<D, NT, EXACT>;
@@ -682,14 +697,20 @@ __device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, const ui
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t x = c[2 * h], y = c[2 * h + 1], x8 = x >> 8, y8 = y >> 8;
-                // n - 8 (lower codes) and 16 (n - 8) (upper codes), times 2^-24;
-                // -8 times the sum of the weights as a product of its own would
-                // take fewer instructions, but a heavy key's code 8 must leave
-                // exactly nothing
-                const uint32_t xa = hadd2(x & 0x000F000Fu, kMinus8), ya = hadd2(y & 0x000F000Fu, kMinus8);
-                const uint32_t xb = hadd2(x & 0x00F000F0u, kMinus128), yb = hadd2(y & 0x00F000F0u, kMinus128);
-                const uint32_t xc = hadd2(x8 & 0x000F000Fu, kMinus8), yc = hadd2(y8 & 0x000F000Fu, kMinus8);
-                const uint32_t xd = hadd2(x8 & 0x00F000F0u, kMinus128), yd = hadd2(y8 & 0x00F000F0u, kMinus128);
+                // bf16 output: n - 8 (lower codes) and 16 (n - 8) (upper codes), times
+                // 2^-24.  -8 times the sum of the weights as a product of its own
+                // would take fewer instructions, but a heavy key's code 8 must
+                // leave exactly nothing.
+                uint32_t xa, ya, xb, yb, xc, yc, xd, yd;
+                if constexpr (EXACT) {
+                    xa = lower8(x, magic), ya = lower8(y, magic), xc = lower8(x8, magic), yc = lower8(y8, magic);
+                    xb = upper8(x, magic), yb = upper8(y, magic), xd = upper8(x8, magic), yd = upper8(y8, magic);
+                } else {
+                    xa = hadd2(x & 0x000F000Fu, kMinus8), ya = hadd2(y & 0x000F000Fu, kMinus8);
+                    xb = hadd2(x & 0x00F000F0u, kMinus128), yb = hadd2(y & 0x00F000F0u, kMinus128);
+                    xc = hadd2(x8 & 0x000F000Fu, kMinus8), yc = hadd2(y8 & 0x000F000Fu, kMinus8);
+                    xd = hadd2(x8 & 0x00F000F0u, kMinus128), yd = hadd2(y8 & 0x00F000F0u, kMinus128);
+                }
                 uint32_t b0[NT], b1[NT];
                 if constexpr (EXACT) {
                     const float4 d = *reinterpret_cast<const float4 *>(
@@ -833,7 +854,7 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
 
         copies_wait();  // K is there; V may be under way
         float s[NT][4][R][2];
-        tile_scores<D, NT, EXACT>(w, s);
+        tile_scores<D, NT, EXACT>(w, p.magic, s);
         __syncwarp();
         if (key0 + kTile < end) {
             ahead(key0 + kTile);
@@ -882,12 +903,13 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
         copies_wait();  // V is there; the next K may be under way
         const int e_max = tile_scales<D, NT, EXACT>(w, seen);
         // f: factor of what is there already; g: of this tile's products.  The
-        // products carry 2^-24 of the codes and the scales' factor (fp32:
-        // 2^(14 - e_max); binary16: 2^-e_max and 2^14 of the weights).
+        // products carry the scales' factor 2^(14 - e_max) (bf16 output:
+        // 2^-e_max, and 2^14 of the weights) and, for bf16 output, 2^-24 of the
+        // codes.
         float f[NT][R], g[NT][R];
         float *pp = reinterpret_cast<float *>(w.rest + L::p) + (w.g >> 1) * 4 + (w.g & 1);
         uint32_t pw[NT][4][2];
-        const float unit_out = pow2i(10 + e_max);
+        const float unit_out = pow2i((EXACT ? -14 : 10) + e_max);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -957,7 +979,7 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
                     const float e = v * raise;
                     return e >= kLow && e < kFull ? e : 0.0f;
                 });
-                tile_values<D, NT, EXACT, true>(w, pw, f, low);
+                tile_values<D, NT, EXACT, true>(w, p.magic, pw, f, low);
                 __syncwarp();
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -970,9 +992,9 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
             hand_over([](float e) { return e; });
         }
         if (edge)
-            tile_values<D, NT, EXACT, true>(w, pw, f, g);
+            tile_values<D, NT, EXACT, true>(w, p.magic, pw, f, g);
         else
-            tile_values<D, NT, EXACT, false>(w, pw, f, g);
+            tile_values<D, NT, EXACT, false>(w, p.magic, pw, f, g);
         __syncwarp();
         if (key0 + kTile < end) fetch_v(key0 + kTile);
     }
@@ -1006,7 +1028,7 @@ __device__ __forceinline__ void each_output(const WarpState<D, NT, EXACT> &w, in
                     for (int h = 0; h < 2; ++h) {
                         const float2 o = w.out[n][b][m][h];
                         const float v = EXACT ? o.x + o.y : k ? o.y : o.x;
-                        put(32 * b + 16 * h + 2 * w.g + m, v * (h ? 0.0625f : 1.0f));
+                        put(32 * b + 16 * h + 2 * w.g + m, v * (!EXACT && h ? 0.0625f : 1.0f));
                     }
         }
 }
@@ -1348,6 +1370,7 @@ cudaError_t launch_stream(const KvCache &c, const AttnArgs &a, cudaStream_t stre
     p.page_shift = c.page_shift;
     p.kv_heads = c.kv_heads;
     p.q_pairs = a.q_stride % 2 == 0 && reinterpret_cast<uintptr_t>(a.q) % (a.q_bf16 ? 4 : 8) == 0;
+    p.magic = 0x64006400u;
     p.warp_records = static_cast<float *>(a.workspace);
     p.cta_records = p.warp_records + static_cast<size_t>(ctas) * kWarps * kRecord;
     p.parts = reinterpret_cast<CtaParts *>(p.cta_records + static_cast<size_t>(ctas) * 2 * kRecord);
