@@ -21,8 +21,8 @@
 // 19 and so on); Q is staged in that order and the outputs are put back.
 //
 // Precision: q, (n - 8) d and the weights are rounded once to binary16 each.
-// A tile's K and V are scaled by powers of two to below 16, q per row to
-// below 2^15 and the weights to at most 2^15, so that nothing overflows; weights
+// A tile's K and V are scaled by powers of two to below 2^-6 (16 where its
+// scales lie far apart), q per row to below 2^15 and the weights to at most 2^15, so that nothing overflows; weights
 // below 2^-38 of a row's largest fall out of binary16's range, which shows
 // only where the heavy keys' codes leave (nearly) nothing: such rows are done
 // again by all warps in fp32.
@@ -71,6 +71,7 @@ struct Tile {
 
 struct TileInfo {
     int k_exp, v_exp;      // K and V of the tile are scaled by 2^-exp
+    int far;               // V's values may reach 16, not 2^-6
     uint32_t lost;         // 16-key groups without a page
     uint32_t odd[2];       // keys whose V holds a NaN or an infinity
 };
@@ -87,7 +88,7 @@ struct TileShared {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
     uint64_t s_full[2], p_full[2], pv_done[2], q_ready, final;
     TileInfo info[kRing];
-    int exps[2][2][kDequantWarps];  // [tile parity][K, V][warp]
+    alignas(16) uint32_t exps[2][2][kDequantWarps];  // [tile parity][K, V][warp]
     int64_t scratch[32];
     Block block;
     uint32_t tmem;
@@ -201,13 +202,31 @@ __device__ __forceinline__ void find_block(const TileParams &p, TileShared &sh) 
 
 // ---- dequantisation ----------------------------------------------------------------
 
-// The 16 bytes of one block to 32 binary16 values times the pair d2, in the
-// words' own order, as four 16-byte chunks.
-__device__ __forceinline__ void dequant_block(const uint4 &codes, uint32_t d2, uint4 (&out)[4]) {
+// The 16 bytes of one block to 32 binary16 values in the words' own order, as
+// four 16-byte chunks; d below 2.
+// near: (n - 8) d 2^-kNear.  A code masked in place is the subnormal number
+// n 2^-24 (16 n 2^-24 for the upper codes), and one multiply-add with exact
+// constants gives the value, rounded once.
+__device__ __forceinline__ void dequant_near(const uint4 &codes, float d, uint4 (&out)[4]) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    const uint32_t magic = 0x64006400u;                      // 1024, 1024
-    const uint32_t minus = 0xE408E408u;                      // -1032
+    const uint32_t low = pack_rn(d * 16384.0f, d * 16384.0f), high = pack_rn(d * 1024.0f, d * 1024.0f);
+    const uint32_t minus = pack_rn(d * -0.0078125f, d * -0.0078125f);  // -8 2^-10
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = w[i], x8 = x >> 8;
+        out[i].x = hfma2(x & 0x000F000Fu, low, minus);
+        out[i].y = hfma2(x & 0x00F000F0u, high, minus);
+        out[i].z = hfma2(x8 & 0x000F000Fu, low, minus);
+        out[i].w = hfma2(x8 & 0x00F000F0u, high, minus);
+    }
+}
+// far: (n - 8) d, by way of 1024 + n, where the scales of a tile lie so far
+// apart that the smallest would leave near's values among the subnormals.
+__device__ __forceinline__ void dequant_far(const uint4 &codes, float d, uint4 (&out)[4]) {
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    const uint32_t magic = 0x64006400u, minus = 0xE408E408u;        // 1024, -1032
     const uint32_t sixteenth = 0x2C002C00u, minus72 = 0xD480D480u;  // 1/16, -72
+    const uint32_t d2 = pack_rn(d, d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t x = w[i], x8 = x >> 8;
@@ -217,6 +236,7 @@ __device__ __forceinline__ void dequant_block(const uint4 &codes, uint32_t d2, u
         out[i].w = hmul2(hfma2((x8 & 0x00F000F0u) | magic, sixteenth, minus72), d2);
     }
 }
+constexpr int kNear = 10, kNearSpan = 6;  // near: exponents of a tile's scales at most so far apart
 
 // What a dequant thread holds of one tile: its key's blocks.
 template <int D>
@@ -274,10 +294,12 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
         load(t + 1, page, next);
         // the tile's largest scales
         TileInfo &info = sh.info[t % kRing];
-        int e[2] = {0, 0};
+        int e[2];
+        bool near[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            uint32_t top = 0;
+            // exponents of the largest and the smallest that is not 0, 64 more
+            uint32_t top = 0, low = 127;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 uint32_t bits = cur.scale[half][u] & 0x7FFFu;
@@ -285,11 +307,15 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
                     if (half && cur.there) atomicOr(&info.odd[key >> 5], 1u << (key & 31));
                     bits = 0;  // NaN and infinity do not set the scale
                 }
-                top = max(top, bits);
+                if (bits) {
+                    const uint32_t x = 64 + exponent(__half2float(__ushort_as_half(static_cast<unsigned short>(bits))));
+                    top = max(top, x);
+                    low = min(low, x);
+                }
             }
             top = __reduce_max_sync(0xFFFFFFFFu, top);
-            e[half] = top ? exponent(__half2float(__ushort_as_half(static_cast<unsigned short>(top)))) : -24;
-            if (lane == 0) sh.exps[t & 1][half][w8] = e[half];
+            low = __reduce_min_sync(0xFFFFFFFFu, low);
+            if (lane == 0) sh.exps[t & 1][half][w8] = top | (127 - low) << 16;
         }
         const unsigned gone = __ballot_sync(0xFFFFFFFFu, !cur.there && page_here != -2);
         if (gone && lane == 0) {
@@ -299,15 +325,22 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
         asm volatile("bar.sync 1, %0;" ::"r"(kDequantWarps * 32) : "memory");
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            int top = -24;
-#pragma unroll
-            for (int w = 0; w < kDequantWarps; ++w)
-                if (D != 64 || (w >> 2) == half) top = max(top, sh.exps[t & 1][half][w]);
-            e[half] = top;
+            // two 16-bit maxima at once
+            const uint4 *from = reinterpret_cast<const uint4 *>(sh.exps[t & 1][half]);
+            uint4 x = from[D == 64 ? half : 0];
+            if constexpr (D != 64) {
+                const uint4 y = from[1];
+                x = make_uint4(__vmaxu2(x.x, y.x), __vmaxu2(x.y, y.y), __vmaxu2(x.z, y.z), __vmaxu2(x.w, y.w));
+            }
+            const uint32_t both = __vmaxu2(__vmaxu2(x.x, x.y), __vmaxu2(x.z, x.w));
+            const int top = both & 0xFFFF, low = 127 - static_cast<int>(both >> 16);
+            e[half] = top ? top - 64 : -24;
+            near[half] = top - low <= kNearSpan;  // also where all are 0
         }
         if (w8 == 0 && lane == 0) {
-            info.k_exp = e[0];
-            info.v_exp = e[1];
+            info.k_exp = e[0] + (near[0] ? kNear : 0);
+            info.v_exp = e[1] + (near[1] ? kNear : 0);
+            info.far = !near[1];
             TileInfo &later = sh.info[(t + kRing / 2) % kRing];  // not in use: readers lag by less
             later.lost = later.odd[0] = later.odd[1] = 0;
         }
@@ -327,7 +360,10 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
                 if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd
                 d *= pow2i(-e[half]);
                 uint4 out[4];
-                dequant_block(cur.codes[half][u], pack_rn(d, d), out);
+                if (near[half])
+                    dequant_near(cur.codes[half][u], d, out);
+                else
+                    dequant_far(cur.codes[half][u], d, out);
                 uint8_t *panel = rows + (b >> 1) * kPanel;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -485,7 +521,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
     const int lo = mine ? first_key(a, pos) : 0, hi = mine ? (a.causal ? min(bk.len, pos + 1) : bk.len) : 0;
     float top = ninf, sum = 0.0f;  // the weights' reference (2^kRaise there), and their sum
     int e_ref = -24;               // exponent of V's unit in O
-    bool faint = false;            // a weight fell below binary16's normal numbers
+    bool faint = false, far = false;  // a weight fell below binary16's normal numbers; a tile was far
     bool ok = true;
     for (int t = 0; t < bk.tiles; ++t) {
         const int j = t * T::QT + qt;
@@ -500,6 +536,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
         tmem_ld_64cols(s_at, s);
         const TileInfo &info = sh.info[t % kRing];
         const float u = unit * pow2i(info.k_exp);
+        far |= info.far;
         const int key0 = bk.key0 + t * kKeys;
         const bool edge = info.lost || info.odd[0] || info.odd[1] || key0 < bk.lo_all || key0 + kKeys > bk.hi_all;
         if (edge) {
@@ -514,7 +551,12 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
 #pragma unroll
         for (int i = 0; i < 4; ++i) most[i] = __uint_as_float(s[i]);
 #pragma unroll
-        for (int i = 4; i < 64; ++i) most[i & 3] = fmaxf(most[i & 3], __uint_as_float(s[i]));
+        for (int i = 4; i < 60; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                most[k] = fmaxf(most[k], fmaxf(__uint_as_float(s[i + k]), __uint_as_float(s[i + 4 + k])));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most[k] = fmaxf(most[k], __uint_as_float(s[60 + k]));
         const float big = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
         const float here = big * u;
         // a new reference where the largest weight would pass 2^15, and where
@@ -562,8 +604,9 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float x = exp2_fast(fmaf(__uint_as_float(s[32 * h + 2 * i]), u, base));
-                const float y = exp2_fast(fmaf(__uint_as_float(s[32 * h + 2 * i + 1]), u, base));
+                const float2 arg = __ffma2_rn(make_float2(__uint_as_float(s[32 * h + 2 * i]), __uint_as_float(s[32 * h + 2 * i + 1])),
+                                              make_float2(u, u), make_float2(base, base));
+                const float x = exp2_fast(arg.x), y = exp2_fast(arg.y);
                 add[i & 1] = __fadd2_rn(add[i & 1], make_float2(x, y));
                 w[i] = pack_rn(x, y);
                 least[i & 1] = hmin2(least[i & 1], w[i]);
@@ -625,12 +668,13 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
         }
         if (mine && a.lse) a.lse[out_row * a.heads + head] = sum == 0.0f ? ninf : (top + log2f(sum)) * kLn2;
     }
-    // A faint weight is off by at most 2^-25, times values below 16, a key.
+    // A faint weight is off by at most 2^-25, times values below 16 (near tiles
+    // only: 2^-6), a key.
     // Scores that lie 24 powers of two apart are themselves uncertain by more
     // than 2^-6 of a weight (binary16 q and K, A >= 8), so an output has to be
     // 2^6 times that sum at least; else the row is done again.
     const float keys = static_cast<float>(bk.tiles * kKeys);
-    const unsigned again = __ballot_sync(0xFFFFFFFFu, ok && mine && faint && least < keys * (1.0f / 32768.0f));
+    const unsigned again = __ballot_sync(0xFFFFFFFFu, ok && mine && faint && least < keys * (far ? pow2i(-15) : pow2i(-15 - kNear)));
     if (lane == 0) sh.again[warp] = again;
 }
 
@@ -737,7 +781,7 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
         sh.abort = 0;
         fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < kRing; i += T::threads) sh.info[i] = TileInfo{0, 0, 0u, {0u, 0u}};
+    for (int i = threadIdx.x; i < kRing; i += T::threads) sh.info[i] = TileInfo{};
     if (threadIdx.x < 8) sh.again[threadIdx.x] = 0;
     if (warp == T::mma_warp) tmem_alloc_cta(smem_addr(&sh.tmem), T::tmem_cols);
     tc_fence_before();

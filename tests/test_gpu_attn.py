@@ -190,6 +190,21 @@ def test_mixed_sizes_within_a_request(qmm):
             c.check(c.call(qmm, out_type))
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 70])
+def test_blocks_of_very_different_scales(qmm, dim, new):
+    """Head dimensions whose scales differ by 2^12 within a key, with queries
+    that make up for it: every block counts."""
+    for out_type in (F32, BF16):
+        c = Case(qmm, [200, 130], [new, new], 4, 1, dim, 32, seed=dim + new)
+        step = np.float32(2.0) ** -(np.arange(dim // 32) * 12 // max(1, dim // 32 - 1))
+        for i in (1, 3):
+            c.arrays[i] = (c.arrays[i].astype(np.float32) * step).astype(np.float16)
+        c.cache = qmm.KvCacheQ4_0(*(torch.from_numpy(a).cuda() for a in c.arrays))
+        c.q = (c.q / torch.from_numpy(np.repeat(step, 32))).float()
+        c.check(c.call(qmm, out_type))
+
+
 def test_zero_scales_and_zero_queries(qmm):
     for new in (1, 70):
         c = Case(qmm, [100], [new], 4, 1, 128, 16, seed=2)
