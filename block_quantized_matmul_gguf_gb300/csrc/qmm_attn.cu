@@ -1393,7 +1393,7 @@ cudaError_t launch_dim(const KvCache &c, const AttnArgs &a, cudaStream_t stream,
 
 size_t attn_workspace_bytes(const KvCache &, int) {
     const size_t ctas = std::min(device_sm_count() * 2, kMaxCtas);  // as the smaller head dimensions take
-    return ctas * ((kWarps + 2) * kRecord * sizeof(float) + sizeof(CtaParts));
+    return std::max(ctas * ((kWarps + 2) * kRecord * sizeof(float) + sizeof(CtaParts)), attn_tiles_workspace_bytes());
 }
 
 cudaError_t launch_attn(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {

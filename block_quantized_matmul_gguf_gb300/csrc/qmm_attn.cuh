@@ -118,6 +118,7 @@ __device__ __forceinline__ float score_unit(float size, int e) {
 // Attention with the tensor cores' tiles (tcgen05), for bf16 outputs of
 // prompts.  Whether it pays for these sizes: attn_tiles_pay.
 bool attn_tiles_pay(const KvCache &cache, const AttnArgs &args);
+size_t attn_tiles_workspace_bytes();
 cudaError_t launch_attn_tiles(const KvCache &cache, const AttnArgs &args, cudaStream_t stream, const LaunchCtx &ctx);
 
 }  // namespace qmm

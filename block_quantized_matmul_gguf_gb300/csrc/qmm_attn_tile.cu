@@ -2,8 +2,8 @@
 // tensor cores, for the prompts' many query rows (bf16 output).
 //
 // One CTA takes 128 query rows (head_dim 256) or 256 (64, 128) of one request
-// and key head -- the query heads of a group side by side -- over all their
-// keys, in tiles of 64:
+// and key head -- the query heads of a group side by side -- over their keys,
+// or a part of them where the blocks are too few for the GPU, in tiles of 64:
 //   S = Q K^T    M = 128 rows, N = 64 keys, K = head_dim; Q in tensor memory
 //   P = 2^(S - m) in binary16, written over S
 //   O += P V     M = 128 rows, N = head_dim, K = 64 keys; O in tensor memory
@@ -22,14 +22,20 @@
 //
 // Precision: q, (n - 8) d and the weights are rounded once to binary16 each.
 // A tile's K and V are scaled by powers of two to below 2^-6 (16 where its
-// scales lie far apart), q per row to below 2^15 and the weights to at most 2^15, so that nothing overflows; weights
-// below 2^-38 of a row's largest fall out of binary16's range, which shows
-// only where the heavy keys' codes leave (nearly) nothing: such rows are done
-// again by all warps in fp32.
+// scales lie far apart), q per row to below 2^15 and the weights to at most
+// 2^15, so that nothing overflows; weights below 2^-38 of a row's largest fall
+// out of binary16's range, which shows only where the heavy keys' codes leave
+// (nearly) nothing: such rows are done again by all warps in fp32.
+//
+// Parts are joined by a second kernel: their outputs and sums, in fp32, are
+// weighted by 2^(m - largest m), in the parts' order.
 //
 // Bound by the issue slots of the dequantisation and the softmax beside the
-// products (about 0.9 slots a cycle at head_dim 256 if the products never
-// waited).
+// products: about 2900 cycles a tile at head_dim 256, of which the products
+// take 1024.  Measured: 2048 tokens of 8 heads of 256 (2 key heads) behind
+// 6000 cached ones 181 us, 650 TFLOP/s; seven prompts of up to 700 tokens of
+// 16 heads of 128 with a window of 1024 keys 94 us; 128 tokens behind 32000
+// 75 us (777 with one CTA a block).
 #include "qmm_attn.cuh"
 #include "qmm_tc.cuh"
 
@@ -76,13 +82,31 @@ struct TileInfo {
     uint32_t odd[2];       // keys whose V holds a NaN or an infinity
 };
 
+// Rows of one request and key head, and the tiles of their keys: all, or a part.
 struct Block {
     int b, kv_head;
-    int q_row0, flat0, rows, all;  // first row of q of the request; first flat row, rows of the block, of the request
+    int q_row0, flat0, rows;       // first row of q of the request; first flat row, rows of the block
     int first, len;
     int lo, hi, lo_all, hi_all;    // keys that any, and that every, row sees
     int key0, tiles;
+    int slot;                      // of a part in the workspace, or -1
 };
+
+// The parts of split blocks in the workspace, those of one block side by side.
+struct TileParts {
+    int count;        // first part of a block: its parts; else 0
+    Block block;
+};
+struct TileHeader {
+    int used;         // slots
+    int pad[3];
+};
+constexpr int kMaxTileCtas = 256;  // SMs that are counted on: at most as many parts
+constexpr int kMaxThreads = 640;
+// Outputs of a part as float4 [rows / 8][D / 4][8 rows], then maximum, sum and
+// error of each row in a float4.
+constexpr int kPartFloats = 128 * 256 + 256 * 4;
+constexpr int kMinPart = 8;  // tiles of a part at least: about what a CTA takes to begin and end
 
 struct TileShared {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
@@ -90,6 +114,7 @@ struct TileShared {
     TileInfo info[kRing];
     alignas(16) uint32_t exps[2][2][kDequantWarps];  // [tile parity][K, V][warp]
     int64_t scratch[32];
+    int64_t blocks[kMaxThreads];  // row blocks before each thread's requests
     Block block;
     uint32_t tmem;
     int abort;
@@ -102,6 +127,10 @@ struct TileParams {
     const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
     int num_pages, page_shift, kv_heads;
     bool q_wide, out_wide;  // rows are 16-byte aligned
+    int split;               // SMs to fill with parts of blocks, or 0: whole blocks only
+    TileHeader *header;
+    TileParts *parts;        // [slots]
+    float *records;          // [slots][kPartFloats]
     LaunchCtx ctx;
 };
 
@@ -132,20 +161,109 @@ __device__ __forceinline__ void registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// ---- which block of rows this CTA takes ------------------------------------------
+// ---- which rows and keys this CTA takes ----------------------------------------------
 
 template <int D>
 __device__ __forceinline__ int request_blocks(const TileParams &p, const RequestRows &r) {
-    return (r.rows * (p.a.heads / p.kv_heads) + Tile<D>::rows - 1) / Tile<D>::rows;
+    return static_cast<int>((static_cast<int64_t>(r.rows) * (p.a.heads / p.kv_heads) + Tile<D>::rows - 1) / Tile<D>::rows);
 }
 
-// Fills sh.block; block.b is -1 for CTAs past the last block.
+template <int D>
+__device__ __forceinline__ Block block_of(const TileParams &p, const RequestRows &r, int b, int at, int kv_head) {
+    using T = Tile<D>;
+    const int heads = p.a.heads / p.kv_heads;
+    Block k;
+    k.b = b;
+    k.kv_head = kv_head;
+    k.q_row0 = r.row0;
+    k.flat0 = at * T::rows;
+    k.rows = min(T::rows, r.rows * heads - k.flat0);
+    k.first = r.first;
+    k.len = r.len;
+    const int pos0 = r.first + k.flat0 / heads, pos1 = r.first + (k.flat0 + k.rows - 1) / heads;
+    k.lo = first_key(p.a, pos0);
+    k.hi = p.a.causal ? min(r.len, pos1 + 1) : r.len;
+    k.lo_all = first_key(p.a, pos1);
+    k.hi_all = p.a.causal ? min(r.len, pos0 + 1) : r.len;
+    k.key0 = k.lo / kKeys * kKeys;
+    k.tiles = k.hi > k.lo ? (k.hi - k.key0 + kKeys - 1) / kKeys : 0;
+    k.slot = -1;
+    return k;
+}
+
+// The last thread whose count is at most x.
+template <int THREADS>
+__device__ __forceinline__ int holder(const int64_t *before, int64_t x) {
+    int lo = 0, n = THREADS;
+    while (n > 1) {
+        const int half = n >> 1;
+        if (before[lo + half] <= x) lo += half, n -= half;
+        else n = half;
+    }
+    return lo;
+}
+
+// Row blocks one after another.
+template <int D>
+struct Walk {
+    int b, at, n;  // request, row blocks of it that come before, its row blocks
+    RequestRows r;
+    // the last rows see the most keys: they go first
+    __device__ __forceinline__ Block block(const TileParams &p, int kv_head) const { return block_of<D>(p, r, b, n - 1 - at, kv_head); }
+    __device__ __forceinline__ void start(const TileParams &p, const TileShared &sh, int64_t block) {
+        constexpr int threads = Tile<D>::threads;
+        const int t = holder<threads>(sh.blocks, block);
+        b = t * ((p.a.batch + threads - 1) / threads);
+        int64_t left = block - sh.blocks[t];
+        for (;; ++b) {
+            r = request_rows(p.a, p.page_shift, b);
+            n = request_blocks<D>(p, r);
+            if (left < n || b + 1 >= p.a.batch) break;
+            left -= n;
+        }
+        at = static_cast<int>(left);
+    }
+    __device__ __forceinline__ void next(const TileParams &p) {
+        ++at;
+        while (at >= n && b + 1 < p.a.batch) {
+            r = request_rows(p.a, p.page_shift, ++b);
+            n = request_blocks<D>(p, r);
+            at = 0;
+        }
+    }
+};
+
+// Exclusive sum over the CTA's threads, and the total.
+template <int THREADS>
+__device__ __forceinline__ int64_t sum_before(TileShared &sh, int64_t mine, int64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += up;
+    }
+    if (lane == 31) sh.scratch[warp] = sum;
+    __syncthreads();
+    int64_t before = sum - mine;
+    total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += sh.scratch[w];
+        total += sh.scratch[w];
+    }
+    __syncthreads();
+    return before;
+}
+
+// Fills sh.block; block.b is -1 for CTAs past the last.
+// Split, a block of more than so many tiles is cut into equal parts for CTAs
+// of their own: all parts run at once where the blocks are fewer than 3/4 of
+// the SMs, and otherwise none has more than two SMs' share of the work.
 template <int D>
 __device__ __forceinline__ void find_block(const TileParams &p, TileShared &sh) {
-    using T = Tile<D>;
+    constexpr int threads = Tile<D>::threads;
     const AttnArgs &a = p.a;
-    const int blk = blockIdx.x / p.kv_heads, kv_head = blockIdx.x - blk * p.kv_heads;
-    const int per = (a.batch + T::threads - 1) / T::threads;
+    const int per = (a.batch + threads - 1) / threads;
     const int b0 = min(a.batch, static_cast<int>(threadIdx.x) * per), b1 = min(a.batch, b0 + per);
     int64_t mine = 0;
     int bad = 0;
@@ -155,44 +273,68 @@ __device__ __forceinline__ void find_block(const TileParams &p, TileShared &sh) 
         bad |= r.bad;
     }
     if (bad && blockIdx.x == 0) record_error(p.ctx, kDevErrIndex);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += up;
-    }
-    if (lane == 31) sh.scratch[warp] = sum;
     if (threadIdx.x == 0) sh.block.b = -1;
+    int64_t blocks;
+    sh.blocks[threadIdx.x] = sum_before<threads>(sh, mine, blocks);
     __syncthreads();
-    int64_t before = sum - mine;
-    for (int w = 0; w < warp; ++w) before += sh.scratch[w];
-    if (blk >= before && blk < before + mine) {
-        for (int b = b0; b < b1; ++b) {
-            const RequestRows r = request_rows(a, p.page_shift, b);
-            const int n = request_blocks<D>(p, r);
-            if (blk >= before + n) {
-                before += n;
+    if (blocks > INT32_MAX / p.kv_heads) blocks = 0;  // requests that overlap: an error by now
+    if (p.split == 0) {
+        const int64_t at = blockIdx.x / p.kv_heads;
+        if (threadIdx.x == 0 && at < blocks) {
+            Walk<D> w;
+            w.start(p, sh, at);
+            sh.block = w.block(p, blockIdx.x - static_cast<int>(at) * p.kv_heads);
+        }
+        __syncthreads();
+        return;
+    }
+    const int64_t each = (blocks + threads - 1) / threads;
+    const int64_t i0 = min(blocks, threadIdx.x * each), i1 = min(blocks, i0 + each);
+    Walk<D> first;
+    int64_t tiles = 0, total;
+    if (i0 < i1) {
+        first.start(p, sh, i0);
+        Walk<D> w = first;
+        for (int64_t i = i0; i < i1; ++i, w.next(p)) tiles += static_cast<int64_t>(w.block(p, 0).tiles) * p.kv_heads;
+    }
+    sum_before<threads>(sh, tiles, total);
+    const int64_t all = blocks * p.kv_heads;
+    const int64_t shares = 4 * all <= 3 * p.split ? p.split - all : p.split / 2;
+    const int64_t most = max(static_cast<int64_t>(kMinPart), (total + shares - 1) / shares);
+    auto parts_of = [&](int n) { return n > most ? static_cast<int>((n + most - 1) / most) : 1; };
+    // CTAs, and in the upper half those that have parts
+    int64_t count = 0;
+    if (i0 < i1) {
+        Walk<D> w = first;
+        for (int64_t i = i0; i < i1; ++i, w.next(p)) {
+            const int n = parts_of(w.block(p, 0).tiles);
+            count += (n > 1 ? (static_cast<int64_t>(n) << 32) + n : 1) * p.kv_heads;
+        }
+    }
+    int64_t ctas;
+    int64_t before = sum_before<threads>(sh, count, ctas);
+    if (threadIdx.x == 0 && blockIdx.x == 0) p.header->used = static_cast<int>(ctas >> 32);
+    if (i0 < i1 && blockIdx.x >= static_cast<uint32_t>(before) && blockIdx.x < static_cast<uint32_t>(before + count)) {
+        Walk<D> w = first;
+        for (int64_t i = i0; i < i1; ++i, w.next(p)) {
+            Block k = w.block(p, 0);
+            const int n = parts_of(k.tiles);
+            const int64_t here = (n > 1 ? (static_cast<int64_t>(n) << 32) + n : 1) * p.kv_heads;
+            if (blockIdx.x >= static_cast<uint32_t>(before + here)) {
+                before += here;
                 continue;
             }
-            // the last rows see the most keys: they go first
-            const int at = n - 1 - static_cast<int>(blk - before), heads = a.heads / p.kv_heads;
-            Block k;
-            k.b = b;
-            k.kv_head = kv_head;
-            k.q_row0 = r.row0;
-            k.all = r.rows * heads;
-            k.flat0 = at * T::rows;
-            k.rows = min(T::rows, k.all - k.flat0);
-            k.first = r.first;
-            k.len = r.len;
-            const int pos0 = r.first + k.flat0 / heads, pos1 = r.first + (k.flat0 + k.rows - 1) / heads;
-            k.lo = first_key(a, pos0);
-            k.hi = a.causal ? min(r.len, pos1 + 1) : r.len;
-            k.lo_all = first_key(a, pos1);
-            k.hi_all = a.causal ? min(r.len, pos0 + 1) : r.len;
-            k.key0 = k.lo / kKeys * kKeys;
-            k.tiles = k.hi > k.lo ? (k.hi - k.key0 + kKeys - 1) / kKeys : 0;
+            const int at = static_cast<int>(blockIdx.x - static_cast<uint32_t>(before));
+            k.kv_head = at / n;
+            if (n > 1) {
+                k.slot = static_cast<int>(before >> 32) + at;
+                const int part = at - k.kv_head * n;
+                p.parts[k.slot] = TileParts{part == 0 ? n : 0, k};
+                const int t0 = static_cast<int>(static_cast<int64_t>(k.tiles) * part / n);
+                const int t1 = static_cast<int>(static_cast<int64_t>(k.tiles) * (part + 1) / n);
+                k.key0 += t0 * kKeys;
+                k.tiles = t1 - t0;
+            }
             sh.block = k;
             break;
         }
@@ -484,35 +626,43 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             f = pow2i(up) * sign;
             unit = score_unit(size, -up);
         };
-        // A bf16 row of up to 128 values fits a thread's registers: one pass (700-token
-        // prompts of head_dim 128: 97.1 -> 92.6 us; at 256 values it costs the loop
-        // below registers, 178.8 -> 180.8 us for a 2048-token chunk).
-        if (D < 256 && a.q_bf16 && p.q_wide) {
-            uint4 raw[D / 8];
+        if (a.q_bf16 && p.q_wide) {  // 128 values of a row under way at once; the last are kept for the second pass
+            constexpr int C = D / 8 < 16 ? D / 8 : 16, H = D / 8 / C;
+            uint4 raw[C];
             const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + q_at);
+            auto load = [&](int h) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) raw[i] = from[i];
+                for (int i = 0; i < C; ++i) raw[i] = __ldg(from + h * C + i);
+            };
+#pragma unroll 1
+            for (int h = H - 1; h >= 0; --h) {
+                load(h);
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                for (int i = 0; i < C; ++i) {
+                    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) bits = max(bits, max((w[k] & 0x7FFFu) << 16, w[k] & 0x7FFF0000u));
+                    for (int k = 0; k < 4; ++k) bits = max(bits, max((w[k] & 0x7FFFu) << 16, w[k] & 0x7FFF0000u));
+                }
             }
             scale_up();
+#pragma unroll 1
+            for (int h = 0; h < H; ++h) {
+                if (h > 0) load(h);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                uint32_t cols[16];
-                auto value = [&](int d) {
-                    const uint4 &r = raw[b * 4 + (d >> 3)];
-                    const uint32_t w = (d >> 1 & 3) == 0 ? r.x : (d >> 1 & 3) == 1 ? r.y : (d >> 1 & 3) == 2 ? r.z : r.w;
-                    return __uint_as_float(d & 1 ? w & 0xFFFF0000u : w << 16) * f;
-                };
+                for (int b = 0; b < C / 4; ++b) {
+                    uint32_t cols[16];
+                    auto value = [&](int d) {
+                        const uint4 &r = raw[b * 4 + (d >> 3)];
+                        const uint32_t w = (d >> 1 & 3) == 0 ? r.x : (d >> 1 & 3) == 1 ? r.y : (d >> 1 & 3) == 2 ? r.z : r.w;
+                        return __uint_as_float(d & 1 ? w & 0xFFFF0000u : w << 16) * f;
+                    };
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {  // values d and d + 2 stand side by side
-                    const int d = ((i >> 2) << 2) + ((i >> 1) & 1) + ((i & 1) << 4);
-                    cols[i] = pack_rn(value(d), value(d + 2));
+                    for (int i = 0; i < 16; ++i) {  // values d and d + 2 stand side by side
+                        const int d = ((i >> 2) << 2) + ((i >> 1) & 1) + ((i & 1) << 4);
+                        cols[i] = pack_rn(value(d), value(d + 2));
+                    }
+                    tmem_st_16cols(q_to + (h * (C / 4) + b) * 16, cols);
                 }
-                tmem_st_16cols(q_to + b * 16, cols);
             }
         } else {
 #pragma unroll 1
@@ -670,7 +820,34 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
     tc_fence_after();
     const int64_t out_row = static_cast<int64_t>(bk.q_row0) + token;
     const int64_t out_at = out_row * a.out_stride + static_cast<int64_t>(head) * D;
-    const float down = sum == 0.0f ? 0.0f : pow2i(e_ref - kRaise) / sum;
+    // A faint weight is off by at most 2^-25, times values below 16 (near tiles
+    // only: 2^-6), a key.
+    // Scores that lie 24 powers of two apart are themselves uncertain by more
+    // than 2^-6 of a weight (binary16 q and K, A >= 8), so an output has to be
+    // 2^6 times that sum at least; else the row is done again.
+    const float error = faint ? static_cast<float>(bk.tiles * kKeys) * (far ? pow2i(-15) : pow2i(-15 - kNear)) : 0.0f;
+    const float back = pow2i(e_ref - kRaise);  // of O's unit
+    if (bk.slot >= 0) {  // the joining kernel goes on
+        float *rec = p.records + static_cast<int64_t>(bk.slot) * kPartFloats;
+        float4 *to = reinterpret_cast<float4 *>(rec) + (row >> 3) * (D / 4 * 8) + (row & 7);
+        if (ok) {
+#pragma unroll 1
+            for (int b = 0; b < NB; ++b) {
+                uint32_t o[32];
+                tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
+                if (!mine) continue;
+#pragma unroll
+                for (int d = 0; d < 32; d += 4)
+                    to[(b * 8 + d / 4) * 8] = make_float4(
+                        __uint_as_float(o[place_of(d)]) * back, __uint_as_float(o[place_of(d + 1)]) * back,
+                        __uint_as_float(o[place_of(d + 2)]) * back, __uint_as_float(o[place_of(d + 3)]) * back);
+            }
+            if (mine) *reinterpret_cast<float4 *>(rec + T::rows * D + row * 4) = make_float4(top, sum, error * back, 0.0f);
+        }
+        if (lane == 0) sh.again[warp] = 0;
+        return;
+    }
+    const float down = sum == 0.0f ? 0.0f : back / sum;
     float least = __uint_as_float(0x7F800000u);
     if (ok) {
 #pragma unroll 1
@@ -705,23 +882,16 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
         }
         if (mine && a.lse) a.lse[out_row * a.heads + head] = sum == 0.0f ? ninf : (top + log2f(sum)) * kLn2;
     }
-    // A faint weight is off by at most 2^-25, times values below 16 (near tiles
-    // only: 2^-6), a key.
-    // Scores that lie 24 powers of two apart are themselves uncertain by more
-    // than 2^-6 of a weight (binary16 q and K, A >= 8), so an output has to be
-    // 2^6 times that sum at least; else the row is done again.
-    const float keys = static_cast<float>(bk.tiles * kKeys);
-    const unsigned again = __ballot_sync(0xFFFFFFFFu, ok && mine && faint && least < keys * (far ? pow2i(-15) : pow2i(-15 - kNear)));
+    const unsigned again = __ballot_sync(0xFFFFFFFFu, ok && mine && least < error);
     if (lane == 0) sh.again[warp] = again;
 }
 
 // One row in fp32 by all warps: warp w takes every W-th key, a lane the same
 // code bytes of each.
-template <int D>
-__device__ __noinline__ void row_again(const TileParams &p, TileShared &sh, float *share, int row) {
-    constexpr int B = D / 64, W = Tile<D>::threads / 32;  // code bytes per lane
+template <int D, int W>
+__device__ __noinline__ void row_again(const TileParams &p, const Block &bk, float *share, float (*part)[2], int row) {
+    constexpr int B = D / 64;  // code bytes per lane
     const AttnArgs &a = p.a;
-    const Block &bk = sh.block;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = a.heads / p.kv_heads;
     const int flat = bk.flat0 + row, token = flat / heads, head = bk.kv_head * heads + flat - token * heads;
     const int64_t at = (static_cast<int64_t>(bk.q_row0) + token) * a.q_stride + static_cast<int64_t>(head) * D;
@@ -774,17 +944,17 @@ __device__ __noinline__ void row_again(const TileParams &p, TileShared &sh, floa
         share[warp * D + d + 16] = o[2 * i + 1];
     }
     if (lane == 0) {
-        sh.part[warp][0] = m;
-        sh.part[warp][1] = l;
+        part[warp][0] = m;
+        part[warp][1] = l;
     }
     __syncthreads();
     float top = ninf, sum = 0.0f;
-    for (int w = 0; w < W; ++w) top = fmaxf(top, sh.part[w][0]);
+    for (int w = 0; w < W; ++w) top = fmaxf(top, part[w][0]);
     const float ref = top == ninf ? 0.0f : top;
-    for (int w = 0; w < W; ++w) sum = fmaf(exp2_fast(sh.part[w][0] - ref), sh.part[w][1], sum);
-    for (int d = threadIdx.x; d < D; d += Tile<D>::threads) {
+    for (int w = 0; w < W; ++w) sum = fmaf(exp2_fast(part[w][0] - ref), part[w][1], sum);
+    for (int d = threadIdx.x; d < D; d += W * 32) {
         float y = 0.0f;
-        for (int w = 0; w < W; ++w) y = fmaf(exp2_fast(sh.part[w][0] - ref), share[w * D + d], y);
+        for (int w = 0; w < W; ++w) y = fmaf(exp2_fast(part[w][0] - ref), share[w * D + d], y);
         store_value(a.out, (static_cast<int64_t>(bk.q_row0) + token) * a.out_stride + static_cast<int64_t>(head) * D + d,
                     true, sum == 0.0f ? 0.0f : y / sum);
     }
@@ -797,11 +967,7 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
     uint8_t *smem = tile_smem + ((1024u - (smem_addr(tile_smem) & 1023u)) & 1023u);
     TileShared &sh = *reinterpret_cast<TileShared *>(smem + 2 * T::stages * T::bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait();
-    pdl_launch_dependents();
-    find_block<D>(p, sh);
-    if (sh.block.b < 0) return;  // the whole CTA
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == T::mma_warp * 32) {
         for (int i = 0; i < T::stages; ++i) {
             mbar_init(sh.k_full + i, kDequantWarps);
             mbar_init(sh.k_empty + i, 1);
@@ -820,6 +986,10 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
     }
     for (int i = threadIdx.x; i < kRing; i += T::threads) sh.info[i] = TileInfo{};
     if (threadIdx.x < 8) sh.again[threadIdx.x] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    find_block<D>(p, sh);
+    if (sh.block.b < 0) return;  // the whole CTA
     if (warp == T::mma_warp) tmem_alloc_cta(smem_addr(&sh.tmem), T::tmem_cols);
     tc_fence_before();
     __syncthreads();
@@ -850,7 +1020,162 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
 #pragma unroll 1
     for (int w = 0; w < T::softmax_warps; ++w)
         for (uint32_t again = sh.again[w]; again; again &= again - 1)
-            row_again<D>(p, sh, reinterpret_cast<float *>(smem), w * 32 + __ffs(again) - 1);
+            row_again<D, T::threads / 32>(p, sh.block, reinterpret_cast<float *>(smem), sh.part, w * 32 + __ffs(again) - 1);
+}
+
+// Joins the parts of split blocks, eight rows at a time: a lane has four
+// values of each of Q quads of one row.  Bound by the latency of its loads,
+// which come from L2.
+template <int D>
+struct Join {
+    static constexpr int warps = D == 64 ? 4 : 8, Q = D / 16 / warps, slices = Tile<D>::rows / 8;
+};
+
+template <int D>
+__global__ void __launch_bounds__(Join<D>::warps * 32) attn_tile_join_kernel(const __grid_constant__ TileParams p) {
+    using T = Tile<D>;
+    using J = Join<D>;
+    constexpr int W = J::warps, Q = J::Q;
+    __shared__ int starts[kMaxTileCtas], counts[kMaxTileCtas];
+    __shared__ int chains;
+    __shared__ float weight[kMaxTileCtas][8];
+    __shared__ float red[W][8][2];
+    __shared__ float least[W][8];
+    __shared__ float share[W * D];
+    __shared__ float part[W][2];
+    pdl_wait();
+    pdl_launch_dependents();
+    const AttnArgs &a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float ninf = __uint_as_float(0xFF800000u);
+    const int used = p.header->used;
+    if (used == 0) return;
+    if (warp == 0) {
+        int k = 0;
+        for (int i = 0; i < used; i += 32) {
+            const int n = i + lane < used ? p.parts[i + lane].count : 0;
+            const unsigned have = __ballot_sync(0xFFFFFFFFu, n > 0);
+            if (n > 0) {
+                const int at = k + __popc(have & ((1u << lane) - 1u));
+                starts[at] = i + lane;
+                counts[at] = n;
+            }
+            k += __popc(have);
+        }
+        if (lane == 0) chains = k;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int item = blockIdx.x; item < chains * J::slices; item += gridDim.x) {
+        const int c = starts[item / J::slices], k = counts[item / J::slices], row0 = item % J::slices * 8;
+        const Block &block = p.parts[c].block;
+        if (row0 >= block.rows) continue;
+        const int row = row0 + (lane & 7);
+        const bool mine = row < block.rows;
+        auto record = [&](int i) { return p.records + static_cast<int64_t>(c + i) * kPartFloats; };
+        // the parts' weights: thread (lane & 7) of parts i, i + 4 W, ...
+        const int i0 = threadIdx.x >> 3;
+        float top = ninf;
+        for (int i = i0; i < k; i += W * 4) {
+            const float t = mine ? record(i)[T::rows * D + row * 4] : ninf;
+            weight[i][lane & 7] = t;
+            top = fmaxf(top, t);
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+        if (lane < 8) red[warp][lane][0] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) top = fmaxf(top, red[w][lane & 7][0]);
+        __syncthreads();
+        const float ref = top == ninf ? 0.0f : top;
+        float sum = 0.0f, error = 0.0f;
+        for (int i = i0; i < k; i += W * 4) {
+            const float4 s = mine ? *reinterpret_cast<const float4 *>(record(i) + T::rows * D + row * 4) : make_float4(ninf, 0.0f, 0.0f, 0.0f);
+            const float f = exp2_fast(s.x - ref);
+            weight[i][lane & 7] = f;
+            sum = fmaf(f, s.y, sum);
+            error = fmaf(f, s.z, error);
+        }
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            error += __shfl_xor_sync(0xFFFFFFFFu, error, o);
+        }
+        if (lane < 8) {
+            red[warp][lane][0] = sum;
+            red[warp][lane][1] = error;
+        }
+        __syncthreads();
+        sum = error = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            sum += red[w][lane & 7][0];
+            error += red[w][lane & 7][1];
+        }
+        float4 v[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (mine) {
+#pragma unroll 4
+            for (int i = 0; i < k; ++i) {
+                const float4 *from = reinterpret_cast<const float4 *>(record(i)) + (row0 >> 3) * (D / 4 * 8) + warp * Q * 32 + lane;
+                const float f = weight[i][lane & 7];
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    const float4 x = from[q * 32];
+                    v[q].x = fmaf(f, x.x, v[q].x);
+                    v[q].y = fmaf(f, x.y, v[q].y);
+                    v[q].z = fmaf(f, x.z, v[q].z);
+                    v[q].w = fmaf(f, x.w, v[q].w);
+                }
+            }
+        }
+        const int heads = a.heads / p.kv_heads, flat = block.flat0 + (mine ? row : 0), token = flat / heads;
+        const int head = block.kv_head * heads + flat - token * heads;
+        const int64_t out_row = static_cast<int64_t>(block.q_row0) + token;
+        const float down = sum == 0.0f ? 0.0f : 1.0f / sum;
+        float low = __uint_as_float(0x7F800000u);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            low = fminf(fminf(low, fminf(fabsf(v[q].x), fabsf(v[q].y))), fminf(fabsf(v[q].z), fabsf(v[q].w)));
+            const int64_t at = out_row * a.out_stride + static_cast<int64_t>(head) * D + ((warp * Q + q) * 4 + (lane >> 3)) * 4;
+            if (!mine) continue;
+            if (p.out_wide) {
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+                    make_uint2(pack_bf16x2(v[q].x * down, v[q].y * down), pack_bf16x2(v[q].z * down, v[q].w * down));
+            } else {
+                store_value(a.out, at, true, v[q].x * down);
+                store_value(a.out, at + 1, true, v[q].y * down);
+                store_value(a.out, at + 2, true, v[q].z * down);
+                store_value(a.out, at + 3, true, v[q].w * down);
+            }
+        }
+        if (warp == 0 && lane < 8 && mine && a.lse)
+            a.lse[out_row * a.heads + head] = sum == 0.0f ? ninf : (top + log2f(sum)) * kLn2;
+        low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, 8));
+        low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, 16));
+        if (lane < 8) least[warp][lane] = low;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) low = fminf(low, least[w][lane & 7]);
+        uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && low < error) & 0xFFu;  // the same in every warp
+        for (; again; again &= again - 1) row_again<D, W>(p, block, share, part, row0 + __ffs(again) - 1);
+        __syncthreads();  // the item's shared values have been read
+    }
+}
+
+// Blocks that can have at most so many tiles are not split: what the search
+// for parts and the joining kernel take (4 us) is a tenth of such a block's
+// time.
+constexpr int kWholeTiles = 32;
+
+int tile_sms() { return std::min(device_sm_count(), kMaxTileCtas); }
+size_t parts_bytes(int sms) { return (sizeof(TileHeader) + sms * sizeof(TileParts) + 255) / 256 * 256; }
+
+// Keys that a block of so many rows can see.
+int64_t key_bound(const KvCache &c, const AttnArgs &a, int rows) {
+    return std::min(a.table_width << c.page_shift, a.window > 0 && a.causal ? a.window + rows : INT64_MAX);
 }
 
 template <int D>
@@ -865,7 +1190,7 @@ cudaError_t launch_tiles(const KvCache &c, const AttnArgs &a, cudaStream_t strea
     static int limits[kMaxDevices];
     constexpr size_t smem = 2 * T::stages * T::bytes + sizeof(TileShared) + 1024;
     static_assert(smem <= 232448 && T::threads / 32 * D * 4 <= 2 * T::stages * T::bytes, "shared memory per CTA");
-    const cudaError_t e = ensure_smem(attn_tile_kernel<D>, smem, false, limits);
+    cudaError_t e = ensure_smem(attn_tile_kernel<D>, smem, false, limits);
     if (e != cudaSuccess) return e;
     TileParams p = {};
     p.a = a;
@@ -880,15 +1205,52 @@ cudaError_t launch_tiles(const KvCache &c, const AttnArgs &a, cudaStream_t strea
     p.q_wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_stride * q_size % 16 == 0;
     p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride * 2 % 16 == 0;
     p.ctx = ctx;
-    return launch_kernel(attn_tile_kernel<D>, dim3(static_cast<unsigned>(tile_blocks<D>(c, a))), dim3(T::threads), smem,
-                         stream, 1, p);
+    // splitting is left out where no block can have many tiles
+    const int sms = tile_sms();
+    const int64_t blocks = tile_blocks<D>(c, a);
+    int64_t ctas = blocks;
+    if (key_bound(c, a, T::rows) > kWholeTiles * kKeys) {
+        p.split = sms;
+        ctas = 4 * blocks <= 3 * sms ? sms : blocks + sms / 2;
+    }
+    p.header = static_cast<TileHeader *>(a.workspace);
+    p.parts = reinterpret_cast<TileParts *>(p.header + 1);
+    p.records = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + parts_bytes(sms));
+    e = launch_kernel(attn_tile_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(T::threads), smem, stream, 1, p);
+    if (e != cudaSuccess || p.split == 0) return e;
+    return launch_kernel(attn_tile_join_kernel<D>, dim3(sms * 4), dim3(Join<D>::warps * 32), 0, stream, 1, p);
 }
 
 }  // namespace
 
+// The streaming form works on 8 query rows of a request and key head at a
+// time, this one on 128 or 256, whether they are there or not.  Picoseconds
+// that a tile of 64 keys costs the whole GPU in either form:
+//   head_dim 256  stream 3000, tiles 12000;  128  1400, 11500;  64  850, 10200
+// and 9 us that this form takes longer to begin and end.  They follow from
+// (us per call, two key heads, stream / tiles):
+//   head_dim 256, one request: 64 rows with 4000 keys 29 / 42, with 32000
+//   60 / 54, 512 rows with 32000 223 / 75, 2048 rows with 32000 786 / 214;
+//   64 requests with 4000 keys: 16 rows 93 / 119, 32 rows 116 / 115, 64 rows 194 / 120
+//   head_dim 128: 64 rows of 64 requests with 4000 keys 96 / 119, 256 rows with
+//   32000 keys 78 / 51;  head_dim 64, the same two: 68 / 107, 56 / 44
+// The requests' lengths are not known here: the table's width stands for
+// them, and their rows are taken to be alike.
 bool attn_tiles_pay(const KvCache &c, const AttnArgs &a) {
-    const int64_t rows = static_cast<int64_t>(a.max_q) * (a.heads / c.kv_heads);
-    return a.out_bf16 && rows >= 64 && tile_blocks<256>(c, a) <= INT32_MAX;
+    if (!a.out_bf16 || tile_blocks<256>(c, a) > INT32_MAX - kMaxTileCtas) return false;
+    const int64_t group = a.heads / c.kv_heads, rows = c.head_dim == 256 ? Tile<256>::rows : Tile<128>::rows;
+    const int64_t each = (a.total_q * group + a.batch - 1) / a.batch, most = a.max_q * group;
+    const int64_t groups = a.batch * ((each + 7) / 8);
+    const int64_t blocks = std::max(a.batch * ((each + rows - 1) / rows), a.batch - 1 + (most + rows - 1) / rows);
+    const double stream = c.head_dim == 256 ? 3000 : c.head_dim == 128 ? 1400 : 850;
+    const double tiles = c.head_dim == 256 ? 12000 : c.head_dim == 128 ? 11500 : 10200;
+    const double keys = static_cast<double>(c.kv_heads) * static_cast<double>(key_bound(c, a, static_cast<int>(rows))) / kKeys;
+    return keys * (static_cast<double>(groups) * stream - static_cast<double>(blocks) * tiles) > 9e6;
+}
+
+size_t attn_tiles_workspace_bytes() {
+    const int sms = tile_sms();
+    return parts_bytes(sms) + static_cast<size_t>(sms) * kPartFloats * sizeof(float);
 }
 
 cudaError_t launch_attn_tiles(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
