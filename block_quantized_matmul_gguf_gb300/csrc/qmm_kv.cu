@@ -154,10 +154,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
 }
 
 // ---- append ------------------------------------------------------------------
-// Eight lanes share a block of 32 values, four each (one 16- or 8-byte load);
-// the extremes meet by shuffles, lanes 0-3 take the codes of lanes 4-7 as
-// their high nibbles and write the block's 16 bytes.  Bound by the bytes of
-// the inputs; a decode step's few blocks are bound by latency.
+// Four lanes share a block of 32 values, eight each (two 16-byte loads of
+// fp32, one of bf16); the extremes meet by shuffles, lanes 0 and 1 take the
+// codes of lanes 2 and 3 as their high nibbles and write eight of the block's
+// 16 bytes.  Bound by the bytes of the inputs; a decode step's few blocks are
+// bound by latency.
 
 struct KvView {
     uint8_t *k_codes, *v_codes;
@@ -172,52 +173,86 @@ __device__ __forceinline__ int64_t cache_row(const KvView &c, int64_t slot, int 
     return ((((slot >> c.page_shift) * c.kv_heads) + head) << c.page_shift) + place;
 }
 
-// How a CTA's threads share tokens: `per` quads a token (a multiple of 32, so
-// that a warp holds one token's), several tokens at a time where they fit.
-// kAhead tokens per thread are loaded before the first is worked on: 4 where
-// that still fills the GPU, else 1.  8191 tokens of 2 x 256 fp32, append and
-// read: 29 us against 36 with 1; 16 tokens: 3.6 us against 5.7 with 4.
-constexpr int kMany = 4;
+// How a CTA's threads share tokens: `per` parts of eight values a token,
+// several tokens at a time where they fit.  kAhead tokens per thread are
+// loaded before the first is worked on: several where that still fills the
+// GPU, else 1.  8191 tokens of 2 x 256 fp32, append and read: 20 us (79 MB,
+// 3.9 TB/s; 27 with 1 and 1, 25 with 4 and 4, 21.4 where the registers allow
+// only 4 and 3 CTAs an SM); 16 tokens: 3.6 us, 5.7 with several.
+constexpr int kAppendMany = 2, kReadMany = 4;
 
 struct Spread {
     int per, par, sub, at;
-    __device__ explicit Spread(int quads) : per(quads) {
+    __device__ explicit Spread(int parts) : per(parts) {
         par = max(1, kThreads / per);
         sub = threadIdx.x / per;
         at = threadIdx.x - sub * per;
-        if (sub >= par) sub = -1;  // threads that are left over
+        if (par == 1) {
+            sub = 0;
+            at = threadIdx.x;
+        } else if (sub >= par) {
+            at = per;  // threads that are left over
+        }
     }
 };
 
 template <bool kWide>
-__device__ __forceinline__ float4 load_quad(const float *p) {
-    if constexpr (kWide) return __ldcs(reinterpret_cast<const float4 *>(p));
-    return make_float4(p[0], p[1], p[2], p[3]);
+__device__ __forceinline__ void load_eight(const float *p, float (&x)[8]) {
+    if constexpr (kWide) {
+        const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = p[i];
+    }
 }
 template <bool kWide>
-__device__ __forceinline__ float4 load_quad(const uint16_t *p) {
-    uint32_t lo, hi;
+__device__ __forceinline__ void load_eight(const uint16_t *p, float (&x)[8]) {
     if constexpr (kWide) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-        lo = v.x;
-        hi = v.y;
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
     } else {
-        lo = p[0] | (static_cast<uint32_t>(p[1]) << 16);
-        hi = p[2] | (static_cast<uint32_t>(p[3]) << 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
     }
-    return make_float4(__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u),
-                       __uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u));
 }
 
-// round(x / d) + 8 within 0..15, IEEE division and rounding to even
-__device__ __forceinline__ uint32_t code_of(float x, float d) {
-    const float r = rintf(__fdiv_rn(x, d)) + 8.0f;
-    return static_cast<uint32_t>(fminf(fmaxf(r, 0.0f), 15.0f));
+// Codes round(x / d) + 8 within 0..15 of eight values, a byte each, with the
+// quotient rounded as IEEE division rounds and then to even.  x (1 / d) lies
+// within 2^-22 of the quotient, relatively, so that it rounds to the same
+// integer unless it is within 1e-5 of halfway between two (|x / d| < 16;
+// larger ones are cut); only those are divided.
+__device__ __forceinline__ void codes_of(const float (&x)[8], float d, uint32_t (&q)[2]) {
+    constexpr float kOne = 12582912.0f;  // 1.5 2^23: here a unit is the last bit
+    const float inv = __fdiv_rn(1.0f, d);
+    float t[8], near = 0.5f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        t[i] = fminf(fmaxf(fmaf(x[i], inv, kOne), kOne - 8.0f), kOne + 7.0f);
+        near = fminf(near, fabsf(fabsf(fmaf(x[i], inv, kOne - t[i])) - 0.5f));
+    }
+    if (near < 1e-5f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t[i] = kOne + fminf(fmaxf(rintf(__fdiv_rn(x[i], d)), -8.0f), 7.0f);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(t[4 * h + i] + 8.0f);
+        q[h] = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+    }
 }
 
-// kWide: rows of quads are aligned to their size.
+// kWide: rows of eight values are aligned to 16 bytes.
 template <typename T, bool kWide, int kAhead>
-__global__ void __launch_bounds__(kThreads) append_kernel(KvView c, const T *__restrict__ k,
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(KvView c, const T *__restrict__ k,
                                                           int64_t k_stride,
                                                           const T *__restrict__ v,
                                                           int64_t v_stride,
@@ -225,40 +260,46 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvView c, const T *__r
                                                           int64_t n, int dim, LaunchCtx ctx) {
     pdl_wait();
     pdl_launch_dependents();
-    const int quads = c.kv_heads * dim / 4;  // of a token's keys, and of its values
-    const Spread sp(2 * quads);
-    if (sp.sub < 0) return;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * sp.par * kAhead + sp.sub; base < n;
+    const int eights = c.kv_heads * dim / 8;  // of a token's keys, and of its values
+    const Spread sp(2 * eights);
+    // all of a warp's threads go through the loops: they shuffle
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * sp.par * kAhead; base < n;
          base += static_cast<int64_t>(gridDim.x) * sp.par * kAhead) {
         int64_t slot[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int64_t token = base + u * sp.par;
-            slot[u] = token < n ? slots[token] : -1;
+            const int64_t token = base + sp.sub + u * sp.par;
+            slot[u] = token < n && sp.at < sp.per ? slots[token] : -1;
             if (slot[u] < -1 || slot[u] >= c.slots) {
                 record_error(ctx, kDevErrIndex);
                 slot[u] = -1;
             }
         }
-        for (int i = sp.at; i < sp.per; i += kThreads) {
-            const int half = i >= quads, at = i - half * quads;
-            const T *src = (half ? v : k) + at * 4;
+        for (int i0 = 0; i0 < sp.per; i0 += kThreads) {
+            const int i = i0 + sp.at;
+            const bool here = i < sp.per;
+            const int half = i >= eights, at = (i - half * eights) * 8;
+            const T *src = (half ? v : k) + at;
             const int64_t stride = half ? v_stride : k_stride;
-            float4 x[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                x[u] = slot[u] >= 0 ? load_quad<kWide>(src + (base + u * sp.par) * stride)
-                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const int head = at * 4 / dim, block = (at * 4 - head * dim) / kQK, lane8 = threadIdx.x & 7;
+            float x[kAhead][8];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (slot[u] < 0) continue;  // the whole warp: one token
-                float top = fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w));
-                float low = fminf(fminf(x[u].x, x[u].y), fminf(x[u].z, x[u].w));
-                // 0 * x is NaN for the values that a block cannot hold
-                float odd = 0.0f * x[u].x + 0.0f * x[u].y + (0.0f * x[u].z + 0.0f * x[u].w);
 #pragma unroll
-                for (int o = 4; o > 0; o >>= 1) {
+                for (int j = 0; j < 8; ++j) x[u][j] = 0.0f;
+                if (here && slot[u] >= 0) load_eight<kWide>(src + (base + sp.sub + u * sp.par) * stride, x[u]);
+            }
+            const int head = at / dim, in = at - head * dim, lane4 = threadIdx.x & 3;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                float top = x[u][0], low = x[u][0], odd = 0.0f * x[u][0];  // 0 x is NaN for what a block cannot hold
+#pragma unroll
+                for (int j = 1; j < 8; ++j) {
+                    top = fmaxf(top, x[u][j]);
+                    low = fminf(low, x[u][j]);
+                    odd = fmaf(0.0f, x[u][j], odd);
+                }
+#pragma unroll
+                for (int o = 2; o > 0; o >>= 1) {
                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
                     low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
                     odd += __shfl_xor_sync(0xFFFFFFFFu, odd, o);
@@ -266,18 +307,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvView c, const T *__r
                 const float e = top >= -low ? top : low;
                 const __half dh = __float2half_rn(fminf(fmaxf(e * -0.125f, -65504.0f), 65504.0f));
                 const float d = __half2float(dh);
-                uint32_t q = 0x08080808u;
+                uint32_t q[2] = {0x08080808u, 0x08080808u};
                 const bool finite = odd == 0.0f;
-                if (finite && d != 0.0f)
-                    q = code_of(x[u].x, d) | (code_of(x[u].y, d) << 8) | (code_of(x[u].z, d) << 16) |
-                        (code_of(x[u].w, d) << 24);
-                const uint32_t high = __shfl_down_sync(0xFFFFFFFFu, q, 4, 8);
+                if (finite && d != 0.0f) codes_of(x[u], d, q);
+                const uint32_t high0 = __shfl_down_sync(0xFFFFFFFFu, q[0], 2, 4);
+                const uint32_t high1 = __shfl_down_sync(0xFFFFFFFFu, q[1], 2, 4);
+                if (!here || slot[u] < 0) continue;
                 const int64_t row = cache_row(c, slot[u], head);
-                if (lane8 < 4)
-                    *reinterpret_cast<uint32_t *>((half ? c.v_codes : c.k_codes) + row * (dim / 2) + block * 16 + lane8 * 4) =
-                        q | (high << 4);
-                if (lane8 == 0)
-                    (half ? c.v_scales : c.k_scales)[row * (dim / kQK) + block] =
+                if (lane4 < 2)
+                    *reinterpret_cast<uint2 *>((half ? c.v_codes : c.k_codes) + row * (dim / 2) + (in / kQK) * 16 + lane4 * 8) =
+                        make_uint2(q[0] | (high0 << 4), q[1] | (high1 << 4));
+                if (lane4 == 0)
+                    (half ? c.v_scales : c.k_scales)[row * (dim / kQK) + in / kQK] =
                         finite ? dh : __ushort_as_half(static_cast<unsigned short>(0x7FFF));
             }
         }
@@ -285,18 +326,39 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvView c, const T *__r
 }
 
 // ---- read ----------------------------------------------------------------------
-// Eight lanes share a block, four consecutive values each (as dequant); keys
-// and values as two halves of a token where both are wanted.
+// Four lanes share a block: four bytes of codes each, which are four
+// consecutive values of its first half and four of its second; keys and values
+// as two halves of a token where both are wanted.  Bound by the bytes written.
+template <bool kWide>
+__device__ __forceinline__ void store_quad(float *dst, const float4 &y) {
+    if constexpr (kWide) {
+        *reinterpret_cast<float4 *>(dst) = y;
+    } else {
+        dst[0] = y.x;
+        dst[1] = y.y;
+        dst[2] = y.z;
+        dst[3] = y.w;
+    }
+}
+
+// (n - 8) f of four bytes: 2^23 + n - (2^23 + 8) is exact
+__device__ __forceinline__ float4 values_of(uint32_t q, float f) {
+    auto value = [&](uint32_t at) {
+        return (__uint_as_float(__byte_perm(q, 0x4B000000u, 0x7440u | at)) - 8388616.0f) * f;
+    };
+    return make_float4(value(0), value(1), value(2), value(3));
+}
+
 template <bool kWide, int kAhead>
-__global__ void __launch_bounds__(kThreads) read_kernel(KvView c, const int64_t *__restrict__ slots,
+__global__ void __launch_bounds__(kThreads, 5) read_kernel(KvView c, const int64_t *__restrict__ slots,
                                                         int64_t n, int dim, float *__restrict__ k_out,
                                                         float *__restrict__ v_out, LaunchCtx ctx) {
     pdl_wait();
     pdl_launch_dependents();
-    const int quads = c.kv_heads * dim / 4;
+    const int eights = c.kv_heads * dim / 8;
     const int only = k_out ? (v_out ? -1 : 0) : 1;  // the half that is wanted, or both
-    const Spread sp(only < 0 ? 2 * quads : quads);
-    if (sp.sub < 0) return;
+    const Spread sp(only < 0 ? 2 * eights : eights);
+    if (sp.at >= sp.per) return;
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * sp.par * kAhead + sp.sub; base < n;
          base += static_cast<int64_t>(gridDim.x) * sp.par * kAhead) {
         int64_t slot[kAhead];
@@ -310,8 +372,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(KvView c, const int64_t 
             }
         }
         for (int i = sp.at; i < sp.per; i += kThreads) {
-            const int half = only < 0 ? i >= quads : only, at = (only < 0 && half ? i - quads : i) * 4;
-            const int head = at / dim, in = at - head * dim;
+            const int half = only < 0 ? i >= eights : only, at = (only < 0 && half ? i - eights : i) * 8;
+            const int head = at / dim, block = (at - head * dim) / kQK, quad = (at & 31) / 2;  // 4 times the lane
+            const uint8_t *codes = half ? c.v_codes : c.k_codes;
+            const __half *scales = half ? c.v_scales : c.k_scales;
             uint32_t w[kAhead];
             __half d[kAhead];
 #pragma unroll
@@ -319,31 +383,20 @@ __global__ void __launch_bounds__(kThreads) read_kernel(KvView c, const int64_t 
                 w[u] = 0x88888888u;  // zeros for slots that are not there
                 d[u] = __ushort_as_half(0);
                 if (slot[u] >= 0) {
-                    const int64_t row = cache_row(c, slot[u], head);
-                    w[u] = *reinterpret_cast<const uint32_t *>((half ? c.v_codes : c.k_codes) + row * (dim / 2) + (in / kQK) * 16 + (in & 15));
-                    d[u] = (half ? c.v_scales : c.k_scales)[row * (dim / kQK) + in / kQK];
+                    const int64_t at_block = cache_row(c, slot[u], head) * (dim / kQK) + block;
+                    w[u] = *reinterpret_cast<const uint32_t *>(codes + at_block * 16 + quad);
+                    d[u] = scales[at_block];
                 }
             }
+            float *out = (half ? v_out : k_out) + (at & ~31) + quad;
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int64_t token = base + u * sp.par;
                 if (token >= n) break;
-                const uint32_t q = w[u] >> ((in & 16) ? 4 : 0);
                 const float f = __half2float(d[u]);
-                float4 y;
-                y.x = (static_cast<float>(q & 15u) - 8.0f) * f;
-                y.y = (static_cast<float>((q >> 8) & 15u) - 8.0f) * f;
-                y.z = (static_cast<float>((q >> 16) & 15u) - 8.0f) * f;
-                y.w = (static_cast<float>((q >> 24) & 15u) - 8.0f) * f;
-                float *dst = (half ? v_out : k_out) + token * quads * 4 + at;
-                if constexpr (kWide) {
-                    *reinterpret_cast<float4 *>(dst) = y;
-                } else {
-                    dst[0] = y.x;
-                    dst[1] = y.y;
-                    dst[2] = y.z;
-                    dst[3] = y.w;
-                }
+                float *dst = out + token * eights * 8;
+                store_quad<kWide>(dst, values_of(w[u] & 0x0F0F0F0Fu, f));
+                store_quad<kWide>(dst + 16, values_of((w[u] >> 4) & 0x0F0F0F0Fu, f));
             }
         }
     }
@@ -361,29 +414,29 @@ KvView view(const KvCache &c) {
     return v;
 }
 
-// CTAs for n tokens of `quads` quads each, `ahead` at a time, at most 32 per SM.
-unsigned grid_for(int64_t n, int quads, int ahead) {
-    const int64_t per_cta = static_cast<int64_t>(std::max(1, kThreads / quads)) * ahead;
+// CTAs for n tokens of `parts` parts each, `ahead` at a time, at most 32 per SM.
+unsigned grid_for(int64_t n, int parts, int ahead) {
+    const int64_t per_cta = static_cast<int64_t>(std::max(1, kThreads / parts)) * ahead;
     const int64_t cap = static_cast<int64_t>(device_sm_count()) * 32;
     return static_cast<unsigned>(std::min((n + per_cta - 1) / per_cta, cap));
 }
 
-// Whether CTAs of kMany tokens fill the GPU.
-bool many(int64_t n, int quads) {
-    return grid_for(n, quads, kMany) >= static_cast<unsigned>(2 * device_sm_count());
+// Whether CTAs of so many tokens a thread fill the GPU.
+bool many(int64_t n, int parts, int ahead) {
+    return grid_for(n, parts, ahead) >= static_cast<unsigned>(2 * device_sm_count());
 }
 
 template <typename T>
 cudaError_t launch_append(const KvCache &c, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                           const int64_t *slots, int64_t n, cudaStream_t stream, const LaunchCtx &ctx) {
-    constexpr uintptr_t quad = 4 * sizeof(T);
-    const bool wide = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % quad == 0 &&
-                      k_stride % 4 == 0 && v_stride % 4 == 0;
-    const int quads = c.kv_heads * c.head_dim / 2;
-    const bool more = many(n, quads);
-    auto *kernel = wide ? (more ? append_kernel<T, true, kMany> : append_kernel<T, true, 1>)
-                        : (more ? append_kernel<T, false, kMany> : append_kernel<T, false, 1>);
-    return launch_kernel(kernel, dim3(grid_for(n, quads, more ? kMany : 1)), dim3(kThreads), 0, stream, 1, view(c),
+    constexpr int64_t values = 16 / sizeof(T);
+    const bool wide = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 16 == 0 &&
+                      k_stride % values == 0 && v_stride % values == 0;
+    const int parts = c.kv_heads * c.head_dim / 4;
+    const bool more = many(n, parts, kAppendMany);
+    auto *kernel = wide ? (more ? append_kernel<T, true, kAppendMany> : append_kernel<T, true, 1>)
+                        : (more ? append_kernel<T, false, kAppendMany> : append_kernel<T, false, 1>);
+    return launch_kernel(kernel, dim3(grid_for(n, parts, more ? kAppendMany : 1)), dim3(kThreads), 0, stream, 1, view(c),
                          static_cast<const T *>(k), k_stride, static_cast<const T *>(v), v_stride, slots, n,
                          c.head_dim, ctx);
 }
@@ -417,11 +470,11 @@ cudaError_t launch_kv_append(const KvCache &c, const void *k, int64_t k_stride, 
 cudaError_t launch_kv_read(const KvCache &c, const int64_t *slots, int64_t n, float *k_out,
                            float *v_out, cudaStream_t stream, const LaunchCtx &ctx) {
     const bool wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 15) == 0;
-    const int quads = c.kv_heads * c.head_dim / 4 * (k_out && v_out ? 2 : 1);
-    const bool more = many(n, quads);
-    auto *kernel = wide ? (more ? read_kernel<true, kMany> : read_kernel<true, 1>)
-                        : (more ? read_kernel<false, kMany> : read_kernel<false, 1>);
-    return launch_kernel(kernel, dim3(grid_for(n, quads, more ? kMany : 1)), dim3(kThreads), 0, stream, 1, view(c),
+    const int parts = c.kv_heads * c.head_dim / 8 * (k_out && v_out ? 2 : 1);
+    const bool more = many(n, parts, kReadMany);
+    auto *kernel = wide ? (more ? read_kernel<true, kReadMany> : read_kernel<true, 1>)
+                        : (more ? read_kernel<false, kReadMany> : read_kernel<false, 1>);
+    return launch_kernel(kernel, dim3(grid_for(n, parts, more ? kReadMany : 1)), dim3(kThreads), 0, stream, 1, view(c),
                          slots, n, c.head_dim, k_out, v_out, ctx);
 }
 
