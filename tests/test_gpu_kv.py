@@ -254,3 +254,27 @@ def test_python_refusals(qmm):
     with pytest.raises(qmm.QmmError):
         bad = qmm.kv_cache_q4_0(1, 16, 2, 96)
         qmm.qmm_kv_read_q4_0(bad, s, torch.zeros(3, 2, 96).cuda(), None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_append_quotients_near_halves(qmm, dtype):
+    """Values at halves of the scale and a few units in the last place beside
+    them round as the fp32 quotient does, ties to even."""
+    rng = np.random.default_rng(12)
+    n, dim = 512, 256
+    d = np.abs(rng.standard_normal((n, 1, dim // 32, 1))).astype(np.float16).astype(np.float32)
+    x = (rng.integers(-8, 8, (n, 1, dim // 32, 32)) + 0.5).astype(np.float32) * d
+    x = (x.view(np.int32) + rng.integers(-3, 4, x.shape, dtype=np.int32)).view(np.float32)
+    x = np.clip(x, -8 * d, 8 * d)
+    x[..., 3] = (-8 * d)[..., 0]  # the extreme: the scale is d
+    t = torch.from_numpy(x.reshape(n, 1, dim))
+    t = t.bfloat16() if dtype == "bf16" else t
+    b = t.float().numpy().reshape(n, 1, -1, 32)
+    cache = qmm.kv_cache_q4_0(n // 64, 64, 1, dim)
+    qmm.qmm_kv_append_q4_0(cache, t.cuda(), t.cuda(), torch.arange(n).cuda())
+    kc, ks, vc, vs = (a.reshape(n, 1, -1) for a in cache_arrays(cache))
+    f = ks.astype(np.float32).reshape(n, 1, -1, 1)
+    assert np.array_equal(ks, vs) and np.array_equal(kc, vc)
+    assert np.array_equal(ks, ref.quantize(t.float().numpy())[1])
+    c = np.clip(np.rint(b / f) + 8, 0, 15).astype(np.uint8)
+    assert np.array_equal(kc, (c[..., :16] | (c[..., 16:] << 4)).reshape(kc.shape))
