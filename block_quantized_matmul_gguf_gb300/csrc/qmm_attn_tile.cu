@@ -15,27 +15,30 @@
 //             registers, to binary16 rows of 64 values with the 128-byte
 //             swizzle; K is then a K-major operand and V, its rows being keys
 //             too, an MN-major one of the same layout
-//   MMA       one thread; the products of tile t + 1 run while tile t is in
-//             the softmax
+//   MMA       one per 128 rows; S of the next tile is formed while a tile is
+//             in the softmax (head_dim 256), or the other rows' products run
 // Values keep the order in which a word of codes gives them (0 2 16 18 1 3 17
 // 19 and so on); Q is staged in that order and the outputs are put back.
 //
 // Precision: q, (n - 8) d and the weights are rounded once to binary16 each.
-// A tile's K and V are scaled by powers of two to below 2^-6 (16 where its
-// scales lie far apart), q per row to below 2^15 and the weights to at most
-// 2^15, so that nothing overflows; weights below 2^-38 of a row's largest fall
-// out of binary16's range, which shows only where the heavy keys' codes leave
-// (nearly) nothing: such rows are done again by all warps in fp32.
+// K and V are scaled by powers of two, one for the keys of each dequant warp,
+// to below 2^-6 (16 where the scales lie far apart), q per row to below 2^15
+// and the weights to at most 2^15, so that nothing overflows; weights below
+// 2^-38 of a row's largest fall out of binary16's range, which shows only
+// where the heavy keys' codes leave (nearly) nothing: such rows are done again
+// by all warps in fp32.
 //
 // Parts are joined by a second kernel: their outputs and sums, in fp32, are
 // weighted by 2^(m - largest m), in the parts' order.
 //
-// Bound by the issue slots of the dequantisation and the softmax beside the
-// products: about 2900 cycles a tile at head_dim 256, of which the products
-// take 1024.  Measured: 2048 tokens of 8 heads of 256 (2 key heads) behind
-// 6000 cached ones 181 us, 650 TFLOP/s; seven prompts of up to 700 tokens of
-// 16 heads of 128 with a window of 1024 keys 94 us; 128 tokens behind 32000
-// 75 us (777 with one CTA a block).
+// Bound by the chain of a tile's steps, which the two buffers of S overlap in
+// part: at head_dim 256 a tile takes 2400 cycles, its dequantisation 2200
+// (eight warps, two an SM quarter, that fill 64 KB of shared memory), its
+// softmax 1600, its products 1290 (48 cycles for 64 columns and 130 for 256,
+// as measured alone).  Measured: 2048 tokens of 8 heads of 256 (2 key heads)
+// behind 6000 cached ones 171 us, 690 TFLOP/s; seven prompts of up to 700
+// tokens of 16 heads of 128 with a window of 1024 keys 94 us; 128 tokens of
+// the first layout behind 32000 75 us (777 with one CTA a block).
 #include "qmm_attn.cuh"
 #include "qmm_tc.cuh"
 
@@ -59,7 +62,7 @@ struct Tile {
     static constexpr int bytes = kKeys * D * 2;
     static constexpr int softmax_warps = 4 * QT;
     static constexpr int mma_warp = softmax_warps + kDequantWarps;
-    static constexpr int threads = (mma_warp + 4) * 32;  // whole warpgroups: three warps only hold registers
+    static constexpr int threads = (mma_warp + 4) * 32;  // whole warpgroups: the last warps only hold registers
     // registers of a thread: at launch, and by role (at most as many in all:
     // 512 x 128 >= 128 x (208 + 2 x 104 + 56), 640 x 96 >= 128 x (2 x 144 + 2 x 72 + 40))
     static constexpr int launch_regs = D == 256 ? 128 : 96;
@@ -73,13 +76,18 @@ struct Tile {
     static constexpr int o_col = 0, q_col = QT * D, s_col = q_col + QT * D / 2;
     static constexpr uint32_t tmem_cols = 512;
     static_assert(s_col + 2 * kKeys <= 512, "tensor memory");
+    // S buffer of tile t for row tile qt (two in all), and the parity of its use
+    static constexpr __host__ __device__ int buffer(int t, int qt) { return QT == 1 ? t & 1 : qt; }
+    static constexpr __host__ __device__ uint32_t phase(int t) { return (QT == 1 ? t >> 1 : t) & 1; }
 };
 
+// What the softmax has to know of a tile, by groups of eight keys.
 struct TileInfo {
-    int k_exp, v_exp;      // K and V of the tile are scaled by 2^-exp
-    int far;               // V's values may reach 16, not 2^-6
+    float k_unit[8];       // K of a group is scaled by 1 / k_unit
+    int v_exp[8];          // V by 2^-(v_exp / 2); odd where its values may reach 16, not 2^-6
     uint32_t lost;         // 16-key groups without a page
     uint32_t odd[2];       // keys whose V holds a NaN or an infinity
+    uint32_t pad;
 };
 
 // Rows of one request and key head, and the tiles of their keys: all, or a part.
@@ -110,9 +118,8 @@ constexpr int kMinPart = 8;  // tiles of a part at least: about what a CTA takes
 
 struct TileShared {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_ready, final;
-    TileInfo info[kRing];
-    alignas(16) uint32_t exps[2][2][kDequantWarps];  // [tile parity][K, V][warp]
+    uint64_t s_full[2], p_full[2], pv_done[2], final[2], q_ready;
+    alignas(16) TileInfo info[kRing];
     int64_t scratch[32];
     int64_t blocks[kMaxThreads];  // row blocks before each thread's requests
     Block block;
@@ -382,10 +389,14 @@ constexpr int kNear = 10, kNearSpan = 6;  // near: exponents of a tile's scales 
 
 // What a dequant thread holds of one tile: its key's blocks.
 template <int D>
-struct Held {
-    uint4 codes[2][Tile<D>::units];
-    uint16_t scale[2][Tile<D>::units];
-    bool there;
+struct Codes {
+    uint4 of[2][Tile<D>::units];
+};
+template <int D>
+struct Scales {
+    uint16_t of[2][Tile<D>::units];
+    int64_t row;   // of the cache
+    bool there, lost;  // the key has a page; or should have
 };
 
 template <int D>
@@ -404,93 +415,94 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
         if (t >= bk.tiles || k < bk.lo || k >= bk.hi) return -2;  // no key
         return table[k >> p.page_shift];
     };
-    auto load = [&](int t, int32_t page, Held<D> &h) {
+    auto load_scales = [&](int t, int32_t page, Scales<D> &h) {
         const int k = bk.key0 + t * kKeys + key;
         h.there = page >= 0 && page < p.num_pages;
-        const int64_t row = h.there ? (((page * p.kv_heads) + bk.kv_head) << p.page_shift) + (k & ((1 << p.page_shift) - 1)) : 0;
+        h.lost = !h.there && page != -2;
+        h.row = h.there ? (((page * p.kv_heads) + bk.kv_head) << p.page_shift) + (k & ((1 << p.page_shift) - 1)) : 0;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                h.codes[half][u] = make_uint4(0u, 0u, 0u, 0u);
-                h.scale[half][u] = 0;
-                if (h.there && half >= half0 && half < half1) {
-                    const int b = block + 4 * u;
-                    h.codes[half][u] = __ldg(reinterpret_cast<const uint4 *>((half ? p.v_codes : p.k_codes) + row * (D / 2)) + b);
-                    h.scale[half][u] = __ldg(reinterpret_cast<const uint16_t *>(half ? p.v_scales : p.k_scales) + row * NB + b);
-                }
+                h.of[half][u] = 0;
+                if (h.there && half >= half0 && half < half1)
+                    h.of[half][u] = __ldg(reinterpret_cast<const uint16_t *>(half ? p.v_scales : p.k_scales) + h.row * NB + block + 4 * u);
             }
-        }
     };
-    int32_t page = page_of(0), page_next = page_of(1);
-    Held<D> next;
-    load(0, page, next);
+    auto load_codes = [&](const Scales<D> &h, Codes<D> &c) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                c.of[half][u] = make_uint4(0u, 0u, 0u, 0u);
+                if (h.there && half >= half0 && half < half1)
+                    c.of[half][u] = __ldg(reinterpret_cast<const uint4 *>((half ? p.v_codes : p.k_codes) + h.row * (D / 2)) + block + 4 * u);
+            }
+    };
+    // codes a tile ahead, scales two, pages three
+    int32_t page = page_of(2);
+    Scales<D> scales, scales1, scales2;
+    Codes<D> next;
+    load_scales(0, page_of(0), scales1);
+    load_scales(1, page_of(1), scales2);
+    load_codes(scales1, next);
     int stage = 0;
     uint32_t phase = 0;
-    bool live = true;
     for (int t = 0; t < bk.tiles; ++t) {
-        Held<D> cur = next;
-        const int32_t page_here = page;
-        page = page_next;
-        page_next = page_of(t + 2);
-        load(t + 1, page, next);
-        // the tile's largest scales
+        const Codes<D> cur = next;
+        scales = scales1;
+        scales1 = scales2;
+        load_codes(scales1, next);
+        load_scales(t + 2, page, scales2);
+        page = page_of(t + 3);
+        // the warp's keys have one power of two for K and one for V, from the
+        // largest and smallest scale: bits of binary16 order as the numbers do
         TileInfo &info = sh.info[t % kRing];
         int e[2];
         bool near[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            // exponents of the largest and the smallest that is not 0, 64 more
-            uint32_t top = 0, low = 127;
+            uint32_t top = 0, low = 0x7FFF;  // low: of those that are not 0
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                uint32_t bits = cur.scale[half][u] & 0x7FFFu;
+                uint32_t bits = scales.of[half][u] & 0x7FFFu;
                 if (bits >= 0x7C00u) {
-                    if (half && cur.there) atomicOr(&info.odd[key >> 5], 1u << (key & 31));
+                    if (half && scales.there) atomicOr(&info.odd[key >> 5], 1u << (key & 31));
                     bits = 0;  // NaN and infinity do not set the scale
                 }
-                if (bits) {
-                    const uint32_t x = 64 + exponent(__half2float(__ushort_as_half(static_cast<unsigned short>(bits))));
-                    top = max(top, x);
-                    low = min(low, x);
-                }
+                top = max(top, bits);
+                low = min(low, bits ? bits : 0x7FFFu);
             }
             top = __reduce_max_sync(0xFFFFFFFFu, top);
             low = __reduce_min_sync(0xFFFFFFFFu, low);
-            if (lane == 0) sh.exps[t & 1][half][w8] = top | (127 - low) << 16;
+            auto scale_of = [](uint32_t bits) { return exponent(__half2float(__ushort_as_half(static_cast<unsigned short>(bits)))); };
+            e[half] = top ? scale_of(top) : -24;
+            near[half] = !top || e[half] - scale_of(low) <= kNearSpan;
         }
-        const unsigned gone = __ballot_sync(0xFFFFFFFFu, !cur.there && page_here != -2);
-        if (gone && lane == 0) {
+        if (__any_sync(0xFFFFFFFFu, scales.lost) && lane == 0) {
             record_error(p.ctx, kDevErrIndex);
             atomicOr(&info.lost, 1u << (key >> 4));  // lane 0's key: the warp's keys lie in one group
         }
-        asm volatile("bar.sync 1, %0;" ::"r"(kDequantWarps * 32) : "memory");
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            // two 16-bit maxima at once
-            const uint4 *from = reinterpret_cast<const uint4 *>(sh.exps[t & 1][half]);
-            uint4 x = from[D == 64 ? half : 0];
-            if constexpr (D != 64) {
-                const uint4 y = from[1];
-                x = make_uint4(__vmaxu2(x.x, y.x), __vmaxu2(x.y, y.y), __vmaxu2(x.z, y.z), __vmaxu2(x.w, y.w));
+        if (lane == 0) {
+            const float k_unit = pow2i(e[0] + (near[0] ? kNear : 0));
+            const int v_exp = near[1] ? 2 * (e[1] + kNear) : 2 * e[1] + 1;
+            if constexpr (D == 64) {
+                if (half0 == 0)
+                    info.k_unit[2 * w8] = info.k_unit[2 * w8 + 1] = k_unit;
+                else
+                    info.v_exp[2 * w8 - 8] = info.v_exp[2 * w8 - 7] = v_exp;
+            } else {
+                info.k_unit[w8] = k_unit;
+                info.v_exp[w8] = v_exp;
             }
-            const uint32_t both = __vmaxu2(__vmaxu2(x.x, x.y), __vmaxu2(x.z, x.w));
-            const int top = both & 0xFFFF, low = 127 - static_cast<int>(both >> 16);
-            e[half] = top ? top - 64 : -24;
-            near[half] = top - low <= kNearSpan;  // also where all are 0
+            if (w8 == 0) {  // not in use: the warps' and the readers' tiles lie less apart
+                TileInfo &later = sh.info[(t + kRing / 2) % kRing];
+                later.lost = later.odd[0] = later.odd[1] = 0;
+            }
         }
-        if (w8 == 0 && lane == 0) {
-            info.k_exp = e[0] + (near[0] ? kNear : 0);
-            info.v_exp = e[1] + (near[1] ? kNear : 0);
-            info.far = !near[1];
-            TileInfo &later = sh.info[(t + kRing / 2) % kRing];  // not in use: readers lag by less
-            later.lost = later.odd[0] = later.odd[1] = 0;
-        }
-        // after a wait that gave up, the warp goes on without waiting: the
-        // others expect it at the barrier above
-        if (live)
-            live = warp_wait_or_abort(smem_addr(sh.k_empty + stage), phase ^ 1u, &sh.abort, p.ctx) &&
-                   warp_wait_or_abort(smem_addr(sh.v_empty + stage), phase ^ 1u, &sh.abort, p.ctx);
+        if (!warp_wait_or_abort(smem_addr(sh.k_empty + stage), phase ^ 1u, &sh.abort, p.ctx) ||
+            !warp_wait_or_abort(smem_addr(sh.v_empty + stage), phase ^ 1u, &sh.abort, p.ctx))
+            break;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             if (half < half0 || half >= half1) continue;
@@ -498,14 +510,14 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int b = block + 4 * u;
-                float d = __half2float(__ushort_as_half(cur.scale[half][u]));
+                float d = __half2float(__ushort_as_half(scales.of[half][u]));
                 if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd
                 d *= pow2i(-e[half]);
                 uint4 out[4];
                 if (near[half])
-                    dequant_near(cur.codes[half][u], d, out);
+                    dequant_near(cur.of[half][u], d, out);
                 else
-                    dequant_far(cur.codes[half][u], d, out);
+                    dequant_far(cur.of[half][u], d, out);
                 uint8_t *panel = rows + (b >> 1) * kPanel;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -527,50 +539,75 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
 
 // ---- the products --------------------------------------------------------------------
 
+// One lane of a warp, the same each time.
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
+// By the elected lane; the whole warp comes here with the same operands.
+__device__ __forceinline__ void product(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void products_done(uint32_t one, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
+        : "memory");
+}
+
+// The whole warp, so that the operands are known to be the same for all lanes:
+// a thread on its own has to move each to the uniform registers that the
+// products take theirs from.
 template <int D>
-__device__ __forceinline__ void mma_role(const TileParams &p, TileShared &sh, uint32_t smem, uint32_t tmem) {
+__device__ __forceinline__ void mma_role(const TileParams &p, TileShared &sh, uint32_t smem_in, uint32_t tmem_in, int qt) {
     using T = Tile<D>;
-    const int jobs = sh.block.tiles * T::QT;
+    const uint32_t smem = __shfl_sync(0xFFFFFFFFu, smem_in, 0), tmem = __shfl_sync(0xFFFFFFFFu, tmem_in, 0);
+    const int tiles = __shfl_sync(0xFFFFFFFFu, sh.block.tiles, 0);
+    constexpr int ahead = 2 / T::QT;  // S buffers of a row tile: S of so many tiles is formed ahead
     constexpr uint32_t qk_desc = tile_idesc(kKeys, false), pv_desc = tile_idesc(D, true);
+    const uint32_t one = elected();
     int *abort = &sh.abort;
     bool issued = false;
-    // job j: rows tile j % QT with key tile j / QT, S buffer j % 2
-    auto qk = [&](int j) -> bool {
-        const int t = j / T::QT, qt = j % T::QT, stage = t % T::stages;
-        if (qt == 0 && !wait_or_abort(smem_addr(sh.k_full + stage), (t / T::stages) & 1u, abort, p.ctx)) return false;
+    auto qk = [&](int t) -> bool {
+        const int stage = t % T::stages, buf = T::buffer(t, qt);
+        if (!warp_wait_or_abort(smem_addr(sh.k_full + stage), (t / T::stages) & 1u, abort, p.ctx)) return false;
         tc_fence_after();
         const uint64_t b0 = sw128_desc(smem + stage * T::bytes);
+        const uint32_t to = tmem + T::s_col + buf * kKeys, from = tmem + T::q_col + qt * (D / 2);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
-            umma_bf16_cta_ta(tmem + T::s_col + (j & 1) * kKeys, tmem + T::q_col + qt * (D / 2) + s * 8,
-                             b0 + (((s >> 2) * kPanel + (s & 3) * 32) >> 4), qk_desc, s > 0);
+            product(one, to, from + s * 8, b0 + (((s >> 2) * kPanel + (s & 3) * 32) >> 4), qk_desc, s > 0);
         issued = true;
-        umma_commit_cta(smem_addr(sh.s_full + (j & 1)));
-        if (qt == T::QT - 1) umma_commit_cta(smem_addr(sh.k_empty + stage));
+        products_done(one, smem_addr(sh.s_full + buf));
+        products_done(one, smem_addr(sh.k_empty + stage));
         return true;
     };
-    bool ok = jobs == 0 || wait_or_abort(smem_addr(&sh.q_ready), 0, abort, p.ctx);
-    if (ok && jobs > 0) ok = qk(0);
-    if (ok && jobs > 1) ok = qk(1);
-    for (int j = 0; ok && j < jobs; ++j) {
-        const int t = j / T::QT, qt = j % T::QT, stage = t % T::stages;
-        if (!wait_or_abort(smem_addr(sh.p_full + (j & 1)), (j >> 1) & 1u, abort, p.ctx)) break;
-        if (qt == 0 && !wait_or_abort(smem_addr(sh.v_full + stage), (t / T::stages) & 1u, abort, p.ctx)) break;
+    bool ok = tiles == 0 || warp_wait_or_abort(smem_addr(&sh.q_ready), 0, abort, p.ctx);
+    for (int t = 0; ok && t < min(ahead, tiles); ++t) ok = qk(t);
+    for (int t = 0; ok && t < tiles; ++t) {
+        const int stage = t % T::stages, buf = T::buffer(t, qt);
+        if (!warp_wait_or_abort(smem_addr(sh.p_full + buf), T::phase(t), abort, p.ctx)) break;
+        if (!warp_wait_or_abort(smem_addr(sh.v_full + stage), (t / T::stages) & 1u, abort, p.ctx)) break;
         tc_fence_after();
         const uint64_t b0 = rows_desc(smem + (T::stages + stage) * T::bytes);
+        const uint32_t to = tmem + T::o_col + qt * D, from = tmem + T::s_col + buf * kKeys;
 #pragma unroll
-        for (int s = 0; s < kKeys / 16; ++s)
-            umma_bf16_cta_ta(tmem + T::o_col + qt * D, tmem + T::s_col + (j & 1) * kKeys + s * 8, b0 + ((s * 2048) >> 4),
-                             pv_desc, t > 0 || s > 0);
-        umma_commit_cta(smem_addr(sh.pv_done + qt));
-        if (qt == T::QT - 1) umma_commit_cta(smem_addr(sh.v_empty + stage));
+        for (int s = 0; s < kKeys / 16; ++s) product(one, to, from + s * 8, b0 + ((s * 2048) >> 4), pv_desc, t > 0 || s > 0);
+        products_done(one, smem_addr(sh.pv_done + qt));
+        products_done(one, smem_addr(sh.v_empty + stage));
         // the next S goes where P lies, once its product has read it (products
         // with different accumulators are not ordered among themselves)
-        if (j + 2 < jobs) ok = wait_or_abort(smem_addr(sh.pv_done + qt), t & 1u, abort, p.ctx) && qk(j + 2);
+        if (t + ahead < tiles) ok = warp_wait_or_abort(smem_addr(sh.pv_done + qt), t & 1u, abort, p.ctx) && qk(t + ahead);
     }
     if (issued) {  // all products end before tensor memory is freed
-        umma_commit_cta(smem_addr(&sh.final));
-        wait_drain(smem_addr(&sh.final), 0, p.ctx);
+        products_done(one, smem_addr(sh.final + qt));
+        wait_drain(smem_addr(sh.final + qt), 0, p.ctx);
     }
 }
 
@@ -711,19 +748,28 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
     bool faint = false, far = false;  // a weight fell below binary16's normal numbers; a tile was far
     bool ok = true;
     for (int t = 0; t < bk.tiles; ++t) {
-        const int j = t * T::QT + qt;
-        if (!warp_wait_or_abort(smem_addr(sh.s_full + (j & 1)), (j >> 1) & 1u, &sh.abort, p.ctx) ||
+        const int buf = T::buffer(t, qt);
+        if (!warp_wait_or_abort(smem_addr(sh.s_full + buf), T::phase(t), &sh.abort, p.ctx) ||
             !warp_wait_or_abort(smem_addr(sh.v_full + t % T::stages), (t / T::stages) & 1u, &sh.abort, p.ctx)) {
             ok = false;
             break;
         }
         tc_fence_after();
-        const uint32_t s_at = tmem + lanes + T::s_col + (j & 1) * kKeys;
+        const uint32_t s_at = tmem + lanes + T::s_col + buf * kKeys;
         uint32_t s[64];
         tmem_ld_64cols(s_at, s);
         const TileInfo &info = sh.info[t % kRing];
-        const float u = unit * pow2i(info.k_exp);
-        far |= info.far;
+        float u[8];
+        int v_exp[8], most_exp = -0x10000;
+#pragma unroll
+        for (int g = 0; g < 8; g += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(info.k_unit + g);
+            const int4 e = *reinterpret_cast<const int4 *>(info.v_exp + g);
+            u[g] = unit * f.x, u[g + 1] = unit * f.y, u[g + 2] = unit * f.z, u[g + 3] = unit * f.w;
+            far |= (e.x | e.y | e.z | e.w) & 1;
+            v_exp[g] = e.x >> 1, v_exp[g + 1] = e.y >> 1, v_exp[g + 2] = e.z >> 1, v_exp[g + 3] = e.w >> 1;
+            most_exp = max(max(most_exp, max(v_exp[g], v_exp[g + 1])), max(v_exp[g + 2], v_exp[g + 3]));
+        }
         const int key0 = bk.key0 + t * kKeys;
         const bool edge = info.lost || info.odd[0] || info.odd[1] || key0 < bk.lo_all || key0 + kKeys > bk.hi_all;
         if (edge) {
@@ -734,22 +780,18 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                 if (key0 + i < lo || key0 + i >= hi || ((lost >> (i >> 4)) & 1u)) s[i] = 0xFF800000u;
             }
         }
-        float most[4];
+        float here = ninf;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) most[i] = __uint_as_float(s[i]);
+        for (int g = 0; g < 8; ++g) {
+            float most = __uint_as_float(s[8 * g]);
 #pragma unroll
-        for (int i = 4; i < 60; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                most[k] = fmaxf(most[k], fmaxf(__uint_as_float(s[i + k]), __uint_as_float(s[i + 4 + k])));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) most[k] = fmaxf(most[k], __uint_as_float(s[60 + k]));
-        const float big = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-        const float here = big * u;
+            for (int k = 1; k < 7; k += 2) most = fmaxf(most, fmaxf(__uint_as_float(s[8 * g + k]), __uint_as_float(s[8 * g + k + 1])));
+            here = fmaxf(here, fmaxf(most, __uint_as_float(s[8 * g + 7])) * u[g]);
+        }
         // a new reference where the largest weight would pass 2^15, and where
         // V's unit grows
         const bool grow = here > top + kSlack;
-        const int e_now = max(e_ref, info.v_exp);
+        const int e_now = max(e_ref, most_exp);
         const float now = grow || top == ninf ? fmaxf(top, here) : top;
         if (__any_sync(0xFFFFFFFFu, now != top || e_now != e_ref)) {
             const float f = top == ninf ? 0.0f : exp2_fast(top - now);
@@ -777,26 +819,33 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             top = now;
             e_ref = e_now;
         }
-        const int shift = info.v_exp - e_ref;
-        const float base = static_cast<float>(kRaise + shift) - (top == ninf ? 0.0f : top);
+        const float top_here = top == ninf ? 0.0f : top;
+        float base[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) base[g] = static_cast<float>(kRaise + v_exp[g] - e_ref) - top_here;
         if (edge) {  // hidden keys' weights are 0 and do not count
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-                faint |= s[i] != 0xFF800000u && fmaf(__uint_as_float(s[i]), u, base) < -14.0f;
+                faint |= s[i] != 0xFF800000u && fmaf(__uint_as_float(s[i]), u[i >> 3], base[i >> 3]) < -14.0f;
         }
-        float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         uint32_t least[2] = {0x7C007C00u, 0x7C007C00u};  // smallest weights
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 arg = __ffma2_rn(make_float2(__uint_as_float(s[32 * h + 2 * i]), __uint_as_float(s[32 * h + 2 * i + 1])),
-                                              make_float2(u, u), make_float2(base, base));
-                const float x = exp2_fast(arg.x), y = exp2_fast(arg.y);
-                add[i & 1] = __fadd2_rn(add[i & 1], make_float2(x, y));
-                w[i] = pack_rn(x, y);
-                least[i & 1] = hmin2(least[i & 1], w[i]);
+            for (int g = 4 * h; g < 4 * h + 4; ++g) {
+                float2 add = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 arg = __ffma2_rn(make_float2(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1])),
+                                                  make_float2(u[g], u[g]), make_float2(base[g], base[g]));
+                    const float2 x = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
+                    add = i == 0 ? x : __fadd2_rn(add, x);
+                    const uint32_t both = pack_rn(x.x, x.y);
+                    w[4 * (g & 3) + i] = both;
+                    least[i & 1] = hmin2(least[i & 1], both);
+                }
+                sum = fmaf(add.x + add.y, pow2i(e_ref - kRaise - v_exp[g]), sum);
             }
             tmem_st_16cols(s_at + 16 * h, w);
         }
@@ -808,11 +857,10 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             ok = false;
             break;
         }
-        sum = fmaf((add[0].x + add[0].y) + (add[1].x + add[1].y), pow2i(-kRaise - shift), sum);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_addr(smem_addr(sh.p_full + (j & 1)));
+        if (lane == 0) mbar_arrive_addr(smem_addr(sh.p_full + buf));
     }
 
     // outputs
@@ -970,17 +1018,17 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
     if (threadIdx.x == T::mma_warp * 32) {
         for (int i = 0; i < T::stages; ++i) {
             mbar_init(sh.k_full + i, kDequantWarps);
-            mbar_init(sh.k_empty + i, 1);
+            mbar_init(sh.k_empty + i, T::QT);
             mbar_init(sh.v_full + i, kDequantWarps);
-            mbar_init(sh.v_empty + i, 1);
+            mbar_init(sh.v_empty + i, T::QT);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sh.s_full + i, 1);
             mbar_init(sh.p_full + i, 4);
             mbar_init(sh.pv_done + i, 1);
+            mbar_init(sh.final + i, 1);
         }
         mbar_init(&sh.q_ready, T::softmax_warps);
-        mbar_init(&sh.final, 1);
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -1004,7 +1052,7 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
         dequant_role<D>(p, sh, smem, warp - T::softmax_warps, lane);
     } else {
         registers_down<T::mma_regs>();
-        if (warp == T::mma_warp && lane == 0) mma_role<D>(p, sh, smem_addr(smem), tmem);
+        if (warp < T::mma_warp + T::QT) mma_role<D>(p, sh, smem_addr(smem), tmem, warp - T::mma_warp);
         __syncwarp();
     }
     tc_fence_before();
