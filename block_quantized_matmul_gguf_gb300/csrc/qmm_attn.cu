@@ -1384,9 +1384,17 @@ cudaError_t launch_stream(const KvCache &c, const AttnArgs &a, cudaStream_t stre
 template <int D>
 cudaError_t launch_dim(const KvCache &c, const AttnArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
     if (a.out_bf16) return launch_stream<D, 1, false>(c, a, stream, ctx);
-    // four rows fill a column tile; with more, two tiles share the codes' work
-    if (static_cast<int64_t>(a.max_q) * (a.heads / c.kv_heads) <= 4) return launch_stream<D, 1, true>(c, a, stream, ctx);
-    return launch_stream<D, 2, true>(c, a, stream, ctx);
+    // Four rows fill a column tile; two tiles share the codes' work, but take
+    // registers from the overlap of tiles.  Us per call with one / two, two
+    // key heads: head_dim 128, 16 requests of 4000 keys: 2 rows 15 / 17, 16
+    // rows 28 / 27; 32 rows of one with 16000 keys 22 / 21, 256 rows 76 / 61,
+    // 2048 rows 499 / 350; head_dim 64, 16 rows 20 / 23, 256 rows 47 / 45, 2048
+    // rows 266 / 214.  head_dim 256, where two tiles' outputs are 256
+    // registers: 4 rows 17 / 26, 8 rows 28 / 43, 256 rows 134 / 146, 2048 rows
+    // 933 / 999.
+    if constexpr (D < 256)
+        if (static_cast<int64_t>(a.max_q) * (a.heads / c.kv_heads) >= 32) return launch_stream<D, 2, true>(c, a, stream, ctx);
+    return launch_stream<D, 1, true>(c, a, stream, ctx);
 }
 
 }  // namespace
