@@ -390,10 +390,14 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_q4_0 *cache, const int64_t *slots, int6
  * q_start[batch] to total_q are not written.  A page index outside the
  * cache, a kv_len beyond the table, more than max_q tokens or a row beyond
  * total_q record QMM_ERR_INDEX; the keys or rows concerned are left out.
- * Arithmetic: scores, softmax statistics and sums in fp32 and the cached
- * values exact.  With out_type QMM_F32, q and the softmax weights enter the
- * products in two binary16 parts (22 bits); with QMM_BF16, in one (11 bits),
- * below the rounding of the output.
+ * Arithmetic: scores, softmax statistics and sums in fp32.  With out_type
+ * QMM_F32 the cached values are exact, and q and the softmax weights enter
+ * the products in two binary16 parts (22 bits).  With QMM_BF16 q and the
+ * weights enter in one (11 bits), below the rounding of the output; calls of
+ * many rows (prompts) also round each cached value to binary16 once, which
+ * the output does not show either but lse does (about 2e-6 of it).  Which
+ * form a call takes depends on its host-side arguments alone, and equal
+ * calls give equal bits.
  * Requires heads a multiple of kv_heads, heads <= 1024, batch and max_q >= 1,
  * total_q >= 0 (0 launches nothing), window >= 0 and 0 unless causal, scale
  * finite, strides at least heads * head_dim, pointers aligned to their type;
