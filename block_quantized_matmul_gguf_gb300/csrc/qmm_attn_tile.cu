@@ -1218,7 +1218,7 @@ __global__ void __launch_bounds__(Join<D>::warps * 32) attn_tile_join_kernel(con
 // time.
 constexpr int kWholeTiles = 32;
 
-int tile_sms() { return std::min(device_sm_count(), kMaxTileCtas); }
+int tile_sms() { return std::min(std::max(device_sm_count(), 2), kMaxTileCtas); }
 size_t parts_bytes(int sms) { return (sizeof(TileHeader) + sms * sizeof(TileParts) + 255) / 256 * 256; }
 
 // Keys that a block of so many rows can see.
