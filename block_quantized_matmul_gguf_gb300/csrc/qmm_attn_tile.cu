@@ -1274,12 +1274,13 @@ cudaError_t launch_tiles(const KvCache &c, const AttnArgs &a, cudaStream_t strea
 // The streaming form works on 8 query rows of a request and key head at a
 // time, this one on 128 or 256, whether they are there or not.  Picoseconds
 // that a tile of 64 keys costs the whole GPU in either form:
-//   head_dim 256  stream 3000, tiles 12000;  128  1400, 11500;  64  850, 10200
+//   head_dim 256  stream 3000, tiles 9500;  128  1400, 11500;  64  850, 10200
 // and 9 us that this form takes longer to begin and end.  They follow from
 // (us per call, two key heads, stream / tiles):
-//   head_dim 256, one request: 64 rows with 4000 keys 29 / 42, with 32000
-//   60 / 54, 512 rows with 32000 223 / 75, 2048 rows with 32000 786 / 214;
-//   64 requests with 4000 keys: 16 rows 93 / 119, 32 rows 116 / 115, 64 rows 194 / 120
+//   head_dim 256, one request: 64 rows with 4000 keys 30 / 40, with 32000
+//   60 / 58, 512 rows with 32000 223 / 75, 2048 rows with 32000 788 / 208;
+//   64 requests with 4000 keys: 16 rows 93 / 112, 32 rows 116 / 110, 64 rows
+//   193 / 111, and 32 rows of one key head 83 / 64
 //   head_dim 128: 64 rows of 64 requests with 4000 keys 96 / 119, 256 rows with
 //   32000 keys 78 / 51;  head_dim 64, the same two: 68 / 107, 56 / 44
 // The requests' lengths are not known here: the table's width stands for
@@ -1291,7 +1292,7 @@ bool attn_tiles_pay(const KvCache &c, const AttnArgs &a) {
     const int64_t groups = a.batch * ((each + 7) / 8);
     const int64_t blocks = std::max(a.batch * ((each + rows - 1) / rows), a.batch - 1 + (most + rows - 1) / rows);
     const double stream = c.head_dim == 256 ? 3000 : c.head_dim == 128 ? 1400 : 850;
-    const double tiles = c.head_dim == 256 ? 12000 : c.head_dim == 128 ? 11500 : 10200;
+    const double tiles = c.head_dim == 256 ? 9500 : c.head_dim == 128 ? 11500 : 10200;
     const double keys = static_cast<double>(c.kv_heads) * static_cast<double>(key_bound(c, a, static_cast<int>(rows))) / kKeys;
     return keys * (static_cast<double>(groups) * stream - static_cast<double>(blocks) * tiles) > 9e6;
 }
