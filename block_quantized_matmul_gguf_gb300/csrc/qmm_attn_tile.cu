@@ -320,8 +320,14 @@ __device__ __forceinline__ void find_block(const TileParams &p, TileShared &sh) 
     }
     int64_t ctas;
     int64_t before = sum_before<threads>(sh, count, ctas);
-    if (threadIdx.x == 0 && blockIdx.x == 0) p.header->used = static_cast<int>(ctas >> 32);
-    if (i0 < i1 && blockIdx.x >= static_cast<uint32_t>(before) && blockIdx.x < static_cast<uint32_t>(before + count)) {
+    // Rows that requests claim twice can make the plan larger than the grid,
+    // which is sized by total_q: parts that no CTA writes must not be joined.
+    const bool fits = static_cast<uint32_t>(ctas) <= gridDim.x;
+    if (threadIdx.x == 0 && blockIdx.x == 0) {
+        p.header->used = fits ? static_cast<int>(ctas >> 32) : 0;
+        if (!fits) record_error(p.ctx, kDevErrIndex);
+    }
+    if (fits && i0 < i1 && blockIdx.x >= static_cast<uint32_t>(before) && blockIdx.x < static_cast<uint32_t>(before + count)) {
         Walk<D> w = first;
         for (int64_t i = i0; i < i1; ++i, w.next(p)) {
             Block k = w.block(p, 0);

@@ -389,7 +389,9 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_q4_0 *cache, const int64_t *slots, int6
  * call may be captured in a graph and replayed for other lengths.  Rows from
  * q_start[batch] to total_q are not written.  A page index outside the
  * cache, a kv_len beyond the table, more than max_q tokens or a row beyond
- * total_q record QMM_ERR_INDEX; the keys or rows concerned are left out.
+ * total_q record QMM_ERR_INDEX; the keys or rows concerned are left out.  So
+ * does a q_start that descends: requests then claim rows twice, and any row
+ * of out and lse may be left as it was.
  * Arithmetic: scores, softmax statistics and sums in fp32.  With out_type
  * QMM_F32 the cached values are exact, and q and the softmax weights enter
  * the products in two binary16 parts (22 bits).  With QMM_BF16 q and the

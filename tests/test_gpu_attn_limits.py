@@ -1,0 +1,40 @@
+"""Attention at the ends of its arguments, in both forms (tables of the
+requests' own width, and wide ones, which select the form of many rows)."""
+import numpy as np
+import pytest
+
+import serving_ref as ref
+import test_gpu_attn as base
+from test_gpu_attn_prompts import Wide
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+qmm = base.qmm
+FORMS = [(base.Case, F32), (base.Case, BF16), (Wide, BF16)]
+
+
+# --- M1
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("starts", [[0, 1000, 0, 1000], [0, 1000, 0, 1000, 0, 1000, 0, 1000]])
+def test_rows_claimed_twice_keep_to_their_arrays(qmm, dim, starts):
+    """Each way back claims all rows again, which makes more blocks and parts
+    than total_q lets the launch expect: nothing outside the rows is written
+    and the error is recorded."""
+    rows, batch = 1000, len(starts) - 1
+    lens = [rows if i % 2 == 0 else 0 for i in range(batch - 1)] + [32000]
+    c = base.Case(qmm, lens, [rows] + [0] * (batch - 1), 8, 2, dim, 64, seed=dim, q_type=BF16)
+    c.dev["q_start"] = torch.tensor(starts, dtype=torch.int32).cuda()
+    guard, q = 64, c.q.cuda()
+    out = torch.full((rows + 2 * guard, 8, dim), 7.0, dtype=BF16).cuda()
+    lse = torch.full((rows + 2 * guard, 8), 7.0).cuda()
+    ws = qmm.attn_workspace(c.cache, 8)
+    space = torch.full((ws.numel() + 512,), 255, dtype=torch.uint8).cuda()  # stale: no number, and counts of -1
+    for fill in (255, 1):
+        space.fill_(fill)
+        qmm.qmm_attn_q4_0(c.cache, q, out[guard:-guard], max_q=rows, scale=c.scale, lse=lse[guard:-guard],
+                          workspace=space[256:-256], **c.dev)
+        assert qmm.qmm_get_device_error() == qmm.QMM_ERR_INDEX
+        for t in (out, lse):
+            assert t[:guard].eq(7.0).all() and t[-guard:].eq(7.0).all()
+        assert space[:256].eq(fill).all() and space[-256:].eq(fill).all()
