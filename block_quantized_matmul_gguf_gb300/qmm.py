@@ -190,6 +190,14 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _stream_object(stream):
+    """torch's object of a stream argument (None, the current one, stays None)."""
+    cuda = _torch_module().cuda
+    if stream is None or isinstance(stream, cuda.Stream):
+        return stream
+    return cuda.ExternalStream(_stream(stream))
+
+
 def _check(status: int, where: str) -> None:
     if status != QMM_OK:
         raise QmmError(status, where)
@@ -453,7 +461,8 @@ _LOGITS_ARGS = struct.Struct("@PqPqqqPPqPPPPPPPqP")
 
 def qmm_attn_q4_0(cache: KvCacheQ4_0, q, out, table, q_start, kv_len, max_q: int, scale: float,
                   causal: bool = True, window: int = 0, lse=None, workspace=None, stream=None) -> None:
-    """Attention of q [rows][heads][head_dim] (fp32 or bf16) over the cache into out (fp32 or bf16)."""
+    """Attention of q [rows][heads][head_dim] (fp32 or bf16) over the cache into out (fp32 or bf16).
+    Without a workspace it takes one from the memory of the stream it runs on."""
     i32 = _torch_module().int32
     rows, heads, _ = q.shape
     qp, q_stride, q_type = _rows(q, heads, cache.head_dim, "q")
@@ -464,7 +473,10 @@ def qmm_attn_q4_0(cache: KvCacheQ4_0, q, out, table, q_start, kv_len, max_q: int
             (lse is not None and lse.numel() != rows * heads):
         raise ValueError("out, lse, table and q_start must match q and kv_len in size")
     if workspace is None:
-        workspace = attn_workspace(cache, heads)
+        # the tensor dies with this call: its bytes go back to the pool of the
+        # stream it was taken under, which must be the one that uses them
+        with _torch.cuda.stream(_stream_object(stream)):
+            workspace = attn_workspace(cache, heads)
     args = _ATTN_ARGS.pack(qp, q_stride, q_type, op, out_stride, out_type, _typed(lse, _torch.float32, "lse"),
                            _typed(table, i32, "table"), width, _typed(q_start, i32, "q_start"),
                            _typed(kv_len, i32, "kv_len"), batch, rows, max_q, heads, scale, bool(causal), window,

@@ -38,3 +38,31 @@ def test_rows_claimed_twice_keep_to_their_arrays(qmm, dim, starts):
         for t in (out, lse):
             assert t[:guard].eq(7.0).all() and t[-guard:].eq(7.0).all()
         assert space[:256].eq(fill).all() and space[-256:].eq(fill).all()
+
+
+@pytest.mark.parametrize("given", ["object", "handle"])
+def test_a_workspace_of_its_own_belongs_to_its_stream(qmm, given):
+    """Without a workspace, on a stream that is not the current one: the memory
+    that the call takes must not serve the current stream while it runs."""
+    c = base.Case(qmm, [9000, 800], [1, 1], 8, 2, 256, 64, seed=9)
+    q, size = c.q.cuda(), qmm.attn_workspace(c.cache, 8).numel()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.empty(size, dtype=torch.uint8, device="cuda")  # the pools of both streams have room
+    torch.cuda.synchronize()
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2]).cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some ms: the call waits behind it
+    qmm.qmm_attn_q4_0(c.cache, q, out, max_q=1, scale=c.scale, lse=lse,
+                      stream=side if given == "object" else side.cuda_stream, **c.dev)
+    assert torch.cuda.current_stream() != side
+    other = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(t.eq(255).all() for t in other)
+    c.check((out, lse))
+    # the default stream by its handle
+    qmm.qmm_attn_q4_0(c.cache, q, out, max_q=1, scale=c.scale, lse=lse, stream=0, **c.dev)
+    torch.cuda.synchronize()
+    c.check((out, lse))
