@@ -1229,7 +1229,7 @@ size_t parts_bytes(int sms) { return (sizeof(TileHeader) + sms * sizeof(TilePart
 
 // Keys that a block of so many rows can see.
 int64_t key_bound(const KvCache &c, const AttnArgs &a, int rows) {
-    return std::min(a.table_width << c.page_shift, a.window > 0 && a.causal ? a.window + rows : INT64_MAX);
+    return std::min(a.table_width << c.page_shift, a.window > 0 && a.causal ? int64_t{a.window} + rows : INT64_MAX);
 }
 
 template <int D>

@@ -14,7 +14,6 @@ qmm = base.qmm
 FORMS = [(base.Case, F32), (base.Case, BF16), (Wide, BF16)]
 
 
-# --- M1
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("starts", [[0, 1000, 0, 1000], [0, 1000, 0, 1000, 0, 1000, 0, 1000]])
 def test_rows_claimed_twice_keep_to_their_arrays(qmm, dim, starts):
@@ -66,3 +65,13 @@ def test_a_workspace_of_its_own_belongs_to_its_stream(qmm, given):
     qmm.qmm_attn_q4_0(c.cache, q, out, max_q=1, scale=c.scale, lse=lse, stream=0, **c.dev)
     torch.cuda.synchronize()
     c.check((out, lse))
+
+
+@pytest.mark.parametrize("lens,new", [([4000, 300], [1, 1]), ([3000, 900], [200, 100])])
+def test_the_largest_window_is_no_window(qmm, lens, new):
+    """The same form is taken, so the same bits come out."""
+    c = base.Case(qmm, lens, new, 8, 2, 128, 64, seed=21, q_type=BF16)
+    want = c.call(qmm, BF16)
+    for window in (2 ** 31 - 1, 2 ** 31 - 64):
+        got = c.call(qmm, BF16, window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
