@@ -86,8 +86,9 @@ struct TileInfo {
     float k_unit[8];       // K of a group is scaled by 1 / k_unit
     int v_exp[8];          // V by 2^-(v_exp / 2); odd where its values may reach 16, not 2^-6
     uint32_t lost;         // 16-key groups without a page
-    uint32_t odd[2];       // keys whose V holds a NaN or an infinity
-    uint32_t pad;
+    uint32_t odd;          // blocks of V in which some key's scale is a NaN or an infinity, a bit each
+    uint32_t pad[2];
+    uint32_t odd_keys[8][2];  // those keys, by block
 };
 
 // Rows of one request and key head, and the tiles of their keys: all, or a part.
@@ -473,7 +474,10 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
             for (int u = 0; u < U; ++u) {
                 uint32_t bits = scales.of[half][u] & 0x7FFFu;
                 if (bits >= 0x7C00u) {
-                    if (half && scales.there) atomicOr(&info.odd[key >> 5], 1u << (key & 31));
+                    if (half && scales.there) {
+                        atomicOr(&info.odd_keys[block + 4 * u][key >> 5], 1u << (key & 31));
+                        atomicOr(&info.odd, 1u << (block + 4 * u));
+                    }
                     bits = 0;  // NaN and infinity do not set the scale
                 }
                 top = max(top, bits);
@@ -501,10 +505,11 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
                 info.k_unit[w8] = k_unit;
                 info.v_exp[w8] = v_exp;
             }
-            if (w8 == 0) {  // not in use: the warps' and the readers' tiles lie less apart
-                TileInfo &later = sh.info[(t + kRing / 2) % kRing];
-                later.lost = later.odd[0] = later.odd[1] = 0;
-            }
+        }
+        if (w8 == 0) {  // not in use: the warps' and the readers' tiles lie less apart
+            TileInfo &later = sh.info[(t + kRing / 2) % kRing];
+            if (lane == 0) later.lost = later.odd = 0;
+            if (lane < 16) later.odd_keys[lane >> 1][lane & 1] = 0;
         }
         if (!warp_wait_or_abort(smem_addr(sh.k_empty + stage), phase ^ 1u, &sh.abort, p.ctx) ||
             !warp_wait_or_abort(smem_addr(sh.v_empty + stage), phase ^ 1u, &sh.abort, p.ctx))
@@ -517,7 +522,7 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
             for (int u = 0; u < U; ++u) {
                 const int b = block + 4 * u;
                 float d = __half2float(__ushort_as_half(scales.of[half][u]));
-                if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd
+                if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd: rows that do not see the key must not either
                 d *= pow2i(-e[half]);
                 uint4 out[4];
                 if (near[half])
@@ -752,6 +757,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
     float top = ninf, sum = 0.0f;  // the weights' reference (2^kRaise there), and their sum
     int e_ref = -24;               // exponent of V's unit in O
     bool faint = false, far = false;  // a weight fell below binary16's normal numbers; a tile was far
+    uint32_t odd = 0;  // blocks of the output that a seen value leaves without a number, a bit each
     bool ok = true;
     for (int t = 0; t < bk.tiles; ++t) {
         const int buf = T::buffer(t, qt);
@@ -777,14 +783,19 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             most_exp = max(max(most_exp, max(v_exp[g], v_exp[g + 1])), max(v_exp[g + 2], v_exp[g + 3]));
         }
         const int key0 = bk.key0 + t * kKeys;
-        const bool edge = info.lost || info.odd[0] || info.odd[1] || key0 < bk.lo_all || key0 + kKeys > bk.hi_all;
+        const bool edge = info.lost || key0 < bk.lo_all || key0 + kKeys > bk.hi_all;
         if (edge) {
-            const uint32_t odd[2] = {info.odd[0], info.odd[1]}, lost = info.lost;
+            const uint32_t lost = info.lost;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                if ((odd[i >> 5] >> (i & 31)) & 1u) s[i] = 0x7FFFFFFFu;  // its value is no number
+            for (int i = 0; i < 64; ++i)
                 if (key0 + i < lo || key0 + i >= hi || ((lost >> (i >> 4)) & 1u)) s[i] = 0xFF800000u;
-            }
+        }
+        if (info.odd) {  // of the keys that the row sees
+            auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
+            const uint32_t seen0 = below(hi - key0) & ~below(lo - key0), seen1 = below(hi - key0 - 32) & ~below(lo - key0 - 32);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                if ((info.odd_keys[b][0] & seen0) | (info.odd_keys[b][1] & seen1)) odd |= 1u << b;
         }
         float here = ninf;
 #pragma unroll
@@ -881,6 +892,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
     // 2^6 times that sum at least; else the row is done again.
     const float error = faint ? static_cast<float>(bk.tiles * kKeys) * (far ? pow2i(-15) : pow2i(-15 - kNear)) : 0.0f;
     const float back = pow2i(e_ref - kRaise);  // of O's unit
+    const float nan = __uint_as_float(0x7FFFFFFFu);
     if (bk.slot >= 0) {  // the joining kernel goes on
         float *rec = p.records + static_cast<int64_t>(bk.slot) * kPartFloats;
         float4 *to = reinterpret_cast<float4 *>(rec) + (row >> 3) * (D / 4 * 8) + (row & 7);
@@ -890,11 +902,12 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                 uint32_t o[32];
                 tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
                 if (!mine) continue;
+                const float unit_out = (odd >> b) & 1u ? nan : back;
 #pragma unroll
                 for (int d = 0; d < 32; d += 4)
                     to[(b * 8 + d / 4) * 8] = make_float4(
-                        __uint_as_float(o[place_of(d)]) * back, __uint_as_float(o[place_of(d + 1)]) * back,
-                        __uint_as_float(o[place_of(d + 2)]) * back, __uint_as_float(o[place_of(d + 3)]) * back);
+                        __uint_as_float(o[place_of(d)]) * unit_out, __uint_as_float(o[place_of(d + 1)]) * unit_out,
+                        __uint_as_float(o[place_of(d + 2)]) * unit_out, __uint_as_float(o[place_of(d + 3)]) * unit_out);
             }
             if (mine) *reinterpret_cast<float4 *>(rec + T::rows * D + row * 4) = make_float4(top, sum, error * back, 0.0f);
         }
@@ -916,6 +929,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
 #pragma unroll
             for (int i = 0; i < 32; ++i) least = fminf(least, fabsf(__uint_as_float(o[i])));
             if (!mine) continue;
+            const float unit_out = (odd >> b) & 1u ? nan : down;
             if (p.out_wide) {
                 uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_at + b * 32);
 #pragma unroll
@@ -924,14 +938,14 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int d = c * 8 + i * 2;
-                        w[i] = pack_bf16x2(__uint_as_float(o[place_of(d)]) * down, __uint_as_float(o[place_of(d + 1)]) * down);
+                        w[i] = pack_bf16x2(__uint_as_float(o[place_of(d)]) * unit_out, __uint_as_float(o[place_of(d + 1)]) * unit_out);
                     }
                     to[c] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             } else {
 #pragma unroll
                 for (int d = 0; d < 32; ++d)
-                    store_value(a.out, out_at + b * 32 + d, true, __uint_as_float(o[place_of(d)]) * down);
+                    store_value(a.out, out_at + b * 32 + d, true, __uint_as_float(o[place_of(d)]) * unit_out);
             }
         }
         if (mine && a.lse) a.lse[out_row * a.heads + head] = sum == 0.0f ? ninf : (top + log2f(sum)) * kLn2;

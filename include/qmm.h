@@ -377,7 +377,9 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_q4_0 *cache, const int64_t *slots, int6
  *            with window > 0 also j > p - window
  *   out    = sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j)
  * A row that sees no key is 0 with lse -inf.  Keys that a row does not see
- * do not enter it, whatever their slots hold.
+ * do not enter it, whatever their slots hold.  A seen value whose scale is no
+ * finite number leaves the 32 outputs of its block without one, and lse as it
+ * is.
  *   q, out     [total_q] rows of heads * head_dim, q_stride and out_stride
  *              elements apart; q_type and out_type may differ
  *   lse        fp32 [total_q][heads], or NULL

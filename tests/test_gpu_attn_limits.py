@@ -75,3 +75,30 @@ def test_the_largest_window_is_no_window(qmm, lens, new):
     for window in (2 ** 31 - 1, 2 ** 31 - 64):
         got = c.call(qmm, BF16, window=window)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("form,out_type", FORMS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("long", [130, 1900])
+def test_a_nan_in_a_seen_value_stays_in_its_dimensions(qmm, form, out_type, dim, window, long):
+    """Neither lse nor the other blocks' outputs depend on it, nor do rows that
+    do not see the key or read another key head."""
+    new, page, block, key = 100, 16, 1, long - 40
+    c = form(qmm, [long, 120], [new, new], 8, 2, dim, page, seed=dim, q_type=BF16)
+    clean = [a.copy() for a in c.arrays]
+    c.arrays[3][c.table[0, key // page], 1, key % page, block] = np.nan
+    c.cache = qmm.KvCacheQ4_0(*(torch.from_numpy(a).cuda() for a in c.arrays))
+    out, lse = c.call(qmm, out_type, window=window)
+    pos = np.arange(long - new, long)
+    rows = np.flatnonzero((pos >= key) & (pos < key + window if window else True))
+    want = np.zeros(out.shape, bool)
+    want[rows[0]:rows[-1] + 1, 4:, 32 * block:32 * block + 32] = True
+    out = out.float().cpu()
+    assert np.array_equal(torch.isnan(out).numpy(), want)
+    # the rest is as without it
+    c.arrays = clean
+    truth = ref.attention(c.q.double().numpy(), *clean, c.table, c.q_start, c.lens, c.scale, True, window)
+    lim_o, lim_l = ref.attention_limits(*truth, bf16=out_type == BF16)
+    assert (np.abs(out.numpy() - truth[0]) <= lim_o)[~want].all()
+    assert (np.abs(lse.cpu().numpy() - truth[1]) <= lim_l).all()
