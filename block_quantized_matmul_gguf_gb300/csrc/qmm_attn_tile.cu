@@ -23,10 +23,15 @@
 // Precision: q, (n - 8) d and the weights are rounded once to binary16 each.
 // K and V are scaled by powers of two, one for the keys of each dequant warp,
 // to below 2^-6 (16 where the scales lie far apart), q per row to below 2^15
-// and the weights to at most 2^15, so that nothing overflows; weights below
-// 2^-38 of a row's largest fall out of binary16's range, which shows only
-// where the heavy keys' codes leave (nearly) nothing: such rows are done again
-// by all warps in fp32.
+// and the weights to at most 2^15, so that nothing overflows.  Weights below
+// 2^-24 of a row's reference lose bits, or all of them, among binary16's
+// subnormal numbers.  That shows only where the heavy keys leave (nearly)
+// nothing of an output, whose size does not tell whether they cancel or are 0
+// there.  A block with such a row goes over its tiles once more, by the same
+// steps, with what was lost of the weights raised by 2^38, and adds the
+// products; four passes cover fp32's range.  The case of 2048 tokens below by
+// the scores' standard deviation: 1.2 195 us, 2.4 to 8 450, 24 740; with a
+// block of values that are all 0 320, 450 to 920, 945.
 //
 // Parts are joined by a second kernel: their outputs and sums, in fp32, are
 // weighted by 2^(m - largest m), in the parts' order.
@@ -43,6 +48,7 @@
 #include "qmm_tc.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace qmm {
 namespace {
@@ -53,6 +59,9 @@ constexpr int kRing = 16;                  // tiles whose exponents are kept
 constexpr int kPanel = kKeys * 128;        // bytes of 64 values of a tile's keys
 constexpr int kRaise = 10;                 // the reference weight is 2^10
 constexpr float kSlack = 5.0f;             // ... and the largest at most 2^15
+constexpr int kPasses = 4;                 // over a block's tiles, at most
+constexpr float kNormal = 1.0f / 16384.0f; // binary16's smallest normal number
+constexpr int kPassRaise = 38;             // what a pass loses of a weight (at most 2^-25) is raised to 2^13
 
 template <int D>
 struct Tile {
@@ -112,9 +121,9 @@ struct TileHeader {
 };
 constexpr int kMaxTileCtas = 256;  // SMs that are counted on: at most as many parts
 constexpr int kMaxThreads = 640;
-// Outputs of a part as float4 [rows / 8][D / 4][8 rows], then maximum, sum and
-// error of each row in a float4.
-constexpr int kPartFloats = 128 * 256 + 256 * 4;
+// Outputs of a part as float4 [rows / 8][D / 4][8 rows], then maximum and sum
+// of each row.
+constexpr int kPartFloats = 128 * 256 + 256 * 2;
 constexpr int kMinPart = 8;  // tiles of a part at least: about what a CTA takes to begin and end
 
 struct TileShared {
@@ -126,8 +135,7 @@ struct TileShared {
     Block block;
     uint32_t tmem;
     int abort;
-    uint32_t again[8];              // rows to do again, a bit each
-    float part[32][2];              // of those: the warps' maxima and sums
+    int again[kPasses];             // whether another pass follows this one
 };
 
 struct TileParams {
@@ -356,6 +364,20 @@ __device__ __forceinline__ void find_block(const TileParams &p, TileShared &sh) 
     __syncthreads();
 }
 
+// ---- passes --------------------------------------------------------------------------
+
+// All threads meet at the end of a pass and learn whether another follows.
+// What they go by is written before the barrier only, so that all go the same
+// way whatever happens to a wait.  Tiles are counted on through the passes,
+// which keeps the phases of the barriers and the ring in step.
+template <int D>
+__device__ __forceinline__ bool another_pass(const TileShared &sh, int pass) {
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(Tile<D>::threads) : "memory");
+    tc_fence_after();
+    return pass + 1 < kPasses && sh.again[pass] != 0;
+}
+
 // ---- dequantisation ----------------------------------------------------------------
 
 // The 16 bytes of one block to 32 binary16 values in the words' own order, as
@@ -446,105 +468,108 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
                     c.of[half][u] = __ldg(reinterpret_cast<const uint4 *>((half ? p.v_codes : p.k_codes) + h.row * (D / 2)) + block + 4 * u);
             }
     };
-    // codes a tile ahead, scales two, pages three
-    int32_t page = page_of(2);
-    Scales<D> scales, scales1, scales2;
-    Codes<D> next;
-    load_scales(0, page_of(0), scales1);
-    load_scales(1, page_of(1), scales2);
-    load_codes(scales1, next);
-    int stage = 0;
+    int stage = 0, t = 0;
     uint32_t phase = 0;
-    for (int t = 0; t < bk.tiles; ++t) {
-        const Codes<D> cur = next;
-        scales = scales1;
-        scales1 = scales2;
+    for (int pass = 0;; ++pass) {
+        // codes a tile ahead, scales two, pages three
+        int32_t page = page_of(2);
+        Scales<D> scales, scales1, scales2;
+        Codes<D> next;
+        load_scales(0, page_of(0), scales1);
+        load_scales(1, page_of(1), scales2);
         load_codes(scales1, next);
-        load_scales(t + 2, page, scales2);
-        page = page_of(t + 3);
-        // the warp's keys have one power of two for K and one for V, from the
-        // largest and smallest scale: bits of binary16 order as the numbers do
-        TileInfo &info = sh.info[t % kRing];
-        int e[2];
-        bool near[2];
+        for (int i = 0; i < bk.tiles; ++i, ++t) {
+            const Codes<D> cur = next;
+            scales = scales1;
+            scales1 = scales2;
+            load_codes(scales1, next);
+            load_scales(i + 2, page, scales2);
+            page = page_of(i + 3);
+            // the warp's keys have one power of two for K and one for V, from the
+            // largest and smallest scale: bits of binary16 order as the numbers do
+            TileInfo &info = sh.info[t % kRing];
+            int e[2];
+            bool near[2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t top = 0, low = 0x7FFF;  // low: of those that are not 0
+            for (int half = 0; half < 2; ++half) {
+                uint32_t top = 0, low = 0x7FFF;  // low: of those that are not 0
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                uint32_t bits = scales.of[half][u] & 0x7FFFu;
-                if (bits >= 0x7C00u) {
-                    if (half && scales.there) {
-                        atomicOr(&info.odd_keys[block + 4 * u][key >> 5], 1u << (key & 31));
-                        atomicOr(&info.odd, 1u << (block + 4 * u));
+                for (int u = 0; u < U; ++u) {
+                    uint32_t bits = scales.of[half][u] & 0x7FFFu;
+                    if (bits >= 0x7C00u) {
+                        if (half && scales.there) {
+                            atomicOr(&info.odd_keys[block + 4 * u][key >> 5], 1u << (key & 31));
+                            atomicOr(&info.odd, 1u << (block + 4 * u));
+                        }
+                        bits = 0;  // NaN and infinity do not set the scale
                     }
-                    bits = 0;  // NaN and infinity do not set the scale
+                    top = max(top, bits);
+                    low = min(low, bits ? bits : 0x7FFFu);
                 }
-                top = max(top, bits);
-                low = min(low, bits ? bits : 0x7FFFu);
+                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                low = __reduce_min_sync(0xFFFFFFFFu, low);
+                auto scale_of = [](uint32_t bits) { return exponent(__half2float(__ushort_as_half(static_cast<unsigned short>(bits)))); };
+                e[half] = top ? scale_of(top) : -24;
+                near[half] = !top || e[half] - scale_of(low) <= kNearSpan;
             }
-            top = __reduce_max_sync(0xFFFFFFFFu, top);
-            low = __reduce_min_sync(0xFFFFFFFFu, low);
-            auto scale_of = [](uint32_t bits) { return exponent(__half2float(__ushort_as_half(static_cast<unsigned short>(bits)))); };
-            e[half] = top ? scale_of(top) : -24;
-            near[half] = !top || e[half] - scale_of(low) <= kNearSpan;
-        }
-        if (__any_sync(0xFFFFFFFFu, scales.lost) && lane == 0) {
-            record_error(p.ctx, kDevErrIndex);
-            atomicOr(&info.lost, 1u << (key >> 4));  // lane 0's key: the warp's keys lie in one group
-        }
-        if (lane == 0) {
-            const float k_unit = pow2i(e[0] + (near[0] ? kNear : 0));
-            const int v_exp = near[1] ? 2 * (e[1] + kNear) : 2 * e[1] + 1;
-            if constexpr (D == 64) {
-                if (half0 == 0)
-                    info.k_unit[2 * w8] = info.k_unit[2 * w8 + 1] = k_unit;
-                else
-                    info.v_exp[2 * w8 - 8] = info.v_exp[2 * w8 - 7] = v_exp;
-            } else {
-                info.k_unit[w8] = k_unit;
-                info.v_exp[w8] = v_exp;
+            if (__any_sync(0xFFFFFFFFu, scales.lost) && lane == 0) {
+                record_error(p.ctx, kDevErrIndex);
+                atomicOr(&info.lost, 1u << (key >> 4));  // lane 0's key: the warp's keys lie in one group
+            }
+            if (lane == 0) {
+                const float k_unit = pow2i(e[0] + (near[0] ? kNear : 0));
+                const int v_exp = near[1] ? 2 * (e[1] + kNear) : 2 * e[1] + 1;
+                if constexpr (D == 64) {
+                    if (half0 == 0)
+                        info.k_unit[2 * w8] = info.k_unit[2 * w8 + 1] = k_unit;
+                    else
+                        info.v_exp[2 * w8 - 8] = info.v_exp[2 * w8 - 7] = v_exp;
+                } else {
+                    info.k_unit[w8] = k_unit;
+                    info.v_exp[w8] = v_exp;
+                }
+            }
+            if (w8 == 0) {  // not in use: the warps' and the readers' tiles lie less apart
+                TileInfo &later = sh.info[(t + kRing / 2) % kRing];
+                if (lane == 0) later.lost = later.odd = 0;
+                if (lane < 16) later.odd_keys[lane >> 1][lane & 1] = 0;
+            }
+            if (!warp_wait_or_abort(smem_addr(sh.k_empty + stage), phase ^ 1u, &sh.abort, p.ctx) ||
+                !warp_wait_or_abort(smem_addr(sh.v_empty + stage), phase ^ 1u, &sh.abort, p.ctx))
+                break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (half < half0 || half >= half1) continue;
+                uint8_t *rows = smem + (half * T::stages + stage) * T::bytes + key * 128;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int b = block + 4 * u;
+                    float d = __half2float(__ushort_as_half(scales.of[half][u]));
+                    if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd: rows that do not see the key must not either
+                    d *= pow2i(-e[half]);
+                    uint4 out[4];
+                    if (near[half])
+                        dequant_near(cur.of[half][u], d, out);
+                    else
+                        dequant_far(cur.of[half][u], d, out);
+                    uint8_t *panel = rows + (b >> 1) * kPanel;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(panel + ((((b & 1) * 4 + i) ^ (key & 7)) << 4)) = out[i];
+                }
+            }
+            fence_proxy_async_smem();  // generic writes -> tensor-core reads
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_addr(smem_addr(sh.k_full + stage));
+                mbar_arrive_addr(smem_addr(sh.v_full + stage));
+            }
+            if (++stage == T::stages) {
+                stage = 0;
+                phase ^= 1u;
             }
         }
-        if (w8 == 0) {  // not in use: the warps' and the readers' tiles lie less apart
-            TileInfo &later = sh.info[(t + kRing / 2) % kRing];
-            if (lane == 0) later.lost = later.odd = 0;
-            if (lane < 16) later.odd_keys[lane >> 1][lane & 1] = 0;
-        }
-        if (!warp_wait_or_abort(smem_addr(sh.k_empty + stage), phase ^ 1u, &sh.abort, p.ctx) ||
-            !warp_wait_or_abort(smem_addr(sh.v_empty + stage), phase ^ 1u, &sh.abort, p.ctx))
-            break;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (half < half0 || half >= half1) continue;
-            uint8_t *rows = smem + (half * T::stages + stage) * T::bytes + key * 128;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int b = block + 4 * u;
-                float d = __half2float(__ushort_as_half(scales.of[half][u]));
-                if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd: rows that do not see the key must not either
-                d *= pow2i(-e[half]);
-                uint4 out[4];
-                if (near[half])
-                    dequant_near(cur.of[half][u], d, out);
-                else
-                    dequant_far(cur.of[half][u], d, out);
-                uint8_t *panel = rows + (b >> 1) * kPanel;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4 *>(panel + ((((b & 1) * 4 + i) ^ (key & 7)) << 4)) = out[i];
-            }
-        }
-        fence_proxy_async_smem();  // generic writes -> tensor-core reads
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive_addr(smem_addr(sh.k_full + stage));
-            mbar_arrive_addr(smem_addr(sh.v_full + stage));
-        }
-        if (++stage == T::stages) {
-            stage = 0;
-            phase ^= 1u;
-        }
+        if (!another_pass<D>(sh, pass)) break;
     }
 }
 
@@ -570,6 +595,12 @@ __device__ __forceinline__ void products_done(uint32_t one, uint32_t bar) {
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
         : "memory");
+}
+
+// 0xFFFF in each half that is less than binary16's normal numbers, of two that
+// are not negative (NaN is not less).
+__device__ __forceinline__ uint32_t subnormal2(uint32_t v) {
+    return __hlt2_mask(*reinterpret_cast<const __half2 *>(&v), __half2half2(__ushort_as_half(static_cast<unsigned short>(0x0400))));
 }
 
 // The whole warp, so that the operands are known to be the same for all lanes:
@@ -600,21 +631,27 @@ __device__ __forceinline__ void mma_role(const TileParams &p, TileShared &sh, ui
         return true;
     };
     bool ok = tiles == 0 || warp_wait_or_abort(smem_addr(&sh.q_ready), 0, abort, p.ctx);
-    for (int t = 0; ok && t < min(ahead, tiles); ++t) ok = qk(t);
-    for (int t = 0; ok && t < tiles; ++t) {
-        const int stage = t % T::stages, buf = T::buffer(t, qt);
-        if (!warp_wait_or_abort(smem_addr(sh.p_full + buf), T::phase(t), abort, p.ctx)) break;
-        if (!warp_wait_or_abort(smem_addr(sh.v_full + stage), (t / T::stages) & 1u, abort, p.ctx)) break;
-        tc_fence_after();
-        const uint64_t b0 = rows_desc(smem + (T::stages + stage) * T::bytes);
-        const uint32_t to = tmem + T::o_col + qt * D, from = tmem + T::s_col + buf * kKeys;
+    int first = 0;  // tile of the pass
+    for (int pass = 0;; ++pass, first += tiles) {
+        const int end = first + tiles;
+        for (int t = first; ok && t < min(first + ahead, end); ++t) ok = qk(t);
+        for (int t = first; ok && t < end; ++t) {
+            const int stage = t % T::stages, buf = T::buffer(t, qt);
+            ok = warp_wait_or_abort(smem_addr(sh.p_full + buf), T::phase(t), abort, p.ctx) &&
+                 warp_wait_or_abort(smem_addr(sh.v_full + stage), (t / T::stages) & 1u, abort, p.ctx);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b0 = rows_desc(smem + (T::stages + stage) * T::bytes);
+            const uint32_t to = tmem + T::o_col + qt * D, from = tmem + T::s_col + buf * kKeys;
 #pragma unroll
-        for (int s = 0; s < kKeys / 16; ++s) product(one, to, from + s * 8, b0 + ((s * 2048) >> 4), pv_desc, t > 0 || s > 0);
-        products_done(one, smem_addr(sh.pv_done + qt));
-        products_done(one, smem_addr(sh.v_empty + stage));
-        // the next S goes where P lies, once its product has read it (products
-        // with different accumulators are not ordered among themselves)
-        if (t + ahead < tiles) ok = warp_wait_or_abort(smem_addr(sh.pv_done + qt), t & 1u, abort, p.ctx) && qk(t + ahead);
+            for (int s = 0; s < kKeys / 16; ++s) product(one, to, from + s * 8, b0 + ((s * 2048) >> 4), pv_desc, t > first || s > 0);
+            products_done(one, smem_addr(sh.pv_done + qt));
+            products_done(one, smem_addr(sh.v_empty + stage));
+            // the next S goes where P lies, once its product has read it (products
+            // with different accumulators are not ordered among themselves)
+            if (t + ahead < end) ok = warp_wait_or_abort(smem_addr(sh.pv_done + qt), t & 1u, abort, p.ctx) && qk(t + ahead);
+        }
+        if (!another_pass<D>(sh, pass)) break;
     }
     if (issued) {  // all products end before tensor memory is freed
         products_done(one, smem_addr(sh.final + qt));
@@ -754,277 +791,293 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
 
     const int pos = bk.first + token;
     const int lo = mine ? first_key(a, pos) : 0, hi = mine ? (a.causal ? min(bk.len, pos + 1) : bk.len) : 0;
-    float top = ninf, sum = 0.0f;  // the weights' reference (2^kRaise there), and their sum
-    int e_ref = -24;               // exponent of V's unit in O
-    bool faint = false, far = false;  // a weight fell below binary16's normal numbers; a tile was far
-    uint32_t odd = 0;  // blocks of the output that a seen value leaves without a number, a bit each
-    bool ok = true;
-    for (int t = 0; t < bk.tiles; ++t) {
-        const int buf = T::buffer(t, qt);
-        if (!warp_wait_or_abort(smem_addr(sh.s_full + buf), T::phase(t), &sh.abort, p.ctx) ||
-            !warp_wait_or_abort(smem_addr(sh.v_full + t % T::stages), (t / T::stages) & 1u, &sh.abort, p.ctx)) {
-            ok = false;
-            break;
-        }
-        tc_fence_after();
-        const uint32_t s_at = tmem + lanes + T::s_col + buf * kKeys;
-        uint32_t s[64];
-        tmem_ld_64cols(s_at, s);
-        const TileInfo &info = sh.info[t % kRing];
-        float u[8];
-        int v_exp[8], most_exp = -0x10000;
-#pragma unroll
-        for (int g = 0; g < 8; g += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(info.k_unit + g);
-            const int4 e = *reinterpret_cast<const int4 *>(info.v_exp + g);
-            u[g] = unit * f.x, u[g + 1] = unit * f.y, u[g + 2] = unit * f.z, u[g + 3] = unit * f.w;
-            far |= (e.x | e.y | e.z | e.w) & 1;
-            v_exp[g] = e.x >> 1, v_exp[g + 1] = e.y >> 1, v_exp[g + 2] = e.z >> 1, v_exp[g + 3] = e.w >> 1;
-            most_exp = max(max(most_exp, max(v_exp[g], v_exp[g + 1])), max(v_exp[g + 2], v_exp[g + 3]));
-        }
-        const int key0 = bk.key0 + t * kKeys;
-        const bool edge = info.lost || key0 < bk.lo_all || key0 + kKeys > bk.hi_all;
-        if (edge) {
-            const uint32_t lost = info.lost;
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (key0 + i < lo || key0 + i >= hi || ((lost >> (i >> 4)) & 1u)) s[i] = 0xFF800000u;
-        }
-        if (info.odd) {  // of the keys that the row sees
-            auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
-            const uint32_t seen0 = below(hi - key0) & ~below(lo - key0), seen1 = below(hi - key0 - 32) & ~below(lo - key0 - 32);
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                if ((info.odd_keys[b][0] & seen0) | (info.odd_keys[b][1] & seen1)) odd |= 1u << b;
-        }
-        float here = ninf;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            float most = __uint_as_float(s[8 * g]);
-#pragma unroll
-            for (int k = 1; k < 7; k += 2) most = fmaxf(most, fmaxf(__uint_as_float(s[8 * g + k]), __uint_as_float(s[8 * g + k + 1])));
-            here = fmaxf(here, fmaxf(most, __uint_as_float(s[8 * g + 7])) * u[g]);
-        }
-        // a new reference where the largest weight would pass 2^15, and where
-        // V's unit grows
-        const bool grow = here > top + kSlack;
-        const int e_now = max(e_ref, most_exp);
-        const float now = grow || top == ninf ? fmaxf(top, here) : top;
-        if (__any_sync(0xFFFFFFFFu, now != top || e_now != e_ref)) {
-            const float f = top == ninf ? 0.0f : exp2_fast(top - now);
-            sum *= f;
-            if (t > 0) {
-                const float scale = f * pow2i(e_ref - e_now);
-                if (!warp_wait_or_abort(smem_addr(sh.pv_done + qt), (t - 1) & 1u, &sh.abort, p.ctx)) {
+    float total = 0.0f; // of the weights
+    uint32_t odd = 0;   // blocks of the output that a seen value leaves without a number, a bit each
+    bool far = false;   // a tile was far
+    bool ok = true, open = mine;  // open: what was lost of the weights may show in the row
+    int first = 0;      // tile of the pass
+    for (int pass = 0;; ++pass, first += bk.tiles) {
+        float top = ninf;   // the weights' reference (2^kRaise there)
+        int e_ref = -24;    // exponent of V's unit in O
+        float sum = 0.0f;   // of the weights (first pass)
+        int faint = 0;      // tiles in which a weight fell below binary16's normal numbers
+        auto tiles = [&](auto is_later) {
+            constexpr bool later = decltype(is_later)::value;
+            for (int t = first; ok && t < first + bk.tiles; ++t) {
+                const int buf = T::buffer(t, qt);
+                if (!warp_wait_or_abort(smem_addr(sh.s_full + buf), T::phase(t), &sh.abort, p.ctx) ||
+                    !warp_wait_or_abort(smem_addr(sh.v_full + t % T::stages), (t / T::stages) & 1u, &sh.abort, p.ctx)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                if (later && !__any_sync(0xFFFFFFFFu, open)) {  // nothing of these rows is wanted: any weights do
+                    if (t > 0 && !warp_wait_or_abort(smem_addr(sh.pv_done + qt), (t - 1) & 1u, &sh.abort, p.ctx)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive_addr(smem_addr(sh.p_full + buf));
+                    continue;
+                }
+                const uint32_t s_at = tmem + lanes + T::s_col + buf * kKeys;
+                uint32_t s[64];
+                tmem_ld_64cols(s_at, s);
+                const TileInfo &info = sh.info[t % kRing];
+                float u[8];
+                int v_exp[8], most_exp = -0x10000;
+#pragma unroll
+                for (int g = 0; g < 8; g += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(info.k_unit + g);
+                    const int4 e = *reinterpret_cast<const int4 *>(info.v_exp + g);
+                    u[g] = unit * f.x, u[g + 1] = unit * f.y, u[g + 2] = unit * f.z, u[g + 3] = unit * f.w;
+                    far |= (e.x | e.y | e.z | e.w) & 1;
+                    v_exp[g] = e.x >> 1, v_exp[g + 1] = e.y >> 1, v_exp[g + 2] = e.z >> 1, v_exp[g + 3] = e.w >> 1;
+                    most_exp = max(max(most_exp, max(v_exp[g], v_exp[g + 1])), max(v_exp[g + 2], v_exp[g + 3]));
+                }
+                const int key0 = bk.key0 + (t - first) * kKeys;
+                const bool edge = info.lost || key0 < bk.lo_all || key0 + kKeys > bk.hi_all;
+                if (edge) {
+                    const uint32_t lost = info.lost;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (key0 + i < lo || key0 + i >= hi || ((lost >> (i >> 4)) & 1u)) s[i] = 0xFF800000u;
+                }
+                if (info.odd) {  // of the keys that the row sees
+                    auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
+                    const uint32_t seen0 = below(hi - key0) & ~below(lo - key0), seen1 = below(hi - key0 - 32) & ~below(lo - key0 - 32);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        if ((info.odd_keys[b][0] & seen0) | (info.odd_keys[b][1] & seen1)) odd |= 1u << b;
+                }
+                float here = ninf;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    float most = __uint_as_float(s[8 * g]);
+#pragma unroll
+                    for (int k = 1; k < 7; k += 2) most = fmaxf(most, fmaxf(__uint_as_float(s[8 * g + k]), __uint_as_float(s[8 * g + k + 1])));
+                    here = fmaxf(here, fmaxf(most, __uint_as_float(s[8 * g + 7])) * u[g]);
+                }
+                // a new reference where the largest weight would pass 2^15, and where
+                // V's unit grows
+                const bool grow = here > top + kSlack;
+                const int e_now = max(e_ref, most_exp);
+                const float now = grow || top == ninf ? fmaxf(top, here) : top;
+                if (__any_sync(0xFFFFFFFFu, now != top || e_now != e_ref)) {
+                    const float f = top == ninf ? 0.0f : exp2_fast(top - now);
+                    sum *= f;
+                    if (t > first) {
+                        const float scale = f * pow2i(e_ref - e_now);
+                        if (!warp_wait_or_abort(smem_addr(sh.pv_done + qt), (t - 1) & 1u, &sh.abort, p.ctx)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32], v[16];
-                    const uint32_t at = tmem + lanes + T::o_col + qt * D + c;
-                    tmem_ld_32cols(at, o);
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32], v[16];
+                            const uint32_t at = tmem + lanes + T::o_col + qt * D + c;
+                            tmem_ld_32cols(at, o);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(o[16 * h + i]) * scale);
+                                tmem_st_16cols(at + 16 * h, v);
+                            }
+                        }
+                    }
+                    top = now;
+                    e_ref = e_now;
+                }
+                const float top_here = top == ninf ? 0.0f : top;
+                float base[8];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) base[g] = static_cast<float>(kRaise + v_exp[g] - e_ref) - top_here;
+                if constexpr (later) {
+                    // What the pass before has lost of the weights.  z, a weight as
+                    // that pass had it, is a subnormal number there or 0; weights
+                    // that were so one pass earlier still leave nothing to it.
+                    const float up = pow2i(kPassRaise * (pass - 1)), raise = pow2i(kPassRaise);
+                    bool low = false;
+                    if (edge) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            low |= s[i] != 0xFF800000u && fmaf(__uint_as_float(s[i]), u[i >> 3], base[i >> 3]) <
+                                                              static_cast<float>(-14 - kPassRaise * pass);
+                    }
+                    float smallest = 1.0f;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(o[16 * h + i]) * scale);
-                        tmem_st_16cols(at + 16 * h, v);
+                        for (int i = 0; i < 16; ++i) {
+                            const int g = 4 * h + (i >> 2);
+                            const float2 arg = __ffma2_rn(make_float2(__uint_as_float(s[32 * h + 2 * i]), __uint_as_float(s[32 * h + 2 * i + 1])),
+                                                          make_float2(u[g], u[g]), make_float2(base[g], base[g]));
+                            const float2 z = __fmul2_rn(make_float2(exp2_fast(arg.x), exp2_fast(arg.y)), make_float2(up, up));
+                            const uint32_t had = pack_rn(z.x, z.y);
+                            const float2 lost = __fadd2_rn(z, make_float2(-low_float(had), -high_float(had)));
+                            const float2 y = __fmul2_rn(lost, make_float2(raise, raise));
+                            w[i] = pack_rn(y.x, y.y) & subnormal2(had);
+                            smallest = fminf(smallest, fminf(z.x, z.y));
+                        }
+                        tmem_st_16cols(s_at + 16 * h, w);
                     }
+                    if (!edge) low = smallest * raise < kNormal;
+                    faint += low ? 1 : 0;
+                } else {
+                    bool low = false;
+                    if (edge) {  // hidden keys' weights are 0 and do not count
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            low |= s[i] != 0xFF800000u && fmaf(__uint_as_float(s[i]), u[i >> 3], base[i >> 3]) < -14.0f;
+                    }
+                    uint32_t least[2] = {0x7C007C00u, 0x7C007C00u};  // smallest weights
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int g = 4 * h; g < 4 * h + 4; ++g) {
+                            float2 add = make_float2(0.0f, 0.0f);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 arg = __ffma2_rn(make_float2(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1])),
+                                                              make_float2(u[g], u[g]), make_float2(base[g], base[g]));
+                                const float2 x = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
+                                add = i == 0 ? x : __fadd2_rn(add, x);
+                                const uint32_t both = pack_rn(x.x, x.y);
+                                w[4 * (g & 3) + i] = both;
+                                least[i & 1] = hmin2(least[i & 1], both);
+                            }
+                            sum = fmaf(add.x + add.y, pow2i(e_ref - kRaise - v_exp[g]), sum);
+                        }
+                        tmem_st_16cols(s_at + 16 * h, w);
+                    }
+                    least[0] = hmin2(least[0], least[1]);
+                    if (!edge) low = (least[0] & 0x7C00u) == 0 || (least[0] & 0x7C000000u) == 0;  // below the normal numbers
+                    faint += low ? 1 : 0;
                 }
-            }
-            top = now;
-            e_ref = e_now;
-        }
-        const float top_here = top == ninf ? 0.0f : top;
-        float base[8];
-#pragma unroll
-        for (int g = 0; g < 8; ++g) base[g] = static_cast<float>(kRaise + v_exp[g] - e_ref) - top_here;
-        if (edge) {  // hidden keys' weights are 0 and do not count
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                faint |= s[i] != 0xFF800000u && fmaf(__uint_as_float(s[i]), u[i >> 3], base[i >> 3]) < -14.0f;
-        }
-        uint32_t least[2] = {0x7C007C00u, 0x7C007C00u};  // smallest weights
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[16];
-#pragma unroll
-            for (int g = 4 * h; g < 4 * h + 4; ++g) {
-                float2 add = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 arg = __ffma2_rn(make_float2(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1])),
-                                                  make_float2(u[g], u[g]), make_float2(base[g], base[g]));
-                    const float2 x = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
-                    add = i == 0 ? x : __fadd2_rn(add, x);
-                    const uint32_t both = pack_rn(x.x, x.y);
-                    w[4 * (g & 3) + i] = both;
-                    least[i & 1] = hmin2(least[i & 1], both);
+                // Every phase of pv_done is waited for in turn, before the next product
+                // can start: a barrier's parity tells neighbouring phases apart only.
+                if (t > 0 && !warp_wait_or_abort(smem_addr(sh.pv_done + qt), (t - 1) & 1u, &sh.abort, p.ctx)) {
+                    ok = false;
+                    break;
                 }
-                sum = fmaf(add.x + add.y, pow2i(e_ref - kRaise - v_exp[g]), sum);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_addr(smem_addr(sh.p_full + buf));
             }
-            tmem_st_16cols(s_at + 16 * h, w);
-        }
-        least[0] = hmin2(least[0], least[1]);
-        if (!edge) faint |= (least[0] & 0x7C00u) == 0 || (least[0] & 0x7C000000u) == 0;  // below the normal numbers
-        // Every phase of pv_done is waited for in turn, before the next product
-        // can start: a barrier's parity tells neighbouring phases apart only.
-        if (t > 0 && !warp_wait_or_abort(smem_addr(sh.pv_done + qt), (t - 1) & 1u, &sh.abort, p.ctx)) {
-            ok = false;
-            break;
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_addr(smem_addr(sh.p_full + buf));
-    }
+        };
+        // Code of its own spares the first pass the test, which costs 5 us of 195
+        // (2048 tokens behind 6000) and of 99 (the windowed prompts).
+        if (pass == 0)
+            tiles(std::false_type{});
+        else
+            tiles(std::true_type{});
+        if (pass == 0) total = sum;
 
-    // outputs
-    if (ok && bk.tiles > 0) ok = warp_wait_or_abort(smem_addr(sh.pv_done + qt), (bk.tiles - 1) & 1u, &sh.abort, p.ctx);
-    tc_fence_after();
-    const int64_t out_row = static_cast<int64_t>(bk.q_row0) + token;
-    const int64_t out_at = out_row * a.out_stride + static_cast<int64_t>(head) * D;
-    // A faint weight is off by at most 2^-25, times values below 16 (near tiles
-    // only: 2^-6), a key.
-    // Scores that lie 24 powers of two apart are themselves uncertain by more
-    // than 2^-6 of a weight (binary16 q and K, A >= 8), so an output has to be
-    // 2^6 times that sum at least; else the row is done again.
-    const float error = faint ? static_cast<float>(bk.tiles * kKeys) * (far ? pow2i(-15) : pow2i(-15 - kNear)) : 0.0f;
-    const float back = pow2i(e_ref - kRaise);  // of O's unit
-    const float nan = __uint_as_float(0x7FFFFFFFu);
-    if (bk.slot >= 0) {  // the joining kernel goes on
-        float *rec = p.records + static_cast<int64_t>(bk.slot) * kPartFloats;
-        float4 *to = reinterpret_cast<float4 *>(rec) + (row >> 3) * (D / 4 * 8) + (row & 7);
+        // outputs
+        if (ok && bk.tiles > 0) ok = warp_wait_or_abort(smem_addr(sh.pv_done + qt), (first + bk.tiles - 1) & 1u, &sh.abort, p.ctx);
+        tc_fence_after();
+        // A faint weight is off by at most 2^-25, times values below 16 (near tiles
+        // only: 2^-6), a key.  Scores that lie 24 powers of two apart are
+        // themselves uncertain by more than 2^-6 of a weight (binary16 q and K,
+        // A >= 8), so an output has to be 2^6 times that sum at least.
+        const float error = static_cast<float>(faint * kKeys) * (far ? pow2i(-15) : pow2i(-15 - kNear));
+        const float back = pow2i(e_ref - kRaise);  // of O's unit
+        const float down = bk.slot >= 0 ? back : total == 0.0f ? 0.0f : back / total;
+        const float raised = pow2i(-kPassRaise * pass);
+        float least = __uint_as_float(0x7F800000u);  // output of the row, by its size and in units of `down`
         if (ok) {
+            const int64_t out_row = static_cast<int64_t>(bk.q_row0) + token;
+            const int64_t out_at = out_row * a.out_stride + static_cast<int64_t>(head) * D;
+            float *rec = p.records + static_cast<int64_t>(max(bk.slot, 0)) * kPartFloats;  // the joining kernel goes on
+            float4 *rec_to = reinterpret_cast<float4 *>(rec) + (row >> 3) * (D / 4 * 8) + (row & 7);
 #pragma unroll 1
             for (int b = 0; b < NB; ++b) {
                 uint32_t o[32];
-                tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
-                if (!mine) continue;
-                const float unit_out = (odd >> b) & 1u ? nan : back;
+                __syncwarp();  // rows that have nothing to write went ahead
+                if (bk.tiles > 0) {
+                    tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
+                } else {
 #pragma unroll
-                for (int d = 0; d < 32; d += 4)
-                    to[(b * 8 + d / 4) * 8] = make_float4(
-                        __uint_as_float(o[place_of(d)]) * unit_out, __uint_as_float(o[place_of(d + 1)]) * unit_out,
-                        __uint_as_float(o[place_of(d + 2)]) * unit_out, __uint_as_float(o[place_of(d + 3)]) * unit_out);
-            }
-            if (mine) *reinterpret_cast<float4 *>(rec + T::rows * D + row * 4) = make_float4(top, sum, error * back, 0.0f);
-        }
-        if (lane == 0) sh.again[warp] = 0;
-        return;
-    }
-    const float down = sum == 0.0f ? 0.0f : back / sum;
-    float least = __uint_as_float(0x7F800000u);
-    if (ok) {
-#pragma unroll 1
-        for (int b = 0; b < NB; ++b) {
-            uint32_t o[32];
-            if (bk.tiles > 0) {
-                tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) least = fminf(least, fabsf(__uint_as_float(o[i])));
-            if (!mine) continue;
-            const float unit_out = (odd >> b) & 1u ? nan : down;
-            if (p.out_wide) {
-                uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_at + b * 32);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int d = c * 8 + i * 2;
-                        w[i] = pack_bf16x2(__uint_as_float(o[place_of(d)]) * unit_out, __uint_as_float(o[place_of(d + 1)]) * unit_out);
-                    }
-                    to[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
-            } else {
+                const float unit_out = (odd >> b) & 1u ? __uint_as_float(0x7FFFFFFFu) : down;
+                if (__builtin_expect(pass > 0, 0)) {
+                    // added to what this thread wrote before, and rounded once more
+                    // (within what the row's scores leave uncertain)
+                    if (!open) continue;
+                    const float raised_out = raised * unit_out;
+                    auto add = [&](int d, float had) {
+                        const float v = fmaf(__uint_as_float(o[place_of(d)]), raised_out, had);
+                        least = fminf(least, fabsf(v));
+                        return v;
+                    };
+                    if (bk.slot >= 0) {
 #pragma unroll
-                for (int d = 0; d < 32; ++d)
-                    store_value(a.out, out_at + b * 32 + d, true, __uint_as_float(o[place_of(d)]) * unit_out);
+                        for (int d = 0; d < 32; d += 4) {
+                            float4 &to = rec_to[(b * 8 + d / 4) * 8];
+                            to = make_float4(add(d, to.x), add(d + 1, to.y), add(d + 2, to.z), add(d + 3, to.w));
+                        }
+                    } else if (p.out_wide) {
+                        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_at + b * 32);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint4 had = to[c];
+                            uint32_t w[4] = {had.x, had.y, had.z, had.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int d = c * 8 + i * 2;
+                                w[i] = pack_bf16x2(add(d, __uint_as_float(w[i] << 16)), add(d + 1, __uint_as_float(w[i] & 0xFFFF0000u)));
+                            }
+                            to[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < 32; ++d)
+                            store_value(a.out, out_at + b * 32 + d, true, add(d, load_value(a.out, out_at + b * 32 + d, true)));
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) least = fminf(least, fabsf(__uint_as_float(o[i])));
+                if (!mine) continue;
+                if (bk.slot >= 0) {
+#pragma unroll
+                    for (int d = 0; d < 32; d += 4)
+                        rec_to[(b * 8 + d / 4) * 8] = make_float4(
+                            __uint_as_float(o[place_of(d)]) * unit_out, __uint_as_float(o[place_of(d + 1)]) * unit_out,
+                            __uint_as_float(o[place_of(d + 2)]) * unit_out, __uint_as_float(o[place_of(d + 3)]) * unit_out);
+                } else if (p.out_wide) {
+                    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_at + b * 32);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int d = c * 8 + i * 2;
+                            w[i] = pack_bf16x2(__uint_as_float(o[place_of(d)]) * unit_out, __uint_as_float(o[place_of(d + 1)]) * unit_out);
+                        }
+                        to[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int d = 0; d < 32; ++d)
+                        store_value(a.out, out_at + b * 32 + d, true, __uint_as_float(o[place_of(d)]) * unit_out);
+                }
+            }
+            if (pass == 0 && mine) {
+                if (bk.slot >= 0)
+                    *reinterpret_cast<float2 *>(rec + T::rows * D + row * 2) = make_float2(top, total);
+                else if (a.lse)
+                    a.lse[out_row * a.heads + head] = total == 0.0f ? ninf : (top + log2f(total)) * kLn2;
             }
         }
-        if (mine && a.lse) a.lse[out_row * a.heads + head] = sum == 0.0f ? ninf : (top + log2f(sum)) * kLn2;
-    }
-    const unsigned again = __ballot_sync(0xFFFFFFFFu, ok && mine && least < error);
-    if (lane == 0) sh.again[warp] = again;
-}
-
-// One row in fp32 by all warps: warp w takes every W-th key, a lane the same
-// code bytes of each.
-template <int D, int W>
-__device__ __noinline__ void row_again(const TileParams &p, const Block &bk, float *share, float (*part)[2], int row) {
-    constexpr int B = D / 64;  // code bytes per lane
-    const AttnArgs &a = p.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = a.heads / p.kv_heads;
-    const int flat = bk.flat0 + row, token = flat / heads, head = bk.kv_head * heads + flat - token * heads;
-    const int64_t at = (static_cast<int64_t>(bk.q_row0) + token) * a.q_stride + static_cast<int64_t>(head) * D;
-    const int pos = bk.first + token;
-    const int lo = first_key(a, pos), hi = a.causal ? min(bk.len, pos + 1) : bk.len;
-    const float ninf = __uint_as_float(0xFF800000u);
-    float q[2 * B], o[2 * B];
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-        const int byte = lane + 32 * i, d = (byte >> 4) * 32 + (byte & 15);
-        q[2 * i] = load_value(a.q, at + d, a.q_bf16);
-        q[2 * i + 1] = load_value(a.q, at + d + 16, a.q_bf16);
-        o[2 * i] = o[2 * i + 1] = 0.0f;
-    }
-    float m = ninf, l = 0.0f;
-    for (int j = lo + warp; j < hi; j += W) {
-        const int32_t page = a.table[bk.b * a.table_width + (j >> p.page_shift)];
-        if (page < 0 || page >= p.num_pages) continue;
-        const int64_t r = (((page * p.kv_heads) + bk.kv_head) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int byte = lane + 32 * i;
-            const uint32_t w = p.k_codes[r * (D / 2) + byte];
-            const float d = __half2float(reinterpret_cast<const __half *>(p.k_scales)[r * (D / 32) + (byte >> 4)]);
-            s = fmaf(q[2 * i], (static_cast<float>(w & 15u) - 8.0f) * d, s);
-            s = fmaf(q[2 * i + 1], (static_cast<float>(w >> 4) - 8.0f) * d, s);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-        s *= a.scale * kLog2e;
-        const float now = fmaxf(m, s), ref = now == ninf ? 0.0f : now;
-        const float f = exp2_fast(m - ref), w = exp2_fast(s - ref);
-        m = now;
-        l = fmaf(l, f, w);
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int byte = lane + 32 * i;
-            const uint32_t c = p.v_codes[r * (D / 2) + byte];
-            const float d = __half2float(reinterpret_cast<const __half *>(p.v_scales)[r * (D / 32) + (byte >> 4)]);
-            o[2 * i] = fmaf(o[2 * i], f, w * ((static_cast<float>(c & 15u) - 8.0f) * d));
-            o[2 * i + 1] = fmaf(o[2 * i + 1], f, w * ((static_cast<float>(c >> 4) - 8.0f) * d));
-        }
-    }
-    __syncthreads();  // the last row's shares have been read
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-        const int byte = lane + 32 * i, d = (byte >> 4) * 32 + (byte & 15);
-        share[warp * D + d] = o[2 * i];
-        share[warp * D + d + 16] = o[2 * i + 1];
-    }
-    if (lane == 0) {
-        part[warp][0] = m;
-        part[warp][1] = l;
-    }
-    __syncthreads();
-    float top = ninf, sum = 0.0f;
-    for (int w = 0; w < W; ++w) top = fmaxf(top, part[w][0]);
-    const float ref = top == ninf ? 0.0f : top;
-    for (int w = 0; w < W; ++w) sum = fmaf(exp2_fast(part[w][0] - ref), part[w][1], sum);
-    for (int d = threadIdx.x; d < D; d += W * 32) {
-        float y = 0.0f;
-        for (int w = 0; w < W; ++w) y = fmaf(exp2_fast(part[w][0] - ref), share[w * D + d], y);
-        store_value(a.out, (static_cast<int64_t>(bk.q_row0) + token) * a.out_stride + static_cast<int64_t>(head) * D + d,
-                    true, sum == 0.0f ? 0.0f : y / sum);
+        open = open && ok && least < (pass == 0 ? error : error * raised * down);
+        if (__any_sync(0xFFFFFFFFu, open) && lane == 0) sh.again[pass] = 1;
+        if (!another_pass<D>(sh, pass)) break;
     }
 }
 
@@ -1053,7 +1106,7 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
         fence_mbar_init();
     }
     for (int i = threadIdx.x; i < kRing; i += T::threads) sh.info[i] = TileInfo{};
-    if (threadIdx.x < 8) sh.again[threadIdx.x] = 0;
+    if (threadIdx.x < kPasses) sh.again[threadIdx.x] = 0;
     pdl_wait();
     pdl_launch_dependents();
     find_block<D>(p, sh);
@@ -1072,23 +1125,17 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
         dequant_role<D>(p, sh, smem, warp - T::softmax_warps, lane);
     } else {
         registers_down<T::mma_regs>();
-        if (warp < T::mma_warp + T::QT) mma_role<D>(p, sh, smem_addr(smem), tmem, warp - T::mma_warp);
+        if (warp < T::mma_warp + T::QT) {
+            mma_role<D>(p, sh, smem_addr(smem), tmem, warp - T::mma_warp);
+        } else {
+            for (int pass = 0; another_pass<D>(sh, pass);) ++pass;
+        }
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // back to equal shares, after the barrier only: a role that ended early
-    // would take the registers that the softmax still waits for
-    if (warp < T::softmax_warps)
-        registers_down<T::launch_regs>();
-    else
-        registers_up<T::launch_regs>();
     if (warp == T::mma_warp) tmem_dealloc_cta(tmem, T::tmem_cols);
-#pragma unroll 1
-    for (int w = 0; w < T::softmax_warps; ++w)
-        for (uint32_t again = sh.again[w]; again; again &= again - 1)
-            row_again<D, T::threads / 32>(p, sh.block, reinterpret_cast<float *>(smem), sh.part, w * 32 + __ffs(again) - 1);
 }
 
 // Joins the parts of split blocks, eight rows at a time: a lane has four
@@ -1107,10 +1154,7 @@ __global__ void __launch_bounds__(Join<D>::warps * 32) attn_tile_join_kernel(con
     __shared__ int starts[kMaxTileCtas], counts[kMaxTileCtas];
     __shared__ int chains;
     __shared__ float weight[kMaxTileCtas][8];
-    __shared__ float red[W][8][2];
-    __shared__ float least[W][8];
-    __shared__ float share[W * D];
-    __shared__ float part[W][2];
+    __shared__ float red[W][8];
     pdl_wait();
     pdl_launch_dependents();
     const AttnArgs &a = p.a;
@@ -1145,42 +1189,32 @@ __global__ void __launch_bounds__(Join<D>::warps * 32) attn_tile_join_kernel(con
         const int i0 = threadIdx.x >> 3;
         float top = ninf;
         for (int i = i0; i < k; i += W * 4) {
-            const float t = mine ? record(i)[T::rows * D + row * 4] : ninf;
+            const float t = mine ? record(i)[T::rows * D + row * 2] : ninf;
             weight[i][lane & 7] = t;
             top = fmaxf(top, t);
         }
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-        if (lane < 8) red[warp][lane][0] = top;
+        if (lane < 8) red[warp][lane] = top;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < W; ++w) top = fmaxf(top, red[w][lane & 7][0]);
+        for (int w = 0; w < W; ++w) top = fmaxf(top, red[w][lane & 7]);
         __syncthreads();
         const float ref = top == ninf ? 0.0f : top;
-        float sum = 0.0f, error = 0.0f;
+        float sum = 0.0f;
         for (int i = i0; i < k; i += W * 4) {
-            const float4 s = mine ? *reinterpret_cast<const float4 *>(record(i) + T::rows * D + row * 4) : make_float4(ninf, 0.0f, 0.0f, 0.0f);
+            const float2 s = mine ? *reinterpret_cast<const float2 *>(record(i) + T::rows * D + row * 2) : make_float2(ninf, 0.0f);
             const float f = exp2_fast(s.x - ref);
             weight[i][lane & 7] = f;
             sum = fmaf(f, s.y, sum);
-            error = fmaf(f, s.z, error);
         }
 #pragma unroll
-        for (int o = 8; o < 32; o <<= 1) {
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            error += __shfl_xor_sync(0xFFFFFFFFu, error, o);
-        }
-        if (lane < 8) {
-            red[warp][lane][0] = sum;
-            red[warp][lane][1] = error;
-        }
+        for (int o = 8; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane < 8) red[warp][lane] = sum;
         __syncthreads();
-        sum = error = 0.0f;
+        sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            sum += red[w][lane & 7][0];
-            error += red[w][lane & 7][1];
-        }
+        for (int w = 0; w < W; ++w) sum += red[w][lane & 7];
         float4 v[Q];
 #pragma unroll
         for (int q = 0; q < Q; ++q) v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1203,10 +1237,8 @@ __global__ void __launch_bounds__(Join<D>::warps * 32) attn_tile_join_kernel(con
         const int head = block.kv_head * heads + flat - token * heads;
         const int64_t out_row = static_cast<int64_t>(block.q_row0) + token;
         const float down = sum == 0.0f ? 0.0f : 1.0f / sum;
-        float low = __uint_as_float(0x7F800000u);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            low = fminf(fminf(low, fminf(fabsf(v[q].x), fabsf(v[q].y))), fminf(fabsf(v[q].z), fabsf(v[q].w)));
             const int64_t at = out_row * a.out_stride + static_cast<int64_t>(head) * D + ((warp * Q + q) * 4 + (lane >> 3)) * 4;
             if (!mine) continue;
             if (p.out_wide) {
@@ -1221,14 +1253,6 @@ __global__ void __launch_bounds__(Join<D>::warps * 32) attn_tile_join_kernel(con
         }
         if (warp == 0 && lane < 8 && mine && a.lse)
             a.lse[out_row * a.heads + head] = sum == 0.0f ? ninf : (top + log2f(sum)) * kLn2;
-        low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, 8));
-        low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, 16));
-        if (lane < 8) least[warp][lane] = low;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < W; ++w) low = fminf(low, least[w][lane & 7]);
-        uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && low < error) & 0xFFu;  // the same in every warp
-        for (; again; again &= again - 1) row_again<D, W>(p, block, share, part, row0 + __ffs(again) - 1);
         __syncthreads();  // the item's shared values have been read
     }
 }
@@ -1257,7 +1281,7 @@ cudaError_t launch_tiles(const KvCache &c, const AttnArgs &a, cudaStream_t strea
     using T = Tile<D>;
     static int limits[kMaxDevices];
     constexpr size_t smem = 2 * T::stages * T::bytes + sizeof(TileShared) + 1024;
-    static_assert(smem <= 232448 && T::threads / 32 * D * 4 <= 2 * T::stages * T::bytes, "shared memory per CTA");
+    static_assert(smem <= 232448, "shared memory per CTA");
     cudaError_t e = ensure_smem(attn_tile_kernel<D>, smem, false, limits);
     if (e != cudaSuccess) return e;
     TileParams p = {};

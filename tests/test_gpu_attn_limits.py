@@ -102,3 +102,47 @@ def test_a_nan_in_a_seen_value_stays_in_its_dimensions(qmm, form, out_type, dim,
     lim_o, lim_l = ref.attention_limits(*truth, bf16=out_type == BF16)
     assert (np.abs(out.numpy() - truth[0]) <= lim_o)[~want].all()
     assert (np.abs(lse.cpu().numpy() - truth[1]) <= lim_l).all()
+
+
+@pytest.mark.parametrize("dim,spread", [(64, 4.0), (128, 10.0), (256, 3.0), (256, 30.0)])
+@pytest.mark.parametrize("lens,new", [([700, 300], [300, 300]), ([4000, 1500], [70, 90])])
+def test_sharp_scores_and_zero_dimensions(qmm, dim, spread, lens, new):
+    """Weights over a range that binary16 does not have, and a block of values
+    that is 0 for every key, as where head dimensions are padded."""
+    c = Wide(qmm, lens, new, 16, 2, dim, 64, seed=dim, q_type=BF16, spread=spread)
+    c.arrays[3][..., -1] = 0
+    c.upload(qmm)
+    first = c.call(qmm, BF16)
+    out, _ = c.check(first)
+    assert (out[..., -32:] == 0).all()
+    for _ in range(3):
+        again = c.call(qmm, BF16)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("dim", [128, 256])
+@pytest.mark.parametrize("zero_block", [False, True])
+def test_sharp_scores_take_a_few_passes_at_most(qmm, dim, zero_block):
+    """Trained attention is sharp, and head dimensions are padded with zeros:
+    neither may cost more than four passes over the keys, with room for the
+    clock."""
+    c = Wide(qmm, [4096], [1024], 16, 2, dim, 64, seed=dim, q_type=BF16)
+    if zero_block:
+        c.arrays[3][..., -1] = 0
+        c.upload(qmm)
+    ws, time = qmm.attn_workspace(c.cache, 16), []
+    for spread in (0.1, 1.0, 4.0, 30.0):
+        q = (c.q.float() * spread).to(BF16).cuda()
+        out = torch.empty_like(q)
+        call = lambda: qmm.qmm_attn_q4_0(c.cache, q, out, max_q=1024, scale=c.scale, workspace=ws, **c.dev)  # noqa: E731
+        for _ in range(2):
+            call()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(5):
+            call()
+        b.record()
+        b.synchronize()
+        time.append(a.elapsed_time(b) / 5)
+    assert max(time) <= 6 * time[0], time
