@@ -29,9 +29,10 @@
 // nothing of an output, whose size does not tell whether they cancel or are 0
 // there.  A block with such a row goes over its tiles once more, by the same
 // steps, with what was lost of the weights raised by 2^38, and adds the
-// products; four passes cover fp32's range.  The case of 2048 tokens below by
-// the scores' standard deviation: 1.2 195 us, 2.4 to 8 450, 24 740; with a
-// block of values that are all 0 320, 450 to 920, 945.
+// products; four passes cover fp32's range.  Dimensions in which every value
+// is 0 (the dequant warps note the others) do not count.  The case of 2048
+// tokens below by the scores' standard deviation: 1.2 198 us, 2.4 427, 4 449, 8
+// 470, 24 744.
 //
 // Parts are joined by a second kernel: their outputs and sums, in fp32, are
 // weighted by 2^(m - largest m), in the parts' order.
@@ -136,6 +137,7 @@ struct TileShared {
     uint32_t tmem;
     int abort;
     int again[kPasses];             // whether another pass follows this one
+    alignas(16) uint32_t live[8][4]; // by block: digits of its codes that leave some key a value other than 0
 };
 
 struct TileParams {
@@ -470,6 +472,7 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
     };
     int stage = 0, t = 0;
     uint32_t phase = 0;
+    uint32_t live[U][4] = {};  // of V's codes
     for (int pass = 0;; ++pass) {
         // codes a tile ahead, scales two, pages three
         int32_t page = page_of(2);
@@ -511,6 +514,23 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
                 auto scale_of = [](uint32_t bits) { return exponent(__half2float(__ushort_as_half(static_cast<unsigned short>(bits)))); };
                 e[half] = top ? scale_of(top) : -24;
                 near[half] = !top || e[half] - scale_of(low) <= kNearSpan;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (scales.of[1][u] & 0x7FFFu) {
+                    const uint4 &c = cur.of[1][u];
+                    live[u][0] |= c.x ^ 0x88888888u, live[u][1] |= c.y ^ 0x88888888u;
+                    live[u][2] |= c.z ^ 0x88888888u, live[u][3] |= c.w ^ 0x88888888u;
+                }
+            if (pass == 0 && i + 1 == bk.tiles) {  // known to the softmax when the last tile is
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                        for (int o = 1; o < (D == 64 ? 16 : 8); o <<= 1) live[u][k] |= __shfl_xor_sync(0xFFFFFFFFu, live[u][k], o);
+                        if (lane % (D == 64 ? 16 : 8) == 0 && live[u][k]) atomicOr(&sh.live[block + 4 * u][k], live[u][k]);
+                    }
             }
             if (__any_sync(0xFFFFFFFFu, scales.lost) && lane == 0) {
                 record_error(p.ctx, kDevErrIndex);
@@ -988,7 +1008,10 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
         const float back = pow2i(e_ref - kRaise);  // of O's unit
         const float down = bk.slot >= 0 ? back : total == 0.0f ? 0.0f : back / total;
         const float raised = pow2i(-kPassRaise * pass);
-        float least = __uint_as_float(0x7F800000u);  // output of the row, by its size and in units of `down`
+        // the row's smallest output that some value enters, in units of `down` (or,
+        // where outputs are added to, as it is)
+        float least = __uint_as_float(0x7F800000u);
+        const bool any_faint = __any_sync(0xFFFFFFFFu, faint > 0);
         if (ok) {
             const int64_t out_row = static_cast<int64_t>(bk.q_row0) + token;
             const int64_t out_at = out_row * a.out_stride + static_cast<int64_t>(head) * D;
@@ -1005,6 +1028,12 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
                 const float unit_out = (odd >> b) & 1u ? __uint_as_float(0x7FFFFFFFu) : down;
+                const uint4 live4 = *reinterpret_cast<const uint4 *>(sh.live[b]);
+                auto look_at = [&](int d, float v) {
+                    const int k = (d & 15) >> 2;
+                    const uint32_t live = k == 0 ? live4.x : k == 1 ? live4.y : k == 2 ? live4.z : live4.w;
+                    if (live & (15u << ((d & 3) * 8 + (d >> 4) * 4))) least = fminf(least, fabsf(v));
+                };
                 if (__builtin_expect(pass > 0, 0)) {
                     // added to what this thread wrote before, and rounded once more
                     // (within what the row's scores leave uncertain)
@@ -1012,7 +1041,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                     const float raised_out = raised * unit_out;
                     auto add = [&](int d, float had) {
                         const float v = fmaf(__uint_as_float(o[place_of(d)]), raised_out, had);
-                        least = fminf(least, fabsf(v));
+                        look_at(d, v);
                         return v;
                     };
                     if (bk.slot >= 0) {
@@ -1041,8 +1070,10 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                     }
                     continue;
                 }
+                if (any_faint) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) least = fminf(least, fabsf(__uint_as_float(o[i])));
+                    for (int d = 0; d < 32; ++d) look_at(d, __uint_as_float(o[place_of(d)]));
+                }
                 if (!mine) continue;
                 if (bk.slot >= 0) {
 #pragma unroll
@@ -1107,6 +1138,7 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
     }
     for (int i = threadIdx.x; i < kRing; i += T::threads) sh.info[i] = TileInfo{};
     if (threadIdx.x < kPasses) sh.again[threadIdx.x] = 0;
+    if (threadIdx.x < 32) sh.live[threadIdx.x >> 2][threadIdx.x & 3] = 0;
     pdl_wait();
     pdl_launch_dependents();
     find_block<D>(p, sh);

@@ -146,3 +146,35 @@ def test_sharp_scores_take_a_few_passes_at_most(qmm, dim, zero_block):
         b.synchronize()
         time.append(a.elapsed_time(b) / 5)
     assert max(time) <= 6 * time[0], time
+
+
+@pytest.mark.parametrize("dim", [128, 256])
+@pytest.mark.parametrize("codes", [False, True])
+def test_dimensions_without_values_take_no_passes(qmm, dim, codes):
+    """Padded head dimensions, half a block of them: by scales of 0 or by codes
+    of 0.  What cannot be other than 0 sends nothing over the keys again."""
+    c = Wide(qmm, [4096], [1024], 16, 2, dim, 64, seed=dim, q_type=BF16)
+    ws, q, out = qmm.attn_workspace(c.cache, 16), c.q.cuda(), torch.empty(c.q.shape, dtype=BF16).cuda()
+
+    def time():
+        call = lambda: qmm.qmm_attn_q4_0(c.cache, q, out, max_q=1024, scale=c.scale, workspace=ws, **c.dev)  # noqa: E731
+        for _ in range(2):
+            call()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(10):
+            call()
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b) / 10
+
+    full = time()
+    if codes:
+        low = c.arrays[2][..., -16:]
+        low[...] = (low & 15) | 0x80  # the last 16 dimensions
+    else:
+        c.arrays[3][..., -1] = 0
+    c.upload(qmm)
+    padded = time()
+    assert (out[..., -16:] == 0).all() and not (out[..., -32:] == 0).all() == codes
+    assert padded <= 1.25 * full, (padded, full)
