@@ -11,10 +11,11 @@
 //   softmax   4 per 128 rows, a thread per row: stages Q, turns S into P,
 //             keeps maximum and sum, scales O when the maximum has grown by
 //             more than 2 (powers of two), writes the output
-//   dequant   8: codes and scales from global memory, a tile ahead in
-//             registers, to binary16 rows of 64 values with the 128-byte
-//             swizzle; K is then a K-major operand and V, its rows being keys
-//             too, an MN-major one of the same layout
+//   dequant   8: codes and scales from global memory (plain loads: an append
+//             may write them until pdl_wait), a tile ahead in registers, to
+//             binary16 rows of 64 values with the 128-byte swizzle; K is then a
+//             K-major operand and V, its rows being keys too, an MN-major one
+//             of the same layout
 //   MMA       one per 128 rows; S of the next tile is formed while a tile is
 //             in the softmax (head_dim 256), or the other rows' products run
 // Values keep the order in which a word of codes gives them (0 2 16 18 1 3 17
@@ -457,7 +458,7 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
             for (int u = 0; u < U; ++u) {
                 h.of[half][u] = 0;
                 if (h.there && half >= half0 && half < half1)
-                    h.of[half][u] = __ldg(reinterpret_cast<const uint16_t *>(half ? p.v_scales : p.k_scales) + h.row * NB + block + 4 * u);
+                    h.of[half][u] = reinterpret_cast<const uint16_t *>(half ? p.v_scales : p.k_scales)[h.row * NB + block + 4 * u];
             }
     };
     auto load_codes = [&](const Scales<D> &h, Codes<D> &c) {
@@ -467,7 +468,7 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
             for (int u = 0; u < U; ++u) {
                 c.of[half][u] = make_uint4(0u, 0u, 0u, 0u);
                 if (h.there && half >= half0 && half < half1)
-                    c.of[half][u] = __ldg(reinterpret_cast<const uint4 *>((half ? p.v_codes : p.k_codes) + h.row * (D / 2)) + block + 4 * u);
+                    c.of[half][u] = reinterpret_cast<const uint4 *>((half ? p.v_codes : p.k_codes) + h.row * (D / 2))[block + 4 * u];
             }
     };
     int stage = 0, t = 0;
@@ -737,7 +738,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + q_at);
             auto load = [&](int h) {
 #pragma unroll
-                for (int i = 0; i < C; ++i) raw[i] = __ldg(from + h * C + i);
+                for (int i = 0; i < C; ++i) raw[i] = from[h * C + i];
             };
 #pragma unroll 1
             for (int h = H - 1; h >= 0; --h) {

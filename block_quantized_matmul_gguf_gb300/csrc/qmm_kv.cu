@@ -250,14 +250,14 @@ __device__ __forceinline__ void codes_of(const float (&x)[8], float d, uint32_t 
     }
 }
 
-// kWide: rows of eight values are aligned to 16 bytes.
+// kWide: rows of eight values are aligned to 16 bytes.  No pointer is
+// __restrict__, here and in read: the compiler would take what they point to
+// as constant for the kernel's lifetime, which begins before pdl_wait, while
+// the kernel that writes it still runs.
 template <typename T, bool kWide, int kAhead>
-__global__ void __launch_bounds__(kThreads, 5) append_kernel(KvView c, const T *__restrict__ k,
-                                                          int64_t k_stride,
-                                                          const T *__restrict__ v,
-                                                          int64_t v_stride,
-                                                          const int64_t *__restrict__ slots,
-                                                          int64_t n, int dim, LaunchCtx ctx) {
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(KvView c, const T *k, int64_t k_stride, const T *v,
+                                                             int64_t v_stride, const int64_t *slots, int64_t n,
+                                                             int dim, LaunchCtx ctx) {
     pdl_wait();
     pdl_launch_dependents();
     const int eights = c.kv_heads * dim / 8;  // of a token's keys, and of its values
@@ -350,9 +350,8 @@ __device__ __forceinline__ float4 values_of(uint32_t q, float f) {
 }
 
 template <bool kWide, int kAhead>
-__global__ void __launch_bounds__(kThreads, 5) read_kernel(KvView c, const int64_t *__restrict__ slots,
-                                                        int64_t n, int dim, float *__restrict__ k_out,
-                                                        float *__restrict__ v_out, LaunchCtx ctx) {
+__global__ void __launch_bounds__(kThreads, 5) read_kernel(KvView c, const int64_t *slots, int64_t n, int dim,
+                                                           float *k_out, float *v_out, LaunchCtx ctx) {
     pdl_wait();
     pdl_launch_dependents();
     const int eights = c.kv_heads * dim / 8;
