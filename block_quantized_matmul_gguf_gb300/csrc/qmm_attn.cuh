@@ -97,7 +97,7 @@ __device__ __forceinline__ RequestRows request_rows(const AttnArgs &a, int page_
     const int s0 = a.q_start[b], s1 = a.q_start[b + 1], total = static_cast<int>(a.total_q);
     const int n = max(s1 - s0, 0), len = a.kv_len[b];
     r.row0 = min(max(s0, 0), total);
-    r.rows = min(max(min(s1, total) - r.row0, 0), n);
+    r.rows = min(min(max(min(s1, total) - r.row0, 0), n), a.max_q);
     const int64_t room = min(a.table_width << page_shift, static_cast<int64_t>(INT32_MAX - 256));
     r.len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), room));
     r.first = max(len, 0) - n;

@@ -384,7 +384,8 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_q4_0 *cache, const int64_t *slots, int6
  *              elements apart; q_type and out_type may differ
  *   lse        fp32 [total_q][heads], or NULL
  *   table      int32 [batch][table_width] page indices
- *   max_q      host-side bound of a request's new tokens
+ *   max_q      host-side bound of a request's new tokens; its later rows are
+ *              left out
  *   workspace  16-byte aligned device memory of at least
  *              qmm_attn_q4_0_workspace_bytes() bytes, scratch of the call
  * The sizes of the launch depend on the host-side arguments alone, so the

@@ -178,3 +178,19 @@ def test_dimensions_without_values_take_no_passes(qmm, dim, codes):
     padded = time()
     assert (out[..., -16:] == 0).all() and not (out[..., -32:] == 0).all() == codes
     assert padded <= 1.25 * full, (padded, full)
+
+
+@pytest.mark.parametrize("form,out_type", FORMS)
+@pytest.mark.parametrize("long", [130, 1900])
+def test_rows_beyond_max_q_are_left_out(qmm, form, out_type, long):
+    c = form(qmm, [long, 120], [100, 50], 16, 2, 128, 16, seed=5, q_type=BF16)
+    c.check(c.call(qmm, out_type))
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
+    want = ref.attention(c.q.double().numpy(), *c.arrays, c.table, c.q_start, c.lens, c.scale, True, 0)
+    limit, limit_lse = ref.attention_limits(*want, bf16=out_type == BF16)
+    out, lse = c.call(qmm, out_type, max_q=60)
+    assert qmm.qmm_get_device_error() == qmm.QMM_ERR_INDEX
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    kept = np.r_[0:60, 100:150]  # of the first request its first 60 tokens, where they stand
+    assert (out[60:100] == 7.0).all() and (lse[60:100] == 7.0).all()
+    assert (np.abs(out - want[0]) <= limit)[kept].all() and (np.abs(lse - want[1]) <= limit_lse)[kept].all()
