@@ -88,7 +88,7 @@ __device__ __forceinline__ int first_key(const AttnArgs &a, int pos) {
 struct RequestRows {
     int row0, rows;  // first row of q, and rows that are there
     int len;         // keys, within the table
-    int first;       // position of row 0 (may be negative)
+    int first;       // position of row row0 (may be negative)
     int bad;         // something had to be cut
 };
 
@@ -100,7 +100,7 @@ __device__ __forceinline__ RequestRows request_rows(const AttnArgs &a, int page_
     r.rows = min(min(max(min(s1, total) - r.row0, 0), n), a.max_q);
     const int64_t room = min(a.table_width << page_shift, static_cast<int64_t>(INT32_MAX - 256));
     r.len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), room));
-    r.first = max(len, 0) - n;
+    r.first = max(len, 0) - n + (r.rows > 0 ? r.row0 - s0 : 0);  // rows cut in front keep their positions
     r.bad = s0 < 0 || s1 > total || s1 < s0 || n > a.max_q || len < 0 || len > room;
     return r;
 }

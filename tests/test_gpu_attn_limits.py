@@ -194,3 +194,17 @@ def test_rows_beyond_max_q_are_left_out(qmm, form, out_type, long):
     kept = np.r_[0:60, 100:150]  # of the first request its first 60 tokens, where they stand
     assert (out[60:100] == 7.0).all() and (lse[60:100] == 7.0).all()
     assert (np.abs(out - want[0]) <= limit)[kept].all() and (np.abs(lse - want[1]) <= limit_lse)[kept].all()
+
+
+@pytest.mark.parametrize("form,out_type", FORMS)
+@pytest.mark.parametrize("long", [130, 1900])
+def test_rows_before_the_first_leave_the_others_in_place(qmm, form, out_type, long):
+    c = form(qmm, [long, 120], [100, 50], 16, 2, 128, 16, seed=6, q_type=BF16)
+    want = ref.attention(c.q.double().numpy(), *c.arrays, c.table, c.q_start, c.lens, c.scale, True, 0)
+    limit, limit_lse = ref.attention_limits(*want, bf16=out_type == BF16)
+    c.q = c.q[3:]
+    c.dev["q_start"] -= 3
+    out, lse = c.call(qmm, out_type)
+    assert qmm.qmm_get_device_error() == qmm.QMM_ERR_INDEX
+    assert (np.abs(out.float().cpu().numpy() - want[0][3:]) <= limit[3:]).all()
+    assert (np.abs(lse.cpu().numpy() - want[1][3:]) <= limit_lse[3:]).all()
