@@ -91,7 +91,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
         if (blockIdx.x == 0) {
             p.q_start[b] = start[b];
             bad |= now > INT32_MAX || page1 > p.table_width;
-            p.kv_len[b] = static_cast<int32_t>(min(now, static_cast<int64_t>(INT32_MAX)));
+            // tokens without a row do not count: the others stand at their positions
+            const int64_t here = had + min(tokens + now - had, p.capacity) - start[b];
+            p.kv_len[b] = static_cast<int32_t>(min(here, static_cast<int64_t>(INT32_MAX)));
         }
         tokens += now - had;
         pages += page1 - page0;

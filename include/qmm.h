@@ -334,7 +334,8 @@ typedef enum qmm_dtype { QMM_F32 = 0, QMM_BF16 = 1 } qmm_dtype;
  * positions, so that a captured graph may run with one capacity for every
  * step.  Where free_pages or a row of the table is too short, the pages and
  * slots concerned are -1; where the tokens exceed capacity, q_start stops at
- * capacity; each of these, and a negative length (taken as 0), records
+ * capacity and kv_len counts the tokens that have a row (table and taken are
+ * those of all); each of these, and a negative length (taken as 0), records
  * QMM_ERR_INDEX.  The same call again gives the same result.
  * Requires batch >= 1 (at most 16384, else QMM_ERR_UNSUPPORTED), page_size
  * as above, table_width >= 1, num_free >= 0, capacity >= 0, both below 2^31;
