@@ -351,8 +351,9 @@ qmm_status qmm_kv_plan(const int32_t *cached, const int32_t *added, int batch,
  * of kv_heads * head_dim values of type `type`, rows k_stride and v_stride
  * elements apart (so that they may be columns of one projection's output);
  * slots[n] names their cache slots: -1 skips the token, any other slot
- * outside the cache is skipped and records QMM_ERR_INDEX.  Two tokens with
- * one slot leave either's block there.
+ * outside the cache is skipped and records QMM_ERR_INDEX.  Two tokens of one
+ * call must not share a slot (a plan gives none twice): codes of one may stay
+ * beside the scale of the other there; other slots are not affected.
  * Per 32 values x: with e = max x if max x >= -min x, else min x, the scale
  * is d = binary16(e / -8), kept within +-65504, and the code of x is
  * round(x / d) (to nearest even) + 8, within 0..15, or 8 where d is 0.  A

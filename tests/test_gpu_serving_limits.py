@@ -23,3 +23,16 @@ def test_plan_counts_only_tokens_that_have_a_row(qmm):
         assert qmm.qmm_get_device_error() == (qmm.QMM_OK if cap == 69 else qmm.QMM_ERR_INDEX)
         assert got[1].tolist() == [0, *np.cumsum(kept)]
         assert got[2].tolist() == (cached + kept).tolist()
+
+
+def test_a_slot_given_twice_spoils_no_other(qmm):
+    """What stands in it is not defined; its neighbours are as they were."""
+    cache = qmm.kv_cache_q4_0(2, 16, 2, 128)
+    x = torch.randn(300, 2, 128).cuda()
+    qmm.qmm_kv_append_q4_0(cache, x[:32], x[:32], torch.arange(32).cuda())
+    before = [a.copy() for a in kv.cache_arrays(cache)]
+    qmm.qmm_kv_append_q4_0(cache, x, x, torch.full((300,), 21).cuda())
+    for a, b in zip(before, kv.cache_arrays(cache)):
+        a[1, :, 5], b[1, :, 5] = 0, 0
+        assert np.array_equal(a, b)
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
