@@ -36,3 +36,48 @@ def test_a_slot_given_twice_spoils_no_other(qmm):
         a[1, :, 5], b[1, :, 5] = 0, 0
         assert np.array_equal(a, b)
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("vocab,extra,mask", [(262144, 0, False), (50001, 9000, True), (3000, 20000, True)])
+def test_long_bias_lists(qmm, vocab, extra, mask):
+    """A bias for every token, and ids that come several times: sums in list
+    order, in a time that grows with the list and not with its square."""
+    rng = np.random.default_rng(vocab)
+    x, h, prompt, rep, freq, pres, _, allowed = lg.make(rng, 2, vocab, 500, 0)
+    def entries():
+        ids = np.concatenate([rng.permutation(vocab), rng.integers(-2, vocab + 2, extra)])
+        rng.shuffle(ids)
+        return [(int(t), float(np.float32(v))) for t, v in zip(ids, rng.standard_normal(len(ids)))]
+    bias = [entries(), entries()[:700]]
+    case = (x, h, prompt, rep, freq, pres, bias, allowed if mask else None)
+    y = lg.call(qmm, *case)
+    lg.check(y, *case)
+    z = torch.from_numpy(x).cuda()
+    lg.call(qmm, z, *case[1:], out=z)  # in place
+    assert torch.equal(y, z)
+    f = lambda a, t: torch.from_numpy(np.asarray(a, t)).cuda()  # noqa: E731
+    flat = [e for b in bias for e in b]
+    kw = dict(bias_ids=f([t for t, _ in flat], np.int32), bias_values=f([v for _, v in flat], np.float32),
+              bias_start=f([0, len(bias[0]), len(flat)], np.int32))
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    qmm.qmm_logits_adjust(z, z, **kw)
+    b.record()
+    b.synchronize()
+    assert a.elapsed_time(b) < 10.0
+
+
+def test_long_bias_lists_keep_the_order(qmm):
+    """1e8 absorbs what comes right after it, beyond the entries kept aside too."""
+    n = 3000
+    rng = np.random.default_rng(1)
+    ids = rng.integers(0, 40, n)
+    vals = rng.choice(np.array([1e8, 1.0, -1e8, 0.5], np.float32), n)
+    zero = np.zeros(1, np.float32)
+    x = rng.standard_normal((1, 50)).astype(np.float32)
+    y = lg.call(qmm, x, [np.zeros(0, np.int64)], np.array([0]), zero + 1, zero, zero,
+                [[(int(t), float(v)) for t, v in zip(ids, vals)]], None).cpu().numpy()[0]
+    s = np.zeros(50, np.float32)
+    for t, v in zip(ids, vals):
+        s[t] = np.float32(s[t] + v)
+    assert np.array_equal(y, x[0] + s)
