@@ -49,6 +49,7 @@ class Generator:
         self.free_at = 0  # pages taken so far
         self.kv_len = torch.zeros(batch, **i32)
         self.history = [[] for _ in range(batch)]
+        self.hidden = torch.zeros((batch, layer.hidden), device=dev)  # last row of each request
         self.prompt_len = torch.zeros(batch, **i32)
 
     def _project(self, weights, x, n_out, k):
@@ -58,9 +59,12 @@ class Generator:
         return qmm.gemm("q4_0", weights, x, n_out, k)
 
     def forward(self, tokens):
-        """tokens: a list of new token ids for each request (any may be empty).
-        Returns the last row's hidden state of each request [batch][hidden]."""
+        """tokens: a list of new token ids for each request; one without any keeps
+        its last row's hidden state (zeros before its first token).
+        Returns those states [batch][hidden]."""
         layer, dev = self.layer, self.layer.device
+        if not any(tokens):
+            return self.hidden
         added = torch.tensor([len(t) for t in tokens], dtype=torch.int32, device=dev)
         total, most = sum(len(t) for t in tokens), max(len(t) for t in tokens)
         page = self.cache.page_size
@@ -96,7 +100,9 @@ class Generator:
         x = x + self._project(layer.wo, out.view(total, width), layer.hidden, width)
         self.kv_len = kv_len
         self.last = dict(q=q.view(out.shape), out=out, q_start=q_start, slots=slots, positions=positions)
-        return x[(q_start[1:] - 1).long().clamp(min=0)].contiguous()
+        ends = x[(q_start[1:] - 1).long().clamp(min=0)]  # of a request without new tokens, another's
+        self.hidden = torch.where((added > 0)[:, None], ends, self.hidden)
+        return self.hidden
 
     def logits(self, rows, repetition=1.1, frequency=0.1, presence=0.1, bias=None, allowed=None):
         """LM head and adjustment of [batch][hidden] rows (at most 16)."""

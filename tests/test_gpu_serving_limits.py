@@ -81,3 +81,29 @@ def test_long_bias_lists_keep_the_order(qmm):
     for t, v in zip(ids, vals):
         s[t] = np.float32(s[t] + v)
     assert np.array_equal(y, x[0] + s)
+
+
+@pytest.fixture(scope="module")
+def gen(qmm):
+    from block_quantized_matmul_gguf_gb300 import generate
+    return generate
+
+
+def small_layer(gen):
+    return gen.Layer(hidden=256, heads=4, kv_heads=2, head_dim=64, vocab=512, seed=3)
+
+
+def test_a_request_without_new_tokens_answers_for_itself(gen):
+    layer = small_layer(gen)
+    g = gen.Generator(layer, 3)
+    first = g.step([[1, 2, 3], [4] * 40, [9, 8]])
+    second = g.step([[first[0]], [], [first[2]]])
+    assert second[1] == first[1]  # its cache and its history are as they were
+    assert g.kv_len.tolist() == [4, 40, 3]
+    assert g.step([[], [], []]) == second
+    assert g.kv_len.tolist() == [4, 40, 3]
+    # beside others or alone, it goes on as if nothing had been between
+    lone = gen.Generator(layer, 3)
+    lone.step([[1, 2, 3], [4] * 40, [9, 8]])
+    lone.step([[first[0]], [], [first[2]]])
+    assert g.step([[], [first[1]], []])[1] == lone.step([[], [first[1]], []])[1]
