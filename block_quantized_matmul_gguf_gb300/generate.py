@@ -72,6 +72,8 @@ class Generator:
         taken = sum(-(-(n + len(t)) // page) - -(-n // page) for n, t in zip(lens, tokens))
         if self.free_at + taken > self.free.numel():
             raise RuntimeError("the cache is full")
+        if max(n + len(t) for n, t in zip(lens, tokens)) > self.table.shape[1] * page:
+            raise RuntimeError("a request is longer than its row of the page table")
         q_start = torch.empty(self.batch + 1, dtype=torch.int32, device=dev)
         kv_len, used = torch.empty_like(self.kv_len), torch.empty(1, dtype=torch.int32, device=dev)
         slots = torch.empty(total, dtype=torch.int64, device=dev)

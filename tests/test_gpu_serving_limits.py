@@ -107,3 +107,13 @@ def test_a_request_without_new_tokens_answers_for_itself(gen):
     lone.step([[1, 2, 3], [4] * 40, [9, 8]])
     lone.step([[first[0]], [], [first[2]]])
     assert g.step([[], [first[1]], []])[1] == lone.step([[], [first[1]], []])[1]
+
+
+def test_a_request_longer_than_its_table_row_is_refused(gen, qmm):
+    g = gen.Generator(small_layer(gen), 2, max_pages=2)
+    g.step([[1] * 30, [2]])
+    with pytest.raises(RuntimeError):
+        g.step([[1] * 3, [2]])
+    assert g.kv_len.tolist() == [30, 1]
+    g.step([[1] * 2, [2]])
+    assert g.kv_len.tolist() == [32, 2] and qmm.qmm_get_device_error() == qmm.QMM_OK
