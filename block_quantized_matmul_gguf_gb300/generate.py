@@ -137,7 +137,8 @@ class Generator:
 
     def run(self, prompts, steps, **adjust):
         """Prompts first, then one token a request and step; the tokens generated."""
-        self.prompt_len = torch.tensor([len(p) for p in prompts], dtype=torch.int32, device=self.layer.device)
+        self.prompt_len = torch.tensor([len(h) + len(p) for h, p in zip(self.history, prompts)], dtype=torch.int32,
+                                       device=self.layer.device)
         made = [[] for _ in prompts]
         tokens = prompts
         for _ in range(steps):

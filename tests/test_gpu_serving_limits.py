@@ -117,3 +117,14 @@ def test_a_request_longer_than_its_table_row_is_refused(gen, qmm):
     assert g.kv_len.tolist() == [30, 1]
     g.step([[1] * 2, [2]])
     assert g.kv_len.tolist() == [32, 2] and qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+def test_a_second_run_counts_its_own_tokens(gen):
+    """What an earlier run brought is prompt to the next one."""
+    layer = small_layer(gen)
+    g = gen.Generator(layer, 1)
+    made = g.run([[1, 2, 3]], 4)[0]
+    before = list(g.history[0])
+    assert before == [1, 2, 3] + made[:3]
+    g.run([[5, 6]], 1)
+    assert g.prompt_len.tolist() == [len(before) + 2]
