@@ -71,7 +71,8 @@ struct Layout {
     static constexpr int bias = q + NT * NB * 512;       // -8 sum q [NT][NB][4 lanes] x {c0, c1, c0, c1}, bf16 only
     static constexpr int d = bias + (EXACT ? 0 : NT * NB * 64);        // V's scales by block: pairs of keys, binary16 or fp32
     static constexpr int p = d + NB * kTile * (EXACT ? 4 : 2);  // weights [rows][p_stride], EXACT only
-    static constexpr int rest_bytes = p + (EXACT ? rows * p_stride * 4 : 0);
+    static constexpr int unit = p + (EXACT ? rows * p_stride * 4 : 0);  // of V's blocks, fp32
+    static constexpr int rest_bytes = unit + (NB * 4 + 15) / 16 * 16;
     // CTAs on an SM: as the registers of the accumulators allow
     static constexpr int ctas = D == 256 ? 1 : D == 128 && NT == 2 ? 1 : 2;
     static constexpr int fit = (232448 / ctas - 1024 - 14336) / (code_bytes + rest_bytes);
@@ -622,50 +623,55 @@ __device__ __forceinline__ void tile_scores(WarpState<D, NT, EXACT> &w, uint32_t
 }
 
 // V's scales, by block and in the order the B operand takes keys: 0 1 8 9
-// 2 3 10 11 ... of each 16.  They are scaled so that the largest lies in
-// [1, 2) (binary16) or [2^14, 2^15) (fp32), and 0 where `seen` has no bit for
-// the key (bit i: key 2 lane + i).  Returns the exponent of the largest.
+// 2 3 10 11 ... of each 16.  They are scaled so that the block's largest lies
+// in [1, 2) (binary16) or [2^14, 2^15) (fp32), and 0 where `seen` has no bit
+// for the key (bit i: key 2 lane + i).  Each block has a unit of its own: one
+// for all would take the low bits of p d from the outputs of small blocks.
 template <int D, int NT, bool EXACT>
-__device__ __forceinline__ int tile_scales(WarpState<D, NT, EXACT> &w, unsigned seen) {
+__device__ __forceinline__ void tile_scales(WarpState<D, NT, EXACT> &w, unsigned seen) {
     using L = Layout<D, NT, EXACT>;
     constexpr int NB = L::NB;
     const uint16_t *vs = reinterpret_cast<const uint16_t *>(w.rest + L::v_scales) + w.lane * 2 * NB;
     uint32_t d[2][NB / 2];
     load_scales<NB>(vs, d[0]);
     load_scales<NB>(vs + NB, d[1]);
-    uint32_t big = 0u;
+    int e[NB];  // exponents of the blocks' largest
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < NB / 2; ++i) {
 #pragma unroll
-        for (int i = 0; i < NB / 2; ++i) {
+        for (int k = 0; k < 2; ++k)
             if (!((seen >> k) & 1u)) d[k][i] = 0u;
-            // NaN is passed over
-            big = hmax2(big, d[k][i] & 0x7FFF7FFFu);
+        // NaN is passed over, and infinity counts as 65504; the order of positive
+        // numbers is that of their bits
+        const uint32_t big = hmin2(hmax2(hmax2(d[0][i] & 0x7FFF7FFFu, d[1][i] & 0x7FFF7FFFu), 0u), 0x7BFF7BFFu);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, h ? big >> 16 : big & 0xFFFFu);
+            e[2 * i + h] = top ? exponent(low_float(top)) : 0;
         }
-    // infinity counts as 65504; the order of positive numbers is that of their bits
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(fmaxf(low_float(big), high_float(big)), 65504.0f)));
-    const int e = top ? exponent(__uint_as_float(top)) : 0;
+    }
+    float *unit = reinterpret_cast<float *>(w.rest + L::unit);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        if (w.lane == b) unit[b] = pow2i(e[b]);
     const int i8 = w.lane >> 3, i4 = (w.lane >> 2) & 1, i2 = w.lane & 3;
     if constexpr (EXACT) {
         float2 *to = reinterpret_cast<float2 *>(w.rest + L::d) + i8 * 8 + i2 * 2 + i4;
-        const float up = pow2i(14 - e);
 #pragma unroll
         for (int i = 0; i < NB / 2; ++i) {
-            to[(2 * i) * (kTile / 2)] = make_float2(low_float(d[0][i]) * up, low_float(d[1][i]) * up);
-            to[(2 * i + 1) * (kTile / 2)] = make_float2(high_float(d[0][i]) * up, high_float(d[1][i]) * up);
+            const float up0 = pow2i(14 - e[2 * i]), up1 = pow2i(14 - e[2 * i + 1]);
+            to[(2 * i) * (kTile / 2)] = make_float2(low_float(d[0][i]) * up0, low_float(d[1][i]) * up0);
+            to[(2 * i + 1) * (kTile / 2)] = make_float2(high_float(d[0][i]) * up1, high_float(d[1][i]) * up1);
         }
     } else {
         uint32_t *to = reinterpret_cast<uint32_t *>(w.rest + L::d) + i8 * 8 + i2 * 2 + i4;
-        // 2^-e in two factors that binary16 has
-        const float f1 = pow2i(min(-e, 15)), f2 = pow2i(-e - min(-e, 15));
-        const uint32_t h1 = pack_rn(f1, f1), h2 = pack_rn(f2, f2);
 #pragma unroll
         for (int i = 0; i < NB / 2; ++i) {
-            to[(2 * i) * (kTile / 2)] = hmul2(hmul2(__byte_perm(d[0][i], d[1][i], 0x5410), h1), h2);
-            to[(2 * i + 1) * (kTile / 2)] = hmul2(hmul2(__byte_perm(d[0][i], d[1][i], 0x7632), h1), h2);
+            const float up0 = pow2i(-e[2 * i]), up1 = pow2i(-e[2 * i + 1]);
+            to[(2 * i) * (kTile / 2)] = pack_rn(low_float(d[0][i]) * up0, low_float(d[1][i]) * up0);
+            to[(2 * i + 1) * (kTile / 2)] = pack_rn(high_float(d[0][i]) * up1, high_float(d[1][i]) * up1);
         }
     }
-    return e;
 }
 
 // -(x & keep)
@@ -673,7 +679,7 @@ __device__ __forceinline__ float minus_part(float x, uint32_t keep) {
     return __uint_as_float((__float_as_uint(x) & keep) ^ 0x80000000u);
 }
 
-// out = out * f + g * sum over the tile's keys of (p d) (n - 8), with the
+// out = out * f + g * unit * sum over the tile's keys of (p d) (n - 8), with the
 // weights in shared memory (EXACT) or in pw, as binary16 B operands.
 // EDGE: some row does not see some key of the tile, whose scale may then be
 // anything.
@@ -688,6 +694,7 @@ __device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, uint32_t
     const int sw = chunk_swizzle<D>(token);
     const uint32_t base = smem_addr(w.codes) + L::codes + token * (D / 2);
     const uint32_t keep = EXACT && (w.g & 1) ? 0xFFFFE000u : 0u;  // odd columns hold the second part
+    const float2 *unit = reinterpret_cast<const float2 *>(w.rest + L::unit);
 #pragma unroll
     for (int bp = 0; bp < NB / 2; ++bp) {
         float acc[NT][2][2][4];
@@ -764,11 +771,14 @@ __device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, uint32_t
                 }
             }
         }
+        const float2 units = unit[bp];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float2 f2 = make_float2(f[n][0], f[n][EXACT ? 0 : 1]), g2 = make_float2(g[n][0], g[n][EXACT ? 0 : 1]);
+            const float2 f2 = make_float2(f[n][0], f[n][EXACT ? 0 : 1]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                const float u = h ? units.y : units.x;
+                const float2 g2 = make_float2(g[n][0] * u, g[n][EXACT ? 0 : 1] * u);
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -776,6 +786,7 @@ __device__ __forceinline__ void tile_values(WarpState<D, NT, EXACT> &w, uint32_t
                         const float2 v = make_float2(acc[n][h][m][2 * i], acc[n][h][m][2 * i + 1]);
                         w.out[n][2 * bp + h][m][i] = __ffma2_rn(w.out[n][2 * bp + h][m][i], f2, __fmul2_rn(v, g2));
                     }
+            }
         }
     }
 }
@@ -908,15 +919,14 @@ __device__ __forceinline__ void run_part(const StreamParams &p, WarpState<D, NT,
                 faint |= u * w.unit[n][k] < top[n][k] - 23.5f;
             }
         copies_wait();  // V is there; the next K may be under way
-        const int e_max = tile_scales<D, NT, EXACT>(w, seen);
+        tile_scales<D, NT, EXACT>(w, seen);
         // f: factor of what is there already; g: of this tile's products.  The
-        // products carry the scales' factor 2^(14 - e_max) (bf16 output:
-        // 2^-e_max, and 2^14 of the weights) and, for bf16 output, 2^-24 of the
-        // codes.
+        // products carry 2^14 of the scales (bf16 output: of the weights) and, for
+        // bf16 output, 2^-24 of the codes, beside their block's unit.
         float f[NT][R], g[NT][R];
         float *pp = reinterpret_cast<float *>(w.rest + L::p) + (w.g >> 1) * 4 + (w.g & 1);
         uint32_t pw[NT][4][2];
-        const float unit_out = pow2i((EXACT ? -14 : 10) + e_max);
+        const float unit_out = pow2i(EXACT ? -14 : 10);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll

@@ -208,3 +208,19 @@ def test_rows_before_the_first_leave_the_others_in_place(qmm, form, out_type, lo
     assert qmm.qmm_get_device_error() == qmm.QMM_ERR_INDEX
     assert (np.abs(out.float().cpu().numpy() - want[0][3:]) <= limit[3:]).all()
     assert (np.abs(lse.cpu().numpy() - want[1][3:]) <= limit_lse[3:]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("out_type", [F32, BF16])
+@pytest.mark.parametrize("span", [10, 16, 24])
+@pytest.mark.parametrize("new", [1, 30])
+def test_small_blocks_of_values_keep_their_bits(qmm, dim, out_type, span, new):
+    """Value scales that fall by 2^span from the first block of a head to the
+    last: each block's outputs are right by their own size."""
+    for seed in range(3):
+        c = base.Case(qmm, [200, 1300], [new, new], 8, 1, dim, 32, seed=span + 100 * seed, q_type=BF16)
+        s = c.arrays[3].astype(np.float32)
+        step = np.float32(2.0) ** -(np.arange(dim // 32) * span // (dim // 32 - 1))
+        c.arrays[3] = (s / np.nanmax(s) * 16 * step).astype(np.float16)
+        c.cache = qmm.KvCacheQ4_0(*(torch.from_numpy(a).cuda() for a in c.arrays))
+        c.check(c.call(qmm, out_type))
