@@ -224,3 +224,37 @@ def test_small_blocks_of_values_keep_their_bits(qmm, dim, out_type, span, new):
         c.arrays[3] = (s / np.nanmax(s) * 16 * step).astype(np.float16)
         c.cache = qmm.KvCacheQ4_0(*(torch.from_numpy(a).cuda() for a in c.arrays))
         c.check(c.call(qmm, out_type))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("spread", [1.0, 12.0])
+@pytest.mark.parametrize("new,window", [(1, 0), (3, 0), (30, 40)])
+def test_bf16_queries_enter_the_streaming_form_exactly(qmm, dim, spread, new, window):
+    """Where q is bf16 and the codes are used as they are, only sums and weights
+    round.  A block's product of integers 0..15 with q, less 8 times q's sum,
+    is formed in sums that keep 18 bits of their largest term; with B = scale *
+    max_j sum_d (n + 8) d |q| a score is off by less than B * 2^-15 (a block
+    takes two sums of 16 terms).  p, p d and the output round once to 11, 11
+    and 8 bits:
+        |out - ref| <= S * (2 * B * 2^-15 + 2^-10) + 2^-8 * |ref| + 1e-30
+        |lse - ref| <= B * 2^-15 + 2^-18 * (1 + |lse|)
+    which, at scores of some hundred, is far below the bound for q and k of 11
+    bits."""
+    c = base.Case(qmm, [300, 90], [new, new], 8, 2, dim, 16, seed=dim + new, q_type=BF16, spread=spread)
+    out, lse = c.call(qmm, BF16, window=window)
+    q = c.q.double().numpy()
+    want, want_lse, _, share = ref.attention(q, *c.arrays, c.table, c.q_start, c.lens, c.scale, True, window)
+    codes = [a.copy() for a in c.arrays[:2]]
+    n = np.concatenate([codes[0].reshape(*codes[0].shape[:-1], -1, 16) & 15,
+                        codes[0].reshape(*codes[0].shape[:-1], -1, 16) >> 4], -1).astype(np.float64) + 8
+    size = (n * np.abs(codes[1].astype(np.float64))[..., None]).reshape(*codes[0].shape[:-1], -1)
+    big = np.zeros(want_lse.shape)
+    for b, length in enumerate(c.lens):
+        rows = slice(int(c.q_start[b]), int(c.q_start[b + 1]))
+        ids = c.table[b, :-(-length // 16)]
+        for h in range(2):
+            k = size[ids, h].reshape(-1, dim)[:length]
+            big[rows, 4 * h:4 * h + 4] = (np.abs(q[rows, 4 * h:4 * h + 4]) @ k.T).max(-1) * c.scale
+    limit = share * (2 * big[..., None] * 2.0 ** -15 + 2.0 ** -10) + 2.0 ** -8 * np.abs(want) + 1e-30
+    assert (np.abs(out.double().cpu().numpy() - want) <= limit).all()
+    assert (np.abs(lse.cpu().numpy() - want_lse) <= big * 2.0 ** -15 + 2.0 ** -18 * (1 + np.abs(want_lse))).all()
