@@ -31,9 +31,9 @@
 // there.  A block with such a row goes over its tiles once more, by the same
 // steps, with what was lost of the weights raised by 2^38, and adds the
 // products; four passes cover fp32's range.  Dimensions in which every value
-// is 0 (the dequant warps note the others) do not count.  The case of 2048
-// tokens below by the scores' standard deviation: 1.2 198 us, 2.4 427, 4 449, 8
-// 470, 24 744.
+// is 0 do not count.  The case of 2048 tokens below by the scores' standard
+// deviation, from a flushed L2: 1.2 200 us, 2.4 409, 4 435, 8 451, 24 722; with
+// one block of values that are all 0 243, 493, 536, 549, 780.
 //
 // Parts are joined by a second kernel: their outputs and sums, in fp32, are
 // weighted by 2^(m - largest m), in the parts' order.
@@ -97,9 +97,7 @@ struct TileInfo {
     float k_unit[8];       // K of a group is scaled by 1 / k_unit
     int v_exp[8];          // V by 2^-(v_exp / 2); odd where its values may reach 16, not 2^-6
     uint32_t lost;         // 16-key groups without a page
-    uint32_t odd;          // blocks of V in which some key's scale is a NaN or an infinity, a bit each
-    uint32_t pad[2];
-    uint32_t odd_keys[8][2];  // those keys, by block
+    uint32_t pad[3];
 };
 
 // Rows of one request and key head, and the tiles of their keys: all, or a part.
@@ -138,7 +136,8 @@ struct TileShared {
     uint32_t tmem;
     int abort;
     int again[kPasses];             // whether another pass follows this one
-    alignas(16) uint32_t live[8][4]; // by block: digits of its codes that leave some key a value other than 0
+    int odd;                        // whether some value's scale is a NaN or an infinity
+    uint4 live[8][8];               // by softmax warp and block: digits of V's codes in which some value is not 0
 };
 
 struct TileParams {
@@ -473,7 +472,6 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
     };
     int stage = 0, t = 0;
     uint32_t phase = 0;
-    uint32_t live[U][4] = {};  // of V's codes
     for (int pass = 0;; ++pass) {
         // codes a tile ahead, scales two, pages three
         int32_t page = page_of(2);
@@ -501,10 +499,7 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
                 for (int u = 0; u < U; ++u) {
                     uint32_t bits = scales.of[half][u] & 0x7FFFu;
                     if (bits >= 0x7C00u) {
-                        if (half && scales.there) {
-                            atomicOr(&info.odd_keys[block + 4 * u][key >> 5], 1u << (key & 31));
-                            atomicOr(&info.odd, 1u << (block + 4 * u));
-                        }
+                        if (half && scales.there) sh.odd = 1;
                         bits = 0;  // NaN and infinity do not set the scale
                     }
                     top = max(top, bits);
@@ -515,23 +510,6 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
                 auto scale_of = [](uint32_t bits) { return exponent(__half2float(__ushort_as_half(static_cast<unsigned short>(bits)))); };
                 e[half] = top ? scale_of(top) : -24;
                 near[half] = !top || e[half] - scale_of(low) <= kNearSpan;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (scales.of[1][u] & 0x7FFFu) {
-                    const uint4 &c = cur.of[1][u];
-                    live[u][0] |= c.x ^ 0x88888888u, live[u][1] |= c.y ^ 0x88888888u;
-                    live[u][2] |= c.z ^ 0x88888888u, live[u][3] |= c.w ^ 0x88888888u;
-                }
-            if (pass == 0 && i + 1 == bk.tiles) {  // known to the softmax when the last tile is
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                        for (int o = 1; o < (D == 64 ? 16 : 8); o <<= 1) live[u][k] |= __shfl_xor_sync(0xFFFFFFFFu, live[u][k], o);
-                        if (lane % (D == 64 ? 16 : 8) == 0 && live[u][k]) atomicOr(&sh.live[block + 4 * u][k], live[u][k]);
-                    }
             }
             if (__any_sync(0xFFFFFFFFu, scales.lost) && lane == 0) {
                 record_error(p.ctx, kDevErrIndex);
@@ -549,11 +527,8 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
                     info.k_unit[w8] = k_unit;
                     info.v_exp[w8] = v_exp;
                 }
-            }
-            if (w8 == 0) {  // not in use: the warps' and the readers' tiles lie less apart
-                TileInfo &later = sh.info[(t + kRing / 2) % kRing];
-                if (lane == 0) later.lost = later.odd = 0;
-                if (lane < 16) later.odd_keys[lane >> 1][lane & 1] = 0;
+                if (w8 == 0)  // not in use: the warps' and the readers' tiles lie less apart
+                    sh.info[(t + kRing / 2) % kRing].lost = 0;
             }
             if (!warp_wait_or_abort(smem_addr(sh.k_empty + stage), phase ^ 1u, &sh.abort, p.ctx) ||
                 !warp_wait_or_abort(smem_addr(sh.v_empty + stage), phase ^ 1u, &sh.abort, p.ctx))
@@ -566,7 +541,7 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
                 for (int u = 0; u < U; ++u) {
                     const int b = block + 4 * u;
                     float d = __half2float(__ushort_as_half(scales.of[half][u]));
-                    if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in info.odd: rows that do not see the key must not either
+                    if (half && !(fabsf(d) <= 65504.0f)) d = 0.0f;  // marked in sh.odd: rows that do not see the key must not either
                     d *= pow2i(-e[half]);
                     uint4 out[4];
                     if (near[half])
@@ -706,6 +681,67 @@ __device__ __forceinline__ void load8(const AttnArgs &a, int64_t at, bool wide, 
 __host__ __device__ constexpr int place_of(int d) {
     return ((d & 15) >> 2) * 8 + ((d & 1) << 2) + ((d >> 4) << 1) + ((d >> 1) & 1);
 }
+
+// A warp looks over the values of one block of V, for the keys of this CTA's
+// tiles: in which digits of the codes some value is not 0, and whether a key of
+// the lane's row (from lo up to hi) has one that is no number.  It is seldom
+// asked: where the dequantisers met such a number, and where an output that
+// lost weights might matter to is exactly 0.  `want`: digits in question, after
+// whose last the rest is left; or none, for all keys.
+template <int D>
+__device__ __noinline__ uint4 look_over(const TileParams &p, const Block &bk, int b, int lo, int hi, const uint4 &want, bool &odd) {
+    constexpr int kBatch = 8, NB = D / 32;
+    const int lane = threadIdx.x & 31, from = max(bk.lo, bk.key0), to = min(bk.hi, bk.key0 + bk.tiles * kKeys);
+    const int32_t *table = p.a.table + bk.b * p.a.table_width;
+    uint32_t live[4] = {};
+    int32_t page[kBatch];
+    auto load_pages = [&](int key0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int key = key0 + 32 * j + lane;
+            page[j] = key < to ? table[key >> p.page_shift] : -1;
+        }
+    };
+    load_pages(from);
+#pragma unroll 1
+    for (int key0 = from; key0 < to; key0 += 32 * kBatch) {
+        uint32_t bits[kBatch];
+        uint4 codes[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int key = key0 + 32 * j + lane;
+            bits[j] = 0;
+            codes[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (page[j] >= 0 && page[j] < p.num_pages) {
+                const int64_t row = (((page[j] * p.kv_heads) + bk.kv_head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+                bits[j] = reinterpret_cast<const uint16_t *>(p.v_scales)[row * NB + b] & 0x7FFFu;
+                codes[j] = reinterpret_cast<const uint4 *>(p.v_codes + row * (D / 2))[b];
+            }
+        }
+        load_pages(min(key0, to - 32 * kBatch) + 32 * kBatch);  // a batch ahead
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (bits[j]) {
+                live[0] |= codes[j].x ^ 0x88888888u, live[1] |= codes[j].y ^ 0x88888888u;
+                live[2] |= codes[j].z ^ 0x88888888u, live[3] |= codes[j].w ^ 0x88888888u;
+            }
+            for (unsigned keys = __ballot_sync(0xFFFFFFFFu, bits[j] >= 0x7C00u); keys; keys &= keys - 1u) {
+                const int key = key0 + 32 * j + __ffs(keys) - 1;
+                odd |= key >= lo && key < hi;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) live[k] = __reduce_or_sync(0xFFFFFFFFu, live[k]);
+        auto dead = [](uint32_t digits, uint32_t of) { return of & ~(digits | digits >> 1 | digits >> 2 | digits >> 3) & 0x11111111u; };
+        const bool any = want.x | want.y | want.z | want.w;
+        if (any && !(dead(live[0], want.x) | dead(live[1], want.y) | dead(live[2], want.z) | dead(live[3], want.w))) break;
+    }
+    return make_uint4(live[0], live[1], live[2], live[3]);
+}
+
+// Where value d of a block stands among the digits of its codes: word and shift.
+__host__ __device__ constexpr int digit_word(int d) { return (d & 15) >> 2; }
+__host__ __device__ constexpr int digit_shift(int d) { return (d & 3) * 8 + (d >> 4) * 4; }
 
 template <int D>
 __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh, uint32_t tmem, int warp, int lane) {
@@ -864,13 +900,6 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                     for (int i = 0; i < 64; ++i)
                         if (key0 + i < lo || key0 + i >= hi || ((lost >> (i >> 4)) & 1u)) s[i] = 0xFF800000u;
                 }
-                if (info.odd) {  // of the keys that the row sees
-                    auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
-                    const uint32_t seen0 = below(hi - key0) & ~below(lo - key0), seen1 = below(hi - key0 - 32) & ~below(lo - key0 - 32);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        if ((info.odd_keys[b][0] & seen0) | (info.odd_keys[b][1] & seen1)) odd |= 1u << b;
-                }
                 float here = ninf;
 #pragma unroll
                 for (int g = 0; g < 8; ++g) {
@@ -1009,10 +1038,22 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
         const float back = pow2i(e_ref - kRaise);  // of O's unit
         const float down = bk.slot >= 0 ? back : total == 0.0f ? 0.0f : back / total;
         const float raised = pow2i(-kPassRaise * pass);
-        // the row's smallest output that some value enters, in units of `down` (or,
-        // where outputs are added to, as it is)
+        if (sh.odd && pass == 0) {
+#pragma unroll 1
+            for (int b = 0; b < NB; ++b) {
+                bool here = false;
+                look_over<D>(p, sh.block, b, lo, hi, make_uint4(0u, 0u, 0u, 0u), here);
+                if (here) odd |= 1u << b;
+            }
+        }
+        // the row's smallest output, in units of `down` (or, where outputs are
+        // added to, as it is)
         float least = __uint_as_float(0x7F800000u);
-        const bool any_faint = __any_sync(0xFFFFFFFFu, faint > 0);
+        auto look_at = [&](const uint4 &live4, int d, float v) {  // of the outputs that some value enters
+            const int k = digit_word(d);
+            const uint32_t live = k == 0 ? live4.x : k == 1 ? live4.y : k == 2 ? live4.z : live4.w;
+            if (live & (15u << digit_shift(d))) least = fminf(least, fabsf(v));
+        };
         if (ok) {
             const int64_t out_row = static_cast<int64_t>(bk.q_row0) + token;
             const int64_t out_at = out_row * a.out_stride + static_cast<int64_t>(head) * D;
@@ -1029,20 +1070,15 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
                 const float unit_out = (odd >> b) & 1u ? __uint_as_float(0x7FFFFFFFu) : down;
-                const uint4 live4 = *reinterpret_cast<const uint4 *>(sh.live[b]);
-                auto look_at = [&](int d, float v) {
-                    const int k = (d & 15) >> 2;
-                    const uint32_t live = k == 0 ? live4.x : k == 1 ? live4.y : k == 2 ? live4.z : live4.w;
-                    if (live & (15u << ((d & 3) * 8 + (d >> 4) * 4))) least = fminf(least, fabsf(v));
-                };
                 if (__builtin_expect(pass > 0, 0)) {
                     // added to what this thread wrote before, and rounded once more
                     // (within what the row's scores leave uncertain)
                     if (!open) continue;
                     const float raised_out = raised * unit_out;
+                    const uint4 live4 = sh.live[warp][b];
                     auto add = [&](int d, float had) {
                         const float v = fmaf(__uint_as_float(o[place_of(d)]), raised_out, had);
-                        look_at(d, v);
+                        look_at(live4, d, v);
                         return v;
                     };
                     if (bk.slot >= 0) {
@@ -1071,10 +1107,8 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                     }
                     continue;
                 }
-                if (any_faint) {
 #pragma unroll
-                    for (int d = 0; d < 32; ++d) look_at(d, __uint_as_float(o[place_of(d)]));
-                }
+                for (int i = 0; i < 32; ++i) least = fminf(least, fabsf(__uint_as_float(o[i])));
                 if (!mine) continue;
                 if (bk.slot >= 0) {
 #pragma unroll
@@ -1108,6 +1142,31 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             }
         }
         open = open && ok && least < (pass == 0 ? error : error * raised * down);
+        if (__builtin_expect(pass == 0 && __any_sync(0xFFFFFFFFu, open), 0)) {
+            // outputs of exactly 0 in which every value is 0 do not count
+            least = __uint_as_float(0x7F800000u);
+#pragma unroll 1
+            for (int b = 0; b < NB; ++b) {
+                uint32_t o[32], zero[4] = {};
+                tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
+#pragma unroll
+                for (int d = 0; d < 32; ++d)
+                    if (__uint_as_float(o[place_of(d)]) == 0.0f) zero[digit_word(d)] |= 15u << digit_shift(d);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) zero[k] = __reduce_and_sync(0xFFFFFFFFu, open ? zero[k] : ~0u);  // in all such rows
+                uint4 live4 = make_uint4(~0u, ~0u, ~0u, ~0u);
+                if (zero[0] | zero[1] | zero[2] | zero[3]) {
+                    bool unused = false;
+                    const uint4 found = look_over<D>(p, sh.block, b, lo, hi, make_uint4(zero[0], zero[1], zero[2], zero[3]), unused);
+                    live4 = make_uint4(found.x | ~zero[0], found.y | ~zero[1], found.z | ~zero[2], found.w | ~zero[3]);
+                }
+#pragma unroll
+                for (int d = 0; d < 32; ++d) look_at(live4, d, __uint_as_float(o[place_of(d)]));
+                if (lane == 0) sh.live[warp][b] = live4;
+                __syncwarp();
+            }
+            open = open && least < error;
+        }
         if (__any_sync(0xFFFFFFFFu, open) && lane == 0) sh.again[pass] = 1;
         if (!another_pass<D>(sh, pass)) break;
     }
@@ -1139,7 +1198,7 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
     }
     for (int i = threadIdx.x; i < kRing; i += T::threads) sh.info[i] = TileInfo{};
     if (threadIdx.x < kPasses) sh.again[threadIdx.x] = 0;
-    if (threadIdx.x < 32) sh.live[threadIdx.x >> 2][threadIdx.x & 3] = 0;
+    if (threadIdx.x == 0) sh.odd = 0;
     pdl_wait();
     pdl_launch_dependents();
     find_block<D>(p, sh);
