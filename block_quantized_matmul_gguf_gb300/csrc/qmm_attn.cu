@@ -21,8 +21,8 @@
 // Precision.  fp32 output: q and p*d enter as two binary16 parts each (22
 // bits) in neighbouring columns, four query rows to 8 columns.  bf16
 // output: one part (11 bits), eight rows.  Both are scaled by powers of two
-// so that the largest lies below 2^15 (q per row, p*d per tile).  Weights
-// below 2^-24 of a tile's largest, which binary16 would lose, take a second
+// so that the largest lies below 2^15 (q per row, p*d per tile and block of 32
+// values).  Weights below 2^-24 of a tile's largest, which binary16 would lose, take a second
 // pass over the tile's values.  V's sums run over 64 keys in the tensor
 // core, then join the fp32 running output.
 //
@@ -37,11 +37,17 @@
 // a maximum, a sum and an unnormalised output per warp; a CTA joins what its
 // warps hold, and a second kernel joins what several CTAs hold.
 //
-// Bound by the instructions that turn codes into operands (57 % of the issue
-// slots, 51 % of DRAM's rate where it runs longest).  Measured, both kernels:
-// 128 requests of up to 8192 keys, 16 heads on 4 of 128, bf16, 88 us (329 MB,
-// 3.7 TB/s); fp32 outputs, 8 heads on 2 of 256: one request of 131071 keys
-// 41.6 us (75 MB), 16 of up to 4097 17 us, one of 301 13 us.
+// Bound, at head_dim 128 in bf16, by the instructions that turn codes into
+// operands and by their dependencies (56 % of the issue slots, 48 % of DRAM's
+// rate); at head_dim 256 in fp32 by latency: two warps an SM quarter issue in
+// 33 % of the slots and wait longest for instructions to be fetched.
+// Measured, both kernels: 128 requests of up to 8192 keys, 16 heads on 4 of
+// 128, bf16, 91.5 us (329 MB, 3.6 TB/s); fp32 outputs, 8 heads on 2 of 256: one
+// request of 131071 keys 40.7 us (75 MB), 16 of up to 4097 17.7 us, one of 301
+// 13 us.  Scores that spread by more than 23 powers of two within a tile take
+// further passes over its values: by their standard deviation 1.2, 2.4, 4 and
+// 8 the 128 requests (from a flushed L2) 101, 112, 138 and 178 us, the 131071
+// keys 59, 62, 68 and 87.
 #include "qmm_attn.cuh"
 
 #include <algorithm>

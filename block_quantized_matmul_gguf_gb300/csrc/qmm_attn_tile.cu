@@ -10,7 +10,7 @@
 // Warps by role:
 //   softmax   4 per 128 rows, a thread per row: stages Q, turns S into P,
 //             keeps maximum and sum, scales O when the maximum has grown by
-//             more than 2 (powers of two), writes the output
+//             more than kSlack powers of two, writes the output
 //   dequant   8: codes and scales from global memory (plain loads: an append
 //             may write them until pdl_wait), a tile ahead in registers, to
 //             binary16 rows of 64 values with the 128-byte swizzle; K is then a
@@ -43,8 +43,8 @@
 // (eight warps, two an SM quarter, that fill 64 KB of shared memory), its
 // softmax 1600, its products 1290 (48 cycles for 64 columns and 130 for 256,
 // as measured alone).  Measured: 2048 tokens of 8 heads of 256 (2 key heads)
-// behind 6000 cached ones 171 us, 690 TFLOP/s; seven prompts of up to 700
-// tokens of 16 heads of 128 with a window of 1024 keys 94 us; 128 tokens of
+// behind 6000 cached ones 176 us, 670 TFLOP/s; seven prompts of up to 700
+// tokens of 16 heads of 128 with a window of 1024 keys 92 us; 128 tokens of
 // the first layout behind 32000 75 us (777 with one CTA a block).
 #include "qmm_attn.cuh"
 #include "qmm_tc.cuh"

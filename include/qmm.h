@@ -357,7 +357,9 @@ qmm_status qmm_kv_plan(const int32_t *cached, const int32_t *added, int batch,
  * Per 32 values x: with e = max x if max x >= -min x, else min x, the scale
  * is d = binary16(e / -8), kept within +-65504, and the code of x is
  * round(x / d) (to nearest even) + 8, within 0..15, or 8 where d is 0.  A
- * block that holds a NaN or an infinity reads back as NaN.
+ * block that holds a NaN or an infinity reads back as NaN.  (GGUF's own
+ * quantizer divides by the scale before its rounding and rounds halves up, so
+ * that its codes may differ by one; the format is the same.)
  * Requires n >= 0 (0 launches nothing), n <= 2^30, strides at least
  * kv_heads * head_dim, k and v aligned to their type, slots to 8 bytes. */
 qmm_status qmm_kv_append_q4_0(const qmm_kv_q4_0 *cache, const void *k, int64_t k_stride,
@@ -399,11 +401,17 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_q4_0 *cache, const int64_t *slots, int6
  * of out and lse may be left as it was.
  * Arithmetic: scores, softmax statistics and sums in fp32.  With out_type
  * QMM_F32 the cached values are exact, and q and the softmax weights enter
- * the products in two binary16 parts (22 bits).  With QMM_BF16 q and the
- * weights enter in one (11 bits), below the rounding of the output; calls of
- * many rows (prompts) also round each cached value to binary16 once, which
- * the output does not show either but lse does (about 2e-6 of it).  Which
- * form a call takes depends on its host-side arguments alone, and equal
+ * the products in two binary16 parts (22 bits).  With QMM_BF16 they enter in
+ * one (11 bits; a bf16 q is exact), and calls of many rows (prompts) also
+ * round each cached value to binary16 once.  Rounding q or a key moves a score
+ * by up to 2^-11 of scale * sum |q k|, at random by far less; it grows with the
+ * scores.  Measured, beside bf16's own rounding of the output: a sixth of it
+ * where scores spread by 1 (standard deviation), a third where by 8 (half with
+ * an fp32 q), and lse off by up to 1e-4 and 5e-3 (1e-2).  A bf16 q in calls of
+ * few rows leaves neither.  In calls of many rows, blocks of values whose
+ * scales lie 2^16 below others of the same key lose bits.  Where lse has to be
+ * exact, take QMM_F32.  Which form a call takes depends on its host-side
+ * arguments alone, of which the table's width stands for the lengths; equal
  * calls give equal bits.
  * Requires heads a multiple of kv_heads, heads <= 1024, batch and max_q >= 1,
  * total_q >= 0 (0 launches nothing), window >= 0 and 0 unless causal, scale
