@@ -32,8 +32,8 @@
 // steps, with what was lost of the weights raised by 2^38, and adds the
 // products; four passes cover fp32's range.  Dimensions in which every value
 // is 0 do not count.  The case of 2048 tokens below by the scores' standard
-// deviation, from a flushed L2: 1.2 200 us, 2.4 409, 4 435, 8 451, 24 722; with
-// one block of values that are all 0 243, 493, 536, 549, 780.
+// deviation, from a flushed L2: 1.2 198 us, 2.4 410, 4 435, 8 448, 24 714; with
+// one block of values that are all 0 196, 427, 465, 482, 712.
 //
 // Parts are joined by a second kernel: their outputs and sums, in fp32, are
 // weighted by 2^(m - largest m), in the parts' order.
@@ -43,7 +43,7 @@
 // (eight warps, two an SM quarter, that fill 64 KB of shared memory), its
 // softmax 1600, its products 1290 (48 cycles for 64 columns and 130 for 256,
 // as measured alone).  Measured: 2048 tokens of 8 heads of 256 (2 key heads)
-// behind 6000 cached ones 176 us, 670 TFLOP/s; seven prompts of up to 700
+// behind 6000 cached ones 168 us, 700 TFLOP/s; seven prompts of up to 700
 // tokens of 16 heads of 128 with a window of 1024 keys 92 us; 128 tokens of
 // the first layout behind 32000 75 us (777 with one CTA a block).
 #include "qmm_attn.cuh"
@@ -137,7 +137,10 @@ struct TileShared {
     int abort;
     int again[kPasses];             // whether another pass follows this one
     int odd;                        // whether some value's scale is a NaN or an infinity
-    uint4 live[8][8];               // by softmax warp and block: digits of V's codes in which some value is not 0
+    int any_zero;                   // whether sh.zero has a digit
+    // by block, digits of V's codes: in which the outputs of a warp's rows are all
+    // 0 that might have lost something, and of those, in which some value is not
+    alignas(16) uint32_t zero[8][4], found[8][4];
 };
 
 struct TileParams {
@@ -687,11 +690,15 @@ __host__ __device__ constexpr int place_of(int d) {
 // the lane's row (from lo up to hi) has one that is no number.  It is seldom
 // asked: where the dequantisers met such a number, and where an output that
 // lost weights might matter to is exactly 0.  `want`: digits in question, after
-// whose last the rest is left; or none, for all keys.
+// whose last the rest is left; or none, for all keys.  The warp takes the keys'
+// `part`th of every `parts` batches.
 template <int D>
-__device__ __noinline__ uint4 look_over(const TileParams &p, const Block &bk, int b, int lo, int hi, const uint4 &want, bool &odd) {
+__device__ __noinline__ uint4 look_over(const TileParams &p, const Block &bk, int b, int lo, int hi, const uint4 &want, int part, int parts,
+                                        bool &odd) {
     constexpr int kBatch = 8, NB = D / 32;
-    const int lane = threadIdx.x & 31, from = max(bk.lo, bk.key0), to = min(bk.hi, bk.key0 + bk.tiles * kKeys);
+    const int step = 32 * kBatch * parts;
+    const int lane = threadIdx.x & 31, from = max(bk.lo, bk.key0) + 32 * kBatch * part;
+    const int to = min(bk.hi, bk.key0 + bk.tiles * kKeys);
     const int32_t *table = p.a.table + bk.b * p.a.table_width;
     uint32_t live[4] = {};
     int32_t page[kBatch];
@@ -704,7 +711,7 @@ __device__ __noinline__ uint4 look_over(const TileParams &p, const Block &bk, in
     };
     load_pages(from);
 #pragma unroll 1
-    for (int key0 = from; key0 < to; key0 += 32 * kBatch) {
+    for (int key0 = from; key0 < to; key0 += step) {
         uint32_t bits[kBatch];
         uint4 codes[kBatch];
 #pragma unroll
@@ -718,7 +725,7 @@ __device__ __noinline__ uint4 look_over(const TileParams &p, const Block &bk, in
                 codes[j] = reinterpret_cast<const uint4 *>(p.v_codes + row * (D / 2))[b];
             }
         }
-        load_pages(min(key0, to - 32 * kBatch) + 32 * kBatch);  // a batch ahead
+        load_pages(min(key0, to - step) + step);  // a batch ahead
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (bits[j]) {
@@ -737,6 +744,11 @@ __device__ __noinline__ uint4 look_over(const TileParams &p, const Block &bk, in
         if (any && !(dead(live[0], want.x) | dead(live[1], want.y) | dead(live[2], want.z) | dead(live[3], want.w))) break;
     }
     return make_uint4(live[0], live[1], live[2], live[3]);
+}
+
+template <int D>
+__device__ __forceinline__ void softmax_barrier() {
+    asm volatile("bar.sync 2, %0;" ::"n"(Tile<D>::softmax_warps * 32) : "memory");
 }
 
 // Where value d of a block stands among the digits of its codes: word and shift.
@@ -942,18 +954,20 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                 const float top_here = top == ninf ? 0.0f : top;
                 float base[8];
 #pragma unroll
-                for (int g = 0; g < 8; ++g) base[g] = static_cast<float>(kRaise + v_exp[g] - e_ref) - top_here;
+                for (int g = 0; g < 8; ++g)
+                    base[g] = static_cast<float>(kRaise + (later ? kPassRaise * (pass - 1) : 0) + v_exp[g] - e_ref) - top_here;
                 if constexpr (later) {
                     // What the pass before has lost of the weights.  z, a weight as
-                    // that pass had it, is a subnormal number there or 0; weights
-                    // that were so one pass earlier still leave nothing to it.
-                    const float up = pow2i(kPassRaise * (pass - 1)), raise = pow2i(kPassRaise);
+                    // that pass had it (within 2^-16 of it, far less than what this one
+                    // adds), is a subnormal number there or 0; weights that were so
+                    // one pass earlier still leave nothing to it.
+                    const float raise = pow2i(kPassRaise);
                     bool low = false;
                     if (edge) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i)
                             low |= s[i] != 0xFF800000u && fmaf(__uint_as_float(s[i]), u[i >> 3], base[i >> 3]) <
-                                                              static_cast<float>(-14 - kPassRaise * pass);
+                                                              static_cast<float>(-14 - kPassRaise);
                     }
                     float smallest = 1.0f;
 #pragma unroll
@@ -964,7 +978,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                             const int g = 4 * h + (i >> 2);
                             const float2 arg = __ffma2_rn(make_float2(__uint_as_float(s[32 * h + 2 * i]), __uint_as_float(s[32 * h + 2 * i + 1])),
                                                           make_float2(u[g], u[g]), make_float2(base[g], base[g]));
-                            const float2 z = __fmul2_rn(make_float2(exp2_fast(arg.x), exp2_fast(arg.y)), make_float2(up, up));
+                            const float2 z = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
                             const uint32_t had = pack_rn(z.x, z.y);
                             const float2 lost = __fadd2_rn(z, make_float2(-low_float(had), -high_float(had)));
                             const float2 y = __fmul2_rn(lost, make_float2(raise, raise));
@@ -1042,13 +1056,17 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
 #pragma unroll 1
             for (int b = 0; b < NB; ++b) {
                 bool here = false;
-                look_over<D>(p, sh.block, b, lo, hi, make_uint4(0u, 0u, 0u, 0u), here);
+                look_over<D>(p, sh.block, b, lo, hi, make_uint4(0u, 0u, 0u, 0u), 0, 1, here);
                 if (here) odd |= 1u << b;
             }
         }
         // the row's smallest output, in units of `down` (or, where outputs are
         // added to, as it is)
         float least = __uint_as_float(0x7F800000u);
+        auto live_of = [&](int b) {
+            const uint4 z = *reinterpret_cast<const uint4 *>(sh.zero[b]), f = *reinterpret_cast<const uint4 *>(sh.found[b]);
+            return make_uint4(f.x | ~z.x, f.y | ~z.y, f.z | ~z.z, f.w | ~z.w);
+        };
         auto look_at = [&](const uint4 &live4, int d, float v) {  // of the outputs that some value enters
             const int k = digit_word(d);
             const uint32_t live = k == 0 ? live4.x : k == 1 ? live4.y : k == 2 ? live4.z : live4.w;
@@ -1075,7 +1093,7 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
                     // (within what the row's scores leave uncertain)
                     if (!open) continue;
                     const float raised_out = raised * unit_out;
-                    const uint4 live4 = sh.live[warp][b];
+                    const uint4 live4 = live_of(b);
                     auto add = [&](int d, float had) {
                         const float v = fmaf(__uint_as_float(o[place_of(d)]), raised_out, had);
                         look_at(live4, d, v);
@@ -1142,30 +1160,50 @@ __device__ __forceinline__ void softmax_role(const TileParams &p, TileShared &sh
             }
         }
         open = open && ok && least < (pass == 0 ? error : error * raised * down);
-        if (__builtin_expect(pass == 0 && __any_sync(0xFFFFFFFFu, open), 0)) {
-            // outputs of exactly 0 in which every value is 0 do not count
-            least = __uint_as_float(0x7F800000u);
+        if (pass == 0) {  // outputs of exactly 0 in which every value is 0 do not count
+            const bool any_open = __any_sync(0xFFFFFFFFu, open);
+            if (any_open) {
 #pragma unroll 1
-            for (int b = 0; b < NB; ++b) {
-                uint32_t o[32], zero[4] = {};
-                tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
+                for (int b = 0; b < NB; ++b) {
+                    uint32_t o[32], zero[4] = {};
+                    tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
 #pragma unroll
-                for (int d = 0; d < 32; ++d)
-                    if (__uint_as_float(o[place_of(d)]) == 0.0f) zero[digit_word(d)] |= 15u << digit_shift(d);
+                    for (int d = 0; d < 32; ++d)
+                        if (__uint_as_float(o[place_of(d)]) == 0.0f) zero[digit_word(d)] |= 15u << digit_shift(d);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) zero[k] = __reduce_and_sync(0xFFFFFFFFu, open ? zero[k] : ~0u);  // in all such rows
-                uint4 live4 = make_uint4(~0u, ~0u, ~0u, ~0u);
-                if (zero[0] | zero[1] | zero[2] | zero[3]) {
-                    bool unused = false;
-                    const uint4 found = look_over<D>(p, sh.block, b, lo, hi, make_uint4(zero[0], zero[1], zero[2], zero[3]), unused);
-                    live4 = make_uint4(found.x | ~zero[0], found.y | ~zero[1], found.z | ~zero[2], found.w | ~zero[3]);
+                    for (int k = 0; k < 4; ++k) {
+                        zero[k] = __reduce_and_sync(0xFFFFFFFFu, open ? zero[k] : ~0u);  // in all such rows
+                        if (lane == 0 && zero[k]) {
+                            atomicOr(&sh.zero[b][k], zero[k]);
+                            sh.any_zero = 1;
+                        }
+                    }
                 }
-#pragma unroll
-                for (int d = 0; d < 32; ++d) look_at(live4, d, __uint_as_float(o[place_of(d)]));
-                if (lane == 0) sh.live[warp][b] = live4;
-                __syncwarp();
             }
-            open = open && least < error;
+            softmax_barrier<D>();
+            if (sh.any_zero) {
+#pragma unroll 1
+                for (int b = 0; b < NB; ++b) {
+                    const uint4 want = *reinterpret_cast<const uint4 *>(sh.zero[b]);
+                    if (!(want.x | want.y | want.z | want.w)) continue;
+                    bool unused = false;
+                    const uint4 f = look_over<D>(p, sh.block, b, lo, hi, want, warp, T::softmax_warps, unused);
+                    if (lane < 4) atomicOr(&sh.found[b][lane], lane == 0 ? f.x : lane == 1 ? f.y : lane == 2 ? f.z : f.w);
+                }
+                softmax_barrier<D>();
+                if (any_open) {
+                    least = __uint_as_float(0x7F800000u);
+#pragma unroll 1
+                    for (int b = 0; b < NB; ++b) {
+                        uint32_t o[32];
+                        tmem_ld_32cols(tmem + lanes + T::o_col + qt * D + b * 32, o);
+                        const uint4 live4 = live_of(b);
+#pragma unroll
+                        for (int d = 0; d < 32; ++d) look_at(live4, d, __uint_as_float(o[place_of(d)]));
+                    }
+                    open = open && least < error;
+                }
+            }
         }
         if (__any_sync(0xFFFFFFFFu, open) && lane == 0) sh.again[pass] = 1;
         if (!another_pass<D>(sh, pass)) break;
@@ -1198,7 +1236,8 @@ __global__ void __launch_bounds__(Tile<D>::threads, 1) attn_tile_kernel(const __
     }
     for (int i = threadIdx.x; i < kRing; i += T::threads) sh.info[i] = TileInfo{};
     if (threadIdx.x < kPasses) sh.again[threadIdx.x] = 0;
-    if (threadIdx.x == 0) sh.odd = 0;
+    if (threadIdx.x == 0) sh.odd = sh.any_zero = 0;
+    if (threadIdx.x < 32) sh.zero[threadIdx.x >> 2][threadIdx.x & 3] = sh.found[threadIdx.x >> 2][threadIdx.x & 3] = 0;
     pdl_wait();
     pdl_launch_dependents();
     find_block<D>(p, sh);
