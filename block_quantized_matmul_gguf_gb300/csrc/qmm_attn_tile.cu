@@ -447,7 +447,7 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
     auto page_of = [&](int t) -> int32_t {
         const int k = bk.key0 + t * kKeys + key;
         if (t >= bk.tiles || k < bk.lo || k >= bk.hi) return -2;  // no key
-        return table[k >> p.page_shift];
+        return max(table[k >> p.page_shift], -1);
     };
     auto load_scales = [&](int t, int32_t page, Scales<D> &h) {
         const int k = bk.key0 + t * kKeys + key;

@@ -258,3 +258,20 @@ def test_bf16_queries_enter_the_streaming_form_exactly(qmm, dim, spread, new, wi
     limit = share * (2 * big[..., None] * 2.0 ** -15 + 2.0 ** -10) + 2.0 ** -8 * np.abs(want) + 1e-30
     assert (np.abs(out.double().cpu().numpy() - want) <= limit).all()
     assert (np.abs(lse.cpu().numpy() - want_lse) <= big * 2.0 ** -15 + 2.0 ** -18 * (1 + np.abs(want_lse))).all()
+
+
+@pytest.mark.parametrize("form,out_type", FORMS)
+@pytest.mark.parametrize("first", [100, 1800])
+def test_every_negative_page_is_a_missing_one(qmm, form, out_type, first):
+    """-2 as well as -1: the keys are left out and recorded."""
+    c = form(qmm, [first, 100], [100, 100], 8, 2, 64, 16, seed=10)
+    outs = []
+    for page in (-1, -2, -3, -(2 ** 31)):
+        t = c.dev["table"].clone()
+        t[0, 1] = page
+        out, lse = torch.empty(c.q.shape, dtype=out_type).cuda(), torch.empty(c.q.shape[:2]).cuda()
+        qmm.qmm_attn_q4_0(c.cache, c.q.cuda(), out, t, c.dev["q_start"], c.dev["kv_len"], 100, c.scale, lse=lse)
+        assert qmm.qmm_get_device_error() == qmm.QMM_ERR_INDEX, page
+        outs.append((out, lse))
+    for out, lse in outs[1:]:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
