@@ -444,15 +444,16 @@ __device__ __forceinline__ void dequant_role(const TileParams &p, TileShared &sh
     const int block = D == 64 ? lane >> 4 : lane >> 3;
     const int half0 = D == 64 ? w8 >> 2 : 0, half1 = D == 64 ? half0 + 1 : 2;
     const int32_t *table = p.a.table + bk.b * p.a.table_width;
+    // the page is not looked at before it is needed, which would wait for the load
     auto page_of = [&](int t) -> int32_t {
         const int k = bk.key0 + t * kKeys + key;
-        if (t >= bk.tiles || k < bk.lo || k >= bk.hi) return -2;  // no key
-        return max(table[k >> p.page_shift], -1);
+        if (t >= bk.tiles || k < bk.lo || k >= bk.hi) return -1;  // no key
+        return table[k >> p.page_shift];
     };
     auto load_scales = [&](int t, int32_t page, Scales<D> &h) {
         const int k = bk.key0 + t * kKeys + key;
         h.there = page >= 0 && page < p.num_pages;
-        h.lost = !h.there && page != -2;
+        h.lost = !h.there && t < bk.tiles && k >= bk.lo && k < bk.hi;
         h.row = h.there ? (((page * p.kv_heads) + bk.kv_head) << p.page_shift) + (k & ((1 << p.page_shift) - 1)) : 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half)
