@@ -555,6 +555,45 @@ qmm_status qmm_kv_append_q4_0(const qmm_kv_q4_0 *cache, const void *k, int64_t k
                                       reinterpret_cast<cudaStream_t>(stream), ctx));
 }
 
+qmm_status qmm_kv_append_rope_q4_0(const qmm_kv_q4_0 *cache, const qmm_rope_args *args, qmm_stream_t stream) {
+    KvCache c;
+    const qmm_status s = check_cache(cache, &c);
+    if (s != QMM_OK) return s;
+    if (!args) return QMM_ERR_NULL;
+    const qmm_rope_args &a = *args;
+    if (a.n < 0 || !valid_dtype(a.type) || a.rot < 2 || a.rot % 2 != 0 || a.rot > c.head_dim || a.table_rows < 1)
+        return QMM_ERR_SHAPE;
+    if (a.n == 0) return QMM_OK;
+    if (!a.k || !a.v || !a.slots || !a.positions || !a.table || (a.q && !a.q_out)) return QMM_ERR_NULL;
+    const int64_t width = static_cast<int64_t>(c.kv_heads) * c.head_dim;
+    const int64_t q_width = a.q ? static_cast<int64_t>(a.heads) * c.head_dim : 0;
+    if (a.k_stride < width || a.v_stride < width) return QMM_ERR_SHAPE;
+    if (a.q && (a.heads < 1 || a.q_stride < q_width || a.q_out_stride < q_width)) return QMM_ERR_SHAPE;
+    if (a.n > kMaxRows || a.k_stride > kMaxIndex || a.v_stride > kMaxIndex || a.table_rows > kMaxIndex ||
+        (a.q && (a.heads > 1024 || a.q_stride > kMaxIndex || a.q_out_stride > kMaxIndex)))
+        return QMM_ERR_UNSUPPORTED;
+    const size_t size = dtype_bytes(a.type);
+    if (!aligned(a.k, size) || !aligned(a.v, size) || !aligned(a.slots, 8) || !aligned(a.positions, 4) ||
+        !aligned(a.table, 4) || (a.q && (!aligned(a.q, size) || !aligned(a.q_out, size))))
+        return QMM_ERR_ALIGN;
+    const Range ins[] = {{a.q, rows_bytes(a.n, a.q_stride, q_width, size)},
+                         {a.k, rows_bytes(a.n, a.k_stride, width, size)},
+                         {a.v, rows_bytes(a.n, a.v_stride, width, size)},
+                         {a.slots, 8 * static_cast<size_t>(a.n)}, {a.positions, 4 * static_cast<size_t>(a.n)},
+                         {a.table, 4 * static_cast<size_t>(a.table_rows) * a.rot}};
+    const Range out = {a.q ? a.q_out : nullptr, rows_bytes(a.n, a.q_out_stride, q_width, size)};
+    if (!outputs_clear(&out, 1, ins, 6)) return QMM_ERR_UNSUPPORTED;
+    for (const Range &r : ins)
+        if (r.p && r.bytes && overlaps_cache(c, r.p, r.bytes)) return QMM_ERR_UNSUPPORTED;
+    if (out.p && overlaps_cache(c, out.p, out.bytes)) return QMM_ERR_UNSUPPORTED;
+    LaunchCtx ctx;
+    if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
+    const RopeArgs r = {a.q, a.k, a.v, a.q ? a.q_out : nullptr, a.table, a.positions, a.slots, a.q ? a.q_stride : 0,
+                        a.q ? a.q_out_stride : 0, a.k_stride, a.v_stride, a.table_rows, a.n, a.q ? a.heads : 0, a.rot,
+                        a.interleaved != 0, a.type == QMM_BF16};
+    return from_cuda(launch_kv_append_rope(c, r, reinterpret_cast<cudaStream_t>(stream), ctx));
+}
+
 qmm_status qmm_kv_read_q4_0(const qmm_kv_q4_0 *cache, const int64_t *slots, int64_t n, float *k_out,
                             float *v_out, qmm_stream_t stream) {
     KvCache c;
@@ -625,6 +664,48 @@ qmm_status qmm_attn_q4_0(const qmm_kv_q4_0 *cache, const qmm_attn_args *args, qm
     return from_cuda(launch_attn(c, k, reinterpret_cast<cudaStream_t>(stream), ctx));
 }
 
+size_t qmm_route_workspace_bytes(int64_t tokens, int experts) {
+    if (tokens < 1 || experts < 1 || tokens > kMaxRows || experts > kMaxExperts) return 0;
+    return route_workspace_bytes(tokens, experts);
+}
+
+qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream) {
+    if (!args) return QMM_ERR_NULL;
+    const qmm_route_args &a = *args;
+    if (a.tokens < 0 || a.experts < 1 || a.topk < 1 || a.groups < 1 || a.group_topk < 1 || a.group_topk > a.groups ||
+        (a.group_best != 1 && a.group_best != 2) || !valid_dtype(a.type) || !(a.scale - a.scale == 0.0f) ||
+        (a.score != QMM_SCORE_SOFTMAX && a.score != QMM_SCORE_SIGMOID))
+        return QMM_ERR_SHAPE;
+    if (a.experts % a.groups != 0 || a.topk > a.experts / a.groups * a.group_topk || a.logits_stride < a.experts)
+        return QMM_ERR_SHAPE;
+    if (a.experts > kMaxExperts || a.topk > kMaxTopk || a.groups > kMaxGroups || a.tokens > kMaxRows / a.topk ||
+        a.logits_stride > kMaxIndex)
+        return QMM_ERR_UNSUPPORTED;
+    if (a.tokens == 0) return QMM_OK;
+    if (!a.logits || !a.ids || !a.weights || !a.expert_start || !a.pairs) return QMM_ERR_NULL;
+    if (!aligned(a.logits, dtype_bytes(a.type)) || !aligned(a.bias, 4) || !aligned(a.count, 4) || !aligned(a.ids, 4) ||
+        !aligned(a.weights, 4) || !aligned(a.expert_start, 4) || !aligned(a.pairs, 4))
+        return QMM_ERR_ALIGN;
+    const size_t need = route_workspace_bytes(a.tokens, a.experts);
+    if (need) {
+        if (!a.workspace) return QMM_ERR_NULL;
+        const qmm_status s = check_workspace(a.workspace, a.workspace_bytes, need);
+        if (s != QMM_OK) return s;
+    }
+    const size_t e = static_cast<size_t>(a.experts), list = 4 * static_cast<size_t>(a.tokens) * a.topk;
+    const Range ins[] = {{a.logits, rows_bytes(a.tokens, a.logits_stride, a.experts, dtype_bytes(a.type))},
+                         {a.bias, 4 * e}, {a.count, 4}};
+    const Range outs[] = {{a.ids, list}, {a.weights, list}, {a.expert_start, 4 * (e + 1)}, {a.pairs, list},
+                          {a.workspace, need}};
+    if (!outputs_clear(outs, 5, ins, 3)) return QMM_ERR_UNSUPPORTED;
+    LaunchCtx ctx;
+    if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
+    const RouteArgs r = {a.logits, a.bias, a.count, a.ids, a.weights, a.expert_start, a.pairs, a.workspace,
+                         a.logits_stride, a.tokens, a.experts, a.topk, a.groups, a.group_topk, a.group_best,
+                         static_cast<int>(a.score), a.scale, a.type == QMM_BF16, a.renormalize != 0};
+    return from_cuda(launch_route(r, reinterpret_cast<cudaStream_t>(stream), ctx));
+}
+
 qmm_status qmm_logits_adjust(const qmm_logits_args *args, qmm_stream_t stream) {
     if (!args) return QMM_ERR_NULL;
     const qmm_logits_args &a = *args;
@@ -681,7 +762,7 @@ const char *qmm_status_string(qmm_status status) {
     return "unknown status";
 }
 
-int qmm_version(void) { return 500; }  // 0.5.0: Q4_0 cache, attention and logits added
+int qmm_version(void) { return 600; }  // 0.6.0: rotation, routing and experts' products added
 
 qmm_status qmm_get_device_error(qmm_stream_t stream) {
     cudaError_t e;

@@ -283,6 +283,42 @@ struct LogitsArgs {
 
 cudaError_t launch_logits_adjust(const LogitsArgs &args, cudaStream_t stream, const LaunchCtx &ctx);
 
+// Keys rotated by their positions and appended with the values, queries rotated.
+struct RopeArgs {
+    const void *q, *k, *v;
+    void *q_out;
+    const float *table;  // [table_rows][rot]: cosines, then sines
+    const int32_t *positions;
+    const int64_t *slots;
+    int64_t q_stride, q_out_stride, k_stride, v_stride, table_rows, n;
+    int heads, rot;  // heads 0: no queries
+    bool interleaved, bf16;
+};
+
+cudaError_t launch_kv_append_rope(const KvCache &cache, const RopeArgs &args, cudaStream_t stream,
+                                  const LaunchCtx &ctx);
+
+// ---- mixture of experts ---------------------------------------------------------
+
+struct RouteArgs {
+    const void *logits;
+    const float *bias;
+    const int32_t *count;
+    int32_t *ids;
+    float *weights;
+    int32_t *expert_start, *pairs;
+    void *workspace;
+    int64_t logits_stride, tokens;
+    int experts, topk, groups, group_topk, group_best;
+    int score;  // 0 softmax, 1 sigmoid
+    float scale;
+    bool bf16, renormalize;
+};
+constexpr int kMaxExperts = 1024, kMaxTopk = 32, kMaxGroups = 32;
+
+size_t route_workspace_bytes(int64_t tokens, int experts);
+cudaError_t launch_route(const RouteArgs &args, cudaStream_t stream, const LaunchCtx &ctx);
+
 cudaError_t launch_selftest_wait(cudaStream_t stream, const LaunchCtx &ctx);
 
 }  // namespace qmm

@@ -3,6 +3,7 @@
 // reading it back (read).  Layout and formulas: include/qmm.h.
 #include "qmm_internal.h"
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -181,7 +182,7 @@ __device__ __forceinline__ int64_t cache_row(const KvView &c, int64_t slot, int 
 // GPU, else 1.  8191 tokens of 2 x 256 fp32, append and read: 20 us (79 MB,
 // 3.9 TB/s; 27 with 1 and 1, 25 with 4 and 4, 21.4 where the registers allow
 // only 4 and 3 CTAs an SM); 16 tokens: 3.6 us, 5.7 with several.
-constexpr int kAppendMany = 2, kReadMany = 4;
+constexpr int kAppendMany = 2, kReadMany = 4, kRopeMany = 2;
 
 struct Spread {
     int per, par, sub, at;
@@ -197,6 +198,9 @@ struct Spread {
         }
     }
 };
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 
 template <bool kWide>
 __device__ __forceinline__ void load_eight(const float *p, float (&x)[8]) {
@@ -252,6 +256,37 @@ __device__ __forceinline__ void codes_of(const float (&x)[8], float d, uint32_t 
     }
 }
 
+// Four lanes' eights x as one block of 32 values, where it is wanted: its 16
+// bytes of codes and its scale.  All of a warp's threads come here.
+__device__ __forceinline__ void append_eight(const float (&x)[8], bool write, uint8_t *codes, __half *scale) {
+    const int lane4 = threadIdx.x & 3;
+    float top = x[0], low = x[0], odd = 0.0f * x[0];  // 0 x is NaN for what a block cannot hold
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+        top = fmaxf(top, x[j]);
+        low = fminf(low, x[j]);
+        odd = fmaf(0.0f, x[j], odd);
+    }
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
+        odd += __shfl_xor_sync(0xFFFFFFFFu, odd, o);
+    }
+    const float e = top >= -low ? top : low;
+    const __half dh = __float2half_rn(fminf(fmaxf(e * -0.125f, -65504.0f), 65504.0f));
+    const float d = __half2float(dh);
+    uint32_t q[2] = {0x08080808u, 0x08080808u};
+    const bool finite = odd == 0.0f;
+    if (finite && d != 0.0f) codes_of(x, d, q);
+    const uint32_t high0 = __shfl_down_sync(0xFFFFFFFFu, q[0], 2, 4);
+    const uint32_t high1 = __shfl_down_sync(0xFFFFFFFFu, q[1], 2, 4);
+    if (!write) return;
+    if (lane4 < 2)
+        *reinterpret_cast<uint2 *>(codes + lane4 * 8) = make_uint2(q[0] | (high0 << 4), q[1] | (high1 << 4));
+    if (lane4 == 0) *scale = finite ? dh : __ushort_as_half(static_cast<unsigned short>(0x7FFF));
+}
+
 // kWide: rows of eight values are aligned to 16 bytes.  No pointer is
 // __restrict__, here and in read: the compiler would take what they point to
 // as constant for the kernel's lifetime, which begins before pdl_wait, while
@@ -290,38 +325,13 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(KvView c, const T *
                 for (int j = 0; j < 8; ++j) x[u][j] = 0.0f;
                 if (here && slot[u] >= 0) load_eight<kWide>(src + (base + sp.sub + u * sp.par) * stride, x[u]);
             }
-            const int head = at / dim, in = at - head * dim, lane4 = threadIdx.x & 3;
+            const int head = at / dim, in = at - head * dim;
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                float top = x[u][0], low = x[u][0], odd = 0.0f * x[u][0];  // 0 x is NaN for what a block cannot hold
-#pragma unroll
-                for (int j = 1; j < 8; ++j) {
-                    top = fmaxf(top, x[u][j]);
-                    low = fminf(low, x[u][j]);
-                    odd = fmaf(0.0f, x[u][j], odd);
-                }
-#pragma unroll
-                for (int o = 2; o > 0; o >>= 1) {
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                    low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
-                    odd += __shfl_xor_sync(0xFFFFFFFFu, odd, o);
-                }
-                const float e = top >= -low ? top : low;
-                const __half dh = __float2half_rn(fminf(fmaxf(e * -0.125f, -65504.0f), 65504.0f));
-                const float d = __half2float(dh);
-                uint32_t q[2] = {0x08080808u, 0x08080808u};
-                const bool finite = odd == 0.0f;
-                if (finite && d != 0.0f) codes_of(x[u], d, q);
-                const uint32_t high0 = __shfl_down_sync(0xFFFFFFFFu, q[0], 2, 4);
-                const uint32_t high1 = __shfl_down_sync(0xFFFFFFFFu, q[1], 2, 4);
-                if (!here || slot[u] < 0) continue;
-                const int64_t row = cache_row(c, slot[u], head);
-                if (lane4 < 2)
-                    *reinterpret_cast<uint2 *>((half ? c.v_codes : c.k_codes) + row * (dim / 2) + (in / kQK) * 16 + lane4 * 8) =
-                        make_uint2(q[0] | (high0 << 4), q[1] | (high1 << 4));
-                if (lane4 == 0)
-                    (half ? c.v_scales : c.k_scales)[row * (dim / kQK) + in / kQK] =
-                        finite ? dh : __ushort_as_half(static_cast<unsigned short>(0x7FFF));
+                const bool write = here && slot[u] >= 0;
+                const int64_t row = write ? cache_row(c, slot[u], head) : 0;
+                append_eight(x[u], write, (half ? c.v_codes : c.k_codes) + row * (dim / 2) + (in / kQK) * 16,
+                             (half ? c.v_scales : c.k_scales) + row * (dim / kQK) + in / kQK);
             }
         }
     }
@@ -403,6 +413,149 @@ __global__ void __launch_bounds__(kThreads, 5) read_kernel(KvView c, const int64
     }
 }
 
+// ---- append with the rotation -------------------------------------------------
+// (a, b) -> (a c - b s, a s + b c) for the pairs (i, i + rot/2) or (2i, 2i + 1)
+// of a head's first rot values, c and s from the position's row of a table.
+// Each product and each sum is rounded once to fp32 (no contraction), so that
+// the codes of a rotated key are defined to the bit; a table made in 64 bits
+// leaves far positions as exact as near ones.  A thread takes eight values as
+// append does; with pairs rot/2 apart it also loads the eight that they pair
+// with, which another thread of the CTA loads too (they come from L1).  Bound
+// by the bytes of the inputs and of the queries out.
+struct RopeView {
+    const float *table;
+    const int32_t *positions;
+    int64_t rows;
+    int rot, half;  // half = rot / 2
+    bool interleaved;
+};
+
+// The eight values at `in` of a head at `src`, rotated by row `turn`.
+template <typename T, bool kWide>
+__device__ __forceinline__ void load_rotated(const T *src, int in, const float *turn, const RopeView &r, float (&x)[8]) {
+    load_eight<kWide>(src + in, x);
+    if (in >= r.rot) return;
+    if constexpr (kWide) {  // rot (interleaved) or rot / 2 is a multiple of 8
+        if (r.interleaved) {
+            const float4 c4 = *reinterpret_cast<const float4 *>(turn + in / 2);
+            const float4 s4 = *reinterpret_cast<const float4 *>(turn + r.half + in / 2);
+            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i], b = x[2 * i + 1];
+                x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(a, s[i]), __fmul_rn(b, c[i]));
+            }
+        } else {
+            const bool second = in >= r.half;
+            const int at = second ? in - r.half : in;
+            float y[8];
+            alignas(16) float c[8], s[8];
+            load_eight<kWide>(src + (second ? at : at + r.half), y);
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {  // rows of the table serve all heads: they stay in L1
+                *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(turn + at + i);
+                *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(turn + r.half + at + i);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = second ? __fadd_rn(__fmul_rn(y[i], s[i]), __fmul_rn(x[i], c[i]))
+                              : __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i], s[i]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = in + i;
+            if (at >= r.rot) break;
+            const bool second = r.interleaved ? at & 1 : at >= r.half;
+            const int pair = r.interleaved ? at >> 1 : second ? at - r.half : at;
+            const int other = r.interleaved ? at ^ 1 : second ? pair : pair + r.half;
+            const float own = x[i], y = to_float(src[other]), c = turn[pair], s = turn[r.half + pair];
+            x[i] = second ? __fadd_rn(__fmul_rn(y, s), __fmul_rn(own, c)) : __fsub_rn(__fmul_rn(own, c), __fmul_rn(y, s));
+        }
+    }
+}
+
+template <bool kWide>
+__device__ __forceinline__ void store_eight(float *p, const float (&x)[8]) {
+    store_quad<kWide>(p, make_float4(x[0], x[1], x[2], x[3]));
+    store_quad<kWide>(p + 4, make_float4(x[4], x[5], x[6], x[7]));
+}
+template <bool kWide>
+__device__ __forceinline__ void store_eight(uint16_t *p, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    if constexpr (kWide) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+template <typename T, bool kWide, int kAhead>
+__global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(KvView c, RopeView r, const T *q, int64_t q_stride, T *q_out,
+                                                                  int64_t q_out_stride, int heads, const T *k, int64_t k_stride,
+                                                                  const T *v, int64_t v_stride, const int64_t *slots,
+                                                                  int64_t n, int dim, LaunchCtx ctx) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int q_eights = heads * dim / 8, eights = c.kv_heads * dim / 8;
+    const Spread sp(q_eights + 2 * eights);
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * sp.par * kAhead; base < n;
+         base += static_cast<int64_t>(gridDim.x) * sp.par * kAhead) {
+        int64_t slot[kAhead], turn[kAhead];  // -1: the token has none
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t token = base + sp.sub + u * sp.par;
+            const bool there = token < n && sp.at < sp.per;
+            slot[u] = there ? slots[token] : -1;
+            turn[u] = there ? r.positions[token] : -1;
+            if (slot[u] < -1 || slot[u] >= c.slots || turn[u] < -1 || turn[u] >= r.rows) {
+                record_error(ctx, kDevErrIndex);
+                turn[u] = -1;
+            }
+            if (turn[u] < 0) slot[u] = -1;
+        }
+        for (int i0 = 0; i0 < sp.per; i0 += kThreads) {
+            const int i = i0 + sp.at;
+            const bool here = i < sp.per;
+            const int part = i < q_eights ? 0 : i < q_eights + eights ? 1 : 2;  // query, key, value
+            const int at = (i - (part == 0 ? 0 : part == 1 ? q_eights : q_eights + eights)) * 8;
+            const int head = at / dim, in = at - head * dim;
+            float x[kAhead][8];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int64_t token = base + sp.sub + u * sp.par;
+                const float *row = r.table + turn[u] * r.rot;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[u][j] = 0.0f;
+                if (here && part == 0 && turn[u] >= 0)
+                    load_rotated<T, kWide>(q + token * q_stride + at - in, in, row, r, x[u]);
+                else if (here && part == 1 && slot[u] >= 0)
+                    load_rotated<T, kWide>(k + token * k_stride + at - in, in, row, r, x[u]);
+                else if (here && part == 2 && slot[u] >= 0)
+                    load_eight<kWide>(v + token * v_stride + at, x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (here && part == 0 && turn[u] >= 0)
+                    store_eight<kWide>(q_out + (base + sp.sub + u * sp.par) * q_out_stride + at, x[u]);
+                const bool write = here && part > 0 && slot[u] >= 0;
+                if (__any_sync(0xFFFFFFFFu, write)) {
+                    const int64_t to = write ? cache_row(c, slot[u], head) : 0;
+                    append_eight(x[u], write, (part == 2 ? c.v_codes : c.k_codes) + to * (dim / 2) + (in / kQK) * 16,
+                                 (part == 2 ? c.v_scales : c.k_scales) + to * (dim / kQK) + in / kQK);
+                }
+            }
+        }
+    }
+}
+
 KvView view(const KvCache &c) {
     KvView v;
     v.k_codes = static_cast<uint8_t *>(c.k_codes);
@@ -442,6 +595,26 @@ cudaError_t launch_append(const KvCache &c, const void *k, int64_t k_stride, con
                          c.head_dim, ctx);
 }
 
+template <typename T>
+cudaError_t launch_rope(const KvCache &c, const RopeArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    constexpr int64_t values = 16 / sizeof(T);
+    const uintptr_t pointers = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                               reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.q_out) |
+                               reinterpret_cast<uintptr_t>(a.table);
+    const bool wide = pointers % 16 == 0 && a.k_stride % values == 0 && a.v_stride % values == 0 &&
+                      (a.heads == 0 || (a.q_stride % values == 0 && a.q_out_stride % values == 0)) &&
+                      a.rot % (a.interleaved ? 8 : 16) == 0;
+    const int parts = (a.heads + 2 * c.kv_heads) * c.head_dim / 8;
+    const bool more = many(a.n, parts, kRopeMany);
+    auto *kernel = wide ? (more ? append_rope_kernel<T, true, kRopeMany> : append_rope_kernel<T, true, 1>)
+                        : (more ? append_rope_kernel<T, false, kRopeMany> : append_rope_kernel<T, false, 1>);
+    const RopeView r = {a.table, a.positions, a.table_rows, a.rot, a.rot / 2, a.interleaved};
+    return launch_kernel(kernel, dim3(grid_for(a.n, parts, more ? kRopeMany : 1)), dim3(kThreads), 0, stream, 1, view(c), r,
+                         static_cast<const T *>(a.q), a.q_stride, static_cast<T *>(a.q_out), a.q_out_stride, a.heads,
+                         static_cast<const T *>(a.k), a.k_stride, static_cast<const T *>(a.v), a.v_stride, a.slots, a.n,
+                         c.head_dim, ctx);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlan &a, cudaStream_t stream, const LaunchCtx &ctx) {
@@ -466,6 +639,10 @@ cudaError_t launch_kv_append(const KvCache &c, const void *k, int64_t k_stride, 
                              cudaStream_t stream, const LaunchCtx &ctx) {
     return bf16 ? launch_append<uint16_t>(c, k, k_stride, v, v_stride, slots, n, stream, ctx)
                 : launch_append<float>(c, k, k_stride, v, v_stride, slots, n, stream, ctx);
+}
+
+cudaError_t launch_kv_append_rope(const KvCache &c, const RopeArgs &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    return a.bf16 ? launch_rope<uint16_t>(c, a, stream, ctx) : launch_rope<float>(c, a, stream, ctx);
 }
 
 cudaError_t launch_kv_read(const KvCache &c, const int64_t *slots, int64_t n, float *k_out,

@@ -38,7 +38,8 @@ EXPORTED = (
     "qmm_gemm_q4_0_ws", "qmm_gemm_q8_0_ws", "qmm_gemm_q4_0_geglu_ws", "qmm_gemm_q4_0_prefill",
     "qmm_gemm_workspace_bytes", "qmm_gemm_geglu_workspace_bytes", "qmm_status_string", "qmm_version", "qmm_get_device_error",
     "qmm_set_wait_timeout_ns", "qmm_selftest_wait_timeout", "qmm_copy",
-    "qmm_kv_plan", "qmm_kv_append_q4_0", "qmm_kv_read_q4_0",
+    "qmm_kv_plan", "qmm_kv_append_q4_0", "qmm_kv_append_rope_q4_0", "qmm_kv_read_q4_0",
+    "qmm_route", "qmm_route_workspace_bytes",
     "qmm_attn_q4_0_workspace_bytes", "qmm_attn_q4_0", "qmm_logits_adjust",
 )
 
@@ -64,6 +65,27 @@ class AttnArgs(ctypes.Structure):
                 ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("batch", ctypes.c_int),
                 ("total_q", ctypes.c_int64), ("max_q", ctypes.c_int), ("heads", ctypes.c_int),
                 ("scale", ctypes.c_float), ("causal", ctypes.c_int), ("window", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class RopeArgs(ctypes.Structure):
+    """struct qmm_rope_args."""
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("q_out_stride", ctypes.c_int64), ("heads", ctypes.c_int), ("k", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64),
+                ("type", ctypes.c_int), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("table", ctypes.c_void_p), ("table_rows", ctypes.c_int64),
+                ("rot", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class RouteArgs(ctypes.Structure):
+    """struct qmm_route_args."""
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64), ("type", ctypes.c_int),
+                ("bias", ctypes.c_void_p), ("count", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("experts", ctypes.c_int), ("topk", ctypes.c_int), ("score", ctypes.c_int),
+                ("groups", ctypes.c_int), ("group_topk", ctypes.c_int), ("group_best", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("scale", ctypes.c_float), ("ids", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("expert_start", ctypes.c_void_p), ("pairs", ctypes.c_void_p),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
@@ -127,7 +149,9 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "qmm_copy": [P, P, SZ, P],
         "qmm_kv_plan": [P, P, I32, P, I64, P, I64, I32, P, P, P, P, I64, P, P],
         "qmm_kv_append_q4_0": [P, P, I64, P, I64, I32, P, I64, P],
+        "qmm_kv_append_rope_q4_0": [P, P, P],
         "qmm_kv_read_q4_0": [P, P, I64, P, P, P],
+        "qmm_route": [P, P],
         "qmm_attn_q4_0": [P, P, P],
         "qmm_logits_adjust": [P, P],
     }
@@ -144,6 +168,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         getattr(lib, name).restype = SZ
     lib.qmm_attn_q4_0_workspace_bytes.argtypes = [P, I32]
     lib.qmm_attn_q4_0_workspace_bytes.restype = SZ
+    lib.qmm_route_workspace_bytes.argtypes = [I64, I32]
+    lib.qmm_route_workspace_bytes.restype = SZ
     lib.qmm_set_wait_timeout_ns.argtypes = [U64]
     lib.qmm_set_wait_timeout_ns.restype = None
     _lib = lib
@@ -434,6 +460,46 @@ def qmm_kv_append_q4_0(cache: KvCacheQ4_0, k, v, slots, stream=None) -> None:
     _check(status, "qmm_kv_append_q4_0")
 
 
+def rope_table(positions: int, rot: int, base: float = 10000.0, freqs=None, device="cuda"):
+    """Cosines and sines of positions 0 .. positions-1, fp32 [positions][rot]: rot/2 cosines, then rot/2
+    sines of position * freqs[i] (radians; base^(-2i/rot) unless given), formed in 64 bits."""
+    import torch
+    f64 = dict(dtype=torch.float64, device=device)
+    if freqs is None:
+        freqs = float(base) ** (torch.arange(rot // 2, **f64) * (-2.0 / rot))
+    freqs = torch.as_tensor(freqs, **f64)
+    if rot % 2 or freqs.shape != (rot // 2,):
+        raise ValueError("rot must be even, with rot/2 frequencies")
+    angle = torch.arange(positions, **f64)[:, None] * freqs
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def qmm_kv_append_rope_q4_0(cache: KvCacheQ4_0, k, v, slots, positions, table, q=None, q_out=None,
+                            interleaved: bool = False, stream=None) -> None:
+    """The append with keys rotated by rows `positions` of table [rows][rot] on the way, and q
+    [n][heads][head_dim] rotated into q_out."""
+    torch = _torch_module()
+    kp, ks, kind = _rows(k, cache.kv_heads, cache.head_dim, "k")
+    vp, vs, other = _rows(v, cache.kv_heads, cache.head_dim, "v")
+    n = slots.numel()
+    if kind != other or k.shape[0] != n or v.shape[0] != n or positions.numel() != n:
+        raise ValueError("k and v must have one dtype and a row for each slot and position")
+    qp = op = qs = os_ = heads = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        heads = q.shape[1]
+        qp, qs, q_kind = _rows(q, heads, cache.head_dim, "q")
+        op, os_, out_kind = _rows(q_out, heads, cache.head_dim, "q_out")
+        if q_kind != kind or out_kind != kind or q.shape[0] != n or q_out.shape[0] != n:
+            raise ValueError("q and q_out must have k's dtype and a row for each slot")
+    rows, rot = table.shape
+    args = _ROPE_ARGS.pack(qp, qs, op, os_, heads, kp, ks, vp, vs, kind, _typed(slots, torch.int64, "slots"),
+                           _typed(positions, torch.int32, "positions"), n, _typed(table, torch.float32, "table"), rows,
+                           rot, bool(interleaved))
+    _check((_lib or load()).qmm_kv_append_rope_q4_0(cache.ref, args, _stream(stream)), "qmm_kv_append_rope_q4_0")
+
+
 def qmm_kv_read_q4_0(cache: KvCacheQ4_0, slots, k_out, v_out, stream=None) -> None:
     """The fp32 values of cache slots, k_out and v_out [n][kv_heads][head_dim] (either may be None)."""
     f32, n = _torch_module().float32, slots.numel()
@@ -453,10 +519,12 @@ def attn_workspace(cache: KvCacheQ4_0, heads: int):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k_codes.device)
 
 
-# struct qmm_attn_args and qmm_logits_args with the compiler's own padding
-# (AttnArgs and LogitsArgs name the fields)
+# the args structs of the same names with the compiler's own padding (AttnArgs
+# and its like name the fields)
 _ATTN_ARGS = struct.Struct("@PqiPqiPPqPPiqiifiiPN")
 _LOGITS_ARGS = struct.Struct("@PqPqqqPPqPPPPPPPqP")
+_ROPE_ARGS = struct.Struct("@PqPqiPqPqiPPqPqii")
+_ROUTE_ARGS = struct.Struct("@PqiPPqiiiiiiifPPPPPN")
 
 
 def qmm_attn_q4_0(cache: KvCacheQ4_0, q, out, table, q_start, kv_len, max_q: int, scale: float,
@@ -512,6 +580,55 @@ def qmm_logits_adjust(logits, out, history=None, hist_start=None, prompt_len=Non
         _typed(bias_values, f32, "bias_values"), _typed(bias_start, i32, "bias_start"),
         0 if bias_ids is None else bias_ids.numel(), _typed(allowed, i32, "allowed"))
     _check((_lib or load()).qmm_logits_adjust(args, _stream(stream)), "qmm_logits_adjust")
+
+
+# ---- mixture of experts ---------------------------------------------------------
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def route_workspace(tokens: int, experts: int, device="cuda"):
+    """A workspace for routing up to so many tokens (calls that overlap on the GPU need their own)."""
+    import torch
+    return torch.empty(max(int(load().qmm_route_workspace_bytes(tokens, experts)), 16), dtype=torch.uint8, device=device)
+
+
+def qmm_route(logits, ids, weights, expert_start, pairs, bias=None, score: str = "softmax", groups: int = 1,
+              group_topk: int = 1, group_best: int = 1, renormalize: bool = True, scale: float = 1.0, count=None,
+              workspace=None, stream=None) -> None:
+    """Experts ids [tokens][topk] and weights of each token from logits [tokens][experts] (fp32 or bf16),
+    and the pairs token * topk + r in the order of their experts.  Without a workspace it takes one from
+    the memory of the stream it runs on."""
+    torch = _torch_module()
+    i32, f32 = torch.int32, torch.float32
+    tokens, experts = logits.shape
+    topk = ids.shape[-1]
+    if logits.dtype is f32:
+        kind = QMM_F32
+    elif logits.dtype is torch.bfloat16:
+        kind = QMM_BF16
+    else:
+        raise ValueError("logits must be float32 or bfloat16")
+    if not logits.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    if logits.stride(1) != 1 and experts > 1:
+        raise ValueError("logits must have dense rows")
+    if tuple(ids.shape) != (tokens, topk) or tuple(weights.shape) != (tokens, topk) or \
+            pairs.numel() != tokens * topk or expert_start.numel() != experts + 1 or \
+            (bias is not None and bias.numel() != experts) or (count is not None and count.numel() != 1):
+        raise ValueError("ids and weights [tokens][topk], pairs [tokens * topk], expert_start [experts + 1] and "
+                         "bias [experts] expected")
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}")
+    if workspace is None:
+        with torch.cuda.stream(_stream_object(stream)):  # as for attention
+            workspace = route_workspace(tokens, experts, logits.device)
+    args = _ROUTE_ARGS.pack(logits.data_ptr(), logits.stride(0) if tokens > 1 else experts, kind, _typed(bias, f32, "bias"),
+                            _typed(count, i32, "count"), tokens, experts, topk, SCORES[score], groups, group_topk,
+                            group_best, bool(renormalize), scale, _typed(ids, i32, "ids"), _typed(weights, f32, "weights"),
+                            _typed(expert_start, i32, "expert_start"), _typed(pairs, i32, "pairs"), _ptr(workspace),
+                            workspace.numel() * workspace.element_size())
+    _check((_lib or load()).qmm_route(args, _stream(stream)), "qmm_route")
 
 
 # ---- tensor-level conveniences (allocate the output, then call the ABI) ----

@@ -21,7 +21,10 @@
  *
  *   kv      : a paged cache of keys and values held in Q4_0: page tables and
  *             slot maps from request lengths, append (quantize), read back
+ *   rope    : the same append with keys and queries rotated by their positions
  *   attn    : attention over that cache, single tokens and prompts
+ *   route   : experts of each token, their weights, pairs by expert
+ *   experts : the GeGLU and down products of each token's experts
  *   logits  : penalties, biases and grammar masks on the LM head's output
  *
  * Block formats (GGUF; 32 weights per block, K a multiple of 32):
@@ -366,6 +369,49 @@ qmm_status qmm_kv_append_q4_0(const qmm_kv_q4_0 *cache, const void *k, int64_t k
                               const void *v, int64_t v_stride, qmm_dtype type,
                               const int64_t *slots, int64_t n, qmm_stream_t stream);
 
+/* The same append with the positions' rotation on the way: keys are rotated,
+ * then quantized as above; values are appended as they are; queries (where q is
+ * not NULL) are rotated into q_out, rounded once to their type.  The first `rot`
+ * values of each head form rot / 2 pairs (a, b): values i and i + rot / 2, or 2i
+ * and 2i + 1 if interleaved; the others pass.  With c and s from the position's
+ * row of `table`, [table_rows][rot], cosines of the pairs then sines:
+ *   (a, b) -> (a c - b s, a s + b c)
+ * in fp32, each product and each sum rounded once (no contraction), so that the
+ * codes are defined to the bit.  A table made in 64 bits leaves far positions
+ * as exact as near ones.
+ *   positions  int32 [n], row of the table; -1 skips the token whole, its row
+ *              of q_out is left as it was (a plan's padding)
+ *   slots      as above; -1 skips the append, the query is rotated
+ * A position or slot outside its array records QMM_ERR_INDEX and skips the
+ * token.  k, v, q and q_out are of one type, strides count elements; heads is
+ * the number of query heads.
+ * Requires n >= 0 (0 launches nothing), n <= 2^30, rot even and 2 <= rot <=
+ * head_dim, table_rows >= 1, strides at least the rows' widths, heads >= 1
+ * where q is given (at most 1024), pointers aligned to their type.  q_out and
+ * the cache must overlap no input or each other. */
+typedef struct qmm_rope_args {
+    const void *q;
+    int64_t q_stride;
+    void *q_out;
+    int64_t q_out_stride;
+    int heads;
+    const void *k;
+    int64_t k_stride;
+    const void *v;
+    int64_t v_stride;
+    qmm_dtype type;
+    const int64_t *slots;
+    const int32_t *positions;
+    int64_t n;
+    const float *table;
+    int64_t table_rows;
+    int rot;
+    int interleaved;
+} qmm_rope_args;
+
+qmm_status qmm_kv_append_rope_q4_0(const qmm_kv_q4_0 *cache, const qmm_rope_args *args,
+                                   qmm_stream_t stream);
+
 /* The fp32 values of n cache slots: k_out and v_out [n][kv_heads][head_dim]
  * (either may be NULL), each (float)(nibble - 8) * scale, exact.  Rows of
  * slots outside the cache are 0 (-1 silently, others record QMM_ERR_INDEX).
@@ -444,6 +490,64 @@ typedef struct qmm_attn_args {
 size_t qmm_attn_q4_0_workspace_bytes(const qmm_kv_q4_0 *cache, int heads);
 qmm_status qmm_attn_q4_0(const qmm_kv_q4_0 *cache, const qmm_attn_args *args,
                          qmm_stream_t stream);
+
+/* ---- Routing to experts ---------------------------------------------------
+ * For each token t < tokens, from l = logits[t][e], e < experts:
+ *   s_e = exp(l_e) / sum_j exp(l_j)  (QMM_SCORE_SOFTMAX)
+ *         or 1 / (1 + exp(-l_e))     (QMM_SCORE_SIGMOID)
+ *   c_e = s_e + bias[e]              (bias NULL: c orders as l does)
+ *   with groups > 1, groups of experts / groups consecutive experts score the
+ *   sum of their group_best (1 or 2) largest c, and the group_topk best are kept
+ *   ids[t]     the topk kept experts of largest c, in that order
+ *   weights[t] their s (without the bias), divided by their sum if
+ *              renormalize, times scale
+ * Equal values go to the lowest index, a NaN comes behind -inf.  The choice is
+ * that of 64-bit arithmetic on the given logits and biases: values that lie
+ * too near for fp32 are formed again.  Weights are fp32 and off by a few 2^-24;
+ * where all scores are 0 (logits -inf) so are the weights.  Then, over all
+ * tokens,
+ *   pairs         int32 [tokens * topk]: the pairs t * topk + r in the order of
+ *                 their experts, those of one expert by token
+ *   expert_start  int32 [experts + 1]: expert e has entries expert_start[e] ..
+ *                 expert_start[e + 1] - 1
+ * which is what the experts' products read.
+ *   count  int32 on the device, or NULL: tokens from *count on are not there
+ *          (padding of a captured graph): ids and pairs -1, weights 0.  A count
+ *          outside 0..tokens is moved to the nearer end, QMM_ERR_INDEX.
+ *   workspace  16-byte aligned device memory of at least
+ *          qmm_route_workspace_bytes() bytes (0 up to 64 tokens), scratch
+ * Requires tokens >= 0 (0 launches nothing), 1 <= topk <= 32, topk at most the
+ * kept groups' experts, groups dividing experts, 1 <= group_topk <= groups,
+ * scale finite, logits_stride >= experts; at most 1024 experts, 32 groups and
+ * 2^30 pairs (else QMM_ERR_UNSUPPORTED).  No output may overlap an input or
+ * another output. */
+typedef enum qmm_score { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
+
+typedef struct qmm_route_args {
+    const void *logits;
+    int64_t logits_stride;
+    qmm_dtype type;
+    const float *bias;
+    const int32_t *count;
+    int64_t tokens;
+    int experts;
+    int topk;
+    qmm_score score;
+    int groups;
+    int group_topk;
+    int group_best;
+    int renormalize;
+    float scale;
+    int32_t *ids;
+    float *weights;
+    int32_t *expert_start;
+    int32_t *pairs;
+    void *workspace;
+    size_t workspace_bytes;
+} qmm_route_args;
+
+size_t qmm_route_workspace_bytes(int64_t tokens, int experts);
+qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
 
 /* ---- Penalties, biases and grammar masks on logits ----------------------
  * out[i][t] for i < rows, t < vocab, from x = logits[i][t]:
