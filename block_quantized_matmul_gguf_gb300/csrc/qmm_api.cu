@@ -706,6 +706,89 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream) {
     return from_cuda(launch_route(r, reinterpret_cast<cudaStream_t>(stream), ctx));
 }
 
+namespace {
+
+constexpr int64_t kExpertsMaxN = int64_t(1) << 24, kExpertsMaxK = int64_t(1) << 20;
+
+// Checks shared by the experts' products.  `w`: weights of one kind.
+qmm_status check_experts(const qmm_expert_plan *plan, const void *w, int64_t n, int64_t k, ExpertsPlan *out) {
+    if (!plan) return QMM_ERR_NULL;
+    if (plan->tokens < 0 || plan->topk < 1 || plan->experts < 1) return QMM_ERR_SHAPE;
+    if (n < 1 || k < kQK || k % kQK != 0) return QMM_ERR_SHAPE;
+    if (plan->experts > kMaxExperts || plan->topk > kMaxTopk || plan->tokens > kMaxRows / plan->topk || n > kExpertsMaxN ||
+        k > kExpertsMaxK)
+        return QMM_ERR_UNSUPPORTED;
+    *out = ExpertsPlan{plan->expert_start, plan->pairs, plan->tokens * plan->topk, plan->experts, plan->topk};
+    if (plan->tokens == 0) return QMM_OK;
+    if (!w || !plan->expert_start || !plan->pairs) return QMM_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(plan->expert_start, 4) || !aligned(plan->pairs, 4)) return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
+size_t experts_bytes(const ExpertsPlan &p, int64_t n, int64_t k) {
+    return static_cast<size_t>(p.experts) * n * (k / kQK) * kQ4_0Bytes;
+}
+
+}  // namespace
+
+qmm_status qmm_experts_geglu_q4_0(const qmm_expert_plan *plan, const void *wg, const void *wu, const void *x, int64_t x_stride,
+                                  qmm_dtype x_type, void *h, int64_t h_stride, qmm_dtype h_type, int64_t n, int64_t k,
+                                  qmm_stream_t stream) {
+    ExpertsPlan p;
+    qmm_status s = check_experts(plan, wg, n, k, &p);
+    if (s == QMM_OK) s = check_experts(plan, wu, n, k, &p);
+    if (s != QMM_OK) return s;
+    if (!valid_dtype(x_type) || !valid_dtype(h_type) || x_stride < k || h_stride < n) return QMM_ERR_SHAPE;
+    if (x_stride > kMaxIndex || h_stride > kMaxIndex) return QMM_ERR_UNSUPPORTED;
+    if (p.pairs_total == 0) return QMM_OK;
+    if (!x || !h) return QMM_ERR_NULL;
+    if (!aligned(x, dtype_bytes(x_type)) || !aligned(h, dtype_bytes(h_type))) return QMM_ERR_ALIGN;
+    const size_t wbytes = experts_bytes(p, n, k);
+    const Range ins[] = {{wg, wbytes}, {wu, wbytes}, {x, rows_bytes(plan->tokens, x_stride, k, dtype_bytes(x_type))},
+                         {p.expert_start, 4 * (static_cast<size_t>(p.experts) + 1)},
+                         {p.pairs, 4 * static_cast<size_t>(p.pairs_total)}};
+    const Range outs[] = {{h, rows_bytes(p.pairs_total, h_stride, n, dtype_bytes(h_type))}};
+    if (!outputs_clear(outs, 1, ins, 5)) return QMM_ERR_UNSUPPORTED;
+    LaunchCtx ctx;
+    if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
+    const ExpertsGeglu a = {p, static_cast<const uint8_t *>(wg), static_cast<const uint8_t *>(wu), x, h, x_stride, h_stride, n, k,
+                            x_type == QMM_BF16, h_type == QMM_BF16};
+    return from_cuda(launch_experts_geglu(a, reinterpret_cast<cudaStream_t>(stream), ctx));
+}
+
+size_t qmm_experts_down_workspace_bytes(int64_t tokens, int topk, int64_t n) {
+    if (tokens < 1 || topk < 1 || topk > kMaxTopk || tokens > kMaxRows / topk || n < 1 || n > kExpertsMaxN) return 0;
+    return experts_down_workspace_bytes(tokens, topk, n);
+}
+
+qmm_status qmm_experts_down_q4_0(const qmm_expert_plan *plan, const void *wd, const void *h, int64_t h_stride, qmm_dtype h_type,
+                                 const int32_t *ids, const float *weights, void *y, int64_t y_stride, qmm_dtype y_type,
+                                 int64_t n, int64_t k, void *workspace, size_t workspace_bytes, qmm_stream_t stream) {
+    ExpertsPlan p;
+    qmm_status s = check_experts(plan, wd, n, k, &p);
+    if (s != QMM_OK) return s;
+    if (!valid_dtype(h_type) || !valid_dtype(y_type) || h_stride < k || y_stride < n) return QMM_ERR_SHAPE;
+    if (h_stride > kMaxIndex || y_stride > kMaxIndex) return QMM_ERR_UNSUPPORTED;
+    if (p.pairs_total == 0) return QMM_OK;
+    if (!h || !ids || !weights || !y || !workspace) return QMM_ERR_NULL;
+    if (!aligned(h, dtype_bytes(h_type)) || !aligned(y, dtype_bytes(y_type)) || !aligned(ids, 4) || !aligned(weights, 4))
+        return QMM_ERR_ALIGN;
+    const size_t need = experts_down_workspace_bytes(plan->tokens, p.topk, n);
+    s = check_workspace(workspace, workspace_bytes, need);
+    if (s != QMM_OK) return s;
+    const size_t list = 4 * static_cast<size_t>(p.pairs_total);
+    const Range ins[] = {{wd, experts_bytes(p, n, k)}, {h, rows_bytes(p.pairs_total, h_stride, k, dtype_bytes(h_type))},
+                         {p.expert_start, 4 * (static_cast<size_t>(p.experts) + 1)}, {p.pairs, list}, {ids, list},
+                         {weights, list}};
+    const Range outs[] = {{y, rows_bytes(plan->tokens, y_stride, n, dtype_bytes(y_type))}, {workspace, need}};
+    if (!outputs_clear(outs, 2, ins, 6)) return QMM_ERR_UNSUPPORTED;
+    LaunchCtx ctx;
+    if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
+    const ExpertsDown a = {p, static_cast<const uint8_t *>(wd), h, ids, weights, y, workspace, h_stride, y_stride, n, k,
+                           h_type == QMM_BF16, y_type == QMM_BF16};
+    return from_cuda(launch_experts_down(a, reinterpret_cast<cudaStream_t>(stream), ctx));
+}
+
 qmm_status qmm_logits_adjust(const qmm_logits_args *args, qmm_stream_t stream) {
     if (!args) return QMM_ERR_NULL;
     const qmm_logits_args &a = *args;

@@ -1,0 +1,672 @@
+// qmm_experts.cuh -- the experts' Q4_0 products (include/qmm.h,
+// qmm_experts_geglu_q4_0 and qmm_experts_down_q4_0): the streaming form, for
+// few rows an expert and for fp32 outputs.
+//
+// Mathematics.  With codes n (0..15) and scales d of 32-weight blocks b,
+//   y[i] = sum_b d_b * sum_j (n_bj - 8) x_bj
+// for the rows x of an expert's pairs.  The integers are exact in binary16, so
+// the inner sums run on mma.sync m16n8k16 with 16 rows of weights as one
+// operand, taken from the 4-bit codes in registers, and 8 pairs' x as the other;
+// the scales join in fp32.
+//
+// Precision.  x enters as one binary16 value, scaled by a power of two per row
+// and 256 values so that the largest lies in [2^14, 2^15): a bf16 x exactly (down
+// to 2^-31 of that largest), an fp32 x rounded to 11 bits, which is less than a
+// bf16 output shows.  For fp32 outputs an fp32 x enters in two parts (22 bits).
+// For bf16 outputs a code masked in place is a subnormal binary16 number, n 2^-24
+// (16 n 2^-24 for the upper of two, the 16 taken out of x), and -8 sum x is where
+// the sum begins; fp32 outputs take two more instructions a pair for the normal
+// numbers n - 8, because the tensor cores' sums of subnormal operands keep some 18
+// bits only.
+//
+// Work.  An item is 32 rows of weights (16 gate and the same 16 up rows for
+// GeGLU) of one expert against one group of 8 NB of its pairs.  A CTA of up to 16
+// warps, one an SM, walks through its own run of items: RW items at a time, each
+// by KW warps that take every KW-th 256 values of K and add their sums in shared
+// memory in a fixed order.  The group's x lies in shared memory as the
+// instruction wants it, made once while the items stay with the group.  Each
+// warp's weights arrive through its own ring of asynchronous copies, 32 rows x 144
+// bytes a stage, so that the eight rows that a quarter of a load touches lie in
+// different banks.
+#pragma once
+
+#include "qmm_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+namespace qmm {
+namespace experts {
+
+constexpr int kMaxWarps = 16;
+constexpr int kStages = 2;
+constexpr int kChunk = 256;   // K values of a stage
+constexpr int kRows = 32;     // weight rows of an item
+
+struct StreamParams {
+    ExpertsPlan plan;
+    const uint8_t *w[2];  // GeGLU: gate and up; down: w[0]
+    const void *x;
+    int64_t x_stride;     // elements
+    void *out;            // GeGLU: h, by the pairs' order; down: fp32 [pairs], by the pair
+    int64_t out_stride;   // elements
+    int64_t n, k;
+    int64_t row_bytes;    // of weights
+    int64_t matrix_bytes; // of an expert
+    int64_t w_bytes;      // of all
+    int chunks;           // of K
+    int blocks;           // of K
+    int rw, kw;           // items at a time, warps an item
+    int row_groups;       // items of rw * rows
+    int x_panel;          // chunks of x that shared memory holds
+    uint32_t magic;       // 1024, 1024 in binary16, in a register
+    bool x_bf16, out_bf16, x_wide;
+    LaunchCtx ctx;
+};
+
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float low_half(uint32_t v) { return __low2float(*reinterpret_cast<const __half2 *>(&v)); }
+__device__ __forceinline__ float high_half(uint32_t v) { return __high2float(*reinterpret_cast<const __half2 *>(&v)); }
+
+// d = a b + c, a 16 x 16 (row), b 16 x 8 (column), fp32 sums
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes, of which the first `bytes` are read and the others zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void barrier(int id, int threads) {
+    asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Shared memory, from its start: rings, x, its scales and sums, partial sums, rows.
+template <bool EXACT, int PARTS, int NB, bool ALIGNED>
+struct StreamLayout {
+    static constexpr int pitch = ALIGNED ? 144 : 176;  // bytes of a row's window in a stage
+    static constexpr int stage = kRows * pitch;
+    static constexpr int x_block = NB * PARTS * 512;   // bytes of 32 values of K
+    __host__ __device__ static int x(int warps) { return warps * kStages * stage; }
+    __host__ __device__ static int scale(int warps, int panel) { return x(warps) + panel * 8 * x_block; }
+    __host__ __device__ static int sums(int warps, int panel) { return scale(warps, panel) + panel * NB * 32; }
+    __host__ __device__ static int part(int warps, int panel) {
+        return sums(warps, panel) + (EXACT ? 0 : panel * 8 * NB * 32);
+    }
+    __host__ __device__ static int rows(int warps, int panel) { return part(warps, panel) + warps * NB * 1024; }
+    __host__ __device__ static int total(int warps, int panel) { return rows(warps, panel) + 2 * 8 * NB * 4 + 64; }
+};
+
+// A place in a CTA's run of items.
+struct Place {
+    int64_t left;  // items of the run from here on
+    int expert, group, row_group;
+    int start, count;  // of the expert's pairs
+};
+
+// The pairs of an expert, bounded.
+__device__ __forceinline__ void expert_range(const StreamParams &p, int e, int &start, int &count) {
+    const int64_t pairs = p.plan.pairs_total;
+    const int64_t a = p.plan.expert_start[e], b = p.plan.expert_start[e + 1];
+    if (a < 0 || b < a || b > pairs) {
+        record_error(p.ctx, kDevErrIndex);
+        start = 0;
+        count = 0;
+        return;
+    }
+    start = static_cast<int>(a);
+    count = static_cast<int>(b - a);
+}
+
+template <int NB>
+__device__ __forceinline__ void advance(const StreamParams &p, Place &at) {
+    if (--at.left <= 0) return;
+    if (++at.row_group < p.row_groups) return;
+    at.row_group = 0;
+    ++at.group;
+    while (at.group * 8 * NB >= at.count) {
+        if (++at.expert >= p.plan.experts) {  // cannot be: the run ends before
+            at.left = 0;
+            return;
+        }
+        at.group = 0;
+        expert_range(p, at.expert, at.start, at.count);
+    }
+}
+
+// 32 rows x one chunk of weights into a stage of this warp's ring.
+template <bool GEGLU, bool ALIGNED>
+__device__ __forceinline__ void load_stage(const StreamParams &p, uint32_t stage, int expert, int64_t row0, int chunk, int lane) {
+    constexpr int pitch = ALIGNED ? 144 : 176;
+    constexpr int pieces = ALIGNED ? 9 : 10;
+    const int bytes = min(8, p.blocks - chunk * 8) * kQ4_0Bytes;
+#pragma unroll
+    for (int i = 0; i < pieces; ++i) {
+        const int at = i * 32 + lane, row = at / pieces, piece = at - row * pieces;
+        const int64_t r = row0 + (GEGLU ? row & 15 : row);
+        const int64_t from = expert * p.matrix_bytes + min(r, p.n - 1) * p.row_bytes + chunk * 144;
+        const uint8_t *w = p.w[GEGLU ? row >> 4 : 0];
+        if constexpr (ALIGNED) {
+            copy16(stage + row * pitch + piece * 16, w + from + piece * 16, 16);
+        } else {
+            const int64_t first = (from & ~int64_t(15)) + piece * 16;
+            if (first < from + bytes)
+                copy16(stage + row * pitch + piece * 16, w + first, static_cast<uint32_t>(min(int64_t(16), p.w_bytes - first)));
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load_four(const T *p, bool wide);
+template <>
+__device__ __forceinline__ float4 load_four<float>(const float *p, bool wide) {
+    if (wide) return *reinterpret_cast<const float4 *>(p);
+    return make_float4(p[0], p[1], p[2], p[3]);
+}
+template <>
+__device__ __forceinline__ float4 load_four<uint16_t>(const uint16_t *p, bool wide) {
+    uint32_t a, b;
+    if (wide) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        a = v.x;
+        b = v.y;
+    } else {
+        a = p[0] | static_cast<uint32_t>(p[1]) << 16;
+        b = p[2] | static_cast<uint32_t>(p[3]) << 16;
+    }
+    return make_float4(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
+                       __uint_as_float(b & 0xFFFF0000u));
+}
+
+// One chunk of eight pairs' x as the products' operand: lane (g, t) makes
+// pair g's values 4t..4t+3 and 16+4t..16+4t+3 of each block, in the order that
+// the codes of a word have.
+template <bool EXACT, int PARTS, int NB, typename T>
+__device__ __forceinline__ void stage_x(const StreamParams &p, char *xs, float *scale, float *sums, const T *row, int chunk,
+                                        int nb, int lane) {
+    const int t = lane & 3, g = lane >> 2;
+    const int blocks = min(8, p.blocks - chunk * 8);
+    float4 v[8][2];
+    float top = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        v[b][0] = v[b][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (row && b < blocks) {
+            v[b][0] = load_four<T>(row + chunk * kChunk + b * 32 + 4 * t, p.x_wide);
+            v[b][1] = load_four<T>(row + chunk * kChunk + b * 32 + 16 + 4 * t, p.x_wide);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            top = fmaxf(fmaxf(fmaxf(top, fabsf(v[b][h].x)), fabsf(v[b][h].y)), fmaxf(fabsf(v[b][h].z), fabsf(v[b][h].w)));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    // top 2^f in [2^14, 2^15); both powers normal (a smaller top stays smaller)
+    const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 15), 254);
+    const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+    if (t == 0) scale[chunk * 8 * NB + nb * 8 + g] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        uint32_t part[PARTS][4];
+        float sum = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float s = EXACT || h == 0 ? f : f * 0.0625f;  // upper codes count 16-fold
+            const float y[4] = {v[b][h].x * s, v[b][h].z * s, v[b][h].y * s, v[b][h].w * s};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t hi = pack_half(y[2 * i], y[2 * i + 1]);
+                part[0][2 * h + i] = hi;
+                if constexpr (PARTS == 2)
+                    part[1][2 * h + i] = pack_half(y[2 * i] - low_half(hi), y[2 * i + 1] - high_half(hi));
+                if constexpr (!EXACT) sum += (low_half(hi) + high_half(hi)) * (h ? 16.0f : 1.0f);
+            }
+        }
+        char *to = xs + ((chunk * 8 + b) * NB + nb) * PARTS * 512;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+            reinterpret_cast<uint4 *>(to + q * 512)[lane] = make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]);
+        if constexpr (!EXACT) {
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+            if (t == 0) sums[(chunk * 8 + b) * 8 * NB + nb * 8 + g] = sum * -4.76837158203125e-07f;  // -8 2^-24
+        }
+    }
+}
+
+// A warp's products of one stage: two tiles of 16 rows against NB groups of
+// eight pairs.  skew: bytes by which each of the lane's four rows (g, g + 8 of
+// both tiles) begins behind its window.
+template <bool EXACT, int PARTS, int NB, bool ALIGNED>
+__device__ __forceinline__ void stage_products(const char *stage, const char *xs, const float *scale, const float *sums,
+                                               int blocks, const int (&skew)[2][2], uint32_t magic, int lane,
+                                               int used, float (&total)[2][NB][4]) {
+    constexpr int pitch = ALIGNED ? 144 : 176;
+    const int t = lane & 3, g = lane >> 2;
+    float acc[2][NB][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
+    auto block = [&](int b, const uint32_t (&q)[2][2], const float (&d)[2][2]) {
+        uint32_t x[NB][PARTS][4];
+        float c[NB][2];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            if (n < used) {
+#pragma unroll
+                for (int s = 0; s < PARTS; ++s) {
+                    const uint4 v = reinterpret_cast<const uint4 *>(xs + ((b * NB + n) * PARTS + s) * 512)[lane];
+                    x[n][s][0] = v.x, x[n][s][1] = v.y, x[n][s][2] = v.z, x[n][s][3] = v.w;
+                }
+                if constexpr (!EXACT) {
+                    const float2 v = *reinterpret_cast<const float2 *>(sums + b * 8 * NB + n * 8 + 2 * t);
+                    c[n][0] = v.x, c[n][1] = v.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t u = q[r][0], v = q[r][1], u8 = u >> 8, v8 = v >> 8;
+            uint32_t a[8];
+            if constexpr (EXACT) {
+                a[0] = hadd2((u & 0x000F000Fu) | magic, 0xE408E408u);  // - 1032
+                a[1] = hadd2((v & 0x000F000Fu) | magic, 0xE408E408u);
+                a[2] = hadd2((u8 & 0x000F000Fu) | magic, 0xE408E408u);
+                a[3] = hadd2((v8 & 0x000F000Fu) | magic, 0xE408E408u);
+                a[4] = hfma2((u & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
+                a[5] = hfma2((v & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+                a[6] = hfma2((u8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+                a[7] = hfma2((v8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+            } else {
+                a[0] = u & 0x000F000Fu, a[1] = v & 0x000F000Fu, a[2] = u8 & 0x000F000Fu, a[3] = v8 & 0x000F000Fu;
+                a[4] = u & 0x00F000F0u, a[5] = v & 0x00F000F0u, a[6] = u8 & 0x00F000F0u, a[7] = v8 & 0x00F000F0u;
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                if (n < used) {
+                    float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if constexpr (!EXACT) z[0] = z[2] = c[n][0], z[1] = z[3] = c[n][1];
+#pragma unroll
+                    for (int s = PARTS - 1; s >= 0; --s) {  // the small part first
+                        mma16816(z, a[0], a[1], a[2], a[3], x[n][s][0], x[n][s][1]);
+                        mma16816(z, a[4], a[5], a[6], a[7], x[n][s][2], x[n][s][3]);
+                    }
+                    acc[r][n][0] = fmaf(d[r][0], z[0], acc[r][n][0]);
+                    acc[r][n][1] = fmaf(d[r][0], z[1], acc[r][n][1]);
+                    acc[r][n][2] = fmaf(d[r][1], z[2], acc[r][n][2]);
+                    acc[r][n][3] = fmaf(d[r][1], z[3], acc[r][n][3]);
+                }
+            }
+        }
+    };
+    if constexpr (ALIGNED) {
+        // two blocks are nine words: the first block's codes begin in the
+        // middle of a word, the second's at one
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t q0[2][2], q1[2][2];
+            float d0[2][2], d1[2][2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const char *row = stage + (r * 16 + h * 8 + g) * pitch + 36 * j;
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(row) + t;
+                    q0[r][h] = __byte_perm(w[0], w[1], 0x5432);
+                    q1[r][h] = w[5];
+                    d0[r][h] = half_bits_to_float(*reinterpret_cast<const uint16_t *>(row));
+                    d1[r][h] = half_bits_to_float(*reinterpret_cast<const uint16_t *>(row + 18));
+                }
+            block(2 * j, q0, d0);
+            block(2 * j + 1, q1, d1);
+        }
+    } else {
+#pragma unroll 1
+        for (int b = 0; b < blocks; ++b) {
+            uint32_t q[2][2];
+            float d[2][2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const char *row = stage + (r * 16 + h * 8 + g) * pitch;
+                    const int at = skew[r][h] + 18 * b;
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(row + ((at + 2) & ~3)) + t;
+                    q[r][h] = __byte_perm(w[0], w[1], (at + 2) & 2 ? 0x5432 : 0x3210);
+                    d[r][h] = half_bits_to_float(*reinterpret_cast<const uint16_t *>(row + at));
+                }
+            block(b, q, d);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const float2 s = *reinterpret_cast<const float2 *>(scale + n * 8 + 2 * t);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = EXACT ? acc[r][n][i] : acc[r][n][i] * 16777216.0f;
+                total[r][n][i] = fmaf(v, i & 1 ? s.y : s.x, total[r][n][i]);
+            }
+    }
+}
+
+// gelu(z) = z / 2 (1 + tanh(a)) = z / (1 + exp(-2a))
+__device__ __forceinline__ float gelu(float z) {
+    const float a = 0.7978845608028654f * fmaf(0.044715f * z, z * z, z);
+    return z / (1.0f + expf(-2.0f * a));
+}
+
+__device__ __forceinline__ void put(void *out, int64_t at, bool bf16, float v) {
+    if (bf16)
+        static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<float *>(out)[at] = v;
+}
+
+template <bool EXACT, int PARTS, int NB, bool GEGLU, bool ALIGNED>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_constant__ StreamParams p) {
+    using L = StreamLayout<EXACT, PARTS, NB, ALIGNED>;
+    extern __shared__ __align__(128) char smem[];
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = lane & 3, g = lane >> 2;
+    const int rw = warp / p.kw, kw = warp - rw * p.kw;  // item among those at a time, part of K
+    char *xs = smem + L::x(warps);
+    float *scale = reinterpret_cast<float *>(smem + L::scale(warps, p.x_panel));
+    float *sums = reinterpret_cast<float *>(smem + L::sums(warps, p.x_panel));
+    float *part = reinterpret_cast<float *>(smem + L::part(warps, p.x_panel));
+    int *src = reinterpret_cast<int *>(smem + L::rows(warps, p.x_panel));  // [8 NB] rows of x, -1 where there is none
+    int *dst = src + 8 * NB;                                              // [8 NB] rows of out
+    int *found = dst + 8 * NB;                                            // the run's first place
+
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // The run: units (expert, group of pairs) x row groups, cut equally.
+    {
+        __shared__ int32_t sum[kMaxWarps];
+        const int threads = blockDim.x;
+        const int per = (p.plan.experts + threads - 1) / threads;
+        const int e0 = min(p.plan.experts, static_cast<int>(threadIdx.x) * per), e1 = min(p.plan.experts, e0 + per);
+        int mine = 0;
+        for (int e = e0; e < e1; ++e) {
+            int start, count;
+            expert_range(p, e, start, count);
+            mine += (count + 8 * NB - 1) / (8 * NB);
+        }
+        int s = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s += u;
+        }
+        if (lane == 31) sum[warp] = s;
+        __syncthreads();
+        int ahead = s - mine, all = 0;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) ahead += sum[w];
+            all += sum[w];
+        }
+        const int64_t items = static_cast<int64_t>(all) * p.row_groups;
+        const int64_t from = items * blockIdx.x / gridDim.x, to = items * (blockIdx.x + 1) / gridDim.x;
+        if (from == to) return;
+        const int unit = static_cast<int>(from / p.row_groups);
+        if (unit >= ahead && unit < ahead + mine) {  // one thread of the CTA
+            for (int e = e0; e < e1; ++e) {
+                int start, count;
+                expert_range(p, e, start, count);
+                const int units = (count + 8 * NB - 1) / (8 * NB);
+                if (unit < ahead + units) {
+                    found[0] = e;
+                    found[1] = unit - ahead;
+                    found[2] = start;
+                    found[3] = count;
+                    break;
+                }
+                ahead += units;
+            }
+            found[4] = static_cast<int>(from - static_cast<int64_t>(unit) * p.row_groups);
+            *reinterpret_cast<int64_t *>(found + 6) = to - from;
+        }
+        __syncthreads();
+    }
+    Place at;
+    at.expert = found[0];
+    at.group = found[1];
+    at.start = found[2];
+    at.count = found[3];
+    at.row_group = found[4];
+    at.left = *reinterpret_cast<const int64_t *>(found + 6);
+
+    constexpr int kItemRows = GEGLU ? 16 : 32;
+    const uint32_t ring = smem_addr(smem) + warp * kStages * L::stage;
+    const char *ring_ptr = smem + warp * kStages * L::stage;
+
+    // Loads run kStages - 1 chunks ahead, through the items.
+    Place load = at;
+    int load_chunk = kw;
+    int loaded = 0;
+    auto load_next = [&]() {
+        while (load.left > 0 && load_chunk >= p.chunks) {
+            advance<NB>(p, load);
+            load_chunk = kw;
+            if (kw >= p.chunks) load.left = 0;
+        }
+        if (load.left > 0) {
+            const int64_t row0 = (static_cast<int64_t>(load.row_group) * p.rw + rw) * kItemRows;
+            if (row0 < p.n)
+                load_stage<GEGLU, ALIGNED>(p, ring + (loaded & (kStages - 1)) * L::stage, load.expert, row0, load_chunk, lane);
+            load_chunk += p.kw;
+            ++loaded;
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) load_next();
+
+    int done = 0;
+    int held_expert = -1, held_group = -1, held_panel = -1;
+    const int panels = (p.chunks + p.x_panel - 1) / p.x_panel;
+    for (; at.left > 0; advance<NB>(p, at)) {
+        const int64_t row0 = (static_cast<int64_t>(at.row_group) * p.rw + rw) * kItemRows;
+        const bool there = row0 < p.n;
+        const int first = at.start + at.group * 8 * NB;              // of the pairs
+        const int cols = min(8 * NB, at.count - at.group * 8 * NB);  // of them here
+        const int used = (cols + 7) / 8;
+        float total[2][NB][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) total[r][n][i] = 0.0f;
+        int skew[2][2] = {{0, 0}, {0, 0}};
+        if constexpr (!ALIGNED) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t row = row0 + (GEGLU ? 0 : r * 16) + h * 8 + g;
+                    skew[r][h] = static_cast<int>((at.expert * p.matrix_bytes + min(row, p.n - 1) * p.row_bytes) & 15);
+                }
+        }
+        for (int panel = 0; panel < panels; ++panel) {
+            const int c0 = panel * p.x_panel, c1 = min(p.chunks, c0 + p.x_panel);
+            if (at.expert != held_expert || at.group != held_group || panel != held_panel) {
+                __syncthreads();
+                if (at.expert != held_expert || at.group != held_group) {
+                    if (threadIdx.x < 8 * NB) {
+                        const int c = threadIdx.x;
+                        int from = -1, to = -1;
+                        if (c < cols) {
+                            const int pair = p.plan.pairs[first + c];
+                            if (pair >= 0 && pair < p.plan.pairs_total) {
+                                from = GEGLU ? pair / p.plan.topk : first + c;
+                                to = GEGLU ? first + c : pair;
+                            } else {
+                                record_error(p.ctx, kDevErrIndex);
+                            }
+                        }
+                        src[c] = from;
+                        dst[c] = to;
+                    }
+                    __syncthreads();
+                }
+                for (int u = warp; u < (c1 - c0) * used; u += warps) {
+                    const int n = u % used, c = u / used;
+                    const int row = src[n * 8 + g];
+                    // addresses count from the panel's first chunk
+                    char *xp = xs - static_cast<int64_t>(c0) * 8 * L::x_block;
+                    float *sp = scale - c0 * 8 * NB, *mp = sums - c0 * 64 * NB;
+                    if (p.x_bf16)
+                        stage_x<EXACT, PARTS, NB, uint16_t>(
+                            p, xp, sp, mp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane);
+                    else
+                        stage_x<EXACT, PARTS, NB, float>(
+                            p, xp, sp, mp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane);
+                }
+                held_expert = at.expert;
+                held_group = at.group;
+                held_panel = panel;
+                __syncthreads();
+            }
+            for (int c = c0 + (kw - c0 % p.kw + p.kw) % p.kw; c < c1; c += p.kw) {
+                load_next();
+                copy_wait<kStages - 1>();
+                __syncwarp();
+                if (there)
+                    stage_products<EXACT, PARTS, NB, ALIGNED>(
+                        ring_ptr + (done & (kStages - 1)) * L::stage, xs + (c - c0) * 8 * L::x_block, scale + (c - c0) * 8 * NB,
+                        sums + (c - c0) * 64 * NB, min(8, p.blocks - c * 8), skew, p.magic, lane, used, total);
+                __syncwarp();
+                ++done;
+            }
+        }
+        // the item's sums: element (r, n, i) of lane is row 16 r + 8 (i / 2) + g, pair 8 n + 2 t + i % 2
+        if (p.kw > 1) {
+            float *mine = part + warp * NB * 256;
+            barrier(1 + rw, p.kw * 32);  // the last item's sums are read
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                    reinterpret_cast<float4 *>(mine)[(r * NB + n) * 32 + lane] =
+                        make_float4(total[r][n][0], total[r][n][1], total[r][n][2], total[r][n][3]);
+            barrier(1 + rw, p.kw * 32);
+            const float *all = part + rw * p.kw * NB * 256;
+            if (there)
+                for (int v = kw * 32 + lane; v < NB * 128; v += p.kw * 32) {
+                    float a = 0.0f, b = 0.0f;
+                    for (int w = 0; w < p.kw; ++w) {
+                        a += all[w * NB * 256 + v];
+                        b += all[w * NB * 256 + NB * 128 + v];
+                    }
+                    const int i = v & 3, l = (v >> 2) & 31, n = v >> 7;
+                    const int col = 8 * n + 2 * (l & 3) + (i & 1);
+                    const int64_t row = row0 + 8 * (i >> 1) + (l >> 2);
+                    const int to = dst[col];
+                    if (to < 0) continue;
+                    if constexpr (GEGLU) {
+                        if (row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, gelu(a) * b);
+                    } else {
+                        if (row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, a);
+                        if (row + 16 < p.n) put(p.out, to * p.out_stride + row + 16, p.out_bf16, b);
+                    }
+                }
+        } else if (there) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int to = dst[8 * n + 2 * t + (i & 1)];
+                    const int64_t row = row0 + 8 * (i >> 1) + g;
+                    if (to < 0) continue;
+                    if constexpr (GEGLU) {
+                        if (row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, gelu(total[0][n][i]) * total[1][n][i]);
+                    } else {
+                        if (row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, total[0][n][i]);
+                        if (row + 16 < p.n) put(p.out, to * p.out_stride + row + 16, p.out_bf16, total[1][n][i]);
+                    }
+                }
+        }
+    }
+    copy_wait<0>();
+}
+
+constexpr int kSharedLimit = 232448 - 256;  // beside the kernel's own
+
+template <bool EXACT, int PARTS, int NB, bool GEGLU, bool ALIGNED>
+cudaError_t launch_stream(StreamParams p, cudaStream_t stream) {
+    using L = StreamLayout<EXACT, PARTS, NB, ALIGNED>;
+    static int limits[kMaxDevices];
+    // as many warps as fit beside all of x, four at least, and x in panels beyond that
+    int warps = kMaxWarps;
+    p.x_panel = p.chunks;
+    while (warps > 4 && L::total(warps, p.x_panel) > kSharedLimit) warps -= 4;
+    while (L::total(warps, p.x_panel) > kSharedLimit) --p.x_panel;
+    p.kw = std::min(p.chunks, std::min(warps, 8));
+    p.rw = warps / p.kw;
+    warps = p.rw * p.kw;
+    constexpr int rows = GEGLU ? 16 : 32;
+    p.row_groups = static_cast<int>((p.n + rows * p.rw - 1) / (rows * p.rw));
+    const int smem = L::total(warps, p.x_panel);
+    const cudaError_t e = ensure_smem(stream_kernel<EXACT, PARTS, NB, GEGLU, ALIGNED>, smem, false, limits);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(stream_kernel<EXACT, PARTS, NB, GEGLU, ALIGNED>, dim3(device_sm_count()), dim3(warps * 32), smem, stream,
+                         1, p);
+}
+
+template <bool GEGLU, bool ALIGNED, int NB>
+cudaError_t launch_precision(const StreamParams &p, bool exact, cudaStream_t stream) {
+    if (!exact) return launch_stream<false, 1, NB, GEGLU, ALIGNED>(p, stream);
+    return p.x_bf16 ? launch_stream<true, 1, NB, GEGLU, ALIGNED>(p, stream) : launch_stream<true, 2, NB, GEGLU, ALIGNED>(p, stream);
+}
+
+// exact: fp32 results (see above).  Groups of 16 pairs where the experts have
+// more than eight on average.
+template <bool GEGLU>
+cudaError_t launch_form(StreamParams &p, bool exact, cudaStream_t stream) {
+    p.blocks = static_cast<int>(p.k / kQK);
+    p.chunks = (p.blocks + 7) / 8;
+    p.row_bytes = static_cast<int64_t>(p.blocks) * kQ4_0Bytes;
+    p.matrix_bytes = p.row_bytes * p.n;
+    p.w_bytes = p.matrix_bytes * p.plan.experts;
+    p.magic = 0x64006400u;
+    p.x_wide = reinterpret_cast<uintptr_t>(p.x) % (p.x_bf16 ? 8 : 16) == 0 && p.x_stride % 4 == 0;  // loads of four
+    const bool aligned = p.k % kChunk == 0;
+    const bool many = p.plan.pairs_total > 8 * static_cast<int64_t>(p.plan.experts);
+    if (aligned)
+        return many ? launch_precision<GEGLU, true, 2>(p, exact, stream) : launch_precision<GEGLU, true, 1>(p, exact, stream);
+    return many ? launch_precision<GEGLU, false, 2>(p, exact, stream) : launch_precision<GEGLU, false, 1>(p, exact, stream);
+}
+
+}  // namespace experts
+}  // namespace qmm

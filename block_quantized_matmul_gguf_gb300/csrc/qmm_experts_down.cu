@@ -1,0 +1,83 @@
+// qmm_experts_down.cu -- the streaming form's down projections
+// (qmm_experts.cuh) and the weighted sums of a token's experts.
+#include "qmm_experts.cuh"
+
+namespace qmm {
+namespace {
+
+// y[t] = sum_r weights[t][r] z[t topk + r] over the r whose expert is there, in
+// their order.  V columns a thread.  Bound by the bytes of z, which the
+// projections left in L2 where it fits.
+struct SumParams {
+    const float *z;
+    const int32_t *ids;
+    const float *weights;
+    void *y;
+    int64_t y_stride, tokens, n;
+    int experts, topk;
+    bool bf16;
+};
+
+template <int V>
+__global__ void __launch_bounds__(256) sum_kernel(SumParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t per = (p.n + V - 1) / V, all = per * p.tokens;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t t = i / per, col = (i - t * per) * V;
+        float sum[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+#pragma unroll 4
+        for (int r = 0; r < p.topk; ++r) {
+            const int64_t pair = t * p.topk + r;
+            const int id = p.ids[pair];
+            if (id < 0 || id >= p.experts) continue;
+            const float w = p.weights[pair];
+            const float *z = p.z + pair * p.n + col;
+            if constexpr (V == 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(z);
+                sum[0] = fmaf(w, f.x, sum[0]);
+                sum[1] = fmaf(w, f.y, sum[1]);
+                sum[2] = fmaf(w, f.z, sum[2]);
+                sum[3] = fmaf(w, f.w, sum[3]);
+            } else {
+                sum[0] = fmaf(w, z[0], sum[0]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) experts::put(p.y, t * p.y_stride + col + v, p.bf16, sum[v]);
+    }
+}
+
+}  // namespace
+
+size_t experts_down_workspace_bytes(int64_t tokens, int topk, int64_t n) {
+    return static_cast<size_t>(tokens) * topk * n * sizeof(float);
+}
+
+cudaError_t launch_experts_down(const ExpertsDown &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    experts::StreamParams p = {};
+    p.plan = a.plan;
+    p.w[0] = p.w[1] = a.wd;
+    p.x = a.h;
+    p.x_stride = a.h_stride;
+    p.x_bf16 = a.h_bf16;
+    p.out = a.workspace;
+    p.out_stride = a.n;
+    p.out_bf16 = false;
+    p.n = a.n;
+    p.k = a.k;
+    p.ctx = ctx;
+    const cudaError_t e = experts::launch_form<false>(p, !a.y_bf16, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t tokens = a.plan.pairs_total / a.plan.topk;
+    const SumParams s = {static_cast<const float *>(a.workspace), a.ids, a.weights, a.y, a.y_stride, tokens, a.n, a.plan.experts,
+                         a.plan.topk, a.y_bf16};
+    const bool wide = a.n % 4 == 0;  // the workspace is aligned
+    const int64_t threads = tokens * (wide ? a.n / 4 : a.n);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((threads + 255) / 256, static_cast<int64_t>(device_sm_count()) * 8));
+    return launch_kernel(wide ? sum_kernel<4> : sum_kernel<1>, dim3(grid), dim3(256), 0, stream, 1, s);
+}
+
+}  // namespace qmm

@@ -319,6 +319,36 @@ constexpr int kMaxExperts = 1024, kMaxTopk = 32, kMaxGroups = 32;
 size_t route_workspace_bytes(int64_t tokens, int experts);
 cudaError_t launch_route(const RouteArgs &args, cudaStream_t stream, const LaunchCtx &ctx);
 
+// Which pairs (token * topk + r) each expert has, as routing left them.
+struct ExpertsPlan {
+    const int32_t *expert_start, *pairs;
+    int64_t pairs_total;  // tokens * topk
+    int experts, topk;
+};
+
+struct ExpertsGeglu {
+    ExpertsPlan plan;
+    const uint8_t *wg, *wu;
+    const void *x;
+    void *h;
+    int64_t x_stride, h_stride, n, k;
+    bool x_bf16, h_bf16;
+};
+cudaError_t launch_experts_geglu(const ExpertsGeglu &args, cudaStream_t stream, const LaunchCtx &ctx);
+
+struct ExpertsDown {
+    ExpertsPlan plan;
+    const uint8_t *wd;
+    const void *h;
+    const int32_t *ids;
+    const float *weights;
+    void *y, *workspace;
+    int64_t h_stride, y_stride, n, k;
+    bool h_bf16, y_bf16;
+};
+size_t experts_down_workspace_bytes(int64_t tokens, int topk, int64_t n);
+cudaError_t launch_experts_down(const ExpertsDown &args, cudaStream_t stream, const LaunchCtx &ctx);
+
 cudaError_t launch_selftest_wait(cudaStream_t stream, const LaunchCtx &ctx);
 
 }  // namespace qmm

@@ -40,6 +40,7 @@ EXPORTED = (
     "qmm_set_wait_timeout_ns", "qmm_selftest_wait_timeout", "qmm_copy",
     "qmm_kv_plan", "qmm_kv_append_q4_0", "qmm_kv_append_rope_q4_0", "qmm_kv_read_q4_0",
     "qmm_route", "qmm_route_workspace_bytes",
+    "qmm_experts_geglu_q4_0", "qmm_experts_down_q4_0", "qmm_experts_down_workspace_bytes",
     "qmm_attn_q4_0_workspace_bytes", "qmm_attn_q4_0", "qmm_logits_adjust",
 )
 
@@ -87,6 +88,12 @@ class RouteArgs(ctypes.Structure):
                 ("renormalize", ctypes.c_int), ("scale", ctypes.c_float), ("ids", ctypes.c_void_p),
                 ("weights", ctypes.c_void_p), ("expert_start", ctypes.c_void_p), ("pairs", ctypes.c_void_p),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class ExpertPlan(ctypes.Structure):
+    """struct qmm_expert_plan."""
+    _fields_ = [("tokens", ctypes.c_int64), ("topk", ctypes.c_int), ("experts", ctypes.c_int),
+                ("expert_start", ctypes.c_void_p), ("pairs", ctypes.c_void_p)]
 
 
 class LogitsArgs(ctypes.Structure):
@@ -152,6 +159,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "qmm_kv_append_rope_q4_0": [P, P, P],
         "qmm_kv_read_q4_0": [P, P, I64, P, P, P],
         "qmm_route": [P, P],
+        "qmm_experts_geglu_q4_0": [P, P, P, P, I64, I32, P, I64, I32, I64, I64, P],
+        "qmm_experts_down_q4_0": [P, P, P, I64, I32, P, P, P, I64, I32, I64, I64, P, SZ, P],
         "qmm_attn_q4_0": [P, P, P],
         "qmm_logits_adjust": [P, P],
     }
@@ -168,6 +177,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         getattr(lib, name).restype = SZ
     lib.qmm_attn_q4_0_workspace_bytes.argtypes = [P, I32]
     lib.qmm_attn_q4_0_workspace_bytes.restype = SZ
+    lib.qmm_experts_down_workspace_bytes.argtypes = [I64, I32, I64]
+    lib.qmm_experts_down_workspace_bytes.restype = SZ
     lib.qmm_route_workspace_bytes.argtypes = [I64, I32]
     lib.qmm_route_workspace_bytes.restype = SZ
     lib.qmm_set_wait_timeout_ns.argtypes = [U64]
@@ -524,6 +535,7 @@ def attn_workspace(cache: KvCacheQ4_0, heads: int):
 _ATTN_ARGS = struct.Struct("@PqiPqiPPqPPiqiifiiPN")
 _LOGITS_ARGS = struct.Struct("@PqPqqqPPqPPPPPPPqP")
 _ROPE_ARGS = struct.Struct("@PqPqiPqPqiPPqPqii")
+_EXPERT_PLAN = struct.Struct("@qiiPP")
 _ROUTE_ARGS = struct.Struct("@PqiPPqiiiiiiifPPPPPN")
 
 
@@ -629,6 +641,77 @@ def qmm_route(logits, ids, weights, expert_start, pairs, bias=None, score: str =
                             _typed(expert_start, i32, "expert_start"), _typed(pairs, i32, "pairs"), _ptr(workspace),
                             workspace.numel() * workspace.element_size())
     _check((_lib or load()).qmm_route(args, _stream(stream)), "qmm_route")
+
+
+def _matrix_rows(t, width: int, what: str):
+    """(pointer, row stride, qmm_dtype) of [n][width] whose rows may lie apart."""
+    dtype = t.dtype
+    if dtype is _torch.float32:
+        kind = QMM_F32
+    elif dtype is _torch.bfloat16:
+        kind = QMM_BF16
+    else:
+        raise ValueError(f"{what} must be float32 or bfloat16")
+    n, w = t.shape
+    row, one = t.stride()
+    if w != width or (one != 1 and width > 1):
+        raise ValueError(f"{what} must be [rows][{width}] with dense rows")
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    return t.data_ptr(), (row if n > 1 else width), kind
+
+
+def _expert_weights(w, experts: int, n: int, k: int, what: str) -> int:
+    if w.numel() * w.element_size() != experts * n * (k // 32) * 18:
+        raise ValueError(f"{what} must hold Q4_0 blocks of [{experts}][{n}][{k}]")
+    return _ptr(w)
+
+
+def experts_workspace(tokens: int, topk: int, n: int, device="cuda"):
+    """A workspace for the down projections of up to so many tokens (calls that overlap on the GPU need their own)."""
+    import torch
+    need = int(load().qmm_experts_down_workspace_bytes(tokens, topk, n))
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+
+
+def qmm_experts_geglu_q4_0(wg, wu, x, h, expert_start, pairs, topk: int, n: int, k: int, stream=None) -> None:
+    """h[i] = gelu(x wg^T) * (x wu^T) of each pair's token and expert, in the order of pairs, from x
+    [tokens][k] (fp32 or bf16) into h [tokens * topk][n] (fp32 or bf16)."""
+    i32 = _torch_module().int32
+    tokens, experts = x.shape[0], expert_start.numel() - 1
+    xp, xs, x_type = _matrix_rows(x, k, "x")
+    hp, hs, h_type = _matrix_rows(h, n, "h")
+    if h.shape[0] != tokens * topk or pairs.numel() != tokens * topk:
+        raise ValueError("h and pairs must have tokens * topk rows")
+    plan = _EXPERT_PLAN.pack(tokens, topk, experts, _typed(expert_start, i32, "expert_start"), _typed(pairs, i32, "pairs"))
+    status = (_lib or load()).qmm_experts_geglu_q4_0(
+        plan, _expert_weights(wg, experts, n, k, "wg"), _expert_weights(wu, experts, n, k, "wu"), xp, xs, x_type, hp, hs,
+        h_type, n, k, _stream(stream))
+    _check(status, "qmm_experts_geglu_q4_0")
+
+
+def qmm_experts_down_q4_0(wd, h, y, ids, weights, expert_start, pairs, n: int, k: int, workspace=None, stream=None) -> None:
+    """y[t] = sum_r weights[t][r] * (h wd^T) of token t's pairs, from h [tokens * topk][k] in the order of
+    pairs (fp32 or bf16) into y [tokens][n] (fp32 or bf16).  Without a workspace it takes one from the
+    memory of the stream it runs on."""
+    torch = _torch_module()
+    i32 = torch.int32
+    tokens, topk = ids.shape
+    experts = expert_start.numel() - 1
+    hp, hs, h_type = _matrix_rows(h, k, "h")
+    yp, ys, y_type = _matrix_rows(y, n, "y")
+    if h.shape[0] != tokens * topk or pairs.numel() != tokens * topk or tuple(weights.shape) != (tokens, topk) or \
+            y.shape[0] != tokens:
+        raise ValueError("h and pairs must have tokens * topk rows, weights the shape of ids, y a row for each token")
+    if workspace is None:
+        with torch.cuda.stream(_stream_object(stream)):  # as for attention
+            workspace = experts_workspace(tokens, topk, n, y.device)
+    plan = _EXPERT_PLAN.pack(tokens, topk, experts, _typed(expert_start, i32, "expert_start"), _typed(pairs, i32, "pairs"))
+    status = (_lib or load()).qmm_experts_down_q4_0(
+        plan, _expert_weights(wd, experts, n, k, "wd"), hp, hs, h_type, _typed(ids, i32, "ids"),
+        _typed(weights, torch.float32, "weights"), yp, ys, y_type, n, k, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(status, "qmm_experts_down_q4_0")
 
 
 # ---- tensor-level conveniences (allocate the output, then call the ABI) ----

@@ -549,6 +549,55 @@ typedef struct qmm_route_args {
 size_t qmm_route_workspace_bytes(int64_t tokens, int experts);
 qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
 
+/* ---- The experts' products ------------------------------------------------
+ * Each expert e has Q4_0 matrices, one after the other: wg, wu [experts][n][k]
+ * (gate and up, k the hidden size) and wd [experts][n][k] (down, n the hidden
+ * size), n rows of k / 32 blocks.  The plan is what qmm_route leaves: entry i of
+ * `pairs` with expert_start[e] <= i < expert_start[e + 1] is pair t * topk + r of
+ * token t, to be worked by expert e.
+ *   geglu  h[i] = gelu(x[t] wg_e^T) * (x[t] wu_e^T), row i in the order of
+ *          `pairs`; x [tokens] rows of k, h [tokens * topk] rows of n; the GELU
+ *          of qmm_gemv_q4_0_geglu.  Rows from expert_start[experts] on are left
+ *          as they were.
+ *   down   y[t] = sum_r weights[t][r] * (h[i] wd_e^T), i the entry of pair
+ *          t * topk + r, over the r with 0 <= ids[t][r] < experts, in their
+ *          order; a token without any gets 0.
+ * Strides count elements; x_type, h_type and y_type may differ.
+ * Arithmetic: sums in fp32.  With an fp32 output the weights are exact, a bf16
+ * input too, and an fp32 input enters in two binary16 parts (22 bits of it, and
+ * 2^-39 of the largest of its row's 256 values around it).  With a bf16 output
+ * an fp32 input enters in 11 bits.  A row of x or h that holds an infinity or a
+ * NaN gives NaN.  Which form a call takes depends on its host-side arguments
+ * alone; equal calls give equal bits, and a pair's row depends on no other pair.
+ * Entries outside their arrays (an expert_start that descends or leaves
+ * 0 .. tokens * topk, a pair outside 0 .. tokens * topk - 1) record
+ * QMM_ERR_INDEX; what they concern is left out.
+ *   workspace  16-byte aligned device memory of at least
+ *              qmm_experts_down_workspace_bytes() bytes, scratch of the call
+ * Requires tokens >= 0 (0 launches nothing), 1 <= topk <= 32, experts <= 1024,
+ * n >= 1, k % 32 == 0, weights 16-byte aligned, other pointers aligned to their
+ * type, strides at least the rows' widths; n <= 2^24, k <= 2^20 and at most
+ * 2^30 pairs (else QMM_ERR_UNSUPPORTED).  Outputs and the workspace must
+ * overlap no input and not each other. */
+typedef struct qmm_expert_plan {
+    int64_t tokens;
+    int topk;
+    int experts;
+    const int32_t *expert_start;
+    const int32_t *pairs;
+} qmm_expert_plan;
+
+qmm_status qmm_experts_geglu_q4_0(const qmm_expert_plan *plan, const void *wg, const void *wu,
+                                  const void *x, int64_t x_stride, qmm_dtype x_type, void *h,
+                                  int64_t h_stride, qmm_dtype h_type, int64_t n, int64_t k,
+                                  qmm_stream_t stream);
+size_t qmm_experts_down_workspace_bytes(int64_t tokens, int topk, int64_t n);
+qmm_status qmm_experts_down_q4_0(const qmm_expert_plan *plan, const void *wd, const void *h,
+                                 int64_t h_stride, qmm_dtype h_type, const int32_t *ids,
+                                 const float *weights, void *y, int64_t y_stride, qmm_dtype y_type,
+                                 int64_t n, int64_t k, void *workspace, size_t workspace_bytes,
+                                 qmm_stream_t stream);
+
 /* ---- Penalties, biases and grammar masks on logits ----------------------
  * out[i][t] for i < rows, t < vocab, from x = logits[i][t]:
  *   1. repetition: where t occurs in row i's history, x > 0 ? x / r : x * r

@@ -71,3 +71,89 @@ def route(logits, bias, topk, score, groups=1, group_topk=1, group_best=1, renor
 # |l - top| at most 40 in the tests; their quotient by a sum by twice that and
 # 10 roundings.  2 (8 + 40 + 40) + 10 < 2^8 units of 2^-24.
 WEIGHT = 2.0 ** -16
+
+
+def blocks(rng, *shape, lo=0.001, hi=0.02):
+    """Random Q4_0 blocks uint8 [..., k/32*18] for weights of shape [..., k]."""
+    *front, k = shape
+    b = rng.integers(0, 256, (*front, k // 32, 18), dtype=np.uint8)
+    d = rng.uniform(lo, hi, (*front, k // 32)).astype(np.float16)
+    b[..., 0:2] = d[..., None].view(np.uint8)
+    return b.reshape(*front, -1)
+
+
+def matrix(b):
+    """float64 weights [..., k], and the scale times (n + 8) of each."""
+    b = b.reshape(*b.shape[:-1], -1, 18)
+    d = np.ascontiguousarray(b[..., :2]).view(np.float16).astype(np.float64)
+    n = np.concatenate([b[..., 2:] & 15, b[..., 2:] >> 4], -1).astype(np.float64)
+    flat = (*b.shape[:-2], -1)
+    return ((n - 8) * d).reshape(flat), (np.abs(d) * (n + 8)).reshape(flat)
+
+
+def gelu(z):
+    return z / 2 * (1 + np.tanh(np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)))
+
+
+def product(x, b, exact, rounded_x):
+    """x [rows][k] times the transpose of a matrix of blocks, and the bound of
+    the kernels' error.  With S = sum |w x| and T = sum d (n + 8) |x|:
+      exact weights (fp32 results): x in two binary16 parts 2^-22, sums of 16
+        products in the tensor cores 2^-19 (17 addends cut at 2^-23), up to 272
+        roundings of block sums and parts 2^-15.9: under 2^-15 S; and of what
+        binary16 cannot reach, 2^-38 of the row's largest x for each weight
+      bf16 results: an fp32 x in 11 bits, half a step 2^-11; in the streaming
+        form sums of subnormal codes that keep 18 bits, 34 addends of T, under
+        2^-12 T; in the tile form each weight rounded to bf16, half a step 2^-8 S
+    """
+    w, wide = matrix(b)
+    a = np.abs(x)
+    s = a @ np.abs(w).T
+    reach = 2.0 ** -38 * a.max(-1, keepdims=True) * np.abs(w).sum(-1)
+    if exact:
+        return x @ w.T, s * 2.0 ** -15 + reach
+    return x @ w.T, s * (2.0 ** -15 + 2.0 ** -8 + (2.0 ** -11 if rounded_x else 0.0)) + a @ wide.T * 2.0 ** -12 + reach
+
+
+def geglu(x, bg, bu, exact, rounded_x):
+    """h and its bound: |gelu'| <= 1.13, the GELU's own evaluation 2^-20 (1 + g^2)."""
+    (g, eg), (u, eu) = product(x, bg, exact, rounded_x), product(x, bu, exact, rounded_x)
+    h = gelu(g) * u
+    return h, (1.13 * np.abs(u) * eg + np.abs(gelu(g)) * eu + 1.13 * eg * eu + 2.0 ** -20 * (1 + g * g) * np.abs(h)
+               + (0.0 if exact else 2.0 ** -8 * np.abs(h)) + 1e-37)
+
+
+def plan_of(ids, experts):
+    """expert_start and pairs of ids [tokens][topk], -1 where there is none."""
+    flat = ids.reshape(-1)
+    there = np.flatnonzero(flat >= 0)
+    pairs = np.full(flat.size, -1, dtype=np.int32)
+    pairs[:there.size] = there[np.argsort(flat[there], kind="stable")]
+    return np.concatenate([[0], np.bincount(flat[there], minlength=experts).cumsum()]).astype(np.int32), pairs
+
+
+def experts_geglu(x, bg, bu, starts, pairs, topk, exact, rounded_x):
+    n = bg.shape[1]
+    h, limit = np.zeros((pairs.size, n)), np.zeros((pairs.size, n))
+    for e in range(starts.size - 1):
+        rows = slice(starts[e], starts[e + 1])
+        if rows.start < rows.stop:
+            h[rows], limit[rows] = geglu(x[pairs[rows] // topk], bg[e], bu[e], exact, rounded_x)
+    return h, limit
+
+
+def experts_down(h, bd, ids, weights, starts, pairs, exact, rounded_x):
+    """y and its bound: the projections' own bounds weighted; the weighted sum
+    rounds at most 33 times; z is rounded to bf16 once in the tile form."""
+    t, topk = ids.shape
+    n = bd.shape[1]
+    y, limit = np.zeros((t, n)), np.zeros((t, n))
+    w = weights.astype(np.float64).reshape(-1)
+    for e in range(starts.size - 1):
+        for i in range(starts[e], starts[e + 1]):
+            z, ez = product(h[i:i + 1], bd[e], exact, rounded_x)
+            p = pairs[i]
+            if 0 <= ids.reshape(-1)[p] < starts.size - 1:
+                y[p // topk] += w[p] * z[0]
+                limit[p // topk] += np.abs(w[p]) * (ez[0] + np.abs(z[0]) * (33 * 2.0 ** -24 + (0.0 if exact else 2.0 ** -8)))
+    return y, limit + (0.0 if exact else 2.0 ** -8 * np.abs(y)) + 1e-37
