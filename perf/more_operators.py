@@ -211,7 +211,7 @@ def prepare(case, seed):
         if case["op"] == "route":
             s["workspace"] = _qmm().route_workspace(case["tokens"], case["experts"])
         if case["op"] == "down":
-            s["workspace"] = _qmm().experts_workspace(case["tokens"], case["topk"], case["n"])
+            s["workspace"] = _qmm().experts_workspace(case["tokens"], case["topk"], case["n"], case["k"])
     return s
 
 
