@@ -731,9 +731,16 @@ size_t experts_bytes(const ExpertsPlan &p, int64_t n, int64_t k) {
 
 }  // namespace
 
+size_t qmm_experts_geglu_workspace_bytes(int64_t tokens, int topk, int experts, int64_t k) {
+    if (tokens < 1 || topk < 1 || topk > kMaxTopk || experts < 1 || experts > kMaxExperts || tokens > kMaxRows / topk ||
+        k < kQK || k > kExpertsMaxK || !experts_are_many(tokens * topk, experts))
+        return 0;
+    return experts_rows_bytes(tokens * topk, k);
+}
+
 qmm_status qmm_experts_geglu_q4_0(const qmm_expert_plan *plan, const void *wg, const void *wu, const void *x, int64_t x_stride,
                                   qmm_dtype x_type, void *h, int64_t h_stride, qmm_dtype h_type, int64_t n, int64_t k,
-                                  qmm_stream_t stream) {
+                                  void *workspace, size_t workspace_bytes, qmm_stream_t stream) {
     ExpertsPlan p;
     qmm_status s = check_experts(plan, wg, n, k, &p);
     if (s == QMM_OK) s = check_experts(plan, wu, n, k, &p);
@@ -743,22 +750,29 @@ qmm_status qmm_experts_geglu_q4_0(const qmm_expert_plan *plan, const void *wg, c
     if (p.pairs_total == 0) return QMM_OK;
     if (!x || !h) return QMM_ERR_NULL;
     if (!aligned(x, dtype_bytes(x_type)) || !aligned(h, dtype_bytes(h_type))) return QMM_ERR_ALIGN;
+    const size_t need = workspace ? qmm_experts_geglu_workspace_bytes(plan->tokens, p.topk, p.experts, k) : 0;
+    if (need) {
+        s = check_workspace(workspace, workspace_bytes, need);
+        if (s != QMM_OK) return s;
+    }
     const size_t wbytes = experts_bytes(p, n, k);
     const Range ins[] = {{wg, wbytes}, {wu, wbytes}, {x, rows_bytes(plan->tokens, x_stride, k, dtype_bytes(x_type))},
                          {p.expert_start, 4 * (static_cast<size_t>(p.experts) + 1)},
                          {p.pairs, 4 * static_cast<size_t>(p.pairs_total)}};
-    const Range outs[] = {{h, rows_bytes(p.pairs_total, h_stride, n, dtype_bytes(h_type))}};
-    if (!outputs_clear(outs, 1, ins, 5)) return QMM_ERR_UNSUPPORTED;
+    const Range outs[] = {{h, rows_bytes(p.pairs_total, h_stride, n, dtype_bytes(h_type))}, {workspace, need}};
+    if (!outputs_clear(outs, 2, ins, 5)) return QMM_ERR_UNSUPPORTED;
     LaunchCtx ctx;
     if (!make_ctx(&ctx)) return QMM_ERR_CUDA;
-    const ExpertsGeglu a = {p, static_cast<const uint8_t *>(wg), static_cast<const uint8_t *>(wu), x, h, x_stride, h_stride, n, k,
-                            x_type == QMM_BF16, h_type == QMM_BF16};
+    const ExpertsGeglu a = {p, static_cast<const uint8_t *>(wg), static_cast<const uint8_t *>(wu), x, h, need ? workspace : nullptr,
+                            x_stride, h_stride, n, k, x_type == QMM_BF16, h_type == QMM_BF16};
     return from_cuda(launch_experts_geglu(a, reinterpret_cast<cudaStream_t>(stream), ctx));
 }
 
-size_t qmm_experts_down_workspace_bytes(int64_t tokens, int topk, int64_t n) {
-    if (tokens < 1 || topk < 1 || topk > kMaxTopk || tokens > kMaxRows / topk || n < 1 || n > kExpertsMaxN) return 0;
-    return experts_down_workspace_bytes(tokens, topk, n);
+size_t qmm_experts_down_workspace_bytes(int64_t tokens, int topk, int64_t n, int64_t k) {
+    if (tokens < 1 || topk < 1 || topk > kMaxTopk || tokens > kMaxRows / topk || n < 1 || n > kExpertsMaxN || k < kQK ||
+        k > kExpertsMaxK)
+        return 0;
+    return experts_down_workspace_bytes(tokens * topk, n, k);
 }
 
 qmm_status qmm_experts_down_q4_0(const qmm_expert_plan *plan, const void *wd, const void *h, int64_t h_stride, qmm_dtype h_type,
@@ -773,7 +787,7 @@ qmm_status qmm_experts_down_q4_0(const qmm_expert_plan *plan, const void *wd, co
     if (!h || !ids || !weights || !y || !workspace) return QMM_ERR_NULL;
     if (!aligned(h, dtype_bytes(h_type)) || !aligned(y, dtype_bytes(y_type)) || !aligned(ids, 4) || !aligned(weights, 4))
         return QMM_ERR_ALIGN;
-    const size_t need = experts_down_workspace_bytes(plan->tokens, p.topk, n);
+    const size_t need = experts_down_workspace_bytes(p.pairs_total, n, k);
     s = check_workspace(workspace, workspace_bytes, need);
     if (s != QMM_OK) return s;
     const size_t list = 4 * static_cast<size_t>(p.pairs_total);

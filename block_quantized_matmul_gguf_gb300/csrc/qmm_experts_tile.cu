@@ -1,0 +1,551 @@
+// qmm_experts_tile.cu -- the experts' Q4_0 products for many rows an expert
+// (prompts, batches of requests), bf16 in and out, on tcgen05 tiles.
+//
+// Mathematics.  Y^T = W_e X_e^T for each expert e and the rows X_e of its pairs.  A
+// first kernel writes those rows in the pairs' order as binary16, scaled by a power
+// of two per row so that the largest value lies in [2^14, 2^15): a bf16 value keeps
+// all its bits down to 2^-29 of the row's largest, and loses what lies below 2^-39 of
+// it.  Each weight w = (n - 8) d is rounded once to binary16 (half a step is 2^-12 of
+// it; beside a bf16 weight's 2^-9 that leaves the output's own rounding the only one
+// that shows: error against 64 bits 1.7e-3 for 2.9e-3) and products are summed in fp32
+// in tensor memory; the epilogue takes the row's power of two out again.  Scales
+// above 8188, whose weights binary16 cannot hold, give infinities here.
+//
+// Structure, as of the prefill GEMM: persistent CTA pairs; a tile is 256 weight rows
+// (128 gate and the same 128 up rows for GeGLU) by up to 128 of an expert's rows,
+// tcgen05.mma.cta_group::2, the weights in tensor memory, x in shared memory.  An
+// expert's rows are cut into equal tiles of a multiple of 32, so that the
+// instruction's N follows the rows that are there.  Two accumulators: one is read out
+// while the next tile's products run.
+//   warp 0      x producer (both CTAs): boxes of 16 rows x 64 values, a lane each
+//   warp 1      MMA issuer (one thread of the leader)
+//   warp 2      weight producer (both CTAs): boxes of 128 rows x 144 bytes
+//   warps 4-7   epilogue
+//   warps 8-23  dequantisers: TMEM lanes 32 (w % 4) .., every fourth 64-wide K stage.
+//               A stage's weights are formed in registers before its slot is waited
+//               for, so that a free slot is filled at once.
+// The binary16 pairs that a word of codes gives without moving its nibbles are
+// values 0 and 2, 1 and 3, so x is written in that order of K too.
+// Which items (expert, tile, row block) there are depends on expert_start: each CTA
+// forms the prefix sums of the experts' tiles in shared memory, and every role finds
+// its pair's items in them by bisection.
+// Every wait is bounded, as in the prefill GEMM.
+#include "qmm_internal.h"
+#include "qmm_tc.cuh"
+
+#include <algorithm>
+
+namespace qmm {
+namespace {
+
+constexpr int BW = 128;      // weight rows of a CTA
+constexpr int BT = 128;      // rows of x in a tile, at most
+constexpr int BK = 64;       // K of a stage
+constexpr int RAW_K = 256;   // K of a raw stage
+constexpr int STAGES = 8;
+constexpr int GROUP = 4;     // stages announced to the MMA thread at once
+constexpr int NGROUPS = STAGES / GROUP;
+constexpr int RAW_STAGES = 6;
+constexpr int X_STAGE_BYTES = BT / 2 * BK * 2;
+constexpr int RAW_ROW = 144;
+constexpr int RAW_STAGE_BYTES = BW * RAW_ROW;
+constexpr uint32_t D_COLS = 2 * BT, A_COLS = BK / 2, TMEM_COLS = 512;  // two accumulators
+static_assert(D_COLS + STAGES * A_COLS <= TMEM_COLS, "tensor memory");
+static_assert(RAW_K / BK % GROUP == 0, "a tile is whole groups");
+
+constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_EPI = 4, EPI_WARPS = 4, WARP_DEQ = 8, DEQ_WARPS = 16;
+constexpr int DEQ_STAGE_WARPS = 4;  // that write one K stage
+constexpr int THREADS = (WARP_DEQ + DEQ_WARPS) * 32;
+constexpr int X_BOX = 16;           // rows of a copy of x
+
+struct Smem {
+    static constexpr int x = 0;
+    static constexpr int raw = STAGES * X_STAGE_BYTES;
+    static constexpr int bars = raw + RAW_STAGES * RAW_STAGE_BYTES;
+    static constexpr int nbars = NGROUPS + STAGES + 2 * RAW_STAGES + 5;
+    static constexpr int tmem_slot = bars + nbars * 8;
+    static constexpr int abort_flag = tmem_slot + 4;
+    static constexpr int tiles = abort_flag + 4;  // [experts + 1] tiles in front of each expert's
+    static int total(int experts) { return tiles + (experts + 1) * 4 + 1024; }
+};
+static_assert(Smem::tiles + (kMaxExperts + 1) * 4 + 1024 <= 232448 - 256, "shared memory of a CTA");
+
+struct TileParams {
+    ExpertsPlan plan;
+    const float *unit;   // power of two of each row of x
+    uint16_t *out;       // GeGLU: h by the pairs' order; down: z by the pair
+    int64_t out_stride;
+    int n, k;
+    int row_blocks;      // of a matrix: of 256 rows (down) or 128 features
+    uint32_t magic;      // 1024, 1024 in binary16, in a register
+    LaunchCtx ctx;
+};
+
+// One item: rows first .. first + cols - 1 of the sorted pairs of `expert`.
+struct Item {
+    int expert, row_block, first, cols, width;  // width: cols up to a multiple of 32
+};
+
+__device__ __forceinline__ int expert_count(const TileParams &p, int e, int &start) {
+    const int64_t a = p.plan.expert_start[e], b = p.plan.expert_start[e + 1];
+    if (a < 0 || b < a || b > p.plan.pairs_total) {
+        record_error(p.ctx, kDevErrIndex);
+        start = 0;
+        return 0;
+    }
+    start = static_cast<int>(a);
+    return static_cast<int>(b - a);
+}
+
+__device__ __forceinline__ Item item_at(const TileParams &p, const int *tiles, int item) {
+    Item it;
+    const int tile = item / p.row_blocks;
+    it.row_block = item - tile * p.row_blocks;
+    int lo = 0, hi = p.plan.experts;  // tiles[lo] <= tile < tiles[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tiles[mid] <= tile)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    it.expert = lo;
+    int start;
+    const int count = expert_count(p, lo, start), parts = tiles[lo + 1] - tiles[lo];
+    const int per = ((count + parts - 1) / parts + 31) & ~31;
+    const int at = (tile - tiles[lo]) * per;
+    it.first = start + at;
+    it.cols = max(0, min(per, count - at));
+    it.width = max(32, (it.cols + 31) & ~31);
+    return it;
+}
+
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+// (n - 8) d of a word's eight codes: values 0 and 2, 1 and 3, 16 and 18, 17 and 19
+// of the block's quarter.
+__device__ __forceinline__ void weights_of(uint32_t q, uint32_t d, uint32_t magic, uint32_t *w) {
+    const uint32_t q8 = q >> 8;
+    w[0] = hmul2(hadd2((q & 0x000F000Fu) | magic, 0xE408E408u), d);                  // - 1032
+    w[1] = hmul2(hadd2((q8 & 0x000F000Fu) | magic, 0xE408E408u), d);
+    w[2] = hmul2(hfma2((q & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u), d);     // / 16 - 72
+    w[3] = hmul2(hfma2((q8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u), d);
+}
+
+// 32 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+// D fp32, A and B binary16, both K-major, M = 256; N goes in at run time.
+constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>((2 * BW) >> 4) << 24);
+
+// G: GeGLU.  A CTA's 128 accumulator rows are then 64 features: in lane quarter q,
+// lanes 0-15 hold the gate rows of features 16q .. 16q+15, lanes 16-31 their up rows.
+template <bool G>
+__global__ void __launch_bounds__(THREADS, 1)
+    experts_tile_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                        const __grid_constant__ CUtensorMap tmap_w2, const __grid_constant__ TileParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = smem_addr(smem_raw);
+    const uint32_t sbase = (raw_base + 1023u) & ~1023u;
+    uint8_t *sgen = smem_raw + (sbase - raw_base);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const LaunchCtx ctx = p.ctx;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const int pair = static_cast<int>(blockIdx.x >> 1), num_pairs = static_cast<int>(gridDim.x >> 1);
+
+    auto bar = [&](int i) -> uint32_t { return sbase + Smem::bars + 8u * i; };
+    auto full = [&](uint32_t i) { return bar(static_cast<int>((i / GROUP) % NGROUPS)); };
+    auto empty = [&](int s) { return bar(NGROUPS + s); };
+    auto raw_full = [&](int r) { return bar(NGROUPS + STAGES + r); };
+    auto raw_empty = [&](int r) { return bar(NGROUPS + STAGES + RAW_STAGES + r); };
+    auto d_full = [&](uint32_t d) { return bar(static_cast<int>(NGROUPS + STAGES + 2 * RAW_STAGES + d)); };
+    auto d_empty = [&](uint32_t d) { return bar(static_cast<int>(NGROUPS + STAGES + 2 * RAW_STAGES + 2 + d)); };
+    const uint32_t final_bar = bar(NGROUPS + STAGES + 2 * RAW_STAGES + 4);
+    int *abort_flag = reinterpret_cast<int *>(sgen + Smem::abort_flag);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + Smem::tmem_slot);
+    int *tiles = reinterpret_cast<int *>(sgen + Smem::tiles);
+
+    if (threadIdx.x == 0) {
+        for (int g = 0; g < NGROUPS; ++g) mbar_init_addr(bar(g), GROUP * (2 + 2 * DEQ_STAGE_WARPS));
+        for (int s = 0; s < STAGES; ++s) mbar_init_addr(empty(s), 1);
+        for (int r = 0; r < RAW_STAGES; ++r) {
+            mbar_init_addr(raw_full(r), 1);
+            mbar_init_addr(raw_empty(r), DEQ_WARPS);
+        }
+        for (uint32_t d = 0; d < 2; ++d) {
+            mbar_init_addr(d_full(d), 1);
+            mbar_init_addr(d_empty(d), 2 * EPI_WARPS);
+        }
+        mbar_init_addr(final_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == WARP_MMA) tmem_alloc_pair(sbase + Smem::tmem_slot, TMEM_COLS);
+    pdl_wait();
+    {  // tiles in front of each expert's
+        __shared__ int32_t part[THREADS / 32];
+        const int per = (p.plan.experts + THREADS - 1) / THREADS;
+        const int e0 = min(p.plan.experts, static_cast<int>(threadIdx.x) * per), e1 = min(p.plan.experts, e0 + per);
+        int mine = 0, start;
+        for (int e = e0; e < e1; ++e) mine += (expert_count(p, e, start) + BT - 1) / BT;
+        int s = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s += u;
+        }
+        if (lane == 31) part[warp] = s;
+        __syncthreads();
+        int before = s - mine;
+        for (int w = 0; w < warp; ++w) before += part[w];
+        for (int e = e0; e < e1; ++e) {
+            tiles[e] = before;
+            before += (expert_count(p, e, start) + BT - 1) / BT;
+            if (e == p.plan.experts - 1) tiles[p.plan.experts] = before;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();  // the peer's barriers exist before anyone signals them
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    const int items = tiles[p.plan.experts] * p.row_blocks;
+    const int KB = p.k / BK, KR = p.k / RAW_K;
+
+    if (warp == WARP_X) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int item = pair; ok && item < items; item += num_pairs) {
+            const Item t = item_at(p, tiles, item);
+            const int half = t.width >> 1;  // rows of this CTA; those behind cols are others', and dropped
+            const int row = t.first + static_cast<int>(rank) * half + lane * X_BOX;
+            for (int kb = 0; kb < KB; ++kb) {
+                const int s = it % STAGES;
+                if (!warp_wait_or_abort(empty(s), ((it / STAGES) & 1u) ^ 1u, abort_flag, ctx)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t xf = map_to_rank(full(it), 0);
+                if (lane == 0) mbar_expect_tx_cluster(xf, static_cast<uint32_t>(half) * BK * 2);
+                __syncwarp();
+                if (lane * X_BOX < half)
+                    tma_load_2d_pair(sbase + Smem::x + s * X_STAGE_BYTES + lane * X_BOX * BK * 2, &tmap_x, kb * BK, row, xf);
+                ++it;
+            }
+        }
+        if (leader && lane == 0) {  // both CTAs' copies complete on the leader's barriers
+            for (int s = 0; s < STAGES; ++s)
+                if (it > static_cast<uint32_t>(s)) {
+                    const uint32_t last = it - 1 - ((it - 1 - s) % STAGES);
+                    wait_drain(full(last), (last / STAGES) & 1u, ctx);
+                }
+        }
+    } else if (warp == WARP_RAW) {
+        if (lane == 0) {
+            uint32_t rit = 0;
+            bool ok = true;
+            for (int item = pair; ok && item < items; item += num_pairs) {
+                const Item t = item_at(p, tiles, item);
+                const int wrow = t.expert * p.n + (G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2)
+                                                     : t.row_block * 2 * BW + static_cast<int>(rank) * BW);
+                for (int kr = 0; kr < KR; ++kr) {
+                    const int r = rit % RAW_STAGES;
+                    if (!wait_or_abort(raw_empty(r), ((rit / RAW_STAGES) & 1u) ^ 1u, abort_flag, ctx)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx_addr(raw_full(r), RAW_STAGE_BYTES);
+                    const uint32_t to = sbase + Smem::raw + r * RAW_STAGE_BYTES;
+                    tma_load_2d(to, &tmap_w, kr * RAW_ROW, wrow, raw_full(r));
+                    if constexpr (G) tma_load_2d(to + (BW / 2) * RAW_ROW, &tmap_w2, kr * RAW_ROW, wrow, raw_full(r));
+                    ++rit;
+                }
+            }
+            for (int r = 0; r < RAW_STAGES; ++r)
+                if (rit > static_cast<uint32_t>(r)) {
+                    const uint32_t last = rit - 1 - ((rit - 1 - r) % RAW_STAGES);
+                    wait_drain(raw_full(r), (last / RAW_STAGES) & 1u, ctx);
+                }
+        }
+    } else if (warp == WARP_MMA) {
+        if (leader && lane == 0) {
+            const uint64_t bdesc0 = sw128_desc(sbase + Smem::x);
+            const uint32_t a0 = tmem_base + D_COLS;
+            uint32_t tiles_done = 0, g = 0, s = 0;
+            uint64_t bdesc = bdesc0;
+            uint32_t a_tmem = a0;
+            bool ok = pair >= items || wait_or_abort(full(0u), 0u, abort_flag, ctx);
+            bool issued = false;
+            for (int item = pair; ok && item < items; item += num_pairs) {
+                const Item t = item_at(p, tiles, item);
+                const uint32_t idesc = kIdesc | static_cast<uint32_t>(t.width >> 3) << 17;
+                const bool last_item = item + num_pairs >= items;
+                const uint32_t d = tiles_done & 1u;  // accumulator
+                if (!wait_or_abort_cluster(d_empty(d), ((tiles_done >> 1) & 1u) ^ 1u, abort_flag, ctx)) break;
+                for (int kb = 0; ok && kb < KB; ++kb, ++g) {
+                    tc_fence_after();
+                    const bool group_end = (g & (GROUP - 1)) == GROUP - 1 && !(last_item && kb == KB - 1);
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        umma_bf16_pair_ta(tmem_base + d * BT, a_tmem + 8 * kk, bdesc + 2 * kk, idesc, (kk != 0 || kb != 0) ? 1u : 0u);
+                        if (kk == 1 && group_end) {
+                            const uint32_t g1 = g + 1;  // the next group's first stage
+                            ok = wait_or_abort(full(g1), (g1 / STAGES) & 1u, abort_flag, ctx);
+                        }
+                    }
+                    issued = true;
+                    umma_commit_pair(empty(0) + 8u * s);
+                    if (++s == STAGES) {
+                        s = 0;
+                        bdesc = bdesc0;
+                        a_tmem = a0;
+                    } else {
+                        bdesc += X_STAGE_BYTES >> 4;
+                        a_tmem += A_COLS;
+                    }
+                }
+                if (ok) umma_commit_pair(d_full(d));
+                ++tiles_done;
+            }
+            if (issued) {  // all products of the pair are done before tensor memory is freed
+                umma_commit_pair(final_bar);
+                wait_drain(final_bar, 0, ctx);
+            }
+        }
+    } else if (warp >= WARP_DEQ) {
+        const int q = warp & 3, set = (warp - WARP_DEQ) >> 2;  // K stage `set` of each raw stage
+        const int row = G ? (lane >> 4) * (BW / 2) + q * 16 + (lane & 15) : q * 32 + lane;
+        const uint32_t full_leader0 = map_to_rank(bar(0), 0);
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS;
+        uint32_t rit = 0;
+        bool ok = true;
+        for (int item = pair; ok && item < items; item += num_pairs) {
+            for (int kr = 0; kr < KR; ++kr, ++rit) {
+                const int r = rit % RAW_STAGES;
+                if (!warp_wait_or_abort(raw_full(r), (rit / RAW_STAGES) & 1u, abort_flag, ctx)) {
+                    ok = false;
+                    break;
+                }
+                // two blocks are nine words; the first's codes begin in the middle of one
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(sgen + Smem::raw + r * RAW_STAGE_BYTES + row * RAW_ROW) + 9 * set;
+                uint32_t wd[9];
+#pragma unroll
+                for (int i = 0; i < 9; ++i) wd[i] = src[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive_addr(raw_empty(r));
+                uint32_t v[32];
+                const uint32_t d0 = __byte_perm(wd[0], 0, 0x1010), d1 = __byte_perm(wd[4], 0, 0x3232);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    weights_of(__byte_perm(wd[i], wd[i + 1], 0x5432), d0, p.magic, v + 4 * i);
+                    weights_of(wd[5 + i], d1, p.magic, v + 16 + 4 * i);
+                }
+                const uint32_t it = rit * (RAW_K / BK) + set;
+                const int s = it % STAGES;
+                if (!warp_wait_or_abort(empty(s), ((it / STAGES) & 1u) ^ 1u, abort_flag, ctx)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                tmem_st_32cols(lane_base + s * A_COLS, v);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(full_leader0 + 8u * ((it / GROUP) % NGROUPS));
+            }
+        }
+    } else if (warp >= WARP_EPI) {
+        const int q = warp & 3;
+        const uint32_t d_empty_leader[2] = {map_to_rank(d_empty(0), 0), map_to_rank(d_empty(1), 0)};
+        uint32_t tiles_done = 0;
+        for (int item = pair; item < items; item += num_pairs) {
+            const Item t = item_at(p, tiles, item);
+            const uint32_t d = tiles_done & 1u;
+            if (!warp_wait_or_abort(d_full(d), (tiles_done >> 1) & 1u, abort_flag, ctx)) break;
+            tc_fence_after();
+            const bool upper = lane >= 16;
+            const int f = G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) + q * 16 + (lane & 15)
+                            : t.row_block * 2 * BW + static_cast<int>(rank) * BW + q * 32 + lane;
+#pragma unroll 1
+            for (int c = 0; c < t.cols; c += 32) {
+                int to = -1;  // row of out of column c + lane, and its unit
+                float unit = 0.0f;
+                if (c + lane < t.cols) {
+                    const int pr = p.plan.pairs[t.first + c + lane];
+                    unit = p.unit[t.first + c + lane];
+                    if (pr >= 0 && pr < p.plan.pairs_total)
+                        to = G ? t.first + c + lane : pr;
+                    else
+                        record_error(ctx, kDevErrIndex);
+                }
+                uint32_t v[32];
+                tmem_ld_32cols(tmem_base + d * BT + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+                if constexpr (G) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        // the lower lanes take columns 0-15, the upper ones 16-31
+                        const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j] : v[16 + j]), 16);
+                        const float s = __shfl_sync(0xFFFFFFFFu, unit, j + (lane & 16));
+                        const float g = (upper ? other : __uint_as_float(v[j])) * s;
+                        const float u = (upper ? __uint_as_float(v[16 + j]) : other) * s;
+                        const int row = __shfl_sync(0xFFFFFFFFu, to, j + (lane & 16));
+                        if (f < p.n && row >= 0) p.out[row * p.out_stride + f] = to_bf16(gelu_tanh_fast(g) * u);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int row = __shfl_sync(0xFFFFFFFFu, to, j);
+                        const float s = __shfl_sync(0xFFFFFFFFu, unit, j);
+                        if (f < p.n && row >= 0) p.out[row * p.out_stride + f] = to_bf16(__uint_as_float(v[j]) * s);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(d_empty_leader[d]);
+            ++tiles_done;
+        }
+    }
+
+    pdl_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();  // the leader has drained; the peer's shared memory may go
+    tc_fence_after();
+    if (warp == WARP_MMA) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+// Rows of x in the pairs' order, as binary16 with their units: a warp a row.
+// GeGLU: row i is x[pairs[i] / topk]; down: row i of h.  Bound by the bytes out.
+struct RowsParams {
+    ExpertsPlan plan;
+    const uint16_t *x;
+    int64_t x_stride;
+    uint4 *rows;  // [pairs][k / 8]
+    float *unit;
+    int k;
+    bool gather;
+    LaunchCtx ctx;
+};
+
+__device__ __forceinline__ float bf16_low(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+constexpr int kRowsWarps = 8;
+
+__global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const __grid_constant__ RowsParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowsWarps + (threadIdx.x >> 5); i < p.plan.pairs_total;
+         i += static_cast<int64_t>(gridDim.x) * kRowsWarps) {
+        int64_t from = i;
+        if (p.gather) {
+            const int pr = p.plan.pairs[i];
+            if (pr < 0 || pr >= p.plan.pairs_total) continue;  // the products drop its column
+            from = pr / p.plan.topk;
+        }
+        const uint16_t *x = p.x + from * p.x_stride;
+        // the largest: bf16 magnitudes order as integers (what is no number makes the
+        // row's results none either)
+        uint32_t top = 0;
+        for (int c = lane; c < p.k / 8; c += 32) {
+            const uint4 v = reinterpret_cast<const uint4 *>(x)[c];
+            for (const uint32_t w : {v.x, v.y, v.z, v.w}) top = max(max(top, w & 0x7FFFu), (w >> 16) & 0x7FFFu);
+        }
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        const int e = min(max(static_cast<int>(top >> 7), 15), 254);  // as in the streaming form
+        const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+        if (lane == 0) p.unit[i] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+        uint4 *out = p.rows + i * (p.k / 8);
+        for (int c = lane; c < p.k / 8; c += 32) {  // block c / 4, values 4 (c % 4) .. and 16 on from there
+            const uint16_t *from8 = x + (c >> 2) * 32 + (c & 3) * 4;
+            const uint2 a = *reinterpret_cast<const uint2 *>(from8), b = *reinterpret_cast<const uint2 *>(from8 + 16);
+            out[c] = make_uint4(pack_f16x2(bf16_low(a.x) * f, bf16_low(a.y) * f), pack_f16x2(bf16_high(a.x) * f, bf16_high(a.y) * f),
+                                pack_f16x2(bf16_low(b.x) * f, bf16_low(b.y) * f), pack_f16x2(bf16_high(b.x) * f, bf16_high(b.y) * f));
+        }
+    }
+}
+
+size_t rows_bytes(int64_t pairs, int64_t k) { return (static_cast<size_t>(pairs) * (2 * k + 4) + 15) & ~size_t(15); }
+
+template <bool G>
+cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t *w2, const uint16_t *x, int64_t x_stride,
+                        uint16_t *out, int64_t out_stride, int64_t n, int64_t k, void *workspace, cudaStream_t stream,
+                        const LaunchCtx &ctx) {
+    uint16_t *xr = static_cast<uint16_t *>(workspace);
+    float *unit = reinterpret_cast<float *>(xr + plan.pairs_total * k);
+    CUtensorMap tx, tw, tw2;
+    const uint64_t row = static_cast<uint64_t>(k / RAW_K) * RAW_ROW, rows = static_cast<uint64_t>(plan.experts) * n;
+    if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, k, plan.pairs_total, k * 2, BK, X_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, row, rows, row, RAW_ROW, G ? BW / 2 : BW) ||
+        !encode_tmap_2d(&tw2, CU_TENSOR_MAP_DATA_TYPE_UINT8, G ? w2 : w, row, rows, row, RAW_ROW, G ? BW / 2 : BW))
+        return cudaErrorInvalidValue;
+    const int tile_rows = G ? BW : 2 * BW;
+    const TileParams p = {plan, unit, out, out_stride, static_cast<int>(n), static_cast<int>(k),
+                          static_cast<int>((n + tile_rows - 1) / tile_rows), 0x64006400u, ctx};
+    static int limits[kMaxDevices];
+    const size_t smem = Smem::total(plan.experts);
+    cudaError_t e = ensure_smem(experts_tile_kernel<G>, smem, true, limits);
+    if (e != cudaSuccess) return e;
+    const RowsParams r = {plan, x, x_stride, reinterpret_cast<uint4 *>(xr), unit, static_cast<int>(k), G, ctx};
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((plan.pairs_total + kRowsWarps - 1) / kRowsWarps,
+                                                                  static_cast<int64_t>(device_sm_count()) * 8));
+    e = launch_kernel(experts_rows_kernel, dim3(grid), dim3(kRowsWarps * 32), 0, stream, 1, r);
+    if (e != cudaSuccess) return e;
+    const unsigned pairs = std::max(1, device_sm_count() / 2);
+    return launch_kernel(experts_tile_kernel<G>, dim3(2 * pairs), dim3(THREADS), smem, stream, 2, tx, tw, tw2, p);
+}
+
+}  // namespace
+
+// Whether the tile form takes a product: bf16 in and out, rows that TMA can
+// copy, and enough pairs an expert on average.
+bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k) {
+    return bf16 && k % RAW_K == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0 &&
+           plan.experts * n < (int64_t(1) << 31) && experts_are_many(plan.pairs_total, plan.experts);
+}
+
+size_t experts_rows_bytes(int64_t pairs, int64_t k) { return rows_bytes(pairs, k); }
+
+cudaError_t launch_experts_tile_geglu(const ExpertsGeglu &a, cudaStream_t stream, const LaunchCtx &ctx) {
+    return launch_tile<true>(a.plan, a.wg, a.wu, static_cast<const uint16_t *>(a.x), a.x_stride, static_cast<uint16_t *>(a.h),
+                             a.h_stride, a.n, a.k, a.workspace, stream, ctx);
+}
+
+cudaError_t launch_experts_tile_down(const ExpertsDown &a, void *z, void *rows, cudaStream_t stream, const LaunchCtx &ctx) {
+    return launch_tile<false>(a.plan, a.wd, nullptr, static_cast<const uint16_t *>(a.h), a.h_stride, static_cast<uint16_t *>(z),
+                              a.n, a.n, a.k, rows, stream, ctx);
+}
+
+}  // namespace qmm

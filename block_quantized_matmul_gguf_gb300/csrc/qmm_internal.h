@@ -330,7 +330,7 @@ struct ExpertsGeglu {
     ExpertsPlan plan;
     const uint8_t *wg, *wu;
     const void *x;
-    void *h;
+    void *h, *workspace;  // none: the streaming form
     int64_t x_stride, h_stride, n, k;
     bool x_bf16, h_bf16;
 };
@@ -346,8 +346,17 @@ struct ExpertsDown {
     int64_t h_stride, y_stride, n, k;
     bool h_bf16, y_bf16;
 };
-size_t experts_down_workspace_bytes(int64_t tokens, int topk, int64_t n);
+size_t experts_down_workspace_bytes(int64_t pairs, int64_t n, int64_t k);
 cudaError_t launch_experts_down(const ExpertsDown &args, cudaStream_t stream, const LaunchCtx &ctx);
+
+// The tile form (qmm_experts_tile.cu) and when it is taken: from so many pairs
+// an expert on average.
+constexpr int64_t kExpertsTilePairs = 8;
+inline bool experts_are_many(int64_t pairs, int experts) { return pairs >= kExpertsTilePairs * experts; }
+bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k);
+cudaError_t launch_experts_tile_geglu(const ExpertsGeglu &args, cudaStream_t stream, const LaunchCtx &ctx);
+size_t experts_rows_bytes(int64_t pairs, int64_t k);  // of x as that form reads it
+cudaError_t launch_experts_tile_down(const ExpertsDown &args, void *z, void *rows, cudaStream_t stream, const LaunchCtx &ctx);
 
 cudaError_t launch_selftest_wait(cudaStream_t stream, const LaunchCtx &ctx);
 

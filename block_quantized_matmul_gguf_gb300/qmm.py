@@ -40,7 +40,8 @@ EXPORTED = (
     "qmm_set_wait_timeout_ns", "qmm_selftest_wait_timeout", "qmm_copy",
     "qmm_kv_plan", "qmm_kv_append_q4_0", "qmm_kv_append_rope_q4_0", "qmm_kv_read_q4_0",
     "qmm_route", "qmm_route_workspace_bytes",
-    "qmm_experts_geglu_q4_0", "qmm_experts_down_q4_0", "qmm_experts_down_workspace_bytes",
+    "qmm_experts_geglu_workspace_bytes", "qmm_experts_geglu_q4_0", "qmm_experts_down_workspace_bytes",
+    "qmm_experts_down_q4_0",
     "qmm_attn_q4_0_workspace_bytes", "qmm_attn_q4_0", "qmm_logits_adjust",
 )
 
@@ -159,7 +160,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "qmm_kv_append_rope_q4_0": [P, P, P],
         "qmm_kv_read_q4_0": [P, P, I64, P, P, P],
         "qmm_route": [P, P],
-        "qmm_experts_geglu_q4_0": [P, P, P, P, I64, I32, P, I64, I32, I64, I64, P],
+        "qmm_experts_geglu_q4_0": [P, P, P, P, I64, I32, P, I64, I32, I64, I64, P, SZ, P],
         "qmm_experts_down_q4_0": [P, P, P, I64, I32, P, P, P, I64, I32, I64, I64, P, SZ, P],
         "qmm_attn_q4_0": [P, P, P],
         "qmm_logits_adjust": [P, P],
@@ -177,7 +178,9 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         getattr(lib, name).restype = SZ
     lib.qmm_attn_q4_0_workspace_bytes.argtypes = [P, I32]
     lib.qmm_attn_q4_0_workspace_bytes.restype = SZ
-    lib.qmm_experts_down_workspace_bytes.argtypes = [I64, I32, I64]
+    lib.qmm_experts_geglu_workspace_bytes.argtypes = [I64, I32, I32, I64]
+    lib.qmm_experts_geglu_workspace_bytes.restype = SZ
+    lib.qmm_experts_down_workspace_bytes.argtypes = [I64, I32, I64, I64]
     lib.qmm_experts_down_workspace_bytes.restype = SZ
     lib.qmm_route_workspace_bytes.argtypes = [I64, I32]
     lib.qmm_route_workspace_bytes.restype = SZ
@@ -667,26 +670,37 @@ def _expert_weights(w, experts: int, n: int, k: int, what: str) -> int:
     return _ptr(w)
 
 
-def experts_workspace(tokens: int, topk: int, n: int, device="cuda"):
-    """A workspace for the down projections of up to so many tokens (calls that overlap on the GPU need their own)."""
+def experts_workspace(tokens: int, topk: int, n: int, k: int, device="cuda"):
+    """A workspace for the products [n][k] of up to so many tokens, of either kind (calls that overlap on the
+    GPU need their own)."""
     import torch
-    need = int(load().qmm_experts_down_workspace_bytes(tokens, topk, n))
+    need = int(load().qmm_experts_down_workspace_bytes(tokens, topk, n, k))
     return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
 
 
-def qmm_experts_geglu_q4_0(wg, wu, x, h, expert_start, pairs, topk: int, n: int, k: int, stream=None) -> None:
+def qmm_experts_geglu_q4_0(wg, wu, x, h, expert_start, pairs, topk: int, n: int, k: int, workspace=None,
+                           stream=None) -> None:
     """h[i] = gelu(x wg^T) * (x wu^T) of each pair's token and expert, in the order of pairs, from x
-    [tokens][k] (fp32 or bf16) into h [tokens * topk][n] (fp32 or bf16)."""
-    i32 = _torch_module().int32
+    [tokens][k] (fp32 or bf16) into h [tokens * topk][n] (fp32 or bf16).  Without a workspace, calls that
+    use one take it from the memory of the stream they run on."""
+    torch = _torch_module()
+    i32 = torch.int32
     tokens, experts = x.shape[0], expert_start.numel() - 1
     xp, xs, x_type = _matrix_rows(x, k, "x")
     hp, hs, h_type = _matrix_rows(h, n, "h")
     if h.shape[0] != tokens * topk or pairs.numel() != tokens * topk:
         raise ValueError("h and pairs must have tokens * topk rows")
+    need = 0
+    if workspace is None and x_type == QMM_BF16 and h_type == QMM_BF16:
+        need = (_lib or load()).qmm_experts_geglu_workspace_bytes(tokens, topk, experts, k)
+        if need:
+            with torch.cuda.stream(_stream_object(stream)):  # as for attention
+                workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
     plan = _EXPERT_PLAN.pack(tokens, topk, experts, _typed(expert_start, i32, "expert_start"), _typed(pairs, i32, "pairs"))
     status = (_lib or load()).qmm_experts_geglu_q4_0(
         plan, _expert_weights(wg, experts, n, k, "wg"), _expert_weights(wu, experts, n, k, "wu"), xp, xs, x_type, hp, hs,
-        h_type, n, k, _stream(stream))
+        h_type, n, k, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream))
     _check(status, "qmm_experts_geglu_q4_0")
 
 
@@ -705,7 +719,7 @@ def qmm_experts_down_q4_0(wd, h, y, ids, weights, expert_start, pairs, n: int, k
         raise ValueError("h and pairs must have tokens * topk rows, weights the shape of ids, y a row for each token")
     if workspace is None:
         with torch.cuda.stream(_stream_object(stream)):  # as for attention
-            workspace = experts_workspace(tokens, topk, n, y.device)
+            workspace = experts_workspace(tokens, topk, n, k, y.device)
     plan = _EXPERT_PLAN.pack(tokens, topk, experts, _typed(expert_start, i32, "expert_start"), _typed(pairs, i32, "pairs"))
     status = (_lib or load()).qmm_experts_down_q4_0(
         plan, _expert_weights(wd, experts, n, k, "wd"), hp, hs, h_type, _typed(ids, i32, "ids"),

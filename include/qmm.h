@@ -566,14 +566,21 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
  * Arithmetic: sums in fp32.  With an fp32 output the weights are exact, a bf16
  * input too, and an fp32 input enters in two binary16 parts (22 bits of it, and
  * 2^-39 of the largest of its row's 256 values around it).  With a bf16 output
- * an fp32 input enters in 11 bits.  A row of x or h that holds an infinity or a
- * NaN gives NaN.  Which form a call takes depends on its host-side arguments
- * alone; equal calls give equal bits, and a pair's row depends on no other pair.
+ * an fp32 input enters in 11 bits, and calls with many pairs an expert (prompts,
+ * bf16 in and out, k % 256 == 0) round each weight once to binary16: 2^-12 of it,
+ * where the output's own rounding is 2^-9; scales beyond 8188 overflow there.
+ * Their down projections are rounded to bf16 once before the sum.  A row of x or
+ * h that holds an infinity or a NaN gives NaN.  Which form a call takes depends on
+ * its host-side arguments alone; equal calls give equal bits, and a pair's row
+ * depends on no other pair.
  * Entries outside their arrays (an expert_start that descends or leaves
  * 0 .. tokens * topk, a pair outside 0 .. tokens * topk - 1) record
  * QMM_ERR_INDEX; what they concern is left out.
  *   workspace  16-byte aligned device memory of at least
- *              qmm_experts_down_workspace_bytes() bytes, scratch of the call
+ *              qmm_experts_geglu_workspace_bytes() or
+ *              qmm_experts_down_workspace_bytes() bytes, scratch of the call.
+ *              For geglu NULL is taken too: prompts are then worked as few rows
+ *              are, more slowly and more exactly.
  * Requires tokens >= 0 (0 launches nothing), 1 <= topk <= 32, experts <= 1024,
  * n >= 1, k % 32 == 0, weights 16-byte aligned, other pointers aligned to their
  * type, strides at least the rows' widths; n <= 2^24, k <= 2^20 and at most
@@ -590,8 +597,9 @@ typedef struct qmm_expert_plan {
 qmm_status qmm_experts_geglu_q4_0(const qmm_expert_plan *plan, const void *wg, const void *wu,
                                   const void *x, int64_t x_stride, qmm_dtype x_type, void *h,
                                   int64_t h_stride, qmm_dtype h_type, int64_t n, int64_t k,
-                                  qmm_stream_t stream);
-size_t qmm_experts_down_workspace_bytes(int64_t tokens, int topk, int64_t n);
+                                  void *workspace, size_t workspace_bytes, qmm_stream_t stream);
+size_t qmm_experts_geglu_workspace_bytes(int64_t tokens, int topk, int experts, int64_t k);
+size_t qmm_experts_down_workspace_bytes(int64_t tokens, int topk, int64_t n, int64_t k);
 qmm_status qmm_experts_down_q4_0(const qmm_expert_plan *plan, const void *wd, const void *h,
                                  int64_t h_stride, qmm_dtype h_type, const int32_t *ids,
                                  const float *weights, void *y, int64_t y_stride, qmm_dtype y_type,

@@ -76,7 +76,7 @@ def run_down(qmm, rng, tokens, experts, topk, n, k, h_type=F32, y_type=F32, kind
     want, limit = ref.experts_down(h.double().numpy(), bd, ids, weights, starts, pairs, y_type is F32, h_type is F32)
     near(y, want, limit, y_type is F32)
     again = torch.full_like(y, 7.0)
-    qmm.qmm_experts_down_q4_0(*args[:2], again, *args[3:], workspace=qmm.experts_workspace(tokens, topk, n))
+    qmm.qmm_experts_down_q4_0(*args[:2], again, *args[3:], workspace=qmm.experts_workspace(tokens, topk, n, k))
     assert torch.equal(again, y)
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
 
@@ -214,7 +214,7 @@ def test_a_layer_in_a_graph(qmm, types, tokens):
     starts, pairs = torch.empty(experts + 1, **i32), torch.empty(tokens * topk, **i32)
     h = torch.empty(tokens * topk, width, dtype=types[0], device="cuda")
     y = torch.empty(tokens, hidden, dtype=types[1], device="cuda")
-    ws, rs = qmm.experts_workspace(tokens, topk, hidden), qmm.route_workspace(tokens, experts)
+    ws, rs = qmm.experts_workspace(tokens, topk, hidden, width), qmm.route_workspace(tokens, experts)
 
     def fill(n):
         x.copy_(torch.from_numpy(rng.standard_normal((tokens, hidden)).astype(np.float32)))
