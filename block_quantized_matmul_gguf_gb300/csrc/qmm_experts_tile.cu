@@ -40,32 +40,32 @@ namespace {
 
 constexpr int BW = 128;      // weight rows of a CTA
 constexpr int BT = 128;      // rows of x in a tile, at most
-constexpr int BK = 64;       // K of a stage
-constexpr int RAW_K = 256;   // K of a raw stage
-constexpr int STAGES = 8;
-constexpr int GROUP = 4;     // stages announced to the MMA thread at once
-constexpr int NGROUPS = STAGES / GROUP;
-constexpr int RAW_STAGES = 6;
-constexpr int X_STAGE_BYTES = BT / 2 * BK * 2;
+constexpr int BK = 64;       // K of a swizzle row of x
+constexpr int CK = 256;      // K of a chunk: eight blocks
+constexpr int SK = 128;      // K of a stage, the pipeline's unit
+constexpr int SUBS = SK / BK;
+constexpr int A_SLOTS = 4, X_SLOTS = 4, RAW_SLOTS = 4;  // in flight: stages, stages, chunks
+constexpr int X_SUB_BYTES = BT * BK * 2, X_SLOT_BYTES = SUBS * X_SUB_BYTES;
 constexpr int RAW_ROW = 144;
-constexpr int RAW_STAGE_BYTES = BW * RAW_ROW;
-constexpr uint32_t D_COLS = 2 * BT, A_COLS = BK / 2, TMEM_COLS = 512;  // two accumulators
-static_assert(D_COLS + STAGES * A_COLS <= TMEM_COLS, "tensor memory");
-static_assert(RAW_K / BK % GROUP == 0, "a tile is whole groups");
+constexpr int RAW_SLOT_BYTES = BW * RAW_ROW;
+constexpr uint32_t D_COLS = 2 * BT, A_COLS = SK / 2, TMEM_COLS = 512;  // two accumulators
+static_assert(D_COLS + A_SLOTS * A_COLS <= TMEM_COLS, "tensor memory");
 
 constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_EPI = 4, EPI_WARPS = 4, WARP_DEQ = 8, DEQ_WARPS = 16;
-constexpr int DEQ_STAGE_WARPS = 4;  // that write one K stage
 constexpr int THREADS = (WARP_DEQ + DEQ_WARPS) * 32;
 constexpr int X_BOX = 16;           // rows of a copy of x
 
 struct Smem {
     static constexpr int x = 0;
-    static constexpr int raw = STAGES * X_STAGE_BYTES;
-    static constexpr int bars = raw + RAW_STAGES * RAW_STAGE_BYTES;
-    static constexpr int nbars = NGROUPS + STAGES + 2 * RAW_STAGES + 5;
+    static constexpr int raw = X_SLOTS * X_SLOT_BYTES;
+    static constexpr int bars = raw + RAW_SLOTS * RAW_SLOT_BYTES;
+    static constexpr int x_full = 0, x_empty = x_full + X_SLOTS, a_full = x_empty + X_SLOTS, a_empty = a_full + A_SLOTS,
+                         raw_full = a_empty + A_SLOTS, raw_empty = raw_full + RAW_SLOTS, d_full = raw_empty + RAW_SLOTS,
+                         d_empty = d_full + 2, final = d_empty + 2, nbars = final + 1;
     static constexpr int tmem_slot = bars + nbars * 8;
     static constexpr int abort_flag = tmem_slot + 4;
-    static constexpr int tiles = abort_flag + 4;  // [experts + 1] tiles in front of each expert's
+    static constexpr int cols = (abort_flag + 4 + 15) / 16 * 16;  // [EPI_WARPS][BT] row of out and unit of each column
+    static constexpr int tiles = cols + EPI_WARPS * BT * 8;       // [experts + 1] tiles in front of each expert's
     static int total(int experts) { return tiles + (experts + 1) * 4 + 1024; }
 };
 static_assert(Smem::tiles + (kMaxExperts + 1) * 4 + 1024 <= 232448 - 256, "shared memory of a CTA");
@@ -78,6 +78,7 @@ struct TileParams {
     int n, k;
     int row_blocks;      // of a matrix: of 256 rows (down) or 128 features
     uint32_t magic;      // 1024, 1024 in binary16, in a register
+    bool even;           // out takes two neighbouring values at once
     LaunchCtx ctx;
 };
 
@@ -146,6 +147,45 @@ __device__ __forceinline__ void weights_of(uint32_t q, uint32_t d, uint32_t magi
     w[3] = hmul2(hfma2((q8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u), d);
 }
 
+// A box of x into the same place of both CTAs, counted on the barrier of each.
+__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
+        "[%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<unsigned short>(3))
+        : "memory");
+}
+
+// One lane of a warp, the same each time.
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
+// By the elected lane; the whole warp comes here with the same operands.
+__device__ __forceinline__ void product(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
+        : "memory");
+}
+// The same on the barrier at this offset in both CTAs.
+__device__ __forceinline__ void commit_both(uint32_t one, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(bar),
+        "r"(one), "h"(static_cast<unsigned short>(3))
+        : "memory");
+}
+
 // 32 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&v)[32]) {
     asm volatile(
@@ -159,8 +199,8 @@ __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&
         : "memory");
 }
 
-// D fp32, A and B binary16, both K-major, M = 256; N goes in at run time.
-constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>((2 * BW) >> 4) << 24);
+// D fp32, A and B binary16, both K-major, M = 128; N goes in at run time.
+constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BW >> 4) << 24);
 
 // G: GeGLU.  A CTA's 128 accumulator rows are then 64 features: in lane quarter q,
 // lanes 0-15 hold the gate rows of features 16q .. 16q+15, lanes 16-31 their up rows.
@@ -175,37 +215,35 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const LaunchCtx ctx = p.ctx;
     const uint32_t rank = cluster_rank();
-    const bool leader = rank == 0;
     const int pair = static_cast<int>(blockIdx.x >> 1), num_pairs = static_cast<int>(gridDim.x >> 1);
 
-    auto bar = [&](int i) -> uint32_t { return sbase + Smem::bars + 8u * i; };
-    auto full = [&](uint32_t i) { return bar(static_cast<int>((i / GROUP) % NGROUPS)); };
-    auto empty = [&](int s) { return bar(NGROUPS + s); };
-    auto raw_full = [&](int r) { return bar(NGROUPS + STAGES + r); };
-    auto raw_empty = [&](int r) { return bar(NGROUPS + STAGES + RAW_STAGES + r); };
-    auto d_full = [&](uint32_t d) { return bar(static_cast<int>(NGROUPS + STAGES + 2 * RAW_STAGES + d)); };
-    auto d_empty = [&](uint32_t d) { return bar(static_cast<int>(NGROUPS + STAGES + 2 * RAW_STAGES + 2 + d)); };
-    const uint32_t final_bar = bar(NGROUPS + STAGES + 2 * RAW_STAGES + 4);
+    auto bar = [&](uint32_t i) -> uint32_t { return sbase + Smem::bars + 8u * i; };
     int *abort_flag = reinterpret_cast<int *>(sgen + Smem::abort_flag);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + Smem::tmem_slot);
     int *tiles = reinterpret_cast<int *>(sgen + Smem::tiles);
 
     if (threadIdx.x == 0) {
-        for (int g = 0; g < NGROUPS; ++g) mbar_init_addr(bar(g), GROUP * (2 + 2 * DEQ_STAGE_WARPS));
-        for (int s = 0; s < STAGES; ++s) mbar_init_addr(empty(s), 1);
-        for (int r = 0; r < RAW_STAGES; ++r) {
-            mbar_init_addr(raw_full(r), 1);
-            mbar_init_addr(raw_empty(r), DEQ_WARPS);
+        for (int i = 0; i < X_SLOTS; ++i) {
+            mbar_init_addr(bar(Smem::x_full + i), 1);
+            mbar_init_addr(bar(Smem::x_empty + i), 2);  // both CTAs have read the slot
         }
-        for (uint32_t d = 0; d < 2; ++d) {
-            mbar_init_addr(d_full(d), 1);
-            mbar_init_addr(d_empty(d), 2 * EPI_WARPS);
+        for (int i = 0; i < A_SLOTS; ++i) {
+            mbar_init_addr(bar(Smem::a_full + i), DEQ_WARPS * SK / CK);
+            mbar_init_addr(bar(Smem::a_empty + i), 1);
         }
-        mbar_init_addr(final_bar, 1);
+        for (int i = 0; i < RAW_SLOTS; ++i) {
+            mbar_init_addr(bar(Smem::raw_full + i), 1);
+            mbar_init_addr(bar(Smem::raw_empty + i), DEQ_WARPS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init_addr(bar(Smem::d_full + i), 1);
+            mbar_init_addr(bar(Smem::d_empty + i), EPI_WARPS);
+        }
+        mbar_init_addr(bar(Smem::final), 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == WARP_MMA) tmem_alloc_pair(sbase + Smem::tmem_slot, TMEM_COLS);
+    if (warp == WARP_MMA) tmem_alloc_cta(sbase + Smem::tmem_slot, TMEM_COLS);
     pdl_wait();
     {  // tiles in front of each expert's
         __shared__ int32_t part[THREADS / 32];
@@ -235,129 +273,121 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     const int items = tiles[p.plan.experts] * p.row_blocks;
-    const int KB = p.k / BK, KR = p.k / RAW_K;
+    const int chunks = p.k / CK;
 
     if (warp == WARP_X) {
         uint32_t it = 0;
         bool ok = true;
         for (int item = pair; ok && item < items; item += num_pairs) {
             const Item t = item_at(p, tiles, item);
-            const int half = t.width >> 1;  // rows of this CTA; those behind cols are others', and dropped
-            const int row = t.first + static_cast<int>(rank) * half + lane * X_BOX;
-            for (int kb = 0; kb < KB; ++kb) {
-                const int s = it % STAGES;
-                if (!warp_wait_or_abort(empty(s), ((it / STAGES) & 1u) ^ 1u, abort_flag, ctx)) {
+            // half of the rows for both CTAs; those behind cols are others', and dropped
+            const int half = t.width >> 1, sub = lane >> 2, box = (lane & 3) * X_BOX;
+            const int row = static_cast<int>(rank) * half + box;
+            for (int st = 0; st < chunks * (CK / SK); ++st, ++it) {
+                const uint32_t s = it % X_SLOTS, full = bar(Smem::x_full + s);
+                if (!warp_wait_or_abort(bar(Smem::x_empty + s), ((it / X_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
                     ok = false;
                     break;
                 }
-                const uint32_t xf = map_to_rank(full(it), 0);
-                if (lane == 0) mbar_expect_tx_cluster(xf, static_cast<uint32_t>(half) * BK * 2);
+                if (lane == 0) mbar_expect_tx_addr(full, static_cast<uint32_t>(t.width) * SK * 2);
                 __syncwarp();
-                if (lane * X_BOX < half)
-                    tma_load_2d_pair(sbase + Smem::x + s * X_STAGE_BYTES + lane * X_BOX * BK * 2, &tmap_x, kb * BK, row, xf);
-                ++it;
+                if (sub < SUBS && box < half)
+                    tma_load_2d_both(sbase + Smem::x + s * X_SLOT_BYTES + sub * X_SUB_BYTES + row * BK * 2, &tmap_x, st * SK + sub * BK,
+                                     t.first + row, full);
             }
         }
-        if (leader && lane == 0) {  // both CTAs' copies complete on the leader's barriers
-            for (int s = 0; s < STAGES; ++s)
-                if (it > static_cast<uint32_t>(s)) {
-                    const uint32_t last = it - 1 - ((it - 1 - s) % STAGES);
-                    wait_drain(full(last), (last / STAGES) & 1u, ctx);
+        if (lane == 0) {
+            // all copies into this CTA have come, and both CTAs have read what this
+            // one sent: nothing of the peer's is on its way here any more
+            for (uint32_t s = 0; s < X_SLOTS; ++s)
+                if (it > s) {
+                    const uint32_t last = it - 1 - ((it - 1 - s) % X_SLOTS);
+                    wait_drain(bar(Smem::x_full + s), (last / X_SLOTS) & 1u, ctx);
+                    if (ok) wait_drain(bar(Smem::x_empty + s), (last / X_SLOTS) & 1u, ctx);
                 }
         }
     } else if (warp == WARP_RAW) {
         if (lane == 0) {
-            uint32_t rit = 0;
+            uint32_t it = 0;
             bool ok = true;
             for (int item = pair; ok && item < items; item += num_pairs) {
                 const Item t = item_at(p, tiles, item);
                 const int wrow = t.expert * p.n + (G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2)
                                                      : t.row_block * 2 * BW + static_cast<int>(rank) * BW);
-                for (int kr = 0; kr < KR; ++kr) {
-                    const int r = rit % RAW_STAGES;
-                    if (!wait_or_abort(raw_empty(r), ((rit / RAW_STAGES) & 1u) ^ 1u, abort_flag, ctx)) {
+                for (int c = 0; c < chunks; ++c, ++it) {
+                    const uint32_t s = it % RAW_SLOTS, full = bar(Smem::raw_full + s);
+                    if (!wait_or_abort(bar(Smem::raw_empty + s), ((it / RAW_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
                         ok = false;
                         break;
                     }
-                    mbar_expect_tx_addr(raw_full(r), RAW_STAGE_BYTES);
-                    const uint32_t to = sbase + Smem::raw + r * RAW_STAGE_BYTES;
-                    tma_load_2d(to, &tmap_w, kr * RAW_ROW, wrow, raw_full(r));
-                    if constexpr (G) tma_load_2d(to + (BW / 2) * RAW_ROW, &tmap_w2, kr * RAW_ROW, wrow, raw_full(r));
-                    ++rit;
+                    mbar_expect_tx_addr(full, RAW_SLOT_BYTES);
+                    const uint32_t to = sbase + Smem::raw + s * RAW_SLOT_BYTES;
+                    tma_load_2d(to, &tmap_w, c * RAW_ROW, wrow, full);
+                    if constexpr (G) tma_load_2d(to + (BW / 2) * RAW_ROW, &tmap_w2, c * RAW_ROW, wrow, full);
                 }
             }
-            for (int r = 0; r < RAW_STAGES; ++r)
-                if (rit > static_cast<uint32_t>(r)) {
-                    const uint32_t last = rit - 1 - ((rit - 1 - r) % RAW_STAGES);
-                    wait_drain(raw_full(r), (last / RAW_STAGES) & 1u, ctx);
+            for (uint32_t s = 0; s < RAW_SLOTS; ++s)
+                if (it > s) {
+                    const uint32_t last = it - 1 - ((it - 1 - s) % RAW_SLOTS);
+                    wait_drain(bar(Smem::raw_full + s), (last / RAW_SLOTS) & 1u, ctx);
                 }
         }
     } else if (warp == WARP_MMA) {
-        if (leader && lane == 0) {
-            const uint64_t bdesc0 = sw128_desc(sbase + Smem::x);
-            const uint32_t a0 = tmem_base + D_COLS;
-            uint32_t tiles_done = 0, g = 0, s = 0;
-            uint64_t bdesc = bdesc0;
-            uint32_t a_tmem = a0;
-            bool ok = pair >= items || wait_or_abort(full(0u), 0u, abort_flag, ctx);
-            bool issued = false;
-            for (int item = pair; ok && item < items; item += num_pairs) {
-                const Item t = item_at(p, tiles, item);
-                const uint32_t idesc = kIdesc | static_cast<uint32_t>(t.width >> 3) << 17;
-                const bool last_item = item + num_pairs >= items;
-                const uint32_t d = tiles_done & 1u;  // accumulator
-                if (!wait_or_abort_cluster(d_empty(d), ((tiles_done >> 1) & 1u) ^ 1u, abort_flag, ctx)) break;
-                for (int kb = 0; ok && kb < KB; ++kb, ++g) {
-                    tc_fence_after();
-                    const bool group_end = (g & (GROUP - 1)) == GROUP - 1 && !(last_item && kb == KB - 1);
+        // the whole warp, so that the operands are known to be the same for all lanes:
+        // a thread on its own has to move each to the uniform registers that the
+        // products take theirs from, and paces the pipeline by that
+        const uint32_t one = elected(), tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
+        const uint32_t bars = __shfl_sync(0xFFFFFFFFu, bar(0), 0);
+        const uint64_t bdesc0 = sw128_desc(__shfl_sync(0xFFFFFFFFu, sbase, 0) + Smem::x);
+        const int stages = __shfl_sync(0xFFFFFFFFu, chunks * (CK / SK), 0);
+        uint32_t tiles_done = 0, it = 0;
+        bool ok = true, issued = false;
+        for (int item = pair; ok && item < items; item += num_pairs) {
+            const uint32_t idesc = kIdesc | static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, item_at(p, tiles, item).width, 0) >> 3) << 17;
+            const uint32_t d = tiles_done & 1u;  // accumulator
+            if (!warp_wait_or_abort(bar(Smem::d_empty + d), ((tiles_done >> 1) & 1u) ^ 1u, abort_flag, ctx)) break;
+            for (int st = 0; st < stages; ++st, ++it) {
+                const uint32_t xs = it % X_SLOTS, as = it % A_SLOTS;
+                ok = warp_wait_or_abort(bar(Smem::x_full + xs), (it / X_SLOTS) & 1u, abort_flag, ctx) &&
+                     warp_wait_or_abort(bar(Smem::a_full + as), (it / A_SLOTS) & 1u, abort_flag, ctx);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t a = tmem + D_COLS + as * A_COLS, to = tmem + d * BT;
+                const uint64_t b = bdesc0 + xs * (X_SLOT_BYTES >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk) {
-                        umma_bf16_pair_ta(tmem_base + d * BT, a_tmem + 8 * kk, bdesc + 2 * kk, idesc, (kk != 0 || kb != 0) ? 1u : 0u);
-                        if (kk == 1 && group_end) {
-                            const uint32_t g1 = g + 1;  // the next group's first stage
-                            ok = wait_or_abort(full(g1), (g1 / STAGES) & 1u, abort_flag, ctx);
-                        }
-                    }
-                    issued = true;
-                    umma_commit_pair(empty(0) + 8u * s);
-                    if (++s == STAGES) {
-                        s = 0;
-                        bdesc = bdesc0;
-                        a_tmem = a0;
-                    } else {
-                        bdesc += X_STAGE_BYTES >> 4;
-                        a_tmem += A_COLS;
-                    }
-                }
-                if (ok) umma_commit_pair(d_full(d));
-                ++tiles_done;
+                for (int k = 0; k < SK / 16; ++k)
+                    product(one, to, a + 8 * k, b + (k / 4) * (X_SUB_BYTES >> 4) + 2 * (k & 3), idesc, k != 0 || st != 0);
+                issued = true;
+                commit(one, bars + 8u * (Smem::a_empty + as));
+                commit_both(one, bars + 8u * (Smem::x_empty + xs));
             }
-            if (issued) {  // all products of the pair are done before tensor memory is freed
-                umma_commit_pair(final_bar);
-                wait_drain(final_bar, 0, ctx);
-            }
+            if (ok) commit(one, bars + 8u * (Smem::d_full + d));
+            ++tiles_done;
+        }
+        if (issued) {  // all products are done before tensor memory is freed
+            commit(one, bars + 8u * Smem::final);
+            wait_drain(bar(Smem::final), 0, ctx);
         }
     } else if (warp >= WARP_DEQ) {
-        const int q = warp & 3, set = (warp - WARP_DEQ) >> 2;  // K stage `set` of each raw stage
+        const int q = warp & 3, sub = (warp - WARP_DEQ) >> 2;  // 64 values of K of each chunk
         const int row = G ? (lane >> 4) * (BW / 2) + q * 16 + (lane & 15) : q * 32 + lane;
-        const uint32_t full_leader0 = map_to_rank(bar(0), 0);
-        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS;
-        uint32_t rit = 0;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS + (sub % SUBS) * (BK / 2);
+        uint32_t it = 0;
         bool ok = true;
         for (int item = pair; ok && item < items; item += num_pairs) {
-            for (int kr = 0; kr < KR; ++kr, ++rit) {
-                const int r = rit % RAW_STAGES;
-                if (!warp_wait_or_abort(raw_full(r), (rit / RAW_STAGES) & 1u, abort_flag, ctx)) {
+            for (int c = 0; c < chunks; ++c, ++it) {
+                const uint32_t r = it % RAW_SLOTS, st = it * (CK / SK) + sub / SUBS, s = st % A_SLOTS;
+                if (!warp_wait_or_abort(bar(Smem::raw_full + r), (it / RAW_SLOTS) & 1u, abort_flag, ctx)) {
                     ok = false;
                     break;
                 }
                 // two blocks are nine words; the first's codes begin in the middle of one
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(sgen + Smem::raw + r * RAW_STAGE_BYTES + row * RAW_ROW) + 9 * set;
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(sgen + Smem::raw + r * RAW_SLOT_BYTES + row * RAW_ROW) + 9 * sub;
                 uint32_t wd[9];
 #pragma unroll
                 for (int i = 0; i < 9; ++i) wd[i] = src[i];
                 __syncwarp();
-                if (lane == 0) mbar_arrive_addr(raw_empty(r));
+                if (lane == 0) mbar_arrive_addr(bar(Smem::raw_empty + r));
                 uint32_t v[32];
                 const uint32_t d0 = __byte_perm(wd[0], 0, 0x1010), d1 = __byte_perm(wd[4], 0, 0x3232);
 #pragma unroll
@@ -365,9 +395,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     weights_of(__byte_perm(wd[i], wd[i + 1], 0x5432), d0, p.magic, v + 4 * i);
                     weights_of(wd[5 + i], d1, p.magic, v + 16 + 4 * i);
                 }
-                const uint32_t it = rit * (RAW_K / BK) + set;
-                const int s = it % STAGES;
-                if (!warp_wait_or_abort(empty(s), ((it / STAGES) & 1u) ^ 1u, abort_flag, ctx)) {
+                if (!warp_wait_or_abort(bar(Smem::a_empty + s), ((st / A_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
                     ok = false;
                     break;
                 }
@@ -376,58 +404,81 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(full_leader0 + 8u * ((it / GROUP) % NGROUPS));
+                if (lane == 0) mbar_arrive_addr(bar(Smem::a_full + s));
             }
         }
     } else if (warp >= WARP_EPI) {
         const int q = warp & 3;
-        const uint32_t d_empty_leader[2] = {map_to_rank(d_empty(0), 0), map_to_rank(d_empty(1), 0)};
+        uint2 *table = reinterpret_cast<uint2 *>(sgen + Smem::cols) + (warp - WARP_EPI) * BT;
+        const bool odd = lane & 1, upper = lane >= 16;
         uint32_t tiles_done = 0;
         for (int item = pair; item < items; item += num_pairs) {
             const Item t = item_at(p, tiles, item);
             const uint32_t d = tiles_done & 1u;
-            if (!warp_wait_or_abort(d_full(d), (tiles_done >> 1) & 1u, abort_flag, ctx)) break;
+            for (int c = lane; c < t.cols; c += 32) {
+                const int pr = p.plan.pairs[t.first + c];
+                int to = -1;
+                if (pr >= 0 && pr < p.plan.pairs_total)
+                    to = G ? t.first + c : pr;
+                else
+                    record_error(ctx, kDevErrIndex);
+                table[c] = make_uint2(static_cast<uint32_t>(to), __float_as_uint(p.unit[t.first + c]));
+            }
+            __syncwarp();
+            if (!warp_wait_or_abort(bar(Smem::d_full + d), (tiles_done >> 1) & 1u, abort_flag, ctx)) break;
             tc_fence_after();
-            const bool upper = lane >= 16;
-            const int f = G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) + q * 16 + (lane & 15)
-                            : t.row_block * 2 * BW + static_cast<int>(rank) * BW + q * 32 + lane;
+            // lanes 2i and 2i + 1 exchange halves of two columns: each then has two
+            // neighbouring features of one
+            const int f = (G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) + q * 16 + (lane & 14)
+                             : t.row_block * 2 * BW + static_cast<int>(rank) * BW + q * 32 + (lane & 30));
+            auto put = [&](int col, float lo, float hi) {
+                if (col >= t.cols) return;
+                const int row = static_cast<int>(table[col].x);
+                if (row < 0 || f >= p.n) return;
+                uint16_t *to = p.out + row * p.out_stride + f;
+                const uint32_t v = pack_bf16x2(lo, hi);
+                if (p.even) {
+                    *reinterpret_cast<uint32_t *>(to) = v;
+                } else {
+                    to[0] = static_cast<uint16_t>(v);
+                    if (f + 1 < p.n) to[1] = static_cast<uint16_t>(v >> 16);
+                }
+            };
 #pragma unroll 1
             for (int c = 0; c < t.cols; c += 32) {
-                int to = -1;  // row of out of column c + lane, and its unit
-                float unit = 0.0f;
-                if (c + lane < t.cols) {
-                    const int pr = p.plan.pairs[t.first + c + lane];
-                    unit = p.unit[t.first + c + lane];
-                    if (pr >= 0 && pr < p.plan.pairs_total)
-                        to = G ? t.first + c + lane : pr;
-                    else
-                        record_error(ctx, kDevErrIndex);
-                }
                 uint32_t v[32];
                 tmem_ld_32cols(tmem_base + d * BT + (static_cast<uint32_t>(q * 32) << 16) + c, v);
                 if constexpr (G) {
+                    // the lower lanes take columns 0-15, the upper ones 16-31
+                    const int c0 = c + (lane & 16);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        // the lower lanes take columns 0-15, the upper ones 16-31
-                        const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j] : v[16 + j]), 16);
-                        const float s = __shfl_sync(0xFFFFFFFFu, unit, j + (lane & 16));
-                        const float g = (upper ? other : __uint_as_float(v[j])) * s;
-                        const float u = (upper ? __uint_as_float(v[16 + j]) : other) * s;
-                        const int row = __shfl_sync(0xFFFFFFFFu, to, j + (lane & 16));
-                        if (f < p.n && row >= 0) p.out[row * p.out_stride + f] = to_bf16(gelu_tanh_fast(g) * u);
+                    for (int j = 0; j < 16; j += 2) {
+                        float h[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j + i] : v[16 + j + i]), 16);
+                            const float s = __uint_as_float(table[c0 + j + i].y);
+                            const float g = (upper ? other : __uint_as_float(v[j + i])) * s;
+                            const float u = (upper ? __uint_as_float(v[16 + j + i]) : other) * s;
+                            h[i] = gelu_tanh_fast(g) * u;
+                        }
+                        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? h[0] : h[1], 1);
+                        put(c0 + j + odd, odd ? got : h[0], odd ? h[1] : got);
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int row = __shfl_sync(0xFFFFFFFFu, to, j);
-                        const float s = __shfl_sync(0xFFFFFFFFu, unit, j);
-                        if (f < p.n && row >= 0) p.out[row * p.out_stride + f] = to_bf16(__uint_as_float(v[j]) * s);
+                    for (int j = 0; j < 32; j += 2) {
+                        const float mine = __uint_as_float(odd ? v[j + 1] : v[j]);
+                        const float got = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(odd ? v[j] : v[j + 1]), 1);
+                        const float s = __uint_as_float(table[c + j + odd].y);
+                        put(c + j + odd, (odd ? got : mine) * s, (odd ? mine : got) * s);
                     }
                 }
             }
+            __syncwarp();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(d_empty_leader[d]);
+            if (lane == 0) mbar_arrive_addr(bar(Smem::d_empty + d));
             ++tiles_done;
         }
     }
@@ -435,9 +486,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    cluster_barrier();  // the leader has drained; the peer's shared memory may go
+    cluster_barrier();  // the peer sends nothing here any more
     tc_fence_after();
-    if (warp == WARP_MMA) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    if (warp == WARP_MMA) tmem_dealloc_cta(tmem_base, TMEM_COLS);
 }
 
 // Rows of x in the pairs' order, as binary16 with their units: a warp a row.
@@ -506,14 +557,15 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
     uint16_t *xr = static_cast<uint16_t *>(workspace);
     float *unit = reinterpret_cast<float *>(xr + plan.pairs_total * k);
     CUtensorMap tx, tw, tw2;
-    const uint64_t row = static_cast<uint64_t>(k / RAW_K) * RAW_ROW, rows = static_cast<uint64_t>(plan.experts) * n;
+    const uint64_t row = static_cast<uint64_t>(k / CK) * RAW_ROW, rows = static_cast<uint64_t>(plan.experts) * n;
     if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, k, plan.pairs_total, k * 2, BK, X_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, row, rows, row, RAW_ROW, G ? BW / 2 : BW) ||
         !encode_tmap_2d(&tw2, CU_TENSOR_MAP_DATA_TYPE_UINT8, G ? w2 : w, row, rows, row, RAW_ROW, G ? BW / 2 : BW))
         return cudaErrorInvalidValue;
     const int tile_rows = G ? BW : 2 * BW;
     const TileParams p = {plan, unit, out, out_stride, static_cast<int>(n), static_cast<int>(k),
-                          static_cast<int>((n + tile_rows - 1) / tile_rows), 0x64006400u, ctx};
+                          static_cast<int>((n + tile_rows - 1) / tile_rows), 0x64006400u,
+                          n % 2 == 0 && out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(out) % 4 == 0, ctx};
     static int limits[kMaxDevices];
     const size_t smem = Smem::total(plan.experts);
     cudaError_t e = ensure_smem(experts_tile_kernel<G>, smem, true, limits);
@@ -532,7 +584,7 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
 // Whether the tile form takes a product: bf16 in and out, rows that TMA can
 // copy, and enough pairs an expert on average.
 bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k) {
-    return bf16 && k % RAW_K == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0 &&
+    return bf16 && k % CK == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0 &&
            plan.experts * n < (int64_t(1) << 31) && experts_are_many(plan.pairs_total, plan.experts);
 }
 
