@@ -16,46 +16,87 @@ struct SumParams {
     int64_t y_stride, tokens, n;
     int experts, topk;
     bool bf16;  // y
+    bool wide;  // y's rows are aligned to 16 bytes
 };
 
-__device__ __forceinline__ float4 four_at(const float *z) { return *reinterpret_cast<const float4 *>(z); }
-__device__ __forceinline__ float4 four_at(const uint16_t *z) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(z);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xFFFF0000u));
+// V columns of the row at z.
+template <int V>
+__device__ __forceinline__ void load_columns(const float *z, float (&f)[V]) {
+    if constexpr (V == 1) {
+        f[0] = *z;
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(z + v);
+            f[v] = a.x, f[v + 1] = a.y, f[v + 2] = a.z, f[v + 3] = a.w;
+        }
+    }
 }
-__device__ __forceinline__ float one_at(const float *z) { return *z; }
-__device__ __forceinline__ float one_at(const uint16_t *z) { return __uint_as_float(static_cast<uint32_t>(*z) << 16); }
+template <int V>
+__device__ __forceinline__ void load_columns(const uint16_t *z, float (&f)[V]) {
+    if constexpr (V == 1) {
+        f[0] = __uint_as_float(static_cast<uint32_t>(*z) << 16);
+    } else {
+        static_assert(V == 8, "16 bytes");
+        const uint4 a = *reinterpret_cast<const uint4 *>(z);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+constexpr int kSumAhead = 8;  // rows of z loaded before the first is added
 
 template <typename T, int V>
-__global__ void __launch_bounds__(256) sum_kernel(SumParams p) {
+__global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumParams p) {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t per = (p.n + V - 1) / V, all = per * p.tokens;
+    const int per = static_cast<int>(p.n / V);
+    const int64_t all = static_cast<int64_t>(per) * p.tokens;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t t = i / per, col = (i - t * per) * V;
+        const int64_t t = i / per;
+        const int col = static_cast<int>(i - t * per) * V;
+        const T *z = static_cast<const T *>(p.z) + t * p.topk * p.n + col;
         float sum[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) sum[v] = 0.0f;
-#pragma unroll 4
-        for (int r = 0; r < p.topk; ++r) {
-            const int64_t pair = t * p.topk + r;
-            const int id = p.ids[pair];
-            if (id < 0 || id >= p.experts) continue;
-            const float w = p.weights[pair];
-            const T *z = static_cast<const T *>(p.z) + pair * p.n + col;
-            if constexpr (V == 4) {
-                const float4 f = four_at(z);
-                sum[0] = fmaf(w, f.x, sum[0]);
-                sum[1] = fmaf(w, f.y, sum[1]);
-                sum[2] = fmaf(w, f.z, sum[2]);
-                sum[3] = fmaf(w, f.w, sum[3]);
-            } else {
-                sum[0] = fmaf(w, one_at(z), sum[0]);
-            }
-        }
+        for (int r0 = 0; r0 < p.topk; r0 += kSumAhead) {
+            float w[kSumAhead], f[kSumAhead][V];
+            bool there[kSumAhead];
 #pragma unroll
-        for (int v = 0; v < V; ++v) experts::put(p.y, t * p.y_stride + col + v, p.bf16, sum[v]);
+            for (int r = 0; r < kSumAhead; ++r) {
+                there[r] = false;
+                if (r0 + r < p.topk) {
+                    const int id = p.ids[t * p.topk + r0 + r];
+                    there[r] = id >= 0 && id < p.experts;
+                    w[r] = p.weights[t * p.topk + r0 + r];
+                    load_columns<V>(z + (r0 + r) * p.n, f[r]);  // of a pair that is not there: not used
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < kSumAhead; ++r)
+                if (there[r])
+#pragma unroll
+                    for (int v = 0; v < V; ++v) sum[v] = fmaf(w[r], f[r][v], sum[v]);
+        }
+        if (V == 8 && p.bf16 && p.wide) {
+            uint32_t o[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(sum[2 * v % V], sum[(2 * v + 1) % V]);
+                o[v] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + t * p.y_stride + col) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else if (V == 4 && !p.bf16 && p.wide) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + t * p.y_stride + col) =
+                make_float4(sum[0], sum[1 % V], sum[2 % V], sum[3 % V]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) experts::put(p.y, t * p.y_stride + col + v, p.bf16, sum[v]);
+        }
     }
 }
 
@@ -90,13 +131,14 @@ cudaError_t launch_experts_down(const ExpertsDown &a, cudaStream_t stream, const
     }
     if (e != cudaSuccess) return e;
     const int64_t tokens = a.plan.pairs_total / a.plan.topk;
-    const SumParams s = {a.workspace, a.ids, a.weights, a.y, a.y_stride, tokens, a.n, a.plan.experts,
-                         a.plan.topk, a.y_bf16};
-    const bool wide = a.n % 4 == 0;  // the workspace is aligned
-    const int64_t threads = tokens * (wide ? a.n / 4 : a.n);
+    const int values = tiles ? 8 : 4;  // of z in 16 bytes
+    const bool whole = a.n % values == 0;  // the workspace is aligned
+    const SumParams s = {a.workspace, a.ids, a.weights, a.y, a.y_stride, tokens, a.n, a.plan.experts, a.plan.topk, a.y_bf16,
+                         reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.y_stride % (a.y_bf16 ? 8 : 4) == 0};
+    const int64_t threads = tokens * (whole ? a.n / values : a.n);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((threads + 255) / 256, static_cast<int64_t>(device_sm_count()) * 8));
-    auto *kernel = tiles ? (wide ? sum_kernel<uint16_t, 4> : sum_kernel<uint16_t, 1>)
-                         : (wide ? sum_kernel<float, 4> : sum_kernel<float, 1>);
+    auto *kernel = tiles ? (whole ? sum_kernel<uint16_t, 8> : sum_kernel<uint16_t, 1>)
+                         : (whole ? sum_kernel<float, 4> : sum_kernel<float, 1>);
     return launch_kernel(kernel, dim3(grid), dim3(256), 0, stream, 1, s);
 }
 

@@ -20,8 +20,8 @@
 //   warp 0      x producer (both CTAs): boxes of 16 rows x 64 values, a lane each
 //   warp 1      MMA issuer (one thread of the leader)
 //   warp 2      weight producer (both CTAs): boxes of 128 rows x 144 bytes
-//   warps 4-7   epilogue
-//   warps 8-23  dequantisers: TMEM lanes 32 (w % 4) .., every fourth 64-wide K stage.
+//   warps 4-11  epilogue, two for each quarter of the lanes
+//   warps 12-27 dequantisers: TMEM lanes 32 (w % 4) .., every fourth 64-wide K stage.
 //               A stage's weights are formed in registers before its slot is waited
 //               for, so that a free slot is filled at once.
 // The binary16 pairs that a word of codes gives without moving its nibbles are
@@ -51,7 +51,7 @@ constexpr int RAW_SLOT_BYTES = BW * RAW_ROW;
 constexpr uint32_t D_COLS = 2 * BT, A_COLS = SK / 2, TMEM_COLS = 512;  // two accumulators
 static_assert(D_COLS + A_SLOTS * A_COLS <= TMEM_COLS, "tensor memory");
 
-constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_EPI = 4, EPI_WARPS = 4, WARP_DEQ = 8, DEQ_WARPS = 16;
+constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_EPI = 4, EPI_WARPS = 8, WARP_DEQ = 12, DEQ_WARPS = 16;
 constexpr int THREADS = (WARP_DEQ + DEQ_WARPS) * 32;
 constexpr int X_BOX = 16;           // rows of a copy of x
 
@@ -64,11 +64,11 @@ struct Smem {
                          d_empty = d_full + 2, final = d_empty + 2, nbars = final + 1;
     static constexpr int tmem_slot = bars + nbars * 8;
     static constexpr int abort_flag = tmem_slot + 4;
-    static constexpr int cols = (abort_flag + 4 + 15) / 16 * 16;  // [EPI_WARPS][BT] row of out and unit of each column
-    static constexpr int tiles = cols + EPI_WARPS * BT * 8;       // [experts + 1] tiles in front of each expert's
-    static int total(int experts) { return tiles + (experts + 1) * 4 + 1024; }
+    static constexpr int cols = (abort_flag + 4 + 15) / 16 * 16;  // [4][BT] place in out and unit of each column
+    static constexpr int tiles = cols + 4 * BT * 16;  // Experts: three arrays of [experts + 1]
+    static int total(int experts) { return tiles + (experts + 1) * 12 + 1024; }
 };
-static_assert(Smem::tiles + (kMaxExperts + 1) * 4 + 1024 <= 232448 - 256, "shared memory of a CTA");
+static_assert(Smem::tiles + (kMaxExperts + 1) * 12 + 1024 <= 232448 - 256, "shared memory of a CTA");
 
 struct TileParams {
     ExpertsPlan plan;
@@ -80,6 +80,11 @@ struct TileParams {
     uint32_t magic;      // 1024, 1024 in binary16, in a register
     bool even;           // out takes two neighbouring values at once
     LaunchCtx ctx;
+};
+
+// The experts' work, in shared memory.
+struct Experts {
+    int *tiles, *start, *count;  // tiles in front of each expert's, its first pair, its pairs
 };
 
 // One item: rows first .. first + cols - 1 of the sorted pairs of `expert`.
@@ -98,24 +103,23 @@ __device__ __forceinline__ int expert_count(const TileParams &p, int e, int &sta
     return static_cast<int>(b - a);
 }
 
-__device__ __forceinline__ Item item_at(const TileParams &p, const int *tiles, int item) {
+__device__ __forceinline__ Item item_at(const TileParams &p, const Experts &ex, int item) {
     Item it;
     const int tile = item / p.row_blocks;
     it.row_block = item - tile * p.row_blocks;
     int lo = 0, hi = p.plan.experts;  // tiles[lo] <= tile < tiles[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (tiles[mid] <= tile)
+        if (ex.tiles[mid] <= tile)
             lo = mid;
         else
             hi = mid;
     }
     it.expert = lo;
-    int start;
-    const int count = expert_count(p, lo, start), parts = tiles[lo + 1] - tiles[lo];
+    const int count = ex.count[lo], parts = ex.tiles[lo + 1] - ex.tiles[lo];
     const int per = ((count + parts - 1) / parts + 31) & ~31;
-    const int at = (tile - tiles[lo]) * per;
-    it.first = start + at;
+    const int at = (tile - ex.tiles[lo]) * per;
+    it.first = ex.start[lo] + at;
     it.cols = max(0, min(per, count - at));
     it.width = max(32, (it.cols + 31) & ~31);
     return it;
@@ -220,7 +224,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto bar = [&](uint32_t i) -> uint32_t { return sbase + Smem::bars + 8u * i; };
     int *abort_flag = reinterpret_cast<int *>(sgen + Smem::abort_flag);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + Smem::tmem_slot);
-    int *tiles = reinterpret_cast<int *>(sgen + Smem::tiles);
+    Experts ex;
+    ex.tiles = reinterpret_cast<int *>(sgen + Smem::tiles);
+    ex.start = ex.tiles + p.plan.experts + 1;
+    ex.count = ex.start + p.plan.experts + 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < X_SLOTS; ++i) {
@@ -262,9 +269,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         int before = s - mine;
         for (int w = 0; w < warp; ++w) before += part[w];
         for (int e = e0; e < e1; ++e) {
-            tiles[e] = before;
-            before += (expert_count(p, e, start) + BT - 1) / BT;
-            if (e == p.plan.experts - 1) tiles[p.plan.experts] = before;
+            const int count = expert_count(p, e, start);
+            ex.tiles[e] = before;
+            ex.start[e] = start;
+            ex.count[e] = count;
+            before += (count + BT - 1) / BT;
+            if (e == p.plan.experts - 1) ex.tiles[p.plan.experts] = before;
         }
     }
     tc_fence_before();
@@ -272,14 +282,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     cluster_barrier();  // the peer's barriers exist before anyone signals them
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
-    const int items = tiles[p.plan.experts] * p.row_blocks;
+    const int items = ex.tiles[p.plan.experts] * p.row_blocks;
     const int chunks = p.k / CK;
 
     if (warp == WARP_X) {
         uint32_t it = 0;
         bool ok = true;
         for (int item = pair; ok && item < items; item += num_pairs) {
-            const Item t = item_at(p, tiles, item);
+            const Item t = item_at(p, ex, item);
             // half of the rows for both CTAs; those behind cols are others', and dropped
             const int half = t.width >> 1, sub = lane >> 2, box = (lane & 3) * X_BOX;
             const int row = static_cast<int>(rank) * half + box;
@@ -311,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t it = 0;
             bool ok = true;
             for (int item = pair; ok && item < items; item += num_pairs) {
-                const Item t = item_at(p, tiles, item);
+                const Item t = item_at(p, ex, item);
                 const int wrow = t.expert * p.n + (G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2)
                                                      : t.row_block * 2 * BW + static_cast<int>(rank) * BW);
                 for (int c = 0; c < chunks; ++c, ++it) {
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t tiles_done = 0, it = 0;
         bool ok = true, issued = false;
         for (int item = pair; ok && item < items; item += num_pairs) {
-            const uint32_t idesc = kIdesc | static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, item_at(p, tiles, item).width, 0) >> 3) << 17;
+            const uint32_t idesc = kIdesc | static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, item_at(p, ex, item).width, 0) >> 3) << 17;
             const uint32_t d = tiles_done & 1u;  // accumulator
             if (!warp_wait_or_abort(bar(Smem::d_empty + d), ((tiles_done >> 1) & 1u) ^ 1u, abort_flag, ctx)) break;
             for (int st = 0; st < stages; ++st, ++it) {
@@ -408,44 +418,46 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
     } else if (warp >= WARP_EPI) {
-        const int q = warp & 3;
-        uint2 *table = reinterpret_cast<uint2 *>(sgen + Smem::cols) + (warp - WARP_EPI) * BT;
+        const int q = warp & 3, part = (warp - WARP_EPI) >> 2;  // the two warps of a quarter take every other 32 columns
         const bool odd = lane & 1, upper = lane >= 16;
+        ulonglong2 *table = reinterpret_cast<ulonglong2 *>(sgen + Smem::cols) + q * BT;
         uint32_t tiles_done = 0;
         for (int item = pair; item < items; item += num_pairs) {
-            const Item t = item_at(p, tiles, item);
+            const Item t = item_at(p, ex, item);
             const uint32_t d = tiles_done & 1u;
-            for (int c = lane; c < t.cols; c += 32) {
-                const int pr = p.plan.pairs[t.first + c];
-                int to = -1;
-                if (pr >= 0 && pr < p.plan.pairs_total)
-                    to = G ? t.first + c : pr;
-                else
-                    record_error(ctx, kDevErrIndex);
-                table[c] = make_uint2(static_cast<uint32_t>(to), __float_as_uint(p.unit[t.first + c]));
+            // lanes 2i and 2i + 1 exchange halves of two columns: each then has two
+            // neighbouring features f, f + 1 of one
+            const int f = G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) + q * 16 + (lane & 14)
+                            : t.row_block * 2 * BW + static_cast<int>(rank) * BW + q * 32 + (lane & 30);
+            for (int c = 32 * part + lane; c < t.width; c += 64) {  // place in out (none: 0) and unit
+                uint16_t *to = nullptr;
+                float unit = 0.0f;
+                if (c < t.cols) {
+                    const int pr = p.plan.pairs[t.first + c];
+                    unit = p.unit[t.first + c];
+                    if (pr >= 0 && pr < p.plan.pairs_total)
+                        to = p.out + (G ? t.first + c : pr) * p.out_stride;
+                    else
+                        record_error(ctx, kDevErrIndex);
+                }
+                table[c] = make_ulonglong2(reinterpret_cast<uint64_t>(to), __float_as_uint(unit));
             }
             __syncwarp();
             if (!warp_wait_or_abort(bar(Smem::d_full + d), (tiles_done >> 1) & 1u, abort_flag, ctx)) break;
             tc_fence_after();
-            // lanes 2i and 2i + 1 exchange halves of two columns: each then has two
-            // neighbouring features of one
-            const int f = (G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) + q * 16 + (lane & 14)
-                             : t.row_block * 2 * BW + static_cast<int>(rank) * BW + q * 32 + (lane & 30));
-            auto put = [&](int col, float lo, float hi) {
-                if (col >= t.cols) return;
-                const int row = static_cast<int>(table[col].x);
-                if (row < 0 || f >= p.n) return;
-                uint16_t *to = p.out + row * p.out_stride + f;
+            auto put = [&](uint64_t to, float lo, float hi) {
+                if (to == 0 || f >= p.n) return;
+                uint16_t *at = reinterpret_cast<uint16_t *>(to) + f;
                 const uint32_t v = pack_bf16x2(lo, hi);
                 if (p.even) {
-                    *reinterpret_cast<uint32_t *>(to) = v;
+                    *reinterpret_cast<uint32_t *>(at) = v;
                 } else {
-                    to[0] = static_cast<uint16_t>(v);
-                    if (f + 1 < p.n) to[1] = static_cast<uint16_t>(v >> 16);
+                    at[0] = static_cast<uint16_t>(v);
+                    if (f + 1 < p.n) at[1] = static_cast<uint16_t>(v >> 16);
                 }
             };
 #pragma unroll 1
-            for (int c = 0; c < t.cols; c += 32) {
+            for (int c = 32 * part; c < t.cols; c += 64) {
                 uint32_t v[32];
                 tmem_ld_32cols(tmem_base + d * BT + (static_cast<uint32_t>(q * 32) << 16) + c, v);
                 if constexpr (G) {
@@ -453,29 +465,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int c0 = c + (lane & 16);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
+                        ulonglong2 to[2];
                         float h[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
+                            to[i] = table[c0 + j + i];
                             const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j + i] : v[16 + j + i]), 16);
-                            const float s = __uint_as_float(table[c0 + j + i].y);
+                            const float s = __uint_as_float(static_cast<uint32_t>(to[i].y));
                             const float g = (upper ? other : __uint_as_float(v[j + i])) * s;
                             const float u = (upper ? __uint_as_float(v[16 + j + i]) : other) * s;
                             h[i] = gelu_tanh_fast(g) * u;
                         }
                         const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? h[0] : h[1], 1);
-                        put(c0 + j + odd, odd ? got : h[0], odd ? h[1] : got);
+                        put(odd ? to[1].x : to[0].x, odd ? got : h[0], odd ? h[1] : got);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         const float mine = __uint_as_float(odd ? v[j + 1] : v[j]);
                         const float got = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(odd ? v[j] : v[j + 1]), 1);
-                        const float s = __uint_as_float(table[c + j + odd].y);
-                        put(c + j + odd, (odd ? got : mine) * s, (odd ? mine : got) * s);
+                        const ulonglong2 to = table[c + j + odd];
+                        const float s = __uint_as_float(static_cast<uint32_t>(to.y));
+                        put(to.x, (odd ? got : mine) * s, (odd ? mine : got) * s);
                     }
                 }
             }
-            __syncwarp();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_addr(bar(Smem::d_empty + d));
