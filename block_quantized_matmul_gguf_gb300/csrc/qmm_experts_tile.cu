@@ -53,7 +53,7 @@ static_assert(D_COLS + A_SLOTS * A_COLS <= TMEM_COLS, "tensor memory");
 
 constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_EPI = 4, EPI_WARPS = 8, WARP_DEQ = 12, DEQ_WARPS = 16;
 constexpr int THREADS = (WARP_DEQ + DEQ_WARPS) * 32;
-constexpr int X_BOX = 16;           // rows of a copy of x
+constexpr int X_BOX = 16, X_WIDE = BT / 2;  // rows of a copy of x: where few are wanted, and otherwise
 
 struct Smem {
     static constexpr int x = 0;
@@ -210,7 +210,8 @@ constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BW >> 4) << 24);
 // lanes 0-15 hold the gate rows of features 16q .. 16q+15, lanes 16-31 their up rows.
 template <bool G>
 __global__ void __launch_bounds__(THREADS, 1)
-    experts_tile_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+    experts_tile_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_x64,
+                        const __grid_constant__ CUtensorMap tmap_w,
                         const __grid_constant__ CUtensorMap tmap_w2, const __grid_constant__ TileParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_addr(smem_raw);
@@ -290,19 +291,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = true;
         for (int item = pair; ok && item < items; item += num_pairs) {
             const Item t = item_at(p, ex, item);
-            // half of the rows for both CTAs; those behind cols are others', and dropped
-            const int half = t.width >> 1, sub = lane >> 2, box = (lane & 3) * X_BOX;
-            const int row = static_cast<int>(rank) * half + box;
+            // half of the rows for both CTAs; those behind cols are others', and
+            // dropped.  One copy of 64 rows a swizzle row where more than 32 are
+            // wanted (the other half's rows that it brings are the same ones)
+            const int half = t.width >> 1, first = static_cast<int>(rank) * half;
+            const bool many = half > 2 * X_BOX;
+            const int sub = many ? lane : lane >> 1, row = first + (many ? 0 : (lane & 1) * X_BOX);
+            const bool mine = sub < SUBS && (many || row < first + half);
+            const CUtensorMap *map = many ? &tmap_x64 : &tmap_x;
+            const uint32_t bytes = static_cast<uint32_t>(many ? 2 * X_WIDE : t.width) * SK * 2;
             for (int st = 0; st < chunks * (CK / SK); ++st, ++it) {
                 const uint32_t s = it % X_SLOTS, full = bar(Smem::x_full + s);
                 if (!warp_wait_or_abort(bar(Smem::x_empty + s), ((it / X_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_expect_tx_addr(full, static_cast<uint32_t>(t.width) * SK * 2);
+                if (lane == 0) mbar_expect_tx_addr(full, bytes);
                 __syncwarp();
-                if (sub < SUBS && box < half)
-                    tma_load_2d_both(sbase + Smem::x + s * X_SLOT_BYTES + sub * X_SUB_BYTES + row * BK * 2, &tmap_x, st * SK + sub * BK,
+                if (mine)
+                    tma_load_2d_both(sbase + Smem::x + s * X_SLOT_BYTES + sub * X_SUB_BYTES + row * BK * 2, map, st * SK + sub * BK,
                                      t.first + row, full);
             }
         }
@@ -570,9 +577,10 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
                         const LaunchCtx &ctx) {
     uint16_t *xr = static_cast<uint16_t *>(workspace);
     float *unit = reinterpret_cast<float *>(xr + plan.pairs_total * k);
-    CUtensorMap tx, tw, tw2;
+    CUtensorMap tx, tx64, tw, tw2;
     const uint64_t row = static_cast<uint64_t>(k / CK) * RAW_ROW, rows = static_cast<uint64_t>(plan.experts) * n;
     if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, k, plan.pairs_total, k * 2, BK, X_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&tx64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, k, plan.pairs_total, k * 2, BK, X_WIDE, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, row, rows, row, RAW_ROW, G ? BW / 2 : BW) ||
         !encode_tmap_2d(&tw2, CU_TENSOR_MAP_DATA_TYPE_UINT8, G ? w2 : w, row, rows, row, RAW_ROW, G ? BW / 2 : BW))
         return cudaErrorInvalidValue;
@@ -590,7 +598,7 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
     e = launch_kernel(experts_rows_kernel, dim3(grid), dim3(kRowsWarps * 32), 0, stream, 1, r);
     if (e != cudaSuccess) return e;
     const unsigned pairs = std::max(1, device_sm_count() / 2);
-    return launch_kernel(experts_tile_kernel<G>, dim3(2 * pairs), dim3(THREADS), smem, stream, 2, tx, tw, tw2, p);
+    return launch_kernel(experts_tile_kernel<G>, dim3(2 * pairs), dim3(THREADS), smem, stream, 2, tx, tx64, tw, tw2, p);
 }
 
 }  // namespace
