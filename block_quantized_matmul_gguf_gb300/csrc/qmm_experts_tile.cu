@@ -65,10 +65,10 @@ struct Smem {
     static constexpr int tmem_slot = bars + nbars * 8;
     static constexpr int abort_flag = tmem_slot + 4;
     static constexpr int cols = (abort_flag + 4 + 15) / 16 * 16;  // [4][BT] place in out and unit of each column
-    static constexpr int tiles = cols + 4 * BT * 16;  // Experts: three arrays of [experts + 1]
-    static int total(int experts) { return tiles + (experts + 1) * 12 + 1024; }
+    static constexpr int tiles = cols + 4 * BT * 16;  // Experts: four arrays of [experts + 1]
+    static int total(int experts) { return tiles + (experts + 1) * 16 + 1024; }
 };
-static_assert(Smem::tiles + (kMaxExperts + 1) * 12 + 1024 <= 232448 - 256, "shared memory of a CTA");
+static_assert(Smem::tiles + (kMaxExperts + 1) * 16 + 1024 <= 232448 - 256, "shared memory of a CTA");
 
 struct TileParams {
     ExpertsPlan plan;
@@ -82,14 +82,17 @@ struct TileParams {
     LaunchCtx ctx;
 };
 
-// The experts' work, in shared memory.
+// The experts' work, in shared memory: tiles in front of each expert's, its first
+// pair, its pairs, and the rows of each of its tiles.
 struct Experts {
-    int *tiles, *start, *count;  // tiles in front of each expert's, its first pair, its pairs
+    int *tiles, *start, *count, *per;
 };
 
-// One item: rows first .. first + cols - 1 of the sorted pairs of `expert`.
+// An item: rows first .. first + cols - 1 of the sorted pairs of `expert`.  A pair of
+// CTAs takes every num_pairs-th item (tile, row block); whole warps step through them.
 struct Item {
-    int expert, row_block, first, cols, width;  // width: cols up to a multiple of 32
+    int tile, row_block;
+    int expert, first, cols, width;  // width: cols up to a multiple of 32
 };
 
 __device__ __forceinline__ int expert_count(const TileParams &p, int e, int &start) {
@@ -103,24 +106,42 @@ __device__ __forceinline__ int expert_count(const TileParams &p, int e, int &sta
     return static_cast<int>(b - a);
 }
 
-__device__ __forceinline__ Item item_at(const TileParams &p, const Experts &ex, int item) {
+struct Items {
+    int item, tile, row_block;      // the next one
+    int tile_step, row_block_step;  // num_pairs as tiles and row blocks
+};
+__device__ __forceinline__ Items items_from(const TileParams &p, int pair, int num_pairs) {
+    Items at;
+    at.item = pair;
+    at.tile = pair / p.row_blocks;
+    at.row_block = pair - at.tile * p.row_blocks;
+    at.tile_step = num_pairs / p.row_blocks;
+    at.row_block_step = num_pairs - at.tile_step * p.row_blocks;
+    return at;
+}
+// The next item, by a whole warp: two ballots find the expert.
+__device__ __forceinline__ Item next_item(const TileParams &p, const Experts &ex, int num_pairs, int lane, Items &at) {
     Item it;
-    const int tile = item / p.row_blocks;
-    it.row_block = item - tile * p.row_blocks;
-    int lo = 0, hi = p.plan.experts;  // tiles[lo] <= tile < tiles[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (ex.tiles[mid] <= tile)
-            lo = mid;
-        else
-            hi = mid;
+    it.tile = at.tile;
+    it.row_block = at.row_block;
+    at.item += num_pairs;
+    at.tile += at.tile_step;
+    at.row_block += at.row_block_step;
+    if (at.row_block >= p.row_blocks) {
+        at.row_block -= p.row_blocks;
+        ++at.tile;
     }
-    it.expert = lo;
-    const int count = ex.count[lo], parts = ex.tiles[lo + 1] - ex.tiles[lo];
-    const int per = ((count + parts - 1) / parts + 31) & ~31;
-    const int at = (tile - ex.tiles[lo]) * per;
-    it.first = ex.start[lo] + at;
-    it.cols = max(0, min(per, count - at));
+    const int each = (p.plan.experts + 31) >> 5;
+    int e = min(lane * each, p.plan.experts);
+    const unsigned coarse = __ballot_sync(0xFFFFFFFFu, ex.tiles[e] <= it.tile);  // grows with e: lanes 0 .. some
+    const int first = (31 - __clz(coarse)) * each;
+    e = min(first + lane, p.plan.experts);
+    const unsigned fine = __ballot_sync(0xFFFFFFFFu, lane < each && ex.tiles[e] <= it.tile);
+    // experts without pairs share the place of the one behind them, which comes last
+    it.expert = min(first + 31 - __clz(fine), p.plan.experts - 1);
+    const int per = ex.per[it.expert], from = (it.tile - ex.tiles[it.expert]) * per;
+    it.first = ex.start[it.expert] + from;
+    it.cols = max(0, min(per, ex.count[it.expert] - from));
     it.width = max(32, (it.cols + 31) & ~31);
     return it;
 }
@@ -158,6 +179,16 @@ __device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap
         "[%4], %5;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<unsigned short>(3))
         : "memory");
+}
+
+// Whether the phase of this parity is over, without waiting.
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
 }
 
 // One lane of a warp, the same each time.
@@ -229,6 +260,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     ex.tiles = reinterpret_cast<int *>(sgen + Smem::tiles);
     ex.start = ex.tiles + p.plan.experts + 1;
     ex.count = ex.start + p.plan.experts + 1;
+    ex.per = ex.count + p.plan.experts + 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < X_SLOTS; ++i) {
@@ -274,7 +306,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             ex.tiles[e] = before;
             ex.start[e] = start;
             ex.count[e] = count;
-            before += (count + BT - 1) / BT;
+            const int parts = (count + BT - 1) / BT;
+            ex.per[e] = parts ? ((count + parts - 1) / parts + 31) & ~31 : 32;
+            before += parts;
             if (e == p.plan.experts - 1) ex.tiles[p.plan.experts] = before;
         }
     }
@@ -286,11 +320,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int items = ex.tiles[p.plan.experts] * p.row_blocks;
     const int chunks = p.k / CK;
 
+    Items at = items_from(p, pair, num_pairs);
     if (warp == WARP_X) {
         uint32_t it = 0;
         bool ok = true;
-        for (int item = pair; ok && item < items; item += num_pairs) {
-            const Item t = item_at(p, ex, item);
+        while (ok && at.item < items) {
+            const Item t = next_item(p, ex, num_pairs, lane, at);
             // half of the rows for both CTAs; those behind cols are others', and
             // dropped.  One copy of 64 rows a swizzle row where more than 32 are
             // wanted (the other half's rows that it brings are the same ones)
@@ -324,31 +359,33 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
         }
     } else if (warp == WARP_RAW) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int item = pair; ok && item < items; item += num_pairs) {
-                const Item t = item_at(p, ex, item);
-                const int wrow = t.expert * p.n + (G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2)
-                                                     : t.row_block * 2 * BW + static_cast<int>(rank) * BW);
-                for (int c = 0; c < chunks; ++c, ++it) {
-                    const uint32_t s = it % RAW_SLOTS, full = bar(Smem::raw_full + s);
-                    if (!wait_or_abort(bar(Smem::raw_empty + s), ((it / RAW_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
-                        ok = false;
-                        break;
-                    }
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && at.item < items) {
+            const Item t = next_item(p, ex, num_pairs, lane, at);
+            const int wrow = t.expert * p.n + (G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2)
+                                                 : t.row_block * 2 * BW + static_cast<int>(rank) * BW);
+            for (int c = 0; c < chunks; ++c, ++it) {
+                const uint32_t s = it % RAW_SLOTS, full = bar(Smem::raw_full + s);
+                if (!warp_wait_or_abort(bar(Smem::raw_empty + s), ((it / RAW_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
                     mbar_expect_tx_addr(full, RAW_SLOT_BYTES);
                     const uint32_t to = sbase + Smem::raw + s * RAW_SLOT_BYTES;
                     tma_load_2d(to, &tmap_w, c * RAW_ROW, wrow, full);
                     if constexpr (G) tma_load_2d(to + (BW / 2) * RAW_ROW, &tmap_w2, c * RAW_ROW, wrow, full);
                 }
+                __syncwarp();
             }
+        }
+        if (lane == 0)
             for (uint32_t s = 0; s < RAW_SLOTS; ++s)
                 if (it > s) {
                     const uint32_t last = it - 1 - ((it - 1 - s) % RAW_SLOTS);
                     wait_drain(bar(Smem::raw_full + s), (last / RAW_SLOTS) & 1u, ctx);
                 }
-        }
     } else if (warp == WARP_MMA) {
         // the whole warp, so that the operands are known to be the same for all lanes:
         // a thread on its own has to move each to the uniform registers that the
@@ -357,17 +394,27 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t bars = __shfl_sync(0xFFFFFFFFu, bar(0), 0);
         const uint64_t bdesc0 = sw128_desc(__shfl_sync(0xFFFFFFFFu, sbase, 0) + Smem::x);
         const int stages = __shfl_sync(0xFFFFFFFFu, chunks * (CK / SK), 0);
+        auto desc_of = [&](const Item &t) {
+            return kIdesc | static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, t.width, 0) >> 3) << 17;
+        };
+        // both of a stage's barriers at once: each look that succeeds takes some 100 cycles
+        auto look = [&](uint32_t i) {
+            return test_wait(bar(Smem::x_full + i % X_SLOTS), (i / X_SLOTS) & 1u) &&
+                   test_wait(bar(Smem::a_full + i % A_SLOTS), (i / A_SLOTS) & 1u);
+        };
         uint32_t tiles_done = 0, it = 0;
         bool ok = true, issued = false;
         for (int item = pair; ok && item < items; item += num_pairs) {
-            const uint32_t idesc = kIdesc | static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, item_at(p, ex, item).width, 0) >> 3) << 17;
+            const uint32_t idesc = desc_of(next_item(p, ex, num_pairs, lane, at));
             const uint32_t d = tiles_done & 1u;  // accumulator
             if (!warp_wait_or_abort(bar(Smem::d_empty + d), ((tiles_done >> 1) & 1u) ^ 1u, abort_flag, ctx)) break;
             for (int st = 0; st < stages; ++st, ++it) {
                 const uint32_t xs = it % X_SLOTS, as = it % A_SLOTS;
-                ok = warp_wait_or_abort(bar(Smem::x_full + xs), (it / X_SLOTS) & 1u, abort_flag, ctx) &&
-                     warp_wait_or_abort(bar(Smem::a_full + as), (it / A_SLOTS) & 1u, abort_flag, ctx);
-                if (!ok) break;
+                if (!__all_sync(0xFFFFFFFFu, look(it))) {
+                    ok = warp_wait_or_abort(bar(Smem::x_full + xs), (it / X_SLOTS) & 1u, abort_flag, ctx) &&
+                         warp_wait_or_abort(bar(Smem::a_full + as), (it / A_SLOTS) & 1u, abort_flag, ctx);
+                    if (!ok) break;
+                }
                 tc_fence_after();
                 const uint32_t a = tmem + D_COLS + as * A_COLS, to = tmem + d * BT;
                 const uint64_t b = bdesc0 + xs * (X_SLOT_BYTES >> 4);
@@ -389,48 +436,40 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = warp & 3, sub = (warp - WARP_DEQ) >> 2;  // 64 values of K of each chunk
         const int row = G ? (lane >> 4) * (BW / 2) + q * 16 + (lane & 15) : q * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS + (sub % SUBS) * (BK / 2);
-        uint32_t it = 0;
+        const uint32_t total = pair < items ? static_cast<uint32_t>((items - pair + num_pairs - 1) / num_pairs) * chunks : 0u;
+        const uint32_t place = static_cast<uint32_t>(row) * RAW_ROW + 36u * sub;
         bool ok = true;
-        for (int item = pair; ok && item < items; item += num_pairs) {
-            for (int c = 0; c < chunks; ++c, ++it) {
-                const uint32_t r = it % RAW_SLOTS, st = it * (CK / SK) + sub / SUBS, s = st % A_SLOTS;
-                if (!warp_wait_or_abort(bar(Smem::raw_full + r), (it / RAW_SLOTS) & 1u, abort_flag, ctx)) {
-                    ok = false;
-                    break;
-                }
-                // two blocks are nine words; the first's codes begin in the middle of one
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(sgen + Smem::raw + r * RAW_SLOT_BYTES + row * RAW_ROW) + 9 * sub;
-                uint32_t wd[9];
+        for (uint32_t it = 0; ok && it < total; ++it) {
+            const uint32_t r = it % RAW_SLOTS, st = it * (CK / SK) + sub / SUBS, s = st % A_SLOTS;
+            if (!warp_wait_or_abort(bar(Smem::raw_full + r), (it / RAW_SLOTS) & 1u, abort_flag, ctx)) break;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(sgen + Smem::raw + r * RAW_SLOT_BYTES + place);
+            uint32_t wd[9];
 #pragma unroll
-                for (int i = 0; i < 9; ++i) wd[i] = src[i];
-                __syncwarp();
-                if (lane == 0) mbar_arrive_addr(bar(Smem::raw_empty + r));
-                uint32_t v[32];
-                const uint32_t d0 = __byte_perm(wd[0], 0, 0x1010), d1 = __byte_perm(wd[4], 0, 0x3232);
+            for (int i = 0; i < 9; ++i) wd[i] = src[i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive_addr(bar(Smem::raw_empty + r));
+            uint32_t v[32];
+            const uint32_t d0 = __byte_perm(wd[0], 0, 0x1010), d1 = __byte_perm(wd[4], 0, 0x3232);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    weights_of(__byte_perm(wd[i], wd[i + 1], 0x5432), d0, p.magic, v + 4 * i);
-                    weights_of(wd[5 + i], d1, p.magic, v + 16 + 4 * i);
-                }
-                if (!warp_wait_or_abort(bar(Smem::a_empty + s), ((st / A_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                tmem_st_32cols(lane_base + s * A_COLS, v);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_addr(bar(Smem::a_full + s));
+            for (int i = 0; i < 4; ++i) {
+                weights_of(__byte_perm(wd[i], wd[i + 1], 0x5432), d0, p.magic, v + 4 * i);
+                weights_of(wd[5 + i], d1, p.magic, v + 16 + 4 * i);
             }
+            if (!warp_wait_or_abort(bar(Smem::a_empty + s), ((st / A_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) break;
+            tc_fence_after();
+            tmem_st_32cols(lane_base + s * A_COLS, v);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_addr(bar(Smem::a_full + s));
         }
     } else if (warp >= WARP_EPI) {
         const int q = warp & 3, part = (warp - WARP_EPI) >> 2;  // the two warps of a quarter take every other 32 columns
         const bool odd = lane & 1, upper = lane >= 16;
         ulonglong2 *table = reinterpret_cast<ulonglong2 *>(sgen + Smem::cols) + q * BT;
         uint32_t tiles_done = 0;
-        for (int item = pair; item < items; item += num_pairs) {
-            const Item t = item_at(p, ex, item);
+        while (at.item < items) {
+            const Item t = next_item(p, ex, num_pairs, lane, at);
             const uint32_t d = tiles_done & 1u;
             // lanes 2i and 2i + 1 exchange halves of two columns: each then has two
             // neighbouring features f, f + 1 of one
