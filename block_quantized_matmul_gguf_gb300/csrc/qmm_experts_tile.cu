@@ -21,9 +21,9 @@
 //   warp 1      MMA issuer (one thread of the leader)
 //   warp 2      weight producer (both CTAs): boxes of 128 rows x 144 bytes
 //   warps 4-11  epilogue, two for each quarter of the lanes
-//   warps 12-27 dequantisers: TMEM lanes 32 (w % 4) .., every fourth 64-wide K stage.
-//               A stage's weights are formed in registers before its slot is waited
-//               for, so that a free slot is filled at once.
+//   warps 12-27 dequantisers: TMEM lanes 32 (w % 4) .., half of every other chunk of 256
+//               K, which is a stage.  Weights are formed in registers before their slot is
+//               waited for, so that a free slot is filled at once.
 // The binary16 pairs that a word of codes gives without moving its nibbles are
 // values 0 and 2, 1 and 3, so x is written in that order of K too.
 // Which items (expert, tile, row block) there are depends on expert_start: each CTA
@@ -268,12 +268,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init_addr(bar(Smem::x_empty + i), 2);  // both CTAs have read the slot
         }
         for (int i = 0; i < A_SLOTS; ++i) {
-            mbar_init_addr(bar(Smem::a_full + i), DEQ_WARPS * SK / CK);
+            mbar_init_addr(bar(Smem::a_full + i), 4);  // a warp of each quarter
             mbar_init_addr(bar(Smem::a_empty + i), 1);
         }
         for (int i = 0; i < RAW_SLOTS; ++i) {
             mbar_init_addr(bar(Smem::raw_full + i), 1);
-            mbar_init_addr(bar(Smem::raw_empty + i), DEQ_WARPS);
+            mbar_init_addr(bar(Smem::raw_empty + i), DEQ_WARPS / 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init_addr(bar(Smem::d_full + i), 1);
@@ -433,31 +433,40 @@ __global__ void __launch_bounds__(THREADS, 1)
             wait_drain(bar(Smem::final), 0, ctx);
         }
     } else if (warp >= WARP_DEQ) {
-        const int q = warp & 3, sub = (warp - WARP_DEQ) >> 2;  // 64 values of K of each chunk
+        // every other chunk, and of it one stage, as two halves of 64 values of K
+        const int q = warp & 3, set = (warp - WARP_DEQ) >> 2, part = set & 1;
         const int row = G ? (lane >> 4) * (BW / 2) + q * 16 + (lane & 15) : q * 32 + lane;
-        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS + (sub % SUBS) * (BK / 2);
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS;
         const uint32_t total = pair < items ? static_cast<uint32_t>((items - pair + num_pairs - 1) / num_pairs) * chunks : 0u;
-        const uint32_t place = static_cast<uint32_t>(row) * RAW_ROW + 36u * sub;
-        bool ok = true;
-        for (uint32_t it = 0; ok && it < total; ++it) {
-            const uint32_t r = it % RAW_SLOTS, st = it * (CK / SK) + sub / SUBS, s = st % A_SLOTS;
+        const uint32_t place = static_cast<uint32_t>(row) * RAW_ROW + 72u * part;
+        for (uint32_t it = set >> 1; it < total; it += 2) {
+            const uint32_t r = it % RAW_SLOTS, st = it * (CK / SK) + part, s = st % A_SLOTS;
             if (!warp_wait_or_abort(bar(Smem::raw_full + r), (it / RAW_SLOTS) & 1u, abort_flag, ctx)) break;
+            // two blocks are nine words; the first's codes begin in the middle of one
             const uint32_t *src = reinterpret_cast<const uint32_t *>(sgen + Smem::raw + r * RAW_SLOT_BYTES + place);
-            uint32_t wd[9];
+            uint32_t wd[2][9];
 #pragma unroll
-            for (int i = 0; i < 9; ++i) wd[i] = src[i];
+            for (int i = 0; i < 18; ++i) wd[i / 9][i % 9] = src[i];
             __syncwarp();
             if (lane == 0) mbar_arrive_addr(bar(Smem::raw_empty + r));
-            uint32_t v[32];
-            const uint32_t d0 = __byte_perm(wd[0], 0, 0x1010), d1 = __byte_perm(wd[4], 0, 0x3232);
+            bool ok = true;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                weights_of(__byte_perm(wd[i], wd[i + 1], 0x5432), d0, p.magic, v + 4 * i);
-                weights_of(wd[5 + i], d1, p.magic, v + 16 + 4 * i);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                const uint32_t d0 = __byte_perm(wd[h][0], 0, 0x1010), d1 = __byte_perm(wd[h][4], 0, 0x3232);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    weights_of(__byte_perm(wd[h][i], wd[h][i + 1], 0x5432), d0, p.magic, v + 4 * i);
+                    weights_of(wd[h][5 + i], d1, p.magic, v + 16 + 4 * i);
+                }
+                if (h == 0) {
+                    ok = warp_wait_or_abort(bar(Smem::a_empty + s), ((st / A_SLOTS) & 1u) ^ 1u, abort_flag, ctx);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                tmem_st_32cols(lane_base + s * A_COLS + h * (A_COLS / 2), v);
             }
-            if (!warp_wait_or_abort(bar(Smem::a_empty + s), ((st / A_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) break;
-            tc_fence_after();
-            tmem_st_32cols(lane_base + s * A_COLS, v);
+            if (!ok) break;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
