@@ -182,7 +182,7 @@ __device__ __forceinline__ int64_t cache_row(const KvView &c, int64_t slot, int 
 // GPU, else 1.  8191 tokens of 2 x 256 fp32, append and read: 20 us (79 MB,
 // 3.9 TB/s; 27 with 1 and 1, 25 with 4 and 4, 21.4 where the registers allow
 // only 4 and 3 CTAs an SM); 16 tokens: 3.6 us, 5.7 with several.
-constexpr int kAppendMany = 2, kReadMany = 4, kRopeMany = 2;
+constexpr int kAppendMany = 2, kReadMany = 4;
 
 struct Spread {
     int per, par, sub, at;
@@ -422,6 +422,8 @@ __global__ void __launch_bounds__(kThreads, 5) read_kernel(KvView c, const int64
 // append does; with pairs rot/2 apart it also loads the eight that they pair
 // with, which another thread of the CTA loads too (they come from L1).  Bound
 // by the bytes of the inputs and of the queries out.
+constexpr int kRopeThreads = 256;
+
 struct RopeView {
     const float *table;
     const int32_t *positions;
@@ -430,49 +432,80 @@ struct RopeView {
     bool interleaved;
 };
 
-// The eight values at `in` of a head at `src`, rotated by row `turn`.
-template <typename T, bool kWide>
-__device__ __forceinline__ void load_rotated(const T *src, int in, const float *turn, const RopeView &r, float (&x)[8]) {
-    load_eight<kWide>(src + in, x);
-    if (in >= r.rot) return;
-    if constexpr (kWide) {  // rot (interleaved) or rot / 2 is a multiple of 8
-        if (r.interleaved) {
-            const float4 c4 = *reinterpret_cast<const float4 *>(turn + in / 2);
-            const float4 s4 = *reinterpret_cast<const float4 *>(turn + r.half + in / 2);
-            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+// Eight values as they lie in memory.
+template <typename T>
+struct Eight {
+    uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Eight<T> raw_eight(const T *p) {
+    Eight<T> e;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-                x[2 * i + 1] = __fadd_rn(__fmul_rn(a, s[i]), __fmul_rn(b, c[i]));
-            }
-        } else {
-            const bool second = in >= r.half;
-            const int at = second ? in - r.half : in;
-            float y[8];
-            alignas(16) float c[8], s[8];
-            load_eight<kWide>(src + (second ? at : at + r.half), y);
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) e.v[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+    return e;
+}
+__device__ __forceinline__ void unpack(const Eight<float> &e, float (&x)[8]) {
+    const uint32_t w[8] = {e.v[0].x, e.v[0].y, e.v[0].z, e.v[0].w, e.v[1].x, e.v[1].y, e.v[1].z, e.v[1].w};
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {  // rows of the table serve all heads: they stay in L1
-                *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(turn + at + i);
-                *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(turn + r.half + at + i);
-            }
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void unpack(const Eight<uint16_t> &e, float (&x)[8]) {
+    const uint32_t w[4] = {e.v[0].x, e.v[0].y, e.v[0].z, e.v[0].w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = second ? __fadd_rn(__fmul_rn(y[i], s[i]), __fmul_rn(x[i], c[i]))
-                              : __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i], s[i]));
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ void load_four(const float *p, float (&x)[8], int at) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    x[at] = v.x, x[at + 1] = v.y, x[at + 2] = v.z, x[at + 3] = v.w;
+}
+
+// Eight values x at `in` of a head, y those that they pair with (pairs rot / 2
+// apart), rotated by row `turn` of the table; rows and rot are aligned.
+template <bool kInterleaved>
+__device__ __forceinline__ void rotate_eight(float (&x)[8], const float (&y)[8], int in, const float *turn, const RopeView &r) {
+    float c[8], s[8];  // rows of the table serve all heads: they stay in L1
+    if constexpr (kInterleaved) {
+        load_four(turn + in / 2, c, 0);
+        load_four(turn + r.half + in / 2, s, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+            x[2 * i + 1] = __fadd_rn(__fmul_rn(a, s[i]), __fmul_rn(b, c[i]));
         }
     } else {
+        const bool second = in >= r.half;
+        const int at = second ? in - r.half : in;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int at = in + i;
-            if (at >= r.rot) break;
-            const bool second = r.interleaved ? at & 1 : at >= r.half;
-            const int pair = r.interleaved ? at >> 1 : second ? at - r.half : at;
-            const int other = r.interleaved ? at ^ 1 : second ? pair : pair + r.half;
-            const float own = x[i], y = to_float(src[other]), c = turn[pair], s = turn[r.half + pair];
-            x[i] = second ? __fadd_rn(__fmul_rn(y, s), __fmul_rn(own, c)) : __fsub_rn(__fmul_rn(own, c), __fmul_rn(y, s));
+        for (int i = 0; i < 8; i += 4) {
+            load_four(turn + at + i, c, i);
+            load_four(turn + r.half + at + i, s, i);
         }
+        // the second of a pair adds, the first subtracts: a sign that is exact
+        const float sign = second ? 1.0f : -1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i], sign * s[i]));
+    }
+}
+
+// The same value by value, of any alignment.
+template <typename T>
+__device__ __forceinline__ void load_rotated(const T *src, int in, const float *turn, const RopeView &r, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int at = in + i;
+        const float own = to_float(src[at]);
+        x[i] = own;
+        if (at >= r.rot) continue;
+        const bool second = r.interleaved ? at & 1 : at >= r.half;
+        const int pair = r.interleaved ? at >> 1 : second ? at - r.half : at;
+        const int other = r.interleaved ? at ^ 1 : second ? pair : pair + r.half;
+        const float y = to_float(src[other]), c = turn[pair], s = turn[r.half + pair];
+        x[i] = second ? __fadd_rn(__fmul_rn(y, s), __fmul_rn(own, c)) : __fsub_rn(__fmul_rn(own, c), __fmul_rn(y, s));
     }
 }
 
@@ -497,61 +530,78 @@ __device__ __forceinline__ void store_eight(uint16_t *p, const float (&x)[8]) {
     }
 }
 
-template <typename T, bool kWide, int kAhead>
-__global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(KvView c, RopeView r, const T *q, int64_t q_stride, T *q_out,
-                                                                  int64_t q_out_stride, int heads, const T *k, int64_t k_stride,
-                                                                  const T *v, int64_t v_stride, const int64_t *slots,
-                                                                  int64_t n, int dim, LaunchCtx ctx) {
+struct RopeWork {
+    const void *q, *k, *v;
+    void *q_out;
+    const int64_t *slots;
+    int64_t q_stride, q_out_stride, k_stride, v_stride, n;
+    int q_eights, eights;  // of a token's queries, and of its keys
+    int parts;             // q_eights + 2 eights
+    int par;               // tokens of a CTA at a time
+    int dim_shift;
+};
+
+// A thread keeps to one eight of a token (blockIdx.y: which share of the eights,
+// where they are more than threads) and goes through the tokens.
+template <typename T, bool kWide, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 6 : 4) append_rope_kernel(KvView c, RopeView r, const __grid_constant__ RopeWork w,
+                                                                      LaunchCtx ctx) {
     pdl_wait();
     pdl_launch_dependents();
-    const int q_eights = heads * dim / 8, eights = c.kv_heads * dim / 8;
-    const Spread sp(q_eights + 2 * eights);
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * sp.par * kAhead; base < n;
-         base += static_cast<int64_t>(gridDim.x) * sp.par * kAhead) {
-        int64_t slot[kAhead], turn[kAhead];  // -1: the token has none
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int64_t token = base + sp.sub + u * sp.par;
-            const bool there = token < n && sp.at < sp.per;
-            slot[u] = there ? slots[token] : -1;
-            turn[u] = there ? r.positions[token] : -1;
-            if (slot[u] < -1 || slot[u] >= c.slots || turn[u] < -1 || turn[u] >= r.rows) {
-                record_error(ctx, kDevErrIndex);
-                turn[u] = -1;
+    const int dim = 1 << w.dim_shift;
+    const int sub = w.par > 1 ? threadIdx.x / w.parts : 0;
+    const int e = w.par > 1 ? threadIdx.x - sub * w.parts : blockIdx.y * blockDim.x + threadIdx.x;
+    // -1: a thread that is left over; it goes along, for the warp's shuffles
+    const int part = e >= w.parts || sub >= w.par ? -1 : e < w.q_eights ? 0 : e < w.q_eights + w.eights ? 1 : 2;
+    const int at = (e - (part <= 0 ? 0 : part == 1 ? w.q_eights : w.q_eights + w.eights)) * 8;
+    const int head = at >> w.dim_shift, in = at & (dim - 1);
+    const int64_t stride = part <= 0 ? w.q_stride : part == 1 ? w.k_stride : w.v_stride;
+    const T *src = static_cast<const T *>(part <= 0 ? w.q : part == 1 ? w.k : w.v) + at;
+    const bool turned = part >= 0 && part < 2 && in < r.rot;
+    const int other = in < r.half ? r.half : -r.half;  // where the eight it pairs with lies
+    uint8_t *const codes = (part == 2 ? c.v_codes : c.k_codes) + (in / kQK) * 16;
+    __half *const scales = (part == 2 ? c.v_scales : c.k_scales) + in / kQK;
+    const bool any = __any_sync(0xFFFFFFFFu, part > 0);  // keys or values in this warp
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * w.par; t0 < w.n; t0 += static_cast<int64_t>(gridDim.x) * w.par) {
+        const int64_t t = t0 + sub;
+        const bool there = t < w.n && part >= 0;
+        int64_t slot = there && part > 0 ? w.slots[t] : -1;
+        int turn = there ? r.positions[t] : -1;
+        Eight<T> own, pair;
+        if constexpr (kWide)
+            if (there) {
+                own = raw_eight<T>(src + t * stride);
+                if (!kInterleaved && turned) pair = raw_eight<T>(src + t * stride + other);
             }
-            if (turn[u] < 0) slot[u] = -1;
+        if (slot < -1 || slot >= c.slots || turn < -1 || turn >= r.rows) {
+            record_error(ctx, kDevErrIndex);
+            slot = -1;
+            if (turn >= r.rows) turn = -1;
         }
-        for (int i0 = 0; i0 < sp.per; i0 += kThreads) {
-            const int i = i0 + sp.at;
-            const bool here = i < sp.per;
-            const int part = i < q_eights ? 0 : i < q_eights + eights ? 1 : 2;  // query, key, value
-            const int at = (i - (part == 0 ? 0 : part == 1 ? q_eights : q_eights + eights)) * 8;
-            const int head = at / dim, in = at - head * dim;
-            float x[kAhead][8];
+        const bool used = turn >= 0 && (part <= 0 || slot >= 0);
+        float v[8];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int64_t token = base + sp.sub + u * sp.par;
-                const float *row = r.table + turn[u] * r.rot;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[u][j] = 0.0f;
-                if (here && part == 0 && turn[u] >= 0)
-                    load_rotated<T, kWide>(q + token * q_stride + at - in, in, row, r, x[u]);
-                else if (here && part == 1 && slot[u] >= 0)
-                    load_rotated<T, kWide>(k + token * k_stride + at - in, in, row, r, x[u]);
-                else if (here && part == 2 && slot[u] >= 0)
-                    load_eight<kWide>(v + token * v_stride + at, x[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (here && part == 0 && turn[u] >= 0)
-                    store_eight<kWide>(q_out + (base + sp.sub + u * sp.par) * q_out_stride + at, x[u]);
-                const bool write = here && part > 0 && slot[u] >= 0;
-                if (__any_sync(0xFFFFFFFFu, write)) {
-                    const int64_t to = write ? cache_row(c, slot[u], head) : 0;
-                    append_eight(x[u], write, (part == 2 ? c.v_codes : c.k_codes) + to * (dim / 2) + (in / kQK) * 16,
-                                 (part == 2 ? c.v_scales : c.k_scales) + to * (dim / kQK) + in / kQK);
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        if (used) {
+            const float *row = r.table + static_cast<int64_t>(turn) * r.rot;
+            if constexpr (kWide) {
+                unpack(own, v);
+                if (turned) {
+                    float y[8] = {};
+                    if (!kInterleaved) unpack(pair, y);
+                    rotate_eight<kInterleaved>(v, y, in, row, r);
                 }
+            } else if (part == 2) {
+                load_eight<false>(src + t * stride, v);
+            } else {
+                load_rotated<T>(src + t * stride - in, in, row, r, v);
             }
+            if (part == 0) store_eight<kWide>(static_cast<T *>(w.q_out) + t * w.q_out_stride + at, v);
+        }
+        if (any) {
+            const bool write = used && part > 0;
+            const int64_t to = write ? cache_row(c, slot, head) : 0;
+            append_eight(v, write, codes + to * (dim / 2), scales + to * (dim / kQK));
         }
     }
 }
@@ -604,15 +654,23 @@ cudaError_t launch_rope(const KvCache &c, const RopeArgs &a, cudaStream_t stream
     const bool wide = pointers % 16 == 0 && a.k_stride % values == 0 && a.v_stride % values == 0 &&
                       (a.heads == 0 || (a.q_stride % values == 0 && a.q_out_stride % values == 0)) &&
                       a.rot % (a.interleaved ? 8 : 16) == 0;
-    const int parts = (a.heads + 2 * c.kv_heads) * c.head_dim / 8;
-    const bool more = many(a.n, parts, kRopeMany);
-    auto *kernel = wide ? (more ? append_rope_kernel<T, true, kRopeMany> : append_rope_kernel<T, true, 1>)
-                        : (more ? append_rope_kernel<T, false, kRopeMany> : append_rope_kernel<T, false, 1>);
     const RopeView r = {a.table, a.positions, a.table_rows, a.rot, a.rot / 2, a.interleaved};
-    return launch_kernel(kernel, dim3(grid_for(a.n, parts, more ? kRopeMany : 1)), dim3(kThreads), 0, stream, 1, view(c), r,
-                         static_cast<const T *>(a.q), a.q_stride, static_cast<T *>(a.q_out), a.q_out_stride, a.heads,
-                         static_cast<const T *>(a.k), a.k_stride, static_cast<const T *>(a.v), a.v_stride, a.slots, a.n,
-                         c.head_dim, ctx);
+    RopeWork w;
+    w.q = a.q, w.k = a.k, w.v = a.v, w.q_out = a.q_out, w.slots = a.slots;
+    w.q_stride = a.q_stride, w.q_out_stride = a.q_out_stride, w.k_stride = a.k_stride, w.v_stride = a.v_stride, w.n = a.n;
+    w.q_eights = a.heads * c.head_dim / 8;
+    w.eights = c.kv_heads * c.head_dim / 8;
+    w.parts = w.q_eights + 2 * w.eights;
+    w.dim_shift = c.head_dim == 64 ? 6 : c.head_dim == 128 ? 7 : 8;
+    w.par = std::max(1, kRopeThreads / w.parts);
+    // whole warps, as many as a token has eights, or its equal shares
+    const int shares = (w.parts + kRopeThreads - 1) / kRopeThreads;
+    const int threads = w.par > 1 ? kRopeThreads : ((w.parts + shares - 1) / shares + 31) / 32 * 32;
+    auto *kernel = !wide ? append_rope_kernel<T, false, false>
+                         : a.interleaved ? append_rope_kernel<T, true, true> : append_rope_kernel<T, true, false>;
+    const int64_t cap = static_cast<int64_t>(device_sm_count()) * 32;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a.n + w.par - 1) / w.par, cap));
+    return launch_kernel(kernel, dim3(grid, shares), dim3(threads), 0, stream, 1, view(c), r, w, ctx);
 }
 
 }  // namespace

@@ -38,7 +38,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSpan = 64;         // tokens of a bit mask, at most
 constexpr int kMaxChunks = 256;   // CTAs: more tokens take more a CTA
 constexpr int kMaxCluster = 8;
-constexpr int kMore = 4;          // candidates beyond topk
+constexpr int kMore = 2;          // candidates beyond topk
 constexpr float kInf = __builtin_huge_valf();
 
 struct RouteParams {
@@ -223,11 +223,10 @@ __device__ __forceinline__ bool choose_by_words(const RouteArgs &a, const uint32
         last = warp_max(w[0]);
         if (last == 0) break;  // none left
         if (lane == r) got = last;
-        if (w[0] == last) {
+        const bool hit = w[0] == last;
 #pragma unroll
-            for (int j = 0; j + 1 < V; ++j) w[j] = w[j + 1];
-            w[V - 1] = 0;
-        }
+        for (int j = 0; j + 1 < V; ++j) w[j] = hit ? w[j + 1] : w[j];
+        w[V - 1] = hit ? 0 : w[V - 1];
     }
     if (__popc(__ballot_sync(0xFFFFFFFFu, got != 0)) < a.topk) return false;  // what is no number has no word
     mine = static_cast<int>(kIndex - (got & kIndex));

@@ -382,8 +382,8 @@ qmm_status qmm_kv_append_q4_0(const qmm_kv_q4_0 *cache, const void *k, int64_t k
  *   positions  int32 [n], row of the table; -1 skips the token whole, its row
  *              of q_out is left as it was (a plan's padding)
  *   slots      as above; -1 skips the append, the query is rotated
- * A position or slot outside its array records QMM_ERR_INDEX and skips the
- * token.  k, v, q and q_out are of one type, strides count elements; heads is
+ * A position outside the table records QMM_ERR_INDEX and skips the token, a slot
+ * outside the cache records it and skips the append.  k, v, q and q_out are of one type, strides count elements; heads is
  * the number of query heads.
  * Requires n >= 0 (0 launches nothing), n <= 2^30, rot even and 2 <= rot <=
  * head_dim, table_rows >= 1, strides at least the rows' widths, heads >= 1

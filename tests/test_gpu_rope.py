@@ -119,7 +119,7 @@ def test_tokens_left_out(qmm):
     q_out = torch.full((n, heads, dim), 7.0, device="cuda")
     qmm.qmm_kv_append_rope_q4_0(cache, k, v, slots, positions, table, q=q, q_out=q_out)
     assert qmm.qmm_get_device_error() == qmm.QMM_ERR_INDEX  # slot 40
-    want_slots, want_pos = [3, -1, -1, -1, -1, 7], [9, 4, -1, -1, -1, 1]
+    want_slots, want_pos = [3, -1, -1, -1, -1, 7], [9, 4, -1, -1, 2, 1]  # its query is rotated
     same(arrays(cache), expected(cache, k.cpu().numpy(), v.cpu().numpy(), want_slots, want_pos, table.cpu().numpy(), dim, False))
     want = experts_ref.turn(q.cpu().numpy(), table.cpu().numpy(), want_pos, dim, False)
     for i, p in enumerate(want_pos):
