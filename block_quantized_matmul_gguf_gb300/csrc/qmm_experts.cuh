@@ -30,7 +30,7 @@
 // different banks.
 #pragma once
 
-#include "qmm_internal.h"
+#include "qmm_tc.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,10 +40,11 @@
 namespace qmm {
 namespace experts {
 
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 8;
 constexpr int kStages = 2;
 constexpr int kChunk = 256;   // K values of a stage
-constexpr int kRows = 32;     // weight rows of an item
+constexpr int kTiles = 4;     // of 16 weight rows, of an item
+constexpr int kRows = 16 * kTiles;
 
 struct StreamParams {
     ExpertsPlan plan;
@@ -87,8 +88,7 @@ __device__ __forceinline__ float high_half(uint32_t v) { return __high2float(*re
 // d = a b + c, a 16 x 16 (row), b 16 x 8 (column), fp32 sums
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -118,13 +118,13 @@ struct StreamLayout {
     __host__ __device__ static int part(int warps, int panel) {
         return sums(warps, panel) + (EXACT ? 0 : panel * 8 * NB * 32);
     }
-    __host__ __device__ static int rows(int warps, int panel) { return part(warps, panel) + warps * NB * 1024; }
+    __host__ __device__ static int rows(int warps, int panel) { return part(warps, panel) + warps * NB * kTiles * 512; }
     __host__ __device__ static int total(int warps, int panel) { return rows(warps, panel) + 2 * 8 * NB * 4 + 64; }
 };
 
 // A place in a CTA's run of items.
 struct Place {
-    int64_t left;  // items of the run from here on
+    int left;  // items of the run from here on
     int expert, group, row_group;
     int start, count;  // of the expert's pairs
 };
@@ -159,25 +159,30 @@ __device__ __forceinline__ void advance(const StreamParams &p, Place &at) {
     }
 }
 
-// 32 rows x one chunk of weights into a stage of this warp's ring.
-template <bool GEGLU, bool ALIGNED>
-__device__ __forceinline__ void load_stage(const StreamParams &p, uint32_t stage, int expert, int64_t row0, int chunk, int lane) {
-    constexpr int pitch = ALIGNED ? 144 : 176;
-    constexpr int pieces = ALIGNED ? 9 : 10;
+// An item's rows x one chunk of weights into a stage of this warp's ring: by TMA
+// boxes where rows allow it, else as the windows of 16-byte pieces that hold them.
+template <bool GEGLU>
+__device__ __forceinline__ void load_boxes(const StreamParams &p, const CUtensorMap *w0, const CUtensorMap *w1, uint32_t stage,
+                                           uint32_t bar, int expert, int64_t row0, int chunk) {
+    const int row = static_cast<int>(expert * p.n + row0);  // rows behind the expert's are not stored
+    mbar_expect_tx_addr(bar, kRows * 144);
+    tma_load_2d(stage, w0, chunk * 144, row, bar);
+    if constexpr (GEGLU) tma_load_2d(stage + kRows / 2 * 144, w1, chunk * 144, row, bar);
+}
+template <bool GEGLU>
+__device__ __forceinline__ void load_windows(const StreamParams &p, uint32_t stage, int expert, int64_t row0, int chunk, int lane) {
+    constexpr int pitch = 176, pieces = 10;
+    constexpr int rows = GEGLU ? kRows / 2 : kRows;  // of a matrix
+    const int64_t first = expert * p.matrix_bytes + chunk * 144;
     const int bytes = min(8, p.blocks - chunk * 8) * kQ4_0Bytes;
-#pragma unroll
-    for (int i = 0; i < pieces; ++i) {
-        const int at = i * 32 + lane, row = at / pieces, piece = at - row * pieces;
-        const int64_t r = row0 + (GEGLU ? row & 15 : row);
-        const int64_t from = expert * p.matrix_bytes + min(r, p.n - 1) * p.row_bytes + chunk * 144;
-        const uint8_t *w = p.w[GEGLU ? row >> 4 : 0];
-        if constexpr (ALIGNED) {
-            copy16(stage + row * pitch + piece * 16, w + from + piece * 16, 16);
-        } else {
-            const int64_t first = (from & ~int64_t(15)) + piece * 16;
-            if (first < from + bytes)
-                copy16(stage + row * pitch + piece * 16, w + first, static_cast<uint32_t>(min(int64_t(16), p.w_bytes - first)));
-        }
+#pragma unroll 1
+    for (int i = 0; i < pieces * kRows / 32; ++i) {
+        const int idx = i * 32 + lane, row = idx / pieces, piece = idx - row * pieces;
+        const int64_t r = row0 + row % rows;
+        const int64_t from = first + min(r, p.n - 1) * p.row_bytes;
+        const int64_t window = (from & ~int64_t(15)) + piece * 16;
+        if (window < from + bytes)
+            copy16(stage + row * pitch + piece * 16, p.w[row / rows] + window, static_cast<uint32_t>(min(int64_t(16), p.w_bytes - window)));
     }
 }
 
@@ -207,7 +212,7 @@ __device__ __forceinline__ float4 load_four<uint16_t>(const uint16_t *p, bool wi
 // pair g's values 4t..4t+3 and 16+4t..16+4t+3 of each block, in the order that
 // the codes of a word have.
 template <bool EXACT, int PARTS, int NB, typename T>
-__device__ __forceinline__ void stage_x(const StreamParams &p, char *xs, float *scale, float *sums, const T *row, int chunk,
+__device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *scale, float *sums, const T *row, int chunk,
                                         int nb, int lane) {
     const int t = lane & 3, g = lane >> 2;
     const int blocks = min(8, p.blocks - chunk * 8);
@@ -264,18 +269,18 @@ __device__ __forceinline__ void stage_x(const StreamParams &p, char *xs, float *
 // both tiles) begins behind its window.
 template <bool EXACT, int PARTS, int NB, bool ALIGNED>
 __device__ __forceinline__ void stage_products(const char *stage, const char *xs, const float *scale, const float *sums,
-                                               int blocks, const int (&skew)[2][2], uint32_t magic, int lane,
-                                               int used, float (&total)[2][NB][4]) {
+                                               int blocks, const int (&skew)[kTiles][2], uint32_t magic, int lane,
+                                               int used, float (&total)[kTiles][NB][4]) {
     constexpr int pitch = ALIGNED ? 144 : 176;
     const int t = lane & 3, g = lane >> 2;
-    float acc[2][NB][4];
+    float acc[kTiles][NB][4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < kTiles; ++r)
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
-    auto block = [&](int b, const uint32_t (&q)[2][2], const float (&d)[2][2]) {
+    auto block = [&](int b, const uint32_t (&q)[kTiles][2], const float (&d)[kTiles][2]) {
         uint32_t x[NB][PARTS][4];
         float c[NB][2];
 #pragma unroll
@@ -292,37 +297,50 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
                 }
             }
         }
+        // the products of the tiles take turns: each waits for the one before it of
+        // its own sum
+        uint32_t a[kTiles][8];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < kTiles; ++r) {
             const uint32_t u = q[r][0], v = q[r][1], u8 = u >> 8, v8 = v >> 8;
-            uint32_t a[8];
             if constexpr (EXACT) {
-                a[0] = hadd2((u & 0x000F000Fu) | magic, 0xE408E408u);  // - 1032
-                a[1] = hadd2((v & 0x000F000Fu) | magic, 0xE408E408u);
-                a[2] = hadd2((u8 & 0x000F000Fu) | magic, 0xE408E408u);
-                a[3] = hadd2((v8 & 0x000F000Fu) | magic, 0xE408E408u);
-                a[4] = hfma2((u & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
-                a[5] = hfma2((v & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
-                a[6] = hfma2((u8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
-                a[7] = hfma2((v8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+                a[r][0] = hadd2((u & 0x000F000Fu) | magic, 0xE408E408u);  // - 1032
+                a[r][1] = hadd2((v & 0x000F000Fu) | magic, 0xE408E408u);
+                a[r][2] = hadd2((u8 & 0x000F000Fu) | magic, 0xE408E408u);
+                a[r][3] = hadd2((v8 & 0x000F000Fu) | magic, 0xE408E408u);
+                a[r][4] = hfma2((u & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
+                a[r][5] = hfma2((v & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+                a[r][6] = hfma2((u8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+                a[r][7] = hfma2((v8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
             } else {
-                a[0] = u & 0x000F000Fu, a[1] = v & 0x000F000Fu, a[2] = u8 & 0x000F000Fu, a[3] = v8 & 0x000F000Fu;
-                a[4] = u & 0x00F000F0u, a[5] = v & 0x00F000F0u, a[6] = u8 & 0x00F000F0u, a[7] = v8 & 0x00F000F0u;
+                a[r][0] = u & 0x000F000Fu, a[r][1] = v & 0x000F000Fu, a[r][2] = u8 & 0x000F000Fu, a[r][3] = v8 & 0x000F000Fu;
+                a[r][4] = u & 0x00F000F0u, a[r][5] = v & 0x00F000F0u, a[r][6] = u8 & 0x00F000F0u, a[r][7] = v8 & 0x00F000F0u;
             }
+        }
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                if (n < used) {
-                    float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if constexpr (!EXACT) z[0] = z[2] = c[n][0], z[1] = z[3] = c[n][1];
+        for (int n = 0; n < NB; ++n) {
+            if (n < used) {
+                float z[kTiles][4];
 #pragma unroll
-                    for (int s = PARTS - 1; s >= 0; --s) {  // the small part first
-                        mma16816(z, a[0], a[1], a[2], a[3], x[n][s][0], x[n][s][1]);
-                        mma16816(z, a[4], a[5], a[6], a[7], x[n][s][2], x[n][s][3]);
-                    }
-                    acc[r][n][0] = fmaf(d[r][0], z[0], acc[r][n][0]);
-                    acc[r][n][1] = fmaf(d[r][0], z[1], acc[r][n][1]);
-                    acc[r][n][2] = fmaf(d[r][1], z[2], acc[r][n][2]);
-                    acc[r][n][3] = fmaf(d[r][1], z[3], acc[r][n][3]);
+                for (int r = 0; r < kTiles; ++r) {
+                    z[r][0] = z[r][2] = EXACT ? 0.0f : c[n][0];
+                    z[r][1] = z[r][3] = EXACT ? 0.0f : c[n][1];
+                }
+#pragma unroll
+                for (int s = PARTS - 1; s >= 0; --s) {  // the small part first
+#pragma unroll
+                    for (int r = 0; r < kTiles; ++r)
+                        mma16816(z[r], a[r][0], a[r][1], a[r][2], a[r][3], x[n][s][0], x[n][s][1]);
+#pragma unroll
+                    for (int r = 0; r < kTiles; ++r)
+                        mma16816(z[r], a[r][4], a[r][5], a[r][6], a[r][7], x[n][s][2], x[n][s][3]);
+                }
+#pragma unroll
+                for (int r = 0; r < kTiles; ++r) {
+                    acc[r][n][0] = fmaf(d[r][0], z[r][0], acc[r][n][0]);
+                    acc[r][n][1] = fmaf(d[r][0], z[r][1], acc[r][n][1]);
+                    acc[r][n][2] = fmaf(d[r][1], z[r][2], acc[r][n][2]);
+                    acc[r][n][3] = fmaf(d[r][1], z[r][3], acc[r][n][3]);
                 }
             }
         }
@@ -330,12 +348,12 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
     if constexpr (ALIGNED) {
         // two blocks are nine words: the first block's codes begin in the
         // middle of a word, the second's at one
-#pragma unroll
+#pragma unroll 2
         for (int j = 0; j < 4; ++j) {
-            uint32_t q0[2][2], q1[2][2];
-            float d0[2][2], d1[2][2];
+            uint32_t q0[kTiles][2], q1[kTiles][2];
+            float d0[kTiles][2], d1[kTiles][2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < kTiles; ++r)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const char *row = stage + (r * 16 + h * 8 + g) * pitch + 36 * j;
@@ -351,10 +369,10 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
     } else {
 #pragma unroll 1
         for (int b = 0; b < blocks; ++b) {
-            uint32_t q[2][2];
-            float d[2][2];
+            uint32_t q[kTiles][2];
+            float d[kTiles][2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < kTiles; ++r)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const char *row = stage + (r * 16 + h * 8 + g) * pitch;
@@ -370,7 +388,7 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
     for (int n = 0; n < NB; ++n) {
         const float2 s = *reinterpret_cast<const float2 *>(scale + n * 8 + 2 * t);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < kTiles; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float v = EXACT ? acc[r][n][i] : acc[r][n][i] * 16777216.0f;
@@ -393,7 +411,9 @@ __device__ __forceinline__ void put(void *out, int64_t at, bool bf16, float v) {
 }
 
 template <bool EXACT, int PARTS, int NB, bool GEGLU, bool ALIGNED>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_constant__ StreamParams p) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_constant__ CUtensorMap w0,
+                                                                   const __grid_constant__ CUtensorMap w1,
+                                                                   const __grid_constant__ StreamParams p) {
     using L = StreamLayout<EXACT, PARTS, NB, ALIGNED>;
     extern __shared__ __align__(128) char smem[];
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -454,7 +474,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                 ahead += units;
             }
             found[4] = static_cast<int>(from - static_cast<int64_t>(unit) * p.row_groups);
-            *reinterpret_cast<int64_t *>(found + 6) = to - from;
+            found[5] = static_cast<int>(to - from);
         }
         __syncthreads();
     }
@@ -464,63 +484,68 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
     at.start = found[2];
     at.count = found[3];
     at.row_group = found[4];
-    at.left = *reinterpret_cast<const int64_t *>(found + 6);
+    at.left = found[5];
 
-    constexpr int kItemRows = GEGLU ? 16 : 32;
+    constexpr int kItemRows = GEGLU ? kRows / 2 : kRows;
+    constexpr int kPairs = GEGLU ? kTiles / 2 : kTiles;  // tiles of out
     const uint32_t ring = smem_addr(smem) + warp * kStages * L::stage;
     const char *ring_ptr = smem + warp * kStages * L::stage;
 
-    // Loads run kStages - 1 chunks ahead, through the items.
-    Place load = at;
-    int load_chunk = kw;
-    int loaded = 0;
-    auto load_next = [&]() {
-        while (load.left > 0 && load_chunk >= p.chunks) {
-            advance<NB>(p, load);
-            load_chunk = kw;
-            if (kw >= p.chunks) load.left = 0;
+    // A chunk of weights is on its way while the one before is worked on, through the
+    // items.  A wait that runs out leaves the rest undone, but not the barriers.
+    __shared__ alignas(8) uint64_t bars[kMaxWarps][kStages];
+    bool ok = true;
+    if constexpr (ALIGNED) {
+        if (lane < kStages) mbar_init(&bars[warp][lane], 1);
+        fence_mbar_init();
+        __syncwarp();
+    }
+    auto load = [&](const Place &from, int chunk, int turn) {
+        const int slot = turn & (kStages - 1);
+        const int64_t row0 = (static_cast<int64_t>(from.row_group) * p.rw + rw) * kItemRows;
+        const bool there = from.left > 0 && row0 < p.n && ok;
+        if constexpr (ALIGNED) {
+            if (there && lane == 0)
+                load_boxes<GEGLU>(p, &w0, &w1, ring + slot * L::stage, smem_addr(&bars[warp][slot]), from.expert, row0, chunk);
+        } else {
+            if (there) load_windows<GEGLU>(p, ring + slot * L::stage, from.expert, row0, chunk, lane);
+            copy_commit();
         }
-        if (load.left > 0) {
-            const int64_t row0 = (static_cast<int64_t>(load.row_group) * p.rw + rw) * kItemRows;
-            if (row0 < p.n)
-                load_stage<GEGLU, ALIGNED>(p, ring + (loaded & (kStages - 1)) * L::stage, load.expert, row0, load_chunk, lane);
-            load_chunk += p.kw;
-            ++loaded;
-        }
-        copy_commit();
     };
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) load_next();
+    uint32_t parity = 0;  // of each stage's barrier, a bit
+    load(at, kw, 0);
 
     int done = 0;
     int held_expert = -1, held_group = -1, held_panel = -1;
     const int panels = (p.chunks + p.x_panel - 1) / p.x_panel;
-    for (; at.left > 0; advance<NB>(p, at)) {
+    while (at.left > 0) {
+        Place next = at;
         const int64_t row0 = (static_cast<int64_t>(at.row_group) * p.rw + rw) * kItemRows;
         const bool there = row0 < p.n;
         const int first = at.start + at.group * 8 * NB;              // of the pairs
         const int cols = min(8 * NB, at.count - at.group * 8 * NB);  // of them here
         const int used = (cols + 7) / 8;
-        float total[2][NB][4];
+        float total[kTiles][NB][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < kTiles; ++r)
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) total[r][n][i] = 0.0f;
-        int skew[2][2] = {{0, 0}, {0, 0}};
+        int skew[kTiles][2] = {};
         if constexpr (!ALIGNED) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < kTiles; ++r)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int64_t row = row0 + (GEGLU ? 0 : r * 16) + h * 8 + g;
+                    const int64_t row = row0 + r % kPairs * 16 + h * 8 + g;
                     skew[r][h] = static_cast<int>((at.expert * p.matrix_bytes + min(row, p.n - 1) * p.row_bytes) & 15);
                 }
         }
         for (int panel = 0; panel < panels; ++panel) {
             const int c0 = panel * p.x_panel, c1 = min(p.chunks, c0 + p.x_panel);
             if (at.expert != held_expert || at.group != held_group || panel != held_panel) {
+                bool other = panel != held_panel;  // the rows of x are not those that shared memory holds
                 __syncthreads();
                 if (at.expert != held_expert || at.group != held_group) {
                     if (threadIdx.x < 8 * NB) {
@@ -535,71 +560,82 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                                 record_error(p.ctx, kDevErrIndex);
                             }
                         }
+                        other |= held_expert < 0 || src[c] != from;  // experts of one token have one row
                         src[c] = from;
                         dst[c] = to;
                     }
-                    __syncthreads();
+                    other = __syncthreads_or(other);
                 }
-                for (int u = warp; u < (c1 - c0) * used; u += warps) {
-                    const int n = u % used, c = u / used;
-                    const int row = src[n * 8 + g];
-                    // addresses count from the panel's first chunk
-                    char *xp = xs - static_cast<int64_t>(c0) * 8 * L::x_block;
-                    float *sp = scale - c0 * 8 * NB, *mp = sums - c0 * 64 * NB;
-                    if (p.x_bf16)
-                        stage_x<EXACT, PARTS, NB, uint16_t>(
-                            p, xp, sp, mp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane);
-                    else
-                        stage_x<EXACT, PARTS, NB, float>(
-                            p, xp, sp, mp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane);
-                }
+                if (other)
+                    for (int u = warp; u < (c1 - c0) * used; u += warps) {
+                        const int n = u % used, c = u / used;
+                        const int row = src[n * 8 + g];
+                        // addresses count from the panel's first chunk
+                        char *xp = xs - static_cast<int64_t>(c0) * 8 * L::x_block;
+                        float *sp = scale - c0 * 8 * NB, *mp = sums - c0 * 64 * NB;
+                        if (p.x_bf16)
+                            stage_x<EXACT, PARTS, NB, uint16_t>(
+                                p, xp, sp, mp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane);
+                        else
+                            stage_x<EXACT, PARTS, NB, float>(
+                                p, xp, sp, mp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane);
+                    }
                 held_expert = at.expert;
                 held_group = at.group;
                 held_panel = panel;
                 __syncthreads();
             }
             for (int c = c0 + (kw - c0 % p.kw + p.kw) % p.kw; c < c1; c += p.kw) {
-                load_next();
-                copy_wait<kStages - 1>();
-                __syncwarp();
-                if (there)
+                if (c + p.kw < p.chunks) {
+                    load(at, c + p.kw, done + 1);
+                } else {
+                    advance<NB>(p, next);
+                    load(next, kw, done + 1);
+                }
+                if constexpr (ALIGNED) {
+                    if (there && ok) {
+                        const int slot = done & (kStages - 1);
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars[warp][slot], parity >> slot & 1u, p.ctx));
+                        parity ^= 1u << slot;
+                    }
+                } else {
+                    copy_wait<1>();
+                    __syncwarp();
+                }
+                if (there && ok)
                     stage_products<EXACT, PARTS, NB, ALIGNED>(
-                        ring_ptr + (done & (kStages - 1)) * L::stage, xs + (c - c0) * 8 * L::x_block, scale + (c - c0) * 8 * NB,
+                        ring_ptr + (done & 1) * L::stage, xs + (c - c0) * 8 * L::x_block, scale + (c - c0) * 8 * NB,
                         sums + (c - c0) * 64 * NB, min(8, p.blocks - c * 8), skew, p.magic, lane, used, total);
                 __syncwarp();
                 ++done;
             }
         }
         // the item's sums: element (r, n, i) of lane is row 16 r + 8 (i / 2) + g, pair 8 n + 2 t + i % 2
+        auto store = [&](int r, int i, int l, int to, float a, float b) {
+            const int64_t row = row0 + 16 * r + 8 * (i >> 1) + (l >> 2);
+            if (to >= 0 && row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, GEGLU ? gelu(a) * b : a);
+        };
         if (p.kw > 1) {
-            float *mine = part + warp * NB * 256;
+            constexpr int kWords = kTiles * NB * 128;  // of a warp's sums
+            float *mine = part + warp * kWords;
             barrier(1 + rw, p.kw * 32);  // the last item's sums are read
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < kTiles; ++r)
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
                     reinterpret_cast<float4 *>(mine)[(r * NB + n) * 32 + lane] =
                         make_float4(total[r][n][0], total[r][n][1], total[r][n][2], total[r][n][3]);
             barrier(1 + rw, p.kw * 32);
-            const float *all = part + rw * p.kw * NB * 256;
+            const float *all = part + rw * p.kw * kWords;
             if (there)
-                for (int v = kw * 32 + lane; v < NB * 128; v += p.kw * 32) {
+                for (int v = kw * 32 + lane; v < kPairs * NB * 128; v += p.kw * 32) {
                     float a = 0.0f, b = 0.0f;
                     for (int w = 0; w < p.kw; ++w) {
-                        a += all[w * NB * 256 + v];
-                        b += all[w * NB * 256 + NB * 128 + v];
+                        a += all[w * kWords + v];
+                        if constexpr (GEGLU) b += all[w * kWords + kPairs * NB * 128 + v];
                     }
-                    const int i = v & 3, l = (v >> 2) & 31, n = v >> 7;
-                    const int col = 8 * n + 2 * (l & 3) + (i & 1);
-                    const int64_t row = row0 + 8 * (i >> 1) + (l >> 2);
-                    const int to = dst[col];
-                    if (to < 0) continue;
-                    if constexpr (GEGLU) {
-                        if (row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, gelu(a) * b);
-                    } else {
-                        if (row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, a);
-                        if (row + 16 < p.n) put(p.out, to * p.out_stride + row + 16, p.out_bf16, b);
-                    }
+                    const int i = v & 3, l = (v >> 2) & 31, n = (v >> 7) % NB, r = v / (NB * 128);
+                    store(r, i, l, dst[8 * n + 2 * (l & 3) + (i & 1)], a, b);
                 }
         } else if (there) {
 #pragma unroll
@@ -607,16 +643,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int to = dst[8 * n + 2 * t + (i & 1)];
-                    const int64_t row = row0 + 8 * (i >> 1) + g;
-                    if (to < 0) continue;
-                    if constexpr (GEGLU) {
-                        if (row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, gelu(total[0][n][i]) * total[1][n][i]);
-                    } else {
-                        if (row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, total[0][n][i]);
-                        if (row + 16 < p.n) put(p.out, to * p.out_stride + row + 16, p.out_bf16, total[1][n][i]);
-                    }
+#pragma unroll
+                    for (int r = 0; r < kPairs; ++r) store(r, i, lane, to, total[r][n][i], total[GEGLU ? r + kPairs : r][n][i]);
                 }
         }
+        at = next;
     }
     copy_wait<0>();
 }
@@ -630,18 +661,43 @@ cudaError_t launch_stream(StreamParams p, cudaStream_t stream) {
     // as many warps as fit beside all of x, four at least, and x in panels beyond that
     int warps = kMaxWarps;
     p.x_panel = p.chunks;
-    while (warps > 4 && L::total(warps, p.x_panel) > kSharedLimit) warps -= 4;
+    while (warps > 4 && L::total(warps, p.x_panel) > kSharedLimit) warps -= 2;
     while (L::total(warps, p.x_panel) > kSharedLimit) --p.x_panel;
-    p.kw = std::min(p.chunks, std::min(warps, 8));
+    // How many warps share an item: many where there are few items (their chunks
+    // follow one another), few where there are many (their sums meet).  In units of a
+    // chunk's time, an item costs its chunks and 0.6 for the sums; the pairs are taken
+    // to spread evenly over the experts.  1, 2, 4 and 8 warps: one token on 8 of 64
+    // experts of 1024 x 2048 29, 16.5, 11.2 and 12.1 us; 16 tokens 60, 44, 46, 55.
+    constexpr int rows = GEGLU ? kRows / 2 : kRows;
+    const int64_t each = (p.plan.pairs_total + p.plan.experts * 8 * NB - 1) / (p.plan.experts * 8 * NB);
+    const int64_t units = std::min(p.plan.pairs_total, p.plan.experts * each);
+    int best = 1;
+    double least = 0.0;
+    for (int kw = 1; kw <= std::min(p.chunks, warps); ++kw) {
+        const int rw = warps / kw;
+        const double items = static_cast<double>(units) * ((p.n + rows * rw - 1) / (rows * rw)) / device_sm_count();
+        const double cost = (items <= 1.0 ? 1.0 : items + 0.5) * ((p.chunks + kw - 1) / kw + (kw > 1 ? 0.6 : 0.0));
+        if (kw == 1 || cost < least) {
+            best = kw;
+            least = cost;
+        }
+    }
+    p.kw = best;
     p.rw = warps / p.kw;
-    warps = p.rw * p.kw;
-    constexpr int rows = GEGLU ? 16 : 32;
     p.row_groups = static_cast<int>((p.n + rows * p.rw - 1) / (rows * p.rw));
+    warps = p.rw * p.kw;
     const int smem = L::total(warps, p.x_panel);
     const cudaError_t e = ensure_smem(stream_kernel<EXACT, PARTS, NB, GEGLU, ALIGNED>, smem, false, limits);
     if (e != cudaSuccess) return e;
+    CUtensorMap w0 = {}, w1 = {};
+    if constexpr (ALIGNED) {
+        const uint64_t all = static_cast<uint64_t>(p.plan.experts) * p.n;
+        if (!encode_tmap_2d(&w0, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w[0], p.row_bytes, all, p.row_bytes, 144, rows) ||
+            !encode_tmap_2d(&w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w[GEGLU ? 1 : 0], p.row_bytes, all, p.row_bytes, 144, rows))
+            return cudaErrorInvalidValue;
+    }
     return launch_kernel(stream_kernel<EXACT, PARTS, NB, GEGLU, ALIGNED>, dim3(device_sm_count()), dim3(warps * 32), smem, stream,
-                         1, p);
+                         1, w0, w1, p);
 }
 
 template <bool GEGLU, bool ALIGNED, int NB>
@@ -661,7 +717,7 @@ cudaError_t launch_form(StreamParams &p, bool exact, cudaStream_t stream) {
     p.w_bytes = p.matrix_bytes * p.plan.experts;
     p.magic = 0x64006400u;
     p.x_wide = reinterpret_cast<uintptr_t>(p.x) % (p.x_bf16 ? 8 : 16) == 0 && p.x_stride % 4 == 0;  // loads of four
-    const bool aligned = p.k % kChunk == 0;
+    const bool aligned = p.k % kChunk == 0 && p.plan.experts * p.n < (int64_t(1) << 31);  // a box's row is 32 bits
     const bool many = p.plan.pairs_total > 8 * static_cast<int64_t>(p.plan.experts);
     if (aligned)
         return many ? launch_precision<GEGLU, true, 2>(p, exact, stream) : launch_precision<GEGLU, true, 1>(p, exact, stream);
