@@ -19,15 +19,15 @@
 // numbers n - 8, because the tensor cores' sums of subnormal operands keep some 18
 // bits only.
 //
-// Work.  An item is 32 rows of weights (16 gate and the same 16 up rows for
-// GeGLU) of one expert against one group of 8 NB of its pairs.  A CTA of up to 16
+// Work.  An item is 64 rows of weights (32 gate and the same 32 up rows for
+// GeGLU) of one expert against one group of 8 NB of its pairs.  A CTA of up to 8
 // warps, one an SM, walks through its own run of items: RW items at a time, each
 // by KW warps that take every KW-th 256 values of K and add their sums in shared
 // memory in a fixed order.  The group's x lies in shared memory as the
-// instruction wants it, made once while the items stay with the group.  Each
-// warp's weights arrive through its own ring of asynchronous copies, 32 rows x 144
-// bytes a stage, so that the eight rows that a quarter of a load touches lie in
-// different banks.
+// instruction wants it, made once while the items stay with the group, or with
+// rows of the same token.  Each warp's weights arrive through its own two stages of
+// 64 rows x 144 bytes, so that the eight rows that a quarter of a load touches lie
+// in different banks: by TMA where K is a multiple of 256, by cp.async otherwise.
 #pragma once
 
 #include "qmm_tc.cuh"
@@ -36,6 +36,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 
 namespace qmm {
 namespace experts {
@@ -264,9 +265,9 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
     }
 }
 
-// A warp's products of one stage: two tiles of 16 rows against NB groups of
+// A warp's products of one stage: kTiles tiles of 16 rows against NB groups of
 // eight pairs.  skew: bytes by which each of the lane's four rows (g, g + 8 of
-// both tiles) begins behind its window.
+// each tile) begins behind its window.
 template <bool EXACT, int PARTS, int NB, bool ALIGNED>
 __device__ __forceinline__ void stage_products(const char *stage, const char *xs, const float *scale, const float *sums,
                                                int blocks, const int (&skew)[kTiles][2], uint32_t magic, int lane,
@@ -664,19 +665,24 @@ cudaError_t launch_stream(StreamParams p, cudaStream_t stream) {
     while (warps > 4 && L::total(warps, p.x_panel) > kSharedLimit) warps -= 2;
     while (L::total(warps, p.x_panel) > kSharedLimit) --p.x_panel;
     // How many warps share an item: many where there are few items (their chunks
-    // follow one another), few where there are many (their sums meet).  In units of a
-    // chunk's time, an item costs its chunks and 0.6 for the sums; the pairs are taken
-    // to spread evenly over the experts.  1, 2, 4 and 8 warps: one token on 8 of 64
-    // experts of 1024 x 2048 29, 16.5, 11.2 and 12.1 us; 16 tokens 60, 44, 46, 55.
+    // follow one another), few where there are many (their sums meet).  A block takes
+    // its items in whole turns; a turn costs its chunks and about 1.2 chunks' time for
+    // x and the sums.  The number of items is what pairs spread at random would give:
+    // an expert is met with 1 - (1 - topk / experts)^tokens, and a count of many pairs
+    // leaves its last tile half full.  Measured with 1, 2, 4 and 8 warps, GeGLU of 8
+    // out of 64 experts of 1024 x 2048: 1 token 25.4, 16.4, 11.2 and 12.1 us, 4 tokens
+    // 25.4, 30.3, 31.0, 31.9, 16 tokens 51.7, 43.9, 45.4, 50.1; 3 leaves warps idle.
     constexpr int rows = GEGLU ? kRows / 2 : kRows;
-    const int64_t each = (p.plan.pairs_total + p.plan.experts * 8 * NB - 1) / (p.plan.experts * 8 * NB);
-    const int64_t units = std::min(p.plan.pairs_total, p.plan.experts * each);
+    const double experts = static_cast<double>(p.plan.experts);
+    const double met = 1.0 - std::pow(1.0 - p.plan.topk / experts, static_cast<double>(p.plan.pairs_total / p.plan.topk));
+    const double tiles = p.plan.pairs_total / (experts * 8 * NB);
+    const double units = experts * (tiles < 0.5 ? met : std::max(met, tiles + 0.5 * (1.0 - 1.0 / (8 * NB))));
     int best = 1;
     double least = 0.0;
-    for (int kw = 1; kw <= std::min(p.chunks, warps); ++kw) {
+    for (int kw = 1; kw <= std::min(p.chunks, warps); kw *= 2) {
         const int rw = warps / kw;
-        const double items = static_cast<double>(units) * ((p.n + rows * rw - 1) / (rows * rw)) / device_sm_count();
-        const double cost = (items <= 1.0 ? 1.0 : items + 0.5) * ((p.chunks + kw - 1) / kw + (kw > 1 ? 0.6 : 0.0));
+        const double turns = std::max(1.0, std::ceil(units * ((p.n + rows * rw - 1) / (rows * rw)) / device_sm_count()));
+        const double cost = turns * ((p.chunks + kw - 1) / kw + 1.2);
         if (kw == 1 || cost < least) {
             best = kw;
             least = cost;
