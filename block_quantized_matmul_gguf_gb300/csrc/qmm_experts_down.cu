@@ -14,74 +14,70 @@ struct SumParams {
     const float *weights;
     void *y;
     int64_t y_stride, tokens, n;
-    int experts, topk;
+    int experts, topk, parts;  // parts: blocks a token
     bool bf16;  // y
     bool wide;  // y's rows are aligned to 16 bytes
 };
 
-// V columns of the row at z.
-template <int V>
-__device__ __forceinline__ void load_columns(const float *z, float (&f)[V]) {
-    if constexpr (V == 1) {
-        f[0] = *z;
-    } else {
+// V columns of a row of z as they are, 16 bytes where V is not 1, and as fp32.
+template <typename T, int V>
+struct Columns {
+    uint4 raw;
+    __device__ __forceinline__ void load(const T *z) {
+        if constexpr (V == 1)
+            raw.x = sizeof(T) == 4 ? __float_as_uint(*reinterpret_cast<const float *>(z)) : *reinterpret_cast<const uint16_t *>(z);
+        else
+            raw = *reinterpret_cast<const uint4 *>(z);
+    }
+    __device__ __forceinline__ void add(float w, float (&sum)[V]) const {
+        static_assert(V == 1 || V * sizeof(T) == 16, "16 bytes");
+        const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-        for (int v = 0; v < V; v += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(z + v);
-            f[v] = a.x, f[v + 1] = a.y, f[v + 2] = a.z, f[v + 3] = a.w;
+        for (int v = 0; v < V; ++v) {
+            const uint32_t q = sizeof(T) == 4 ? r[v % 4] : v % 2 ? r[v / 2 % 4] & 0xFFFF0000u : r[v / 2 % 4] << 16;
+            sum[v] = fmaf(w, __uint_as_float(q), sum[v]);
         }
     }
-}
-template <int V>
-__device__ __forceinline__ void load_columns(const uint16_t *z, float (&f)[V]) {
-    if constexpr (V == 1) {
-        f[0] = __uint_as_float(static_cast<uint32_t>(*z) << 16);
-    } else {
-        static_assert(V == 8, "16 bytes");
-        const uint4 a = *reinterpret_cast<const uint4 *>(z);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-}
+};
 
 constexpr int kSumAhead = 8;  // rows of z loaded before the first is added
 
+// A block: one token's columns.  A lane reads one pair's expert and weight and the
+// warp hands them round.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumParams p) {
     pdl_wait();
     pdl_launch_dependents();
-    const int per = static_cast<int>(p.n / V);
-    const int64_t all = static_cast<int64_t>(per) * p.tokens;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t t = i / per;
-        const int col = static_cast<int>(i - t * per) * V;
+    const int lane = threadIdx.x & 31;
+    for (int64_t u = blockIdx.x; u < p.tokens * p.parts; u += gridDim.x) {
+        const int64_t t = u / p.parts;
+        const int64_t col = (static_cast<int64_t>(u - t * p.parts) * blockDim.x + threadIdx.x) * V;
+        const bool mine = col < p.n;  // p.n: a multiple of V
         const T *z = static_cast<const T *>(p.z) + t * p.topk * p.n + col;
         float sum[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) sum[v] = 0.0f;
-        for (int r0 = 0; r0 < p.topk; r0 += kSumAhead) {
-            float w[kSumAhead], f[kSumAhead][V];
-            bool there[kSumAhead];
+        for (int r32 = 0; r32 < p.topk; r32 += 32) {
+            int id = -1;
+            float weight = 0.0f;
+            if (r32 + lane < p.topk) {
+                id = p.ids[t * p.topk + r32 + lane];
+                weight = p.weights[t * p.topk + r32 + lane];
+            }
+            const uint32_t there = __ballot_sync(0xFFFFFFFFu, id >= 0 && id < p.experts);
+            for (int r0 = 0; r0 < 32 && r32 + r0 < p.topk; r0 += kSumAhead) {
+                Columns<T, V> f[kSumAhead];
 #pragma unroll
-            for (int r = 0; r < kSumAhead; ++r) {
-                there[r] = false;
-                if (r0 + r < p.topk) {
-                    const int id = p.ids[t * p.topk + r0 + r];
-                    there[r] = id >= 0 && id < p.experts;
-                    w[r] = p.weights[t * p.topk + r0 + r];
-                    load_columns<V>(z + (r0 + r) * p.n, f[r]);  // of a pair that is not there: not used
+                for (int r = 0; r < kSumAhead; ++r)
+                    if (mine && (there >> (r0 + r) & 1)) f[r].load(z + (r32 + r0 + r) * p.n);
+#pragma unroll
+                for (int r = 0; r < kSumAhead; ++r) {
+                    const float w = __shfl_sync(0xFFFFFFFFu, weight, r0 + r);
+                    if (mine && (there >> (r0 + r) & 1)) f[r].add(w, sum);
                 }
             }
-#pragma unroll
-            for (int r = 0; r < kSumAhead; ++r)
-                if (there[r])
-#pragma unroll
-                    for (int v = 0; v < V; ++v) sum[v] = fmaf(w[r], f[r][v], sum[v]);
         }
+        if (!mine) continue;
         if (V == 8 && p.bf16 && p.wide) {
             uint32_t o[4];
 #pragma unroll
@@ -133,13 +129,15 @@ cudaError_t launch_experts_down(const ExpertsDown &a, cudaStream_t stream, const
     const int64_t tokens = a.plan.pairs_total / a.plan.topk;
     const int values = tiles ? 8 : 4;  // of z in 16 bytes
     const bool whole = a.n % values == 0;  // the workspace is aligned
-    const SumParams s = {a.workspace, a.ids, a.weights, a.y, a.y_stride, tokens, a.n, a.plan.experts, a.plan.topk, a.y_bf16,
+    const int64_t per = whole ? a.n / values : a.n;
+    const int threads = static_cast<int>(std::min<int64_t>(256, (per + 31) / 32 * 32));
+    const int parts = static_cast<int>((per + threads - 1) / threads);
+    const SumParams s = {a.workspace, a.ids, a.weights, a.y, a.y_stride, tokens, a.n, a.plan.experts, a.plan.topk, parts, a.y_bf16,
                          reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.y_stride % (a.y_bf16 ? 8 : 4) == 0};
-    const int64_t threads = tokens * (whole ? a.n / values : a.n);
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((threads + 255) / 256, static_cast<int64_t>(device_sm_count()) * 8));
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tokens * parts, int64_t(1) << 30));
     auto *kernel = tiles ? (whole ? sum_kernel<uint16_t, 8> : sum_kernel<uint16_t, 1>)
                          : (whole ? sum_kernel<float, 4> : sum_kernel<float, 1>);
-    return launch_kernel(kernel, dim3(grid), dim3(256), 0, stream, 1, s);
+    return launch_kernel(kernel, dim3(grid), dim3(threads), 0, stream, 1, s);
 }
 
 }  // namespace qmm

@@ -581,7 +581,20 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t largest(const uint4 &v, uint32_t top) {
+    for (const uint32_t w : {v.x, v.y, v.z, v.w}) top = max(max(top, w & 0x7FFFu), (w >> 16) & 0x7FFFu);
+    return top;
+}
+__device__ __forceinline__ uint2 shuffle2(const uint2 &v, int src) {
+    return make_uint2(__shfl_sync(0xFFFFFFFFu, v.x, src), __shfl_sync(0xFFFFFFFFu, v.y, src));
+}
+__device__ __forceinline__ uint4 scaled_eight(const uint2 &a, const uint2 &b, float f) {
+    return make_uint4(pack_f16x2(bf16_low(a.x) * f, bf16_low(a.y) * f), pack_f16x2(bf16_high(a.x) * f, bf16_high(a.y) * f),
+                      pack_f16x2(bf16_low(b.x) * f, bf16_low(b.y) * f), pack_f16x2(bf16_high(b.x) * f, bf16_high(b.y) * f));
+}
+
 constexpr int kRowsWarps = 8;
+constexpr int kRowsHeld = 8;  // 256 values each
 
 __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const __grid_constant__ RowsParams p) {
     pdl_wait();
@@ -596,23 +609,38 @@ __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const __g
             from = pr / p.plan.topk;
         }
         const uint16_t *x = p.x + from * p.x_stride;
+        // the row stays in registers where it has 2048 values or fewer
+        const int all = p.k / 8;
+        uint4 held[kRowsHeld];
         // the largest: bf16 magnitudes order as integers (what is no number makes the
         // row's results none either)
         uint32_t top = 0;
-        for (int c = lane; c < p.k / 8; c += 32) {
-            const uint4 v = reinterpret_cast<const uint4 *>(x)[c];
-            for (const uint32_t w : {v.x, v.y, v.z, v.w}) top = max(max(top, w & 0x7FFFu), (w >> 16) & 0x7FFFu);
+#pragma unroll
+        for (int j = 0; j < kRowsHeld; ++j) {
+            held[j] = make_uint4(0, 0, 0, 0);
+            if (j * 32 + lane < all) held[j] = reinterpret_cast<const uint4 *>(x)[j * 32 + lane];
         }
+#pragma unroll
+        for (int j = 0; j < kRowsHeld; ++j) top = largest(held[j], top);
+        for (int c = kRowsHeld * 32 + lane; c < all; c += 32) top = largest(reinterpret_cast<const uint4 *>(x)[c], top);
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         const int e = min(max(static_cast<int>(top >> 7), 15), 254);  // as in the streaming form
         const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
         if (lane == 0) p.unit[i] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-        uint4 *out = p.rows + i * (p.k / 8);
-        for (int c = lane; c < p.k / 8; c += 32) {  // block c / 4, values 4 (c % 4) .. and 16 on from there
+        uint4 *out = p.rows + i * all;
+        // eight c: of block c / 4, the values from 4 (c % 4) on and from 16 + 4 (c % 4) on
+#pragma unroll
+        for (int j = 0; j < kRowsHeld; ++j) {
+            if (j * 32 >= all) break;  // all: a multiple of 32
+            const uint4 v = held[j];  // lane q of four: the block's values from 8 q on
+            const int q = lane & 3, src = (lane & ~3) | (q >> 1);
+            const uint2 a0 = shuffle2(make_uint2(v.x, v.y), src), a1 = shuffle2(make_uint2(v.z, v.w), src);
+            const uint2 b0 = shuffle2(make_uint2(v.x, v.y), src + 2), b1 = shuffle2(make_uint2(v.z, v.w), src + 2);
+            out[j * 32 + lane] = scaled_eight(q & 1 ? a1 : a0, q & 1 ? b1 : b0, f);
+        }
+        for (int c = kRowsHeld * 32 + lane; c < all; c += 32) {
             const uint16_t *from8 = x + (c >> 2) * 32 + (c & 3) * 4;
-            const uint2 a = *reinterpret_cast<const uint2 *>(from8), b = *reinterpret_cast<const uint2 *>(from8 + 16);
-            out[c] = make_uint4(pack_f16x2(bf16_low(a.x) * f, bf16_low(a.y) * f), pack_f16x2(bf16_high(a.x) * f, bf16_high(a.y) * f),
-                                pack_f16x2(bf16_low(b.x) * f, bf16_low(b.y) * f), pack_f16x2(bf16_high(b.x) * f, bf16_high(b.y) * f));
+            out[c] = scaled_eight(*reinterpret_cast<const uint2 *>(from8), *reinterpret_cast<const uint2 *>(from8 + 16), f);
         }
     }
 }
@@ -641,8 +669,7 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
     cudaError_t e = ensure_smem(experts_tile_kernel<G>, smem, true, limits);
     if (e != cudaSuccess) return e;
     const RowsParams r = {plan, x, x_stride, reinterpret_cast<uint4 *>(xr), unit, static_cast<int>(k), G, ctx};
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((plan.pairs_total + kRowsWarps - 1) / kRowsWarps,
-                                                                  static_cast<int64_t>(device_sm_count()) * 8));
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((plan.pairs_total + kRowsWarps - 1) / kRowsWarps, int64_t(1) << 30));
     e = launch_kernel(experts_rows_kernel, dim3(grid), dim3(kRowsWarps * 32), 0, stream, 1, r);
     if (e != cudaSuccess) return e;
     const unsigned pairs = std::max(1, device_sm_count() / 2);
