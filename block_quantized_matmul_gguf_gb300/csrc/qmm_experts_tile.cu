@@ -682,7 +682,7 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
 // copy, and enough pairs an expert on average.
 bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k) {
     return bf16 && k % CK == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0 &&
-           plan.experts * n < (int64_t(1) << 31) && experts_are_many(plan.pairs_total, plan.experts);
+           plan.experts * n < (int64_t(1) << 31) && experts_are_many(plan.pairs_total, plan.experts, k);
 }
 
 size_t experts_rows_bytes(int64_t pairs, int64_t k) { return rows_bytes(pairs, k); }
