@@ -11,25 +11,33 @@
 // in tensor memory; the epilogue takes the row's power of two out again.  Scales
 // above 8188, whose weights binary16 cannot hold, give infinities here.
 //
-// Structure, as of the prefill GEMM: persistent CTA pairs; a tile is 256 weight rows
-// (128 gate and the same 128 up rows for GeGLU) by up to 128 of an expert's rows,
-// tcgen05.mma.cta_group::2, the weights in tensor memory, x in shared memory.  An
-// expert's rows are cut into equal tiles of a multiple of 32, so that the
-// instruction's N follows the rows that are there.  Two accumulators: one is read out
-// while the next tile's products run.
-//   warp 0      x producer (both CTAs): boxes of 16 rows x 64 values, a lane each
-//   warp 1      MMA issuer (one thread of the leader)
-//   warp 2      weight producer (both CTAs): boxes of 128 rows x 144 bytes
+// Structure: persistent clusters of two CTAs; an item is 256 weight rows (128 gate
+// and the same 128 up rows for GeGLU), half for each CTA, by up to 128 of an expert's
+// rows.  A CTA's products are tcgen05.mma.cta_group::1 with M = 128: its weights in
+// tensor memory, x in shared memory, where each CTA loads one half of the item's rows
+// for both (multicast).  An expert's rows are cut into equal tiles of a multiple of
+// 32, so that the instruction's N follows the rows that are there.  Two accumulators:
+// one is read out while the next item's products run.
+//   warp 0      x: a box of 64 rows x 64 values a lane, or two of 16 rows for small tiles
+//               (a copy's cost is its box's, not its rows': boxes of 16 alone cost 23 us
+//               more at 2047 tokens)
+//   warp 1      MMA, issued by the whole warp's elected lane
+//   warp 2      weights as they are: boxes of 64 or 128 rows x 144 bytes
 //   warps 4-11  epilogue, two for each quarter of the lanes
-//   warps 12-27 dequantisers: TMEM lanes 32 (w % 4) .., half of every other chunk of 256
-//               K, which is a stage.  Weights are formed in registers before their slot is
-//               waited for, so that a free slot is filled at once.
+//   warps 12-27 dequantisers: TMEM lanes 32 (w % 4) .., one stage (128 of K) of every
+//               other chunk (256 of K).  Weights are formed in registers before their
+//               slot is waited for, so that a free slot is filled at once.
 // The binary16 pairs that a word of codes gives without moving its nibbles are
 // values 0 and 2, 1 and 3, so x is written in that order of K too.
 // Which items (expert, tile, row block) there are depends on expert_start: each CTA
 // forms the prefix sums of the experts' tiles in shared memory, and every role finds
-// its pair's items in them by bisection.
+// its pair's items in them by two ballots.
 // Every wait is bounded, as in the prefill GEMM.
+//
+// Bound by the dequantisers and their hand-over to the tensor cores for prompts (8 out
+// of 64 experts of 1024 x 2048, 2047 tokens: tiles 107 us of 123 to 126, 1.28 PFLOP/s), by
+// the weights' bytes and the fill of each expert's pipeline below some 16 rows an
+// expert (128 tokens: 46.5 us, 3.3 TB/s).  The rows' kernel writes 67 MB in 15 us.
 #include "qmm_internal.h"
 #include "qmm_tc.cuh"
 

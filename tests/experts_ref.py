@@ -104,7 +104,9 @@ def product(x, b, exact, rounded_x):
         binary16 cannot reach, 2^-38 of the row's largest x for each weight
       bf16 results: an fp32 x in 11 bits, half a step 2^-11; in the streaming
         form sums of subnormal codes that keep 18 bits, 34 addends of T, under
-        2^-12 T; in the tile form each weight rounded to bf16, half a step 2^-8 S
+        2^-12 T; in the tile form each weight rounded to binary16, half a step
+        2^-12 S and 2^-25 of each x below its normal numbers, and up to 512
+        accumulations cut at 2^-23: 2^-14 S
     """
     w, wide = matrix(b)
     a = np.abs(x)
@@ -112,7 +114,8 @@ def product(x, b, exact, rounded_x):
     reach = 2.0 ** -38 * a.max(-1, keepdims=True) * np.abs(w).sum(-1)
     if exact:
         return x @ w.T, s * 2.0 ** -15 + reach
-    return x @ w.T, s * (2.0 ** -15 + 2.0 ** -8 + (2.0 ** -11 if rounded_x else 0.0)) + a @ wide.T * 2.0 ** -12 + reach
+    return x @ w.T, (s * (2.0 ** -14 + 2.0 ** -12 + (2.0 ** -11 if rounded_x else 0.0)) + a @ wide.T * 2.0 ** -12
+                      + a.sum(-1, keepdims=True) * 2.0 ** -25 + reach)
 
 
 def geglu(x, bg, bu, exact, rounded_x):
