@@ -6,7 +6,8 @@ The compute lives in a C-ABI shared library (``libqmm.so``, built from
 the same entry-point names.  :mod:`block_quantized_matmul_gguf_gb300.synth`
 draws the seeded synthetic inputs, and
 :mod:`block_quantized_matmul_gguf_gb300.generate` runs the serving calls (page
-plan, 4-bit cache, attention, logits) together as a small loop.  Importing the package loads nothing; the
-binding raises if the CUDA library is missing.
+plan, 4-bit cache, rotation, attention, experts, logits) together as a small
+loop.  Importing the package loads nothing; the binding raises if the CUDA
+library is missing.
 """
 __all__ = ["qmm", "synth", "build", "generate"]

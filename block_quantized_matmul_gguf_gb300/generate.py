@@ -1,12 +1,15 @@
 """A small generation loop over the library's calls, as a serving program runs
 them: plan the pages of a step, project q, k and v with Q4_0 weights, append
 keys and values to the 4-bit cache, attend, project back, apply the Q8_0 LM
-head, adjust the logits, take the largest.
+head, adjust the logits, take the largest.  With a rotation, queries and keys
+are rotated on their way; with experts, each token is routed to some of them
+and their GeGLU and down products follow the attention.
 
-One attention layer with a residual, random weights of the given sizes and no
-tokenizer: it shows how the calls fit together, not a language model.
+One layer with residuals, random weights of the given sizes and no tokenizer:
+it shows how the calls fit together, not a language model.
 
     python -m block_quantized_matmul_gguf_gb300.generate --steps 16
+    python -m block_quantized_matmul_gguf_gb300.generate --rope 10000 --experts 16
 """
 from __future__ import annotations
 
@@ -18,9 +21,11 @@ from . import qmm, synth
 
 
 class Layer:
-    """Random weights of one attention layer, an embedding and an LM head."""
+    """Random weights of one attention layer, an embedding and an LM head; of `experts` experts of
+    `expert_width` features and their router, `topk` a token; positions rotate by base `rope` if given."""
 
-    def __init__(self, hidden=512, heads=8, kv_heads=2, head_dim=64, vocab=2048, seed=0, device="cuda"):
+    def __init__(self, hidden=512, heads=8, kv_heads=2, head_dim=64, vocab=2048, seed=0, device="cuda", rope=None,
+                 experts=0, topk=2, expert_width=256):
         self.hidden, self.heads, self.kv_heads, self.head_dim, self.vocab = hidden, heads, kv_heads, head_dim, vocab
         self.device = torch.device(device)
 
@@ -34,6 +39,12 @@ class Layer:
         self.wo = blocks(synth.q4_0_weights(hidden, width, seed=seed, stream=3))
         self.head = blocks(synth.q8_0_weights(vocab, hidden, seed=seed, stream=4))
         self.embedding = blocks(synth.activations_f32(vocab, hidden, seed=seed, stream=5))
+        self.rope, self.experts, self.topk, self.expert_width = rope, experts, topk, expert_width
+        if experts:
+            self.router = blocks(synth.q4_0_weights(experts, hidden, seed=seed, stream=6))
+            self.wg = blocks(synth.q4_0_weights(experts * expert_width, hidden, seed=seed, stream=7))
+            self.wu = blocks(synth.q4_0_weights(experts * expert_width, hidden, seed=seed, stream=8))
+            self.wd = blocks(synth.q4_0_weights(experts * hidden, expert_width, seed=seed, stream=9))
 
 
 class Generator:
@@ -51,12 +62,30 @@ class Generator:
         self.history = [[] for _ in range(batch)]
         self.hidden = torch.zeros((batch, layer.hidden), device=dev)  # last row of each request
         self.prompt_len = torch.zeros(batch, **i32)
+        self.rotations = None if layer.rope is None else qmm.rope_table(max_pages * page_size, layer.head_dim,
+                                                                        layer.rope, device=dev)
 
     def _project(self, weights, x, n_out, k):
         """Rows of x times a Q4_0 matrix: fp32 up to 16 rows, else bf16 in and fp32 out."""
         if x.dtype == torch.float32:
             return qmm.gemv("q4_0", weights, x, n_out, k)
         return qmm.gemm("q4_0", weights, x, n_out, k)
+
+    def _experts(self, x):
+        """Each row of x through the experts that its router's logits choose."""
+        layer, tokens = self.layer, x.shape[0]
+        topk, experts, dev = layer.topk, layer.experts, x.device
+        i32 = dict(dtype=torch.int32, device=dev)
+        logits = self._project(layer.router, x, experts, layer.hidden)
+        ids, weights = torch.empty((tokens, topk), **i32), torch.empty((tokens, topk), device=dev)
+        starts, pairs = torch.empty(experts + 1, **i32), torch.empty(tokens * topk, **i32)
+        qmm.qmm_route(logits, ids, weights, starts, pairs)
+        h = torch.empty((tokens * topk, layer.expert_width), dtype=x.dtype, device=dev)
+        qmm.qmm_experts_geglu_q4_0(layer.wg, layer.wu, x, h, starts, pairs, topk, layer.expert_width, layer.hidden)
+        y = torch.empty_like(x)
+        qmm.qmm_experts_down_q4_0(layer.wd, h, y, ids, weights, starts, pairs, layer.hidden, layer.expert_width)
+        self.routed = dict(x=x, logits=logits, ids=ids, weights=weights, starts=starts, pairs=pairs, h=h, y=y)
+        return y
 
     def forward(self, tokens):
         """tokens: a list of new token ids for each request; one without any keeps
@@ -95,13 +124,21 @@ class Generator:
             q, k, v = (self._project(w, act, n, layer.hidden)
                        for w, n in ((layer.wq, width), (layer.wk, kv_width), (layer.wv, kv_width)))
         heads = (total, layer.kv_heads, layer.head_dim)
-        qmm.qmm_kv_append_q4_0(self.cache, k.view(heads), v.view(heads), slots)
         out = torch.empty((total, layer.heads, layer.head_dim), dtype=act.dtype, device=dev)
-        qmm.qmm_attn_q4_0(self.cache, q.view(out.shape), out, self.table, q_start, kv_len, most,
+        q = q.view(out.shape)
+        if self.rotations is None:
+            qmm.qmm_kv_append_q4_0(self.cache, k.view(heads), v.view(heads), slots)
+        else:
+            plain, q = q, torch.empty_like(q)
+            qmm.qmm_kv_append_rope_q4_0(self.cache, k.view(heads), v.view(heads), slots, positions, self.rotations,
+                                        q=plain, q_out=q)
+        qmm.qmm_attn_q4_0(self.cache, q, out, self.table, q_start, kv_len, most,
                           layer.head_dim ** -0.5, workspace=self.workspace)
         x = x + self._project(layer.wo, out.view(total, width), layer.hidden, width)
         self.kv_len = kv_len
-        self.last = dict(q=q.view(out.shape), out=out, q_start=q_start, slots=slots, positions=positions)
+        self.last = dict(q=q, out=out, q_start=q_start, slots=slots, positions=positions)
+        if layer.experts:
+            x = x + self._experts(x if small else x.bfloat16())
         ends = x[(q_start[1:] - 1).long().clamp(min=0)]  # of a request without new tokens, another's
         self.hidden = torch.where((added > 0)[:, None], ends, self.hidden)
         return self.hidden
@@ -153,8 +190,11 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=16)
     ap.add_argument("--seed", type=int, default=0)
+    ap.add_argument("--rope", type=float, help="rotate queries and keys, with this base")
+    ap.add_argument("--experts", type=int, default=0, help="a mixture of so many experts after the attention")
+    ap.add_argument("--topk", type=int, default=2, help="experts a token")
     a = ap.parse_args()
-    layer = Layer(seed=a.seed)
+    layer = Layer(seed=a.seed, rope=a.rope, experts=a.experts, topk=a.topk)
     prompts = [[1, 2, 3, 4, 5], list(range(40, 120)), [7]]
     made = Generator(layer, len(prompts)).run(prompts, a.steps)
     for p, m in zip(prompts, made):
