@@ -650,7 +650,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
         }
         at = next;
     }
-    copy_wait<0>();
+    if constexpr (ALIGNED) {
+        // a copy may still be on its way where a wait ran out; once more, with the same limit
+        if (!ok && lane < kStages) wait_drain(smem_addr(&bars[warp][lane]), parity >> lane & 1u, p.ctx);
+        __syncwarp();
+    } else {
+        copy_wait<0>();
+    }
 }
 
 constexpr int kSharedLimit = 232448 - 256;  // beside the kernel's own

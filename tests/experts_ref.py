@@ -99,22 +99,24 @@ def product(x, b, exact, rounded_x):
     """x [rows][k] times the transpose of a matrix of blocks, and the bound of
     the kernels' error.  With S = sum |w x| and T = sum d (n + 8) |x|:
       exact weights (fp32 results): x in two binary16 parts 2^-22, sums of 16
-        products in the tensor cores 2^-19 (17 addends cut at 2^-23), up to 272
-        roundings of block sums and parts 2^-15.9: under 2^-15 S; and of what
-        binary16 cannot reach, 2^-38 of the row's largest x for each weight
+        products in the tensor cores 2^-19 (17 addends cut at 2^-23), K / 32 + 16
+        roundings of block sums and parts: 2^-15.9 for K to 8192, 2^-15 S in all,
+        and beyond that K 2^-28 S; and of what binary16 cannot reach, 2^-38 of the
+        row's largest x for each weight
       bf16 results: an fp32 x in 11 bits, half a step 2^-11; in the streaming
         form sums of subnormal codes that keep 18 bits, 34 addends of T, under
         2^-12 T; in the tile form each weight rounded to binary16, half a step
-        2^-12 S and 2^-25 of each x below its normal numbers, and up to 512
-        accumulations cut at 2^-23: 2^-14 S
+        2^-12 S and 2^-25 of each x below its normal numbers, and K / 16
+        accumulations cut at 2^-23: 2^-14 S for K to 8192, beyond that K 2^-27 S
     """
     w, wide = matrix(b)
     a = np.abs(x)
     s = a @ np.abs(w).T
     reach = 2.0 ** -38 * a.max(-1, keepdims=True) * np.abs(w).sum(-1)
+    long = max(1.0, x.shape[-1] / 8192)
     if exact:
-        return x @ w.T, s * 2.0 ** -15 + reach
-    return x @ w.T, (s * (2.0 ** -14 + 2.0 ** -12 + (2.0 ** -11 if rounded_x else 0.0)) + a @ wide.T * 2.0 ** -12
+        return x @ w.T, s * 2.0 ** -15 * long + reach
+    return x @ w.T, (s * (2.0 ** -14 * long + 2.0 ** -12 + (2.0 ** -11 if rounded_x else 0.0)) + a @ wide.T * 2.0 ** -12
                       + a.sum(-1, keepdims=True) * 2.0 ** -25 + reach)
 
 

@@ -334,3 +334,79 @@ def test_refusals(qmm):
     none = torch.zeros(0, 64, device="cuda")
     qmm.qmm_experts_geglu_q4_0(wg, wg, none, torch.zeros(0, 32, device="cuda"), starts, pairs[:0], 2, 32, 64)
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("types", TYPES, ids=str)
+@pytest.mark.parametrize("k", [65536, 65568])
+def test_long_rows(qmm, types, k):
+    rng = np.random.default_rng(k)
+    run_geglu(qmm, rng, 3, 3, 2, 20, k, *types)
+    run_down(qmm, rng, 3, 3, 2, 20, k, *types)
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)], ids=str)
+@pytest.mark.parametrize("k", [2048, 2080])
+@pytest.mark.parametrize("tokens", [3, 1100])
+def test_offsets_past_32_bits(qmm, types, k, tokens):
+    """The last of 1024 experts of 5 GB of weights, rows of x and h 2^21 elements apart."""
+    experts, n = 1024, 4352
+    rng = np.random.default_rng(k + tokens)
+    row = k // 32 * 18
+    w = [torch.zeros((experts, n, row), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    assert w[0].numel() > 1 << 32
+    last = [ref.blocks(rng, 1, n, k) for _ in w]
+    for t, b in zip(w, last):
+        t[-1] = dev(b[0])
+    ids = np.full((tokens, 1), experts - 1)
+    starts, pairs = ref.plan_of(ids, experts)
+    apart = 1 << 21
+    x = rng.standard_normal((tokens, k)).astype(np.float32)
+    wide = torch.zeros((tokens, apart), dtype=types[0], device="cuda")[:, :k]
+    wide.copy_(torch.from_numpy(x))
+    some = [0, tokens // 2, tokens - 1]
+    want, limit = ref.geglu(wide[some].double().cpu().numpy(), last[0][0], last[1][0], types[1] is F32, types[0] is F32)
+    h = torch.zeros((tokens, apart), dtype=types[1], device="cuda")[:, :n]
+    qmm.qmm_experts_geglu_q4_0(w[0], w[1], wide, h, dev(starts), dev(pairs), 1, n, k)
+    near(h[some], want, limit, types[1] is F32)
+    del h
+    y = torch.zeros((tokens, apart), dtype=types[1], device="cuda")[:, :n]
+    ones = torch.ones((tokens, 1), device="cuda")
+    qmm.qmm_experts_down_q4_0(w[0], wide, y, dev(ids.astype(np.int32)), ones, dev(starts), dev(pairs), n, k)
+    local, order = ref.plan_of(np.zeros((3, 1), dtype=np.int64), 1)
+    want, limit = ref.experts_down(wide[some].double().cpu().numpy(), last[0], np.zeros((3, 1), dtype=np.int64),
+                                   np.ones((3, 1)), local, order, types[1] is F32, types[0] is F32)
+    near(y[some], want, limit, types[1] is F32)
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+def test_two_streams_at_once(qmm):
+    """Calls that overlap, each with a workspace of its own, give what they give alone."""
+    rng = np.random.default_rng(77)
+    tokens, experts, topk, n, k = 300, 8, 2, 512, 1024
+    cases = []
+    for _ in range(2):
+        ids = choice(rng, tokens, experts, topk)
+        starts, pairs = ref.plan_of(ids, experts)
+        x = dev(rng.standard_normal((tokens, k)).astype(np.float32), BF16)
+        cases.append((dev(ref.blocks(rng, experts, n, k)), dev(ref.blocks(rng, experts, n, k)), dev(ref.blocks(rng, experts, k, n)),
+                      x, dev(ids.astype(np.int32)), dev(rng.random((tokens, topk)).astype(np.float32)), dev(starts), dev(pairs)))
+
+    def layer(c, stream=None):
+        wg, wu, wd, x, ids, weights, starts, pairs = c
+        h = torch.empty((tokens * topk, n), dtype=BF16, device="cuda")
+        y = torch.empty((tokens, k), dtype=BF16, device="cuda")
+        for _ in range(20):
+            qmm.qmm_experts_geglu_q4_0(wg, wu, x, h, starts, pairs, topk, n, k, stream=stream)
+            qmm.qmm_experts_down_q4_0(wd, h, y, ids, weights, starts, pairs, k, n, stream=stream)
+        return y
+
+    alone = [layer(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    both = []
+    for c, s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            both.append(layer(c))
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert torch.equal(a, b)
