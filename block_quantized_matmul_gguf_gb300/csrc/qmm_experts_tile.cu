@@ -18,9 +18,10 @@
 // for both (multicast).  An expert's rows are cut into equal tiles of a multiple of
 // 32, so that the instruction's N follows the rows that are there.  Two accumulators:
 // one is read out while the next item's products run.
-//   warp 0      x: a box of 64 rows x 64 values a lane, or two of 16 rows for small tiles
-//               (a copy's cost is its box's, not its rows': boxes of 16 alone cost 23 us
-//               more at 2047 tokens)
+//   warps 0, 3  x, every other stage each, whose copies take most of their time to
+//               issue (one warp for all: 128 tokens 46.6 us, two 43.4).  A box of 64 rows
+//               x 64 values a lane, or two of 16 rows for small tiles (a copy's cost is
+//               its box's, not its rows': boxes of 16 alone cost 23 us more at 2047 tokens)
 //   warp 1      MMA, issued by the whole warp's elected lane
 //   warp 2      weights as they are: boxes of 64 or 128 rows x 144 bytes
 //   warps 4-11  epilogue, two for each quarter of the lanes
@@ -57,9 +58,10 @@ constexpr int X_SUB_BYTES = BT * BK * 2, X_SLOT_BYTES = SUBS * X_SUB_BYTES;
 constexpr int RAW_ROW = 144;
 constexpr int RAW_SLOT_BYTES = BW * RAW_ROW;
 constexpr uint32_t D_COLS = 2 * BT, A_COLS = SK / 2, TMEM_COLS = 512;  // two accumulators
+static_assert(X_SLOTS % 2 == 0 && CK / SK % 2 == 0, "two x warps");
 static_assert(D_COLS + A_SLOTS * A_COLS <= TMEM_COLS, "tensor memory");
 
-constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_EPI = 4, EPI_WARPS = 8, WARP_DEQ = 12, DEQ_WARPS = 16;
+constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_X1 = 3, WARP_EPI = 4, EPI_WARPS = 8, WARP_DEQ = 12, DEQ_WARPS = 16;
 constexpr int THREADS = (WARP_DEQ + DEQ_WARPS) * 32;
 constexpr int X_BOX = 16, X_WIDE = BT / 2;  // rows of a copy of x: where few are wanted, and otherwise
 
@@ -329,8 +331,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int chunks = p.k / CK;
 
     Items at = items_from(p, pair, num_pairs);
-    if (warp == WARP_X) {
-        uint32_t it = 0;
+    if (warp == WARP_X || warp == WARP_X1) {
+        const uint32_t which = warp == WARP_X1;  // every other stage; an item has an even number of them
+        uint32_t it = which;
         bool ok = true;
         while (ok && at.item < items) {
             const Item t = next_item(p, ex, num_pairs, lane, at);
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool mine = sub < SUBS && (many || row < first + half);
             const CUtensorMap *map = many ? &tmap_x64 : &tmap_x;
             const uint32_t bytes = static_cast<uint32_t>(many ? 2 * X_WIDE : t.width) * SK * 2;
-            for (int st = 0; st < chunks * (CK / SK); ++st, ++it) {
+            for (int st = static_cast<int>(which); st < chunks * (CK / SK); st += 2, it += 2) {
                 const uint32_t s = it % X_SLOTS, full = bar(Smem::x_full + s);
                 if (!warp_wait_or_abort(bar(Smem::x_empty + s), ((it / X_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
                     ok = false;
@@ -359,9 +362,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             // all copies into this CTA have come, and both CTAs have read what this
             // one sent: nothing of the peer's is on its way here any more
-            for (uint32_t s = 0; s < X_SLOTS; ++s)
+            for (uint32_t s = which; s < X_SLOTS; s += 2)
                 if (it > s) {
-                    const uint32_t last = it - 1 - ((it - 1 - s) % X_SLOTS);
+                    const uint32_t last = it - 2 - ((it - 2 - s) % X_SLOTS);
                     wait_drain(bar(Smem::x_full + s), (last / X_SLOTS) & 1u, ctx);
                     if (ok) wait_drain(bar(Smem::x_empty + s), (last / X_SLOTS) & 1u, ctx);
                 }
