@@ -106,7 +106,7 @@ struct Item {
 };
 
 __device__ __forceinline__ int expert_count(const TileParams &p, int e, int &start) {
-    const int64_t a = p.plan.expert_start[e], b = p.plan.expert_start[e + 1];
+    const int64_t a = __ldcg(p.plan.expert_start + e), b = __ldcg(p.plan.expert_start + e + 1);
     if (a < 0 || b < a || b > p.plan.pairs_total) {
         record_error(p.ctx, kDevErrIndex);
         start = 0;
@@ -294,7 +294,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_mbar_init();
     }
     if (warp == WARP_MMA) tmem_alloc_cta(sbase + Smem::tmem_slot, TMEM_COLS);
-    pdl_wait();
+    // This kernel is launched behind the rows' kernel alone, each of whose threads lets it
+    // begin only after its own wait for all that came before: what is older than the
+    // rows is complete and in memory by now.  So the plan (read past L1) and the weights
+    // (TMA) are taken at once, and only the warps that read rows and units or write
+    // results wait for the rows' kernel: 128 tokens 43.4 -> 40.0 us.
     {  // tiles in front of each expert's
         __shared__ int32_t part[THREADS / 32];
         const int per = (p.plan.experts + THREADS - 1) / THREADS;
@@ -332,6 +336,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     Items at = items_from(p, pair, num_pairs);
     if (warp == WARP_X || warp == WARP_X1) {
+        pdl_wait();
         const uint32_t which = warp == WARP_X1;  // every other stage; an item has an even number of them
         uint32_t it = which;
         bool ok = true;
@@ -488,6 +493,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool odd = lane & 1, upper = lane >= 16;
         ulonglong2 *table = reinterpret_cast<ulonglong2 *>(sgen + Smem::cols) + q * BT;
         uint32_t tiles_done = 0;
+        pdl_wait();
         while (at.item < items) {
             const Item t = next_item(p, ex, num_pairs, lane, at);
             const uint32_t d = tiles_done & 1u;
@@ -611,6 +617,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const __g
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
+    // (the tile kernel relies on this order of the two, in every thread)
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowsWarps + (threadIdx.x >> 5); i < p.plan.pairs_total;
          i += static_cast<int64_t>(gridDim.x) * kRowsWarps) {
         int64_t from = i;

@@ -410,3 +410,33 @@ def test_two_streams_at_once(qmm):
     torch.cuda.synchronize()
     for a, b in zip(alone, both):
         assert torch.equal(a, b)
+
+
+def test_plans_and_weights_written_just_before(qmm):
+    """Calls back to back, each with a plan and weights that the stream writes right before it."""
+    rng = np.random.default_rng(91)
+    tokens, experts, topk, n, k = 64, 16, 2, 256, 512
+    x = dev(rng.standard_normal((tokens, k)).astype(np.float32), BF16)
+    sets = []
+    for kind in ("any", "same", "padded", "any"):
+        ids = choice(rng, tokens, experts, topk, kind)
+        starts, pairs = ref.plan_of(ids, experts)
+        sets.append((dev(ref.blocks(rng, experts, n, k)), dev(ref.blocks(rng, experts, n, k)), dev(starts), dev(pairs)))
+    ws = qmm.experts_workspace(tokens, topk, n, k)
+    want = []
+    for wg, wu, starts, pairs in sets:
+        h = torch.zeros((tokens * topk, n), dtype=BF16, device="cuda")
+        qmm.qmm_experts_geglu_q4_0(wg, wu, x, h, starts, pairs, topk, n, k, workspace=ws)
+        torch.cuda.synchronize()
+        want.append(h)
+    live = [torch.empty_like(t) for t in sets[0]]
+    got = [torch.zeros_like(h) for h in want]
+    for _ in range(50):
+        for s, h in zip(sets, got):
+            h.zero_()
+            for to, t in zip(live, s):
+                to.copy_(t)
+            qmm.qmm_experts_geglu_q4_0(live[0], live[1], x, h, live[2], live[3], topk, n, k, workspace=ws)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
