@@ -53,10 +53,19 @@ constexpr int BK = 64;       // K of a swizzle row of x
 constexpr int CK = 256;      // K of a chunk: eight blocks
 constexpr int SK = 128;      // K of a stage, the pipeline's unit
 constexpr int SUBS = SK / BK;
-constexpr int A_SLOTS = 4, X_SLOTS = 4, RAW_SLOTS = 4;  // in flight: stages, stages, chunks
+constexpr int A_SLOTS = 4, X_SLOTS = 4;  // stages in flight
 constexpr int X_SUB_BYTES = BT * BK * 2, X_SLOT_BYTES = SUBS * X_SUB_BYTES;
-constexpr int RAW_ROW = 144;
-constexpr int RAW_SLOT_BYTES = BW * RAW_ROW;
+// A chunk of a row of weights is 144 bytes.  Where K is a multiple of 256 every row
+// begins on 16 bytes and TMA copies boxes of them (WHOLE).  Otherwise the 16-byte
+// pieces that hold them are copied, each row behind its own skew.
+constexpr int RAW_CHUNK = 144;
+template <bool WHOLE>
+struct Raw {
+    static constexpr int slots = WHOLE ? 4 : 3;  // chunks in flight
+    static constexpr int pieces = 10;            // of 16 bytes, for 144 and a skew of up to 14
+    static constexpr int row = WHOLE ? RAW_CHUNK : 176;  // 176: 8 rows in different banks, as 144
+    static constexpr int slot_bytes = BW * row;
+};
 constexpr uint32_t D_COLS = 2 * BT, A_COLS = SK / 2, TMEM_COLS = 512;  // two accumulators
 static_assert(X_SLOTS % 2 == 0 && CK / SK % 2 == 0, "two x warps");
 static_assert(D_COLS + A_SLOTS * A_COLS <= TMEM_COLS, "tensor memory");
@@ -65,27 +74,34 @@ constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_X1 = 3, WARP_EPI = 4,
 constexpr int THREADS = (WARP_DEQ + DEQ_WARPS) * 32;
 constexpr int X_BOX = 16, X_WIDE = BT / 2;  // rows of a copy of x: where few are wanted, and otherwise
 
-struct Smem {
+template <bool WHOLE>
+struct Layout {
+    static constexpr int RAW_SLOTS = Raw<WHOLE>::slots;
     static constexpr int x = 0;
     static constexpr int raw = X_SLOTS * X_SLOT_BYTES;
-    static constexpr int bars = raw + RAW_SLOTS * RAW_SLOT_BYTES;
+    static constexpr int bars = raw + RAW_SLOTS * Raw<WHOLE>::slot_bytes;
     static constexpr int x_full = 0, x_empty = x_full + X_SLOTS, a_full = x_empty + X_SLOTS, a_empty = a_full + A_SLOTS,
                          raw_full = a_empty + A_SLOTS, raw_empty = raw_full + RAW_SLOTS, d_full = raw_empty + RAW_SLOTS,
                          d_empty = d_full + 2, final = d_empty + 2, nbars = final + 1;
     static constexpr int tmem_slot = bars + nbars * 8;
     static constexpr int abort_flag = tmem_slot + 4;
     static constexpr int cols = (abort_flag + 4 + 15) / 16 * 16;  // [4][BT] place in out and unit of each column
-    static constexpr int tiles = cols + 4 * BT * 16;  // Experts: four arrays of [experts + 1]
+    static constexpr int skew = cols + 4 * BT * 16;  // [RAW_SLOTS][32]: rows' skews repeat after 32
+    static constexpr int tiles = skew + (WHOLE ? 0 : RAW_SLOTS * 128);  // Experts: four arrays of [experts + 1]
     static int total(int experts) { return tiles + (experts + 1) * 16 + 1024; }
 };
-static_assert(Smem::tiles + (kMaxExperts + 1) * 16 + 1024 <= 232448 - 256, "shared memory of a CTA");
+static_assert(Layout<true>::tiles + (kMaxExperts + 1) * 16 + 1024 <= 232448 - 256 &&
+                  Layout<false>::tiles + (kMaxExperts + 1) * 16 + 1024 <= 232448 - 256,
+              "shared memory of a CTA");
 
 struct TileParams {
     ExpertsPlan plan;
     const float *unit;   // power of two of each row of x
     uint16_t *out;       // GeGLU: h by the pairs' order; down: z by the pair
     int64_t out_stride;
-    int n, k;
+    const uint8_t *w[2];  // not WHOLE: gate and up, or w[0]
+    int64_t row_bytes;
+    int n, chunks, blocks;  // chunks and blocks of K
     int row_blocks;      // of a matrix: of 256 rows (down) or 128 features
     uint32_t magic;      // 1024, 1024 in binary16, in a register
     bool even;           // out takes two neighbouring values at once
@@ -231,6 +247,19 @@ __device__ __forceinline__ void commit_both(uint32_t one, uint32_t bar) {
         : "memory");
 }
 
+// 16 bytes, of which the first `bytes` are read and the others zeros
+__device__ __forceinline__ void copy16_some(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// An arrival of this thread at the barrier once its copies so far are there.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // 32 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&v)[32]) {
     asm volatile(
@@ -249,11 +278,13 @@ constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BW >> 4) << 24);
 
 // G: GeGLU.  A CTA's 128 accumulator rows are then 64 features: in lane quarter q,
 // lanes 0-15 hold the gate rows of features 16q .. 16q+15, lanes 16-31 their up rows.
-template <bool G>
+template <bool G, bool WHOLE>
 __global__ void __launch_bounds__(THREADS, 1)
     experts_tile_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_x64,
                         const __grid_constant__ CUtensorMap tmap_w,
                         const __grid_constant__ CUtensorMap tmap_w2, const __grid_constant__ TileParams p) {
+    using Smem = Layout<WHOLE>;
+    constexpr int RAW_SLOTS = Smem::RAW_SLOTS, RAW_ROW = Raw<WHOLE>::row, RAW_SLOT_BYTES = Raw<WHOLE>::slot_bytes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_addr(smem_raw);
     const uint32_t sbase = (raw_base + 1023u) & ~1023u;
@@ -282,7 +313,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init_addr(bar(Smem::a_empty + i), 1);
         }
         for (int i = 0; i < RAW_SLOTS; ++i) {
-            mbar_init_addr(bar(Smem::raw_full + i), 1);
+            mbar_init_addr(bar(Smem::raw_full + i), WHOLE ? 1 : 33);  // 33: each lane's copies, and the skews
             mbar_init_addr(bar(Smem::raw_empty + i), DEQ_WARPS / 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -332,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     const int items = ex.tiles[p.plan.experts] * p.row_blocks;
-    const int chunks = p.k / CK;
+    const int chunks = p.chunks;
 
     Items at = items_from(p, pair, num_pairs);
     if (warp == WARP_X || warp == WARP_X1) {
@@ -375,27 +406,71 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
         }
     } else if (warp == WARP_RAW) {
+        const int64_t w_bytes = p.plan.experts * p.row_bytes * p.n;
         uint32_t it = 0;
         bool ok = true;
         while (ok && at.item < items) {
             const Item t = next_item(p, ex, num_pairs, lane, at);
-            const int wrow = t.expert * p.n + (G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2)
-                                                 : t.row_block * 2 * BW + static_cast<int>(rank) * BW);
+            const int row0 = G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) : t.row_block * 2 * BW + static_cast<int>(rank) * BW;
+            // 10 pieces a row, 32 rows in ten steps, and so on: a row's skew repeats after
+            // 32 rows, whose bytes are a multiple of 16.  Rows behind the expert's are
+            // another's or zeros, and dropped.
+            const int64_t base = (static_cast<int64_t>(t.expert) * p.n + row0) * p.row_bytes;
+            const int64_t first = base & ~int64_t(15);
+            int window[Raw<WHOLE>::pieces];  // from first on
+            auto place_of = [&](int i) { return (i * 32 + lane) / 10 * RAW_ROW + (i * 32 + lane) % 10 * 16; };
+            const int skew = static_cast<int>(base + lane * p.row_bytes) & 15;
+            if constexpr (!WHOLE) {
+#pragma unroll
+                for (int i = 0; i < Raw<WHOLE>::pieces; ++i) {
+                    const int at32 = i * 32 + lane;
+                    window[i] = static_cast<int>(((base + at32 / 10 * p.row_bytes) & ~int64_t(15)) - first) + at32 % 10 * 16;
+                }
+            }
             for (int c = 0; c < chunks; ++c, ++it) {
                 const uint32_t s = it % RAW_SLOTS, full = bar(Smem::raw_full + s);
                 if (!warp_wait_or_abort(bar(Smem::raw_empty + s), ((it / RAW_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
-                    mbar_expect_tx_addr(full, RAW_SLOT_BYTES);
-                    const uint32_t to = sbase + Smem::raw + s * RAW_SLOT_BYTES;
-                    tma_load_2d(to, &tmap_w, c * RAW_ROW, wrow, full);
-                    if constexpr (G) tma_load_2d(to + (BW / 2) * RAW_ROW, &tmap_w2, c * RAW_ROW, wrow, full);
+                const uint32_t to = sbase + Smem::raw + s * RAW_SLOT_BYTES;
+                if constexpr (WHOLE) {
+                    if (lane == 0) {
+                        const int wrow = t.expert * p.n + row0;
+                        mbar_expect_tx_addr(full, RAW_SLOT_BYTES);
+                        tma_load_2d(to, &tmap_w, c * RAW_CHUNK, wrow, full);
+                        if constexpr (G) tma_load_2d(to + (BW / 2) * RAW_ROW, &tmap_w2, c * RAW_CHUNK, wrow, full);
+                    }
+                    __syncwarp();
+                } else {
+#pragma unroll 1
+                    for (int rows32 = 0; rows32 < BW / 32; ++rows32) {
+                        const uint8_t *w = p.w[G ? rows32 >> 1 : 0];
+                        const int64_t more = first + (G ? rows32 & 1 : rows32) * 32 * p.row_bytes + c * RAW_CHUNK;
+                        const uint32_t to32 = to + rows32 * 32 * RAW_ROW;
+                        if (more + 32 * p.row_bytes + 176 <= w_bytes) {  // windows end below 31 rows + 176 bytes
+                            const uint8_t *src = w + more;
+#pragma unroll
+                            for (int i = 0; i < Raw<WHOLE>::pieces; ++i) copy16(to32 + place_of(i), src + window[i]);
+                        } else {
+#pragma unroll 1
+                            for (int i = 0; i < Raw<WHOLE>::pieces; ++i) {
+                                const int at32 = i * 32 + lane;
+                                const int64_t from = more + ((base + at32 / 10 * p.row_bytes) & ~int64_t(15)) - first + at32 % 10 * 16;
+                                const int64_t left = w_bytes - from;
+                                copy16_some(to32 + place_of(i), w + (left > 0 ? from : 0),
+                                            left >= 16 ? 16u : left > 0 ? static_cast<uint32_t>(left) : 0u);
+                            }
+                        }
+                    }
+                    copies_arrive(full);
+                    reinterpret_cast<int *>(sgen + Smem::skew)[s * 32 + lane] = skew;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_addr(full);
                 }
-                __syncwarp();
             }
         }
+        if constexpr (!WHOLE) copies_wait();
         if (lane == 0)
             for (uint32_t s = 0; s < RAW_SLOTS; ++s)
                 if (it > s) {
@@ -455,14 +530,37 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS;
         const uint32_t total = pair < items ? static_cast<uint32_t>((items - pair + num_pairs - 1) / num_pairs) * chunks : 0u;
         const uint32_t place = static_cast<uint32_t>(row) * RAW_ROW + 72u * part;
+        int c = (set >> 1) % chunks;  // chunk of its item
         for (uint32_t it = set >> 1; it < total; it += 2) {
             const uint32_t r = it % RAW_SLOTS, st = it * (CK / SK) + part, s = st % A_SLOTS;
             if (!warp_wait_or_abort(bar(Smem::raw_full + r), (it / RAW_SLOTS) & 1u, abort_flag, ctx)) break;
             // two blocks are nine words; the first's codes begin in the middle of one
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(sgen + Smem::raw + r * RAW_SLOT_BYTES + place);
+            const uint8_t *from = sgen + Smem::raw + r * RAW_SLOT_BYTES + place;
             uint32_t wd[2][9];
+            if constexpr (WHOLE) {
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(from);
 #pragma unroll
-            for (int i = 0; i < 18; ++i) wd[i / 9][i % 9] = src[i];
+                for (int i = 0; i < 18; ++i) wd[i / 9][i % 9] = src[i];
+            } else {
+                const int skew = reinterpret_cast<const int *>(sgen + Smem::skew)[r * 32 + (row & 31)];  // even
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(from + (skew & ~3));
+                const uint32_t which = skew & 2 ? 0x5432u : 0x3210u;
+                uint32_t last = src[0];
+#pragma unroll
+                for (int i = 0; i < 18; ++i) {
+                    const uint32_t next = src[i + 1];
+                    wd[i / 9][i % 9] = __byte_perm(last, next, which);
+                    last = next;
+                }
+                const int behind = p.blocks - 8 * c - 4 * part;  // blocks of K from here on
+                // no weights behind K: codes are finite, so a scale of 0 takes them out
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (behind <= 2 * h) wd[h][0] &= 0xFFFF0000u;
+                    if (behind <= 2 * h + 1) wd[h][4] &= 0x0000FFFFu;
+                }
+                for (c += 2; c >= chunks;) c -= chunks;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive_addr(bar(Smem::raw_empty + r));
             bool ok = true;
@@ -583,9 +681,9 @@ struct RowsParams {
     ExpertsPlan plan;
     const uint16_t *x;
     int64_t x_stride;
-    uint4 *rows;  // [pairs][k / 8]
+    uint4 *rows;  // [pairs][padded / 8], zeros behind k
     float *unit;
-    int k;
+    int k, padded;
     bool gather;
     LaunchCtx ctx;
 };
@@ -628,7 +726,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const __g
         }
         const uint16_t *x = p.x + from * p.x_stride;
         // the row stays in registers where it has 2048 values or fewer
-        const int all = p.k / 8;
+        const int all = p.k / 8, padded = p.padded / 8;  // padded: a multiple of 32
         uint4 held[kRowsHeld];
         // the largest: bf16 magnitudes order as integers (what is no number makes the
         // row's results none either)
@@ -645,74 +743,84 @@ __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const __g
         const int e = min(max(static_cast<int>(top >> 7), 15), 254);  // as in the streaming form
         const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
         if (lane == 0) p.unit[i] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-        uint4 *out = p.rows + i * all;
+        uint4 *out = p.rows + i * padded;
         // eight c: of block c / 4, the values from 4 (c % 4) on and from 16 + 4 (c % 4) on
 #pragma unroll
         for (int j = 0; j < kRowsHeld; ++j) {
-            if (j * 32 >= all) break;  // all: a multiple of 32
+            if (j * 32 >= padded) break;
             const uint4 v = held[j];  // lane q of four: the block's values from 8 q on
             const int q = lane & 3, src = (lane & ~3) | (q >> 1);
             const uint2 a0 = shuffle2(make_uint2(v.x, v.y), src), a1 = shuffle2(make_uint2(v.z, v.w), src);
             const uint2 b0 = shuffle2(make_uint2(v.x, v.y), src + 2), b1 = shuffle2(make_uint2(v.z, v.w), src + 2);
             out[j * 32 + lane] = scaled_eight(q & 1 ? a1 : a0, q & 1 ? b1 : b0, f);
         }
-        for (int c = kRowsHeld * 32 + lane; c < all; c += 32) {
+        for (int c = kRowsHeld * 32 + lane; c < padded; c += 32) {
+            if (c >= all) {
+                out[c] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
             const uint16_t *from8 = x + (c >> 2) * 32 + (c & 3) * 4;
             out[c] = scaled_eight(*reinterpret_cast<const uint2 *>(from8), *reinterpret_cast<const uint2 *>(from8 + 16), f);
         }
     }
 }
 
-size_t rows_bytes(int64_t pairs, int64_t k) { return (static_cast<size_t>(pairs) * (2 * k + 4) + 15) & ~size_t(15); }
+int64_t padded_k(int64_t k) { return (k + CK - 1) / CK * CK; }
+size_t rows_bytes(int64_t pairs, int64_t k) { return (static_cast<size_t>(pairs) * (2 * padded_k(k) + 4) + 15) & ~size_t(15); }
 
-template <bool G>
+template <bool G, bool WHOLE>
 cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t *w2, const uint16_t *x, int64_t x_stride,
                         uint16_t *out, int64_t out_stride, int64_t n, int64_t k, void *workspace, cudaStream_t stream,
                         const LaunchCtx &ctx) {
+    const int64_t padded = padded_k(k);
     uint16_t *xr = static_cast<uint16_t *>(workspace);
-    float *unit = reinterpret_cast<float *>(xr + plan.pairs_total * k);
-    CUtensorMap tx, tx64, tw, tw2;
-    const uint64_t row = static_cast<uint64_t>(k / CK) * RAW_ROW, rows = static_cast<uint64_t>(plan.experts) * n;
-    if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, k, plan.pairs_total, k * 2, BK, X_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&tx64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, k, plan.pairs_total, k * 2, BK, X_WIDE, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, row, rows, row, RAW_ROW, G ? BW / 2 : BW) ||
-        !encode_tmap_2d(&tw2, CU_TENSOR_MAP_DATA_TYPE_UINT8, G ? w2 : w, row, rows, row, RAW_ROW, G ? BW / 2 : BW))
+    float *unit = reinterpret_cast<float *>(xr + plan.pairs_total * padded);
+    CUtensorMap tx, tx64, tw = {}, tw2 = {};
+    const uint64_t row = static_cast<uint64_t>(k / kQK) * kQ4_0Bytes, rows = static_cast<uint64_t>(plan.experts) * n;
+    if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, padded, plan.pairs_total, padded * 2, BK, X_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&tx64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, padded, plan.pairs_total, padded * 2, BK, X_WIDE, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    if (WHOLE && (!encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, row, rows, row, RAW_CHUNK, G ? BW / 2 : BW) ||
+                  !encode_tmap_2d(&tw2, CU_TENSOR_MAP_DATA_TYPE_UINT8, G ? w2 : w, row, rows, row, RAW_CHUNK, G ? BW / 2 : BW)))
         return cudaErrorInvalidValue;
     const int tile_rows = G ? BW : 2 * BW;
-    const TileParams p = {plan, unit, out, out_stride, static_cast<int>(n), static_cast<int>(k),
+    const TileParams p = {plan, unit, out, out_stride, {w, G ? w2 : w}, static_cast<int64_t>(row), static_cast<int>(n),
+                          static_cast<int>(padded / CK), static_cast<int>(k / kQK),
                           static_cast<int>((n + tile_rows - 1) / tile_rows), 0x64006400u,
                           n % 2 == 0 && out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(out) % 4 == 0, ctx};
     static int limits[kMaxDevices];
-    const size_t smem = Smem::total(plan.experts);
-    cudaError_t e = ensure_smem(experts_tile_kernel<G>, smem, true, limits);
+    const size_t smem = Layout<WHOLE>::total(plan.experts);
+    cudaError_t e = ensure_smem(experts_tile_kernel<G, WHOLE>, smem, true, limits);
     if (e != cudaSuccess) return e;
-    const RowsParams r = {plan, x, x_stride, reinterpret_cast<uint4 *>(xr), unit, static_cast<int>(k), G, ctx};
+    const RowsParams r = {plan, x, x_stride, reinterpret_cast<uint4 *>(xr), unit, static_cast<int>(k), static_cast<int>(padded), G, ctx};
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((plan.pairs_total + kRowsWarps - 1) / kRowsWarps, int64_t(1) << 30));
     e = launch_kernel(experts_rows_kernel, dim3(grid), dim3(kRowsWarps * 32), 0, stream, 1, r);
     if (e != cudaSuccess) return e;
     const unsigned pairs = std::max(1, device_sm_count() / 2);
-    return launch_kernel(experts_tile_kernel<G>, dim3(2 * pairs), dim3(THREADS), smem, stream, 2, tx, tx64, tw, tw2, p);
+    return launch_kernel(experts_tile_kernel<G, WHOLE>, dim3(2 * pairs), dim3(THREADS), smem, stream, 2, tx, tx64, tw, tw2, p);
 }
 
 }  // namespace
 
-// Whether the tile form takes a product: bf16 in and out, rows that TMA can
-// copy, and enough pairs an expert on average.
+// Whether the tile form takes a product: bf16 in and out, rows of x in 16-byte
+// pieces, and enough pairs an expert on average.
 bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k) {
-    return bf16 && k % CK == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0 &&
+    return bf16 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0 &&
            plan.experts * n < (int64_t(1) << 31) && experts_are_many(plan.pairs_total, plan.experts, k);
 }
 
 size_t experts_rows_bytes(int64_t pairs, int64_t k) { return rows_bytes(pairs, k); }
 
 cudaError_t launch_experts_tile_geglu(const ExpertsGeglu &a, cudaStream_t stream, const LaunchCtx &ctx) {
-    return launch_tile<true>(a.plan, a.wg, a.wu, static_cast<const uint16_t *>(a.x), a.x_stride, static_cast<uint16_t *>(a.h),
-                             a.h_stride, a.n, a.k, a.workspace, stream, ctx);
+    auto *launch = a.k % CK == 0 ? launch_tile<true, true> : launch_tile<true, false>;
+    return launch(a.plan, a.wg, a.wu, static_cast<const uint16_t *>(a.x), a.x_stride, static_cast<uint16_t *>(a.h), a.h_stride,
+                  a.n, a.k, a.workspace, stream, ctx);
 }
 
 cudaError_t launch_experts_tile_down(const ExpertsDown &a, void *z, void *rows, cudaStream_t stream, const LaunchCtx &ctx) {
-    return launch_tile<false>(a.plan, a.wd, nullptr, static_cast<const uint16_t *>(a.h), a.h_stride, static_cast<uint16_t *>(z),
-                              a.n, a.n, a.k, rows, stream, ctx);
+    auto *launch = a.k % CK == 0 ? launch_tile<false, true> : launch_tile<false, false>;
+    return launch(a.plan, a.wd, nullptr, static_cast<const uint16_t *>(a.h), a.h_stride, static_cast<uint16_t *>(z), a.n, a.n, a.k,
+                  rows, stream, ctx);
 }
 
 }  // namespace qmm

@@ -566,8 +566,8 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
  * Arithmetic: sums in fp32.  With an fp32 output the weights are exact, a bf16
  * input too, and an fp32 input enters in two binary16 parts (22 bits of it, and
  * 2^-39 of the largest of its row's 256 values around it).  With a bf16 output
- * an fp32 input enters in 11 bits.  With bf16 in and out, k % 256 == 0, and as many
- * pairs as experts at least or k >= 4096, each weight is rounded once to binary16:
+ * an fp32 input enters in 11 bits.  With bf16 in and out, rows of x or h in
+ * multiples of 16 bytes, and as many pairs as experts at least or k >= 4096, each weight is rounded once to binary16:
  * 2^-12 of it, where the output's own rounding is 2^-9; scales beyond 8188 overflow
  * there.
  * Their down projections are rounded to bf16 once before the sum.  A row of x or
