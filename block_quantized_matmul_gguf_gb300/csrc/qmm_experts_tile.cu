@@ -70,7 +70,7 @@ constexpr uint32_t D_COLS = 2 * BT, A_COLS = SK / 2, TMEM_COLS = 512;  // two ac
 static_assert(X_SLOTS % 2 == 0 && CK / SK % 2 == 0, "two x warps");
 static_assert(D_COLS + A_SLOTS * A_COLS <= TMEM_COLS, "tensor memory");
 
-constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_X1 = 3, WARP_EPI = 4, EPI_WARPS = 8, WARP_DEQ = 12, DEQ_WARPS = 16;
+constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_THIRD = 3, WARP_EPI = 4, EPI_WARPS = 8, WARP_DEQ = 12, DEQ_WARPS = 16;
 constexpr int THREADS = (WARP_DEQ + DEQ_WARPS) * 32;
 constexpr int X_BOX = 16, X_WIDE = BT / 2;  // rows of a copy of x: where few are wanted, and otherwise
 
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init_addr(bar(Smem::a_empty + i), 1);
         }
         for (int i = 0; i < RAW_SLOTS; ++i) {
-            mbar_init_addr(bar(Smem::raw_full + i), WHOLE ? 1 : 33);  // 33: each lane's copies, and the skews
+            mbar_init_addr(bar(Smem::raw_full + i), WHOLE ? 1 : 65);  // 65: each lane's copies in two warps, and the skews
             mbar_init_addr(bar(Smem::raw_empty + i), DEQ_WARPS / 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -366,9 +366,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int chunks = p.chunks;
 
     Items at = items_from(p, pair, num_pairs);
-    if (warp == WARP_X || warp == WARP_X1) {
+    if (warp == WARP_X || (WHOLE && warp == WARP_THIRD)) {
         pdl_wait();
-        const uint32_t which = warp == WARP_X1;  // every other stage; an item has an even number of them
+        constexpr int step = WHOLE ? 2 : 1;  // every other stage; an item has an even number of them
+        const uint32_t which = warp != WARP_X;
         uint32_t it = which;
         bool ok = true;
         while (ok && at.item < items) {
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool mine = sub < SUBS && (many || row < first + half);
             const CUtensorMap *map = many ? &tmap_x64 : &tmap_x;
             const uint32_t bytes = static_cast<uint32_t>(many ? 2 * X_WIDE : t.width) * SK * 2;
-            for (int st = static_cast<int>(which); st < chunks * (CK / SK); st += 2, it += 2) {
+            for (int st = static_cast<int>(which); st < chunks * (CK / SK); st += step, it += step) {
                 const uint32_t s = it % X_SLOTS, full = bar(Smem::x_full + s);
                 if (!warp_wait_or_abort(bar(Smem::x_empty + s), ((it / X_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
                     ok = false;
@@ -398,15 +399,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             // all copies into this CTA have come, and both CTAs have read what this
             // one sent: nothing of the peer's is on its way here any more
-            for (uint32_t s = which; s < X_SLOTS; s += 2)
+            for (uint32_t s = which; s < X_SLOTS; s += step)
                 if (it > s) {
-                    const uint32_t last = it - 2 - ((it - 2 - s) % X_SLOTS);
+                    const uint32_t last = it - step - ((it - step - s) % X_SLOTS);
                     wait_drain(bar(Smem::x_full + s), (last / X_SLOTS) & 1u, ctx);
                     if (ok) wait_drain(bar(Smem::x_empty + s), (last / X_SLOTS) & 1u, ctx);
                 }
         }
-    } else if (warp == WARP_RAW) {
+    } else if (warp == WARP_RAW || warp == WARP_THIRD) {
         const int64_t w_bytes = p.plan.experts * p.row_bytes * p.n;
+        const int half = warp == WARP_THIRD;  // not WHOLE: of the rows
         uint32_t it = 0;
         bool ok = true;
         while (ok && at.item < items) {
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                 } else {
 #pragma unroll 1
-                    for (int rows32 = 0; rows32 < BW / 32; ++rows32) {
+                    for (int rows32 = half * (BW / 64); rows32 < (half + 1) * (BW / 64); ++rows32) {
                         const uint8_t *w = p.w[G ? rows32 >> 1 : 0];
                         const int64_t more = first + (G ? rows32 & 1 : rows32) * 32 * p.row_bytes + c * RAW_CHUNK;
                         const uint32_t to32 = to + rows32 * 32 * RAW_ROW;
@@ -464,9 +466,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                     copies_arrive(full);
-                    reinterpret_cast<int *>(sgen + Smem::skew)[s * 32 + lane] = skew;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_addr(full);
+                    if (half == 0) {
+                        reinterpret_cast<int *>(sgen + Smem::skew)[s * 32 + lane] = skew;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_addr(full);
+                    }
                 }
             }
         }
