@@ -24,6 +24,10 @@
 //               its box's, not its rows': boxes of 16 alone cost 23 us more at 2047 tokens)
 //   warp 1      MMA, issued by the whole warp's elected lane
 //   warp 2      weights as they are: boxes of 64 or 128 rows x 144 bytes
+//   warps 28-31 the same where K is no multiple of 256 and rows lie on no 16 bytes:
+//               the pieces of 16 that hold them, by cp.async, 32 rows a warp (GeGLU of 64
+//               experts of 1024 x 2016, 2047 tokens: one warp 203 us, two 173, four 147;
+//               a bulk copy a row, as TMA wants a request for each, 592)
 //   warps 4-11  epilogue, two for each quarter of the lanes
 //   warps 12-27 dequantisers: TMEM lanes 32 (w % 4) .., one stage (128 of K) of every
 //               other chunk (256 of K).  Weights are formed in registers before their
@@ -70,8 +74,10 @@ constexpr uint32_t D_COLS = 2 * BT, A_COLS = SK / 2, TMEM_COLS = 512;  // two ac
 static_assert(X_SLOTS % 2 == 0 && CK / SK % 2 == 0, "two x warps");
 static_assert(D_COLS + A_SLOTS * A_COLS <= TMEM_COLS, "tensor memory");
 
-constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_THIRD = 3, WARP_EPI = 4, EPI_WARPS = 8, WARP_DEQ = 12, DEQ_WARPS = 16;
-constexpr int THREADS = (WARP_DEQ + DEQ_WARPS) * 32;
+constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_X1 = 3, WARP_EPI = 4, EPI_WARPS = 8, WARP_DEQ = 12, DEQ_WARPS = 16;
+constexpr int WARP_COPY = WARP_DEQ + DEQ_WARPS, COPY_WARPS = BW / 32;  // not WHOLE: warps that copy weights
+template <bool WHOLE>
+constexpr int kTileThreads = (WARP_COPY + (WHOLE ? 0 : COPY_WARPS)) * 32;
 constexpr int X_BOX = 16, X_WIDE = BT / 2;  // rows of a copy of x: where few are wanted, and otherwise
 
 template <bool WHOLE>
@@ -279,7 +285,7 @@ constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BW >> 4) << 24);
 // G: GeGLU.  A CTA's 128 accumulator rows are then 64 features: in lane quarter q,
 // lanes 0-15 hold the gate rows of features 16q .. 16q+15, lanes 16-31 their up rows.
 template <bool G, bool WHOLE>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
     experts_tile_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_x64,
                         const __grid_constant__ CUtensorMap tmap_w,
                         const __grid_constant__ CUtensorMap tmap_w2, const __grid_constant__ TileParams p) {
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init_addr(bar(Smem::a_empty + i), 1);
         }
         for (int i = 0; i < RAW_SLOTS; ++i) {
-            mbar_init_addr(bar(Smem::raw_full + i), WHOLE ? 1 : 65);  // 65: each lane's copies in two warps, and the skews
+            mbar_init_addr(bar(Smem::raw_full + i), WHOLE ? 1 : COPY_WARPS * 32 + 1);  // each lane's copies, and the skews
             mbar_init_addr(bar(Smem::raw_empty + i), DEQ_WARPS / 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -331,8 +337,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // (TMA) are taken at once, and only the warps that read rows and units or write
     // results wait for the rows' kernel: 128 tokens 43.4 -> 40.0 us.
     {  // tiles in front of each expert's
-        __shared__ int32_t part[THREADS / 32];
-        const int per = (p.plan.experts + THREADS - 1) / THREADS;
+        __shared__ int32_t part[kTileThreads<WHOLE> / 32];
+        const int per = (p.plan.experts + kTileThreads<WHOLE> - 1) / kTileThreads<WHOLE>;
         const int e0 = min(p.plan.experts, static_cast<int>(threadIdx.x) * per), e1 = min(p.plan.experts, e0 + per);
         int mine = 0, start;
         for (int e = e0; e < e1; ++e) mine += (expert_count(p, e, start) + BT - 1) / BT;
@@ -366,10 +372,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int chunks = p.chunks;
 
     Items at = items_from(p, pair, num_pairs);
-    if (warp == WARP_X || (WHOLE && warp == WARP_THIRD)) {
+    if (warp == WARP_X || warp == WARP_X1) {
         pdl_wait();
-        constexpr int step = WHOLE ? 2 : 1;  // every other stage; an item has an even number of them
-        const uint32_t which = warp != WARP_X;
+        const uint32_t which = warp != WARP_X;  // every other stage; an item has an even number of them
         uint32_t it = which;
         bool ok = true;
         while (ok && at.item < items) {
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool mine = sub < SUBS && (many || row < first + half);
             const CUtensorMap *map = many ? &tmap_x64 : &tmap_x;
             const uint32_t bytes = static_cast<uint32_t>(many ? 2 * X_WIDE : t.width) * SK * 2;
-            for (int st = static_cast<int>(which); st < chunks * (CK / SK); st += step, it += step) {
+            for (int st = static_cast<int>(which); st < chunks * (CK / SK); st += 2, it += 2) {
                 const uint32_t s = it % X_SLOTS, full = bar(Smem::x_full + s);
                 if (!warp_wait_or_abort(bar(Smem::x_empty + s), ((it / X_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
                     ok = false;
@@ -399,22 +404,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             // all copies into this CTA have come, and both CTAs have read what this
             // one sent: nothing of the peer's is on its way here any more
-            for (uint32_t s = which; s < X_SLOTS; s += step)
+            for (uint32_t s = which; s < X_SLOTS; s += 2)
                 if (it > s) {
-                    const uint32_t last = it - step - ((it - step - s) % X_SLOTS);
+                    const uint32_t last = it - 2 - ((it - 2 - s) % X_SLOTS);
                     wait_drain(bar(Smem::x_full + s), (last / X_SLOTS) & 1u, ctx);
                     if (ok) wait_drain(bar(Smem::x_empty + s), (last / X_SLOTS) & 1u, ctx);
                 }
         }
-    } else if (warp == WARP_RAW || warp == WARP_THIRD) {
+    } else if (WHOLE ? warp == WARP_RAW : warp >= WARP_COPY) {
         const int64_t w_bytes = p.plan.experts * p.row_bytes * p.n;
-        const int half = warp == WARP_THIRD;  // not WHOLE: of the rows
+        const int rows32 = warp - WARP_COPY;  // not WHOLE: which 32 rows of the slot
         uint32_t it = 0;
         bool ok = true;
         while (ok && at.item < items) {
             const Item t = next_item(p, ex, num_pairs, lane, at);
             const int row0 = G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) : t.row_block * 2 * BW + static_cast<int>(rank) * BW;
-            // 10 pieces a row, 32 rows in ten steps, and so on: a row's skew repeats after
+            // A warp copies 32 rows, 10 pieces each, in ten steps.  A row's skew repeats after
             // 32 rows, whose bytes are a multiple of 16.  Rows behind the expert's are
             // another's or zeros, and dropped.
             const int64_t base = (static_cast<int64_t>(t.expert) * p.n + row0) * p.row_bytes;
@@ -445,28 +450,25 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     __syncwarp();
                 } else {
-#pragma unroll 1
-                    for (int rows32 = half * (BW / 64); rows32 < (half + 1) * (BW / 64); ++rows32) {
-                        const uint8_t *w = p.w[G ? rows32 >> 1 : 0];
-                        const int64_t more = first + (G ? rows32 & 1 : rows32) * 32 * p.row_bytes + c * RAW_CHUNK;
-                        const uint32_t to32 = to + rows32 * 32 * RAW_ROW;
-                        if (more + 32 * p.row_bytes + 176 <= w_bytes) {  // windows end below 31 rows + 176 bytes
-                            const uint8_t *src = w + more;
+                    const uint8_t *w = p.w[G ? rows32 >> 1 : 0];
+                    const int64_t more = first + (G ? rows32 & 1 : rows32) * 32 * p.row_bytes + c * RAW_CHUNK;
+                    const uint32_t to32 = to + rows32 * 32 * RAW_ROW;
+                    if (more + 32 * p.row_bytes + 176 <= w_bytes) {  // windows end below 31 rows + 176 bytes
+                        const uint8_t *src = w + more;
 #pragma unroll
-                            for (int i = 0; i < Raw<WHOLE>::pieces; ++i) copy16(to32 + place_of(i), src + window[i]);
-                        } else {
+                        for (int i = 0; i < Raw<WHOLE>::pieces; ++i) copy16(to32 + place_of(i), src + window[i]);
+                    } else {
 #pragma unroll 1
-                            for (int i = 0; i < Raw<WHOLE>::pieces; ++i) {
-                                const int at32 = i * 32 + lane;
-                                const int64_t from = more + ((base + at32 / 10 * p.row_bytes) & ~int64_t(15)) - first + at32 % 10 * 16;
-                                const int64_t left = w_bytes - from;
-                                copy16_some(to32 + place_of(i), w + (left > 0 ? from : 0),
-                                            left >= 16 ? 16u : left > 0 ? static_cast<uint32_t>(left) : 0u);
-                            }
+                        for (int i = 0; i < Raw<WHOLE>::pieces; ++i) {
+                            const int at32 = i * 32 + lane;
+                            const int64_t from = more + ((base + at32 / 10 * p.row_bytes) & ~int64_t(15)) - first + at32 % 10 * 16;
+                            const int64_t left = w_bytes - from;
+                            copy16_some(to32 + place_of(i), w + (left > 0 ? from : 0),
+                                        left >= 16 ? 16u : left > 0 ? static_cast<uint32_t>(left) : 0u);
                         }
                     }
                     copies_arrive(full);
-                    if (half == 0) {
+                    if (rows32 == 0) {
                         reinterpret_cast<int *>(sgen + Smem::skew)[s * 32 + lane] = skew;
                         __syncwarp();
                         if (lane == 0) mbar_arrive_addr(full);
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             commit(one, bars + 8u * Smem::final);
             wait_drain(bar(Smem::final), 0, ctx);
         }
-    } else if (warp >= WARP_DEQ) {
+    } else if (warp >= WARP_DEQ && warp < WARP_COPY) {
         // every other chunk, and of it one stage, as two halves of 64 values of K
         const int q = warp & 3, set = (warp - WARP_DEQ) >> 2, part = set & 1;
         const int row = G ? (lane >> 4) * (BW / 2) + q * 16 + (lane & 15) : q * 32 + lane;
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_addr(bar(Smem::a_full + s));
         }
-    } else if (warp >= WARP_EPI) {
+    } else if (warp >= WARP_EPI && warp < WARP_DEQ) {
         const int q = warp & 3, part = (warp - WARP_EPI) >> 2;  // the two warps of a quarter take every other 32 columns
         const bool odd = lane & 1, upper = lane >= 16;
         ulonglong2 *table = reinterpret_cast<ulonglong2 *>(sgen + Smem::cols) + q * BT;
@@ -801,7 +803,7 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
     e = launch_kernel(experts_rows_kernel, dim3(grid), dim3(kRowsWarps * 32), 0, stream, 1, r);
     if (e != cudaSuccess) return e;
     const unsigned pairs = std::max(1, device_sm_count() / 2);
-    return launch_kernel(experts_tile_kernel<G, WHOLE>, dim3(2 * pairs), dim3(THREADS), smem, stream, 2, tx, tx64, tw, tw2, p);
+    return launch_kernel(experts_tile_kernel<G, WHOLE>, dim3(2 * pairs), dim3(kTileThreads<WHOLE>), smem, stream, 2, tx, tx64, tw, tw2, p);
 }
 
 }  // namespace

@@ -349,13 +349,15 @@ struct ExpertsDown {
 size_t experts_down_workspace_bytes(int64_t pairs, int64_t n, int64_t k);
 cudaError_t launch_experts_down(const ExpertsDown &args, cudaStream_t stream, const LaunchCtx &ctx);
 
-// The tile form (qmm_experts_tile.cu) and when it is taken: from one pair an expert
-// on average, or where K is long and the streaming form's x is too much for it.
-// Streaming against tiles, bf16, GeGLU of 8 out of 64 experts of 1024 x 2048: 2
-// tokens 15.6 and 18.4 us, 6 25.9 and 29.5, 8 41.2 and 34.8, 63 60.8 and 45.0; their
-// down projections: 6 tokens 16.9 and 20.3, 8 31.2 and 22.7.  Two out of 8 experts
-// of 14336 x 4096, one token: 46.7 and 45.9, and down, K 14336: 71.1 and 53.6.
-inline bool experts_are_many(int64_t pairs, int experts, int64_t k) { return pairs >= experts || k >= 4096; }
+// The tile form (qmm_experts_tile.cu) and when it is taken: from half a pair an expert
+// on average, or where K is long and the streaming form's x is too much for it.  Below
+// that the GPU's times are alike, and the host has one launch and no maps of x to make.
+// Streaming against tiles, bf16, GeGLU of 8 out of 64 experts of 1024 x 2048: 1 token
+// 11.5 and 11.4 us, 4 25.9 and 24.6, 7 31.4 and 25.1, 63 60.8 and 38.6; down: 1 token
+// 11.1 and 10.5, 6 16.8 and 18.1, 7 31.8 and 21.2.  Four out of 64 experts of 800 x
+// 1568, 8 tokens: 37.7 and 23.8.  Down, two out of 8 experts of 4096 x 14336, one
+// token: 71.1 and 46.4.
+inline bool experts_are_many(int64_t pairs, int experts, int64_t k) { return 2 * pairs >= experts || k >= 4096; }
 bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k);
 cudaError_t launch_experts_tile_geglu(const ExpertsGeglu &args, cudaStream_t stream, const LaunchCtx &ctx);
 size_t experts_rows_bytes(int64_t pairs, int64_t k);  // of x as that form reads it

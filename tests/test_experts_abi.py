@@ -178,8 +178,9 @@ def test_products_need_a_plan(lib):
 
 def test_workspace_sizes(lib):
     small, many = lib.qmm_experts_geglu_workspace_bytes, lib.qmm_experts_down_workspace_bytes
-    assert small(3, 2, 8, 256) == 0  # fewer pairs than experts: no rows to lay out
-    assert small(4, 2, 8, 256) >= 8 * 256 * 2 and small(1, 1, 8, 4096) >= 4096 * 2
+    assert small(1, 3, 8, 256) == 0  # few pairs for the experts: no rows to lay out
+    assert small(2, 2, 8, 256) >= 4 * 256 * 2 and small(1, 1, 8, 4096) >= 4096 * 2
+    assert small(2, 2, 8, 288) >= 4 * 512 * 2  # rows are laid out in multiples of 256
     assert small(0, 2, 8, 256) == small(4, 33, 8, 256) == small(4, 2, 1025, 256) == small(4, 2, 8, 1 << 21) == 0
     # z as fp32, or as bf16 with the rows of h behind it
     assert many(4, 2, 64, 256) >= 8 * 64 * 4 and many(4, 2, 64, 256) >= 8 * (64 + 256) * 2

@@ -84,9 +84,9 @@ def run_down(qmm, rng, tokens, experts, topk, n, k, h_type=F32, y_type=F32, kind
 SIZES = [  # tokens, experts, topk, n, k
     (1, 1, 1, 1, 32), (1, 4, 2, 16, 256), (3, 5, 5, 33, 64), (2, 8, 3, 100, 512), (7, 3, 2, 48, 288), (9, 16, 4, 130, 96),
     (16, 8, 2, 64, 1024), (31, 6, 3, 20, 800), (5, 4, 2, 96, 2048), (4, 3, 3, 40, 4096), (3, 2, 2, 33, 8192),
-    (2, 64, 4, 130, 512), (3, 40, 8, 70, 2048), (1, 64, 8, 300, 4096),
+    (2, 64, 4, 130, 512), (2, 40, 8, 70, 2048), (1, 64, 8, 300, 4096),
 ]
-LONG = [(70, 4, 2, 40, 256), (130, 3, 2, 64, 512), (300, 8, 4, 260, 256), (513, 2, 1, 136, 512), (257, 16, 8, 64, 288), (20, 64, 2, 100, 512), (90, 5, 2, 150, 32),
+LONG = [(70, 4, 2, 40, 256), (130, 3, 2, 64, 512), (300, 8, 4, 260, 256), (513, 2, 1, 136, 512), (257, 16, 8, 64, 288), (20, 96, 2, 100, 512), (90, 5, 2, 150, 32),
         (140, 3, 1, 70, 992), (200, 6, 3, 129, 2080), (60, 16, 4, 256, 480)]
 TYPES = [(F32, F32), (BF16, BF16), (BF16, F32), (F32, BF16)]
 
