@@ -39,10 +39,15 @@
 // its pair's items in them by two ballots.
 // Every wait is bounded, as in the prefill GEMM.
 //
-// Bound by the dequantisers and their hand-over to the tensor cores for prompts (8 out
-// of 64 experts of 1024 x 2048, 2047 tokens: tiles 107 us of 123 to 126, 1.28 PFLOP/s), by
-// the weights' bytes and the fill of each expert's pipeline below some 16 rows an
-// expert (128 tokens: 46.5 us, 3.3 TB/s).  The rows' kernel writes 67 MB in 15 us.
+// Bound, for prompts, by the hand-overs between the roles and by the x slots' round
+// trip, with the tensor cores at work 64 % of the time and two thirds of the issue slots
+// taken (8 out of 64 experts of 1024 x 2048, 2047 tokens: 105 us of 122, 1.31 PFLOP/s;
+// without the weights' arithmetic 6 us less, with an eighth of the products 11, without
+// loads 12).  With few rows an expert by the weights' bytes and the fill of each
+// item's pipeline (128 tokens: 39.6 us in all, 3.9 TB/s).  The rows' kernel writes 67 MB
+// in 15 us for prompts.  Tiles of 192 rows, which dequantise experts of 257 to 384 rows
+// twice instead of three times, fit tensor memory with stages of 64 of K alone, and
+// those cost more hand-overs than they save (131 us for 125).
 #include "qmm_internal.h"
 #include "qmm_tc.cuh"
 

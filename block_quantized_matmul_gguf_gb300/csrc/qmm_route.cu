@@ -6,8 +6,9 @@
 // among the kept groups, ties to the lowest index.  Without a bias c orders as
 // l does, and the choice compares the logits themselves.  With one, c is
 // formed in fp32 with an error that the comments bound; where compared values
-// lie nearer than that allows, they are formed again in 64 bits.  So the choice is that of 64 bits everywhere, at the
-// price of 32 (a token in some thousands takes the second way).
+// lie nearer than that allows, they are formed again in 64 bits.  So the choice is
+// that of 64 bits everywhere, at the price of 32 (a token in some thousands takes the
+// second way).
 //
 // A warp per token.  Each lane sorts its values as words of a key's upper bits and
 // the expert's index, so that a round of the choice is one warp-wide maximum; a few
@@ -22,8 +23,9 @@
 // memory; beyond, clusters leave them in the workspace and a second launch places
 // the pairs.
 //
-// Bound by latency for few tokens, by instructions for many (some 500 a token
-// with 256 experts).
+// Bound by latency for few tokens (one of 64 experts 4.0 us, 128 of 128 6.4), by
+// instructions and their dependencies for many (some 500 a token with 256 experts:
+// 8191 of them 29 us with the second launch, 53 % of the issue slots).
 #include "qmm_internal.h"
 
 #include <cooperative_groups.h>
