@@ -12,7 +12,9 @@
 // Precision.  x enters as one binary16 value, scaled by a power of two per row
 // and 256 values so that the largest lies in [2^14, 2^15): a bf16 x exactly (down
 // to 2^-31 of that largest), an fp32 x rounded to 11 bits, which is less than a
-// bf16 output shows.  For fp32 outputs an fp32 x enters in two parts (22 bits).
+// bf16 output shows.  For fp32 outputs an fp32 x enters in two parts (22 bits), which
+// are two products, or, with up to four pairs, other columns of one (16 tokens 44.1 us
+// for two, 40.6 for one).
 // For bf16 outputs a code masked in place is a subnormal binary16 number, n 2^-24
 // (16 n 2^-24 for the upper of two, the 16 taken out of x), and -8 sum x is where
 // the sum begins; fp32 outputs take two more instructions a pair for the normal
@@ -37,6 +39,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace qmm {
 namespace experts {
@@ -214,7 +217,7 @@ __device__ __forceinline__ float4 load_four<uint16_t>(const uint16_t *p, bool wi
 // the codes of a word have.
 template <bool EXACT, int PARTS, int NB, typename T>
 __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *scale, float *sums, const T *row, int chunk,
-                                        int nb, int lane) {
+                                     int nb, int lane, bool packed) {
     const int t = lane & 3, g = lane >> 2;
     const int blocks = min(8, p.blocks - chunk * 8);
     float4 v[8][2];
@@ -252,6 +255,13 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
                     part[1][2 * h + i] = pack_half(y[2 * i] - low_half(hi), y[2 * i + 1] - high_half(hi));
                 if constexpr (!EXACT) sum += (low_half(hi) + high_half(hi)) * (h ? 16.0f : 1.0f);
             }
+        }
+        if (PARTS == 2 && packed) {
+            const bool low = g >= 4;
+            reinterpret_cast<uint4 *>(xs + (chunk * 8 + b) * 512)[lane] =
+                make_uint4(low ? part[PARTS - 1][0] : part[0][0], low ? part[PARTS - 1][1] : part[0][1],
+                           low ? part[PARTS - 1][2] : part[0][2], low ? part[PARTS - 1][3] : part[0][3]);
+            continue;
         }
         char *to = xs + ((chunk * 8 + b) * NB + nb) * PARTS * 512;
 #pragma unroll
@@ -518,6 +528,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
 
     int done = 0;
     int held_expert = -1, held_group = -1, held_panel = -1;
+    bool held_packed = false;
     const int panels = (p.chunks + p.x_panel - 1) / p.x_panel;
     while (at.left > 0) {
         Place next = at;
@@ -526,6 +537,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
         const int first = at.start + at.group * 8 * NB;              // of the pairs
         const int cols = min(8 * NB, at.count - at.group * 8 * NB);  // of them here
         const int used = (cols + 7) / 8;
+        const bool packed = PARTS == 2 && NB == 1 && cols <= 4;  // columns 4 .. 7: the small parts of 0 .. 3
+        const int x_block = packed ? 512 : L::x_block;
         float total[kTiles][NB][4];
 #pragma unroll
         for (int r = 0; r < kTiles; ++r)
@@ -546,7 +559,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
         for (int panel = 0; panel < panels; ++panel) {
             const int c0 = panel * p.x_panel, c1 = min(p.chunks, c0 + p.x_panel);
             if (at.expert != held_expert || at.group != held_group || panel != held_panel) {
-                bool other = panel != held_panel;  // the rows of x are not those that shared memory holds
+                // the rows of x are not those that shared memory holds, or not in that order
+                bool other = panel != held_panel || packed != held_packed;
                 __syncthreads();
                 if (at.expert != held_expert || at.group != held_group) {
                     if (threadIdx.x < 8 * NB) {
@@ -570,20 +584,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                 if (other)
                     for (int u = warp; u < (c1 - c0) * used; u += warps) {
                         const int n = u % used, c = u / used;
-                        const int row = src[n * 8 + g];
+                        const int row = src[packed ? g & 3 : n * 8 + g];
                         // addresses count from the panel's first chunk
-                        char *xp = xs - static_cast<int64_t>(c0) * 8 * L::x_block;
+                        char *xp = xs - static_cast<int64_t>(c0) * 8 * x_block;
                         float *sp = scale - c0 * 8 * NB, *mp = sums - c0 * 64 * NB;
                         if (p.x_bf16)
                             stage_x<EXACT, PARTS, NB, uint16_t>(
-                                p, xp, sp, mp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane);
+                                p, xp, sp, mp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane, packed);
                         else
                             stage_x<EXACT, PARTS, NB, float>(
-                                p, xp, sp, mp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane);
+                                p, xp, sp, mp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane, packed);
                     }
                 held_expert = at.expert;
                 held_group = at.group;
                 held_panel = panel;
+                held_packed = packed;
                 __syncthreads();
             }
             for (int c = c0 + (kw - c0 % p.kw + p.kw) % p.kw; c < c1; c += p.kw) {
@@ -603,14 +618,26 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                     copy_wait<1>();
                     __syncwarp();
                 }
-                if (there && ok)
-                    stage_products<EXACT, PARTS, NB, ALIGNED>(
-                        ring_ptr + (done & 1) * L::stage, xs + (c - c0) * 8 * L::x_block, scale + (c - c0) * 8 * NB,
-                        sums + (c - c0) * 64 * NB, min(8, p.blocks - c * 8), skew, p.magic, lane, used, total);
+                if (there && ok) {
+                    auto products = [&](auto parts) {
+                        stage_products<EXACT, decltype(parts)::value, NB, ALIGNED>(
+                            ring_ptr + (done & 1) * L::stage, xs + (c - c0) * 8 * x_block, scale + (c - c0) * 8 * NB,
+                            sums + (c - c0) * 64 * NB, min(8, p.blocks - c * 8), skew, p.magic, lane, used, total);
+                    };
+                    if (packed)
+                        products(std::integral_constant<int, 1>());
+                    else
+                        products(std::integral_constant<int, PARTS>());
+                }
                 __syncwarp();
                 ++done;
             }
         }
+        if (packed)  // both parts of columns 2 t and 2 t + 1
+#pragma unroll
+            for (int r = 0; r < kTiles; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) total[r][0][i] += __shfl_xor_sync(0xFFFFFFFFu, total[r][0][i], 2);
         // the item's sums: element (r, n, i) of lane is row 16 r + 8 (i / 2) + g, pair 8 n + 2 t + i % 2
         auto store = [&](int r, int i, int l, int to, float a, float b) {
             const int64_t row = row0 + 16 * r + 8 * (i >> 1) + (l >> 2);
