@@ -173,20 +173,43 @@ __device__ __forceinline__ void load_boxes(const StreamParams &p, const CUtensor
     tma_load_2d(stage, w0, chunk * 144, row, bar);
     if constexpr (GEGLU) tma_load_2d(stage + kRows / 2 * 144, w1, chunk * 144, row, bar);
 }
+// Ten pieces a row, 32 rows in ten steps, which repeat: a row's skew does, as the bytes
+// of 32 rows are a multiple of 16.
+struct Windows {
+    int64_t base = -1, first;  // of the item's rows, and down to 16 bytes
+    int at[10];                // the lane's pieces from there
+};
 template <bool GEGLU>
-__device__ __forceinline__ void load_windows(const StreamParams &p, uint32_t stage, int expert, int64_t row0, int chunk, int lane) {
+__device__ __forceinline__ void load_windows(const StreamParams &p, Windows &win, uint32_t stage, int expert, int64_t row0, int chunk,
+                                             int lane) {
     constexpr int pitch = 176, pieces = 10;
-    constexpr int rows = GEGLU ? kRows / 2 : kRows;  // of a matrix
-    const int64_t first = expert * p.matrix_bytes + chunk * 144;
-    const int bytes = min(8, p.blocks - chunk * 8) * kQ4_0Bytes;
+    const int64_t base = expert * p.matrix_bytes + row0 * p.row_bytes;
+    auto piece = [&](int i) {
+        const int at32 = i * 32 + lane;
+        return ((base + at32 / pieces * p.row_bytes) & ~int64_t(15)) - (base & ~int64_t(15)) + at32 % pieces * 16;
+    };
+    auto place = [&](int i) { return (i * 32 + lane) / pieces * pitch + (i * 32 + lane) % pieces * 16; };
+    if (base != win.base) {
+        win.base = base;
+        win.first = base & ~int64_t(15);
+#pragma unroll
+        for (int i = 0; i < pieces; ++i) win.at[i] = static_cast<int>(piece(i));
+    }
 #pragma unroll 1
-    for (int i = 0; i < pieces * kRows / 32; ++i) {
-        const int idx = i * 32 + lane, row = idx / pieces, piece = idx - row * pieces;
-        const int64_t r = row0 + row % rows;
-        const int64_t from = first + min(r, p.n - 1) * p.row_bytes;
-        const int64_t window = (from & ~int64_t(15)) + piece * 16;
-        if (window < from + bytes)
-            copy16(stage + row * pitch + piece * 16, p.w[row / rows] + window, static_cast<uint32_t>(min(int64_t(16), p.w_bytes - window)));
+    for (int rows32 = 0; rows32 < kRows / 32; ++rows32) {  // rows behind the expert's are not stored
+        const uint8_t *w = p.w[GEGLU ? rows32 : 0];
+        const int64_t from = win.first + (GEGLU ? 0 : rows32) * 32 * p.row_bytes + chunk * 144;
+        const uint32_t to = stage + rows32 * 32 * pitch;
+        if (from + 32 * p.row_bytes + pitch <= p.w_bytes) {  // windows end below 31 rows + 176 bytes
+#pragma unroll
+            for (int i = 0; i < pieces; ++i) copy16(to + place(i), w + from + win.at[i], 16);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < pieces; ++i) {
+                const int64_t at = from + piece(i), left = p.w_bytes - at;
+                copy16(to + place(i), w + (left > 0 ? at : 0), left >= 16 ? 16u : left > 0 ? static_cast<uint32_t>(left) : 0u);
+            }
+        }
     }
 }
 
@@ -276,11 +299,11 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
 }
 
 // A warp's products of one stage: kTiles tiles of 16 rows against NB groups of
-// eight pairs.  skew: bytes by which each of the lane's four rows (g, g + 8 of
-// each tile) begins behind its window.
+// eight pairs.  skew: bytes by which the lane's rows (g, g + 8 of each tile, which
+// repeat after two) begin behind their windows.
 template <bool EXACT, int PARTS, int NB, bool ALIGNED>
 __device__ __forceinline__ void stage_products(const char *stage, const char *xs, const float *scale, const float *sums,
-                                               int blocks, const int (&skew)[kTiles][2], uint32_t magic, int lane,
+                                               int blocks, const int (&skew)[2][2], uint32_t magic, int lane,
                                                int used, float (&total)[kTiles][NB][4]) {
     constexpr int pitch = ALIGNED ? 144 : 176;
     const int t = lane & 3, g = lane >> 2;
@@ -378,21 +401,26 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
             block(2 * j + 1, q1, d1);
         }
     } else {
-#pragma unroll 1
-        for (int b = 0; b < blocks; ++b) {
-            uint32_t q[kTiles][2];
-            float d[kTiles][2];
+        // the same behind each row's skew; an odd number of blocks ends with one of scale 0
+#pragma unroll 2
+        for (int j = 0; 2 * j < blocks; ++j) {
+            uint32_t q0[kTiles][2], q1[kTiles][2];
+            float d0[kTiles][2], d1[kTiles][2];
+            const bool both = 2 * j + 1 < blocks;
 #pragma unroll
             for (int r = 0; r < kTiles; ++r)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const char *row = stage + (r * 16 + h * 8 + g) * pitch;
-                    const int at = skew[r][h] + 18 * b;
-                    const uint32_t *w = reinterpret_cast<const uint32_t *>(row + ((at + 2) & ~3)) + t;
-                    q[r][h] = __byte_perm(w[0], w[1], (at + 2) & 2 ? 0x5432 : 0x3210);
-                    d[r][h] = half_bits_to_float(*reinterpret_cast<const uint16_t *>(row + at));
+                    const int at = skew[r & 1][h];  // repeats after 32 rows
+                    const char *row = stage + (r * 16 + h * 8 + g) * pitch + 36 * j;
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(row + (at & ~3)) + t;
+                    q0[r][h] = __byte_perm(w[0], w[1], at & 2 ? 0x7654 : 0x5432);
+                    q1[r][h] = __byte_perm(w[5], w[6], at & 2 ? 0x5432 : 0x3210);
+                    d0[r][h] = half_bits_to_float(*reinterpret_cast<const uint16_t *>(row + at));
+                    d1[r][h] = both ? half_bits_to_float(*reinterpret_cast<const uint16_t *>(row + at + 18)) : 0.0f;
                 }
-            block(b, q, d);
+            block(2 * j, q0, d0);
+            block(2 * j + 1, q1, d1);
         }
     }
 #pragma unroll
@@ -511,6 +539,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
         fence_mbar_init();
         __syncwarp();
     }
+    Windows windows;
     auto load = [&](const Place &from, int chunk, int turn) {
         const int slot = turn & (kStages - 1);
         const int64_t row0 = (static_cast<int64_t>(from.row_group) * p.rw + rw) * kItemRows;
@@ -519,7 +548,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
             if (there && lane == 0)
                 load_boxes<GEGLU>(p, &w0, &w1, ring + slot * L::stage, smem_addr(&bars[warp][slot]), from.expert, row0, chunk);
         } else {
-            if (there) load_windows<GEGLU>(p, ring + slot * L::stage, from.expert, row0, chunk, lane);
+            if (there) load_windows<GEGLU>(p, windows, ring + slot * L::stage, from.expert, row0, chunk, lane);
             copy_commit();
         }
     };
@@ -546,15 +575,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) total[r][n][i] = 0.0f;
-        int skew[kTiles][2] = {};
+        int skew[2][2] = {};
         if constexpr (!ALIGNED) {
+            const int64_t base = at.expert * p.matrix_bytes + row0 * p.row_bytes;
 #pragma unroll
-            for (int r = 0; r < kTiles; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t row = row0 + r % kPairs * 16 + h * 8 + g;
-                    skew[r][h] = static_cast<int>((at.expert * p.matrix_bytes + min(row, p.n - 1) * p.row_bytes) & 15);
-                }
+            for (int i = 0; i < 4; ++i) skew[i >> 1][i & 1] = static_cast<int>(base + (i * 8 + g) * p.row_bytes) & 15;
         }
         for (int panel = 0; panel < panels; ++panel) {
             const int c0 = panel * p.x_panel, c1 = min(p.chunks, c0 + p.x_panel);
