@@ -355,8 +355,8 @@ cudaError_t launch_experts_down(const ExpertsDown &args, cudaStream_t stream, co
 // Streaming against tiles, bf16, GeGLU of 8 out of 64 experts of 1024 x 2048: 1 token
 // 11.5 and 11.4 us, 4 25.9 and 24.6, 7 31.4 and 25.1, 63 60.8 and 38.6; down: 1 token
 // 11.1 and 10.5, 6 16.8 and 18.1, 7 31.8 and 21.2.  Four out of 64 experts of 800 x
-// 1568, 8 tokens: 37.7 and 23.8.  Down, two out of 8 experts of 4096 x 14336, one
-// token: 71.1 and 46.4.
+// 1568, 8 tokens: 29.2 and 23.8.  Down, two out of 8 experts of 4096 x 14336, one
+// token: 75.4 and 46.4.
 inline bool experts_are_many(int64_t pairs, int experts, int64_t k) { return 2 * pairs >= experts || k >= 4096; }
 bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k);
 cudaError_t launch_experts_tile_geglu(const ExpertsGeglu &args, cudaStream_t stream, const LaunchCtx &ctx);
