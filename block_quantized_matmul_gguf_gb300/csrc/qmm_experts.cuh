@@ -50,6 +50,8 @@ constexpr int kChunk = 256;   // K values of a stage
 constexpr int kTiles = 4;     // of 16 weight rows, of an item
 constexpr int kRows = 16 * kTiles;
 
+constexpr int kMostUnits = (1 << 30) - 1;  // where sums stop: above those of any plan, and twice it fits
+
 struct StreamParams {
     ExpertsPlan plan;
     const uint8_t *w[2];  // GeGLU: gate and up; down: w[0]
@@ -485,14 +487,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-            if (lane >= o) s += u;
+            if (lane >= o) s = min(s + u, kMostUnits);
         }
         if (lane == 31) sum[warp] = s;
         __syncthreads();
         int ahead = s - mine, all = 0;
         for (int w = 0; w < warps; ++w) {
-            if (w < warp) ahead += sum[w];
-            all += sum[w];
+            if (w < warp) ahead = min(ahead + sum[w], kMostUnits);
+            all = min(all + sum[w], kMostUnits);
+        }
+        // a plan whose experts claim more than its pairs is not worked: sums stay exact
+        if (all > p.plan.pairs_total / (8 * NB) + p.plan.experts) {
+            if (threadIdx.x == 0) record_error(p.ctx, kDevErrIndex);
+            return;
         }
         const int64_t items = static_cast<int64_t>(all) * p.row_groups;
         const int64_t from = items * blockIdx.x / gridDim.x, to = items * (blockIdx.x + 1) / gridDim.x;

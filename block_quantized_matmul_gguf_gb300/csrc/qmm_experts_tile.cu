@@ -105,6 +105,8 @@ static_assert(Layout<true>::tiles + (kMaxExperts + 1) * 16 + 1024 <= 232448 - 25
                   Layout<false>::tiles + (kMaxExperts + 1) * 16 + 1024 <= 232448 - 256,
               "shared memory of a CTA");
 
+constexpr int MOST_TILES = (1 << 30) - 1;  // where sums stop: above those of any plan, and twice it fits
+
 struct TileParams {
     ExpertsPlan plan;
     const float *unit;   // power of two of each row of x
@@ -351,12 +353,12 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-            if (lane >= o) s += u;
+            if (lane >= o) s = min(s + u, MOST_TILES);
         }
         if (lane == 31) part[warp] = s;
         __syncthreads();
         int before = s - mine;
-        for (int w = 0; w < warp; ++w) before += part[w];
+        for (int w = 0; w < warp; ++w) before = min(before + part[w], MOST_TILES);
         for (int e = e0; e < e1; ++e) {
             const int count = expert_count(p, e, start);
             ex.tiles[e] = before;
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
             ex.count[e] = count;
             const int parts = (count + BT - 1) / BT;
             ex.per[e] = parts ? ((count + parts - 1) / parts + 31) & ~31 : 32;
-            before += parts;
+            before = min(before + parts, MOST_TILES);
             if (e == p.plan.experts - 1) ex.tiles[p.plan.experts] = before;
         }
     }
@@ -373,7 +375,10 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
     cluster_barrier();  // the peer's barriers exist before anyone signals them
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
-    const int items = ex.tiles[p.plan.experts] * p.row_blocks;
+    // a plan whose experts claim more than its pairs is not worked: sums stay exact
+    const bool sound = ex.tiles[p.plan.experts] <= p.plan.pairs_total / BT + p.plan.experts;
+    if (!sound && threadIdx.x == 0) record_error(ctx, kDevErrIndex);
+    const int items = sound ? ex.tiles[p.plan.experts] * p.row_blocks : 0;
     const int chunks = p.chunks;
 
     Items at = items_from(p, pair, num_pairs);

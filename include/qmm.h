@@ -576,7 +576,9 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
  * other pair.
  * Entries outside their arrays (an expert_start that descends or leaves
  * 0 .. tokens * topk, a pair outside 0 .. tokens * topk - 1) record
- * QMM_ERR_INDEX; what they concern is left out.
+ * QMM_ERR_INDEX; what they concern is left out (in down, y of those tokens is
+ * undefined), and of a plan whose experts claim many more entries than there are,
+ * all is.
  *   workspace  16-byte aligned device memory of at least
  *              qmm_experts_geglu_workspace_bytes() or
  *              qmm_experts_down_workspace_bytes() bytes, scratch of the call.

@@ -348,7 +348,7 @@ def test_long_rows(qmm, types, k):
 @pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)], ids=str)
 @pytest.mark.parametrize("k", [2048, 2080])
 @pytest.mark.parametrize("tokens", [3, 1100])
-def test_offsets_past_32_bits(qmm, types, k, tokens):
+def test_rows_far_apart_of_the_last_expert(qmm, types, k, tokens):
     """The last of 1024 experts of 5 GB of weights, rows of x and h 2^21 elements apart."""
     experts, n = 1024, 4352
     rng = np.random.default_rng(k + tokens)
@@ -441,3 +441,25 @@ def test_plans_and_weights_written_just_before(qmm):
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)], ids=str)
+@pytest.mark.parametrize("k", [256, 288])
+def test_a_plan_with_more_than_its_pairs_is_not_worked(qmm, types, k):
+    """Starts 0, P, 0, P ..: every other expert claims all pairs."""
+    tokens, experts, topk, n = 200, 64, 2, 64
+    rng = np.random.default_rng(5)
+    pairs = np.arange(tokens * topk, dtype=np.int32)
+    starts = np.array([0, tokens * topk] * (experts // 2) + [0], dtype=np.int32)
+    x = torch.from_numpy(rng.standard_normal((tokens, k)).astype(np.float32)).to(types[0]).cuda()
+    b = dev(ref.blocks(rng, experts, n, k))
+    h = torch.full((tokens * topk, n), 7.0, dtype=types[1], device="cuda")
+    qmm.qmm_experts_geglu_q4_0(b, b, x, h, dev(starts), dev(pairs), topk, n, k)
+    assert qmm.qmm_get_device_error() == qmm.QMM_ERR_INDEX
+    assert (h == 7.0).all()
+    # the same call of a sound plan, right behind it
+    ids = choice(rng, tokens, experts, topk)
+    starts, pairs = ref.plan_of(ids, experts)
+    qmm.qmm_experts_geglu_q4_0(b, b, x, h, dev(starts), dev(pairs), topk, n, k)
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
+    assert (h != 7.0).any()
