@@ -110,7 +110,7 @@ constexpr int MOST_TILES = (1 << 30) - 1;  // where sums stop: above those of an
 struct TileParams {
     ExpertsPlan plan;
     const float *unit;   // power of two of each row of x
-    uint16_t *out;       // GeGLU: h by the pairs' order; down: z by the pair
+    void *out;           // GeGLU: h in bf16 by the pairs' order; down: z in fp32 by the pair
     int64_t out_stride;
     const uint8_t *w[2];  // not WHOLE: gate and up, or w[0]
     int64_t row_bytes;
@@ -616,30 +616,40 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
             const int f = G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) + q * 16 + (lane & 14)
                             : t.row_block * 2 * BW + static_cast<int>(rank) * BW + q * 32 + (lane & 30);
             for (int c = 32 * part + lane; c < t.width; c += 64) {  // place in out (none: 0) and unit
-                uint16_t *to = nullptr;
+                uint64_t to = 0;
                 float unit = 0.0f;
                 if (c < t.cols) {
                     const int pr = p.plan.pairs[t.first + c];
                     unit = p.unit[t.first + c];
                     if (pr >= 0 && pr < p.plan.pairs_total)
-                        to = p.out + (G ? t.first + c : pr) * p.out_stride;
+                        to = reinterpret_cast<uint64_t>(p.out) + (G ? t.first + c : pr) * p.out_stride * (G ? 2 : 4);
                     else
                         record_error(ctx, kDevErrIndex);
                 }
-                table[c] = make_ulonglong2(reinterpret_cast<uint64_t>(to), __float_as_uint(unit));
+                table[c] = make_ulonglong2(to, __float_as_uint(unit));
             }
             __syncwarp();
             if (!warp_wait_or_abort(bar(Smem::d_full + d), (tiles_done >> 1) & 1u, abort_flag, ctx)) break;
             tc_fence_after();
             auto put = [&](uint64_t to, float lo, float hi) {
                 if (to == 0 || f >= p.n) return;
-                uint16_t *at = reinterpret_cast<uint16_t *>(to) + f;
-                const uint32_t v = pack_bf16x2(lo, hi);
-                if (p.even) {
-                    *reinterpret_cast<uint32_t *>(at) = v;
+                if constexpr (G) {
+                    uint16_t *at = reinterpret_cast<uint16_t *>(to) + f;
+                    const uint32_t v = pack_bf16x2(lo, hi);
+                    if (p.even) {
+                        *reinterpret_cast<uint32_t *>(at) = v;
+                    } else {
+                        at[0] = static_cast<uint16_t>(v);
+                        if (f + 1 < p.n) at[1] = static_cast<uint16_t>(v >> 16);
+                    }
                 } else {
-                    at[0] = static_cast<uint16_t>(v);
-                    if (f + 1 < p.n) at[1] = static_cast<uint16_t>(v >> 16);
+                    float *at = reinterpret_cast<float *>(to) + f;
+                    if (p.even) {
+                        *reinterpret_cast<float2 *>(at) = make_float2(lo, hi);
+                    } else {
+                        at[0] = lo;
+                        if (f + 1 < p.n) at[1] = hi;
+                    }
                 }
             };
 #pragma unroll 1
@@ -786,7 +796,7 @@ size_t rows_bytes(int64_t pairs, int64_t k) { return (static_cast<size_t>(pairs)
 
 template <bool G, bool WHOLE>
 cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t *w2, const uint16_t *x, int64_t x_stride,
-                        uint16_t *out, int64_t out_stride, int64_t n, int64_t k, void *workspace, cudaStream_t stream,
+                        void *out, int64_t out_stride, int64_t n, int64_t k, void *workspace, cudaStream_t stream,
                         const LaunchCtx &ctx) {
     const int64_t padded = padded_k(k);
     uint16_t *xr = static_cast<uint16_t *>(workspace);
@@ -803,7 +813,7 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
     const TileParams p = {plan, unit, out, out_stride, {w, G ? w2 : w}, static_cast<int64_t>(row), static_cast<int>(n),
                           static_cast<int>(padded / CK), static_cast<int>(k / kQK),
                           static_cast<int>((n + tile_rows - 1) / tile_rows), 0x64006400u,
-                          n % 2 == 0 && out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(out) % 4 == 0, ctx};
+                          n % 2 == 0 && out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(out) % (G ? 4 : 8) == 0, ctx};
     static int limits[kMaxDevices];
     const size_t smem = Layout<WHOLE>::total(plan.experts);
     cudaError_t e = ensure_smem(experts_tile_kernel<G, WHOLE>, smem, true, limits);
@@ -829,13 +839,13 @@ size_t experts_rows_bytes(int64_t pairs, int64_t k) { return rows_bytes(pairs, k
 
 cudaError_t launch_experts_tile_geglu(const ExpertsGeglu &a, cudaStream_t stream, const LaunchCtx &ctx) {
     auto *launch = a.k % CK == 0 ? launch_tile<true, true> : launch_tile<true, false>;
-    return launch(a.plan, a.wg, a.wu, static_cast<const uint16_t *>(a.x), a.x_stride, static_cast<uint16_t *>(a.h), a.h_stride,
-                  a.n, a.k, a.workspace, stream, ctx);
+    return launch(a.plan, a.wg, a.wu, static_cast<const uint16_t *>(a.x), a.x_stride, a.h, a.h_stride, a.n, a.k,
+                  a.workspace, stream, ctx);
 }
 
 cudaError_t launch_experts_tile_down(const ExpertsDown &a, void *z, void *rows, cudaStream_t stream, const LaunchCtx &ctx) {
     auto *launch = a.k % CK == 0 ? launch_tile<false, true> : launch_tile<false, false>;
-    return launch(a.plan, a.wd, nullptr, static_cast<const uint16_t *>(a.h), a.h_stride, static_cast<uint16_t *>(z), a.n, a.n, a.k,
+    return launch(a.plan, a.wd, nullptr, static_cast<const uint16_t *>(a.h), a.h_stride, z, a.n, a.n, a.k,
                   rows, stream, ctx);
 }
 

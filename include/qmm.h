@@ -569,9 +569,9 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
  * an fp32 input enters in 11 bits.  With bf16 in and out, rows of x or h on
  * multiples of 16 bytes, and half as many pairs as experts at least or k >= 4096,
  * each weight is rounded once to binary16: 2^-12 of it, where the output's own
- * rounding is 2^-9; scales beyond 8188 overflow there.  The down projections of such
- * calls are rounded to bf16 once before the sum.  A row of x or h that holds an
- * infinity or a NaN gives NaN.  Which form a call takes depends on its host-side
+ * rounding is 2^-9; scales beyond 8188 overflow there.  The down projections stay
+ * in fp32 up to the sum's own rounding.  A row of x or h that holds an infinity or
+ * a NaN gives NaN.  Which form a call takes depends on its host-side
  * arguments alone; equal calls give equal bits, and a pair's row depends on no
  * other pair.
  * Entries outside their arrays (an expert_start that descends or leaves
