@@ -1,15 +1,13 @@
 // qmm_experts_tile.cu -- the experts' Q4_0 products for many rows an expert
 // (prompts, batches of requests), bf16 in and out, on tcgen05 tiles.
 //
-// Mathematics.  Y^T = W_e X_e^T for each expert e and the rows X_e of its pairs.  A
-// first kernel writes those rows in the pairs' order as binary16, scaled by a power
-// of two per row so that the largest value lies in [2^14, 2^15): a bf16 value keeps
-// all its bits down to 2^-29 of the row's largest, and loses what lies below 2^-39 of
-// it.  Each weight w = (n - 8) d is rounded once to binary16 (half a step is 2^-12 of
-// it; beside a bf16 weight's 2^-9 that leaves the output's own rounding the only one
-// that shows: error against 64 bits 1.7e-3 for 2.9e-3) and products are summed in fp32
-// in tensor memory; the epilogue takes the row's power of two out again.  Scales
-// above 8188, whose weights binary16 cannot hold, give infinities here.
+// Mathematics.  Y^T = W_e X_e^T for each expert e and the rows X_e of its pairs, which a
+// first kernel writes in the pairs' order.  A weight w = (n - 8) d has 14 bits and enters
+// as two bf16 parts of 8 bits each that add up to it (weights_of), which are two
+// products into the same accumulator: each product is exact, for any scale, and sums
+// are fp32 in tensor memory.  One binary16 part would take half the products (GeGLU of
+// 2047 tokens 184 us for 122), but rounds each weight by up to 2^-12 of it and holds none
+// of scales above 8188.
 //
 // Structure: persistent clusters of two CTAs; an item is 256 weight rows (128 gate
 // and the same 128 up rows for GeGLU), half for each CTA, by up to 128 of an expert's
@@ -29,25 +27,19 @@
 //               experts of 1024 x 2016, 2047 tokens: one warp 203 us, two 173, four 147;
 //               a bulk copy a row, as TMA wants a request for each, 592)
 //   warps 4-11  epilogue, two for each quarter of the lanes
-//   warps 12-27 dequantisers: TMEM lanes 32 (w % 4) .., one stage (128 of K) of every
-//               other chunk (256 of K).  Weights are formed in registers before their
-//               slot is waited for, so that a free slot is filled at once.
-// The binary16 pairs that a word of codes gives without moving its nibbles are
-// values 0 and 2, 1 and 3, so x is written in that order of K too.
+//   warps 12-27 dequantisers: TMEM lanes 32 (w % 4) .., one stage (64 of K) of every
+//               chunk (256 of K).  The first block's weights are formed in registers
+//               before their slot is waited for, so that a free slot is filled at once.
+// The pairs that a word of codes gives without a permutation are values 0 and 2, 1 and
+// 3, so x is written in that order of K too.
 // Which items (expert, tile, row block) there are depends on expert_start: each CTA
 // forms the prefix sums of the experts' tiles in shared memory, and every role finds
 // its pair's items in them by two ballots.
 // Every wait is bounded, as in the prefill GEMM.
 //
-// Bound, for prompts, by the hand-overs between the roles and by the x slots' round
-// trip, with the tensor cores at work 64 % of the time and two thirds of the issue slots
-// taken (8 out of 64 experts of 1024 x 2048, 2047 tokens: 105 us of 122, 1.31 PFLOP/s;
-// without the weights' arithmetic 6 us less, with an eighth of the products 11, without
-// loads 12).  With few rows an expert by the weights' bytes and the fill of each
-// item's pipeline (128 tokens: 39.6 us in all, 3.9 TB/s).  The rows' kernel writes 67 MB
-// in 15 us for prompts.  Tiles of 192 rows, which dequantise experts of 257 to 384 rows
-// twice instead of three times, fit tensor memory with stages of 64 of K alone, and
-// those cost more hand-overs than they save (131 us for 125).
+// Bound, for prompts, by the tensor cores (8 out of 64 experts of 1024 x 2048, 2047
+// tokens: 184 us with the rows, 1.49 PFLOP/s of products).  With few rows an expert by the
+// weights' arithmetic and the fill of each item's pipeline (128 tokens: 55 us in all).
 #include "qmm_internal.h"
 #include "qmm_tc.cuh"
 
@@ -60,9 +52,11 @@ constexpr int BW = 128;      // weight rows of a CTA
 constexpr int BT = 128;      // rows of x in a tile, at most
 constexpr int BK = 64;       // K of a swizzle row of x
 constexpr int CK = 256;      // K of a chunk: eight blocks
-constexpr int SK = 128;      // K of a stage, the pipeline's unit
+constexpr int SK = 128;      // K of a stage of x
+constexpr int AK = 64;       // K of a stage of weights
 constexpr int SUBS = SK / BK;
 constexpr int A_SLOTS = 4, X_SLOTS = 4;  // stages in flight
+static_assert(AK == BK && CK / AK == A_SLOTS, "a set of dequantisers keeps to one slot");
 constexpr int X_SUB_BYTES = BT * BK * 2, X_SLOT_BYTES = SUBS * X_SUB_BYTES;
 // A chunk of a row of weights is 144 bytes.  Where K is a multiple of 256 every row
 // begins on 16 bytes and TMA copies boxes of them (WHOLE).  Otherwise the 16-byte
@@ -75,7 +69,7 @@ struct Raw {
     static constexpr int row = WHOLE ? RAW_CHUNK : 176;  // 176: 8 rows in different banks, as 144
     static constexpr int slot_bytes = BW * row;
 };
-constexpr uint32_t D_COLS = 2 * BT, A_COLS = SK / 2, TMEM_COLS = 512;  // two accumulators
+constexpr uint32_t D_COLS = 2 * BT, A_COLS = AK, TMEM_COLS = 512;  // two accumulators; two parts of the weights
 static_assert(X_SLOTS % 2 == 0 && CK / SK % 2 == 0, "two x warps");
 static_assert(D_COLS + A_SLOTS * A_COLS <= TMEM_COLS, "tensor memory");
 
@@ -96,8 +90,8 @@ struct Layout {
                          d_empty = d_full + 2, final = d_empty + 2, nbars = final + 1;
     static constexpr int tmem_slot = bars + nbars * 8;
     static constexpr int abort_flag = tmem_slot + 4;
-    static constexpr int cols = (abort_flag + 4 + 15) / 16 * 16;  // [4][BT] place in out and unit of each column
-    static constexpr int skew = cols + 4 * BT * 16;  // [RAW_SLOTS][32]: rows' skews repeat after 32
+    static constexpr int cols = (abort_flag + 4 + 15) / 16 * 16;  // [4][BT] place in out of each column
+    static constexpr int skew = cols + 4 * BT * 8;  // [RAW_SLOTS][32]: rows' skews repeat after 32
     static constexpr int tiles = skew + (WHOLE ? 0 : RAW_SLOTS * 128);  // Experts: four arrays of [experts + 1]
     static int total(int experts) { return tiles + (experts + 1) * 16 + 1024; }
 };
@@ -109,14 +103,13 @@ constexpr int MOST_TILES = (1 << 30) - 1;  // where sums stop: above those of an
 
 struct TileParams {
     ExpertsPlan plan;
-    const float *unit;   // power of two of each row of x
     void *out;           // GeGLU: h in bf16 by the pairs' order; down: z in fp32 by the pair
     int64_t out_stride;
     const uint8_t *w[2];  // not WHOLE: gate and up, or w[0]
     int64_t row_bytes;
     int n, chunks, blocks;  // chunks and blocks of K
     int row_blocks;      // of a matrix: of 256 rows (down) or 128 features
-    uint32_t magic;      // 1024, 1024 in binary16, in a register
+    uint32_t magic;      // 16, 16 in bf16, in a register
     bool even;           // out takes two neighbouring values at once
     LaunchCtx ctx;
 };
@@ -185,30 +178,37 @@ __device__ __forceinline__ Item next_item(const TileParams &p, const Experts &ex
     return it;
 }
 
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
 
-// (n - 8) d of a word's eight codes: values 0 and 2, 1 and 3, 16 and 18, 17 and 19
-// of the block's quarter.
-__device__ __forceinline__ void weights_of(uint32_t q, uint32_t d, uint32_t magic, uint32_t *w) {
-    const uint32_t q8 = q >> 8;
-    w[0] = hmul2(hadd2((q & 0x000F000Fu) | magic, 0xE408E408u), d);                  // - 1032
-    w[1] = hmul2(hadd2((q8 & 0x000F000Fu) | magic, 0xE408E408u), d);
-    w[2] = hmul2(hfma2((q & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u), d);     // / 16 - 72
-    w[3] = hmul2(hfma2((q8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u), d);
+// A block's scale d in two parts of 5 bits each, and -24 times each (7 bits), as bf16
+// pairs.  d has 11 bits; what rounding it to 5 leaves is a whole number of its last
+// place from -32 to 32, which has 5 bits too.
+struct Scale {
+    uint32_t high, low, high24, low24;
+};
+__device__ __forceinline__ uint32_t twice(float v) { return __byte_perm(__float_as_uint(v), 0, 0x3232); }
+__device__ __forceinline__ Scale scale_of(uint32_t half_bits) {
+    const float d = half_bits_to_float(static_cast<uint16_t>(half_bits));
+    const float high = __uint_as_float((__float_as_uint(d) + 0x40000u) & 0xFFF80000u), low = d - high;
+    return Scale{twice(high), twice(low), twice(high * -24.0f), twice(low * -24.0f)};
+}
+
+// (n - 8) d of a word's eight codes in two parts: values 0 and 2, 1 and 3, 16 and 18,
+// 17 and 19 of the block's quarter.  n - 8 has 3 bits (-8 one), so that each part
+// has 8 and is exact in bf16; 16 + n is its code in the place of the upper mantissa
+// bits of 16.
+__device__ __forceinline__ void weights_of(uint32_t q, const Scale &d, uint32_t magic, uint32_t *high, uint32_t *low) {
+    const uint32_t at[4] = {q << 3, q >> 5, q >> 1, q >> 9};  // bytes 0 and 2, 1 and 3: their lower codes, their upper ones
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t m = (at[i] & 0x00780078u) | magic;
+        high[i] = fma_bf16x2(m, d.high, d.high24);
+        low[i] = fma_bf16x2(m, d.low, d.low24);
+    }
 }
 
 // A box of x into the same place of both CTAs, counted on the barrier of each.
@@ -286,8 +286,8 @@ __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&
         : "memory");
 }
 
-// D fp32, A and B binary16, both K-major, M = 128; N goes in at run time.
-constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BW >> 4) << 24);
+// D fp32, A and B bf16, both K-major, M = 128; N goes in at run time.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BW >> 4) << 24);
 
 // G: GeGLU.  A CTA's 128 accumulator rows are then 64 features: in lane quarter q,
 // lanes 0-15 hold the gate rows of features 16q .. 16q+15, lanes 16-31 their up rows.
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
         }
         for (int i = 0; i < RAW_SLOTS; ++i) {
             mbar_init_addr(bar(Smem::raw_full + i), WHOLE ? 1 : COPY_WARPS * 32 + 1);  // each lane's copies, and the skews
-            mbar_init_addr(bar(Smem::raw_empty + i), DEQ_WARPS / 2);
+            mbar_init_addr(bar(Smem::raw_empty + i), DEQ_WARPS);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init_addr(bar(Smem::d_full + i), 1);
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
     // This kernel is launched behind the rows' kernel alone, each of whose threads lets it
     // begin only after its own wait for all that came before: what is older than the
     // rows is complete and in memory by now.  So the plan (read past L1) and the weights
-    // (TMA) are taken at once, and only the warps that read rows and units or write
+    // (TMA) are taken at once, and only the warps that read rows or write
     // results wait for the rows' kernel: 128 tokens 43.4 -> 40.0 us.
     {  // tiles in front of each expert's
         __shared__ int32_t part[kTileThreads<WHOLE> / 32];
@@ -504,10 +504,10 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
         auto desc_of = [&](const Item &t) {
             return kIdesc | static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, t.width, 0) >> 3) << 17;
         };
-        // both of a stage's barriers at once: each look that succeeds takes some 100 cycles
+        // both barriers of a stage of x at once: each look that succeeds takes some 100 cycles
         auto look = [&](uint32_t i) {
             return test_wait(bar(Smem::x_full + i % X_SLOTS), (i / X_SLOTS) & 1u) &&
-                   test_wait(bar(Smem::a_full + i % A_SLOTS), (i / A_SLOTS) & 1u);
+                   test_wait(bar(Smem::a_full + 2 * i % A_SLOTS), (2 * i / A_SLOTS) & 1u);
         };
         uint32_t tiles_done = 0, it = 0;
         bool ok = true, issued = false;
@@ -516,20 +516,32 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
             const uint32_t d = tiles_done & 1u;  // accumulator
             if (!warp_wait_or_abort(bar(Smem::d_empty + d), ((tiles_done >> 1) & 1u) ^ 1u, abort_flag, ctx)) break;
             for (int st = 0; st < stages; ++st, ++it) {
-                const uint32_t xs = it % X_SLOTS, as = it % A_SLOTS;
+                const uint32_t xs = it % X_SLOTS;
                 if (!__all_sync(0xFFFFFFFFu, look(it))) {
                     ok = warp_wait_or_abort(bar(Smem::x_full + xs), (it / X_SLOTS) & 1u, abort_flag, ctx) &&
-                         warp_wait_or_abort(bar(Smem::a_full + as), (it / A_SLOTS) & 1u, abort_flag, ctx);
+                         warp_wait_or_abort(bar(Smem::a_full + 2 * it % A_SLOTS), (2 * it / A_SLOTS) & 1u, abort_flag, ctx);
                     if (!ok) break;
                 }
-                tc_fence_after();
-                const uint32_t a = tmem + D_COLS + as * A_COLS, to = tmem + d * BT;
+                const uint32_t to = tmem + d * BT;
                 const uint64_t b = bdesc0 + xs * (X_SLOT_BYTES >> 4);
 #pragma unroll
-                for (int k = 0; k < SK / 16; ++k)
-                    product(one, to, a + 8 * k, b + (k / 4) * (X_SUB_BYTES >> 4) + 2 * (k & 3), idesc, k != 0 || st != 0);
-                issued = true;
-                commit(one, bars + 8u * (Smem::a_empty + as));
+                for (int h = 0; h < SUBS; ++h) {
+                    const uint32_t w = SUBS * it + h, as = w % A_SLOTS, a = tmem + D_COLS + as * A_COLS;
+                    if (h > 0) {
+                        ok = warp_wait_or_abort(bar(Smem::a_full + as), (w / A_SLOTS) & 1u, abort_flag, ctx);
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < AK / 16; ++k) {  // the low part first
+                        const uint64_t bk = b + h * (X_SUB_BYTES >> 4) + 2 * k;
+                        product(one, to, a + 16 * k + 8, bk, idesc, k != 0 || h != 0 || st != 0);
+                        product(one, to, a + 16 * k, bk, idesc, 1);
+                    }
+                    issued = true;
+                    commit(one, bars + 8u * (Smem::a_empty + as));
+                }
+                if (!ok) break;
                 commit_both(one, bars + 8u * (Smem::x_empty + xs));
             }
             if (ok) commit(one, bars + 8u * (Smem::d_full + d));
@@ -540,72 +552,68 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
             wait_drain(bar(Smem::final), 0, ctx);
         }
     } else if (warp >= WARP_DEQ && warp < WARP_COPY) {
-        // every other chunk, and of it one stage, as two halves of 64 values of K
-        const int q = warp & 3, set = (warp - WARP_DEQ) >> 2, part = set & 1;
+        // one stage of every chunk: two blocks of K
+        const int q = warp & 3, part = (warp - WARP_DEQ) >> 2;
         const int row = G ? (lane >> 4) * (BW / 2) + q * 16 + (lane & 15) : q * 32 + lane;
-        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS;
+        const uint32_t to = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS + part * A_COLS;
         const uint32_t total = pair < items ? static_cast<uint32_t>((items - pair + num_pairs - 1) / num_pairs) * chunks : 0u;
-        const uint32_t place = static_cast<uint32_t>(row) * RAW_ROW + 72u * part;
-        int c = (set >> 1) % chunks;  // chunk of its item
-        for (uint32_t it = set >> 1; it < total; it += 2) {
-            const uint32_t r = it % RAW_SLOTS, st = it * (CK / SK) + part, s = st % A_SLOTS;
+        const uint32_t place = static_cast<uint32_t>(row) * RAW_ROW + 36u * part;
+        int c = 0;  // chunk of its item
+        for (uint32_t it = 0; it < total; ++it) {
+            const uint32_t r = it % RAW_SLOTS;
             if (!warp_wait_or_abort(bar(Smem::raw_full + r), (it / RAW_SLOTS) & 1u, abort_flag, ctx)) break;
             // two blocks are nine words; the first's codes begin in the middle of one
             const uint8_t *from = sgen + Smem::raw + r * RAW_SLOT_BYTES + place;
-            uint32_t wd[2][9];
+            uint32_t wd[9];
             if constexpr (WHOLE) {
                 const uint32_t *src = reinterpret_cast<const uint32_t *>(from);
 #pragma unroll
-                for (int i = 0; i < 18; ++i) wd[i / 9][i % 9] = src[i];
+                for (int i = 0; i < 9; ++i) wd[i] = src[i];
             } else {
                 const int skew = reinterpret_cast<const int *>(sgen + Smem::skew)[r * 32 + (row & 31)];  // even
                 const uint32_t *src = reinterpret_cast<const uint32_t *>(from + (skew & ~3));
                 const uint32_t which = skew & 2 ? 0x5432u : 0x3210u;
                 uint32_t last = src[0];
 #pragma unroll
-                for (int i = 0; i < 18; ++i) {
+                for (int i = 0; i < 9; ++i) {
                     const uint32_t next = src[i + 1];
-                    wd[i / 9][i % 9] = __byte_perm(last, next, which);
+                    wd[i] = __byte_perm(last, next, which);
                     last = next;
                 }
-                const int behind = p.blocks - 8 * c - 4 * part;  // blocks of K from here on
+                const int behind = p.blocks - 8 * c - 2 * part;  // blocks of K from here on
                 // no weights behind K: codes are finite, so a scale of 0 takes them out
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (behind <= 2 * h) wd[h][0] &= 0xFFFF0000u;
-                    if (behind <= 2 * h + 1) wd[h][4] &= 0x0000FFFFu;
-                }
-                for (c += 2; c >= chunks;) c -= chunks;
+                if (behind <= 0) wd[0] &= 0xFFFF0000u;
+                if (behind <= 1) wd[4] &= 0x0000FFFFu;
+                if (++c == chunks) c = 0;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive_addr(bar(Smem::raw_empty + r));
-            bool ok = true;
+            // columns of a block: 16 of K's high and low parts, the other 16's
+            uint32_t v[32];
+            const Scale d0 = scale_of(wd[0] & 0xFFFFu), d1 = scale_of(wd[4] >> 16);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t v[32];
-                const uint32_t d0 = __byte_perm(wd[h][0], 0, 0x1010), d1 = __byte_perm(wd[h][4], 0, 0x3232);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    weights_of(__byte_perm(wd[h][i], wd[h][i + 1], 0x5432), d0, p.magic, v + 4 * i);
-                    weights_of(wd[h][5 + i], d1, p.magic, v + 16 + 4 * i);
-                }
-                if (h == 0) {
-                    ok = warp_wait_or_abort(bar(Smem::a_empty + s), ((st / A_SLOTS) & 1u) ^ 1u, abort_flag, ctx);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                tmem_st_32cols(lane_base + s * A_COLS + h * (A_COLS / 2), v);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t *at = v + (i >> 1) * 16 + (i & 1) * 4;
+                weights_of(__byte_perm(wd[i], wd[i + 1], 0x5432), d0, p.magic, at, at + 8);
             }
-            if (!ok) break;
+            if (!warp_wait_or_abort(bar(Smem::a_empty + part), (it & 1u) ^ 1u, abort_flag, ctx)) break;
+            tc_fence_after();
+            tmem_st_32cols(to, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t *at = v + (i >> 1) * 16 + (i & 1) * 4;
+                weights_of(wd[5 + i], d1, p.magic, at, at + 8);
+            }
+            tmem_st_32cols(to + A_COLS / 2, v);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_addr(bar(Smem::a_full + s));
+            if (lane == 0) mbar_arrive_addr(bar(Smem::a_full + part));
         }
     } else if (warp >= WARP_EPI && warp < WARP_DEQ) {
         const int q = warp & 3, part = (warp - WARP_EPI) >> 2;  // the two warps of a quarter take every other 32 columns
         const bool odd = lane & 1, upper = lane >= 16;
-        ulonglong2 *table = reinterpret_cast<ulonglong2 *>(sgen + Smem::cols) + q * BT;
+        uint64_t *table = reinterpret_cast<uint64_t *>(sgen + Smem::cols) + q * BT;
         uint32_t tiles_done = 0;
         pdl_wait();
         while (at.item < items) {
@@ -615,18 +623,16 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
             // neighbouring features f, f + 1 of one
             const int f = G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) + q * 16 + (lane & 14)
                             : t.row_block * 2 * BW + static_cast<int>(rank) * BW + q * 32 + (lane & 30);
-            for (int c = 32 * part + lane; c < t.width; c += 64) {  // place in out (none: 0) and unit
+            for (int c = 32 * part + lane; c < t.width; c += 64) {  // place in out (none: 0)
                 uint64_t to = 0;
-                float unit = 0.0f;
                 if (c < t.cols) {
                     const int pr = p.plan.pairs[t.first + c];
-                    unit = p.unit[t.first + c];
                     if (pr >= 0 && pr < p.plan.pairs_total)
                         to = reinterpret_cast<uint64_t>(p.out) + (G ? t.first + c : pr) * p.out_stride * (G ? 2 : 4);
                     else
                         record_error(ctx, kDevErrIndex);
                 }
-                table[c] = make_ulonglong2(to, __float_as_uint(unit));
+                table[c] = to;
             }
             __syncwarp();
             if (!warp_wait_or_abort(bar(Smem::d_full + d), (tiles_done >> 1) & 1u, abort_flag, ctx)) break;
@@ -661,28 +667,23 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
                     const int c0 = c + (lane & 16);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
-                        ulonglong2 to[2];
                         float h[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            to[i] = table[c0 + j + i];
                             const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j + i] : v[16 + j + i]), 16);
-                            const float s = __uint_as_float(static_cast<uint32_t>(to[i].y));
-                            const float g = (upper ? other : __uint_as_float(v[j + i])) * s;
-                            const float u = (upper ? __uint_as_float(v[16 + j + i]) : other) * s;
+                            const float g = upper ? other : __uint_as_float(v[j + i]);
+                            const float u = upper ? __uint_as_float(v[16 + j + i]) : other;
                             h[i] = gelu_tanh_fast(g) * u;
                         }
                         const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? h[0] : h[1], 1);
-                        put(odd ? to[1].x : to[0].x, odd ? got : h[0], odd ? h[1] : got);
+                        put(table[c0 + j + odd], odd ? got : h[0], odd ? h[1] : got);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         const float mine = __uint_as_float(odd ? v[j + 1] : v[j]);
                         const float got = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(odd ? v[j] : v[j + 1]), 1);
-                        const ulonglong2 to = table[c + j + odd];
-                        const float s = __uint_as_float(static_cast<uint32_t>(to.y));
-                        put(to.x, (odd ? got : mine) * s, (odd ? mine : got) * s);
+                        put(table[c + j + odd], odd ? got : mine, odd ? mine : got);
                     }
                 }
             }
@@ -701,41 +702,20 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
     if (warp == WARP_MMA) tmem_dealloc_cta(tmem_base, TMEM_COLS);
 }
 
-// Rows of x in the pairs' order, as binary16 with their units: a warp a row.
+// Rows of x in the pairs' order, and of K in the weights': a warp a row.
 // GeGLU: row i is x[pairs[i] / topk]; down: row i of h.  Bound by the bytes out.
 struct RowsParams {
     ExpertsPlan plan;
     const uint16_t *x;
     int64_t x_stride;
     uint4 *rows;  // [pairs][padded / 8], zeros behind k
-    float *unit;
     int k, padded;
     bool gather;
     LaunchCtx ctx;
 };
 
-__device__ __forceinline__ float bf16_low(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_high(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t largest(const uint4 &v, uint32_t top) {
-    for (const uint32_t w : {v.x, v.y, v.z, v.w}) top = max(max(top, w & 0x7FFFu), (w >> 16) & 0x7FFFu);
-    return top;
-}
-__device__ __forceinline__ uint2 shuffle2(const uint2 &v, int src) {
-    return make_uint2(__shfl_sync(0xFFFFFFFFu, v.x, src), __shfl_sync(0xFFFFFFFFu, v.y, src));
-}
-__device__ __forceinline__ uint4 scaled_eight(const uint2 &a, const uint2 &b, float f) {
-    return make_uint4(pack_f16x2(bf16_low(a.x) * f, bf16_low(a.y) * f), pack_f16x2(bf16_high(a.x) * f, bf16_high(a.y) * f),
-                      pack_f16x2(bf16_low(b.x) * f, bf16_low(b.y) * f), pack_f16x2(bf16_high(b.x) * f, bf16_high(b.y) * f));
-}
-
 constexpr int kRowsWarps = 8;
-constexpr int kRowsHeld = 8;  // 256 values each
+constexpr int kRowsHeld = 8;  // 256 values each, loaded before the first is written
 
 __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const __grid_constant__ RowsParams p) {
     pdl_wait();
@@ -750,49 +730,32 @@ __global__ void __launch_bounds__(kRowsWarps * 32) experts_rows_kernel(const __g
             if (pr < 0 || pr >= p.plan.pairs_total) continue;  // the products drop its column
             from = pr / p.plan.topk;
         }
-        const uint16_t *x = p.x + from * p.x_stride;
-        // the row stays in registers where it has 2048 values or fewer
+        // eight c, of block c / 4: the values from 4 (c % 4) on and from 16 + 4 (c % 4) on
         const int all = p.k / 8, padded = p.padded / 8;  // padded: a multiple of 32
-        uint4 held[kRowsHeld];
-        // the largest: bf16 magnitudes order as integers (what is no number makes the
-        // row's results none either)
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < kRowsHeld; ++j) {
-            held[j] = make_uint4(0, 0, 0, 0);
-            if (j * 32 + lane < all) held[j] = reinterpret_cast<const uint4 *>(x)[j * 32 + lane];
-        }
-#pragma unroll
-        for (int j = 0; j < kRowsHeld; ++j) top = largest(held[j], top);
-        for (int c = kRowsHeld * 32 + lane; c < all; c += 32) top = largest(reinterpret_cast<const uint4 *>(x)[c], top);
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        const int e = min(max(static_cast<int>(top >> 7), 15), 254);  // as in the streaming form
-        const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-        if (lane == 0) p.unit[i] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+        const uint16_t *x = p.x + from * p.x_stride + (lane >> 2) * 32 + (lane & 3) * 4;
         uint4 *out = p.rows + i * padded;
-        // eight c: of block c / 4, the values from 4 (c % 4) on and from 16 + 4 (c % 4) on
+        for (int c0 = 0; c0 < padded; c0 += kRowsHeld * 32) {
+            uint2 a[kRowsHeld], b[kRowsHeld];
 #pragma unroll
-        for (int j = 0; j < kRowsHeld; ++j) {
-            if (j * 32 >= padded) break;
-            const uint4 v = held[j];  // lane q of four: the block's values from 8 q on
-            const int q = lane & 3, src = (lane & ~3) | (q >> 1);
-            const uint2 a0 = shuffle2(make_uint2(v.x, v.y), src), a1 = shuffle2(make_uint2(v.z, v.w), src);
-            const uint2 b0 = shuffle2(make_uint2(v.x, v.y), src + 2), b1 = shuffle2(make_uint2(v.z, v.w), src + 2);
-            out[j * 32 + lane] = scaled_eight(q & 1 ? a1 : a0, q & 1 ? b1 : b0, f);
-        }
-        for (int c = kRowsHeld * 32 + lane; c < padded; c += 32) {
-            if (c >= all) {
-                out[c] = make_uint4(0, 0, 0, 0);
-                continue;
+            for (int j = 0; j < kRowsHeld; ++j) {
+                a[j] = b[j] = make_uint2(0, 0);
+                if (c0 + j * 32 + lane < all) {
+                    a[j] = *reinterpret_cast<const uint2 *>(x + (c0 + j * 32) * 8);
+                    b[j] = *reinterpret_cast<const uint2 *>(x + (c0 + j * 32) * 8 + 16);
+                }
             }
-            const uint16_t *from8 = x + (c >> 2) * 32 + (c & 3) * 4;
-            out[c] = scaled_eight(*reinterpret_cast<const uint2 *>(from8), *reinterpret_cast<const uint2 *>(from8 + 16), f);
+#pragma unroll
+            for (int j = 0; j < kRowsHeld; ++j) {
+                if (c0 + j * 32 >= padded) break;
+                out[c0 + j * 32 + lane] = make_uint4(__byte_perm(a[j].x, a[j].y, 0x5410), __byte_perm(a[j].x, a[j].y, 0x7632),
+                                                     __byte_perm(b[j].x, b[j].y, 0x5410), __byte_perm(b[j].x, b[j].y, 0x7632));
+            }
         }
     }
 }
 
 int64_t padded_k(int64_t k) { return (k + CK - 1) / CK * CK; }
-size_t rows_bytes(int64_t pairs, int64_t k) { return (static_cast<size_t>(pairs) * (2 * padded_k(k) + 4) + 15) & ~size_t(15); }
+size_t rows_bytes(int64_t pairs, int64_t k) { return static_cast<size_t>(pairs) * 2 * padded_k(k); }
 
 template <bool G, bool WHOLE>
 cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t *w2, const uint16_t *x, int64_t x_stride,
@@ -800,25 +763,24 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
                         const LaunchCtx &ctx) {
     const int64_t padded = padded_k(k);
     uint16_t *xr = static_cast<uint16_t *>(workspace);
-    float *unit = reinterpret_cast<float *>(xr + plan.pairs_total * padded);
     CUtensorMap tx, tx64, tw = {}, tw2 = {};
     const uint64_t row = static_cast<uint64_t>(k / kQK) * kQ4_0Bytes, rows = static_cast<uint64_t>(plan.experts) * n;
-    if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, padded, plan.pairs_total, padded * 2, BK, X_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&tx64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xr, padded, plan.pairs_total, padded * 2, BK, X_WIDE, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, xr, padded, plan.pairs_total, padded * 2, BK, X_BOX, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&tx64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, xr, padded, plan.pairs_total, padded * 2, BK, X_WIDE, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     if (WHOLE && (!encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, row, rows, row, RAW_CHUNK, G ? BW / 2 : BW) ||
                   !encode_tmap_2d(&tw2, CU_TENSOR_MAP_DATA_TYPE_UINT8, G ? w2 : w, row, rows, row, RAW_CHUNK, G ? BW / 2 : BW)))
         return cudaErrorInvalidValue;
     const int tile_rows = G ? BW : 2 * BW;
-    const TileParams p = {plan, unit, out, out_stride, {w, G ? w2 : w}, static_cast<int64_t>(row), static_cast<int>(n),
+    const TileParams p = {plan, out, out_stride, {w, G ? w2 : w}, static_cast<int64_t>(row), static_cast<int>(n),
                           static_cast<int>(padded / CK), static_cast<int>(k / kQK),
-                          static_cast<int>((n + tile_rows - 1) / tile_rows), 0x64006400u,
+                          static_cast<int>((n + tile_rows - 1) / tile_rows), 0x41804180u,
                           n % 2 == 0 && out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(out) % (G ? 4 : 8) == 0, ctx};
     static int limits[kMaxDevices];
     const size_t smem = Layout<WHOLE>::total(plan.experts);
     cudaError_t e = ensure_smem(experts_tile_kernel<G, WHOLE>, smem, true, limits);
     if (e != cudaSuccess) return e;
-    const RowsParams r = {plan, x, x_stride, reinterpret_cast<uint4 *>(xr), unit, static_cast<int>(k), static_cast<int>(padded), G, ctx};
+    const RowsParams r = {plan, x, x_stride, reinterpret_cast<uint4 *>(xr), static_cast<int>(k), static_cast<int>(padded), G, ctx};
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((plan.pairs_total + kRowsWarps - 1) / kRowsWarps, int64_t(1) << 30));
     e = launch_kernel(experts_rows_kernel, dim3(grid), dim3(kRowsWarps * 32), 0, stream, 1, r);
     if (e != cudaSuccess) return e;

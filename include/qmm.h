@@ -568,9 +568,8 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
  * 2^-39 of the largest of its row's 256 values around it).  With a bf16 output
  * an fp32 input enters in 11 bits.  With bf16 in and out, rows of x or h on
  * multiples of 16 bytes, and half as many pairs as experts at least or k >= 4096,
- * each weight is rounded once to binary16: 2^-12 of it, where the output's own
- * rounding is 2^-9; scales beyond 8188 overflow there.  The down projections stay
- * in fp32 up to the sum's own rounding.  A row of x or h that holds an infinity or
+ * weights and inputs are exact too.  The down projections stay in fp32 up to the
+ * sum's own rounding. A row of x or h that holds an infinity or
  * a NaN gives NaN.  Which form a call takes depends on its host-side
  * arguments alone; equal calls give equal bits, and a pair's row depends on no
  * other pair.
@@ -582,8 +581,7 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
  *   workspace  16-byte aligned device memory of at least
  *              qmm_experts_geglu_workspace_bytes() or
  *              qmm_experts_down_workspace_bytes() bytes, scratch of the call.
- *              For geglu NULL is taken too: weights are then not rounded, and many
- *              rows take longer.
+ *              For geglu NULL is taken too: many rows then take longer.
  * Requires tokens >= 0 (0 launches nothing), 1 <= topk <= 32, experts <= 1024,
  * n >= 1, k % 32 == 0, weights 16-byte aligned, other pointers aligned to their
  * type, strides at least the rows' widths; n <= 2^24, k <= 2^20 and at most

@@ -51,3 +51,66 @@ def test_projections_are_not_rounded_before_the_sum(qmm, types, tokens, experts)
     want = np.einsum("tk,tnk->tn", x.double().numpy(), w[first] - w[first + 1])
     assert np.linalg.norm(y.double().cpu().numpy() - want) <= 2.0 ** -8 * np.linalg.norm(want)
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+TILES = [(3, 4), (90, 4)]  # tokens and experts that take the tile form
+
+
+@pytest.mark.parametrize("k", [64, 256, 288, 1024])
+@pytest.mark.parametrize("tokens,experts", TILES)
+def test_weights_enter_whole(qmm, tokens, experts, k):
+    """Each row of x holds v and -v where two blocks have one code c and scales that are
+    neighbours in binary16.  v c (d - d') has every addend and sum within 24 bits, so
+    that nothing but the result's rounding is left: half a step, 2^-8 |y|; the GELU
+    adds 2^-11."""
+    rng = np.random.default_rng(tokens + k)
+    n = 48
+    b = ref.blocks(rng, experts, n, k)
+    row = b.reshape(experts, n, k // 32, 18)
+    row[:, :, 1] = row[:, :, 0]
+    d = row[:, :, 0, :2].copy().view(np.uint16) + np.uint16(1)  # the next scale
+    row[:, :, 1, :2] = d.view(np.uint8)
+    ids = rng.integers(0, experts, (tokens, 1))
+    starts, pairs = ref.plan_of(ids, experts)
+    at = rng.integers(0, 32, tokens)
+    x = np.zeros((tokens, k), dtype=np.float32)
+    v = torch.from_numpy(rng.uniform(50000, 100000, tokens).astype(np.float32)).bfloat16().float().numpy()
+    x[np.arange(tokens), at], x[np.arange(tokens), 32 + at] = v, -v
+    w, _ = ref.matrix(b)
+    want = np.einsum("tk,tnk->tn", x.astype(np.float64), w[ids[:, 0]])[pairs]
+    h = torch.empty(tokens, n, dtype=BF16, device="cuda")
+    qmm.qmm_experts_geglu_q4_0(dev(b), dev(b), dev(x, BF16), h, dev(starts), dev(pairs), 1, n, k)
+    z = ref.gelu(want) * want
+    assert (np.abs(h.double().cpu().numpy() - z) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(z) + 2.0 ** -11 * np.abs(want)).all()
+    y = torch.empty(tokens, n, dtype=BF16, device="cuda")
+    ones = torch.ones(tokens, 1, device="cuda")
+    qmm.qmm_experts_down_q4_0(dev(b), dev(x[pairs], BF16), y, dev(ids.astype(np.int32)), ones, dev(starts), dev(pairs), n, k)
+    assert (np.abs(y.double().cpu().numpy()[pairs] - want) <= 2.0 ** -8 * np.abs(want)).all()
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("k", [256, 288])
+@pytest.mark.parametrize("tokens,experts", TILES)
+def test_scales_and_rows_of_any_range(qmm, tokens, experts, k):
+    """Scales to the largest of binary16, whose weights that type cannot hold; and rows whose largest
+    value, 1e30, meets weights of 0.  Bounds: those of exact products, and the result's rounding."""
+    rng = np.random.default_rng(tokens + k)
+    n, topk = 40, 2
+    ids = np.argsort(rng.random((tokens, experts)), axis=1)[:, :topk]
+    starts, pairs = ref.plan_of(ids, experts)
+    weights = rng.random((tokens, topk)).astype(np.float32)
+    h = torch.from_numpy(rng.standard_normal((tokens * topk, k)).astype(np.float32)).bfloat16()
+    for lo, hi in ((8000, 65504), (0.001, 0.02), (6e-8, 1e-5)):
+        b = ref.blocks(rng, experts, n, k, lo=lo, hi=hi)
+        row = b.reshape(experts, n, k // 32, 18)
+        row[:, :, 1, 2 + 5] = row[:, :, 1, 2 + 5] & 0xF0 | 8  # value 37 of each row of weights is 0
+        clean = h.clone()
+        clean[:, 37] = 0
+        want, limit = ref.experts_down(clean.double().numpy(), b, ids, weights, starts, pairs, True, False)
+        odd = clean.clone()
+        odd[:, 37] = 1e30
+        for rows in (clean, odd):
+            y = torch.empty(tokens, n, dtype=BF16, device="cuda")
+            qmm.qmm_experts_down_q4_0(dev(b), rows.cuda(), y, dev(ids.astype(np.int32)), dev(weights), dev(starts), dev(pairs), n, k)
+            assert (np.abs(y.double().cpu().numpy() - want) <= limit + 2.0 ** -8 * (np.abs(want) + limit)).all()
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
