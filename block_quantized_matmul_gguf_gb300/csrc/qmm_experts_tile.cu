@@ -9,17 +9,12 @@
 // 2047 tokens 184 us for 122), but rounds each weight by up to 2^-12 of it and holds none
 // of scales above 8188.
 //
-// Structure: persistent clusters of two CTAs; an item is 256 weight rows (128 gate
-// and the same 128 up rows for GeGLU), half for each CTA, by up to 128 of an expert's
-// rows.  A CTA's products are tcgen05.mma.cta_group::1 with M = 128: its weights in
-// tensor memory, x in shared memory, where each CTA loads one half of the item's rows
-// for both (multicast).  An expert's rows are cut into equal tiles of a multiple of
-// 32, so that the instruction's N follows the rows that are there.  Two accumulators:
-// one is read out while the next item's products run.
-//   warps 0, 3  x, every other stage each, whose copies take most of their time to
-//               issue (one warp for all: 128 tokens 46.6 us, two 43.4).  A box of 64 rows
-//               x 64 values a lane, or two of 16 rows for small tiles (a copy's cost is
-//               its box's, not its rows': boxes of 16 alone cost 23 us more at 2047 tokens)
+// Structure: one persistent CTA an SM; an item is 128 weight rows (64 gate and the same
+// 64 up rows for GeGLU) by up to 128 of an expert's rows: tcgen05.mma.cta_group::1 with
+// M = 128, the weights in tensor memory, x in shared memory.  An expert's rows are cut
+// into equal tiles of a multiple of 32, so that the instruction's N follows the rows that
+// are there.  Two accumulators: one is read out while the next item's products run.
+//   warps 0, 3  x, every other stage each: boxes of 64 and 32 rows x 64 values, a lane each
 //   warp 1      MMA, issued by the whole warp's elected lane
 //   warp 2      weights as they are: boxes of 64 or 128 rows x 144 bytes
 //   warps 28-31 the same where K is no multiple of 256 and rows lie on no 16 bytes:
@@ -34,12 +29,12 @@
 // 3, so x is written in that order of K too.
 // Which items (expert, tile, row block) there are depends on expert_start: each CTA
 // forms the prefix sums of the experts' tiles in shared memory, and every role finds
-// its pair's items in them by two ballots.
+// its CTA's items in them by two ballots.
 // Every wait is bounded, as in the prefill GEMM.
 //
 // Bound, for prompts, by the tensor cores (8 out of 64 experts of 1024 x 2048, 2047
 // tokens: 184 us with the rows, 1.49 PFLOP/s of products).  With few rows an expert by the
-// weights' arithmetic and the fill of each item's pipeline (128 tokens: 55 us in all).
+// weights' arithmetic and the fill of each item's pipeline (128 tokens: 54 us in all).
 #include "qmm_internal.h"
 #include "qmm_tc.cuh"
 
@@ -77,7 +72,7 @@ constexpr int WARP_X = 0, WARP_MMA = 1, WARP_RAW = 2, WARP_X1 = 3, WARP_EPI = 4,
 constexpr int WARP_COPY = WARP_DEQ + DEQ_WARPS, COPY_WARPS = BW / 32;  // not WHOLE: warps that copy weights
 template <bool WHOLE>
 constexpr int kTileThreads = (WARP_COPY + (WHOLE ? 0 : COPY_WARPS)) * 32;
-constexpr int X_BOX = 16, X_WIDE = BT / 2;  // rows of a copy of x: where few are wanted, and otherwise
+constexpr int X_WIDE = 64, X_BOX = 32;  // rows of a copy of x: as many wide ones as fit, and one more for the rest
 
 template <bool WHOLE>
 struct Layout {
@@ -108,7 +103,7 @@ struct TileParams {
     const uint8_t *w[2];  // not WHOLE: gate and up, or w[0]
     int64_t row_bytes;
     int n, chunks, blocks;  // chunks and blocks of K
-    int row_blocks;      // of a matrix: of 256 rows (down) or 128 features
+    int row_blocks;      // of a matrix: of 128 rows (down) or 64 features
     uint32_t magic;      // 16, 16 in bf16, in a register
     bool even;           // out takes two neighbouring values at once
     LaunchCtx ctx;
@@ -120,8 +115,8 @@ struct Experts {
     int *tiles, *start, *count, *per;
 };
 
-// An item: rows first .. first + cols - 1 of the sorted pairs of `expert`.  A pair of
-// CTAs takes every num_pairs-th item (tile, row block); whole warps step through them.
+// An item: rows first .. first + cols - 1 of the sorted pairs of `expert`.  A CTA takes
+// every gridDim.x-th item (tile, row block); whole warps step through them.
 struct Item {
     int tile, row_block;
     int expert, first, cols, width;  // width: cols up to a multiple of 32
@@ -140,23 +135,24 @@ __device__ __forceinline__ int expert_count(const TileParams &p, int e, int &sta
 
 struct Items {
     int item, tile, row_block;      // the next one
-    int tile_step, row_block_step;  // num_pairs as tiles and row blocks
+    int tile_step, row_block_step;  // gridDim.x as tiles and row blocks
 };
-__device__ __forceinline__ Items items_from(const TileParams &p, int pair, int num_pairs) {
+__device__ __forceinline__ Items items_from(const TileParams &p) {
+    const int first = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
     Items at;
-    at.item = pair;
-    at.tile = pair / p.row_blocks;
-    at.row_block = pair - at.tile * p.row_blocks;
-    at.tile_step = num_pairs / p.row_blocks;
-    at.row_block_step = num_pairs - at.tile_step * p.row_blocks;
+    at.item = first;
+    at.tile = first / p.row_blocks;
+    at.row_block = first - at.tile * p.row_blocks;
+    at.tile_step = step / p.row_blocks;
+    at.row_block_step = step - at.tile_step * p.row_blocks;
     return at;
 }
 // The next item, by a whole warp: two ballots find the expert.
-__device__ __forceinline__ Item next_item(const TileParams &p, const Experts &ex, int num_pairs, int lane, Items &at) {
+__device__ __forceinline__ Item next_item(const TileParams &p, const Experts &ex, int lane, Items &at) {
     Item it;
     it.tile = at.tile;
     it.row_block = at.row_block;
-    at.item += num_pairs;
+    at.item += static_cast<int>(gridDim.x);
     at.tile += at.tile_step;
     at.row_block += at.row_block_step;
     if (at.row_block >= p.row_blocks) {
@@ -211,15 +207,6 @@ __device__ __forceinline__ void weights_of(uint32_t q, const Scale &d, uint32_t 
     }
 }
 
-// A box of x into the same place of both CTAs, counted on the barrier of each.
-__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
-        "[%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<unsigned short>(3))
-        : "memory");
-}
-
 // Whether the phase of this parity is over, without waiting.
 __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -251,15 +238,6 @@ __device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
         : "memory");
 }
-// The same on the barrier at this offset in both CTAs.
-__device__ __forceinline__ void commit_both(uint32_t one, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(bar),
-        "r"(one), "h"(static_cast<unsigned short>(3))
-        : "memory");
-}
-
 // 16 bytes, of which the first `bytes` are read and the others zeros
 __device__ __forceinline__ void copy16_some(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -304,8 +282,6 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
     uint8_t *sgen = smem_raw + (sbase - raw_base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const LaunchCtx ctx = p.ctx;
-    const uint32_t rank = cluster_rank();
-    const int pair = static_cast<int>(blockIdx.x >> 1), num_pairs = static_cast<int>(gridDim.x >> 1);
 
     auto bar = [&](uint32_t i) -> uint32_t { return sbase + Smem::bars + 8u * i; };
     int *abort_flag = reinterpret_cast<int *>(sgen + Smem::abort_flag);
@@ -319,7 +295,7 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < X_SLOTS; ++i) {
             mbar_init_addr(bar(Smem::x_full + i), 1);
-            mbar_init_addr(bar(Smem::x_empty + i), 2);  // both CTAs have read the slot
+            mbar_init_addr(bar(Smem::x_empty + i), 1);
         }
         for (int i = 0; i < A_SLOTS; ++i) {
             mbar_init_addr(bar(Smem::a_full + i), 4);  // a warp of each quarter
@@ -372,7 +348,6 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_barrier();  // the peer's barriers exist before anyone signals them
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     // a plan whose experts claim more than its pairs is not worked: sums stay exact
@@ -381,23 +356,19 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
     const int items = sound ? ex.tiles[p.plan.experts] * p.row_blocks : 0;
     const int chunks = p.chunks;
 
-    Items at = items_from(p, pair, num_pairs);
+    Items at = items_from(p);
     if (warp == WARP_X || warp == WARP_X1) {
         pdl_wait();
         const uint32_t which = warp != WARP_X;  // every other stage; an item has an even number of them
         uint32_t it = which;
         bool ok = true;
         while (ok && at.item < items) {
-            const Item t = next_item(p, ex, num_pairs, lane, at);
-            // half of the rows for both CTAs; those behind cols are others', and
-            // dropped.  One copy of 64 rows a swizzle row where more than 32 are
-            // wanted (the other half's rows that it brings are the same ones)
-            const int half = t.width >> 1, first = static_cast<int>(rank) * half;
-            const bool many = half > 2 * X_BOX;
-            const int sub = many ? lane : lane >> 1, row = first + (many ? 0 : (lane & 1) * X_BOX);
-            const bool mine = sub < SUBS && (many || row < first + half);
-            const CUtensorMap *map = many ? &tmap_x64 : &tmap_x;
-            const uint32_t bytes = static_cast<uint32_t>(many ? 2 * X_WIDE : t.width) * SK * 2;
+            const Item t = next_item(p, ex, lane, at);
+            // rows behind cols are others', and dropped
+            const int sub = lane & (SUBS - 1), row = (lane / SUBS) * X_WIDE;
+            const bool wide = row + X_WIDE <= t.width, mine = row < t.width;
+            const CUtensorMap *map = wide ? &tmap_x64 : &tmap_x;
+            const uint32_t bytes = static_cast<uint32_t>(t.width) * SK * 2;
             for (int st = static_cast<int>(which); st < chunks * (CK / SK); st += 2, it += 2) {
                 const uint32_t s = it % X_SLOTS, full = bar(Smem::x_full + s);
                 if (!warp_wait_or_abort(bar(Smem::x_empty + s), ((it / X_SLOTS) & 1u) ^ 1u, abort_flag, ctx)) {
@@ -407,18 +378,16 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
                 if (lane == 0) mbar_expect_tx_addr(full, bytes);
                 __syncwarp();
                 if (mine)
-                    tma_load_2d_both(sbase + Smem::x + s * X_SLOT_BYTES + sub * X_SUB_BYTES + row * BK * 2, map, st * SK + sub * BK,
-                                     t.first + row, full);
+                    tma_load_2d(sbase + Smem::x + s * X_SLOT_BYTES + sub * X_SUB_BYTES + row * BK * 2, map, st * SK + sub * BK,
+                                t.first + row, full);
             }
         }
         if (lane == 0) {
-            // all copies into this CTA have come, and both CTAs have read what this
-            // one sent: nothing of the peer's is on its way here any more
+            // all copies have come
             for (uint32_t s = which; s < X_SLOTS; s += 2)
                 if (it > s) {
                     const uint32_t last = it - 2 - ((it - 2 - s) % X_SLOTS);
                     wait_drain(bar(Smem::x_full + s), (last / X_SLOTS) & 1u, ctx);
-                    if (ok) wait_drain(bar(Smem::x_empty + s), (last / X_SLOTS) & 1u, ctx);
                 }
         }
     } else if (WHOLE ? warp == WARP_RAW : warp >= WARP_COPY) {
@@ -427,8 +396,8 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
         uint32_t it = 0;
         bool ok = true;
         while (ok && at.item < items) {
-            const Item t = next_item(p, ex, num_pairs, lane, at);
-            const int row0 = G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) : t.row_block * 2 * BW + static_cast<int>(rank) * BW;
+            const Item t = next_item(p, ex, lane, at);
+            const int row0 = t.row_block * (G ? BW / 2 : BW);
             // A warp copies 32 rows, 10 pieces each, in ten steps.  A row's skew repeats after
             // 32 rows, whose bytes are a multiple of 16.  Rows behind the expert's are
             // another's or zeros, and dropped.
@@ -511,8 +480,8 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
         };
         uint32_t tiles_done = 0, it = 0;
         bool ok = true, issued = false;
-        for (int item = pair; ok && item < items; item += num_pairs) {
-            const uint32_t idesc = desc_of(next_item(p, ex, num_pairs, lane, at));
+        while (ok && at.item < items) {
+            const uint32_t idesc = desc_of(next_item(p, ex, lane, at));
             const uint32_t d = tiles_done & 1u;  // accumulator
             if (!warp_wait_or_abort(bar(Smem::d_empty + d), ((tiles_done >> 1) & 1u) ^ 1u, abort_flag, ctx)) break;
             for (int st = 0; st < stages; ++st, ++it) {
@@ -542,7 +511,7 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
                     commit(one, bars + 8u * (Smem::a_empty + as));
                 }
                 if (!ok) break;
-                commit_both(one, bars + 8u * (Smem::x_empty + xs));
+                commit(one, bars + 8u * (Smem::x_empty + xs));
             }
             if (ok) commit(one, bars + 8u * (Smem::d_full + d));
             ++tiles_done;
@@ -556,7 +525,8 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
         const int q = warp & 3, part = (warp - WARP_DEQ) >> 2;
         const int row = G ? (lane >> 4) * (BW / 2) + q * 16 + (lane & 15) : q * 32 + lane;
         const uint32_t to = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + D_COLS + part * A_COLS;
-        const uint32_t total = pair < items ? static_cast<uint32_t>((items - pair + num_pairs - 1) / num_pairs) * chunks : 0u;
+        const int ctas = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
+        const uint32_t total = first < items ? static_cast<uint32_t>((items - first + ctas - 1) / ctas) * chunks : 0u;
         const uint32_t place = static_cast<uint32_t>(row) * RAW_ROW + 36u * part;
         int c = 0;  // chunk of its item
         for (uint32_t it = 0; it < total; ++it) {
@@ -617,12 +587,11 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
         uint32_t tiles_done = 0;
         pdl_wait();
         while (at.item < items) {
-            const Item t = next_item(p, ex, num_pairs, lane, at);
+            const Item t = next_item(p, ex, lane, at);
             const uint32_t d = tiles_done & 1u;
             // lanes 2i and 2i + 1 exchange halves of two columns: each then has two
             // neighbouring features f, f + 1 of one
-            const int f = G ? t.row_block * BW + static_cast<int>(rank) * (BW / 2) + q * 16 + (lane & 14)
-                            : t.row_block * 2 * BW + static_cast<int>(rank) * BW + q * 32 + (lane & 30);
+            const int f = t.row_block * (G ? BW / 2 : BW) + (G ? q * 16 + (lane & 14) : q * 32 + (lane & 30));
             for (int c = 32 * part + lane; c < t.width; c += 64) {  // place in out (none: 0)
                 uint64_t to = 0;
                 if (c < t.cols) {
@@ -697,7 +666,6 @@ __global__ void __launch_bounds__(kTileThreads<WHOLE>, 1)
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    cluster_barrier();  // the peer sends nothing here any more
     tc_fence_after();
     if (warp == WARP_MMA) tmem_dealloc_cta(tmem_base, TMEM_COLS);
 }
@@ -771,21 +739,21 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
     if (WHOLE && (!encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, row, rows, row, RAW_CHUNK, G ? BW / 2 : BW) ||
                   !encode_tmap_2d(&tw2, CU_TENSOR_MAP_DATA_TYPE_UINT8, G ? w2 : w, row, rows, row, RAW_CHUNK, G ? BW / 2 : BW)))
         return cudaErrorInvalidValue;
-    const int tile_rows = G ? BW : 2 * BW;
+    const int tile_rows = G ? BW / 2 : BW;
     const TileParams p = {plan, out, out_stride, {w, G ? w2 : w}, static_cast<int64_t>(row), static_cast<int>(n),
                           static_cast<int>(padded / CK), static_cast<int>(k / kQK),
                           static_cast<int>((n + tile_rows - 1) / tile_rows), 0x41804180u,
                           n % 2 == 0 && out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(out) % (G ? 4 : 8) == 0, ctx};
     static int limits[kMaxDevices];
     const size_t smem = Layout<WHOLE>::total(plan.experts);
-    cudaError_t e = ensure_smem(experts_tile_kernel<G, WHOLE>, smem, true, limits);
+    cudaError_t e = ensure_smem(experts_tile_kernel<G, WHOLE>, smem, false, limits);
     if (e != cudaSuccess) return e;
     const RowsParams r = {plan, x, x_stride, reinterpret_cast<uint4 *>(xr), static_cast<int>(k), static_cast<int>(padded), G, ctx};
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((plan.pairs_total + kRowsWarps - 1) / kRowsWarps, int64_t(1) << 30));
     e = launch_kernel(experts_rows_kernel, dim3(grid), dim3(kRowsWarps * 32), 0, stream, 1, r);
     if (e != cudaSuccess) return e;
-    const unsigned pairs = std::max(1, device_sm_count() / 2);
-    return launch_kernel(experts_tile_kernel<G, WHOLE>, dim3(2 * pairs), dim3(kTileThreads<WHOLE>), smem, stream, 2, tx, tx64, tw, tw2, p);
+    return launch_kernel(experts_tile_kernel<G, WHOLE>, dim3(device_sm_count()), dim3(kTileThreads<WHOLE>), smem, stream, 1, tx, tx64,
+                         tw, tw2, p);
 }
 
 }  // namespace
