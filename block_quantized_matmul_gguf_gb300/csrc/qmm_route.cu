@@ -87,9 +87,24 @@ struct Norm {
     float top, inv;  // softmax: the largest logit (0 where it is no finite number) and 1 / sum of exp(l - top), 0 for none
 };
 
-// A score as it is returned.
+// A score as it is returned; the sigmoid by the exponential that does not overflow.
 __device__ __forceinline__ float score_of(float l, const Norm &n, bool softmax) {
-    return softmax ? expf(l - n.top) * n.inv : 1.0f / (1.0f + expf(-l));
+    if (softmax) return expf(l - n.top) * n.inv;
+    const float e = expf(-fabsf(l));
+    return (l < 0.0f ? e : 1.0f) / (1.0f + e);
+}
+
+// Below this a score is 0 in 64 bits, and counts as 0: log 2^-1075.
+constexpr float kNoScore = -745.1332f;
+
+// A chosen expert's score over some common factor, for a quotient by their sum: `most`
+// is the chosen experts' largest logit.  The scores themselves may be too small for 32
+// bits.  A softmax's are exp(l) but for a factor, and so are a sigmoid's, to 2^-92, where
+// no logit is above -64.
+__device__ __forceinline__ float relative_score(float l, float most, const Norm &n, bool softmax) {
+    if (softmax && n.inv != n.inv) return n.inv;  // no number among the logits
+    if (softmax ? l - n.top < kNoScore : l < kNoScore) return 0.0f;
+    return softmax || most < -64.0f ? expf(l - most) : score_of(l, n, false);
 }
 // A score as it is compared; near values are formed again in 64 bits.
 __device__ __forceinline__ float rough_score(float l, const Norm &n, bool softmax) {
@@ -560,8 +575,12 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 2 : 1) route_kernel(const _
                 }
                 id = choose<V, T>(p, row, norm, l, s.scratch + static_cast<size_t>(warp) * a.experts * 8, lane);
                 const bool chosen = lane < a.topk;
-                w = chosen ? score_of(load_logit(row, id), norm, a.score == 0) : 0.0f;
-                if (a.renormalize) {
+                const float mine = chosen ? load_logit(row, id) : -kInf;
+                if (!a.renormalize) {
+                    w = chosen ? score_of(mine, norm, a.score == 0) : 0.0f;
+                } else {
+                    const float most = value_of(warp_max(order_of(mine)));
+                    w = chosen ? relative_score(mine, most, norm, a.score == 0) : 0.0f;
                     float sum = w;
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);

@@ -503,9 +503,11 @@ qmm_status qmm_attn_q4_0(const qmm_kv_q4_0 *cache, const qmm_attn_args *args,
  *              renormalize, times scale
  * Equal values go to the lowest index, a NaN comes behind -inf.  The choice is
  * that of 64-bit arithmetic on the given logits and biases: values that lie
- * too near for fp32 are formed again.  Weights are fp32 and off by a few 2^-24;
- * where all scores are 0 (logits -inf) so are the weights.  Then, over all
- * tokens,
+ * too near for fp32 are formed again.  Weights are fp32: off by a few 2^-24 of
+ * themselves, and by 2^-24 for each 1 that the logit lies from the largest.  Those
+ * that are renormalized keep their quotients however small the scores are; scores
+ * that are 0 in 64 bits (logits of -inf, or 745 below 0 or, for a softmax, below the
+ * largest) have weights of 0.  Then, over all tokens,
  *   pairs         int32 [tokens * topk]: the pairs t * topk + r in the order of
  *                 their experts, those of one expert by token
  *   expert_start  int32 [experts + 1]: expert e has entries expert_start[e] ..
