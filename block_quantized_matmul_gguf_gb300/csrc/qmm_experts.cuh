@@ -9,17 +9,13 @@
 // operand, taken from the 4-bit codes in registers, and 8 pairs' x as the other;
 // the scales join in fp32.
 //
-// Precision.  x enters as one binary16 value, scaled by a power of two per row
-// and 256 values so that the largest lies in [2^14, 2^15): a bf16 x exactly (down
-// to 2^-31 of that largest), an fp32 x rounded to 11 bits, which is less than a
-// bf16 output shows.  For fp32 outputs an fp32 x enters in two parts (22 bits), which
-// are two products, or, with up to four pairs, other columns of one (16 tokens 44.1 us
-// for two, 40.6 for one).
-// For bf16 outputs a code masked in place is a subnormal binary16 number, n 2^-24
-// (16 n 2^-24 for the upper of two, the 16 taken out of x), and -8 sum x is where
-// the sum begins; fp32 outputs take two more instructions a pair for the normal
-// numbers n - 8, because the tensor cores' sums of subnormal operands keep some 18
-// bits only.
+// Precision.  A bf16 x enters as one binary16 value, scaled by a power of two per row
+// and 256 values so that the largest lies in [2^14, 2^15): exactly (down to 2^-31 of
+// that largest).  An fp32 x enters in two parts (22 bits), which are two products, or,
+// with up to four pairs, other columns of one (16 tokens 44.1 us for two, 40.6 for one).
+// The codes are made n - 8 before the products: left as the subnormal numbers that a
+// word holds they save two instructions a pair, but the tensor cores' sums of
+// subnormal operands keep some 18 bits only.
 //
 // Work.  An item is 64 rows of weights (32 gate and the same 32 up rows for
 // GeGLU) of one expert against one group of 8 NB of its pairs.  A CTA of up to 8
@@ -112,18 +108,15 @@ __device__ __forceinline__ void barrier(int id, int threads) {
     asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Shared memory, from its start: rings, x, its scales and sums, partial sums, rows.
-template <bool EXACT, int PARTS, int NB, bool ALIGNED>
+// Shared memory, from its start: rings, x, its scales, partial sums, rows.
+template <int PARTS, int NB, bool ALIGNED>
 struct StreamLayout {
     static constexpr int pitch = ALIGNED ? 144 : 176;  // bytes of a row's window in a stage
     static constexpr int stage = kRows * pitch;
     static constexpr int x_block = NB * PARTS * 512;   // bytes of 32 values of K
     __host__ __device__ static int x(int warps) { return warps * kStages * stage; }
     __host__ __device__ static int scale(int warps, int panel) { return x(warps) + panel * 8 * x_block; }
-    __host__ __device__ static int sums(int warps, int panel) { return scale(warps, panel) + panel * NB * 32; }
-    __host__ __device__ static int part(int warps, int panel) {
-        return sums(warps, panel) + (EXACT ? 0 : panel * 8 * NB * 32);
-    }
+    __host__ __device__ static int part(int warps, int panel) { return scale(warps, panel) + panel * NB * 32; }
     __host__ __device__ static int rows(int warps, int panel) { return part(warps, panel) + warps * NB * kTiles * 512; }
     __host__ __device__ static int total(int warps, int panel) { return rows(warps, panel) + 2 * 8 * NB * 4 + 64; }
 };
@@ -240,9 +233,9 @@ __device__ __forceinline__ float4 load_four<uint16_t>(const uint16_t *p, bool wi
 // One chunk of eight pairs' x as the products' operand: lane (g, t) makes
 // pair g's values 4t..4t+3 and 16+4t..16+4t+3 of each block, in the order that
 // the codes of a word have.
-template <bool EXACT, int PARTS, int NB, typename T>
-__device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *scale, float *sums, const T *row, int chunk,
-                                     int nb, int lane, bool packed) {
+template <int PARTS, int NB, typename T>
+__device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *scale, const T *row, int chunk, int nb, int lane,
+                                     bool packed) {
     const int t = lane & 3, g = lane >> 2;
     const int blocks = min(8, p.blocks - chunk * 8);
     float4 v[8][2];
@@ -267,18 +260,15 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
         uint32_t part[PARTS][4];
-        float sum = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float s = EXACT || h == 0 ? f : f * 0.0625f;  // upper codes count 16-fold
-            const float y[4] = {v[b][h].x * s, v[b][h].z * s, v[b][h].y * s, v[b][h].w * s};
+            const float y[4] = {v[b][h].x * f, v[b][h].z * f, v[b][h].y * f, v[b][h].w * f};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t hi = pack_half(y[2 * i], y[2 * i + 1]);
                 part[0][2 * h + i] = hi;
                 if constexpr (PARTS == 2)
                     part[1][2 * h + i] = pack_half(y[2 * i] - low_half(hi), y[2 * i + 1] - high_half(hi));
-                if constexpr (!EXACT) sum += (low_half(hi) + high_half(hi)) * (h ? 16.0f : 1.0f);
             }
         }
         if (PARTS == 2 && packed) {
@@ -292,20 +282,15 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
 #pragma unroll
         for (int q = 0; q < PARTS; ++q)
             reinterpret_cast<uint4 *>(to + q * 512)[lane] = make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]);
-        if constexpr (!EXACT) {
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-            if (t == 0) sums[(chunk * 8 + b) * 8 * NB + nb * 8 + g] = sum * -4.76837158203125e-07f;  // -8 2^-24
-        }
     }
 }
 
 // A warp's products of one stage: kTiles tiles of 16 rows against NB groups of
 // eight pairs.  skew: bytes by which the lane's rows (g, g + 8 of each tile, which
 // repeat after two) begin behind their windows.
-template <bool EXACT, int PARTS, int NB, bool ALIGNED>
-__device__ __forceinline__ void stage_products(const char *stage, const char *xs, const float *scale, const float *sums,
-                                               int blocks, const int (&skew)[2][2], uint32_t magic, int lane,
+template <int PARTS, int NB, bool ALIGNED>
+__device__ __forceinline__ void stage_products(const char *stage, const char *xs, const float *scale, int blocks,
+                                               const int (&skew)[2][2], uint32_t magic, int lane,
                                                int used, float (&total)[kTiles][NB][4]) {
     constexpr int pitch = ALIGNED ? 144 : 176;
     const int t = lane & 3, g = lane >> 2;
@@ -318,7 +303,6 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
             for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
     auto block = [&](int b, const uint32_t (&q)[kTiles][2], const float (&d)[kTiles][2]) {
         uint32_t x[NB][PARTS][4];
-        float c[NB][2];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             if (n < used) {
@@ -326,10 +310,6 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
                 for (int s = 0; s < PARTS; ++s) {
                     const uint4 v = reinterpret_cast<const uint4 *>(xs + ((b * NB + n) * PARTS + s) * 512)[lane];
                     x[n][s][0] = v.x, x[n][s][1] = v.y, x[n][s][2] = v.z, x[n][s][3] = v.w;
-                }
-                if constexpr (!EXACT) {
-                    const float2 v = *reinterpret_cast<const float2 *>(sums + b * 8 * NB + n * 8 + 2 * t);
-                    c[n][0] = v.x, c[n][1] = v.y;
                 }
             }
         }
@@ -339,29 +319,21 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
 #pragma unroll
         for (int r = 0; r < kTiles; ++r) {
             const uint32_t u = q[r][0], v = q[r][1], u8 = u >> 8, v8 = v >> 8;
-            if constexpr (EXACT) {
-                a[r][0] = hadd2((u & 0x000F000Fu) | magic, 0xE408E408u);  // - 1032
-                a[r][1] = hadd2((v & 0x000F000Fu) | magic, 0xE408E408u);
-                a[r][2] = hadd2((u8 & 0x000F000Fu) | magic, 0xE408E408u);
-                a[r][3] = hadd2((v8 & 0x000F000Fu) | magic, 0xE408E408u);
-                a[r][4] = hfma2((u & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
-                a[r][5] = hfma2((v & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
-                a[r][6] = hfma2((u8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
-                a[r][7] = hfma2((v8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
-            } else {
-                a[r][0] = u & 0x000F000Fu, a[r][1] = v & 0x000F000Fu, a[r][2] = u8 & 0x000F000Fu, a[r][3] = v8 & 0x000F000Fu;
-                a[r][4] = u & 0x00F000F0u, a[r][5] = v & 0x00F000F0u, a[r][6] = u8 & 0x00F000F0u, a[r][7] = v8 & 0x00F000F0u;
-            }
+            a[r][0] = hadd2((u & 0x000F000Fu) | magic, 0xE408E408u);  // - 1032
+            a[r][1] = hadd2((v & 0x000F000Fu) | magic, 0xE408E408u);
+            a[r][2] = hadd2((u8 & 0x000F000Fu) | magic, 0xE408E408u);
+            a[r][3] = hadd2((v8 & 0x000F000Fu) | magic, 0xE408E408u);
+            a[r][4] = hfma2((u & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
+            a[r][5] = hfma2((v & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+            a[r][6] = hfma2((u8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+            a[r][7] = hfma2((v8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             if (n < used) {
                 float z[kTiles][4];
 #pragma unroll
-                for (int r = 0; r < kTiles; ++r) {
-                    z[r][0] = z[r][2] = EXACT ? 0.0f : c[n][0];
-                    z[r][1] = z[r][3] = EXACT ? 0.0f : c[n][1];
-                }
+                for (int r = 0; r < kTiles; ++r) z[r][0] = z[r][1] = z[r][2] = z[r][3] = 0.0f;
 #pragma unroll
                 for (int s = PARTS - 1; s >= 0; --s) {  // the small part first
 #pragma unroll
@@ -431,10 +403,7 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
 #pragma unroll
         for (int r = 0; r < kTiles; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float v = EXACT ? acc[r][n][i] : acc[r][n][i] * 16777216.0f;
-                total[r][n][i] = fmaf(v, i & 1 ? s.y : s.x, total[r][n][i]);
-            }
+            for (int i = 0; i < 4; ++i) total[r][n][i] = fmaf(acc[r][n][i], i & 1 ? s.y : s.x, total[r][n][i]);
     }
 }
 
@@ -451,18 +420,17 @@ __device__ __forceinline__ void put(void *out, int64_t at, bool bf16, float v) {
         static_cast<float *>(out)[at] = v;
 }
 
-template <bool EXACT, int PARTS, int NB, bool GEGLU, bool ALIGNED>
+template <int PARTS, int NB, bool GEGLU, bool ALIGNED>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_constant__ CUtensorMap w0,
                                                                    const __grid_constant__ CUtensorMap w1,
                                                                    const __grid_constant__ StreamParams p) {
-    using L = StreamLayout<EXACT, PARTS, NB, ALIGNED>;
+    using L = StreamLayout<PARTS, NB, ALIGNED>;
     extern __shared__ __align__(128) char smem[];
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = lane & 3, g = lane >> 2;
     const int rw = warp / p.kw, kw = warp - rw * p.kw;  // item among those at a time, part of K
     char *xs = smem + L::x(warps);
     float *scale = reinterpret_cast<float *>(smem + L::scale(warps, p.x_panel));
-    float *sums = reinterpret_cast<float *>(smem + L::sums(warps, p.x_panel));
     float *part = reinterpret_cast<float *>(smem + L::part(warps, p.x_panel));
     int *src = reinterpret_cast<int *>(smem + L::rows(warps, p.x_panel));  // [8 NB] rows of x, -1 where there is none
     int *dst = src + 8 * NB;                                              // [8 NB] rows of out
@@ -619,13 +587,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                         const int row = src[packed ? g & 3 : n * 8 + g];
                         // addresses count from the panel's first chunk
                         char *xp = xs - static_cast<int64_t>(c0) * 8 * x_block;
-                        float *sp = scale - c0 * 8 * NB, *mp = sums - c0 * 64 * NB;
+                        float *sp = scale - c0 * 8 * NB;
                         if (p.x_bf16)
-                            stage_x<EXACT, PARTS, NB, uint16_t>(
-                                p, xp, sp, mp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane, packed);
+                            stage_x<PARTS, NB, uint16_t>(
+                                p, xp, sp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane, packed);
                         else
-                            stage_x<EXACT, PARTS, NB, float>(
-                                p, xp, sp, mp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane, packed);
+                            stage_x<PARTS, NB, float>(
+                                p, xp, sp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane, packed);
                     }
                 held_expert = at.expert;
                 held_group = at.group;
@@ -652,9 +620,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                 }
                 if (there && ok) {
                     auto products = [&](auto parts) {
-                        stage_products<EXACT, decltype(parts)::value, NB, ALIGNED>(
+                        stage_products<decltype(parts)::value, NB, ALIGNED>(
                             ring_ptr + (done & 1) * L::stage, xs + (c - c0) * 8 * x_block, scale + (c - c0) * 8 * NB,
-                            sums + (c - c0) * 64 * NB, min(8, p.blocks - c * 8), skew, p.magic, lane, used, total);
+                            min(8, p.blocks - c * 8), skew, p.magic, lane, used, total);
                     };
                     if (packed)
                         products(std::integral_constant<int, 1>());
@@ -720,9 +688,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
 
 constexpr int kSharedLimit = 232448 - 256;  // beside the kernel's own
 
-template <bool EXACT, int PARTS, int NB, bool GEGLU, bool ALIGNED>
+template <int PARTS, int NB, bool GEGLU, bool ALIGNED>
 cudaError_t launch_stream(StreamParams p, cudaStream_t stream) {
-    using L = StreamLayout<EXACT, PARTS, NB, ALIGNED>;
+    using L = StreamLayout<PARTS, NB, ALIGNED>;
     static int limits[kMaxDevices];
     // as many warps as fit beside all of x, four at least, and x in panels beyond that
     int warps = kMaxWarps;
@@ -758,7 +726,7 @@ cudaError_t launch_stream(StreamParams p, cudaStream_t stream) {
     p.row_groups = static_cast<int>((p.n + rows * p.rw - 1) / (rows * p.rw));
     warps = p.rw * p.kw;
     const int smem = L::total(warps, p.x_panel);
-    const cudaError_t e = ensure_smem(stream_kernel<EXACT, PARTS, NB, GEGLU, ALIGNED>, smem, false, limits);
+    const cudaError_t e = ensure_smem(stream_kernel<PARTS, NB, GEGLU, ALIGNED>, smem, false, limits);
     if (e != cudaSuccess) return e;
     CUtensorMap w0 = {}, w1 = {};
     if constexpr (ALIGNED) {
@@ -767,20 +735,18 @@ cudaError_t launch_stream(StreamParams p, cudaStream_t stream) {
             !encode_tmap_2d(&w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w[GEGLU ? 1 : 0], p.row_bytes, all, p.row_bytes, 144, rows))
             return cudaErrorInvalidValue;
     }
-    return launch_kernel(stream_kernel<EXACT, PARTS, NB, GEGLU, ALIGNED>, dim3(device_sm_count()), dim3(warps * 32), smem, stream,
+    return launch_kernel(stream_kernel<PARTS, NB, GEGLU, ALIGNED>, dim3(device_sm_count()), dim3(warps * 32), smem, stream,
                          1, w0, w1, p);
 }
 
 template <bool GEGLU, bool ALIGNED, int NB>
-cudaError_t launch_precision(const StreamParams &p, bool exact, cudaStream_t stream) {
-    if (!exact) return launch_stream<false, 1, NB, GEGLU, ALIGNED>(p, stream);
-    return p.x_bf16 ? launch_stream<true, 1, NB, GEGLU, ALIGNED>(p, stream) : launch_stream<true, 2, NB, GEGLU, ALIGNED>(p, stream);
+cudaError_t launch_parts(const StreamParams &p, cudaStream_t stream) {
+    return p.x_bf16 ? launch_stream<1, NB, GEGLU, ALIGNED>(p, stream) : launch_stream<2, NB, GEGLU, ALIGNED>(p, stream);
 }
 
-// exact: fp32 results (see above).  Groups of 16 pairs where the experts have
-// more than eight on average.
+// Groups of 16 pairs where the experts have more than eight on average.
 template <bool GEGLU>
-cudaError_t launch_form(StreamParams &p, bool exact, cudaStream_t stream) {
+cudaError_t launch_form(StreamParams &p, cudaStream_t stream) {
     p.blocks = static_cast<int>(p.k / kQK);
     p.chunks = (p.blocks + 7) / 8;
     p.row_bytes = static_cast<int64_t>(p.blocks) * kQ4_0Bytes;
@@ -790,9 +756,8 @@ cudaError_t launch_form(StreamParams &p, bool exact, cudaStream_t stream) {
     p.x_wide = reinterpret_cast<uintptr_t>(p.x) % (p.x_bf16 ? 8 : 16) == 0 && p.x_stride % 4 == 0;  // loads of four
     const bool aligned = p.k % kChunk == 0 && p.plan.experts * p.n < (int64_t(1) << 31);  // a box's row is 32 bits
     const bool many = p.plan.pairs_total > 8 * static_cast<int64_t>(p.plan.experts);
-    if (aligned)
-        return many ? launch_precision<GEGLU, true, 2>(p, exact, stream) : launch_precision<GEGLU, true, 1>(p, exact, stream);
-    return many ? launch_precision<GEGLU, false, 2>(p, exact, stream) : launch_precision<GEGLU, false, 1>(p, exact, stream);
+    if (aligned) return many ? launch_parts<GEGLU, true, 2>(p, stream) : launch_parts<GEGLU, true, 1>(p, stream);
+    return many ? launch_parts<GEGLU, false, 2>(p, stream) : launch_parts<GEGLU, false, 1>(p, stream);
 }
 
 }  // namespace experts

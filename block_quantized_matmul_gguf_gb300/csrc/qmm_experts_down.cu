@@ -119,7 +119,7 @@ cudaError_t launch_experts_down(const ExpertsDown &a, cudaStream_t stream, const
         p.n = a.n;
         p.k = a.k;
         p.ctx = ctx;
-        e = experts::launch_form<false>(p, !a.y_bf16, stream);
+        e = experts::launch_form<false>(p, stream);
     }
     if (e != cudaSuccess) return e;
     const int64_t tokens = a.plan.pairs_total / a.plan.topk;

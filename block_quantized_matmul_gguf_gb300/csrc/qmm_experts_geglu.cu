@@ -19,7 +19,7 @@ cudaError_t launch_experts_geglu(const ExpertsGeglu &a, cudaStream_t stream, con
     p.n = a.n;
     p.k = a.k;
     p.ctx = ctx;
-    return experts::launch_form<true>(p, !a.h_bf16, stream);
+    return experts::launch_form<true>(p, stream);
 }
 
 }  // namespace qmm

@@ -114,3 +114,67 @@ def test_scales_and_rows_of_any_range(qmm, tokens, experts, k):
             qmm.qmm_experts_down_q4_0(dev(b), rows.cuda(), y, dev(ids.astype(np.int32)), dev(weights), dev(starts), dev(pairs), n, k)
             assert (np.abs(y.double().cpu().numpy() - want) <= limit + 2.0 ** -8 * (np.abs(want) + limit)).all()
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)], ids=str)
+@pytest.mark.parametrize("tokens,experts", [(3, 64), (7, 64), (1, 4), (90, 4)])
+@pytest.mark.parametrize("k", [256, 288])
+def test_inputs_and_codes_enter_whole(qmm, types, tokens, experts, k):
+    """Rows that hold v in one place and -(v + 1) in another with the same weight w: y = -w.
+    v has 13 bits (8 for bf16, where -(v + 1) is split over two places), so that the products
+    of v and a code are exact and those with a scale off by 2^-24 of 2^13 w, twice: within
+    2^-10 |w|, and the result's rounding of 2^-8 |w| or 2^-24."""
+    rng = np.random.default_rng(tokens + experts + k)
+    n = 48
+    b = ref.blocks(rng, experts, n, k)
+    row = b.reshape(experts, n, k // 32, 18)
+    row[:, :, 1] = row[:, :, 0]
+    row[:, :, 2] = row[:, :, 0]
+    ids = rng.integers(0, experts, (tokens, 1))
+    starts, pairs = ref.plan_of(ids, experts)
+    at = rng.integers(0, 32, tokens)
+    every = np.arange(tokens)
+    x = np.zeros((tokens, k), dtype=np.float32)
+    if types[0] is F32:
+        v = rng.integers(1 << 12, (1 << 13) - 1, tokens).astype(np.float32)
+        x[every, at], x[every, 32 + at] = v, -(v + 1)
+    else:
+        v = 32 * rng.integers(128, 256, tokens).astype(np.float32)
+        x[every, at], x[every, 32 + at], x[every, 64 + at] = v, -v, -1
+    w, _ = ref.matrix(b)
+    want = -w[ids[:, 0], :, at]
+    y = torch.empty(tokens, n, dtype=types[1], device="cuda")
+    ones = torch.ones(tokens, 1, device="cuda")
+    qmm.qmm_experts_down_q4_0(dev(b), dev(x[pairs], types[0]), y, dev(ids.astype(np.int32)), ones, dev(starts), dev(pairs), n, k)
+    limit = 2.0 ** -10 + (2.0 ** -24 if types[1] is F32 else 2.0 ** -8)
+    assert (np.abs(y.double().cpu().numpy() - want) <= limit * np.abs(want)).all()
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("tokens,experts,types", [(3, 64, t) for t in ((F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16))] +
+                         [(90, 4, t) for t in ((F32, F32), (F32, BF16), (BF16, F32))], ids=str)
+def test_sums_of_a_block_are_whole(qmm, types, tokens, experts):
+    """v, -v and -1 in a block of one code, v of 17 bits, in the streaming form: integers to
+    2^20 whose sum, the code, is exact in 24 bits; times the scale exact too, but for the
+    result's rounding.  (The tile form adds products of weights: 14 bits below each of v's
+    17, so that addends of 2^17 |w| leave 2^-6 |w| in 24 bits.)"""
+    rng = np.random.default_rng(tokens + experts)
+    n, k = 48, 256
+    b = ref.blocks(rng, experts, n, k)
+    row = b.reshape(experts, n, k // 32, 18)
+    row[:, :, 0, 2:] = rng.integers(0, 16, (experts, n, 1)) * 17
+    ids = rng.integers(0, experts, (tokens, 1))
+    starts, pairs = ref.plan_of(ids, experts)
+    x = np.zeros((tokens, k), dtype=np.float32)
+    for t in range(tokens):
+        at = rng.permutation(32)[:3]
+        v = 512 * int(rng.integers(128, 256))
+        x[t, at] = v, -v, -1
+    w, _ = ref.matrix(b)
+    want = -w[ids[:, 0], :, 0]
+    y = torch.empty(tokens, n, dtype=types[1], device="cuda")
+    ones = torch.ones(tokens, 1, device="cuda")
+    qmm.qmm_experts_down_q4_0(dev(b), dev(x[pairs], types[0]), y, dev(ids.astype(np.int32)), ones, dev(starts), dev(pairs), n, k)
+    limit = 0.0 if types[1] is F32 else 2.0 ** -8
+    assert (np.abs(y.double().cpu().numpy() - want) <= limit * np.abs(want)).all()
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
