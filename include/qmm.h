@@ -571,124 +571,7 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
  * where a bf16 input is exact too; else streaming, where an input is held in binary16
  * with a power of two for each 256 values of a row: a bf16 one exactly, down to 2^-31
  * of the largest of the 256, an fp32 one in two parts, 22 bits of it and 2^-39 of that
- * largest.  A row of x or h that holds an infinity or a NaN gives NaN.
- * Which form a call takes depends on its host-side
- * arguments alone, of which the table's width stands for the lengths; equal
- * calls give equal bits.
- * Requires heads a multiple of kv_heads, heads <= 1024, batch and max_q >= 1,
- * total_q >= 0 (0 launches nothing), window >= 0 and 0 unless causal, scale
- * finite, strides at least heads * head_dim, pointers aligned to their type;
- * at most 2^30 rows and batch <= 16384 (else QMM_ERR_UNSUPPORTED).  out and
- * lse must overlap no input. */
-typedef struct qmm_attn_args {
-    const void *q;
-    int64_t q_stride;
-    qmm_dtype q_type;
-    void *out;
-    int64_t out_stride;
-    qmm_dtype out_type;
-    float *lse;
-    const int32_t *table;
-    int64_t table_width;
-    const int32_t *q_start;
-    const int32_t *kv_len;
-    int batch;
-    int64_t total_q;
-    int max_q;
-    int heads;
-    float scale;
-    int causal;
-    int window;
-    void *workspace;
-    size_t workspace_bytes;
-} qmm_attn_args;
-
-size_t qmm_attn_q4_0_workspace_bytes(const qmm_kv_q4_0 *cache, int heads);
-qmm_status qmm_attn_q4_0(const qmm_kv_q4_0 *cache, const qmm_attn_args *args,
-                         qmm_stream_t stream);
-
-/* ---- Routing to experts ---------------------------------------------------
- * For each token t < tokens, from l = logits[t][e], e < experts:
- *   s_e = exp(l_e) / sum_j exp(l_j)  (QMM_SCORE_SOFTMAX)
- *         or 1 / (1 + exp(-l_e))     (QMM_SCORE_SIGMOID)
- *   c_e = s_e + bias[e]              (bias NULL: c orders as l does)
- *   with groups > 1, groups of experts / groups consecutive experts score the
- *   sum of their group_best (1 or 2) largest c, and the group_topk best are kept
- *   ids[t]     the topk kept experts of largest c, in that order
- *   weights[t] their s (without the bias), divided by their sum if
- *              renormalize, times scale
- * Equal values go to the lowest index, a NaN comes behind -inf.  The choice is
- * that of 64-bit arithmetic on the given logits and biases: values that lie
- * too near for fp32 are formed again.  Weights are fp32: off by a few 2^-24 of
- * themselves, and by 2^-24 for each 1 that the logit lies from the largest.  Those
- * that are renormalized keep their quotients however small the scores are; scores
- * that are 0 in 64 bits (logits of -inf, or 745 below 0 or, for a softmax, below the
- * largest) have weights of 0.  Then, over all tokens,
- *   pairs         int32 [tokens * topk]: the pairs t * topk + r in the order of
- *                 their experts, those of one expert by token
- *   expert_start  int32 [experts + 1]: expert e has entries expert_start[e] ..
- *                 expert_start[e + 1] - 1
- * which is what the experts' products read.
- *   count  int32 on the device, or NULL: tokens from *count on are not there
- *          (padding of a captured graph): ids and pairs -1, weights 0.  A count
- *          outside 0..tokens is moved to the nearer end, QMM_ERR_INDEX.
- *   workspace  16-byte aligned device memory of at least
- *          qmm_route_workspace_bytes() bytes (0 up to 512 tokens), scratch
- * Requires tokens >= 0 (0 launches nothing), 1 <= topk <= 32, topk at most the
- * kept groups' experts, groups dividing experts, 1 <= group_topk <= groups,
- * scale finite, logits_stride >= experts; at most 1024 experts, 32 groups and
- * 2^30 pairs (else QMM_ERR_UNSUPPORTED).  No output may overlap an input or
- * another output. */
-typedef enum qmm_score { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
-
-typedef struct qmm_route_args {
-    const void *logits;
-    int64_t logits_stride;
-    qmm_dtype type;
-    const float *bias;
-    const int32_t *count;
-    int64_t tokens;
-    int experts;
-    int topk;
-    qmm_score score;
-    int groups;
-    int group_topk;
-    int group_best;
-    int renormalize;
-    float scale;
-    int32_t *ids;
-    float *weights;
-    int32_t *expert_start;
-    int32_t *pairs;
-    void *workspace;
-    size_t workspace_bytes;
-} qmm_route_args;
-
-size_t qmm_route_workspace_bytes(int64_t tokens, int experts);
-qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
-
-/* ---- The experts' products ------------------------------------------------
- * Each expert e has Q4_0 matrices, one after the other: wg, wu [experts][n][k]
- * (gate and up, k the hidden size) and wd [experts][n][k] (down, n the hidden
- * size), n rows of k / 32 blocks.  The plan is what qmm_route leaves: entry i of
- * `pairs` with expert_start[e] <= i < expert_start[e + 1] is pair t * topk + r of
- * token t, to be worked by expert e.
- *   geglu  h[i] = gelu(x[t] wg_e^T) * (x[t] wu_e^T), row i in the order of
- *          `pairs`; x [tokens] rows of k, h [tokens * topk] rows of n; the GELU
- *          of qmm_gemv_q4_0_geglu.  Rows from expert_start[experts] on are left
- *          as they were.
- *   down   y[t] = sum_r weights[t][r] * (h[i] wd_e^T), i the entry of pair
- *          t * topk + r, over the r with 0 <= ids[t][r] < experts, in their
- *          order; a token without any gets 0.
- * Strides count elements; x_type, h_type and y_type may differ.
- * Arithmetic: sums in fp32.  With an fp32 output the weights are exact, a bf16
- * input too, and an fp32 input enters in two binary16 parts (22 bits of it, and
- * 2^-39 of the largest of its row's 256 values around it).  With a bf16 output
- * an fp32 input enters in 11 bits.  With bf16 in and out, rows of x or h on
- * multiples of 16 bytes, and half as many pairs as experts at least or k >= 4096,
- * weights and inputs are exact too.  The down projections stay in fp32 up to the
- * sum's own rounding. A row of x or h that holds an infinity or
- * a NaN gives NaN.  Which form a call takes depends on its host-side
+ * largest.  A row of x or h that holds an infinity or a NaN gives NaN. Which form a call takes depends on its host-side
  * arguments alone; equal calls give equal bits, and a pair's row depends on no
  * other pair.
  * Entries outside their arrays (an expert_start that descends or leaves
