@@ -11,8 +11,11 @@
 //
 // Precision.  A bf16 x enters as one binary16 value, scaled by a power of two per row
 // and 256 values so that the largest lies in [2^14, 2^15): exactly (down to 2^-31 of
-// that largest).  An fp32 x enters in two parts (22 bits), which are two products, or,
-// with up to four pairs, other columns of one (16 tokens 44.1 us for two, 40.6 for one).
+// that largest).  An fp32 x enters in two parts (22 bits): two products into one sum,
+// or, for groups of eight pairs, other columns of one product (`split`), whose eight
+// columns then are four pairs, so that a group has two.  Each part is then a
+// sum of its own and both meet at the end, however full the group is: a pair's bits
+// do not depend on the others (16 tokens of 8 of 64 experts of 1024 x 2048: 42.9 us).
 // The codes are made n - 8 before the products: left as the subnormal numbers that a
 // word holds they save two instructions a pair, but the tensor cores' sums of
 // subnormal operands keep some 18 bits only.
@@ -108,6 +111,16 @@ __device__ __forceinline__ void barrier(int id, int threads) {
     asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// How a group of 8 NB pairs lies in the products: blocks of eight columns, and the parts
+// of x that are products of their own; split: columns 0 .. 3 are four pairs' large parts, 4 .. 7 their small ones.
+template <int PARTS, int NB>
+struct Columns {
+    static constexpr bool split = PARTS == 2 && NB == 1;
+    static constexpr int blocks = split ? 2 : NB, parts = split ? 1 : PARTS;
+    static constexpr int pairs = split ? 4 : 8;    // of a block
+    static constexpr int lanes = split ? 16 : 32;  // of a warp that hold sums of their own
+};
+
 // Shared memory, from its start: rings, x, its scales, partial sums, rows.
 template <int PARTS, int NB, bool ALIGNED>
 struct StreamLayout {
@@ -116,7 +129,7 @@ struct StreamLayout {
     static constexpr int x_block = NB * PARTS * 512;   // bytes of 32 values of K
     __host__ __device__ static int x(int warps) { return warps * kStages * stage; }
     __host__ __device__ static int scale(int warps, int panel) { return x(warps) + panel * 8 * x_block; }
-    __host__ __device__ static int part(int warps, int panel) { return scale(warps, panel) + panel * NB * 32; }
+    __host__ __device__ static int part(int warps, int panel) { return scale(warps, panel) + panel * Columns<PARTS, NB>::blocks * 32; }
     __host__ __device__ static int rows(int warps, int panel) { return part(warps, panel) + warps * NB * kTiles * 512; }
     __host__ __device__ static int total(int warps, int panel) { return rows(warps, panel) + 2 * 8 * NB * 4 + 64; }
 };
@@ -230,12 +243,12 @@ __device__ __forceinline__ float4 load_four<uint16_t>(const uint16_t *p, bool wi
                        __uint_as_float(b & 0xFFFF0000u));
 }
 
-// One chunk of eight pairs' x as the products' operand: lane (g, t) makes
-// pair g's values 4t..4t+3 and 16+4t..16+4t+3 of each block, in the order that
+// One chunk of x as the products' operand, eight columns of it: lane (g, t) makes
+// column g's values 4t..4t+3 and 16+4t..16+4t+3 of each block, in the order that
 // the codes of a word have.
 template <int PARTS, int NB, typename T>
-__device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *scale, const T *row, int chunk, int nb, int lane,
-                                     bool packed) {
+__device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *scale, const T *row, int chunk, int nb, int lane) {
+    using C = Columns<PARTS, NB>;
     const int t = lane & 3, g = lane >> 2;
     const int blocks = min(8, p.blocks - chunk * 8);
     float4 v[8][2];
@@ -256,7 +269,7 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
     // top 2^f in [2^14, 2^15); both powers normal (a smaller top stays smaller)
     const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 15), 254);
     const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-    if (t == 0) scale[chunk * 8 * NB + nb * 8 + g] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+    if (t == 0) scale[(chunk * C::blocks + nb) * 8 + g] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
         uint32_t part[PARTS][4];
@@ -271,46 +284,43 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
                     part[1][2 * h + i] = pack_half(y[2 * i] - low_half(hi), y[2 * i + 1] - high_half(hi));
             }
         }
-        if (PARTS == 2 && packed) {
+        char *to = xs + ((chunk * 8 + b) * C::blocks + nb) * C::parts * 512;
+        if constexpr (C::split) {
             const bool low = g >= 4;
-            reinterpret_cast<uint4 *>(xs + (chunk * 8 + b) * 512)[lane] =
-                make_uint4(low ? part[PARTS - 1][0] : part[0][0], low ? part[PARTS - 1][1] : part[0][1],
-                           low ? part[PARTS - 1][2] : part[0][2], low ? part[PARTS - 1][3] : part[0][3]);
-            continue;
-        }
-        char *to = xs + ((chunk * 8 + b) * NB + nb) * PARTS * 512;
+            reinterpret_cast<uint4 *>(to)[lane] = make_uint4(low ? part[1][0] : part[0][0], low ? part[1][1] : part[0][1],
+                                                             low ? part[1][2] : part[0][2], low ? part[1][3] : part[0][3]);
+        } else {
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-            reinterpret_cast<uint4 *>(to + q * 512)[lane] = make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]);
+            for (int q = 0; q < PARTS; ++q)
+                reinterpret_cast<uint4 *>(to + q * 512)[lane] = make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]);
+        }
     }
 }
 
-// A warp's products of one stage: kTiles tiles of 16 rows against NB groups of
-// eight pairs.  skew: bytes by which the lane's rows (g, g + 8 of each tile, which
+// A warp's products of one stage: kTiles tiles of 16 rows against the first USED
+// of NB blocks of eight columns.  skew: bytes by which the lane's rows (g, g + 8 of each tile, which
 // repeat after two) begin behind their windows.
-template <int PARTS, int NB, bool ALIGNED>
+template <int PARTS, int NB, int USED, bool ALIGNED>
 __device__ __forceinline__ void stage_products(const char *stage, const char *xs, const float *scale, int blocks,
                                                const int (&skew)[2][2], uint32_t magic, int lane,
-                                               int used, float (&total)[kTiles][NB][4]) {
+                                               float (&total)[kTiles][NB][4]) {
     constexpr int pitch = ALIGNED ? 144 : 176;
     const int t = lane & 3, g = lane >> 2;
-    float acc[kTiles][NB][4];
+    float acc[kTiles][USED][4];
 #pragma unroll
     for (int r = 0; r < kTiles; ++r)
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < USED; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
     auto block = [&](int b, const uint32_t (&q)[kTiles][2], const float (&d)[kTiles][2]) {
-        uint32_t x[NB][PARTS][4];
+        uint32_t x[USED][PARTS][4];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            if (n < used) {
+        for (int n = 0; n < USED; ++n) {
 #pragma unroll
-                for (int s = 0; s < PARTS; ++s) {
-                    const uint4 v = reinterpret_cast<const uint4 *>(xs + ((b * NB + n) * PARTS + s) * 512)[lane];
-                    x[n][s][0] = v.x, x[n][s][1] = v.y, x[n][s][2] = v.z, x[n][s][3] = v.w;
-                }
+            for (int s = 0; s < PARTS; ++s) {
+                const uint4 v = reinterpret_cast<const uint4 *>(xs + ((b * NB + n) * PARTS + s) * 512)[lane];
+                x[n][s][0] = v.x, x[n][s][1] = v.y, x[n][s][2] = v.z, x[n][s][3] = v.w;
             }
         }
         // the products of the tiles take turns: each waits for the one before it of
@@ -329,34 +339,32 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
             a[r][7] = hfma2((v8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
         }
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            if (n < used) {
-                float z[kTiles][4];
+        for (int n = 0; n < USED; ++n) {
+            float z[kTiles][4];
 #pragma unroll
-                for (int r = 0; r < kTiles; ++r) z[r][0] = z[r][1] = z[r][2] = z[r][3] = 0.0f;
+            for (int r = 0; r < kTiles; ++r) z[r][0] = z[r][1] = z[r][2] = z[r][3] = 0.0f;
 #pragma unroll
-                for (int s = PARTS - 1; s >= 0; --s) {  // the small part first
+            for (int s = PARTS - 1; s >= 0; --s) {  // the small part first
 #pragma unroll
-                    for (int r = 0; r < kTiles; ++r)
-                        mma16816(z[r], a[r][0], a[r][1], a[r][2], a[r][3], x[n][s][0], x[n][s][1]);
+                for (int r = 0; r < kTiles; ++r)
+                    mma16816(z[r], a[r][0], a[r][1], a[r][2], a[r][3], x[n][s][0], x[n][s][1]);
 #pragma unroll
-                    for (int r = 0; r < kTiles; ++r)
-                        mma16816(z[r], a[r][4], a[r][5], a[r][6], a[r][7], x[n][s][2], x[n][s][3]);
-                }
+                for (int r = 0; r < kTiles; ++r)
+                    mma16816(z[r], a[r][4], a[r][5], a[r][6], a[r][7], x[n][s][2], x[n][s][3]);
+            }
 #pragma unroll
-                for (int r = 0; r < kTiles; ++r) {
-                    acc[r][n][0] = fmaf(d[r][0], z[r][0], acc[r][n][0]);
-                    acc[r][n][1] = fmaf(d[r][0], z[r][1], acc[r][n][1]);
-                    acc[r][n][2] = fmaf(d[r][1], z[r][2], acc[r][n][2]);
-                    acc[r][n][3] = fmaf(d[r][1], z[r][3], acc[r][n][3]);
-                }
+            for (int r = 0; r < kTiles; ++r) {
+                acc[r][n][0] = fmaf(d[r][0], z[r][0], acc[r][n][0]);
+                acc[r][n][1] = fmaf(d[r][0], z[r][1], acc[r][n][1]);
+                acc[r][n][2] = fmaf(d[r][1], z[r][2], acc[r][n][2]);
+                acc[r][n][3] = fmaf(d[r][1], z[r][3], acc[r][n][3]);
             }
         }
     };
     if constexpr (ALIGNED) {
         // two blocks are nine words: the first block's codes begin in the
         // middle of a word, the second's at one
-#pragma unroll 2
+#pragma unroll (USED > 1 ? 1 : 2)
         for (int j = 0; j < 4; ++j) {
             uint32_t q0[kTiles][2], q1[kTiles][2];
             float d0[kTiles][2], d1[kTiles][2];
@@ -376,7 +384,7 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
         }
     } else {
         // the same behind each row's skew; an odd number of blocks ends with one of scale 0
-#pragma unroll 2
+#pragma unroll (USED > 1 ? 1 : 2)
         for (int j = 0; 2 * j < blocks; ++j) {
             uint32_t q0[kTiles][2], q1[kTiles][2];
             float d0[kTiles][2], d1[kTiles][2];
@@ -398,7 +406,7 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
         }
     }
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
+    for (int n = 0; n < USED; ++n) {
         const float2 s = *reinterpret_cast<const float2 *>(scale + n * 8 + 2 * t);
 #pragma unroll
         for (int r = 0; r < kTiles; ++r)
@@ -425,6 +433,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                                                                    const __grid_constant__ CUtensorMap w1,
                                                                    const __grid_constant__ StreamParams p) {
     using L = StreamLayout<PARTS, NB, ALIGNED>;
+    using C = Columns<PARTS, NB>;
     extern __shared__ __align__(128) char smem[];
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = lane & 3, g = lane >> 2;
@@ -532,7 +541,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
 
     int done = 0;
     int held_expert = -1, held_group = -1, held_panel = -1;
-    bool held_packed = false;
     const int panels = (p.chunks + p.x_panel - 1) / p.x_panel;
     while (at.left > 0) {
         Place next = at;
@@ -540,14 +548,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
         const bool there = row0 < p.n;
         const int first = at.start + at.group * 8 * NB;              // of the pairs
         const int cols = min(8 * NB, at.count - at.group * 8 * NB);  // of them here
-        const int used = (cols + 7) / 8;
-        const bool packed = PARTS == 2 && NB == 1 && cols <= 4;  // columns 4 .. 7: the small parts of 0 .. 3
-        const int x_block = packed ? 512 : L::x_block;
-        float total[kTiles][NB][4];
+        const int used = (cols + C::pairs - 1) / C::pairs;           // blocks of columns
+        float total[kTiles][C::blocks][4];
 #pragma unroll
         for (int r = 0; r < kTiles; ++r)
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < C::blocks; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) total[r][n][i] = 0.0f;
         int skew[2][2] = {};
@@ -560,7 +566,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
             const int c0 = panel * p.x_panel, c1 = min(p.chunks, c0 + p.x_panel);
             if (at.expert != held_expert || at.group != held_group || panel != held_panel) {
                 // the rows of x are not those that shared memory holds, or not in that order
-                bool other = panel != held_panel || packed != held_packed;
+                bool other = panel != held_panel;
                 __syncthreads();
                 if (at.expert != held_expert || at.group != held_group) {
                     if (threadIdx.x < 8 * NB) {
@@ -584,21 +590,20 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                 if (other)
                     for (int u = warp; u < (c1 - c0) * used; u += warps) {
                         const int n = u % used, c = u / used;
-                        const int row = src[packed ? g & 3 : n * 8 + g];
+                        const int row = src[n * C::pairs + g % C::pairs];
                         // addresses count from the panel's first chunk
-                        char *xp = xs - static_cast<int64_t>(c0) * 8 * x_block;
-                        float *sp = scale - c0 * 8 * NB;
+                        char *xp = xs - static_cast<int64_t>(c0) * 8 * L::x_block;
+                        float *sp = scale - c0 * 8 * C::blocks;
                         if (p.x_bf16)
                             stage_x<PARTS, NB, uint16_t>(
-                                p, xp, sp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane, packed);
+                                p, xp, sp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane);
                         else
                             stage_x<PARTS, NB, float>(
-                                p, xp, sp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane, packed);
+                                p, xp, sp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane);
                     }
                 held_expert = at.expert;
                 held_group = at.group;
                 held_panel = panel;
-                held_packed = packed;
                 __syncthreads();
             }
             for (int c = c0 + (kw - c0 % p.kw + p.kw) % p.kw; c < c1; c += p.kw) {
@@ -619,61 +624,68 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                     __syncwarp();
                 }
                 if (there && ok) {
-                    auto products = [&](auto parts) {
-                        stage_products<decltype(parts)::value, NB, ALIGNED>(
-                            ring_ptr + (done & 1) * L::stage, xs + (c - c0) * 8 * x_block, scale + (c - c0) * 8 * NB,
-                            min(8, p.blocks - c * 8), skew, p.magic, lane, used, total);
+                    auto products = [&](auto blocks) {
+                        stage_products<C::parts, C::blocks, decltype(blocks)::value, ALIGNED>(
+                            ring_ptr + (done & 1) * L::stage, xs + (c - c0) * 8 * L::x_block, scale + (c - c0) * 8 * C::blocks,
+                            min(8, p.blocks - c * 8), skew, p.magic, lane, total);
                     };
-                    if (packed)
+                    if (C::blocks > 1 && used == 1)
                         products(std::integral_constant<int, 1>());
                     else
-                        products(std::integral_constant<int, PARTS>());
+                        products(std::integral_constant<int, C::blocks>());
                 }
                 __syncwarp();
                 ++done;
             }
         }
-        if (packed)  // both parts of columns 2 t and 2 t + 1
+        if constexpr (C::split)  // both parts of columns 2 t and 2 t + 1
 #pragma unroll
-            for (int r = 0; r < kTiles; ++r)
+            for (int n = 0; n < C::blocks; ++n)
+                if (n < used)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) total[r][0][i] += __shfl_xor_sync(0xFFFFFFFFu, total[r][0][i], 2);
-        // the item's sums: element (r, n, i) of lane is row 16 r + 8 (i / 2) + g, pair 8 n + 2 t + i % 2
-        auto store = [&](int r, int i, int l, int to, float a, float b) {
+                    for (int r = 0; r < kTiles; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) total[r][n][i] += __shfl_xor_sync(0xFFFFFFFFu, total[r][n][i], 2);
+        // the item's sums: element (r, n, i) of lane is row 16 r + 8 (i / 2) + g, column 2 t + i % 2 of block n
+        auto store = [&](int r, int n, int i, int l, float a, float b) {
             const int64_t row = row0 + 16 * r + 8 * (i >> 1) + (l >> 2);
+            const int to = dst[n * C::pairs + 2 * (l & 3) + (i & 1)];
             if (to >= 0 && row < p.n) put(p.out, to * p.out_stride + row, p.out_bf16, GEGLU ? gelu(a) * b : a);
         };
+        const bool own = !C::split || t < 2;  // sums that no other lane has too
         if (p.kw > 1) {
-            constexpr int kWords = kTiles * NB * 128;  // of a warp's sums
+            constexpr int kTileWords = C::lanes * 4, kBlockWords = kTiles * kTileWords, kWords = C::blocks * kBlockWords;
             float *mine = part + warp * kWords;
             barrier(1 + rw, p.kw * 32);  // the last item's sums are read
 #pragma unroll
-            for (int r = 0; r < kTiles; ++r)
+            for (int n = 0; n < C::blocks; ++n)
+                if (own && n < used)
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
-                    reinterpret_cast<float4 *>(mine)[(r * NB + n) * 32 + lane] =
-                        make_float4(total[r][n][0], total[r][n][1], total[r][n][2], total[r][n][3]);
+                    for (int r = 0; r < kTiles; ++r)
+                        reinterpret_cast<float4 *>(mine + n * kBlockWords + r * kTileWords)[C::split ? 2 * g + t : lane] =
+                            make_float4(total[r][n][0], total[r][n][1], total[r][n][2], total[r][n][3]);
             barrier(1 + rw, p.kw * 32);
             const float *all = part + rw * p.kw * kWords;
             if (there)
-                for (int v = kw * 32 + lane; v < kPairs * NB * 128; v += p.kw * 32) {
+                for (int v = kw * 32 + lane; v < used * kPairs * kTileWords; v += p.kw * 32) {
+                    const int n = v / (kPairs * kTileWords), in = v % (kPairs * kTileWords);
+                    const float *from = all + n * kBlockWords + in;
                     float a = 0.0f, b = 0.0f;
                     for (int w = 0; w < p.kw; ++w) {
-                        a += all[w * kWords + v];
-                        if constexpr (GEGLU) b += all[w * kWords + kPairs * NB * 128 + v];
+                        a += from[w * kWords];
+                        if constexpr (GEGLU) b += from[w * kWords + kPairs * kTileWords];
                     }
-                    const int i = v & 3, l = (v >> 2) & 31, n = (v >> 7) % NB, r = v / (NB * 128);
-                    store(r, i, l, dst[8 * n + 2 * (l & 3) + (i & 1)], a, b);
+                    const int l = (in >> 2) % C::lanes;
+                    store(in / kTileWords, n, in & 3, C::split ? (l >> 1) * 4 + (l & 1) : l, a, b);
                 }
-        } else if (there) {
+        } else if (there && own) {
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < C::blocks; ++n)
+                if (n < used)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int to = dst[8 * n + 2 * t + (i & 1)];
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int r = 0; r < kPairs; ++r) store(r, i, lane, to, total[r][n][i], total[GEGLU ? r + kPairs : r][n][i]);
-                }
+                        for (int r = 0; r < kPairs; ++r) store(r, n, i, lane, total[r][n][i], total[GEGLU ? r + kPairs : r][n][i]);
         }
         at = next;
     }
