@@ -571,9 +571,10 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
  * where a bf16 input is exact too; else streaming, where an input is held in binary16
  * with a power of two for each 256 values of a row: a bf16 one exactly, down to 2^-31
  * of the largest of the 256, an fp32 one in two parts, 22 bits of it and 2^-39 of that
- * largest.  A row of x or h that holds an infinity or a NaN gives NaN. Which form a call takes depends on its host-side
- * arguments alone; equal calls give equal bits, and a pair's row depends on no
- * other pair.
+ * largest.  A row of x or h that holds a NaN gives NaN, one that holds an infinity
+ * infinities or NaN, no finite value.  Which form a call takes depends on its
+ * host-side arguments alone; equal calls give equal bits, and a pair's row depends
+ * on no other pair.
  * Entries outside their arrays (an expert_start that descends or leaves
  * 0 .. tokens * topk, a pair outside 0 .. tokens * topk - 1) record
  * QMM_ERR_INDEX; what they concern is left out (in down, y of those tokens is

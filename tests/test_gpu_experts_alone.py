@@ -49,3 +49,38 @@ def test_a_row_does_not_depend_on_its_neighbours(qmm, types, tokens, experts, k)
             first = row
         assert torch.equal(row[0], first[0]) and torch.equal(row[1], first[1]), others
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)], ids=str)
+@pytest.mark.parametrize("tokens,experts", [(12, 64), (12, 2), (200, 2)])
+@pytest.mark.parametrize("k", [512, 288])
+def test_rows_without_a_number(qmm, types, tokens, experts, k):
+    """A NaN in a row makes all of its results NaN, an infinity of either sign none of them
+    finite, also where its weights are 0; the other rows keep their bits."""
+    rng = np.random.default_rng(tokens + experts + k)
+    n = 48
+    b = ref.blocks(rng, experts, n, k)
+    row = b.reshape(experts, n, k // 32, 18)
+    row[:, ::3, 0, 2:] = 0x88  # weights of 0
+    row[:, 1, :, 2:] = 0x88    # and a whole row of them
+    w = dev(b)
+    ids = rng.integers(0, experts, (tokens, 1))
+    starts, pairs = ref.plan_of(ids, experts)
+    x = rng.standard_normal((tokens, k)).astype(np.float32)
+    odd = x.copy()
+    odd[1, 5], odd[4, 7], odd[6, 100], odd[7, k - 1] = np.nan, np.inf, -np.inf, np.nan
+    ones = torch.ones(tokens, 1, device="cuda")
+    got = []
+    for rows in (x, odd):
+        h = torch.empty(tokens, n, dtype=types[1], device="cuda")
+        qmm.qmm_experts_geglu_q4_0(w, w, dev(rows, types[0]), h, dev(starts), dev(pairs), 1, n, k)
+        y = torch.empty(tokens, n, dtype=types[1], device="cuda")
+        qmm.qmm_experts_down_q4_0(w, dev(rows[pairs], types[0]), y, dev(ids.astype(np.int32)), ones, dev(starts), dev(pairs), n, k)
+        by_token = torch.empty_like(h)
+        by_token[torch.from_numpy(pairs).long().cuda()] = h
+        got.append((by_token, y))
+    for plain, rows in zip(*got):
+        assert torch.isnan(rows[[1, 7]]).all() and not torch.isfinite(rows[[4, 6]]).any()
+        keep = np.delete(np.arange(tokens), [1, 4, 6, 7])
+        assert torch.equal(plain[keep], rows[keep])
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
