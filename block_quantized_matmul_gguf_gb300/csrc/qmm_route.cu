@@ -739,9 +739,11 @@ cudaError_t launch_t(const RouteParams &p, cudaStream_t stream) {
 
 }  // namespace
 
+// Of a call with any number of tokens up to this one: the CTAs are most at 8192, and
+// fewer again where a CTA takes more.
 size_t route_workspace_bytes(int64_t tokens, int experts) {
     RouteParams p;
-    shape(tokens, p);
+    shape(std::min<int64_t>(tokens, kMaxChunks * 32), p);
     return p.chunks == p.cluster ? 0 : static_cast<size_t>(p.chunks / p.cluster + p.chunks) * experts * sizeof(int32_t);
 }
 

@@ -517,7 +517,8 @@ qmm_status qmm_attn_q4_0(const qmm_kv_q4_0 *cache, const qmm_attn_args *args,
  *          (padding of a captured graph): ids and pairs -1, weights 0.  A count
  *          outside 0..tokens is moved to the nearer end, QMM_ERR_INDEX.
  *   workspace  16-byte aligned device memory of at least
- *          qmm_route_workspace_bytes() bytes (0 up to 512 tokens), scratch
+ *          qmm_route_workspace_bytes() bytes (0 up to 512 tokens), scratch; what
+ *          it gives for a number of tokens is enough for any smaller one
  * Requires tokens >= 0 (0 launches nothing), 1 <= topk <= 32, topk at most the
  * kept groups' experts, groups dividing experts, 1 <= group_topk <= groups,
  * scale finite, logits_stride >= experts; at most 1024 experts, 32 groups and
