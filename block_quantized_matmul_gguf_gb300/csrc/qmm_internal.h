@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
 #include <utility>
 
 #include <cuda_runtime.h>
@@ -59,8 +60,10 @@ int current_device();
 // current device.  `limits` is the caller's per-kernel cache (one slot per
 // device, a static array local to the launcher of that one kernel), so the
 // attribute call is made only when that kernel's limit grows and launches
-// inside stream capture make no attribute calls once warmed up.
+// inside stream capture make no attribute calls once warmed up.  Host threads that
+// raise it take turns, so that the attribute and the cache only grow.
 constexpr int kMaxDevices = 64;
+inline std::mutex smem_limits_mutex;
 
 template <typename Kernel>
 cudaError_t ensure_smem(Kernel kernel, size_t bytes, bool cluster, int (&limits)[kMaxDevices]) {
@@ -68,6 +71,8 @@ cudaError_t ensure_smem(Kernel kernel, size_t bytes, bool cluster, int (&limits)
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (static_cast<int>(bytes) <= __atomic_load_n(&limits[dev], __ATOMIC_ACQUIRE))
         return cudaSuccess;
+    const std::lock_guard<std::mutex> lock(smem_limits_mutex);
+    if (static_cast<int>(bytes) <= limits[dev]) return cudaSuccess;  // another thread's, meanwhile
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(bytes));
     if (e == cudaSuccess && cluster)

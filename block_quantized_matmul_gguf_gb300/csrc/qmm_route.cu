@@ -755,13 +755,10 @@ cudaError_t launch_route(const RouteArgs &args, cudaStream_t stream, const Launc
     p.group_magic = ((1u << 21) + size - 1) / size;
     p.hist = static_cast<int32_t *>(args.workspace);
     p.ctx = ctx;
-    static int limits[kMaxDevices];
-    const size_t place = smem_bytes(args, false);
-    cudaError_t e = cudaSuccess;
-    if (p.chunks != p.cluster && place > 32 * 1024) e = ensure_smem(place_kernel, place, false, limits);
-    if (e != cudaSuccess) return e;
-    e = args.bf16 ? launch_t<uint16_t>(p, stream) : launch_t<float>(p, stream);
+    const cudaError_t e = args.bf16 ? launch_t<uint16_t>(p, stream) : launch_t<float>(p, stream);
     if (e != cudaSuccess || p.chunks == p.cluster) return e;
+    static_assert(kMaxExperts * 16 + kSpan * kMaxTopk * 4 <= 48 * 1024, "place_kernel keeps to the default limit");
+    const size_t place = smem_bytes(args, false);
     return launch_kernel(place_kernel, dim3(p.chunks), dim3(kThreads), place, stream, 1, p);
 }
 
