@@ -4,16 +4,16 @@
 //
 // Mathematics.  With codes n (0..15) and scales d of 32-weight blocks b,
 //   y[i] = sum_b d_b * sum_j (n_bj - 8) x_bj
-// for the rows x of an expert's pairs.  The integers are exact in binary16, so
+// for the rows x of an expert's pairs.  The integers are exact in binary16 and bf16, so
 // the inner sums run on mma.sync m16n8k16 with 16 rows of weights as one
 // operand, taken from the 4-bit codes in registers, and 8 pairs' x as the other;
 // the scales join in fp32.
 //
-// Precision.  A bf16 x enters as one binary16 value, scaled by a power of two per row
-// and 256 values so that the largest lies in [2^14, 2^15): exactly (down to 2^-31 of
-// that largest).  An fp32 x enters in two parts (22 bits): two products into one sum,
-// or, for groups of eight pairs, other columns of one product (`split`), whose eight
-// columns then are four pairs, so that a group has two.  Each part is then a
+// Precision.  A bf16 x enters as it is (PARTS 1).  An fp32 x enters in two binary16
+// parts (PARTS 2), scaled by a power of two per row and 256 values so that the largest
+// lies in [2^14, 2^15): 22 bits, down to 2^-39 of that largest.  They are two products into
+// one sum, or, for groups of eight pairs, other columns of one product (`split`), whose
+// eight columns then are four pairs, so that a group has two.  Each part is then a
 // sum of its own and both meet at the end, however full the group is: a pair's bits
 // do not depend on the others (16 tokens of 8 of 64 experts of 1024 x 2048: 42.9 us).
 // The codes are made n - 8 before the products: left as the subnormal numbers that a
@@ -67,7 +67,7 @@ struct StreamParams {
     int rw, kw;           // items at a time, warps an item
     int row_groups;       // items of rw * rows
     int x_panel;          // chunks of x that shared memory holds
-    uint32_t magic;       // 1024, 1024 in binary16, in a register
+    uint32_t magic;       // 1024, 1024 in binary16, or 16, 16 in bf16, in a register
     bool x_bf16, out_bf16, x_wide;
     LaunchCtx ctx;
 };
@@ -82,6 +82,11 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -90,12 +95,17 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 __device__ __forceinline__ float low_half(uint32_t v) { return __low2float(*reinterpret_cast<const __half2 *>(&v)); }
 __device__ __forceinline__ float high_half(uint32_t v) { return __high2float(*reinterpret_cast<const __half2 *>(&v)); }
 
-// d = a b + c, a 16 x 16 (row), b 16 x 8 (column), fp32 sums
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// d = a b + c, a 16 x 16 (row), b 16 x 8 (column), binary16 or bf16, fp32 sums
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 16 bytes, of which the first `bytes` are read and the others zeros
@@ -221,33 +231,36 @@ __device__ __forceinline__ void load_windows(const StreamParams &p, Windows &win
     }
 }
 
-template <typename T>
-__device__ __forceinline__ float4 load_four(const T *p, bool wide);
-template <>
-__device__ __forceinline__ float4 load_four<float>(const float *p, bool wide) {
+__device__ __forceinline__ float4 load_four(const float *p, bool wide) {
     if (wide) return *reinterpret_cast<const float4 *>(p);
     return make_float4(p[0], p[1], p[2], p[3]);
 }
-template <>
-__device__ __forceinline__ float4 load_four<uint16_t>(const uint16_t *p, bool wide) {
-    uint32_t a, b;
-    if (wide) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        a = v.x;
-        b = v.y;
-    } else {
-        a = p[0] | static_cast<uint32_t>(p[1]) << 16;
-        b = p[2] | static_cast<uint32_t>(p[3]) << 16;
-    }
-    return make_float4(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
-                       __uint_as_float(b & 0xFFFF0000u));
+__device__ __forceinline__ uint2 load_four(const uint16_t *p, bool wide) {
+    if (wide) return *reinterpret_cast<const uint2 *>(p);
+    return make_uint2(p[0] | static_cast<uint32_t>(p[1]) << 16, p[2] | static_cast<uint32_t>(p[3]) << 16);
 }
 
 // One chunk of x as the products' operand, eight columns of it: lane (g, t) makes
 // column g's values 4t..4t+3 and 16+4t..16+4t+3 of each block, in the order that
-// the codes of a word have.
-template <int PARTS, int NB, typename T>
-__device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *scale, const T *row, int chunk, int nb, int lane) {
+// the codes of a word have.  bf16 values stay as they are.
+template <int NB>
+__device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *, const uint16_t *row, int chunk, int nb, int lane) {
+    const int t = lane & 3;
+    const int blocks = min(8, p.blocks - chunk * 8);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        uint2 v[2] = {};
+        if (row && b < blocks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[h] = load_four(row + chunk * kChunk + b * 32 + h * 16 + 4 * t, p.x_wide);
+        reinterpret_cast<uint4 *>(xs + ((chunk * 8 + b) * NB + nb) * 512)[lane] =
+            make_uint4(__byte_perm(v[0].x, v[0].y, 0x5410), __byte_perm(v[0].x, v[0].y, 0x7632),
+                       __byte_perm(v[1].x, v[1].y, 0x5410), __byte_perm(v[1].x, v[1].y, 0x7632));
+    }
+}
+template <int NB>
+__device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *scale, const float *row, int chunk, int nb, int lane) {
+    constexpr int PARTS = 2;
     using C = Columns<PARTS, NB>;
     const int t = lane & 3, g = lane >> 2;
     const int blocks = min(8, p.blocks - chunk * 8);
@@ -257,8 +270,8 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
     for (int b = 0; b < 8; ++b) {
         v[b][0] = v[b][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (row && b < blocks) {
-            v[b][0] = load_four<T>(row + chunk * kChunk + b * 32 + 4 * t, p.x_wide);
-            v[b][1] = load_four<T>(row + chunk * kChunk + b * 32 + 16 + 4 * t, p.x_wide);
+            v[b][0] = load_four(row + chunk * kChunk + b * 32 + 4 * t, p.x_wide);
+            v[b][1] = load_four(row + chunk * kChunk + b * 32 + 16 + 4 * t, p.x_wide);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -280,8 +293,7 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
             for (int i = 0; i < 2; ++i) {
                 const uint32_t hi = pack_half(y[2 * i], y[2 * i + 1]);
                 part[0][2 * h + i] = hi;
-                if constexpr (PARTS == 2)
-                    part[1][2 * h + i] = pack_half(y[2 * i] - low_half(hi), y[2 * i + 1] - high_half(hi));
+                part[1][2 * h + i] = pack_half(y[2 * i] - low_half(hi), y[2 * i + 1] - high_half(hi));
             }
         }
         char *to = xs + ((chunk * 8 + b) * C::blocks + nb) * C::parts * 512;
@@ -300,7 +312,7 @@ __device__ __noinline__ void stage_x(const StreamParams &p, char *xs, float *sca
 // A warp's products of one stage: kTiles tiles of 16 rows against the first USED
 // of NB blocks of eight columns.  skew: bytes by which the lane's rows (g, g + 8 of each tile, which
 // repeat after two) begin behind their windows.
-template <int PARTS, int NB, int USED, bool ALIGNED>
+template <bool BF16, int PARTS, int NB, int USED, bool ALIGNED>
 __device__ __forceinline__ void stage_products(const char *stage, const char *xs, const float *scale, int blocks,
                                                const int (&skew)[2][2], uint32_t magic, int lane,
                                                float (&total)[kTiles][NB][4]) {
@@ -312,7 +324,7 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
 #pragma unroll
         for (int n = 0; n < USED; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) acc[r][n][i] = BF16 ? total[r][n][i] : 0.0f;
     auto block = [&](int b, const uint32_t (&q)[kTiles][2], const float (&d)[kTiles][2]) {
         uint32_t x[USED][PARTS][4];
 #pragma unroll
@@ -328,15 +340,22 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
         uint32_t a[kTiles][8];
 #pragma unroll
         for (int r = 0; r < kTiles; ++r) {
-            const uint32_t u = q[r][0], v = q[r][1], u8 = u >> 8, v8 = v >> 8;
-            a[r][0] = hadd2((u & 0x000F000Fu) | magic, 0xE408E408u);  // - 1032
-            a[r][1] = hadd2((v & 0x000F000Fu) | magic, 0xE408E408u);
-            a[r][2] = hadd2((u8 & 0x000F000Fu) | magic, 0xE408E408u);
-            a[r][3] = hadd2((v8 & 0x000F000Fu) | magic, 0xE408E408u);
-            a[r][4] = hfma2((u & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
-            a[r][5] = hfma2((v & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
-            a[r][6] = hfma2((u8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
-            a[r][7] = hfma2((v8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+            const uint32_t u = q[r][0], v = q[r][1];
+            if constexpr (BF16) {  // 16 + n, n in the place of 16's upper mantissa bits, - 24
+                auto codes = [&](uint32_t w) { return add_bf16x2((w & 0x00780078u) | magic, 0xC1C0C1C0u); };
+                a[r][0] = codes(u << 3), a[r][1] = codes(v << 3), a[r][2] = codes(u >> 5), a[r][3] = codes(v >> 5);
+                a[r][4] = codes(u >> 1), a[r][5] = codes(v >> 1), a[r][6] = codes(u >> 9), a[r][7] = codes(v >> 9);
+            } else {
+                const uint32_t u8 = u >> 8, v8 = v >> 8;
+                a[r][0] = hadd2((u & 0x000F000Fu) | magic, 0xE408E408u);  // - 1032
+                a[r][1] = hadd2((v & 0x000F000Fu) | magic, 0xE408E408u);
+                a[r][2] = hadd2((u8 & 0x000F000Fu) | magic, 0xE408E408u);
+                a[r][3] = hadd2((v8 & 0x000F000Fu) | magic, 0xE408E408u);
+                a[r][4] = hfma2((u & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
+                a[r][5] = hfma2((v & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+                a[r][6] = hfma2((u8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+                a[r][7] = hfma2((v8 & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);
+            }
         }
 #pragma unroll
         for (int n = 0; n < USED; ++n) {
@@ -347,10 +366,10 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
             for (int s = PARTS - 1; s >= 0; --s) {  // the small part first
 #pragma unroll
                 for (int r = 0; r < kTiles; ++r)
-                    mma16816(z[r], a[r][0], a[r][1], a[r][2], a[r][3], x[n][s][0], x[n][s][1]);
+                    mma<BF16>(z[r], a[r][0], a[r][1], a[r][2], a[r][3], x[n][s][0], x[n][s][1]);
 #pragma unroll
                 for (int r = 0; r < kTiles; ++r)
-                    mma16816(z[r], a[r][4], a[r][5], a[r][6], a[r][7], x[n][s][2], x[n][s][3]);
+                    mma<BF16>(z[r], a[r][4], a[r][5], a[r][6], a[r][7], x[n][s][2], x[n][s][3]);
             }
 #pragma unroll
             for (int r = 0; r < kTiles; ++r) {
@@ -407,11 +426,12 @@ __device__ __forceinline__ void stage_products(const char *stage, const char *xs
     }
 #pragma unroll
     for (int n = 0; n < USED; ++n) {
-        const float2 s = *reinterpret_cast<const float2 *>(scale + n * 8 + 2 * t);
+        const float2 s = BF16 ? float2{} : *reinterpret_cast<const float2 *>(scale + n * 8 + 2 * t);
 #pragma unroll
         for (int r = 0; r < kTiles; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) total[r][n][i] = fmaf(acc[r][n][i], i & 1 ? s.y : s.x, total[r][n][i]);
+            for (int i = 0; i < 4; ++i)
+                total[r][n][i] = BF16 ? acc[r][n][i] : fmaf(acc[r][n][i], i & 1 ? s.y : s.x, total[r][n][i]);
     }
 }
 
@@ -594,12 +614,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                         // addresses count from the panel's first chunk
                         char *xp = xs - static_cast<int64_t>(c0) * 8 * L::x_block;
                         float *sp = scale - c0 * 8 * C::blocks;
-                        if (p.x_bf16)
-                            stage_x<PARTS, NB, uint16_t>(
-                                p, xp, sp, row < 0 ? nullptr : static_cast<const uint16_t *>(p.x) + row * p.x_stride, c0 + c, n, lane);
-                        else
-                            stage_x<PARTS, NB, float>(
-                                p, xp, sp, row < 0 ? nullptr : static_cast<const float *>(p.x) + row * p.x_stride, c0 + c, n, lane);
+                        using T = std::conditional_t<PARTS == 1, uint16_t, float>;
+                        stage_x<NB>(p, xp, sp, row < 0 ? nullptr : static_cast<const T *>(p.x) + row * p.x_stride, c0 + c, n, lane);
                     }
                 held_expert = at.expert;
                 held_group = at.group;
@@ -625,7 +641,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) stream_kernel(const __grid_
                 }
                 if (there && ok) {
                     auto products = [&](auto blocks) {
-                        stage_products<C::parts, C::blocks, decltype(blocks)::value, ALIGNED>(
+                        stage_products<PARTS == 1, C::parts, C::blocks, decltype(blocks)::value, ALIGNED>(
                             ring_ptr + (done & 1) * L::stage, xs + (c - c0) * 8 * L::x_block, scale + (c - c0) * 8 * C::blocks,
                             min(8, p.blocks - c * 8), skew, p.magic, lane, total);
                     };
@@ -764,7 +780,7 @@ cudaError_t launch_form(StreamParams &p, cudaStream_t stream) {
     p.row_bytes = static_cast<int64_t>(p.blocks) * kQ4_0Bytes;
     p.matrix_bytes = p.row_bytes * p.n;
     p.w_bytes = p.matrix_bytes * p.plan.experts;
-    p.magic = 0x64006400u;
+    p.magic = p.x_bf16 ? 0x41804180u : 0x64006400u;
     p.x_wide = reinterpret_cast<uintptr_t>(p.x) % (p.x_bf16 ? 8 : 16) == 0 && p.x_stride % 4 == 0;  // loads of four
     const bool aligned = p.k % kChunk == 0 && p.plan.experts * p.n < (int64_t(1) << 31);  // a box's row is 32 bits
     const bool many = p.plan.pairs_total > 8 * static_cast<int64_t>(p.plan.experts);

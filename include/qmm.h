@@ -566,13 +566,10 @@ qmm_status qmm_route(const qmm_route_args *args, qmm_stream_t stream);
  *          t * topk + r, over the r with 0 <= ids[t][r] < experts, in their
  *          order; a token without any gets 0.
  * Strides count elements; x_type, h_type and y_type may differ.
- * Arithmetic: weights are exact, sums and the projections of down in fp32 up to the
- * output's own rounding.  Two forms: with bf16 in and out, rows of x or h on multiples
- * of 16 bytes, and half as many pairs as experts at least or k >= 4096, on tiles,
- * where a bf16 input is exact too; else streaming, where an input is held in binary16
- * with a power of two for each 256 values of a row: a bf16 one exactly, down to 2^-31
- * of the largest of the 256, an fp32 one in two parts, 22 bits of it and 2^-39 of that
- * largest.  A row of x or h that holds a NaN gives NaN, one that holds an infinity
+ * Arithmetic: weights and a bf16 input are exact, an fp32 input enters in two binary16
+ * parts with a power of two for each 256 values of a row (22 bits of it, and 2^-39 of
+ * the largest of the 256); sums and the projections of down are fp32 up to the output's
+ * own rounding. A row of x or h that holds a NaN gives NaN, one that holds an infinity
  * infinities or NaN, no finite value.  Which form a call takes depends on its
  * host-side arguments alone; equal calls give equal bits, and a pair's row depends
  * on no other pair.

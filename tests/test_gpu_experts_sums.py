@@ -178,3 +178,30 @@ def test_sums_of_a_block_are_whole(qmm, types, tokens, experts):
     limit = 0.0 if types[1] is F32 else 2.0 ** -8
     assert (np.abs(y.double().cpu().numpy() - want) <= limit * np.abs(want)).all()
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("y_type", [F32, BF16], ids=str)
+@pytest.mark.parametrize("tokens,experts", [(3, 64), (3, 4), (40, 16), (90, 4)])
+@pytest.mark.parametrize("k", [256, 288])
+def test_bf16_rows_of_any_range(qmm, y_type, tokens, experts, k):
+    """Rows whose largest value, 1e30, meets weights of 0, beside values of 1 and of 1e-30; in all
+    forms.  Bounds: those of exact products of the other values, and the result's rounding."""
+    rng = np.random.default_rng(tokens + experts + k)
+    n, topk = 40, 2
+    ids = np.argsort(rng.random((tokens, experts)), axis=1)[:, :topk]
+    starts, pairs = ref.plan_of(ids, experts)
+    weights = rng.random((tokens, topk)).astype(np.float32)
+    b = ref.blocks(rng, experts, n, k)
+    row = b.reshape(experts, n, k // 32, 18)
+    row[:, :, 1, 2 + 5] = row[:, :, 1, 2 + 5] & 0xF0 | 8  # value 37 of each row of weights is 0
+    h = rng.standard_normal((tokens * topk, k)).astype(np.float32)
+    h[::3] *= 1e-30
+    h[:, 37] = 0
+    h = torch.from_numpy(h).bfloat16()
+    want, limit = ref.experts_down(h.double().numpy(), b, ids, weights, starts, pairs, True, False)
+    h[:, 37] = 1e30
+    y = torch.empty(tokens, n, dtype=y_type, device="cuda")
+    qmm.qmm_experts_down_q4_0(dev(b), h.cuda(), y, dev(ids.astype(np.int32)), dev(weights), dev(starts), dev(pairs), n, k)
+    limit = limit + (2.0 ** -8 if y_type is BF16 else 2.0 ** -24) * (np.abs(want) + limit)
+    assert (np.abs(y.double().cpu().numpy() - want) <= limit).all()
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
