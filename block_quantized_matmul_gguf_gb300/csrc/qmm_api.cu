@@ -733,7 +733,7 @@ size_t experts_bytes(const ExpertsPlan &p, int64_t n, int64_t k) {
 
 size_t qmm_experts_geglu_workspace_bytes(int64_t tokens, int topk, int experts, int64_t k) {
     if (tokens < 1 || topk < 1 || topk > kMaxTopk || experts < 1 || experts > kMaxExperts || tokens > kMaxRows / topk ||
-        k < kQK || k > kExpertsMaxK || !experts_are_many(tokens * topk, experts, k))
+        k < kQK || k > kExpertsMaxK || !experts_take_room(tokens * topk, experts, k))
         return 0;
     return experts_rows_bytes(tokens * topk, k);
 }

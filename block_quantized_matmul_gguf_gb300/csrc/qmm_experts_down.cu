@@ -102,7 +102,7 @@ size_t experts_down_workspace_bytes(int64_t pairs, int64_t n, int64_t k) {
 }
 
 cudaError_t launch_experts_down(const ExpertsDown &a, cudaStream_t stream, const LaunchCtx &ctx) {
-    const bool tiles = experts_tiles_pay(a.plan, a.h, a.h_stride, a.h_bf16 && a.y_bf16, a.n, a.k);
+    const bool tiles = experts_tiles_pay(a.plan, a.h, a.h_stride, a.h_bf16 && a.y_bf16, a.n, a.k, false);
     cudaError_t e;
     if (tiles) {
         e = launch_experts_tile_down(a, a.workspace, static_cast<char *>(a.workspace) + z_bytes(a.plan.pairs_total, a.n), stream, ctx);

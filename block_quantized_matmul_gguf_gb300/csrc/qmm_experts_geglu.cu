@@ -4,7 +4,7 @@
 namespace qmm {
 
 cudaError_t launch_experts_geglu(const ExpertsGeglu &a, cudaStream_t stream, const LaunchCtx &ctx) {
-    if (a.workspace && experts_tiles_pay(a.plan, a.x, a.x_stride, a.x_bf16 && a.h_bf16, a.n, a.k))
+    if (a.workspace && experts_tiles_pay(a.plan, a.x, a.x_stride, a.x_bf16 && a.h_bf16, a.n, a.k, true))
         return launch_experts_tile_geglu(a, stream, ctx);
     experts::StreamParams p = {};
     p.plan = a.plan;

@@ -760,9 +760,9 @@ cudaError_t launch_tile(const ExpertsPlan &plan, const uint8_t *w, const uint8_t
 
 // Whether the tile form takes a product: bf16 in and out, rows of x in 16-byte
 // pieces, and enough pairs an expert on average.
-bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k) {
+bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k, bool geglu) {
     return bf16 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0 &&
-           plan.experts * n < (int64_t(1) << 31) && experts_are_many(plan.pairs_total, plan.experts, k);
+           plan.experts * n < (int64_t(1) << 31) && experts_are_many(plan.pairs_total, plan.experts, k, geglu);
 }
 
 size_t experts_rows_bytes(int64_t pairs, int64_t k) { return rows_bytes(pairs, k); }

@@ -354,16 +354,24 @@ struct ExpertsDown {
 size_t experts_down_workspace_bytes(int64_t pairs, int64_t n, int64_t k);
 cudaError_t launch_experts_down(const ExpertsDown &args, cudaStream_t stream, const LaunchCtx &ctx);
 
-// The tile form (qmm_experts_tile.cu) and when it is taken: from half a pair an expert
-// on average, or where K is long and the streaming form's x is too much for it.  Below
-// that the GPU's times are alike, and the host has one launch and no maps of x to make.
-// Streaming against tiles, bf16, GeGLU of 8 out of 64 experts of 1024 x 2048: 1 token
-// 11.5 and 11.4 us, 4 25.9 and 24.6, 7 31.4 and 25.1, 63 60.8 and 38.6; down: 1 token
-// 11.1 and 10.5, 6 16.8 and 18.1, 7 31.8 and 21.2.  Four out of 64 experts of 800 x
-// 1568, 8 tokens: 29.2 and 23.8.  Down, two out of 8 experts of 4096 x 14336, one
-// token: 75.4 and 46.4.
-inline bool experts_are_many(int64_t pairs, int experts, int64_t k) { return 2 * pairs >= experts || k >= 4096; }
-bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k);
+// The tile form (qmm_experts_tile.cu) and when it is taken, by pairs an expert on
+// average.  Streaming against tiles, bf16, us:
+//   GeGLU, 8 of 64 experts of 1024 x 2048: 1 token 10.8 and 12.7, 4 25.1 and 33.2, 16 41.0
+//   and 46.8, 32 (4 pairs an expert) 47.8 and 53.0, 48 64.9 and 53.2, 128 113 and 54;
+//   4 of 64 of 800 x 1568: 16 tokens 31.7 and 37.1, 64 45.8 and 51.6, 100 (6.25) 58.1 and
+//   48.9; 2 of 8 of 14336 x 4096: 1 token 38 and 59, 16 (4) 150 and 160; 4 of 8 of 1024 x
+//   2048: 8 tokens (4) 11.0 and 12.2, 16 15.5 and 12.2.
+//   down, 8 of 64 experts of 2048 x 1024: 4 tokens 16.1 and 18.8, 6 (0.75) 16.2 and
+//   21.9, 7 30.0 and 25.3, 16 33.1 and 31.3, 32 32.5 and 33.9, 63 41.8 and 35.1; 4 of 64
+//   of 1568 x 800: 16 tokens 25.4 and 24.4, 64 45.4 and 34.3; long rows, 2 of 8 of 4096 x
+//   14336: 1 token 64 and 55, 4 167 and 98, 16 122 and 100.
+inline bool experts_are_many(int64_t pairs, int experts, int64_t k, bool geglu) {
+    return geglu ? pairs >= 5 * static_cast<int64_t>(experts) : 5 * pairs >= 4 * static_cast<int64_t>(experts) || k >= 4096;
+}
+// Where a GeGLU call asks for the tile form's room: from fewer pairs on, so that a
+// program's workspaces do not hang on where that border lies.
+inline bool experts_take_room(int64_t pairs, int experts, int64_t k) { return 2 * pairs >= experts || k >= 4096; }
+bool experts_tiles_pay(const ExpertsPlan &plan, const void *x, int64_t x_stride, bool bf16, int64_t n, int64_t k, bool geglu);
 cudaError_t launch_experts_tile_geglu(const ExpertsGeglu &args, cudaStream_t stream, const LaunchCtx &ctx);
 size_t experts_rows_bytes(int64_t pairs, int64_t k);  // of x as that form reads it
 cudaError_t launch_experts_tile_down(const ExpertsDown &args, void *z, void *rows, cudaStream_t stream, const LaunchCtx &ctx);
