@@ -15,7 +15,7 @@
 // one sum, or, for groups of eight pairs, other columns of one product (`split`), whose
 // eight columns then are four pairs, so that a group has two.  Each part is then a
 // sum of its own and both meet at the end, however full the group is: a pair's bits
-// do not depend on the others (16 tokens of 8 of 64 experts of 1024 x 2048: 42.9 us).
+// do not depend on the others (16 tokens of 8 of 64 experts of 1024 x 2048: 43 us).
 // The codes are made n - 8 before the products: left as the subnormal numbers that a
 // word holds they save two instructions a pair, but the tensor cores' sums of
 // subnormal operands keep some 18 bits only.
@@ -730,9 +730,9 @@ cudaError_t launch_stream(StreamParams p, cudaStream_t stream) {
     // its items in whole turns; a turn costs its chunks and about 1.2 chunks' time for
     // x and the sums.  The number of items is what pairs spread at random would give:
     // an expert is met with 1 - (1 - topk / experts)^tokens, and a count of many pairs
-    // leaves its last tile half full.  Measured with 1, 2, 4 and 8 warps, GeGLU of 8
-    // out of 64 experts of 1024 x 2048: 1 token 25.4, 16.4, 11.2 and 12.1 us, 4 tokens
-    // 25.4, 30.3, 31.0, 31.9, 16 tokens 51.7, 43.9, 45.4, 50.1; 3 leaves warps idle.
+    // leaves its last tile half full.  Measured with 1, 2, 4 and 8 warps, fp32 GeGLU of 8
+    // out of 64 experts of 1024 x 2048: 1 token 21.8, 14.2, 10.3 and 11.0 us, 4 tokens
+    // 23.5, 26.8, 23.4, 25.7, 16 tokens 52.9, 43.4, 46.7, 53.3, 63 tokens 79, 71, 75, 86.
     constexpr int rows = GEGLU ? kRows / 2 : kRows;
     const double experts = static_cast<double>(p.plan.experts);
     const double met = 1.0 - std::pow(1.0 - p.plan.topk / experts, static_cast<double>(p.plan.pairs_total / p.plan.topk));

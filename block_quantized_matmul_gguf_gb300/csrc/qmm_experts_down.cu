@@ -8,7 +8,8 @@ namespace {
 // y[t] = sum_r weights[t][r] z[t topk + r] over the r whose expert is there, in
 // their order.  V columns a thread.  z is fp32: rounded to bf16, each projection
 // would be off by as much as the result's own rounding.  Bound by the bytes of z,
-// which the projections left in L2 where it fits.
+// which the projections left in L2 where it fits (2047 tokens x 8 to 2048 columns, 134 MB:
+// 26 us of the call's 129, 5.5 TB/s with y).
 struct SumParams {
     const float *z;
     const int32_t *ids;

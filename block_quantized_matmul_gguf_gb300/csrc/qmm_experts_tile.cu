@@ -19,8 +19,9 @@
 //   warp 2      weights as they are: boxes of 64 or 128 rows x 144 bytes
 //   warps 28-31 the same where K is no multiple of 256 and rows lie on no 16 bytes:
 //               the pieces of 16 that hold them, by cp.async, 32 rows a warp (GeGLU of 64
-//               experts of 1024 x 2016, 2047 tokens: one warp 203 us, two 173, four 147;
-//               a bulk copy a row, as TMA wants a request for each, 592)
+//               experts of 1024 x 2016, 2047 tokens: 195 us, where K of 2048 takes 182;
+//               with one warp for all rows and weights in one part 203 for four warps'
+//               147, and with a bulk copy a row, as TMA wants a request for each, 592)
 //   warps 4-11  epilogue, two for each quarter of the lanes
 //   warps 12-27 dequantisers: TMEM lanes 32 (w % 4) .., one stage (64 of K) of every
 //               chunk (256 of K).  The first block's weights are formed in registers
@@ -32,9 +33,11 @@
 // its CTA's items in them by two ballots.
 // Every wait is bounded, as in the prefill GEMM.
 //
-// Bound, for prompts, by the tensor cores (8 out of 64 experts of 1024 x 2048, 2047
-// tokens: 184 us with the rows, 1.49 PFLOP/s of products).  With few rows an expert by the
-// weights' arithmetic and the fill of each item's pipeline (128 tokens: 54 us in all).
+// Bound, for prompts, by the tensor cores, at work 79 % of the time, 71 to 91 by SM
+// (8 out of 64 experts of 1024 x 2048, 2047 tokens: 182 us with 14 for the rows,
+// 1.51 PFLOP/s of products over all; without the low parts 134).  With few rows an expert by
+// the hand-overs of its stages, no one of which is the bound (128 tokens: 54 us; without the
+// low parts 50, without the weights' arithmetic 49, with an eighth of the products 47).
 #include "qmm_internal.h"
 #include "qmm_tc.cuh"
 

@@ -23,7 +23,7 @@
 // memory; beyond, clusters leave them in the workspace and a second launch places
 // the pairs.
 //
-// Bound by latency for few tokens (one of 64 experts 4.0 us, 128 of 128 6.4), by
+// Bound by latency for few tokens (one of 64 experts 4.2 us, 128 of 128 6.5), by
 // instructions and their dependencies for many (some 500 a token with 256 experts:
 // 8191 of them 29 us with the second launch, 53 % of the issue slots).
 #include "qmm_internal.h"

@@ -205,3 +205,30 @@ def test_bf16_rows_of_any_range(qmm, y_type, tokens, experts, k):
     limit = limit + (2.0 ** -8 if y_type is BF16 else 2.0 ** -24) * (np.abs(want) + limit)
     assert (np.abs(y.double().cpu().numpy() - want) <= limit).all()
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (F32, BF16)], ids=str)
+@pytest.mark.parametrize("size", [(3, 64, 4, 130, 512), (16, 8, 2, 64, 1024), (70, 4, 2, 40, 256), (300, 8, 4, 260, 256), (257, 16, 8, 64, 288),
+                                  (200, 6, 3, 129, 2080), (33, 4, 2, 96, 2048)], ids=str)
+def test_bf16_results_are_rounded_once(qmm, size, types):
+    """Both products within the bounds of fp32 results, and half a step of bf16."""
+    tokens, experts, topk, n, k = size
+    rng = np.random.default_rng(sum(size))
+    ids = np.argsort(rng.random((tokens, experts)), axis=1)[:, :topk]
+    starts, pairs = ref.plan_of(ids, experts)
+    bg, bu = ref.blocks(rng, experts, n, k), ref.blocks(rng, experts, n, k)
+
+    def near(got, want, limit):
+        limit = limit + 2.0 ** -8 * (np.abs(want) + limit)
+        assert (np.abs(got.double().cpu().numpy() - want) <= limit).all()
+
+    x = torch.from_numpy(rng.standard_normal((tokens, k)).astype(np.float32)).to(types[0])
+    h = torch.empty(tokens * topk, n, dtype=BF16, device="cuda")
+    qmm.qmm_experts_geglu_q4_0(dev(bg), dev(bu), x.cuda(), h, dev(starts), dev(pairs), topk, n, k)
+    near(h, *ref.experts_geglu(x.double().numpy(), bg, bu, starts, pairs, topk, True, False))
+    x = torch.from_numpy(rng.standard_normal((tokens * topk, k)).astype(np.float32)).to(types[0])
+    weights = rng.standard_normal((tokens, topk)).astype(np.float32)
+    y = torch.empty(tokens, n, dtype=BF16, device="cuda")
+    qmm.qmm_experts_down_q4_0(dev(bg), x.cuda(), y, dev(ids.astype(np.int32)), dev(weights), dev(starts), dev(pairs), n, k)
+    near(y, *ref.experts_down(x.double().numpy(), bg, ids, weights, starts, pairs, True, False))
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
