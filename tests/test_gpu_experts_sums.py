@@ -232,3 +232,26 @@ def test_bf16_results_are_rounded_once(qmm, size, types):
     qmm.qmm_experts_down_q4_0(dev(bg), x.cuda(), y, dev(ids.astype(np.int32)), dev(weights), dev(starts), dev(pairs), n, k)
     near(y, *ref.experts_down(x.double().numpy(), bg, ids, weights, starts, pairs, True, False))
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (F32, F32)], ids=str)
+@pytest.mark.parametrize("tokens,experts", [(3, 64), (90, 4)])
+@pytest.mark.parametrize("k", [256, 288])
+def test_scales_of_both_signs(qmm, types, tokens, experts, k):
+    """Scales as quantizers leave them, negative where the largest value is positive, and 0 among them."""
+    rng = np.random.default_rng(tokens + experts + k)
+    n, topk = 72, 2
+    b = ref.blocks(rng, experts, n, k)
+    row = b.reshape(experts, n, k // 32, 18)
+    row[..., 1] ^= (rng.integers(0, 2, row.shape[:3]) * 128).astype(np.uint8)  # binary16's sign
+    row[:, 5::7, 2, :2] = 0
+    ids = np.argsort(rng.random((tokens, experts)), axis=1)[:, :topk]
+    starts, pairs = ref.plan_of(ids, experts)
+    weights = rng.standard_normal((tokens, topk)).astype(np.float32)
+    h = torch.from_numpy(rng.standard_normal((tokens * topk, k)).astype(np.float32)).to(types[0])
+    want, limit = ref.experts_down(h.double().numpy(), b, ids, weights, starts, pairs, True, False)
+    y = torch.empty(tokens, n, dtype=types[1], device="cuda")
+    qmm.qmm_experts_down_q4_0(dev(b), h.cuda(), y, dev(ids.astype(np.int32)), dev(weights), dev(starts), dev(pairs), n, k)
+    limit = limit + (2.0 ** -8 if types[1] is BF16 else 2.0 ** -24) * (np.abs(want) + limit)
+    assert (np.abs(y.double().cpu().numpy() - want) <= limit).all()
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
